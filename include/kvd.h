@@ -45,7 +45,8 @@
  *              e = (t%2) + 2·(r/8) + 4·(t/8)
  *      BF16 element index within the tile: (i·32 + lane)·8 + e
  *      FP8  byte index within the tile:   ((i/2)·32 + lane)·16 + (i%2)·8 + e
- *  - The pool is written only through kvd_append_kv.
+ *  - The pool is written only through kvd_append_kv, kvd_rope_append, the fused append of
+ *    kvd_decode_attn, kvd_tier_move and kvd_compact.
  *  - A mixed pool (KVD_MIXED) gives every record the BF16 size, 8192 bytes; a block stored
  *    in E4M3 or E5M2 puts the 4224-byte FP8 record (codes of its own format, then the 32
  *    scales) at the start of its slot and leaves the rest unused.
@@ -455,6 +456,129 @@ KVD_API kvd_status kvd_combine_splits(const float* part_o, const float* part_lse
 KVD_API kvd_status kvd_accum_scores(const float* logits, int64_t logits_stride, const float* lse,
                             const int32_t* seq_lens, int batch, int n_q, float inv_LH,
                             float* scores, int64_t scores_stride, void* stream);
+
+/* Rotary positions.  The pages cache keys that already carry their position and describe no
+ * rotation; these two entry points have no counterpart in them.  Pair j < rot_dim/2 of a head's
+ * first rot_dim dims, (j, j + rot_dim/2) or, interleaved, (2j, 2j+1), is turned by the angle
+ * pos·θ_j; the other dims pass through:
+ *   y_a = m·(x_a·cos − x_b·sin),  y_b = m·(x_a·sin + x_b·cos). */
+typedef enum {
+    KVD_ROPE_PLAIN = 0,       /* θ_j = base^(−2j/rot_dim), m = 1 */
+    KVD_ROPE_LINEAR = 1,      /* θ_j / factor (positions interpolated) */
+    KVD_ROPE_NTK = 2,         /* base·factor^(rot_dim/(rot_dim − 2)) for base; rot_dim ≥ 4 */
+    KVD_ROPE_BANDED = 3,      /* with u_j = original_len·θ_j/2π turns over the original length and
+                                 w = clamp((u_j − low)/(high − low), 0, 1): θ_j·(w + (1 − w)/factor) */
+    KVD_ROPE_YARN = 4         /* θ_j·(1 − r) + θ_j·r/factor with r rising linearly over the pair index from
+                                 max(floor(j(high)), 0) to min(ceil(j(low)), rot_dim − 1), j(u) =
+                                 rot_dim·ln(original_len/(2π·u))/(2·ln base) the pair of u turns, the
+                                 interval at least 0.001 long; m = 0.1·ln(factor) + 1 */
+} kvd_rope_rule;
+
+typedef struct {
+    int32_t rule;             /* kvd_rope_rule */
+    double factor;            /* LINEAR, NTK, BANDED, YARN: ≥ 1 */
+    double original_len;      /* BANDED, YARN: the length the model was trained on, > 0 */
+    double low, high;         /* BANDED, YARN: turn counts, 0 < low < high */
+} kvd_rope_scaling;
+
+typedef struct {
+    const float* turns;       /* f32 [rot_dim/2][2], device, 8-byte aligned: θ_j/2π as hi + lo */
+    int32_t rot_dim;          /* even, 2 .. 128 */
+    int32_t interleaved;      /* 0: pairs (j, j + rot_dim/2); 1: pairs (2j, 2j+1) */
+    float mscale;             /* m */
+} kvd_rope_desc;
+
+/* The frequencies of a rule, in fp64, as the fp32 pairs kvd_rope_append reads: turns[2j] the
+ * nearest float of θ_j/2π, turns[2j+1] the nearest float of what is left; *mscale = m.  scaling
+ * NULL is KVD_ROPE_PLAIN.  base > 1.  Host memory, host only; copy turns to the device once. */
+KVD_API kvd_status kvd_rope_freqs(int rot_dim, double base, const kvd_rope_scaling* scaling, float* turns,
+                                  float* mscale);
+
+/* Rotate a chunk's queries and keys and append its K and V, one launch for one layer.
+ * For token n < n_tokens at position positions[n]: q_out[n][h] = R(positions[n])·q[n][h] for the
+ * n_q query heads, and the key R(positions[n])·k[n][h], rounded to bf16, and the value v[n][h] are
+ * written for every KV head h at slot_mapping[n] as kvd_append_kv writes them (bit for bit the same
+ * as appending the rotated keys).  cos and sin are good to about 2^-23 at every position.
+ *  q, k, v       bf16, device; token n's heads start at n·stride elements, heads of 128 contiguous
+ *                (slices of one projection's output have one stride); 16-byte aligned, strides
+ *                multiples of 8 and ≥ heads·128
+ *  q_out         bf16, likewise; may be q itself with q's stride.  n_q = 0: only the append (q and
+ *                q_out may be NULL)
+ *  positions     int32 [n_tokens], device, in [0, 2^24): a token outside is skipped whole (its
+ *                q_out row is left as it was) with KVD_ERR_OOB in the error word
+ *  slot_mapping  int64 [n_tokens], device, as in kvd_append_kv (s < 0: no append for that token; no
+ *                slot twice in one call)
+ * Every pool kind, host-tier blocks included.  n_tokens = 0 is a no-op. */
+KVD_API kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_stride, int n_q,
+                                   const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                                   const int32_t* positions, const kvd_rope_desc* rope,
+                                   const int64_t* slot_mapping, int n_tokens, void* q_out, int64_t q_out_stride,
+                                   void* stream);
+
+/* Bytes of kvd_chunk_attn's workspace (does not depend on the lengths).  Host only. */
+KVD_API kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int batch, size_t* bytes_out);
+
+/* Causal attention of a chunk of new tokens of every request over its paged cache, one layer
+ * (a prompt's chunk, drafted tokens to verify, single tokens, mixed in one batch).  Page "LLM에서 KV
+ * 캐시는 얼마나 생길까", section "KV 캐시란": the prompt's tokens are attended in parallel, each over
+ * the keys up to its own.  The new tokens' K and V are in the cache already (kvd_rope_append or
+ * kvd_append_kv).  Request b's new tokens are the rows q_start[b] .. q_start[b+1]-1 of q; with
+ * T of them, row i sits at position seq_lens[b] - T + i and attends the retained positions up to it.
+ *  q            bf16 [n_tokens][n_q][128], device, 16-byte aligned
+ *  q_start      int32 [batch + 1], device, 0 ≤ q_start[b] ≤ q_start[b+1] ≤ n_tokens.  Rows outside
+ *               every request are neither read nor written.  A request whose pair breaks this is
+ *               skipped with KVD_ERR_OOB in the error word; T = 0 is a request with nothing to do
+ *  seq_lens     int32 [batch], device: cached tokens, the new ones included; in
+ *               [T, max_blocks_per_seq·16], else KVD_ERR_OOB and the rows get out = 0, lse = −inf
+ *  block_table, max_blocks_per_seq, retain_mask, softmax_scale as in kvd_decode_attn; a block id
+ *               outside the pool (and its host tier) is reported and its 16 positions are not attended
+ *  workspace    device scratch, 256-byte aligned, ≥ kvd_chunk_workspace_bytes; needs no
+ *               initialisation and keeps nothing from call to call.  Calls that may run at the same
+ *               time need one each
+ *  out          [n_tokens][n_q][128] in out_dtype (KVD_BF16 or KVD_F32), 16-byte aligned
+ *  lse_out      f32 [n_tokens][n_q] natural-log log-sum-exp, or NULL
+ * A row with nothing to attend gets out = 0 and lse = −inf.  What a masked position's slot holds
+ * (not yet written, a NaN) does not reach the result.  Every pool kind.  In an INT4 / INT2 pool
+ * code·scale + zero is rounded to bf16 before the products; the other kinds' K and V enter them
+ * exactly.  Weights are rounded to bf16 for the product with V, sums are fp32.
+ * n_tokens = 0 or batch = 0 is a no-op. */
+KVD_API kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start,
+                                  int n_tokens, const int32_t* block_table, int max_blocks_per_seq,
+                                  const int32_t* seq_lens, int batch, const uint16_t* retain_mask,
+                                  float softmax_scale, void* workspace, size_t workspace_bytes, void* out,
+                                  int out_dtype, float* lse_out, void* stream);
+
+/* Bytes of kvd_compact's workspace.  Host only. */
+KVD_API kvd_status kvd_compact_workspace_bytes(const kvd_pool* pool, int batch, int max_blocks_per_seq,
+                                               size_t* bytes_out);
+
+/* Copy the retained slots of a batch to dense blocks, in every layer and KV head.  Page "기술 요약:
+ * 모든 사고가 HBM 을 필요로 하는 것은 아님", section "1. 4 단계 분류": evicted tokens (tier T3) are
+ * dropped; the retain mask masks them, this frees the pages they leave half empty.  The j-th
+ * retained position of request b (positions 0 .. seq_lens[b]-1, in order) goes to slot j%16 of block
+ * new_table[b][j/16]; the slots behind the last one in its block are zeroed, and
+ * retain_mask[new block] = 0xffff.  The old blocks are left as they are: when nothing else uses them
+ * they are free once the stream has passed the call.  Without a mask it copies the requests (a fork).
+ *  block_table  int32 [batch][max_blocks_per_seq], device.  Requests may share old blocks
+ *  seq_lens     int32 [batch], device, in [0, max_blocks_per_seq·16], else KVD_ERR_OOB on the device
+ *               and the request is taken as empty
+ *  retain_mask  uint16 [num_blocks + host_blocks], device, or NULL (all slots kept); in/out
+ *  new_table    int32 [batch][new_max_blocks], device; of row b the first ⌈new_lens[b]/16⌉ ids are
+ *               used.  A used id that is outside the pool (and host tier), is used twice or is also
+ *               read by the call is reported (KVD_ERR_OOB) and not written
+ *  new_lens     int32 [batch], device, out: retained positions (not seq_lens itself).  A request that
+ *               does not fit its new row is reported (KVD_ERR_OOB) and gets 0, nothing copied
+ *  scores       f32 [batch][scores_stride] or NULL: importance scores by position; new_scores
+ *               f32 [batch][new_scores_stride] gets those of the retained positions (0 for a
+ *               position at or past scores_stride), then zeros
+ *  workspace    device scratch, 256-byte aligned, ≥ kvd_compact_workspace_bytes
+ * Needs num_blocks + host_blocks ≤ 2^27 and at most 65,535 requests.  A mixed pool is
+ * KVD_ERR_UNSUPPORTED: a block's format cannot hold another's codes.  batch = 0 is a no-op. */
+KVD_API kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int max_blocks_per_seq,
+                               const int32_t* seq_lens, int batch, uint16_t* retain_mask, const int32_t* new_table,
+                               int new_max_blocks, int32_t* new_lens, const float* scores, int64_t scores_stride,
+                               float* new_scores, int64_t new_scores_stride, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* Synchronise `stream`, return the pool's device error word in *code (KVD_OK if none) and
  * clear it. */

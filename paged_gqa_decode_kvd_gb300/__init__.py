@@ -31,6 +31,12 @@ from ._lib import (  # noqa: F401
     KvdError,
     kvd_accum_scores,
     kvd_append_kv,
+    kvd_chunk_attn,
+    kvd_chunk_workspace_bytes,
+    kvd_compact,
+    kvd_compact_workspace_bytes,
+    kvd_rope_append,
+    kvd_rope_freqs,
     kvd_pool_attach_host_tier,
     kvd_tier_bytes,
     kvd_tier_prefetch,
@@ -53,6 +59,21 @@ from ._lib import (  # noqa: F401
     load,
     status_string,
 )
+
+
+class Rope:
+    """Rotary positions of a model: the device table of kvd_rope_append, its pairing and its scale.
+
+    scaling: "plain", "linear" (factor), "ntk" (factor), "banded" or "yarn" (factor, original_len, low, high:
+    turn counts over the original length)."""
+
+    def __init__(self, rot_dim: int, base: float, interleaved: bool = False, device="cuda", scaling: str = "plain",
+                 factor: float = 1.0, original_len: float = 0.0, low: float = 1.0, high: float = 1.0):
+        import torch
+
+        turns, self.mscale = kvd_rope_freqs(rot_dim, base, scaling, factor, original_len, low, high)
+        self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
+        self.turns = torch.from_numpy(turns).to(device)
 
 
 class KVPool:

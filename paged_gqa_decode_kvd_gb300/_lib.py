@@ -22,7 +22,10 @@ SYMBOLS = [
     "kvd_get_device_error", "kvd_selftest_wait_timeout", "kvd_decode_attn_noalloc",
     "kvd_tier_bytes", "kvd_pool_attach_host_tier", "kvd_tier_prefetch", "kvd_tier_plan", "kvd_tier_move",
     "kvd_tier_reassign", "kvd_measure_read_stream", "kvd_pool_set_block_formats", "kvd_decode_plan",
+    "kvd_rope_freqs", "kvd_rope_append", "kvd_chunk_workspace_bytes", "kvd_chunk_attn",
+    "kvd_compact_workspace_bytes", "kvd_compact",
 ]
+ROPE_RULES = {"plain": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvd_rope_rule
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -40,6 +43,16 @@ class PoolDesc(ctypes.Structure):
     _fields_ = [("num_layers", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("d_h", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int64), ("kv_dtype", ctypes.c_int32),
                 ("group_size", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("rule", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
 
 
 _lib = None
@@ -106,6 +119,19 @@ def load(build_if_missing: bool = True):
     lib.kvd_decode_plan.argtypes = [P, i32, P, i32, P, i32, i32, i32, P, P, sz, P]
     lib.kvd_measure_read_stream.restype = i32
     lib.kvd_measure_read_stream.argtypes = [P, sz, P, sz, P]
+    f64 = ctypes.c_double
+    lib.kvd_rope_freqs.restype = i32
+    lib.kvd_rope_freqs.argtypes = [i32, f64, ctypes.POINTER(RopeScaling), P, P]
+    lib.kvd_rope_append.restype = i32
+    lib.kvd_rope_append.argtypes = [P, i32, P, i64, i32, P, i64, P, i64, P, ctypes.POINTER(RopeDesc), P, i32, P, i64, P]
+    lib.kvd_chunk_workspace_bytes.restype = i32
+    lib.kvd_chunk_workspace_bytes.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
+    lib.kvd_chunk_attn.restype = i32
+    lib.kvd_chunk_attn.argtypes = [P, i32, P, i32, P, i32, P, i32, P, i32, P, f32, P, sz, P, i32, P, P]
+    lib.kvd_compact_workspace_bytes.restype = i32
+    lib.kvd_compact_workspace_bytes.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
+    lib.kvd_compact.restype = i32
+    lib.kvd_compact.argtypes = [P, P, i32, P, i32, P, P, i32, P, P, i64, P, i64, P, sz, P]
     _lib = lib
     return lib
 
@@ -325,3 +351,122 @@ def kvd_measure_read_stream(buf, sink, stream=None):
     _check("kvd_measure_read_stream", load().kvd_measure_read_stream(
         _ptr(buf), buf.numel() * buf.element_size(), _ptr(sink), sink.numel() * sink.element_size(),
         _stream(stream)))
+
+
+def kvd_rope_freqs(rot_dim, base, scaling="plain", factor=1.0, original_len=0.0, low=1.0, high=1.0):
+    """(turns, mscale): the rotary frequencies of a rule ("plain", "linear", "ntk", "banded", "yarn") in turns
+    per position, float32 numpy [rot_dim/2][2] as hi + lo, and the factor on cos and sin; host only."""
+    import numpy as np
+
+    if scaling not in ROPE_RULES:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_RULES)}")
+    turns, m = np.zeros((max(1, int(rot_dim) // 2), 2), np.float32), ctypes.c_float()
+    sc = RopeScaling(ROPE_RULES[scaling], float(factor), float(original_len), float(low), float(high))
+    _check("kvd_rope_freqs", load().kvd_rope_freqs(int(rot_dim), float(base), ctypes.byref(sc),
+                                                   turns.ctypes.data_as(ctypes.c_void_p), ctypes.byref(m)))
+    return turns, m.value
+
+
+def _heads(t, name):
+    """Token stride of a bf16 [n][heads][128] tensor (a slice of a projection's output counts)."""
+    import torch
+
+    if t.dim() != 3 or t.shape[2] != 128 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16 [tokens][heads][128]")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1) * 128
+
+
+def _like(t, name, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def kvd_rope_append(handle, layer, q, k_new, v_new, positions, rope, slot_mapping, q_out=None, stream=None):
+    """Rotate q (into q_out, or in place) and k_new at `positions` (int32) and append k_new, v_new at
+    slot_mapping (int64).  rope: a Rope.  q, k_new, v_new: bf16 [n][heads][128], heads of a token
+    contiguous; q may be None (append only)."""
+    import torch
+
+    n = int(k_new.shape[0])
+    ks, vs = _heads(k_new, "k_new"), _heads(v_new, "v_new")
+    dev = k_new.device
+    if v_new.shape != k_new.shape or v_new.device != dev or rope.turns.device != dev:
+        raise ValueError("k_new, v_new and rope must agree in shape and device")
+    _like(positions, "positions", torch.int32, (n,), dev)
+    _like(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
+    n_q, qs, os_ = 0, 0, 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        if q.shape[0] != n or q_out.shape != q.shape or q.device != dev or q_out.device != dev:
+            raise ValueError("q and q_out must have k_new's tokens and device")
+        n_q, qs, os_ = int(q.shape[1]), _heads(q, "q"), _heads(q_out, "q_out")
+    d = RopeDesc(rope.turns.data_ptr(), rope.rot_dim, 1 if rope.interleaved else 0, rope.mscale)
+    _check("kvd_rope_append", load().kvd_rope_append(
+        handle, int(layer), _ptr(q), qs, n_q, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(positions), ctypes.byref(d),
+        _ptr(slot_mapping), n, _ptr(q_out if q is not None else None), os_, _stream(stream)))
+
+
+def kvd_chunk_workspace_bytes(handle, n_q, batch):
+    """Bytes of kvd_chunk_attn's workspace; host only."""
+    b = ctypes.c_size_t()
+    _check("kvd_chunk_workspace_bytes", load().kvd_chunk_workspace_bytes(handle, int(n_q), int(batch), ctypes.byref(b)))
+    return b.value
+
+
+def kvd_chunk_attn(handle, layer, q, q_start, block_table, seq_lens, workspace, out, retain_mask=None,
+                   softmax_scale=None, lse_out=None, stream=None):
+    """Causal attention of the rows q_start[b] .. q_start[b+1]-1 of q (bf16 [n][n_q][128]) over request b's
+    cached tokens, the last seq_lens[b] of which they are; out bf16 or float32 like q, lse_out f32 [n][n_q]."""
+    import torch
+
+    n, n_q, d_h = q.shape
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or d_h != 128:
+        raise ValueError("q must be contiguous bfloat16 [tokens][heads][128]")
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be bfloat16 or float32")
+    _like(out, "out", out.dtype, q.shape, q.device)
+    batch = int(seq_lens.shape[0])
+    _like(seq_lens, "seq_lens", torch.int32, (batch,), q.device)
+    _like(q_start, "q_start", torch.int32, (batch + 1,), q.device)
+    _like(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), q.device)
+    if lse_out is not None:
+        _like(lse_out, "lse_out", torch.float32, (n, n_q), q.device)
+    if softmax_scale is None:
+        softmax_scale = d_h ** -0.5
+    _check("kvd_chunk_attn", load().kvd_chunk_attn(
+        handle, int(layer), _ptr(q), n_q, _ptr(q_start), n, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        batch, _ptr(retain_mask), float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(out), KVD_F32 if out.dtype == torch.float32 else KVD_BF16, _ptr(lse_out), _stream(stream)))
+
+
+def kvd_compact_workspace_bytes(handle, batch, max_blocks_per_seq):
+    """Bytes of kvd_compact's workspace; host only."""
+    b = ctypes.c_size_t()
+    _check("kvd_compact_workspace_bytes", load().kvd_compact_workspace_bytes(handle, int(batch), int(max_blocks_per_seq),
+                                                                             ctypes.byref(b)))
+    return b.value
+
+
+def kvd_compact(handle, block_table, seq_lens, new_table, new_lens, workspace, retain_mask=None, scores=None,
+                new_scores=None, stream=None):
+    """Copy the retained slots of every request to the dense blocks new_table names (all layers and heads);
+    new_lens (int32) gets the retained counts, new_scores the retained positions' scores."""
+    import torch
+
+    batch, mb = block_table.shape
+    dev = block_table.device
+    _like(block_table, "block_table", torch.int32, (batch, mb), dev)
+    _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _like(new_table, "new_table", torch.int32, (batch, new_table.shape[1]), dev)
+    _like(new_lens, "new_lens", torch.int32, (batch,), dev)
+    ss = ns = 0
+    if scores is not None and new_scores is not None:
+        ss, ns = int(scores.shape[1]), int(new_scores.shape[1])
+        _like(scores, "scores", torch.float32, (batch, ss), dev)
+        _like(new_scores, "new_scores", torch.float32, (batch, ns), dev)
+    _check("kvd_compact", load().kvd_compact(
+        handle, _ptr(block_table), mb, _ptr(seq_lens), batch, _ptr(retain_mask), _ptr(new_table), new_table.shape[1],
+        _ptr(new_lens), _ptr(scores), ss, _ptr(new_scores), ns, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))

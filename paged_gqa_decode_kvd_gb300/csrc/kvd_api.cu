@@ -1,11 +1,13 @@
 // kvd_api.cu — the exported C ABI: argument checks, split plan, launches, error word.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <new>
 
 #include "../../include/kvd.h"
+#include "kvd_chunk.h"
 #include "kvd_common.cuh"
 #include "kvd_internal.h"
 
@@ -591,6 +593,216 @@ kvd_status kvd_decode_plan(kvd_pool* pool, int n_q, const int32_t* block_table, 
     p.nsplit = S;
     int32_t* plan = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.plan);
     return cuda_status(kvd::launch_plan(p, plan, static_cast<cudaStream_t>(stream)));
+}
+
+kvd_status kvd_rope_freqs(int rot_dim, double base, const kvd_rope_scaling* scaling, float* turns, float* mscale) {
+    constexpr double kTwoPi = 6.283185307179586476925;
+    if (!turns || !mscale || rot_dim < 2 || (rot_dim & 1) || !(base > 1.0) || std::isinf(base)) return KVD_ERR_INVALID;
+    if (rot_dim > kvd::kDh) return KVD_ERR_UNSUPPORTED;
+    const int rule = scaling ? scaling->rule : KVD_ROPE_PLAIN;
+    if (rule < KVD_ROPE_PLAIN || rule > KVD_ROPE_YARN) return KVD_ERR_INVALID;
+    const bool bands = rule == KVD_ROPE_BANDED || rule == KVD_ROPE_YARN;
+    const double factor = rule == KVD_ROPE_PLAIN ? 1.0 : scaling->factor;
+    if (!(factor >= 1.0) || std::isinf(factor)) return KVD_ERR_INVALID;
+    if (bands && (!(scaling->original_len > 0.0) || std::isinf(scaling->original_len) || !(scaling->low > 0.0) ||
+                  !(scaling->low < scaling->high) || std::isinf(scaling->high)))
+        return KVD_ERR_INVALID;
+    if (rule == KVD_ROPE_NTK) {
+        if (rot_dim < 4) return KVD_ERR_INVALID;
+        base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+    }
+    double first = 0.0, width = 1.0;   // YARN: the ramp over the pair index
+    if (rule == KVD_ROPE_YARN) {
+        auto pair = [&](double u) { return rot_dim * std::log(scaling->original_len / (kTwoPi * u)) / (2.0 * std::log(base)); };
+        first = std::fmax(std::floor(pair(scaling->high)), 0.0);
+        width = std::fmax(std::fmin(std::ceil(pair(scaling->low)), rot_dim - 1.0) - first, 0.001);
+    }
+    for (int j = 0; j < rot_dim / 2; ++j) {
+        double f = std::pow(base, -2.0 * j / rot_dim);
+        if (rule == KVD_ROPE_LINEAR) f /= factor;
+        if (rule == KVD_ROPE_BANDED) {
+            const double w = (scaling->original_len * f / kTwoPi - scaling->low) / (scaling->high - scaling->low);
+            const double c = std::fmin(std::fmax(w, 0.0), 1.0);
+            f = f * c + f / factor * (1.0 - c);
+        }
+        if (rule == KVD_ROPE_YARN) {
+            const double r = std::fmin(std::fmax((j - first) / width, 0.0), 1.0);
+            f = f * (1.0 - r) + f / factor * r;
+        }
+        const double t = f / kTwoPi;
+        turns[2 * j] = static_cast<float>(t);
+        turns[2 * j + 1] = static_cast<float>(t - static_cast<double>(turns[2 * j]));
+    }
+    *mscale = rule == KVD_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+    return KVD_OK;
+}
+
+kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_stride, int n_q, const void* k_new,
+                           int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* positions,
+                           const kvd_rope_desc* rope, const int64_t* slot_mapping, int n_tokens, void* q_out,
+                           int64_t q_out_stride, void* stream) {
+    if (!pool || layer < 0 || layer >= pool->desc.num_layers || n_q < 0 || n_tokens < 0 || !rope) return KVD_ERR_INVALID;
+    if (rope->rot_dim < 2 || (rope->rot_dim & 1) || !rope->turns || (rope->interleaved != 0 && rope->interleaved != 1))
+        return KVD_ERR_INVALID;
+    if (rope->rot_dim > kvd::kDh || n_q > 65536) return KVD_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return KVD_OK;
+    if (!k_new || !v_new || !positions || !slot_mapping || (n_q > 0 && (!q || !q_out))) return KVD_ERR_INVALID;
+    const int64_t kv_row = static_cast<int64_t>(pool->desc.n_kv) * kvd::kDh, q_row = static_cast<int64_t>(n_q) * kvd::kDh;
+    if (k_stride < kv_row || v_stride < kv_row || (k_stride & 7) || (v_stride & 7)) return KVD_ERR_INVALID;
+    if (n_q > 0 && (q_stride < q_row || q_out_stride < q_row || (q_stride & 7) || (q_out_stride & 7) || !aligned16(q) ||
+                    !aligned16(q_out)))
+        return KVD_ERR_INVALID;
+    if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(rope->turns) & 7u)) return KVD_ERR_INVALID;
+    if (n_q > 0 && q_out == q && q_out_stride != q_stride) return KVD_ERR_INVALID;
+    if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
+    kvd::RopeParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k_new);
+    p.v = static_cast<const uint16_t*>(v_new);
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.turns = reinterpret_cast<const float2*>(rope->turns);
+    p.kv = pool->mem + static_cast<size_t>(layer) * pool->layer_bytes;
+    p.host_kv = pool->host_kv ? pool->host_kv + static_cast<size_t>(layer) * pool->host_layer_bytes : nullptr;
+    p.block_fmt = pool->block_fmt;
+    p.err = pool->err;
+    p.num_blocks = pool->desc.num_blocks;
+    p.host_blocks = pool->host_blocks;
+    p.n_tokens = n_tokens;
+    p.n_q = n_q;
+    p.n_kv = pool->desc.n_kv;
+    p.ng = pool_ng(&pool->desc);
+    p.rot = rope->rot_dim;
+    p.interleaved = rope->interleaved;
+    p.heads_per_cta = 0;
+    p.mscale = rope->mscale;
+    return cuda_status(kvd::launch_rope_append(p, pool_kind(pool), pool->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+static kvd_status check_chunk_shape(const kvd_pool* pool, int n_q, int batch) {
+    if (!pool || n_q < 1 || batch < 0 || n_q % pool->desc.n_kv != 0) return KVD_ERR_INVALID;
+    if (n_q / pool->desc.n_kv > kvd::kMaxG || batch > kvd::kMaxBatch) return KVD_ERR_UNSUPPORTED;
+    return KVD_OK;
+}
+
+kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int batch, size_t* bytes_out) {
+    kvd_status st = check_chunk_shape(pool, n_q, batch);
+    if (st != KVD_OK) return st;
+    if (!bytes_out) return KVD_ERR_INVALID;
+    *bytes_out = 256;
+    return KVD_OK;
+}
+
+kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start, int n_tokens,
+                          const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                          const uint16_t* retain_mask, float softmax_scale, void* workspace, size_t workspace_bytes,
+                          void* out, int out_dtype, float* lse_out, void* stream) {
+    kvd_status st = check_chunk_shape(pool, n_q, batch);
+    if (st != KVD_OK) return st;
+    if (layer < 0 || layer >= pool->desc.num_layers || n_tokens < 0 || max_blocks_per_seq < 1) return KVD_ERR_INVALID;
+    if (out_dtype != KVD_BF16 && out_dtype != KVD_F32) return KVD_ERR_INVALID;
+    if (batch == 0 || n_tokens == 0) return KVD_OK;
+    if (!q || !q_start || !block_table || !seq_lens || !workspace || !out) return KVD_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return KVD_ERR_INVALID;
+    size_t need = 0;
+    st = kvd_chunk_workspace_bytes(pool, n_q, batch, &need);
+    if (st != KVD_OK) return st;
+    if (workspace_bytes < need) return KVD_ERR_NOMEM;
+    if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
+    kvd::ChunkParams p;
+    p.kv = pool->mem + static_cast<size_t>(layer) * pool->layer_bytes;
+    p.stage = !pool->host_blocks ? nullptr
+              : pool->host_direct ? pool->host_kv + static_cast<size_t>(layer) * pool->host_layer_bytes
+                                  : pool->staging + static_cast<size_t>(layer % 2) * pool->host_layer_bytes;
+    p.block_fmt = pool->block_fmt;
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_start = q_start;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.retain = retain_mask;
+    p.out = out;
+    p.lse_out = lse_out;
+    p.err = pool->err;
+    p.num_blocks = pool->desc.num_blocks;
+    p.host_blocks = pool->host_blocks;
+    p.record_bytes = static_cast<int64_t>(record_bytes(&pool->desc));
+    p.n_tokens = n_tokens;
+    p.max_blocks = max_blocks_per_seq;
+    p.B = batch;
+    p.n_q = n_q;
+    p.n_kv = pool->desc.n_kv;
+    p.g = n_q / pool->desc.n_kv;
+    p.ng = pool_ng(&pool->desc);
+    p.out_f32 = out_dtype == KVD_F32;
+    p.scale_log2 = softmax_scale * kvd::kLog2e;
+    return cuda_status(kvd::launch_chunk(p, pool_kind(pool), static_cast<cudaStream_t>(stream)));
+}
+
+static kvd_status compact_layout(const kvd_pool* pool, int batch, int max_blocks_per_seq, size_t* claim_off, size_t* total) {
+    if (!pool || batch < 0 || max_blocks_per_seq < 1) return KVD_ERR_INVALID;
+    if (pool->desc.kv_dtype == KVD_MIXED || batch > 65535) return KVD_ERR_UNSUPPORTED;
+    if (pool->desc.num_blocks + pool->host_blocks > (1 << 27)) return KVD_ERR_UNSUPPORTED;
+    size_t n = 0;
+    if (!mul_ok(static_cast<size_t>(batch), static_cast<size_t>(max_blocks_per_seq), &n) ||
+        !mul_ok(n, kvd::kBs * sizeof(uint32_t), &n))
+        return KVD_ERR_INVALID;
+    *claim_off = align256(n);
+    *total = align256(*claim_off + static_cast<size_t>(pool->desc.num_blocks + pool->host_blocks) * sizeof(uint32_t));
+    return KVD_OK;
+}
+
+kvd_status kvd_compact_workspace_bytes(const kvd_pool* pool, int batch, int max_blocks_per_seq, size_t* bytes_out) {
+    size_t claim = 0, total = 0;
+    kvd_status st = compact_layout(pool, batch, max_blocks_per_seq, &claim, &total);
+    if (st != KVD_OK) return st;
+    if (!bytes_out) return KVD_ERR_INVALID;
+    *bytes_out = total;
+    return KVD_OK;
+}
+
+kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                       int batch, uint16_t* retain_mask, const int32_t* new_table, int new_max_blocks,
+                       int32_t* new_lens, const float* scores, int64_t scores_stride, float* new_scores,
+                       int64_t new_scores_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    size_t claim = 0, total = 0;
+    kvd_status st = compact_layout(pool, batch, max_blocks_per_seq, &claim, &total);
+    if (st != KVD_OK) return st;
+    if (new_max_blocks < 1) return KVD_ERR_INVALID;
+    if (batch == 0) return KVD_OK;
+    if (!block_table || !seq_lens || !new_table || !new_lens || new_lens == seq_lens || !workspace ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return KVD_ERR_INVALID;
+    if ((scores == nullptr) != (new_scores == nullptr)) return KVD_ERR_INVALID;
+    if (scores && (scores == new_scores || scores_stride < 1 || new_scores_stride < 1)) return KVD_ERR_INVALID;
+    if (workspace_bytes < total) return KVD_ERR_NOMEM;
+    kvd::CompactParams p;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.new_table = new_table;
+    p.retain = retain_mask;
+    p.new_lens = new_lens;
+    p.scores = scores;
+    p.new_scores = new_scores;
+    p.scores_stride = scores_stride;
+    p.new_scores_stride = new_scores_stride;
+    p.source = static_cast<uint32_t*>(workspace);
+    p.claim = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + claim);
+    p.kv = pool->mem;
+    p.host_kv = pool->host_kv;
+    p.err = pool->err;
+    p.num_blocks = pool->desc.num_blocks;
+    p.host_blocks = pool->host_blocks;
+    p.max_blocks = max_blocks_per_seq;
+    p.new_max_blocks = new_max_blocks;
+    p.B = batch;
+    p.L = pool->desc.num_layers;
+    p.n_kv = pool->desc.n_kv;
+    return cuda_status(kvd::launch_compact(p, pool_kind(pool), pool_ng(&pool->desc), static_cast<cudaStream_t>(stream)));
 }
 
 kvd_status kvd_combine_splits(const float* part_o, const float* part_lse, const int32_t* unit_first,

@@ -1,0 +1,338 @@
+// kvd_rope.cu — rotary positions of a chunk's queries and keys, fused with the append of its K and V.
+//
+// Pair j of a head, (x_j, x_{j + rot/2}) or (x_2j, x_{2j+1}), is turned by the angle pos·θ_j:
+//   y_a = m·(x_a cos − x_b sin),  y_b = m·(x_a sin + x_b cos);  dims past rot pass through.
+// The queries go to q_out; the keys, rounded to bf16, and the values go to their pool slots as
+// the plain append writes them, so rope + append is bit for bit the two steps in a row.
+//
+// Angles: θ_j is given in turns per position as an fp32 pair hi + lo (48 bits).  p = pos·hi has
+// its rounding error in one fma, so frac(p) + error + pos·lo is the position's place in the turn to
+// about 2^-25 for every pos < 2^24, where a single fp32 product is off by up to pos·θ·2^-24 radians
+// (0.008 at position 131,072).  cos and sin come once per (token, pair) and serve every head.
+//
+// Bound: HBM, 4·128 B per query row and 8·128 B per (token, KV head) against a few FMAs per element.
+#include "kvd_chunk.h"
+#include "kvd_common.cuh"
+
+namespace kvd {
+namespace {
+
+constexpr int kTok = 16;               // tokens per CTA: the most that share a block
+constexpr int kRopeThreads = 256;
+constexpr int kRowPad = kDh + 8;       // bf16 elements per staged row (bank spread)
+
+struct RopeSmem {
+    float2 cs[kTok][kDh / 2];                              // (cos, sin)·m per (token, pair)
+    __align__(16) uint16_t krow[2][kTok][kRowPad];         // rotated K rows of one head, then its V rows
+    int64_t slot[kTok];
+    int src[kBs];                                          // the token that goes to slot offset t, or -1
+    int ok[kTok];                                          // the token takes part
+    int shared_offset;                                     // two tokens want the same slot offset
+};
+
+// One row of 128 values by 16 lanes, 8 consecutive dims each (lane16 = lane % 16), rotated in fp32
+// and rounded to bf16.
+template <bool INTERLEAVED>
+__device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2* cs, int rot, int lane16) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t out[4];
+    if constexpr (INTERLEAVED) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = lane16 * 8 + 2 * i;
+            const float2 x = unpack_bf16(w[i]);
+            out[i] = w[i];
+            if (d < rot) {
+                const float2 c = cs[d >> 1];
+                out[i] = pack_bf16(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+            }
+        }
+        return make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    const int half = rot >> 1;
+    float x[8], y[8];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack_bf16(w[i]);
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
+    }
+    const int lane = threadIdx.x & 31;
+    // The partner of dim d is d + half (d < half) or d − half.  Its lane and word are fetched by
+    // shuffles: with half = 8·hl + hr the element at offset e has its partner at offset e ± hr, one
+    // lane further when that leaves the lane's eight.
+    const int hl = half >> 3, hr = half & 7;
+    const int base = lane & 16;
+    if (hr == 0) {
+        const bool low = lane16 < hl;
+        const int other = base | ((low ? lane16 + hl : lane16 - hl) & 15);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 pv = unpack_bf16(__shfl_sync(kFull, w[i], other));
+            #pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int e = 2 * i + k, d = lane16 * 8 + e;
+                const float b = k ? pv.y : pv.x;
+                y[e] = x[e];
+                if (d < rot) {
+                    const float2 c = cs[low ? d : d - half];
+                    y[e] = low ? x[e] * c.x - b * c.y : b * c.y + x[e] * c.x;
+                }
+            }
+        }
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int d = lane16 * 8 + e;
+            const bool low = d < half;
+            const int pd = (low ? d + half : d - half) & (kDh - 1);
+            // every lane reads the wanted word of its partner lane: four shuffles, one selected
+            uint32_t pw = 0;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = __shfl_sync(kFull, w[i], base | (pd >> 3));
+                if (((pd & 7) >> 1) == i) pw = v;
+            }
+            const float2 pv = unpack_bf16(pw);
+            const float b = (pd & 1) ? pv.y : pv.x;
+            y[e] = x[e];
+            if (d < rot) {
+                const float2 c = cs[low ? d : d - half];
+                y[e] = low ? x[e] * c.x - b * c.y : b * c.y + x[e] * c.x;
+            }
+        }
+    }
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // dims past rot keep their bits (a NaN's payload too)
+        const int d = lane16 * 8 + 2 * i;
+        const uint32_t v = pack_bf16(y[2 * i], y[2 * i + 1]);
+        out[i] = d + 1 < rot ? v : d >= rot ? w[i] : (v & 0xffffu) | (w[i] & 0xffff0000u);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int KIND, int NG>
+__device__ __forceinline__ int64_t record_size() {
+    constexpr int kBits = KIND == kKindInt4 ? 4 : 2;
+    return KIND == kKindFp8 || KIND == kKindAngle ? kRecordFp8
+           : is_lowbit(KIND)                      ? lowbit_record_bytes(kBits, NG)
+                                                  : kRecordBf16;
+}
+
+// The K and V rows of one token of one head, from shared memory, into its record: as the append.
+template <int KIND, int NG>
+__device__ __forceinline__ void put_token(const RopeParams& p, uint8_t* record, int64_t blk, int t,
+                                          const uint16_t* k, const uint16_t* v, int lane) {
+    if constexpr (is_lowbit(KIND)) {
+        write_token_lowbit<KIND == kKindInt4 ? 4 : 2, NG>(record, t, k, v, lane);
+    } else if constexpr (KIND == kKindAngle) {
+        write_token<kFmtE4m3, true>(record, t, k, v, lane);
+    } else if constexpr (KIND == kKindMixed) {
+        const int fmt = block_format(p.block_fmt[blk]);
+        if (fmt == kFmtBf16) write_token<kFmtBf16>(record, t, k, v, lane);
+        else if (fmt == kFmtE4m3) write_token<kFmtE4m3>(record, t, k, v, lane);
+        else if (fmt == kFmtE5m2) write_token<kFmtE5m2>(record, t, k, v, lane);
+        else if (lane == 0) report(p.err, KVD_ERR_OOB);
+    } else {
+        write_token<KIND == kKindFp8 ? kFmtE4m3 : kFmtBf16>(record, t, k, v, lane);
+    }
+}
+
+// CTA (tile of 16 tokens, group of heads).  Heads 0 .. n_q-1 of the list are query heads, the rest
+// KV heads.  Tiles start at a multiple of 16 slots behind the first token's block start, so a chunk
+// of one request fills whole blocks (a record's 16-byte pieces hold two or four of its tokens).
+template <int KIND, int NG, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
+    __shared__ RopeSmem s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t first = p.slot_mapping[0];
+    const int shift = first > 0 ? static_cast<int>(first % kBs) : 0;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTok - shift;
+    const int h0 = blockIdx.y * p.heads_per_cta;
+    const int h1 = min(h0 + p.heads_per_cta, p.n_q + p.n_kv);
+    if (tid < kTok) {
+        const int64_t n = n0 + tid;
+        int ok = n >= 0 && n < p.n_tokens;
+        int64_t slot = -1;
+        if (ok) {
+            const int pos = p.positions[n];
+            if (pos < 0 || pos >= kMaxRopePos) {
+                if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
+                ok = 0;
+            } else {
+                slot = p.slot_mapping[n];
+                if (slot >= 0 && slot / kBs >= p.num_blocks + p.host_blocks) {
+                    if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
+                    slot = -1;
+                }
+            }
+        }
+        s.ok[tid] = ok;
+        s.slot[tid] = slot;
+    }
+    __syncthreads();
+    if (h1 > p.n_q && tid < kBs) {   // slot offset -> token
+        int found = -1, twice = 0;
+        for (int i = 0; i < kTok; ++i) {
+            if (s.slot[i] >= 0 && s.slot[i] % kBs == tid) {
+                twice |= found >= 0;
+                found = i;
+            }
+        }
+        s.src[tid] = found;
+        const unsigned any = __ballot_sync(0xffffu, twice);
+        if (tid == 0) s.shared_offset = any != 0;
+    }
+    const int pairs = p.rot >> 1;
+    for (int i = tid; i < kTok * pairs; i += kRopeThreads) {
+        const int tk = i / pairs, j = i % pairs;
+        float2 c = make_float2(0.f, 0.f);
+        if (s.ok[tk]) {
+            const float pos = static_cast<float>(p.positions[n0 + tk]);
+            const float2 f = p.turns[j];
+            const float a = __fmul_rn(pos, f.x);
+            const float rest = __fmaf_rn(pos, f.x, -a);
+            const float turn = __fadd_rn(__fsub_rn(a, rintf(a)), __fmaf_rn(pos, f.y, rest));
+            float sn, cn;
+            sincospif(2.f * turn, &sn, &cn);
+            c = make_float2(cn * p.mscale, sn * p.mscale);
+        }
+        s.cs[tk][j] = c;
+    }
+    __syncthreads();
+    const int half_id = tid >> 4, lane16 = tid & 15;   // 16 half-warps, a row each
+    for (int h = h0; h < h1; ++h) {
+        if (h < p.n_q) {
+            const int tk = half_id;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (s.ok[tk])
+                x = *reinterpret_cast<const uint4*>(p.q + (n0 + tk) * p.q_stride + h * kDh + lane16 * 8);
+            x = rotate_row<INTERLEAVED>(x, s.cs[tk], p.rot, lane16);
+            if (s.ok[tk])
+                *reinterpret_cast<uint4*>(p.q_out + (n0 + tk) * p.q_out_stride + h * kDh + lane16 * 8) = x;
+            continue;
+        }
+        const int kh = h - p.n_q;
+        {
+            const int tk = half_id;
+            uint4 k = make_uint4(0, 0, 0, 0), v = k;
+            if (s.slot[tk] >= 0) {
+                k = *reinterpret_cast<const uint4*>(p.k + (n0 + tk) * p.k_stride + kh * kDh + lane16 * 8);
+                v = *reinterpret_cast<const uint4*>(p.v + (n0 + tk) * p.v_stride + kh * kDh + lane16 * 8);
+            }
+            k = rotate_row<INTERLEAVED>(k, s.cs[tk], p.rot, lane16);
+            *reinterpret_cast<uint4*>(&s.krow[0][tk][lane16 * 8]) = k;
+            *reinterpret_cast<uint4*>(&s.krow[1][tk][lane16 * 8]) = v;
+        }
+        __syncthreads();
+        const int64_t kRec = record_size<KIND, NG>();
+        auto record = [&](int tk) -> uint8_t* {
+            const int64_t blk = s.slot[tk] / kBs;
+            return blk < p.num_blocks ? p.kv + (blk * p.n_kv + kh) * kRec
+                                      : p.host_kv + ((blk - p.num_blocks) * p.n_kv + kh) * kRec;
+        };
+        if (KIND == kKindBf16 && !s.shared_offset) {
+            // 16-byte pieces of the two tiles: a K piece holds dims (2x, 2x+1, 2x+8, 2x+9) of tokens
+            // t and t + 8, a V piece tokens (2x, 2x+1, 2x+8, 2x+9) of dims r and r + 8.  Whole
+            // pieces where their tokens go to the same record, smaller stores where they do not.
+            for (int c = tid; c < 512; c += kRopeThreads) {
+                const int i = (c >> 5) & 7, l = c & 31, x = l & 3, r = l >> 2;
+                if (c < 256) {
+                    const int ta = s.src[r], tb = s.src[r + 8];
+                    const int d = 16 * i + 2 * x;
+                    uint32_t a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+                    if (ta >= 0) {
+                        a0 = *reinterpret_cast<const uint32_t*>(&s.krow[0][ta][d]);
+                        a1 = *reinterpret_cast<const uint32_t*>(&s.krow[0][ta][d + 8]);
+                    }
+                    if (tb >= 0) {
+                        b0 = *reinterpret_cast<const uint32_t*>(&s.krow[0][tb][d]);
+                        b1 = *reinterpret_cast<const uint32_t*>(&s.krow[0][tb][d + 8]);
+                    }
+                    uint8_t* pa = ta >= 0 ? record(ta) : nullptr;
+                    uint8_t* pb = tb >= 0 ? record(tb) : nullptr;
+                    if (pa == pb) {
+                        if (pa) *reinterpret_cast<uint4*>(pa + c * 16) = make_uint4(a0, b0, a1, b1);
+                    } else {
+                        if (pa) {
+                            *reinterpret_cast<uint32_t*>(pa + c * 16) = a0;
+                            *reinterpret_cast<uint32_t*>(pa + c * 16 + 8) = a1;
+                        }
+                        if (pb) {
+                            *reinterpret_cast<uint32_t*>(pb + c * 16 + 4) = b0;
+                            *reinterpret_cast<uint32_t*>(pb + c * 16 + 12) = b1;
+                        }
+                    }
+                } else {
+                    const int d = 16 * i + r;
+                    uint16_t lo[4], hi[4];
+                    uint8_t* rec[4];
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tk = s.src[2 * x + (k & 1) + 8 * (k >> 1)];
+                        rec[k] = tk >= 0 ? record(tk) : nullptr;
+                        lo[k] = tk >= 0 ? s.krow[1][tk][d] : 0;
+                        hi[k] = tk >= 0 ? s.krow[1][tk][d + 8] : 0;
+                    }
+                    const int off = c * 16;   // the V tile follows the K tile: pieces 256 .. 511
+                    auto two = [](uint16_t a, uint16_t b) { return a | (static_cast<uint32_t>(b) << 16); };
+                    if (rec[0] == rec[1] && rec[0] == rec[2] && rec[0] == rec[3]) {
+                        if (rec[0])
+                            *reinterpret_cast<uint4*>(rec[0] + off) =
+                                make_uint4(two(lo[0], lo[1]), two(hi[0], hi[1]), two(lo[2], lo[3]), two(hi[2], hi[3]));
+                    } else {
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (!rec[k]) continue;
+                            const int at = off + (k & 1) * 2 + (k >> 1) * 8;
+                            *reinterpret_cast<uint16_t*>(rec[k] + at) = lo[k];
+                            *reinterpret_cast<uint16_t*>(rec[k] + at + 4) = hi[k];
+                        }
+                    }
+                }
+            }
+        } else {
+            for (int tk = warp; tk < kTok; tk += kRopeThreads / 32) {
+                if (s.slot[tk] < 0) continue;
+                put_token<KIND, NG>(p, record(tk), s.slot[tk] / kBs, static_cast<int>(s.slot[tk] % kBs), s.krow[0][tk],
+                                    s.krow[1][tk], lane);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int KIND, int NG>
+cudaError_t launch(const RopeParams& p, dim3 grid, cudaStream_t stream) {
+    return p.interleaved ? launch_dependent(rope_append_kernel<KIND, NG, true>, grid, dim3(kRopeThreads), 0, -1, stream, p)
+                         : launch_dependent(rope_append_kernel<KIND, NG, false>, grid, dim3(kRopeThreads), 0, -1, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(RopeParams p, int kind, int num_sms, cudaStream_t stream) {
+    const int64_t tiles = (p.n_tokens + kTok - 1) / kTok + 1;   // one more: the first tile may start before token 0
+    const int heads = p.n_q + p.n_kv;
+    p.heads_per_cta = 8;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + p.heads_per_cta - 1) / p.heads_per_cta));
+    (void)num_sms;
+    switch (kind) {
+        case kKindFp8: return launch<kKindFp8, 1>(p, grid, stream);
+        case kKindMixed: return launch<kKindMixed, 1>(p, grid, stream);
+        case kKindAngle: return launch<kKindAngle, 1>(p, grid, stream);
+        case kKindInt4:
+            return p.ng == 4   ? launch<kKindInt4, 4>(p, grid, stream)
+                   : p.ng == 2 ? launch<kKindInt4, 2>(p, grid, stream)
+                               : launch<kKindInt4, 1>(p, grid, stream);
+        case kKindInt2:
+            return p.ng == 4   ? launch<kKindInt2, 4>(p, grid, stream)
+                   : p.ng == 2 ? launch<kKindInt2, 2>(p, grid, stream)
+                               : launch<kKindInt2, 1>(p, grid, stream);
+        default: return launch<kKindBf16, 1>(p, grid, stream);
+    }
+}
+
+}  // namespace kvd
