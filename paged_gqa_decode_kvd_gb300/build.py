@@ -17,8 +17,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvd.so")
 SOURCES = ["kvd_api.cu", "kvd_append.cu", "kvd_decode.cu", "kvd_decode_lowbit.cu", "kvd_combine.cu", "kvd_noalloc.cu",
-           "kvd_tier.cu", "kvd_measure.cu", "kvd_rope.cu", "kvd_chunk.cu", "kvd_compact.cu"]
-HEADERS = ["kvd_common.cuh", "kvd_internal.h", "kvd_decode_kernel.cuh", "kvd_chunk.h", os.path.join("..", "..", "include", "kvd.h")]
+           "kvd_tier.cu", "kvd_measure.cu", "kvd_rope.cu", "kvd_chunk.cu",
+           "kvd_chunk_lowbit.cu", "kvd_compact.cu"]
+HEADERS = ["kvd_common.cuh", "kvd_internal.h", "kvd_decode_kernel.cuh", "kvd_chunk.h", "kvd_tcgen.cuh",
+           "kvd_chunk_kernel.cuh", os.path.join("..", "..", "include", "kvd.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr"]
 

@@ -690,11 +690,26 @@ static kvd_status check_chunk_shape(const kvd_pool* pool, int n_q, int batch) {
     return KVD_OK;
 }
 
+struct ChunkLayout {
+    size_t part, ml, seg, total;
+};
+
+// Two partials a CTA (its first and its last unit may be cut), one CTA per SM.
+static ChunkLayout chunk_layout(const kvd_pool* pool) {
+    const size_t slots = 2 * static_cast<size_t>(pool->num_sms);
+    ChunkLayout w;
+    w.part = 0;
+    w.ml = align256(w.part + slots * kvd::kDh * kvd::kChunkUnitRows * sizeof(float));
+    w.seg = align256(w.ml + slots * 2 * kvd::kChunkUnitRows * sizeof(float));
+    w.total = align256(w.seg + slots * sizeof(int4));
+    return w;
+}
+
 kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int batch, size_t* bytes_out) {
     kvd_status st = check_chunk_shape(pool, n_q, batch);
     if (st != KVD_OK) return st;
     if (!bytes_out) return KVD_ERR_INVALID;
-    *bytes_out = 256;
+    *bytes_out = chunk_layout(pool).total;
     return KVD_OK;
 }
 
@@ -730,6 +745,12 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
     p.err = pool->err;
     p.num_blocks = pool->desc.num_blocks;
     p.host_blocks = pool->host_blocks;
+    const ChunkLayout w = chunk_layout(pool);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part = reinterpret_cast<float*>(ws + w.part);
+    p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+    p.part_seg = reinterpret_cast<int4*>(ws + w.seg);
+    p.host_direct = pool->host_blocks ? pool->host_direct : 0;
     p.record_bytes = static_cast<int64_t>(record_bytes(&pool->desc));
     p.n_tokens = n_tokens;
     p.max_blocks = max_blocks_per_seq;
@@ -740,7 +761,7 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
     p.ng = pool_ng(&pool->desc);
     p.out_f32 = out_dtype == KVD_F32;
     p.scale_log2 = softmax_scale * kvd::kLog2e;
-    return cuda_status(kvd::launch_chunk(p, pool_kind(pool), static_cast<cudaStream_t>(stream)));
+    return cuda_status(kvd::launch_chunk(p, pool_kind(pool), pool->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 static kvd_status compact_layout(const kvd_pool* pool, int batch, int max_blocks_per_seq, size_t* claim_off, size_t* total) {

@@ -45,10 +45,14 @@ struct ChunkParams {
     const uint16_t* retain;      // [num_blocks + host_blocks] or null
     void* out;
     float* lse_out;
+    float* part;                 // workspace: [2·CTAs][128 dims][256 rows] unnormalised sums
+    float* part_ml;              // workspace: [2·CTAs][2][256] maximum (log2 domain), sum of weights
+    int4* part_seg;              // workspace: [2·CTAs] (request or −1, head | unit << 16, first tile, end tile)
     int32_t* err;
     int64_t num_blocks;
     int64_t host_blocks;
     int64_t record_bytes;
+    int host_direct;             // host-tier records are read from host memory, by cp.async
     int n_tokens;
     int max_blocks;
     int B;
@@ -59,7 +63,9 @@ struct ChunkParams {
     int out_f32;
     float scale_log2;            // softmax_scale·log2(e)
 };
-cudaError_t launch_chunk(const ChunkParams& p, int kind, cudaStream_t stream);
+constexpr int kChunkUnitRows = 256;    // rows of a unit of work
+cudaError_t launch_chunk(const ChunkParams& p, int kind, int ctas, cudaStream_t stream);
+cudaError_t launch_chunk_lowbit(const ChunkParams& p, int kind, int ctas, cudaStream_t stream);   // INT4 / INT2
 
 struct CompactParams {
     const int32_t* block_table;  // [B][max_blocks]

@@ -1,0 +1,1072 @@
+// kvd_chunk_kernel.cuh — causal attention of a chunk of new tokens over the paged cache: the kernel
+// template shared by the translation units that instantiate its pool kinds.
+//
+// Row (token i of the T new tokens of request b, query head h): with len = seq_lens[b] and
+// position P = len − T + i,
+//   l_t = softmax_scale · q·K_t for t ≤ P (−inf where slot t is evicted),
+//   out = Σ_t softmax(l)_t · V_t,  lse = log Σ_t exp(l_t).
+//
+// Work.  A unit is (request, KV head, TQ = ⌊256/g⌋ new tokens): up to 256 rows (token, head of the
+// group) that share every K and V.  Its cost is its tiles of 64 positions up to its last row's.  The
+// units' tiles, laid end to end, are cut into equal ranges, one per CTA (one CTA per SM), so every
+// CTA does the same number of tiles whatever the batch holds; a unit cut by a range border leaves
+// fp32 partials (unnormalised sum, maximum, sum of weights) that chunk_combine_kernel joins.
+//
+// One CTA, four roles:
+//  * producer warp: follows the block table and bulk-copies (TMA engine) the four 16-token records
+//    of a tile into a raw ring;
+//  * repack warpgroup: turns the records' mma.m16n8k16 fragment order into the 128-byte-swizzled
+//    K-major operands the tensor cores read, by 16-byte shared loads and stores and register renaming
+//    only.  A K piece holds four dims of tokens t and t + 8: two pieces give eight dims of each, so
+//    the operand's dims stand in the order 32j + {2x, 2x+1, 2x+8, 2x+9, 16 + the same} (q is laid
+//    out alike, the product does not care).  A V piece holds four tokens of dims r and r + 8: the pieces
+//    of two blocks give eight tokens of each, which fixes the order of a tile's 64 columns:
+//    column 32p + 8x + 4u + w = token 2x + (w & 1) + 8(w >> 1) of block 2p + u.  8-bit codes become
+//    bf16 exactly on the way; low-bit codes become bf16(code·scale + zero);
+//  * MMA warp: one thread issues S = Q·K^T and O += P·V, Q and P from tensor memory (reading them
+//    from shared memory would take its whole bandwidth), accumulators in tensor memory;
+//  * two softmax warpgroups, one thread a row: online softmax in fp32 (exp2 domain), P back to tensor
+//    memory as bf16.  The reference maximum moves only when a row's maximum passes it by 8 (weights up
+//    to 2^8), so O is rarely rescaled.
+// With more than 128 rows the warpgroups take 128 rows each and share every tile; with fewer they
+// take the even and the odd tiles of the same rows and are merged at the unit's end.
+//
+// 8-bit records: the K scale multiplies the fp32 logit, the V scale the fp32 weight before it is
+// rounded, so codes enter the MMAs exactly.  Angle-domain keys: q enters as its direction code, with
+// ||q||/||d_q|| in the row's scale and the key's factor in the column's.
+//
+// Masked positions: logits become −inf by selection and V is zeroed, so what a slot holds does not
+// matter.  Inside the chunk a token's V is attended by later rows and masked for earlier ones, and
+// 0·NaN would reach the earlier ones: non-finite V there is zeroed too, noted, and added at the end
+// to the rows that attend it.
+#pragma once
+
+#include "kvd_chunk.h"
+#include "kvd_tcgen.cuh"
+
+namespace kvd {
+namespace chunk {
+
+constexpr int kTile = 64;              // positions per tile: four blocks
+constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
+constexpr int kUnitRows = 2 * kWgRows;
+constexpr int kThreads = 448;          // softmax 2 × 128, repack 128, producer 32, MMA 32
+constexpr int kRepackWarp = 8, kProducerWarp = 12, kMmaWarp = 13;
+constexpr int kStages = 3;             // operand stages (K 16 KiB + V 16 KiB)
+constexpr int kOpBytes = 16384;
+constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kColS = 0, kColO = 128, kColQ = 384;   // tensor memory columns: S/P 2 × 64, O 2 × 128, Q 2 × 64
+constexpr int kMinTiles = 4;           // smallest share of a CTA
+
+constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
+constexpr int raw_stages(int kind) { return kind == kKindBf16 ? 4 : kind == kKindMixed ? 3 : 6; }
+constexpr int max_record(int kind) {
+    return kind == kKindBf16 || kind == kKindMixed ? kRecordBf16
+           : kind == kKindInt4                     ? lowbit_record_bytes(4, 4)
+           : kind == kKindInt2                     ? lowbit_record_bytes(2, 4)
+                                                   : kRecordFp8;
+}
+
+struct StageInfo {
+    unsigned long long mask;     // bit 16·block + t: position may be attended
+    unsigned long long nonfin[4];   // by repack warp; column n: its V has non-finite elements, zeroed in the operand
+};
+
+template <int KIND>
+struct Smem {
+    uint8_t op[kStages][2][kOpBytes];                           // K, V operands; 1,024-byte aligned
+    uint8_t raw[raw_stages(KIND)][4][max_record(KIND)];
+    float factor[has_factors(KIND) ? kStages : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
+    float ml[2][kWgRows];                                       // merge: WG 1's maximum and sum
+    uint32_t meta[raw_stages(KIND)][4];                         // block words
+    StageInfo info[kStages];
+    uint64_t raw_full[raw_stages(KIND)], raw_empty[raw_stages(KIND)];
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t q_ready[2], merge_full, merge_empty, drain;
+    int64_t remaining;
+    int b, h, qt, off;
+    uint32_t tmem;
+    int abort;
+};
+
+// ------------------------------------------------------------------ schedule
+// Σ_{i<n} ⌊(a·i + c)/m⌋.
+__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t c) {
+    int64_t ans = 0;
+    if (n <= 0) return 0;
+    while (true) {
+        ans += n * (n - 1) / 2 * (a / m) + n * (c / m);
+        a %= m;
+        c %= m;
+        const int64_t y = a * n + c;
+        if (y < m) return ans;
+        n = y / m;
+        c = y % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+}
+
+struct Request {
+    int s0, T, len;   // first row, new tokens, context (−1: bad length, nothing is attended)
+};
+
+__device__ __forceinline__ Request load_request(const ChunkParams& p, int b, bool tell) {
+    Request r;
+    r.s0 = p.q_start[b];
+    const int s1 = p.q_start[b + 1];
+    r.T = 0;
+    r.len = -1;
+    if (r.s0 < 0 || s1 < r.s0 || s1 > p.n_tokens) {
+        if (tell) report(p.err, KVD_ERR_OOB);
+        return r;
+    }
+    r.T = s1 - r.s0;
+    if (r.T == 0) return r;
+    r.len = p.seq_lens[b];
+    if (r.len < r.T || static_cast<int64_t>(r.len) > static_cast<int64_t>(p.max_blocks) * kBs) {
+        if (tell) report(p.err, KVD_ERR_OOB);
+        r.len = -1;
+    }
+    return r;
+}
+__device__ __forceinline__ int unit_end(const Request& r, int qt, int tq) {   // positions the unit attends
+    return r.len < 0 ? 0 : r.len - r.T + min((qt + 1) * tq, r.T);
+}
+__device__ __forceinline__ int unit_tiles(const Request& r, int qt, int tq) {
+    return r.len < 0 ? 1 : (unit_end(r, qt, tq) + kTile - 1) / kTile;
+}
+__device__ inline int64_t tiles_before(const Request& r, int k, int tq) {   // tiles of units 0 .. k-1 of one head
+    if (r.len < 0) return k;
+    const int n = (r.T + tq - 1) / tq;
+    const int whole = min(k, n - 1);
+    int64_t s = floor_sum(whole, kTile, tq, static_cast<int64_t>(r.len) - r.T + tq + kTile - 1);
+    if (k == n) s += unit_tiles(r, n - 1, tq);
+    return s;
+}
+
+struct Segment {
+    int b, h, qt;
+    int t0, t1, tiles;       // this CTA's tiles of the unit's
+    int s0, T, len;
+    int end;                 // positions the unit attends
+    int first;               // position of its first row
+    int tok0, rows;
+    bool two;                // the warpgroups take 128 rows each
+};
+
+// The CTA's segments in order; every role walks them on its own.
+struct Walk {
+    int64_t remaining;
+    int b, h, qt, off;
+    Request r;
+    template <class S>
+    __device__ __forceinline__ Walk(const ChunkParams& p, const S& s)
+        : remaining(s.remaining), b(s.b), h(s.h), qt(s.qt), off(s.off) {
+        if (remaining > 0) r = load_request(p, b, false);
+    }
+    __device__ __forceinline__ bool next(const ChunkParams& p, Segment& g) {
+        if (remaining <= 0) return false;
+        const int tq = kUnitRows / p.g;
+        g.b = b;
+        g.h = h;
+        g.qt = qt;
+        g.tiles = unit_tiles(r, qt, tq);
+        g.t0 = off;
+        g.t1 = static_cast<int>(min(static_cast<int64_t>(g.tiles), off + remaining));
+        g.s0 = r.s0;
+        g.T = r.T;
+        g.len = r.len;
+        g.end = unit_end(r, qt, tq);
+        g.tok0 = qt * tq;
+        g.first = r.len < 0 ? -1 : r.len - r.T + g.tok0;
+        g.rows = min(tq, r.T - g.tok0) * p.g;
+        g.two = g.rows > kWgRows;
+        remaining -= g.t1 - g.t0;
+        off = 0;
+        if (remaining > 0) {
+            if (++qt * tq >= r.T) {
+                qt = 0;
+                if (++h == p.n_kv) {
+                    h = 0;
+                    do {
+                        if (++b >= p.B) {
+                            remaining = 0;
+                            return true;
+                        }
+                        r = load_request(p, b, false);
+                    } while (r.T == 0);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// A CTA's share of the schedule, by every thread of the block; scratch holds p.B int64.
+template <class S>
+__device__ inline void make_schedule(const ChunkParams& p, S& s, int64_t* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int tq = kUnitRows / p.g;
+    for (int b = tid; b < p.B; b += kThreads) {
+        const Request r = load_request(p, b, blockIdx.x == 0);
+        scratch[b] = r.T ? tiles_before(r, (r.T + tq - 1) / tq, tq) * p.n_kv : 0;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        int64_t total = 0;
+        for (int b = lane; b < p.B; b += 32) total += scratch[b];
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+        const int64_t most = (total + kMinTiles - 1) / kMinTiles;
+        const int64_t ctas = most < gridDim.x ? (most < 1 ? 1 : most) : gridDim.x;
+        const int64_t lo = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
+        const int64_t hi = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+        if (lane == 0) s.remaining = hi - lo;
+        int64_t before = 0;
+        for (int b0 = 0; hi > lo && b0 < p.B; b0 += 32) {
+            const int64_t c = b0 + lane < p.B ? scratch[b0 + lane] : 0;
+            int64_t up = c;
+            #pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(kFull, up, o);
+                if (lane >= o) up += v;
+            }
+            up += before;
+            if (lo >= up - c && lo < up) {
+                const int b = b0 + lane;
+                const Request r = load_request(p, b, false);
+                const int64_t head = c / p.n_kv, rem = lo - (up - c);
+                const int64_t in = rem % head;
+                int a = 0, z = (r.T + tq - 1) / tq - 1;   // the last unit that starts at or before `in`
+                while (a < z) {
+                    const int mid = (a + z + 1) / 2;
+                    if (tiles_before(r, mid, tq) <= in) a = mid;
+                    else z = mid - 1;
+                }
+                s.b = b;
+                s.h = static_cast<int>(rem / head);
+                s.qt = a;
+                s.off = static_cast<int>(in - tiles_before(r, a, tq));
+            }
+            before = __shfl_sync(kFull, up, 31);
+            if (before > lo) break;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- repack
+// Column of token t of block k of a tile, and the position within the tile of a column.
+__host__ __device__ constexpr int column_of(int k, int t) {
+    return 32 * (k >> 1) + 8 * ((t & 7) >> 1) + 4 * (k & 1) + (t & 1) + 2 * (t >> 3);
+}
+__host__ __device__ constexpr int place_of(int n) {
+    return 16 * (2 * (n >> 5) + ((n >> 2) & 1)) + 2 * ((n >> 3) & 3) + (n & 1) + 8 * ((n >> 1) & 1);
+}
+
+__device__ __forceinline__ void put16(uint8_t* base, int row, int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    *reinterpret_cast<uint4*>(base + row * 128 + ((piece ^ (row & 7)) << 4)) = make_uint4(a, b, c, d);
+}
+__device__ __forceinline__ void put_k(uint8_t* op, int n, int j, int x, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    put16(op + (j >> 1) * 8192, n, 4 * (j & 1) + x, a, b, c, d);
+}
+
+__device__ __forceinline__ uint32_t pair_mask(uint32_t m, int t) {
+    return ((m >> t & 1u) ? 0xffffu : 0u) | ((m >> (t + 1) & 1u) ? 0xffff0000u : 0u);
+}
+
+struct VPut {
+    uint8_t* op;
+    unsigned long long bad;    // columns with non-finite elements
+    bool look;                 // the tile holds positions some rows attend and others do not
+    // Tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p and 2p+1, dim d; valid bits of the two blocks.
+    __device__ __forceinline__ void put(int d, int p, int x, uint32_t a, uint32_t b, uint32_t c, uint32_t e, uint32_t m0,
+                                        uint32_t m1) {
+        if ((m0 & m1) != 0xffffu) {
+            a &= pair_mask(m0, 2 * x);
+            b &= pair_mask(m0, 2 * x + 8);
+            c &= pair_mask(m1, 2 * x);
+            e &= pair_mask(m1, 2 * x + 8);
+        }
+        if (look) {
+            uint32_t w[4] = {a, b, c, e};
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if ((w[i] >> (16 * k) & 0x7f80u) == 0x7f80u) {
+                        bad |= 1ull << (32 * p + 8 * x + 2 * i + k);
+                        w[i] &= k ? 0x0000ffffu : 0xffff0000u;
+                    }
+                }
+            }
+            a = w[0];
+            b = w[1];
+            c = w[2];
+            e = w[3];
+        }
+        put16(op, d, 4 * p + x, a, b, c, e);
+    }
+};
+
+// Four 8-bit codes -> two packed bf16 pairs, exact.  An E4M3 (E5M2) code is moved into a bf16's sign,
+// exponent and mantissa bits and scaled by 2^120 (2^112), the difference of the exponent biases;
+// codes with the top exponent pattern that are not numbers go through the conversion instruction.
+template <int FMT>
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    constexpr uint32_t kBits = FMT == kFmtE5m2 ? 0x0fe00fe0u : 0x07f007f0u;
+    constexpr int kShift = FMT == kFmtE5m2 ? 3 : 4;
+    constexpr uint32_t kUp = FMT == kFmtE5m2 ? 0x77807780u : 0x7b807b80u;
+    const uint32_t special = FMT == kFmtE5m2 ? ((w & 0x7c7c7c7cu) + 0x04040404u) & 0x80808080u
+                                             : ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    if (special) {
+        uint32_t a, b;
+        f8x4_to_f16x2x2<FMT>(w, a, b);
+        const float2 x = unpack_f16(a), y = unpack_f16(b);
+        lo = pack_bf16(x.x, x.y);
+        hi = pack_bf16(y.x, y.y);
+        return;
+    }
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+    uint32_t pa = ((a >> kShift) & kBits) | (a & 0x80008000u), pb = ((b >> kShift) & kBits) | (b & 0x80008000u);
+    const __nv_bfloat162 up = *reinterpret_cast<const __nv_bfloat162*>(&kUp);
+    __nv_bfloat162 ra = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&pa), up);
+    __nv_bfloat162 rb = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&pb), up);
+    lo = *reinterpret_cast<uint32_t*>(&ra);
+    hi = *reinterpret_cast<uint32_t*>(&rb);
+}
+
+// K of block k (its record, 16-bit or 8-bit) by one warp.
+template <int FMT>
+__device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, int k, int lane) {
+    const int x = lane & 3, j0 = (lane >> 2) & 1, tl = lane >> 3;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // lanes of an eight read one 64-byte half each and write all eight pieces of two rows' line
+        const int t = 2 * tl + ((i & 1) ^ j0), j = 2 * (i >> 1) + j0;
+        const int n = column_of(k, t);
+        if constexpr (FMT == kFmtBf16) {
+            const uint4 a = *reinterpret_cast<const uint4*>(rec + ((2 * j) * 32 + 4 * t + x) * 16);
+            const uint4 b = *reinterpret_cast<const uint4*>(rec + ((2 * j + 1) * 32 + 4 * t + x) * 16);
+            put_k(op, n, j, x, a.x, a.z, b.x, b.z);
+            put_k(op, n + 2, j, x, a.y, a.w, b.y, b.w);
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(rec + (j * 32 + 4 * t + x) * 16);
+            uint32_t lo[4], hi[4];
+            codes_to_bf16<FMT>(a.x, lo[0], hi[0]);
+            codes_to_bf16<FMT>(a.y, lo[1], hi[1]);
+            codes_to_bf16<FMT>(a.z, lo[2], hi[2]);
+            codes_to_bf16<FMT>(a.w, lo[3], hi[3]);
+            put_k(op, n, j, x, lo[0], lo[1], lo[2], lo[3]);
+            put_k(op, n + 2, j, x, hi[0], hi[1], hi[2], hi[3]);
+        }
+    }
+}
+
+// A V piece of two dims as bf16: group i (dims 16i + r and 16i + r + 8), lane 4r + x: tokens
+// (2x, 2x+1) of dim r, of dim r + 8, tokens (2x+8, 2x+9) of dim r, of dim r + 8.
+template <int FMT>
+__device__ __forceinline__ uint4 v_piece(const uint8_t* rec, int i, int l) {
+    if constexpr (FMT == kFmtBf16) {
+        return *reinterpret_cast<const uint4*>(rec + kTileBf16 + (i * 32 + l) * 16);
+    } else {
+        const uint2 a = *reinterpret_cast<const uint2*>(rec + kTileFp8 + ((i >> 1) * 32 + l) * 16 + (i & 1) * 8);
+        uint4 o;
+        codes_to_bf16<FMT>(a.x, o.x, o.y);
+        codes_to_bf16<FMT>(a.y, o.z, o.w);
+        return o;
+    }
+}
+
+// V of the tile, groups 2·warp and 2·warp + 1, by one warp; f0, f1: formats of the two blocks.
+template <int KIND>
+__device__ __forceinline__ uint4 v_piece_kind(const uint8_t* rec, uint32_t word, int i, int l) {
+    if constexpr (KIND == kKindBf16) {
+        return v_piece<kFmtBf16>(rec, i, l);
+    } else if constexpr (KIND == kKindMixed) {
+        const int f = (word >> 17) & 3u;
+        return f == kFmtBf16 ? v_piece<kFmtBf16>(rec, i, l)
+               : f == kFmtE4m3 ? v_piece<kFmtE4m3>(rec, i, l) : v_piece<kFmtE5m2>(rec, i, l);
+    } else {
+        return v_piece<kFmtE4m3>(rec, i, l);
+    }
+}
+template <int KIND>
+__device__ __forceinline__ void repack_v(const uint8_t (*rec)[max_record(KIND)], const uint32_t (&word)[4], VPut& out, int warp,
+                                         int lane) {
+    const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
+    const uint32_t w0 = word[2 * p], w1 = word[2 * p + 1];
+    const uint32_t m0 = w0 & 0xffffu, m1 = w1 & 0xffffu;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int group = 2 * warp + (i >> 1), r = 2 * rl + ((i & 1) ^ p);
+        const uint4 a = v_piece_kind<KIND>(rec[2 * p], w0, group, 4 * r + x);
+        const uint4 b = v_piece_kind<KIND>(rec[2 * p + 1], w1, group, 4 * r + x);
+        out.put(16 * group + r, p, x, a.x, a.z, b.x, b.z, m0, m1);
+        out.put(16 * group + r + 8, p, x, a.y, a.w, b.y, b.w, m0, m1);
+    }
+}
+
+// Low-bit codes: value = bf16(fp32(code·scale + zero)); one rounding, since the MMA takes bf16.
+template <int BITS>
+__device__ __forceinline__ uint32_t low_pair(uint32_t word, int h, int j, float2 sz0, float2 sz1) {
+    const uint32_t c0 = word >> (8 * j + BITS * h) & ((1u << BITS) - 1), c1 = word >> (8 * (j + 1) + BITS * h) & ((1u << BITS) - 1);
+    return pack_bf16(fmaf(static_cast<float>(c0), sz0.x, sz0.y), fmaf(static_cast<float>(c1), sz1.x, sz1.y));
+}
+template <int BITS>
+__device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, int k, int ng, int lane) {
+    constexpr int kPer = 8 / BITS, kTileB = lowbit_tile_bytes(BITS);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + 2 * kTileB);
+    const int x = lane & 3, r = lane >> 2;
+    const int n = column_of(k, r);
+    #pragma unroll
+    for (int kg = 0; kg < 8 / kPer; ++kg) {
+        #pragma unroll
+        for (int th = 0; th < 2; ++th) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + lowbit_word(kg, lane, th) * 4);
+            #pragma unroll
+            for (int q = 0; q < kPer / 2; ++q) {   // 32 dims each: one group of the row
+                const int j = kg * (kPer / 2) + q;
+                const float2 sz = unpack_f16(meta[(r + 8 * th) * ng + j * ng / 4]);
+                put_k(op, n + 2 * th, j, x, low_pair<BITS>(w, 2 * q, 0, sz, sz), low_pair<BITS>(w, 2 * q, 2, sz, sz),
+                      low_pair<BITS>(w, 2 * q + 1, 0, sz, sz), low_pair<BITS>(w, 2 * q + 1, 2, sz, sz));
+            }
+        }
+    }
+}
+template <int KIND, int BITS>
+__device__ __forceinline__ void repack_v_low(const uint8_t (*rec)[max_record(KIND)], const uint32_t (&word)[4], VPut& out,
+                                             int ng, int warp, int lane) {
+    constexpr int kPer = 8 / BITS, kTileB = lowbit_tile_bytes(BITS);
+    const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
+    #pragma unroll 1
+    for (int i = 0; i < 2; ++i) {   // eight groups of 16 dims: 2·warp and 2·warp + 1
+        const int group = 2 * warp + i, kg = group / kPer, h = group % kPer;
+        #pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int r = 2 * rl + (s ^ p);
+            uint32_t o[2][4];   // dims r, r + 8: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p, 2p+1
+            #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t* b = rec[2 * p + u];
+                const uint32_t* meta = reinterpret_cast<const uint32_t*>(b + 2 * kTileB) + kBs * ng;
+                const int gi = group * ng / 8;
+                #pragma unroll
+                for (int th = 0; th < 2; ++th) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(b + kTileB + lowbit_word(kg, 4 * r + x, th) * 4);
+                    const int t = 2 * x + 8 * th;
+                    const float2 s0 = unpack_f16(meta[t * ng + gi]), s1 = unpack_f16(meta[(t + 1) * ng + gi]);
+                    o[0][2 * u + th] = low_pair<BITS>(w, h, 0, s0, s1);
+                    o[1][2 * u + th] = low_pair<BITS>(w, h, 2, s0, s1);
+                }
+            }
+            const uint32_t m0 = word[2 * p] & 0xffffu, m1 = word[2 * p + 1] & 0xffffu;
+            out.put(16 * group + r, p, x, o[0][0], o[0][1], o[0][2], o[0][3], m0, m1);
+            out.put(16 * group + r + 8, p, x, o[1][0], o[1][1], o[1][2], o[1][3], m0, m1);
+        }
+    }
+}
+
+// -------------------------------------------------------------------- pool
+__device__ __forceinline__ const uint8_t* record_at(const ChunkParams& p, int64_t id, int h) {
+    return id < p.num_blocks ? p.kv + (id * p.n_kv + h) * p.record_bytes
+                             : p.stage + ((id - p.num_blocks) * p.n_kv + h) * p.record_bytes;
+}
+
+// Block word: bits 0-15 positions that may be attended, bit 16 the record is copied, bits 17-18 its
+// format (mixed pools).
+template <int KIND>
+__device__ __forceinline__ uint32_t block_word_of(const ChunkParams& p, int phys, int j, int end) {
+    if (phys < 0 || phys >= p.num_blocks + p.host_blocks) {
+        report(p.err, KVD_ERR_OOB);
+        return 0;
+    }
+    const int left = end - j * kBs;
+    uint32_t m = left >= kBs ? 0xffffu : (1u << left) - 1u;
+    if (p.retain) m &= p.retain[phys];
+    int f = kFmtBf16;
+    if constexpr (KIND == kKindMixed) {
+        f = block_format(p.block_fmt[phys]);
+        if (f < 0) {
+            report(p.err, KVD_ERR_OOB);
+            return 0;
+        }
+    }
+    return m ? m | 0x10000u | static_cast<uint32_t>(f) << 17 : 0u;
+}
+
+// V of (position, dim) as attention reads it: only for positions with non-finite values.
+template <int KIND>
+__device__ __noinline__ float pool_value(const ChunkParams& p, int b, int h, int pos, int d) {
+    const int phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+    const uint8_t* rec = record_at(p, phys, h);
+    const int t = pos % kBs;
+    int fl, fe;
+    const int i = v_frag_i(t, d, &fl, &fe);
+    if constexpr (is_lowbit(KIND)) {
+        constexpr int kBits = KIND == kKindInt4 ? 4 : 2, kT = lowbit_tile_bytes(kBits);
+        const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + 2 * kT) + kBs * p.ng;
+        const float2 sz = unpack_f16(meta[t * p.ng + d * p.ng / kDh]);
+        const uint32_t c = rec[kT + lowbit_v_byte(kBits, t, d)] >> (kBits * ((d / 16) % (8 / kBits))) & ((1 << kBits) - 1);
+        return static_cast<float>(c) * sz.x + sz.y;
+    } else {
+        int f = KIND == kKindBf16 ? kFmtBf16 : kFmtE4m3;
+        if constexpr (KIND == kKindMixed) f = block_format(p.block_fmt[phys]);
+        if (f == kFmtBf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec)[kBs * kDh + bf16_tile_index(i, fl, fe)]);
+        const __half_raw v = __nv_cvt_fp8_to_halfraw(rec[kTileFp8 + fp8_tile_index(i, fl, fe)], f == kFmtE5m2 ? __NV_E5M2 : __NV_E4M3);
+        return __half2float(__half(v)) * reinterpret_cast<const float*>(rec + 2 * kTileFp8)[kBs + t];
+    }
+}
+
+// ------------------------------------------------------------------ the roles
+template <int KIND>
+__device__ __forceinline__ bool wait_bar(Smem<KIND>& s, const ChunkParams& p, uint64_t* bar, uint32_t phase) {
+    if (mbar_wait(bar, phase & 1u, &s.abort, kWaitNs)) return true;
+    if (atomicExch(&s.abort, 1) == 0) report(p.err, KVD_ERR_TIMEOUT);
+    return false;
+}
+
+template <int KIND>
+__device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, int lane) {
+    constexpr int kRaw = raw_stages(KIND);
+    Walk walk(p, s);
+    Segment g;
+    uint32_t k = 0;
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const int32_t* row = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks;
+        for (int tb = g.t0; ok && tb < g.t1; tb += 8) {
+            const int j = 4 * tb + lane;   // 32 blocks: eight tiles
+            uint32_t word = 0;
+            const uint8_t* rec = nullptr;
+            bool host = false;
+            if (j < 4 * g.t1 && j * kBs < g.end) {
+                const int phys = row[j];
+                word = block_word_of<KIND>(p, phys, j, g.end);
+                if (word) rec = record_at(p, phys, g.h);
+                host = word && p.host_direct && phys >= p.num_blocks;
+            }
+            const int n = min(8, g.t1 - tb);
+            for (int i = 0; i < n; ++i, ++k) {
+                const int st = k % kRaw;
+                ok = wait_bar(s, p, &s.raw_empty[st], (k / kRaw) + 1);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                const bool mine = (lane >> 2) == i;
+                uint32_t bytes = 0;
+                if (mine) {
+                    s.meta[st][lane & 3] = word;
+                    if (word)
+                        bytes = KIND == kKindMixed && ((word >> 17) & 3u) != kFmtBf16 ? kRecordFp8
+                                                                                     : static_cast<uint32_t>(p.record_bytes);
+                }
+                uint32_t bulk = host ? 0 : bytes;
+                bulk += __shfl_xor_sync(kFull, bulk, 1);
+                bulk += __shfl_xor_sync(kFull, bulk, 2);
+                if (p.host_direct) {   // records in host memory: copied by the load path, the whole warp
+                    unsigned hosts = __ballot_sync(kFull, mine && host);
+                    fence_proxy_async_shared();
+                    while (hosts) {
+                        const int l = __ffs(hosts) - 1;
+                        hosts &= hosts - 1;
+                        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+                            __shfl_sync(kFull, reinterpret_cast<unsigned long long>(rec), l));
+                        for (int c = lane; c < p.record_bytes / 16; c += 32)
+                            cp_async16_g2s(s.raw[st][l & 3] + 16 * c, src + 16 * c);
+                    }
+                    cp_async_mbar_arrive(&s.raw_full[st]);
+                }
+                __syncwarp();
+                if (lane == 4 * i) {
+                    if (bulk) mbar_arrive_expect_tx(&s.raw_full[st], bulk);
+                    else mbar_arrive(&s.raw_full[st]);
+                }
+                __syncwarp();
+                if (mine && word && !host) bulk_copy(s.raw[st][lane & 3], rec, bytes, &s.raw_full[st]);
+            }
+        }
+    }
+    if (!ok) {   // the copies in flight land before the block leaves
+        const uint32_t from = k > kRaw ? k - kRaw : 0;
+        for (uint32_t i = from; i < k; ++i) mbar_wait(&s.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr, kWaitNs);
+    }
+}
+
+template <int KIND>
+__device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
+    constexpr int kRaw = raw_stages(KIND);
+    Walk walk(p, s);
+    Segment g;
+    uint32_t k = 0;
+    while (walk.next(p, g)) {
+        for (int t = g.t0; t < g.t1; ++t, ++k) {
+            const int st = k % kRaw, op = k % kStages;
+            bool ok = wait_bar(s, p, &s.kv_empty[op], (k / kStages) + 1) && wait_bar(s, p, &s.raw_full[st], k / kRaw);
+            if (!__all_sync(kFull, ok)) return;
+            uint32_t word[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) word[i] = s.meta[st][i];
+            const bool look = t * kTile + kTile - 1 > g.first;
+            if (warp == 0 && lane == 0) {
+                s.info[op].mask = static_cast<unsigned long long>(word[0] & 0xffffu) |
+                                  static_cast<unsigned long long>(word[1] & 0xffffu) << 16 |
+                                  static_cast<unsigned long long>(word[2] & 0xffffu) << 32 |
+                                  static_cast<unsigned long long>(word[3] & 0xffffu) << 48;
+            }
+            uint8_t* kop = s.op[op][0];
+            VPut v{s.op[op][1], 0ull, look};
+            const uint8_t* rec = s.raw[st][warp];
+            if constexpr (KIND == kKindBf16) {
+                repack_k<kFmtBf16>(rec, kop, warp, lane);
+                repack_v<KIND>(s.raw[st], word, v, warp, lane);
+            } else if constexpr (is_lowbit(KIND)) {
+                constexpr int kBits = KIND == kKindInt4 ? 4 : 2;
+                repack_k_low<kBits>(rec, kop, warp, p.ng, lane);
+                repack_v_low<KIND, kBits>(s.raw[st], word, v, p.ng, warp, lane);
+            } else {
+                int f = kFmtE4m3;
+                if constexpr (KIND == kKindMixed) f = (word[warp] >> 17) & 3u;
+                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(rec, kop, warp, lane);
+                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(rec, kop, warp, lane);
+                else repack_k<kFmtE4m3>(rec, kop, warp, lane);
+                repack_v<KIND>(s.raw[st], word, v, warp, lane);
+                if (lane < kBs) {
+                    const float* sc = reinterpret_cast<const float*>(rec + 2 * kTileFp8);
+                    const bool on = word[warp] >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
+                    const int n = column_of(warp, lane);
+                    s.factor[op][0][n] = wide ? 1.f : sc[lane];
+                    s.factor[op][1][n] = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
+                }
+            }
+            fence_proxy_async_shared();
+            if (look) {
+                const uint32_t lo = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad));
+                const uint32_t hi = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad >> 32));
+                v.bad = static_cast<unsigned long long>(hi) << 32 | lo;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                s.info[op].nonfin[warp] = v.bad;
+                mbar_arrive(&s.raw_empty[st]);
+                mbar_arrive(&s.kv_full[op]);
+            }
+        }
+    }
+}
+
+template <int KIND>
+__device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p) {
+    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
+    const uint32_t tmem = s.tmem;
+    const uint32_t op0 = smem_u32(s.op);
+    Walk walk(p, s);
+    Segment g;
+    uint32_t base = 0, segs = 0, twos = 0, pk[2] = {0, 0};
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const int n = g.t1 - g.t0;
+        const int rounds = g.two ? n : (n + 1) / 2;
+        ok = wait_bar(s, p, &s.q_ready[0], segs) && (!g.two || wait_bar(s, p, &s.q_ready[1], twos));
+        tcgen_fence_after();
+        auto tile = [&](int w, int i) { return base + (g.two ? i : 2 * i + w); };
+        auto exists = [&](int w, int i) { return g.two ? i < n : 2 * i + w < n; };
+        auto score = [&](int w, int i) {   // S_w = Q·K^T
+            const uint32_t k = tile(w, i), st = k % kStages;
+            ok = wait_bar(s, p, &s.kv_full[st], k / kStages);
+            if (!ok) return;
+            tcgen_fence_after();
+            const uint32_t addr = op0 + st * 2 * kOpBytes;
+            const uint32_t q = tmem + kColQ + (g.two ? w * 64 : 0);
+            #pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                mma_ts(tmem + kColS + w * 64, q + ks * 8, smem_desc_sw128(addr + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
+            mma_commit(&s.s_full[w]);
+        };
+        for (int w = 0; ok && w < 2; ++w)
+            if (exists(w, 0)) score(w, 0);
+        for (int i = 0; ok && i < rounds; ++i) {
+            for (int w = 0; ok && w < 2; ++w) {
+                if (!exists(w, i)) continue;
+                const uint32_t k = tile(w, i), st = k % kStages;
+                ok = wait_bar(s, p, &s.p_full[w], pk[w]);
+                if (!ok) break;
+                ++pk[w];
+                tcgen_fence_after();
+                const uint32_t addr = op0 + st * 2 * kOpBytes + kOpBytes;
+                #pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 64 + ks * 8, smem_desc_sw128(addr + ks * 32), kDescO,
+                           i > 0 || ks > 0);
+                if (!g.two || w == 1) mma_commit(&s.kv_empty[st]);
+                if (exists(w, i + 1)) score(w, i + 1);
+                else mma_commit(&s.o_done[w]);
+            }
+        }
+        base += n;
+        ++segs;
+        if (g.two) ++twos;
+    }
+    if (!ok) {   // what was issued completes before tensor memory is freed
+        mma_commit(&s.drain);
+        mbar_wait(&s.drain, 0, nullptr, kWaitNs);
+    }
+}
+
+// A row of q as the A operand: tensor memory column 16j + 4x + m of a row holds the pair of dims
+// 32j + 2x + 8m, the order of the K operand.  Returns the factor of the row's logits (angle-domain).
+template <int KIND>
+__device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t* q, bool row, bool store, bool flip, uint32_t addr) {
+    float factor = 1.f;
+    uint32_t w[2][32];
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row) v = *reinterpret_cast<const uint4*>(q + 8 * i);
+        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+        #pragma unroll
+        for (int x = 0; x < 4; ++x) w[i >> 3][16 * ((i >> 2) & 1) + 4 * x + (i & 3)] = flip ? e[x] ^ 0x80008000u : e[x];
+    }
+    if constexpr (KIND == kKindAngle) {   // the E4M3 code of the row at its absmax scale, ||q||/||d_q||
+        float top = 0.f;
+        #pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            const float2 v = unpack_bf16(w[i >> 5][i & 31]);
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+        const float sc = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+        float r2 = 0.f, d2 = 0.f;
+        #pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            const float2 v = unpack_bf16(w[i >> 5][i & 31]);
+            const float a = __fdiv_rn(v.x, sc), b = __fdiv_rn(v.y, sc);
+            const float c = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+            const float d = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+            r2 += a * a + b * b;
+            d2 += c * c + d * d;
+            w[i >> 5][i & 31] = pack_bf16(c, d);
+        }
+        factor = d2 == 0.f ? 0.f : sc * sqrtf(r2 / d2);
+    }
+    if (store) {
+        tmem_st32(addr, w[0]);
+        tmem_st32(addr + 32, w[1]);
+        tmem_wait_st();
+    }
+    return factor;
+}
+
+template <int KIND>
+__device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& p, int w, int tid, int lane) {
+    const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
+    const uint32_t tmem = s.tmem + lanes;
+    const uint32_t col_s = tmem + kColS + w * 64, col_o = tmem + kColO + w * 128;
+    // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
+    const bool flip = p.scale_log2 < 0.f;
+    const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    Walk walk(p, s);
+    Segment g;
+    uint32_t base = 0, sk = 0, ok_count = 0, merges = 0;
+    bool merge_pending = false;
+    int seg_index = 0;
+    while (walk.next(p, g)) {
+        const int n = g.t1 - g.t0;
+        const int mine = g.two ? n : (n + 1 - w) / 2;   // tiles of this warpgroup
+        const int row = g.two ? w * kWgRows + tid : tid;
+        const bool live = row < g.rows;
+        const int token = g.tok0 + row / p.g, head = g.h * p.g + row % p.g;
+        const int64_t out_row = (static_cast<int64_t>(g.s0) + token) * p.n_q + head;
+        const int pos = g.len < 0 ? -1 : g.len - g.T + token;
+        float rs = load_query<KIND>(p, p.q + (live ? out_row : 0) * kDh,
+                                    live && (g.two || w == 0 || KIND == kKindAngle), g.two || w == 0, flip,
+                                    tmem + kColQ + (g.two ? w * 64 : 0)) * scale;
+        rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
+        tcgen_fence_before();
+        __syncwarp();
+        if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
+        if (merge_pending) {   // WG 0 has read the last unit's O of this warpgroup
+            if (!__all_sync(kFull, wait_bar(s, p, &s.merge_empty, merges - 1))) return;
+            merge_pending = false;
+        }
+        float m = -INFINITY, l = 0.f;
+        int flagged = 0;
+        unsigned long long flag_mask[8];
+        int flag_tile[8];
+        for (int i = 0; i < mine; ++i) {
+            const uint32_t k = base + (g.two ? i : 2 * i + w);
+            const int st = k % kStages;
+            const int t = g.t0 + (g.two ? i : 2 * i + w);
+            bool ok = wait_bar(s, p, &s.s_full[w], sk) && wait_bar(s, p, &s.kv_full[st], k / kStages);
+            if (!__all_sync(kFull, ok)) return;
+            ++sk;
+            tcgen_fence_after();
+            uint32_t raw[2][32];
+            tmem_ld32(col_s, raw[0]);
+            tmem_ld32(col_s + 32, raw[1]);
+            tmem_wait_ld(raw[0]);
+            tmem_wait_ld(raw[1]);
+            float x[kTile];
+            #pragma unroll
+            for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
+            if constexpr (has_factors(KIND)) {
+                #pragma unroll
+                for (int c = 0; c < kTile; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&s.factor[st][0][c]);
+                    x[c] *= f.x;
+                    x[c + 1] *= f.y;
+                    x[c + 2] *= f.z;
+                    x[c + 3] *= f.w;
+                }
+            }
+            unsigned long long may = s.info[st].mask;
+            const int t_end = t * kTile + kTile - 1;
+            if (may != ~0ull || t_end > g.first) {
+                const int left = pos - t * kTile;   // the row attends places 0 .. left
+                if (left < kTile - 1) may &= left < 0 ? 0ull : (2ull << left) - 1ull;
+                const uint32_t lo = static_cast<uint32_t>(may), hi = static_cast<uint32_t>(may >> 32);
+                #pragma unroll
+                for (int c = 0; c < kTile; ++c) {
+                    const int at = place_of(c);
+                    if (!((at < 32 ? lo >> at : hi >> (at - 32)) & 1u)) x[c] = -INFINITY;
+                }
+                const unsigned long long bad =
+                    s.info[st].nonfin[0] | s.info[st].nonfin[1] | s.info[st].nonfin[2] | s.info[st].nonfin[3];
+                if (bad && flagged < 8) {
+                    flag_mask[flagged] = bad;
+                    flag_tile[flagged++] = t;
+                }
+            }
+            float top = -INFINITY;
+            #pragma unroll
+            for (int c = 0; c < kTile; ++c) top = fmaxf(top, x[c]);
+            top *= rs;
+            if (__any_sync(kFull, top > m + kLazy)) {
+                const float nm = fmaxf(m, top);
+                const float f = m == nm ? 1.f : ex2(m - nm);
+                m = nm;
+                l *= f;
+                if (i > 0) {   // the last PV has completed: its commit came before this S's
+                    #pragma unroll 1
+                    for (int c = 0; c < kDh; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(col_o + c, o);
+                        tmem_wait_ld(o);
+                        #pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(col_o + c, o);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pw[32];
+            #pragma unroll
+            for (int c = 0; c < kTile; c += 4) {
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[c + e] = ex2(fmaf(x[c + e], rs, -ref));
+                    sum[e] += x[c + e];
+                }
+                if constexpr (has_factors(KIND)) {
+                    const float4 f = *reinterpret_cast<const float4*>(&s.factor[st][1][c]);
+                    x[c] *= f.x;
+                    x[c + 1] *= f.y;
+                    x[c + 2] *= f.z;
+                    x[c + 3] *= f.w;
+                }
+                pw[c / 2] = pack_bf16(x[c], x[c + 1]);
+                pw[c / 2 + 1] = pack_bf16(x[c + 2], x[c + 3]);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st32(col_s, pw);
+            tmem_wait_st();
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.p_full[w]);
+        }
+        if (mine > 0) {
+            if (!__all_sync(kFull, wait_bar(s, p, &s.o_done[w], ok_count))) return;
+            ++ok_count;
+            tcgen_fence_after();
+        }
+        base += n;
+        const bool merging = !g.two && n > 1;   // both warpgroups hold a part of the rows
+        if (merging && w == 1) {
+            // O stays in tensor memory: the lanes are the same rows in both warpgroups
+            s.ml[0][tid] = m;
+            s.ml[1][tid] = l;
+        }
+        float f0 = 1.f, f1 = 0.f;
+        if (merging) {
+            if (w == 1) {
+                // non-finite values noted by this warpgroup are added to its own O below
+                for (int e = 0; e < flagged; ++e) {
+                    #pragma unroll 1
+                    for (int c = 0; c < kDh; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(col_o + c, o);
+                        tmem_wait_ld(o);
+                        #pragma unroll
+                        for (int d = 0; d < 32; ++d) {
+                            for (unsigned long long bits = flag_mask[e]; bits; bits &= bits - 1) {
+                                const int at = flag_tile[e] * kTile + place_of(__ffsll(bits) - 1);
+                                if (!live || at > pos) continue;
+                                const float v = pool_value<KIND>(p, g.b, g.h, at, c + d);
+                                if (!isfinite(v)) o[d] = __float_as_uint(__uint_as_float(o[d]) + v);
+                            }
+                        }
+                        __syncwarp();
+                        tmem_st32(col_o + c, o);
+                    }
+                }
+                tmem_wait_st();
+                tcgen_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.merge_full);
+                ++merges;
+                merge_pending = true;
+                ++seg_index;
+                continue;
+            }
+            if (!__all_sync(kFull, wait_bar(s, p, &s.merge_full, merges))) return;
+            ++merges;
+            tcgen_fence_after();
+            const float m1 = s.ml[0][tid], l1 = s.ml[1][tid];
+            const float M = fmaxf(m, m1);
+            f0 = m == -INFINITY ? 0.f : ex2(m - M);
+            f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+            if (m == M) f0 = M == -INFINITY ? f0 : 1.f;
+            if (m1 == M) f1 = M == -INFINITY ? f1 : 1.f;
+            l = (m == -INFINITY && l == 0.f ? 0.f : l * f0) + (m1 == -INFINITY && l1 == 0.f ? 0.f : l1 * f1);
+            m = M;
+        } else if (!g.two && w == 1) {
+            ++seg_index;
+            continue;
+        }
+        const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+        const int slot = 2 * blockIdx.x + (seg_index > 0);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        #pragma unroll 1
+        for (int c = 0; c < kDh; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(col_o + c, o);
+            tmem_wait_ld(o);
+            float y[32];
+            #pragma unroll
+            for (int d = 0; d < 32; ++d) y[d] = __uint_as_float(o[d]);
+            if (merging) {
+                tmem_ld32(tmem + kColO + 128 + c, o);
+                tmem_wait_ld(o);
+                #pragma unroll
+                for (int d = 0; d < 32; ++d) y[d] = y[d] * f0 + __uint_as_float(o[d]) * f1;
+            }
+            for (int e = 0; e < flagged; ++e) {
+                for (unsigned long long bits = flag_mask[e]; bits; bits &= bits - 1) {
+                    const int at = flag_tile[e] * kTile + place_of(__ffsll(bits) - 1);
+                    if (!live || at > pos) continue;
+                    #pragma unroll
+                    for (int d = 0; d < 32; ++d) {
+                        const float v = pool_value<KIND>(p, g.b, g.h, at, c + d);
+                        if (!isfinite(v)) y[d] += v;
+                    }
+                }
+            }
+            __syncwarp();
+            if (!live) continue;
+            if (!whole) {
+                float* part = p.part + static_cast<int64_t>(slot) * kDh * kUnitRows + row;
+                #pragma unroll
+                for (int d = 0; d < 32; ++d) part[(c + d) * kUnitRows] = y[d];
+            } else if (p.out_f32) {
+                float4* o4 = reinterpret_cast<float4*>(static_cast<float*>(p.out) + out_row * kDh + c);
+                #pragma unroll
+                for (int d = 0; d < 32; d += 4) o4[d / 4] = make_float4(y[d] * inv, y[d + 1] * inv, y[d + 2] * inv, y[d + 3] * inv);
+            } else {
+                uint4* o8 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * kDh + c);
+                #pragma unroll
+                for (int d = 0; d < 32; d += 8)
+                    o8[d / 8] = make_uint4(pack_bf16(y[d] * inv, y[d + 1] * inv), pack_bf16(y[d + 2] * inv, y[d + 3] * inv),
+                                           pack_bf16(y[d + 4] * inv, y[d + 5] * inv), pack_bf16(y[d + 6] * inv, y[d + 7] * inv));
+            }
+        }
+        if (live) {
+            if (!whole) {
+                p.part_ml[static_cast<int64_t>(slot) * 2 * kUnitRows + row] = m;
+                p.part_ml[static_cast<int64_t>(slot) * 2 * kUnitRows + kUnitRows + row] = l;
+            } else if (p.lse_out) {
+                p.lse_out[out_row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+            }
+        }
+        if (tid == 0 && w == 0 && !whole) p.part_seg[slot] = make_int4(g.b, g.h | g.qt << 16, g.t0, g.t1);
+        if (merging) {
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.merge_empty);
+        }
+        ++seg_index;
+    }
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem<KIND>& s = *reinterpret_cast<Smem<KIND>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    constexpr int kRaw = raw_stages(KIND);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == kMmaWarp) tmem_alloc_all(&s.tmem);
+    if (tid == 0) {
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&s.raw_full[i], 1);
+            mbar_init(&s.raw_empty[i], 4);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.kv_full[i], 4);
+            mbar_init(&s.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_ready[i], 4);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.o_done[i], 1);
+        }
+        mbar_init(&s.merge_full, 4);
+        mbar_init(&s.merge_empty, 4);
+        mbar_init(&s.drain, 1);
+        mbar_fence_init();
+        s.abort = 0;
+        s.remaining = 0;
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
+    make_schedule(p, s, reinterpret_cast<int64_t*>(s.raw));
+    fence_proxy_async_shared();   // the schedule's scratch lies where the copies will land
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    if (warp < 4) softmax_group<KIND>(s, p, 0, tid, lane);
+    else if (warp < 8) softmax_group<KIND>(s, p, 1, tid - 128, lane);
+    else if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
+    else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
+    else if (lane == 0) mma_issuer<KIND>(s, p);
+    __syncwarp();
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    if (warp == kMmaWarp) tmem_free_all(s.tmem);
+}
+
+template <int KIND>
+cudaError_t launch_kind(const ChunkParams& p, int grid, cudaStream_t stream) {
+    const size_t smem = sizeof(Smem<KIND>) + 1024;
+    static_assert(sizeof(Smem<KIND>) + 1024 <= 232448, "shared memory of one SM");
+    const cudaError_t e =
+        cudaFuncSetAttribute(chunk_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(chunk_kernel<KIND>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, -1, stream, p);
+}
+
+}  // namespace chunk
+}  // namespace kvd
