@@ -23,7 +23,7 @@
 //    of two blocks give eight tokens of each, which fixes the order of a tile's 64 columns:
 //    column 32p + 8x + 4u + w = token 2x + (w & 1) + 8(w >> 1) of block 2p + u.  8-bit codes become
 //    bf16 exactly on the way; low-bit codes become bf16(code·scale + zero);
-//  * MMA warp: one thread issues S = Q·K^T and O += P·V, Q and P from tensor memory (reading them
+//  * MMA warp: issues S = Q·K^T and O += P·V, Q and P from tensor memory (reading them
 //    from shared memory would take its whole bandwidth), accumulators in tensor memory;
 //  * two softmax warpgroups, one thread a row: online softmax in fp32 (exp2 domain), P back to tensor
 //    memory as bf16.  The reference maximum moves only when a row's maximum passes it by 8 (weights up
@@ -56,6 +56,7 @@ constexpr int kStages = 3;             // operand stages (K 16 KiB + V 16 KiB)
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kTries = 64;             // tries of a wait before its limit is looked at
 constexpr int kColS = 0, kColO = 128, kColQ = 384;   // tensor memory columns: S/P 2 × 64, O 2 × 128, Q 2 × 64
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
@@ -339,31 +340,51 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
     hi = *reinterpret_cast<uint32_t*>(&rb);
 }
 
-// K of block k (its record, 16-bit or 8-bit) by one warp.
+// K of block k (its record, 16-bit or 8-bit) by one warp: every load first, then the stores.  Lanes of
+// an eight read one 64-byte half each and write all eight pieces of two rows' 128-byte lines, so neither
+// side has bank conflicts.
 template <int FMT>
-__device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, int k, int lane) {
-    const int x = lane & 3, j0 = (lane >> 2) & 1, tl = lane >> 3;
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // lanes of an eight read one 64-byte half each and write all eight pieces of two rows' line
-        const int t = 2 * tl + ((i & 1) ^ j0), j = 2 * (i >> 1) + j0;
-        const int n = column_of(k, t);
-        if constexpr (FMT == kFmtBf16) {
-            const uint4 a = *reinterpret_cast<const uint4*>(rec + ((2 * j) * 32 + 4 * t + x) * 16);
-            const uint4 b = *reinterpret_cast<const uint4*>(rec + ((2 * j + 1) * 32 + 4 * t + x) * 16);
-            put_k(op, n, j, x, a.x, a.z, b.x, b.z);
-            put_k(op, n + 2, j, x, a.y, a.w, b.y, b.w);
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(rec + (j * 32 + 4 * t + x) * 16);
-            uint32_t lo[4], hi[4];
-            codes_to_bf16<FMT>(a.x, lo[0], hi[0]);
-            codes_to_bf16<FMT>(a.y, lo[1], hi[1]);
-            codes_to_bf16<FMT>(a.z, lo[2], hi[2]);
-            codes_to_bf16<FMT>(a.w, lo[3], hi[3]);
-            put_k(op, n, j, x, lo[0], lo[1], lo[2], lo[3]);
-            put_k(op, n + 2, j, x, hi[0], hi[1], hi[2], hi[3]);
+struct KPieces {
+    uint4 a[4], b[FMT == kFmtBf16 ? 4 : 1];
+    __device__ __forceinline__ void load(const uint8_t* rec, int lane) {
+        const int x = lane & 3, j0 = (lane >> 2) & 1, tl = lane >> 3;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 2 * tl + ((i & 1) ^ j0), j = 2 * (i >> 1) + j0;
+            if constexpr (FMT == kFmtBf16) {
+                a[i] = *reinterpret_cast<const uint4*>(rec + ((2 * j) * 32 + 4 * t + x) * 16);
+                b[i] = *reinterpret_cast<const uint4*>(rec + ((2 * j + 1) * 32 + 4 * t + x) * 16);
+            } else {
+                a[i] = *reinterpret_cast<const uint4*>(rec + (j * 32 + 4 * t + x) * 16);
+            }
         }
     }
+    __device__ __forceinline__ void store(uint8_t* op, int k, int lane) const {
+        const int x = lane & 3, j0 = (lane >> 2) & 1, tl = lane >> 3;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 2 * tl + ((i & 1) ^ j0), j = 2 * (i >> 1) + j0;
+            const int n = column_of(k, t);
+            if constexpr (FMT == kFmtBf16) {
+                put_k(op, n, j, x, a[i].x, a[i].z, b[i].x, b[i].z);
+                put_k(op, n + 2, j, x, a[i].y, a[i].w, b[i].y, b[i].w);
+            } else {
+                uint32_t lo[4], hi[4];
+                codes_to_bf16<FMT>(a[i].x, lo[0], hi[0]);
+                codes_to_bf16<FMT>(a[i].y, lo[1], hi[1]);
+                codes_to_bf16<FMT>(a[i].z, lo[2], hi[2]);
+                codes_to_bf16<FMT>(a[i].w, lo[3], hi[3]);
+                put_k(op, n, j, x, lo[0], lo[1], lo[2], lo[3]);
+                put_k(op, n + 2, j, x, hi[0], hi[1], hi[2], hi[3]);
+            }
+        }
+    }
+};
+template <int FMT>
+__device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, int k, int lane) {
+    KPieces<FMT> q;
+    q.load(rec, lane);
+    q.store(op, k, lane);
 }
 
 // A V piece of two dims as bf16: group i (dims 16i + r and 16i + r + 8), lane 4r + x: tokens
@@ -400,13 +421,27 @@ __device__ __forceinline__ void repack_v(const uint8_t (*rec)[max_record(KIND)],
     const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
     const uint32_t w0 = word[2 * p], w1 = word[2 * p + 1];
     const uint32_t m0 = w0 & 0xffffu, m1 = w1 & 0xffffu;
+    uint4 a[4], b[4];
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int group = 2 * warp + (i >> 1), r = 2 * rl + ((i & 1) ^ p);
-        const uint4 a = v_piece_kind<KIND>(rec[2 * p], w0, group, 4 * r + x);
-        const uint4 b = v_piece_kind<KIND>(rec[2 * p + 1], w1, group, 4 * r + x);
-        out.put(16 * group + r, p, x, a.x, a.z, b.x, b.z, m0, m1);
-        out.put(16 * group + r + 8, p, x, a.y, a.w, b.y, b.w, m0, m1);
+        a[i] = v_piece_kind<KIND>(rec[2 * p], w0, group, 4 * r + x);
+        b[i] = v_piece_kind<KIND>(rec[2 * p + 1], w1, group, 4 * r + x);
+    }
+    if (!out.look && (w0 & w1 & 0xffffu) == 0xffffu) {   // the usual tile: every position attended by every row
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 16 * (2 * warp + (i >> 1)) + 2 * rl + ((i & 1) ^ p);
+            put16(out.op, d, 4 * p + x, a[i].x, a[i].z, b[i].x, b[i].z);
+            put16(out.op, d + 8, 4 * p + x, a[i].y, a[i].w, b[i].y, b[i].w);
+        }
+        return;
+    }
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int d = 16 * (2 * warp + (i >> 1)) + 2 * rl + ((i & 1) ^ p);
+        out.put(d, p, x, a[i].x, a[i].z, b[i].x, b[i].z, m0, m1);
+        out.put(d + 8, p, x, a[i].y, a[i].w, b[i].y, b[i].w, m0, m1);
     }
 }
 
@@ -524,6 +559,11 @@ __device__ __noinline__ float pool_value(const ChunkParams& p, int b, int h, int
 // ------------------------------------------------------------------ the roles
 template <int KIND>
 __device__ __forceinline__ bool wait_bar(Smem<KIND>& s, const ChunkParams& p, uint64_t* bar, uint32_t phase) {
+    // Most waits end within a few tries; the timer, whose read takes about a thousand cycles, is
+    // looked at only after many.
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i)
+        if (mbar_try_wait(bar, phase & 1u)) return true;
     if (mbar_wait(bar, phase & 1u, &s.abort, kWaitNs)) return true;
     if (atomicExch(&s.abort, 1) == 0) report(p.err, KVD_ERR_TIMEOUT);
     return false;
@@ -660,56 +700,62 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
 template <int KIND>
 __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p) {
     constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
-    const uint32_t tmem = s.tmem;
-    const uint32_t op0 = smem_u32(s.op);
+    const uint32_t el = elect_one();
+    const uint32_t tmem = uniform(s.tmem);
+    const uint32_t op0 = uniform(smem_u32(s.op));
     Walk walk(p, s);
     Segment g;
     uint32_t base = 0, segs = 0, twos = 0, pk[2] = {0, 0};
     bool ok = true;
     while (ok && walk.next(p, g)) {
-        const int n = g.t1 - g.t0;
-        const int rounds = g.two ? n : (n + 1) / 2;
-        ok = wait_bar(s, p, &s.q_ready[0], segs) && (!g.two || wait_bar(s, p, &s.q_ready[1], twos));
+        const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
+        const uint32_t rounds = two ? n : (n + 1) / 2;
+        ok = wait_bar(s, p, &s.q_ready[0], segs) && (!two || wait_bar(s, p, &s.q_ready[1], twos));
+        ok = __all_sync(kFull, ok);
         tcgen_fence_after();
-        auto tile = [&](int w, int i) { return base + (g.two ? i : 2 * i + w); };
-        auto exists = [&](int w, int i) { return g.two ? i < n : 2 * i + w < n; };
-        auto score = [&](int w, int i) {   // S_w = Q·K^T
+        auto tile = [&](uint32_t w, uint32_t i) { return base + (two ? i : 2 * i + w); };
+        auto exists = [&](uint32_t w, uint32_t i) { return two ? i < n : 2 * i + w < n; };
+        auto score = [&](uint32_t w, uint32_t i) {   // S_w = Q·K^T
             const uint32_t k = tile(w, i), st = k % kStages;
-            ok = wait_bar(s, p, &s.kv_full[st], k / kStages);
+            ok = __all_sync(kFull, wait_bar(s, p, &s.kv_full[st], k / kStages));
             if (!ok) return;
             tcgen_fence_after();
-            const uint32_t addr = op0 + st * 2 * kOpBytes;
-            const uint32_t q = tmem + kColQ + (g.two ? w * 64 : 0);
+            const uint32_t addr = uniform(op0 + st * 2 * kOpBytes);
+            const uint32_t q = uniform(tmem + kColQ + (two ? w * 64 : 0)), d = uniform(tmem + kColS + w * 64);
             #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tmem + kColS + w * 64, q + ks * 8, smem_desc_sw128(addr + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
-            mma_commit(&s.s_full[w]);
+                mma_ts(d, q + ks * 8, smem_desc_sw128(addr + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0, el);
+            if (el) mma_commit(&s.s_full[w]);
         };
-        for (int w = 0; ok && w < 2; ++w)
+        #pragma unroll 1
+        for (uint32_t w = 0; ok && w < 2; ++w)
             if (exists(w, 0)) score(w, 0);
-        for (int i = 0; ok && i < rounds; ++i) {
-            for (int w = 0; ok && w < 2; ++w) {
+        #pragma unroll 1
+        for (uint32_t i = 0; ok && i < rounds; ++i) {
+            #pragma unroll 1
+            for (uint32_t w = 0; ok && w < 2; ++w) {
                 if (!exists(w, i)) continue;
                 const uint32_t k = tile(w, i), st = k % kStages;
-                ok = wait_bar(s, p, &s.p_full[w], pk[w]);
+                ok = __all_sync(kFull, wait_bar(s, p, &s.p_full[w], pk[w]));
                 if (!ok) break;
                 ++pk[w];
                 tcgen_fence_after();
-                const uint32_t addr = op0 + st * 2 * kOpBytes + kOpBytes;
+                const uint32_t addr = uniform(op0 + st * 2 * kOpBytes + kOpBytes);
+                const uint32_t a = uniform(tmem + kColS + w * 64), d = uniform(tmem + kColO + w * 128);
+                const uint32_t more = uniform(i > 0);
                 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(tmem + kColO + w * 128, tmem + kColS + w * 64 + ks * 8, smem_desc_sw128(addr + ks * 32), kDescO,
-                           i > 0 || ks > 0);
-                if (!g.two || w == 1) mma_commit(&s.kv_empty[st]);
+                    mma_ts(d, a + ks * 8, smem_desc_sw128(addr + ks * 32), kDescO, more || ks > 0, el);
+                if (el && (!two || w == 1)) mma_commit(&s.kv_empty[st]);
                 if (exists(w, i + 1)) score(w, i + 1);
-                else mma_commit(&s.o_done[w]);
+                else if (el) mma_commit(&s.o_done[w]);
             }
         }
         base += n;
         ++segs;
-        if (g.two) ++twos;
+        if (two) ++twos;
     }
-    if (!ok) {   // what was issued completes before tensor memory is freed
+    if (!ok && el) {   // what was issued completes before tensor memory is freed
         mma_commit(&s.drain);
         mbar_wait(&s.drain, 0, nullptr, kWaitNs);
     }
@@ -1050,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     else if (warp < 8) softmax_group<KIND>(s, p, 1, tid - 128, lane);
     else if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
     else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-    else if (lane == 0) mma_issuer<KIND>(s, p);
+    else mma_issuer<KIND>(s, p);
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();

@@ -61,22 +61,34 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // eight rows 1,024 bytes apart, 16-byte piece c of row r at c ^ (r % 8).  Address 1,024-byte aligned;
 // 16 elements further along K = 32 bytes.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+    return static_cast<uint64_t>(addr >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 // bf16 × bf16 -> fp32, both operands K-major.
 __host__ __device__ constexpr uint32_t mma_desc_bf16(int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24);
 }
-// D[128][N] (+)= A[128][16] (tensor memory) · B[N][16]^T (shared memory).  One thread issues it.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+// One thread of a converged warp: 1 there, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+// The value lane 0 has: equal in every lane already, and known to the compiler as such, so that it can
+// stand in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
+// D[128][N] (+)= A[128][16] (tensor memory) · B[N][16]^T (shared memory).  The whole warp runs it with
+// uniform operands, the elected thread issues: 32 to 64 cycles per instruction (its execution), where a
+// single thread under a branch took 100 (operands moved to uniform registers one by one).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add, uint32_t elected) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add))
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(elected)
         : "memory");
 }
-// Arrive on bar once every MMA this thread issued so far has completed.
+// Arrive on bar once every MMA this thread issued so far has completed (the elected thread).
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
