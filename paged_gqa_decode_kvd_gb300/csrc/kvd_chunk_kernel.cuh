@@ -50,18 +50,18 @@ namespace chunk {
 constexpr int kTile = 64;              // positions per tile: four blocks
 constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
-constexpr int kThreads = 448;          // softmax 2 × 128, repack 128, producer 32, MMA 32
+constexpr int kThreads = 512;          // softmax 2 × 128, repack 128, producer 32, MMA 2 × 32, one warp idle
 constexpr int kRepackWarp = 8, kProducerWarp = 12, kMmaWarp = 13;
 constexpr int kStages = 3;             // operand stages (K 16 KiB + V 16 KiB)
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kTries = 64;             // tries of a wait before its limit is looked at
-constexpr int kColS = 0, kColO = 128, kColQ = 384;   // tensor memory columns: S/P 2 × 64, O 2 × 128, Q 2 × 64
+constexpr int kTries = 200000;         // tries of a wait: a second or so
+constexpr int kColS = 0, kColP = 128, kColQ = 192, kColO = 256;   // tensor memory columns: S 2 × 64, P 2 × 32, Q 2 × 32, O 2 × 128
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
-constexpr int raw_stages(int kind) { return kind == kKindBf16 ? 4 : kind == kKindMixed ? 3 : 6; }
+constexpr int raw_stages(int kind) { return kind == kKindBf16 ? 3 : kind == kKindMixed ? 2 : 5; }
 constexpr int max_record(int kind) {
     return kind == kKindBf16 || kind == kKindMixed ? kRecordBf16
            : kind == kKindInt4                     ? lowbit_record_bytes(4, 4)
@@ -77,6 +77,7 @@ struct StageInfo {
 template <int KIND>
 struct Smem {
     uint8_t op[kStages][2][kOpBytes];                           // K, V operands; 1,024-byte aligned
+    uint8_t q[2][kOpBytes];                                     // second half of q's dims, 128 rows each
     uint8_t raw[raw_stages(KIND)][4][max_record(KIND)];
     float factor[has_factors(KIND) ? kStages : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
     float ml[2][kWgRows];                                       // merge: WG 1's maximum and sum
@@ -84,8 +85,8 @@ struct Smem {
     StageInfo info[kStages];
     uint64_t raw_full[raw_stages(KIND)], raw_empty[raw_stages(KIND)];
     uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t s_full[2], p_full[2], o_done[2];
-    uint64_t q_ready[2], merge_full, merge_empty, drain;
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t q_ready[2], merge_full, merge_empty, drain[2];
     int64_t remaining;
     int b, h, qt, off;
     uint32_t tmem;
@@ -557,14 +558,33 @@ __device__ __noinline__ float pool_value(const ChunkParams& p, int b, int h, int
 }
 
 // ------------------------------------------------------------------ the roles
+// Wait for the barrier's phase with the given parity: one instruction when it is there already.  A try
+// suspends the warp for some 8,000 cycles at most and wakes within about 130, so the limit, a second or
+// so, is a count of tries; reading the timer would add 700 cycles to every wait.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        ".reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra AGAIN;\n\t"
+        "DONE:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kTries)
+        : "memory");
+    return ok != 0;
+}
 template <int KIND>
 __device__ __forceinline__ bool wait_bar(Smem<KIND>& s, const ChunkParams& p, uint64_t* bar, uint32_t phase) {
-    // Most waits end within a few tries; the timer, whose read takes about a thousand cycles, is
-    // looked at only after many.
-    #pragma unroll 1
-    for (int i = 0; i < kTries; ++i)
-        if (mbar_try_wait(bar, phase & 1u)) return true;
-    if (mbar_wait(bar, phase & 1u, &s.abort, kWaitNs)) return true;
+    if (wait_phase(bar, phase & 1u)) return true;
     if (atomicExch(&s.abort, 1) == 0) report(p.err, KVD_ERR_TIMEOUT);
     return false;
 }
@@ -697,74 +717,100 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
     }
 }
 
+// The MMAs of warpgroup W, by one warp: S_W of the next tile as soon as the warpgroup has this one's in
+// registers, then O_W += P_W·V.  A warp for each warpgroup, since one that looks at the barriers of both
+// in turn answers each some 700 cycles late.
 template <int KIND>
-__device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p) {
+__device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
     constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
-    const uint32_t el = elect_one();
+    const uint32_t el = elect_one(), W = uniform(warpgroup);
     const uint32_t tmem = uniform(s.tmem);
-    const uint32_t op0 = uniform(smem_u32(s.op));
+    const uint32_t op0 = uniform(smem_u32(s.op)), q0 = uniform(smem_u32(s.q));
+    const uint32_t col_s = uniform(tmem + kColS + W * 64), col_p = uniform(tmem + kColP + W * 32);
+    const uint32_t col_o = uniform(tmem + kColO + W * 128);
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, segs = 0, twos = 0, pk[2] = {0, 0};
+    uint32_t base = 0, segs[2] = {0, 0}, step = 0;   // tiles before the segment; phases of q_ready, of s_free and p_full
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
-        const uint32_t rounds = two ? n : (n + 1) / 2;
-        ok = wait_bar(s, p, &s.q_ready[0], segs) && (!two || wait_bar(s, p, &s.q_ready[1], twos));
-        ok = __all_sync(kFull, ok);
+        const uint32_t mine = two ? n : (n + 1 - W) / 2, stride = two ? 1 : 2;
+        const uint32_t which = two ? W : 0;   // whose rows
+        // both barriers' phases are followed in order, whether this warp has tiles or not
+        ok = wait_bar(s, p, &s.q_ready[0], segs[0]) && (!two || W == 0 || wait_bar(s, p, &s.q_ready[1], segs[1]));
         tcgen_fence_after();
-        auto tile = [&](uint32_t w, uint32_t i) { return base + (two ? i : 2 * i + w); };
-        auto exists = [&](uint32_t w, uint32_t i) { return two ? i < n : 2 * i + w < n; };
-        auto score = [&](uint32_t w, uint32_t i) {   // S_w = Q·K^T
-            const uint32_t k = tile(w, i), st = k % kStages;
-            ok = __all_sync(kFull, wait_bar(s, p, &s.kv_full[st], k / kStages));
-            if (!ok) return;
+        const uint32_t k0 = base + (two ? 0 : W);
+        uint32_t ss = k0 % kStages, sp = (k0 / kStages) & 1u;   // stage and phase of the next S
+        uint32_t vs = ss;                                       // stage of the next O
+        const uint32_t a = uniform(tmem + kColQ + which * 32), b = uniform(q0 + which * kOpBytes);
+        auto score = [&]() {   // S_W = Q·K^T; its operands are there
             tcgen_fence_after();
-            const uint32_t addr = uniform(op0 + st * 2 * kOpBytes);
-            const uint32_t q = uniform(tmem + kColQ + (two ? w * 64 : 0)), d = uniform(tmem + kColS + w * 64);
+            const uint32_t addr = uniform(op0 + ss * (2 * kOpBytes));
             #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_ts(d, q + ks * 8, smem_desc_sw128(addr + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0, el);
-            if (el) mma_commit(&s.s_full[w]);
+            for (int ks = 0; ks < 4; ++ks)
+                mma_ts(col_s, a + ks * 8, smem_desc_sw128(addr + ks * 32), kDescS, ks > 0, el);
+            #pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                mma_ss(col_s, smem_desc_sw128(b + ks * 32), smem_desc_sw128(addr + 8192 + ks * 32), kDescS, true, el);
+            if (el) mma_commit(&s.s_full[W]);
+            ss += stride;
+            if (ss >= kStages) {
+                ss -= kStages;
+                sp ^= 1u;
+            }
         };
+        if (ok && mine > 0) {
+            ok = wait_bar(s, p, &s.kv_full[ss], sp);
+            if (ok) score();
+        }
         #pragma unroll 1
-        for (uint32_t w = 0; ok && w < 2; ++w)
-            if (exists(w, 0)) score(w, 0);
-        #pragma unroll 1
-        for (uint32_t i = 0; ok && i < rounds; ++i) {
-            #pragma unroll 1
-            for (uint32_t w = 0; ok && w < 2; ++w) {
-                if (!exists(w, i)) continue;
-                const uint32_t k = tile(w, i), st = k % kStages;
-                ok = __all_sync(kFull, wait_bar(s, p, &s.p_full[w], pk[w]));
-                if (!ok) break;
-                ++pk[w];
-                tcgen_fence_after();
-                const uint32_t addr = uniform(op0 + st * 2 * kOpBytes + kOpBytes);
-                const uint32_t a = uniform(tmem + kColS + w * 64), d = uniform(tmem + kColO + w * 128);
-                const uint32_t more = uniform(i > 0);
-                #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ts(d, a + ks * 8, smem_desc_sw128(addr + ks * 32), kDescO, more || ks > 0, el);
-                if (el && (!two || w == 1)) mma_commit(&s.kv_empty[st]);
-                if (exists(w, i + 1)) score(w, i + 1);
-                else if (el) mma_commit(&s.o_done[w]);
+        for (uint32_t i = 0; ok && i < mine; ++i, ++step) {
+            ok = wait_bar(s, p, &s.s_free[W], step);
+            if (!ok) break;
+            // the next tile's S first, if its operands are there: a tile still on its way does not hold up O
+            uint32_t later = i + 1 < mine;
+            if (later && uniform(mbar_try_now(&s.kv_full[ss], sp))) {
+                score();
+                later = 0;
+            }
+            ok = wait_bar(s, p, &s.p_full[W], step);
+            if (!ok) break;
+            tcgen_fence_after();
+            const uint32_t addr = uniform(op0 + vs * (2 * kOpBytes) + kOpBytes);
+            const uint32_t more = uniform(i);
+            #pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                mma_ts(col_o, col_p + ks * 8, smem_desc_sw128(addr + ks * 32), kDescO, more || ks > 0, el);
+            if (el) {
+                mma_commit(&s.pv_done[W]);
+                mma_commit(&s.kv_empty[vs]);
+                if (!two) mbar_arrive(&s.kv_empty[vs]);   // two arrivals a stage: no other warpgroup reads it
+            }
+            vs += stride;
+            if (vs >= kStages) vs -= kStages;
+            if (later) {
+                ok = wait_bar(s, p, &s.kv_full[ss], sp);
+                if (ok) score();
             }
         }
         base += n;
-        ++segs;
-        if (two) ++twos;
+        ++segs[0];
+        if (two) ++segs[1];
     }
+    __syncwarp();
     if (!ok && el) {   // what was issued completes before tensor memory is freed
-        mma_commit(&s.drain);
-        mbar_wait(&s.drain, 0, nullptr, kWaitNs);
+        mma_commit(&s.drain[W]);
+        mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
     }
 }
 
-// A row of q as the A operand: tensor memory column 16j + 4x + m of a row holds the pair of dims
-// 32j + 2x + 8m, the order of the K operand.  Returns the factor of the row's logits (angle-domain).
+// A row of q as the A operand, in the dim order of the K operand: word 16j + 4x + m is the pair of dims
+// 32j + 2x + 8m.  The first 64 dims go to tensor memory, the others to shared memory: S and P then have
+// columns of their own, and S_w of the next tile is computed while the warpgroup works on this one's.
+// Returns the factor of the row's logits (angle-domain).
 template <int KIND>
-__device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t* q, bool row, bool store, bool flip, uint32_t addr) {
+__device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t* q, bool row, bool store, bool flip, uint32_t addr,
+                                            uint8_t* line, int r) {
     float factor = 1.f;
     uint32_t w[2][32];
     #pragma unroll
@@ -798,8 +844,10 @@ __device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t
     }
     if (store) {
         tmem_st32(addr, w[0]);
-        tmem_st32(addr + 32, w[1]);
+        #pragma unroll
+        for (int c = 0; c < 8; ++c) put16(line, r, c, w[1][4 * c], w[1][4 * c + 1], w[1][4 * c + 2], w[1][4 * c + 3]);
         tmem_wait_st();
+        fence_proxy_async_shared();
     }
     return factor;
 }
@@ -808,13 +856,13 @@ template <int KIND>
 __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& p, int w, int tid, int lane) {
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
     const uint32_t tmem = s.tmem + lanes;
-    const uint32_t col_s = tmem + kColS + w * 64, col_o = tmem + kColO + w * 128;
+    const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 32, col_o = tmem + kColO + w * 128;
     // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
     const bool flip = p.scale_log2 < 0.f;
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, sk = 0, ok_count = 0, merges = 0;
+    uint32_t base = 0, sk = 0, pvk = 0, merges = 0;   // phases of s_full, pv_done, the merge
     bool merge_pending = false;
     int seg_index = 0;
     while (walk.next(p, g)) {
@@ -827,7 +875,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         const int pos = g.len < 0 ? -1 : g.len - g.T + token;
         float rs = load_query<KIND>(p, p.q + (live ? out_row : 0) * kDh,
                                     live && (g.two || w == 0 || KIND == kKindAngle), g.two || w == 0, flip,
-                                    tmem + kColQ + (g.two ? w * 64 : 0)) * scale;
+                                    tmem + kColQ + (g.two ? w * 32 : 0), s.q[g.two ? w : 0], tid) * scale;
         rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
         tcgen_fence_before();
         __syncwarp();
@@ -853,6 +901,9 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             tmem_ld32(col_s + 32, raw[1]);
             tmem_wait_ld(raw[0]);
             tmem_wait_ld(raw[1]);
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_free[w]);
             float x[kTile];
             #pragma unroll
             for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
@@ -888,12 +939,17 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             #pragma unroll
             for (int c = 0; c < kTile; ++c) top = fmaxf(top, x[c]);
             top *= rs;
+            if (i > 0) {   // the last tile's O is complete and its P read
+                if (!__all_sync(kFull, wait_bar(s, p, &s.pv_done[w], pvk))) return;
+                ++pvk;
+                tcgen_fence_after();
+            }
             if (__any_sync(kFull, top > m + kLazy)) {
                 const float nm = fmaxf(m, top);
                 const float f = m == nm ? 1.f : ex2(m - nm);
                 m = nm;
                 l *= f;
-                if (i > 0) {   // the last PV has completed: its commit came before this S's
+                if (i > 0) {
                     #pragma unroll 1
                     for (int c = 0; c < kDh; c += 32) {
                         uint32_t o[32];
@@ -926,15 +982,15 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 pw[c / 2 + 1] = pack_bf16(x[c + 2], x[c + 3]);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(col_s, pw);
+            tmem_st32(col_p, pw);
             tmem_wait_st();
             tcgen_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.p_full[w]);
         }
         if (mine > 0) {
-            if (!__all_sync(kFull, wait_bar(s, p, &s.o_done[w], ok_count))) return;
-            ++ok_count;
+            if (!__all_sync(kFull, wait_bar(s, p, &s.pv_done[w], pvk))) return;
+            ++pvk;
             tcgen_fence_after();
         }
         base += n;
@@ -1069,17 +1125,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.kv_full[i], 4);
-            mbar_init(&s.kv_empty[i], 1);
+            mbar_init(&s.kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_ready[i], 4);
+            mbar_init(&s.drain[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 4);
-            mbar_init(&s.o_done[i], 1);
+            mbar_init(&s.s_free[i], 4);
+            mbar_init(&s.pv_done[i], 1);
         }
         mbar_init(&s.merge_full, 4);
         mbar_init(&s.merge_empty, 4);
-        mbar_init(&s.drain, 1);
         mbar_fence_init();
         s.abort = 0;
         s.remaining = 0;
@@ -1092,11 +1149,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
-    if (warp < 4) softmax_group<KIND>(s, p, 0, tid, lane);
-    else if (warp < 8) softmax_group<KIND>(s, p, 1, tid - 128, lane);
+    // one copy of each role's code: with one per warpgroup the loops outgrow the instruction cache
+    // (its misses took 90% of the next level's rate, and every role ran at half speed)
+    if (warp < 8) softmax_group<KIND>(s, p, warp >> 2, tid & 127, lane);
     else if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
     else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-    else mma_issuer<KIND>(s, p);
+    else if (warp < kMmaWarp + 2) mma_issuer<KIND>(s, p, warp - kMmaWarp);
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();
