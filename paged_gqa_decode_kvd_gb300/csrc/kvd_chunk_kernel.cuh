@@ -86,6 +86,7 @@ struct Smem {
     uint64_t raw_full[raw_stages(KIND)], raw_empty[raw_stages(KIND)];
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t turn[2];   // a warpgroup may work on its logits
     uint64_t q_ready[2], merge_full, merge_empty, drain[2];
     int64_t remaining;
     int b, h, qt, off;
@@ -341,51 +342,63 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
     hi = *reinterpret_cast<uint32_t*>(&rb);
 }
 
-// K of block k (its record, 16-bit or 8-bit) by one warp: every load first, then the stores.  Lanes of
-// an eight read one 64-byte half each and write all eight pieces of two rows' 128-byte lines, so neither
-// side has bank conflicts.
-template <int FMT>
-struct KPieces {
-    uint4 a[4], b[FMT == kFmtBf16 ? 4 : 1];
-    __device__ __forceinline__ void load(const uint8_t* rec, int lane) {
-        const int x = lane & 3, j0 = (lane >> 2) & 1, tl = lane >> 3;
+// A lane's byte offsets, the same for every tile; [q] for the even and the odd pieces.  K: the warp's block;
+// lanes of an eight read one 64-byte half each and write all eight pieces of two rows' 128-byte lines.  V: the
+// warp's 32 dims of all four blocks, likewise.  Neither side has bank conflicts.
+struct Offsets {
+    int k_ld[2][2], k_st[2][2];   // [8-bit record][q], [q][token t, t + 8]
+    int v_ld[2][2], v_st[2];      // [8-bit record][q], [q]
+    __device__ __forceinline__ Offsets(int warp, int lane) {
+        const int x = lane & 3, h = (lane >> 2) & 1, l = lane >> 3;
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 2 * tl + ((i & 1) ^ j0), j = 2 * (i >> 1) + j0;
-            if constexpr (FMT == kFmtBf16) {
-                a[i] = *reinterpret_cast<const uint4*>(rec + ((2 * j) * 32 + 4 * t + x) * 16);
-                b[i] = *reinterpret_cast<const uint4*>(rec + ((2 * j + 1) * 32 + 4 * t + x) * 16);
-            } else {
-                a[i] = *reinterpret_cast<const uint4*>(rec + (j * 32 + 4 * t + x) * 16);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(uint8_t* op, int k, int lane) const {
-        const int x = lane & 3, j0 = (lane >> 2) & 1, tl = lane >> 3;
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 2 * tl + ((i & 1) ^ j0), j = 2 * (i >> 1) + j0;
-            const int n = column_of(k, t);
-            if constexpr (FMT == kFmtBf16) {
-                put_k(op, n, j, x, a[i].x, a[i].z, b[i].x, b[i].z);
-                put_k(op, n + 2, j, x, a[i].y, a[i].w, b[i].y, b[i].w);
-            } else {
-                uint32_t lo[4], hi[4];
-                codes_to_bf16<FMT>(a[i].x, lo[0], hi[0]);
-                codes_to_bf16<FMT>(a[i].y, lo[1], hi[1]);
-                codes_to_bf16<FMT>(a[i].z, lo[2], hi[2]);
-                codes_to_bf16<FMT>(a[i].w, lo[3], hi[3]);
-                put_k(op, n, j, x, lo[0], lo[1], lo[2], lo[3]);
-                put_k(op, n + 2, j, x, hi[0], hi[1], hi[2], hi[3]);
-            }
+        for (int q = 0; q < 2; ++q) {
+            const int t = 2 * l + (q ^ h);   // K: token (mod 8); V: dim (mod 8)
+            const int n = column_of(warp, t);
+            k_ld[0][q] = h * 1024 + (4 * t + x) * 16;
+            k_ld[1][q] = h * 512 + (4 * t + x) * 16;
+            k_st[q][0] = n * 128 + (((4 * h + x) ^ (n & 7)) << 4);
+            k_st[q][1] = (n + 2) * 128 + (((4 * h + x) ^ ((n + 2) & 7)) << 4);
+            v_ld[0][q] = kTileBf16 + warp * 1024 + (4 * t + x) * 16;
+            v_ld[1][q] = kTileFp8 + warp * 512 + (4 * t + x) * 16;
+            v_st[q] = warp * 4096 + t * 128 + (((4 * h + x) ^ t) << 4);
         }
     }
 };
+
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void st16(uint8_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+
 template <int FMT>
-__device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, int k, int lane) {
-    KPieces<FMT> q;
-    q.load(rec, lane);
-    q.store(op, k, lane);
+__device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, const Offsets& o) {
+    if constexpr (FMT == kFmtBf16) {
+        uint4 a[4], b[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = ld16(rec + o.k_ld[0][i & 1] + (i >> 1) * 2048);
+            b[i] = ld16(rec + o.k_ld[0][i & 1] + (i >> 1) * 2048 + 512);
+        }
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            st16(op + o.k_st[i & 1][0] + (i >> 1) * 8192, a[i].x, a[i].z, b[i].x, b[i].z);
+            st16(op + o.k_st[i & 1][1] + (i >> 1) * 8192, a[i].y, a[i].w, b[i].y, b[i].w);
+        }
+    } else {
+        uint4 a[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = ld16(rec + o.k_ld[1][i & 1] + (i >> 1) * 1024);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t lo[4], hi[4];
+            codes_to_bf16<FMT>(a[i].x, lo[0], hi[0]);
+            codes_to_bf16<FMT>(a[i].y, lo[1], hi[1]);
+            codes_to_bf16<FMT>(a[i].z, lo[2], hi[2]);
+            codes_to_bf16<FMT>(a[i].w, lo[3], hi[3]);
+            st16(op + o.k_st[i & 1][0] + (i >> 1) * 8192, lo[0], lo[1], lo[2], lo[3]);
+            st16(op + o.k_st[i & 1][1] + (i >> 1) * 8192, hi[0], hi[1], hi[2], hi[3]);
+        }
+    }
 }
 
 // A V piece of two dims as bf16: group i (dims 16i + r and 16i + r + 8), lane 4r + x: tokens
@@ -403,7 +416,6 @@ __device__ __forceinline__ uint4 v_piece(const uint8_t* rec, int i, int l) {
     }
 }
 
-// V of the tile, groups 2·warp and 2·warp + 1, by one warp; f0, f1: formats of the two blocks.
 template <int KIND>
 __device__ __forceinline__ uint4 v_piece_kind(const uint8_t* rec, uint32_t word, int i, int l) {
     if constexpr (KIND == kKindBf16) {
@@ -416,33 +428,59 @@ __device__ __forceinline__ uint4 v_piece_kind(const uint8_t* rec, uint32_t word,
         return v_piece<kFmtE4m3>(rec, i, l);
     }
 }
+// raw: the tile's four records.
 template <int KIND>
-__device__ __forceinline__ void repack_v(const uint8_t (*rec)[max_record(KIND)], const uint32_t (&word)[4], VPut& out, int warp,
+__device__ __forceinline__ void repack_v(const uint8_t* raw, const uint32_t (&word)[4], VPut& out, const Offsets& o, int warp,
                                          int lane) {
+    constexpr int kRec = max_record(KIND);
     const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
-    const uint32_t w0 = word[2 * p], w1 = word[2 * p + 1];
-    const uint32_t m0 = w0 & 0xffffu, m1 = w1 & 0xffffu;
-    uint4 a[4], b[4];
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int group = 2 * warp + (i >> 1), r = 2 * rl + ((i & 1) ^ p);
-        a[i] = v_piece_kind<KIND>(rec[2 * p], w0, group, 4 * r + x);
-        b[i] = v_piece_kind<KIND>(rec[2 * p + 1], w1, group, 4 * r + x);
-    }
-    if (!out.look && (w0 & w1 & 0xffffu) == 0xffffu) {   // the usual tile: every position attended by every row
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = 16 * (2 * warp + (i >> 1)) + 2 * rl + ((i & 1) ^ p);
-            put16(out.op, d, 4 * p + x, a[i].x, a[i].z, b[i].x, b[i].z);
-            put16(out.op, d + 8, 4 * p + x, a[i].y, a[i].w, b[i].y, b[i].w);
+    const uint8_t* r0 = raw + 2 * p * kRec;
+    if (KIND != kKindMixed && !out.look && (word[0] & word[1] & word[2] & word[3] & 0xffffu) == 0xffffu) {
+        // the usual tile: every position attended by every row
+        if constexpr (KIND == kKindBf16) {
+            uint4 a[4], b[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = ld16(r0 + o.v_ld[0][i & 1] + (i >> 1) * 512);
+                b[i] = ld16(r0 + o.v_ld[0][i & 1] + (i >> 1) * 512 + kRec);
+            }
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint8_t* to = out.op + o.v_st[i & 1] + (i >> 1) * 2048;
+                st16(to, a[i].x, a[i].z, b[i].x, b[i].z);
+                st16(to + 1024, a[i].y, a[i].w, b[i].y, b[i].w);
+            }
+        } else {
+            uint4 a[2], b[2];
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                a[q] = ld16(r0 + o.v_ld[1][q]);
+                b[q] = ld16(r0 + o.v_ld[1][q] + kRec);
+            }
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = i & 1;
+                uint32_t lo[4], hi[4];
+                codes_to_bf16<kFmtE4m3>(i >> 1 ? a[q].z : a[q].x, lo[0], hi[0]);
+                codes_to_bf16<kFmtE4m3>(i >> 1 ? a[q].w : a[q].y, lo[1], hi[1]);
+                codes_to_bf16<kFmtE4m3>(i >> 1 ? b[q].z : b[q].x, lo[2], hi[2]);
+                codes_to_bf16<kFmtE4m3>(i >> 1 ? b[q].w : b[q].y, lo[3], hi[3]);
+                uint8_t* to = out.op + o.v_st[q] + (i >> 1) * 2048;
+                st16(to, lo[0], lo[1], lo[2], lo[3]);
+                st16(to + 1024, hi[0], hi[1], hi[2], hi[3]);
+            }
         }
         return;
     }
-    #pragma unroll
+    const uint32_t w0 = word[2 * p], w1 = word[2 * p + 1];
+    const uint32_t m0 = w0 & 0xffffu, m1 = w1 & 0xffffu;
+    #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
-        const int d = 16 * (2 * warp + (i >> 1)) + 2 * rl + ((i & 1) ^ p);
-        out.put(d, p, x, a[i].x, a[i].z, b[i].x, b[i].z, m0, m1);
-        out.put(d + 8, p, x, a[i].y, a[i].w, b[i].y, b[i].w, m0, m1);
+        const int group = 2 * warp + (i >> 1), r = 2 * rl + ((i & 1) ^ p);
+        const uint4 a = v_piece_kind<KIND>(r0, w0, group, 4 * r + x);
+        const uint4 b = v_piece_kind<KIND>(r0 + kRec, w1, group, 4 * r + x);
+        out.put(16 * group + r, p, x, a.x, a.z, b.x, b.z, m0, m1);
+        out.put(16 * group + r + 8, p, x, a.y, a.w, b.y, b.w, m0, m1);
     }
 }
 
@@ -558,34 +596,15 @@ __device__ __noinline__ float pool_value(const ChunkParams& p, int b, int h, int
 }
 
 // ------------------------------------------------------------------ the roles
-// Wait for the barrier's phase with the given parity: one instruction when it is there already.  A try
-// suspends the warp for some 8,000 cycles at most and wakes within about 130, so the limit, a second or
-// so, is a count of tries; reading the timer would add 700 cycles to every wait.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t"
-        ".reg .pred p;\n\t"
-        ".reg .u32 n;\n\t"
-        "mov.u32 n, %3;\n\t"
-        "AGAIN:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@p bra DONE;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 p, n, 0;\n\t"
-        "@p bra AGAIN;\n\t"
-        "DONE:\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "n"(kTries)
-        : "memory");
-    return ok != 0;
-}
+// Wait of a whole warp for a barrier's phase; one answer for all its lanes.  A try suspends the warp for
+// some 8,000 cycles at most and wakes within about 130, so the limit, a second or so, is a count of tries;
+// reading the timer would add 700 cycles to every wait that is not over at once.
 template <int KIND>
-__device__ __forceinline__ bool wait_bar(Smem<KIND>& s, const ChunkParams& p, uint64_t* bar, uint32_t phase) {
-    if (wait_phase(bar, phase & 1u)) return true;
-    if (atomicExch(&s.abort, 1) == 0) report(p.err, KVD_ERR_TIMEOUT);
+__device__ __forceinline__ bool wait_bar(Smem<KIND>& s, uint64_t* bar, uint32_t phase) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i)
+        if (__all_sync(kFull, mbar_try_wait(bar, phase & 1u))) return true;
+    s.abort = 1;   // reported at the kernel's end
     return false;
 }
 
@@ -612,8 +631,7 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
             const int n = min(8, g.t1 - tb);
             for (int i = 0; i < n; ++i, ++k) {
                 const int st = k % kRaw;
-                ok = wait_bar(s, p, &s.raw_empty[st], (k / kRaw) + 1);
-                ok = __all_sync(kFull, ok);
+                ok = wait_bar(s, &s.raw_empty[st], (k / kRaw) + 1);
                 if (!ok) break;
                 const bool mine = (lane >> 2) == i;
                 uint32_t bytes = 0;
@@ -658,14 +676,15 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
 template <int KIND>
 __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
     constexpr int kRaw = raw_stages(KIND);
+    const Offsets off(warp, lane);
     Walk walk(p, s);
     Segment g;
     uint32_t k = 0;
     while (walk.next(p, g)) {
         for (int t = g.t0; t < g.t1; ++t, ++k) {
             const int st = k % kRaw, op = k % kStages;
-            bool ok = wait_bar(s, p, &s.kv_empty[op], (k / kStages) + 1) && wait_bar(s, p, &s.raw_full[st], k / kRaw);
-            if (!__all_sync(kFull, ok)) return;
+            bool ok = wait_bar(s, &s.kv_empty[op], (k / kStages) + 1) && wait_bar(s, &s.raw_full[st], k / kRaw);
+            if (!ok) return;
             uint32_t word[4];
             #pragma unroll
             for (int i = 0; i < 4; ++i) word[i] = s.meta[st][i];
@@ -678,10 +697,10 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
             }
             uint8_t* kop = s.op[op][0];
             VPut v{s.op[op][1], 0ull, look};
-            const uint8_t* rec = s.raw[st][warp];
+            const uint8_t* rec = s.raw[st][warp];   // this warp's block
             if constexpr (KIND == kKindBf16) {
-                repack_k<kFmtBf16>(rec, kop, warp, lane);
-                repack_v<KIND>(s.raw[st], word, v, warp, lane);
+                repack_k<kFmtBf16>(rec, kop, off);
+                repack_v<KIND>(s.raw[st][0], word, v, off, warp, lane);
             } else if constexpr (is_lowbit(KIND)) {
                 constexpr int kBits = KIND == kKindInt4 ? 4 : 2;
                 repack_k_low<kBits>(rec, kop, warp, p.ng, lane);
@@ -689,10 +708,10 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
             } else {
                 int f = kFmtE4m3;
                 if constexpr (KIND == kKindMixed) f = (word[warp] >> 17) & 3u;
-                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(rec, kop, warp, lane);
-                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(rec, kop, warp, lane);
-                else repack_k<kFmtE4m3>(rec, kop, warp, lane);
-                repack_v<KIND>(s.raw[st], word, v, warp, lane);
+                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(rec, kop, off);
+                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(rec, kop, off);
+                else repack_k<kFmtE4m3>(rec, kop, off);
+                repack_v<KIND>(s.raw[st][0], word, v, off, warp, lane);
                 if (lane < kBs) {
                     const float* sc = reinterpret_cast<const float*>(rec + 2 * kTileFp8);
                     const bool on = word[warp] >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
@@ -737,7 +756,7 @@ __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, 
         const uint32_t mine = two ? n : (n + 1 - W) / 2, stride = two ? 1 : 2;
         const uint32_t which = two ? W : 0;   // whose rows
         // both barriers' phases are followed in order, whether this warp has tiles or not
-        ok = wait_bar(s, p, &s.q_ready[0], segs[0]) && (!two || W == 0 || wait_bar(s, p, &s.q_ready[1], segs[1]));
+        ok = wait_bar(s, &s.q_ready[0], segs[0]) && (!two || W == 0 || wait_bar(s, &s.q_ready[1], segs[1]));
         tcgen_fence_after();
         const uint32_t k0 = base + (two ? 0 : W);
         uint32_t ss = k0 % kStages, sp = (k0 / kStages) & 1u;   // stage and phase of the next S
@@ -760,12 +779,12 @@ __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, 
             }
         };
         if (ok && mine > 0) {
-            ok = wait_bar(s, p, &s.kv_full[ss], sp);
+            ok = wait_bar(s, &s.kv_full[ss], sp);
             if (ok) score();
         }
         #pragma unroll 1
         for (uint32_t i = 0; ok && i < mine; ++i, ++step) {
-            ok = wait_bar(s, p, &s.s_free[W], step);
+            ok = wait_bar(s, &s.s_free[W], step);
             if (!ok) break;
             // the next tile's S first, if its operands are there: a tile still on its way does not hold up O
             uint32_t later = i + 1 < mine;
@@ -773,7 +792,7 @@ __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, 
                 score();
                 later = 0;
             }
-            ok = wait_bar(s, p, &s.p_full[W], step);
+            ok = wait_bar(s, &s.p_full[W], step);
             if (!ok) break;
             tcgen_fence_after();
             const uint32_t addr = uniform(op0 + vs * (2 * kOpBytes) + kOpBytes);
@@ -789,7 +808,7 @@ __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, 
             vs += stride;
             if (vs >= kStages) vs -= kStages;
             if (later) {
-                ok = wait_bar(s, p, &s.kv_full[ss], sp);
+                ok = wait_bar(s, &s.kv_full[ss], sp);
                 if (ok) score();
             }
         }
@@ -862,7 +881,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, sk = 0, pvk = 0, merges = 0;   // phases of s_full, pv_done, the merge
+    uint32_t base = 0, sk = 0, pvk = 0, merges = 0, turns = 0;   // phases of s_full, pv_done, the merge; turns taken
     bool merge_pending = false;
     int seg_index = 0;
     while (walk.next(p, g)) {
@@ -881,7 +900,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         __syncwarp();
         if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
         if (merge_pending) {   // WG 0 has read the last unit's O of this warpgroup
-            if (!__all_sync(kFull, wait_bar(s, p, &s.merge_empty, merges - 1))) return;
+            if (!wait_bar(s, &s.merge_empty, merges - 1)) return;
             merge_pending = false;
         }
         float m = -INFINITY, l = 0.f;
@@ -892,8 +911,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             const uint32_t k = base + (g.two ? i : 2 * i + w);
             const int st = k % kStages;
             const int t = g.t0 + (g.two ? i : 2 * i + w);
-            bool ok = wait_bar(s, p, &s.s_full[w], sk) && wait_bar(s, p, &s.kv_full[st], k / kStages);
-            if (!__all_sync(kFull, ok)) return;
+            // (kv_full: the stage's mask and factors, there since before the MMAs)
+            if (!wait_bar(s, &s.s_full[w], sk) || !wait_bar(s, &s.kv_full[st], k / kStages)) return;
             ++sk;
             tcgen_fence_after();
             uint32_t raw[2][32];
@@ -904,6 +923,13 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             tcgen_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.s_free[w]);
+            // The warpgroups take turns from here to the end of the exponentials.  Left to themselves their
+            // warps share each scheduler, the four of a warpgroup end up to 950 cycles apart, and the MMAs wait
+            // for the last.
+            if (g.two) {
+                if (w + turns > 0 && !wait_bar(s, &s.turn[w], turns - 1 + w)) return;
+                ++turns;
+            }
             float x[kTile];
             #pragma unroll
             for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
@@ -935,16 +961,22 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     flag_tile[flagged++] = t;
                 }
             }
-            float top = -INFINITY;
+            float top = max3(x[0], x[1], x[2]), top2 = max3(x[3], x[4], x[5]);
             #pragma unroll
-            for (int c = 0; c < kTile; ++c) top = fmaxf(top, x[c]);
-            top *= rs;
-            if (i > 0) {   // the last tile's O is complete and its P read
-                if (!__all_sync(kFull, wait_bar(s, p, &s.pv_done[w], pvk))) return;
-                ++pvk;
-                tcgen_fence_after();
+            for (int c = 6; c < kTile - 2; c += 4) {
+                top = max3(top, x[c], x[c + 1]);
+                top2 = max3(top2, x[c + 2], x[c + 3]);
             }
+            top = fmaxf(max3(top, x[kTile - 2], x[kTile - 1]), top2) * rs;
+            // The last tile's O is complete and its P read: needed here to rescale O, else only by the store of P.
+            bool waited = i == 0;
             if (__any_sync(kFull, top > m + kLazy)) {
+                if (!waited) {
+                    if (!wait_bar(s, &s.pv_done[w], pvk)) return;
+                    ++pvk;
+                    waited = true;
+                    tcgen_fence_after();
+                }
                 const float nm = fmaxf(m, top);
                 const float f = m == nm ? 1.f : ex2(m - nm);
                 m = nm;
@@ -962,14 +994,17 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 rs2 = make_float2(rs, rs), ref2 = make_float2(-ref, -ref);
             uint32_t pw[32];
             #pragma unroll
             for (int c = 0; c < kTile; c += 4) {
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[c + e] = ex2(fmaf(x[c + e], rs, -ref));
-                    sum[e] += x[c + e];
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 y = fma2(make_float2(x[c + e], x[c + e + 1]), rs2, ref2);
+                    x[c + e] = ex2(y.x);
+                    x[c + e + 1] = ex2(y.y);
+                    sum[e / 2] = add2(sum[e / 2], make_float2(x[c + e], x[c + e + 1]));
                 }
                 if constexpr (has_factors(KIND)) {
                     const float4 f = *reinterpret_cast<const float4*>(&s.factor[st][1][c]);
@@ -981,7 +1016,13 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 pw[c / 2] = pack_bf16(x[c], x[c + 1]);
                 pw[c / 2 + 1] = pack_bf16(x[c + 2], x[c + 3]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (g.two && lane == 0) mbar_arrive(&s.turn[w ^ 1]);
+            if (!waited) {
+                if (!wait_bar(s, &s.pv_done[w], pvk)) return;
+                ++pvk;
+                tcgen_fence_after();
+            }
             tmem_st32(col_p, pw);
             tmem_wait_st();
             tcgen_fence_before();
@@ -989,7 +1030,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (lane == 0) mbar_arrive(&s.p_full[w]);
         }
         if (mine > 0) {
-            if (!__all_sync(kFull, wait_bar(s, p, &s.pv_done[w], pvk))) return;
+            if (!wait_bar(s, &s.pv_done[w], pvk)) return;
             ++pvk;
             tcgen_fence_after();
         }
@@ -1032,7 +1073,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 ++seg_index;
                 continue;
             }
-            if (!__all_sync(kFull, wait_bar(s, p, &s.merge_full, merges))) return;
+            if (!wait_bar(s, &s.merge_full, merges)) return;
             ++merges;
             tcgen_fence_after();
             const float m1 = s.ml[0][tid], l1 = s.ml[1][tid];
@@ -1129,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_ready[i], 4);
+            mbar_init(&s.turn[i], 4);
             mbar_init(&s.drain[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 4);
@@ -1151,14 +1193,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     tcgen_fence_after();
     // one copy of each role's code: with one per warpgroup the loops outgrow the instruction cache
     // (its misses took 90% of the next level's rate, and every role ran at half speed)
-    if (warp < 8) softmax_group<KIND>(s, p, warp >> 2, tid & 127, lane);
-    else if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
-    else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-    else if (warp < kMmaWarp + 2) mma_issuer<KIND>(s, p, warp - kMmaWarp);
+    // Registers: 512 threads at 128 take the whole file; 2·128·168 + 2·128·88 = 512·128.
+    if (warp < 8) {
+        take_registers<168>();
+        softmax_group<KIND>(s, p, warp >> 2, tid & 127, lane);
+    } else {
+        give_registers<88>();
+        if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
+        else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
+        else if (warp < kMmaWarp + 2) mma_issuer<KIND>(s, p, warp - kMmaWarp);
+    }
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
+    if (tid == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
     if (warp == kMmaWarp) tmem_free_all(s.tmem);
 }
 
