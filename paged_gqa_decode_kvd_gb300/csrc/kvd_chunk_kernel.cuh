@@ -52,16 +52,17 @@ constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
 constexpr int kThreads = 512;          // softmax 2 × 128, repack 128, producer 32, MMA 2 × 32, one warp idle
 constexpr int kRepackWarp = 8, kProducerWarp = 12, kMmaWarp = 13;
-constexpr int kStages = 3;             // operand stages (K 16 KiB + V 16 KiB)
+constexpr int kKStages = 2, kVStages = 3;   // operand stages, 16 KiB each
+constexpr int kInfos = 4;              // tiles whose masks and factors are kept
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kTries = 200000;         // tries of a wait: a second or so
-constexpr int kColS = 0, kColP = 128, kColQ = 192, kColO = 256;   // tensor memory columns: S 2 × 64, P 2 × 32, Q 2 × 32, O 2 × 128
+constexpr int kColS = 0, kColP = 128, kColO = 256;   // tensor memory columns: S 2 × 64, P 2 × 2 × 32, O 2 × 128
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
-constexpr int raw_stages(int kind) { return kind == kKindBf16 ? 3 : kind == kKindMixed ? 2 : 5; }
+constexpr int raw_stages(int kind) { return kind == kKindBf16 ? 5 : kind == kKindMixed ? 4 : 8; }   // two records each
 constexpr int max_record(int kind) {
     return kind == kKindBf16 || kind == kKindMixed ? kRecordBf16
            : kind == kKindInt4                     ? lowbit_record_bytes(4, 4)
@@ -69,29 +70,29 @@ constexpr int max_record(int kind) {
                                                    : kRecordFp8;
 }
 
-struct StageInfo {
-    unsigned long long mask;     // bit 16·block + t: position may be attended
+struct TileInfo {
+    unsigned long long mask;        // bit 16·block + t: position may be attended
     unsigned long long nonfin[4];   // by repack warp; column n: its V has non-finite elements, zeroed in the operand
 };
 
 template <int KIND>
 struct Smem {
-    uint8_t op[kStages][2][kOpBytes];                           // K, V operands; 1,024-byte aligned
-    uint8_t q[2][kOpBytes];                                     // second half of q's dims, 128 rows each
-    uint8_t raw[raw_stages(KIND)][4][max_record(KIND)];
-    float factor[has_factors(KIND) ? kStages : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
-    float ml[2][kWgRows];                                       // merge: WG 1's maximum and sum
-    uint32_t meta[raw_stages(KIND)][4];                         // block words
-    StageInfo info[kStages];
+    uint8_t k[kKStages][kOpBytes], v[kVStages][kOpBytes];       // operands; 1,024-byte aligned
+    uint8_t q[2][2 * kOpBytes];                                 // 128 rows each
+    uint8_t raw[raw_stages(KIND)][2][max_record(KIND)];
+    float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
+    TileInfo info[kInfos];
+    uint32_t meta[raw_stages(KIND)][2];                         // block words
     uint64_t raw_full[raw_stages(KIND)], raw_empty[raw_stages(KIND)];
-    uint64_t kv_full[kStages], kv_empty[kStages];
-    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
-    uint64_t turn[2];   // a warpgroup may work on its logits
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t s_full[2], s_taken[2], p_last[2], pv_done[2];
     uint64_t q_ready[2], merge_full, merge_empty, drain[2];
     int64_t remaining;
     int b, h, qt, off;
     uint32_t tmem;
     int abort;
+    // the merge of the two warpgroups: WG 1's maximum and sum, where no query of its own is
+    __device__ __forceinline__ float* ml() { return reinterpret_cast<float*>(q[1]); }
 };
 
 // ------------------------------------------------------------------ schedule
@@ -428,13 +429,12 @@ __device__ __forceinline__ uint4 v_piece_kind(const uint8_t* rec, uint32_t word,
         return v_piece<kFmtE4m3>(rec, i, l);
     }
 }
-// raw: the tile's four records.
+// pair: the lane's two records.
 template <int KIND>
-__device__ __forceinline__ void repack_v(const uint8_t* raw, const uint32_t (&word)[4], VPut& out, const Offsets& o, int warp,
+__device__ __forceinline__ void repack_v(const uint8_t* r0, const uint32_t (&word)[4], VPut& out, const Offsets& o, int warp,
                                          int lane) {
     constexpr int kRec = max_record(KIND);
     const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
-    const uint8_t* r0 = raw + 2 * p * kRec;
     if (KIND != kKindMixed && !out.look && (word[0] & word[1] & word[2] & word[3] & 0xffffu) == 0xffffu) {
         // the usual tile: every position attended by every row
         if constexpr (KIND == kKindBf16) {
@@ -512,7 +512,7 @@ __device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, in
     }
 }
 template <int KIND, int BITS>
-__device__ __forceinline__ void repack_v_low(const uint8_t (*rec)[max_record(KIND)], const uint32_t (&word)[4], VPut& out,
+__device__ __forceinline__ void repack_v_low(const uint8_t* pair, const uint32_t (&word)[4], VPut& out,
                                              int ng, int warp, int lane) {
     constexpr int kPer = 8 / BITS, kTileB = lowbit_tile_bytes(BITS);
     const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
@@ -525,7 +525,7 @@ __device__ __forceinline__ void repack_v_low(const uint8_t (*rec)[max_record(KIN
             uint32_t o[2][4];   // dims r, r + 8: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p, 2p+1
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint8_t* b = rec[2 * p + u];
+                const uint8_t* b = pair + u * max_record(KIND);
                 const uint32_t* meta = reinterpret_cast<const uint32_t*>(b + 2 * kTileB) + kBs * ng;
                 const int gi = group * ng / 8;
                 #pragma unroll
@@ -576,6 +576,7 @@ __device__ __forceinline__ uint32_t block_word_of(const ChunkParams& p, int phys
 template <int KIND>
 __device__ __noinline__ float pool_value(const ChunkParams& p, int b, int h, int pos, int d) {
     const int phys = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+    if (phys < 0 || phys >= p.num_blocks + p.host_blocks) return 0.f;
     const uint8_t* rec = record_at(p, phys, h);
     const int t = pos % kBs;
     int fl, fe;
@@ -608,12 +609,26 @@ __device__ __forceinline__ bool wait_bar(Smem<KIND>& s, uint64_t* bar, uint32_t 
     return false;
 }
 
+// Three waits with one vote; the third only if `third`.
+template <int KIND>
+__device__ __forceinline__ bool wait_three(Smem<KIND>& s, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c,
+                                           uint32_t pc, bool third) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        const bool x = mbar_try_wait(a, pa & 1u), y = mbar_try_now(b, pb & 1u);
+        const bool z = !third || mbar_try_now(c, pc & 1u);
+        if (__all_sync(kFull, x && y && z)) return true;
+    }
+    s.abort = 1;
+    return false;
+}
+
 template <int KIND>
 __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, int lane) {
     constexpr int kRaw = raw_stages(KIND);
     Walk walk(p, s);
     Segment g;
-    uint32_t k = 0;
+    uint32_t k = 0;   // pairs of blocks so far: two a tile
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const int32_t* row = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks;
@@ -628,22 +643,17 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
                 if (word) rec = record_at(p, phys, g.h);
                 host = word && p.host_direct && phys >= p.num_blocks;
             }
-            const int n = min(8, g.t1 - tb);
+            uint32_t bytes = 0;
+            if (word && !host)
+                bytes = KIND == kKindMixed && ((word >> 17) & 3u) != kFmtBf16 ? kRecordFp8 : static_cast<uint32_t>(p.record_bytes);
+            const uint32_t both = bytes + __shfl_xor_sync(kFull, bytes, 1);
+            const int n = 2 * min(8, g.t1 - tb);
             for (int i = 0; i < n; ++i, ++k) {
                 const int st = k % kRaw;
                 ok = wait_bar(s, &s.raw_empty[st], (k / kRaw) + 1);
                 if (!ok) break;
-                const bool mine = (lane >> 2) == i;
-                uint32_t bytes = 0;
-                if (mine) {
-                    s.meta[st][lane & 3] = word;
-                    if (word)
-                        bytes = KIND == kKindMixed && ((word >> 17) & 3u) != kFmtBf16 ? kRecordFp8
-                                                                                     : static_cast<uint32_t>(p.record_bytes);
-                }
-                uint32_t bulk = host ? 0 : bytes;
-                bulk += __shfl_xor_sync(kFull, bulk, 1);
-                bulk += __shfl_xor_sync(kFull, bulk, 2);
+                const bool mine = (lane >> 1) == i;
+                if (mine) s.meta[st][lane & 1] = word;
                 if (p.host_direct) {   // records in host memory: copied by the load path, the whole warp
                     unsigned hosts = __ballot_sync(kFull, mine && host);
                     fence_proxy_async_shared();
@@ -653,17 +663,17 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
                         const uint8_t* src = reinterpret_cast<const uint8_t*>(
                             __shfl_sync(kFull, reinterpret_cast<unsigned long long>(rec), l));
                         for (int c = lane; c < p.record_bytes / 16; c += 32)
-                            cp_async16_g2s(s.raw[st][l & 3] + 16 * c, src + 16 * c);
+                            cp_async16_g2s(s.raw[st][l & 1] + 16 * c, src + 16 * c);
                     }
                     cp_async_mbar_arrive(&s.raw_full[st]);
                 }
                 __syncwarp();
-                if (lane == 4 * i) {
-                    if (bulk) mbar_arrive_expect_tx(&s.raw_full[st], bulk);
+                if (lane == 2 * i) {
+                    if (both) mbar_arrive_expect_tx(&s.raw_full[st], both);
                     else mbar_arrive(&s.raw_full[st]);
                 }
                 __syncwarp();
-                if (mine && word && !host) bulk_copy(s.raw[st][lane & 3], rec, bytes, &s.raw_full[st]);
+                if (mine && bytes) bulk_copy(s.raw[st][lane & 1], rec, bytes, &s.raw_full[st]);
             }
         }
     }
@@ -682,44 +692,46 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
     uint32_t k = 0;
     while (walk.next(p, g)) {
         for (int t = g.t0; t < g.t1; ++t, ++k) {
-            const int st = k % kRaw, op = k % kStages;
-            bool ok = wait_bar(s, &s.kv_empty[op], (k / kStages) + 1) && wait_bar(s, &s.raw_full[st], k / kRaw);
-            if (!ok) return;
-            uint32_t word[4];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) word[i] = s.meta[st][i];
+            const int r0 = (2 * k) % kRaw, r1 = (2 * k + 1) % kRaw;   // the tile's pairs of blocks
+            const int ks = k % kKStages, vs = k % kVStages, in = k % kInfos;
+            if (!wait_bar(s, &s.raw_full[r0], 2 * k / kRaw) || !wait_bar(s, &s.raw_full[r1], (2 * k + 1) / kRaw) ||
+                !wait_bar(s, &s.k_empty[ks], (k / kKStages) + 1))
+                return;
+            const uint32_t word[4] = {s.meta[r0][0], s.meta[r0][1], s.meta[r1][0], s.meta[r1][1]};
+            const uint32_t mine = warp < 2 ? (warp & 1 ? word[1] : word[0]) : (warp & 1 ? word[3] : word[2]);
             const bool look = t * kTile + kTile - 1 > g.first;
-            if (warp == 0 && lane == 0) {
-                s.info[op].mask = static_cast<unsigned long long>(word[0] & 0xffffu) |
+            if (warp == 0 && lane == 0)
+                s.info[in].mask = static_cast<unsigned long long>(word[0] & 0xffffu) |
                                   static_cast<unsigned long long>(word[1] & 0xffffu) << 16 |
                                   static_cast<unsigned long long>(word[2] & 0xffffu) << 32 |
                                   static_cast<unsigned long long>(word[3] & 0xffffu) << 48;
-            }
-            uint8_t* kop = s.op[op][0];
-            VPut v{s.op[op][1], 0ull, look};
-            const uint8_t* rec = s.raw[st][warp];   // this warp's block
+            const uint8_t* rec = s.raw[warp < 2 ? r0 : r1][warp & 1];   // this warp's block
             if constexpr (KIND == kKindBf16) {
-                repack_k<kFmtBf16>(rec, kop, off);
-                repack_v<KIND>(s.raw[st][0], word, v, off, warp, lane);
+                repack_k<kFmtBf16>(rec, s.k[ks], off);
             } else if constexpr (is_lowbit(KIND)) {
-                constexpr int kBits = KIND == kKindInt4 ? 4 : 2;
-                repack_k_low<kBits>(rec, kop, warp, p.ng, lane);
-                repack_v_low<KIND, kBits>(s.raw[st], word, v, p.ng, warp, lane);
+                repack_k_low<KIND == kKindInt4 ? 4 : 2>(rec, s.k[ks], warp, p.ng, lane);
             } else {
                 int f = kFmtE4m3;
-                if constexpr (KIND == kKindMixed) f = (word[warp] >> 17) & 3u;
-                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(rec, kop, off);
-                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(rec, kop, off);
-                else repack_k<kFmtE4m3>(rec, kop, off);
-                repack_v<KIND>(s.raw[st][0], word, v, off, warp, lane);
+                if constexpr (KIND == kKindMixed) f = (mine >> 17) & 3u;
+                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(rec, s.k[ks], off);
+                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(rec, s.k[ks], off);
+                else repack_k<kFmtE4m3>(rec, s.k[ks], off);
                 if (lane < kBs) {
                     const float* sc = reinterpret_cast<const float*>(rec + 2 * kTileFp8);
-                    const bool on = word[warp] >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
+                    const bool on = mine >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
                     const int n = column_of(warp, lane);
-                    s.factor[op][0][n] = wide ? 1.f : sc[lane];
-                    s.factor[op][1][n] = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
+                    s.factor[in][0][n] = wide ? 1.f : sc[lane];
+                    s.factor[in][1][n] = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
                 }
             }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.k_full[ks]);
+            if (!wait_bar(s, &s.v_empty[vs], (k / kVStages) + 1)) return;
+            VPut v{s.v[vs], 0ull, look};
+            const uint8_t* pair = s.raw[(lane & 4) ? r1 : r0][0];   // lanes take the pair of blocks of their columns
+            if constexpr (is_lowbit(KIND)) repack_v_low<KIND, KIND == kKindInt4 ? 4 : 2>(pair, word, v, p.ng, warp, lane);
+            else repack_v<KIND>(pair, word, v, off, warp, lane);
             fence_proxy_async_shared();
             if (look) {
                 const uint32_t lo = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad));
@@ -728,108 +740,108 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
             }
             __syncwarp();
             if (lane == 0) {
-                s.info[op].nonfin[warp] = v.bad;
-                mbar_arrive(&s.raw_empty[st]);
-                mbar_arrive(&s.kv_full[op]);
+                s.info[in].nonfin[warp] = v.bad;
+                mbar_arrive(&s.v_full[vs]);
+                mbar_arrive(&s.raw_empty[r0]);
+                mbar_arrive(&s.raw_empty[r1]);
             }
         }
     }
 }
 
-// The MMAs of warpgroup W, by one warp: S_W of the next tile as soon as the warpgroup has this one's in
-// registers, then O_W += P_W·V.  A warp for each warpgroup, since one that looks at the barriers of both
-// in turn answers each some 700 cycles late.
+// The MMAs of warpgroup W, by one warp.  One arrival a step, s_taken: S(i) is in the warpgroup's registers
+// and P(i−1) in tensor memory; then O += P(i−1)·V(i−1) and S(i+1) = Q·K(i+1) are issued together, and one
+// commit, s_full, says that both are done.  So a warpgroup waits once a step, P needs two buffers (P(i+1)
+// is written when PV(i−1) is done), and the two warpgroups' bundles, some 650 cycles each, stagger them.
+// (Before, S and PV had barriers of their own and the waits, 100 to 300 cycles each, were most of a step.)
 template <int KIND>
 __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
     constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
-    const uint32_t el = elect_one(), W = uniform(warpgroup);
+    const uint32_t W = uniform(warpgroup);
     const uint32_t tmem = uniform(s.tmem);
-    const uint32_t op0 = uniform(smem_u32(s.op)), q0 = uniform(smem_u32(s.q));
-    const uint32_t col_s = uniform(tmem + kColS + W * 64), col_p = uniform(tmem + kColP + W * 32);
-    const uint32_t col_o = uniform(tmem + kColO + W * 128);
+    const uint32_t k_op = uniform(smem_u32(s.k)), v_op = uniform(smem_u32(s.v)), q_op = uniform(smem_u32(s.q));
+    const uint32_t col_s = uniform(tmem + kColS + W * 64), col_o = uniform(tmem + kColO + W * 128);
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, segs[2] = {0, 0}, step = 0;   // tiles before the segment; phases of q_ready, of s_free and p_full
+    uint32_t base = 0, segs[2] = {0, 0}, step = 0, ends = 0;   // tiles before the segment; phases of q_ready, s_taken, p_last
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
         const uint32_t mine = two ? n : (n + 1 - W) / 2, stride = two ? 1 : 2;
-        const uint32_t which = two ? W : 0;   // whose rows
         // both barriers' phases are followed in order, whether this warp has tiles or not
         ok = wait_bar(s, &s.q_ready[0], segs[0]) && (!two || W == 0 || wait_bar(s, &s.q_ready[1], segs[1]));
-        tcgen_fence_after();
         const uint32_t k0 = base + (two ? 0 : W);
-        uint32_t ss = k0 % kStages, sp = (k0 / kStages) & 1u;   // stage and phase of the next S
-        uint32_t vs = ss;                                       // stage of the next O
-        const uint32_t a = uniform(tmem + kColQ + which * 32), b = uniform(q0 + which * kOpBytes);
-        auto score = [&]() {   // S_W = Q·K^T; its operands are there
+        const uint32_t a = uniform(q_op + (two ? W : 0) * 2 * kOpBytes);
+        auto score = [&](uint32_t k) {   // S = Q·K^T of tile k
+            const uint32_t st = k % kKStages;
+            ok = wait_bar(s, &s.k_full[st], k / kKStages);
+            if (!ok) return;
             tcgen_fence_after();
-            const uint32_t addr = uniform(op0 + ss * (2 * kOpBytes));
-            #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_ts(col_s, a + ks * 8, smem_desc_sw128(addr + ks * 32), kDescS, ks > 0, el);
-            #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_ss(col_s, smem_desc_sw128(b + ks * 32), smem_desc_sw128(addr + 8192 + ks * 32), kDescS, true, el);
-            if (el) mma_commit(&s.s_full[W]);
-            ss += stride;
-            if (ss >= kStages) {
-                ss -= kStages;
-                sp ^= 1u;
+            const uint32_t b = uniform(k_op + st * kOpBytes);
+            if (elect_one()) {
+                #pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ss(col_s, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
+                           smem_desc_sw128(b + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
+                mma_commit(&s.s_full[W]);
             }
+            __syncwarp();
         };
-        if (ok && mine > 0) {
-            ok = wait_bar(s, &s.kv_full[ss], sp);
-            if (ok) score();
-        }
+        if (ok && mine > 0) score(k0);
         #pragma unroll 1
-        for (uint32_t i = 0; ok && i < mine; ++i, ++step) {
-            ok = wait_bar(s, &s.s_free[W], step);
-            if (!ok) break;
-            // the next tile's S first, if its operands are there: a tile still on its way does not hold up O
-            uint32_t later = i + 1 < mine;
-            if (later && uniform(mbar_try_now(&s.kv_full[ss], sp))) {
-                score();
-                later = 0;
-            }
-            ok = wait_bar(s, &s.p_full[W], step);
+        for (uint32_t i = 0; ok && mine > 0 && i <= mine; ++i) {
+            // (the last P has a barrier of its own: a warp may be there before another has taken its S)
+            ok = i < mine ? wait_bar(s, &s.s_taken[W], step++) : wait_bar(s, &s.p_last[W], ends++);
             if (!ok) break;
             tcgen_fence_after();
-            const uint32_t addr = uniform(op0 + vs * (2 * kOpBytes) + kOpBytes);
-            const uint32_t more = uniform(i);
-            #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                mma_ts(col_o, col_p + ks * 8, smem_desc_sw128(addr + ks * 32), kDescO, more || ks > 0, el);
-            if (el) {
-                mma_commit(&s.pv_done[W]);
-                mma_commit(&s.kv_empty[vs]);
-                if (!two) mbar_arrive(&s.kv_empty[vs]);   // two arrivals a stage: no other warpgroup reads it
+            const uint32_t k = k0 + i * stride;
+            if (elect_one()) {   // two arrivals a stage: from both warpgroups, or twice from the one that has the tile
+                if (i < mine) {
+                    mbar_arrive(&s.k_empty[k % kKStages]);
+                    if (!two) mbar_arrive(&s.k_empty[k % kKStages]);
+                }
+                if (two && i >= 2 && i < mine) mbar_arrive(&s.v_empty[(k - 2) % kVStages]);   // S(i) came after PV(i−2)
             }
-            vs += stride;
-            if (vs >= kStages) vs -= kStages;
-            if (later) {
-                ok = wait_bar(s, &s.kv_full[ss], sp);
-                if (ok) score();
+            __syncwarp();
+            if (i > 0) {   // O += P·V of the tile before
+                const uint32_t kp = k - stride, st = kp % kVStages;
+                ok = wait_bar(s, &s.v_full[st], kp / kVStages);
+                if (!ok) break;
+                tcgen_fence_after();
+                const uint32_t b = uniform(v_op + st * kOpBytes), c = uniform(tmem + kColP + W * 64 + ((i - 1) & 1) * 32);
+                const uint32_t more = uniform(i > 1);
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ts(col_o, c + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
+                    mma_commit(&s.pv_done[W]);
+                    // The stage goes back with the MMAs where no later step says that they are done: the last two, and
+                    // with tiles taken in turn every one (two steps later is four tiles, more than there are stages).
+                    if (!two || i == mine) mma_commit(&s.v_empty[st]);
+                    if (!two) mbar_arrive(&s.v_empty[st]);
+                    if (two && i == mine && i >= 2) mma_commit(&s.v_empty[(kp - 1) % kVStages]);
+                }
+                __syncwarp();
             }
+            if (i + 1 < mine) score(k + stride);
         }
         base += n;
         ++segs[0];
         if (two) ++segs[1];
     }
     __syncwarp();
-    if (!ok && el) {   // what was issued completes before tensor memory is freed
-        mma_commit(&s.drain[W]);
+    if (!ok) {   // what was issued completes before tensor memory is freed
+        if (elect_one()) mma_commit(&s.drain[W]);
+        __syncwarp();
         mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
     }
 }
 
 // A row of q as the A operand, in the dim order of the K operand: word 16j + 4x + m is the pair of dims
-// 32j + 2x + 8m.  The first 64 dims go to tensor memory, the others to shared memory: S and P then have
-// columns of their own, and S_w of the next tile is computed while the warpgroup works on this one's.
-// Returns the factor of the row's logits (angle-domain).
+// 32j + 2x + 8m.  Returns the factor of the row's logits (angle-domain).
 template <int KIND>
-__device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t* q, bool row, bool store, bool flip, uint32_t addr,
-                                            uint8_t* line, int r) {
+__device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t* q, bool row, bool store, bool flip, uint8_t* op,
+                                            int r) {
     float factor = 1.f;
     uint32_t w[2][32];
     #pragma unroll
@@ -862,10 +874,10 @@ __device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t
         factor = d2 == 0.f ? 0.f : sc * sqrtf(r2 / d2);
     }
     if (store) {
-        tmem_st32(addr, w[0]);
         #pragma unroll
-        for (int c = 0; c < 8; ++c) put16(line, r, c, w[1][4 * c], w[1][4 * c + 1], w[1][4 * c + 2], w[1][4 * c + 3]);
-        tmem_wait_st();
+        for (int c = 0; c < 16; ++c)
+            put16(op + (c >> 3) * kOpBytes, r, c & 7, w[c >> 3][4 * (c & 7)], w[c >> 3][4 * (c & 7) + 1], w[c >> 3][4 * (c & 7) + 2],
+                  w[c >> 3][4 * (c & 7) + 3]);
         fence_proxy_async_shared();
     }
     return factor;
@@ -875,13 +887,13 @@ template <int KIND>
 __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& p, int w, int tid, int lane) {
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
     const uint32_t tmem = s.tmem + lanes;
-    const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 32, col_o = tmem + kColO + w * 128;
+    const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 64, col_o = tmem + kColO + w * 128;
     // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
     const bool flip = p.scale_log2 < 0.f;
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, sk = 0, pvk = 0, merges = 0, turns = 0;   // phases of s_full, pv_done, the merge; turns taken
+    uint32_t base = 0, done = 0, merges = 0;   // tiles before the segment, of both and of this warpgroup; phases of the merge
     bool merge_pending = false;
     int seg_index = 0;
     while (walk.next(p, g)) {
@@ -892,58 +904,51 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         const int token = g.tok0 + row / p.g, head = g.h * p.g + row % p.g;
         const int64_t out_row = (static_cast<int64_t>(g.s0) + token) * p.n_q + head;
         const int pos = g.len < 0 ? -1 : g.len - g.T + token;
-        float rs = load_query<KIND>(p, p.q + (live ? out_row : 0) * kDh,
-                                    live && (g.two || w == 0 || KIND == kKindAngle), g.two || w == 0, flip,
-                                    tmem + kColQ + (g.two ? w * 32 : 0), s.q[g.two ? w : 0], tid) * scale;
-        rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
-        tcgen_fence_before();
-        __syncwarp();
-        if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
-        if (merge_pending) {   // WG 0 has read the last unit's O of this warpgroup
+        if (merge_pending) {   // WG 0 has read the last unit's O and sums of this warpgroup
             if (!wait_bar(s, &s.merge_empty, merges - 1)) return;
             merge_pending = false;
         }
+        float rs = load_query<KIND>(p, p.q + (live ? out_row : 0) * kDh,
+                                    live && (g.two || w == 0 || KIND == kKindAngle), g.two || w == 0, flip, s.q[g.two ? w : 0],
+                                    tid) * scale;
+        rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
+        __syncwarp();
+        if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
         float m = -INFINITY, l = 0.f;
         int flagged = 0;
         unsigned long long flag_mask[8];
         int flag_tile[8];
         for (int i = 0; i < mine; ++i) {
             const uint32_t k = base + (g.two ? i : 2 * i + w);
-            const int st = k % kStages;
+            const int in = k % kInfos;
             const int t = g.t0 + (g.two ? i : 2 * i + w);
-            // (kv_full: the stage's mask and factors, there since before the MMAs)
-            if (!wait_bar(s, &s.s_full[w], sk) || !wait_bar(s, &s.kv_full[st], k / kStages)) return;
-            ++sk;
+            // S(i) is there; so are the tile's mask and factors (k_full), and PV(i−2) is done, which leaves P(i)'s
+            // buffer free (pv_done, of which every phase is seen in order)
+            if (!wait_three(s, &s.s_full[w], done + i, &s.k_full[k % kKStages], k / kKStages, &s.pv_done[w], done + i - 2, i >= 2))
+                return;
             tcgen_fence_after();
             uint32_t raw[2][32];
             tmem_ld32(col_s, raw[0]);
             tmem_ld32(col_s + 32, raw[1]);
+            unsigned long long may = s.info[in].mask;
             tmem_wait_ld(raw[0]);
             tmem_wait_ld(raw[1]);
             tcgen_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.s_free[w]);
-            // The warpgroups take turns from here to the end of the exponentials.  Left to themselves their
-            // warps share each scheduler, the four of a warpgroup end up to 950 cycles apart, and the MMAs wait
-            // for the last.
-            if (g.two) {
-                if (w + turns > 0 && !wait_bar(s, &s.turn[w], turns - 1 + w)) return;
-                ++turns;
-            }
+            if (lane == 0) mbar_arrive(&s.s_taken[w]);
             float x[kTile];
             #pragma unroll
             for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
             if constexpr (has_factors(KIND)) {
                 #pragma unroll
                 for (int c = 0; c < kTile; c += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&s.factor[st][0][c]);
+                    const float4 f = *reinterpret_cast<const float4*>(&s.factor[in][0][c]);
                     x[c] *= f.x;
                     x[c + 1] *= f.y;
                     x[c + 2] *= f.z;
                     x[c + 3] *= f.w;
                 }
             }
-            unsigned long long may = s.info[st].mask;
             const int t_end = t * kTile + kTile - 1;
             if (may != ~0ull || t_end > g.first) {
                 const int left = pos - t * kTile;   // the row attends places 0 .. left
@@ -954,12 +959,6 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     const int at = place_of(c);
                     if (!((at < 32 ? lo >> at : hi >> (at - 32)) & 1u)) x[c] = -INFINITY;
                 }
-                const unsigned long long bad =
-                    s.info[st].nonfin[0] | s.info[st].nonfin[1] | s.info[st].nonfin[2] | s.info[st].nonfin[3];
-                if (bad && flagged < 8) {
-                    flag_mask[flagged] = bad;
-                    flag_tile[flagged++] = t;
-                }
             }
             float top = max3(x[0], x[1], x[2]), top2 = max3(x[3], x[4], x[5]);
             #pragma unroll
@@ -968,13 +967,9 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 top2 = max3(top2, x[c + 2], x[c + 3]);
             }
             top = fmaxf(max3(top, x[kTile - 2], x[kTile - 1]), top2) * rs;
-            // The last tile's O is complete and its P read: needed here to rescale O, else only by the store of P.
-            bool waited = i == 0;
             if (__any_sync(kFull, top > m + kLazy)) {
-                if (!waited) {
-                    if (!wait_bar(s, &s.pv_done[w], pvk)) return;
-                    ++pvk;
-                    waited = true;
+                if (i > 0) {   // O of the tiles before is complete
+                    if (!wait_bar(s, &s.pv_done[w], done + i - 1)) return;
                     tcgen_fence_after();
                 }
                 const float nm = fmaxf(m, top);
@@ -1007,7 +1002,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     sum[e / 2] = add2(sum[e / 2], make_float2(x[c + e], x[c + e + 1]));
                 }
                 if constexpr (has_factors(KIND)) {
-                    const float4 f = *reinterpret_cast<const float4*>(&s.factor[st][1][c]);
+                    const float4 f = *reinterpret_cast<const float4*>(&s.factor[in][1][c]);
                     x[c] *= f.x;
                     x[c + 1] *= f.y;
                     x[c + 2] *= f.z;
@@ -1017,29 +1012,33 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 pw[c / 2 + 1] = pack_bf16(x[c + 2], x[c + 3]);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            if (g.two && lane == 0) mbar_arrive(&s.turn[w ^ 1]);
-            if (!waited) {
-                if (!wait_bar(s, &s.pv_done[w], pvk)) return;
-                ++pvk;
-                tcgen_fence_after();
+            tmem_st32(col_p + (i & 1) * 32, pw);
+            tmem_wait_st();   // also before the registers are written again
+            if (t_end > g.first) {   // non-finite V that only some rows attend (v_full: the repack has looked)
+                if (!wait_bar(s, &s.v_full[k % kVStages], k / kVStages)) return;
+                const unsigned long long* n4 = s.info[in].nonfin;
+                const unsigned long long bad = n4[0] | n4[1] | n4[2] | n4[3];
+                if (bad && flagged < 8) {
+                    flag_mask[flagged] = bad;
+                    flag_tile[flagged++] = t;
+                }
             }
-            tmem_st32(col_p, pw);
-            tmem_wait_st();
-            tcgen_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_full[w]);
         }
         if (mine > 0) {
-            if (!wait_bar(s, &s.pv_done[w], pvk)) return;
-            ++pvk;
+            if (mine >= 2 && !wait_bar(s, &s.pv_done[w], done + mine - 2)) return;
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.p_last[w]);
+            if (!wait_bar(s, &s.pv_done[w], done + mine - 1)) return;
             tcgen_fence_after();
+            done += mine;
         }
         base += n;
         const bool merging = !g.two && n > 1;   // both warpgroups hold a part of the rows
         if (merging && w == 1) {
             // O stays in tensor memory: the lanes are the same rows in both warpgroups
-            s.ml[0][tid] = m;
-            s.ml[1][tid] = l;
+            s.ml()[tid] = m;
+            s.ml()[kWgRows + tid] = l;
         }
         float f0 = 1.f, f1 = 0.f;
         if (merging) {
@@ -1076,7 +1075,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (!wait_bar(s, &s.merge_full, merges)) return;
             ++merges;
             tcgen_fence_after();
-            const float m1 = s.ml[0][tid], l1 = s.ml[1][tid];
+            const float m1 = s.ml()[tid], l1 = s.ml()[kWgRows + tid];
             const float M = fmaxf(m, m1);
             f0 = m == -INFINITY ? 0.f : ex2(m - M);
             f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
@@ -1164,17 +1163,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
             mbar_init(&s.raw_full[i], 1);
             mbar_init(&s.raw_empty[i], 4);
         }
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&s.kv_full[i], 4);
-            mbar_init(&s.kv_empty[i], 2);
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(&s.k_full[i], 4);
+            mbar_init(&s.k_empty[i], 2);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&s.v_full[i], 4);
+            mbar_init(&s.v_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_ready[i], 4);
-            mbar_init(&s.turn[i], 4);
             mbar_init(&s.drain[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 4);
-            mbar_init(&s.s_free[i], 4);
+            mbar_init(&s.s_taken[i], 4);
+            mbar_init(&s.p_last[i], 4);
             mbar_init(&s.pv_done[i], 1);
         }
         mbar_init(&s.merge_full, 4);

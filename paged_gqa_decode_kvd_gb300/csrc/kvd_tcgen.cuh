@@ -103,35 +103,32 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
 __host__ __device__ constexpr uint32_t mma_desc_bf16(int m, int n) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n / 8) << 17) | (static_cast<uint32_t>(m / 16) << 24);
 }
-// One thread of a converged warp: 1 there, 0 elsewhere.
-__device__ __forceinline__ uint32_t elect_one() {
+// One thread of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p;
+    return p != 0;
 }
 // The value lane 0 has: equal in every lane already, and known to the compiler as such, so that it can
 // stand in a uniform register.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(kFull, x, 0); }
-// D[128][N] (+)= A[128][16] (tensor memory) · B[N][16]^T (shared memory).  The whole warp runs it with
-// uniform operands, the elected thread issues: 32 to 64 cycles per instruction (its execution), where a
-// single thread under a branch took 100 (operands moved to uniform registers one by one).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add, uint32_t elected) {
+// D[128][N] (+)= A[128][16] · B[N][16]^T (B in shared memory), by one thread: inside `if (elect_one())` of a
+// converged warp with uniform operands an instruction issues in its execution time (32 cycles for N = 64);
+// under a branch on the thread's index it takes 100, since the operands may then differ from lane to lane.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t add) {   // A: tensor memory
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "setp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(elected)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"(add)
         : "memory");
 }
-// The same with A in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add, uint32_t elected) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {   // A: shared memory
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "setp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(elected)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"(add)
         : "memory");
 }
 // Whether the phase of the given parity has completed, without waiting.
@@ -146,7 +143,7 @@ __device__ __forceinline__ uint32_t mbar_try_now(uint64_t* bar, uint32_t parity)
         : "memory");
     return ok;
 }
-// Arrive on bar once every MMA this thread issued so far has completed (the elected thread).
+// Arrive on bar once every MMA this thread issued so far has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
