@@ -50,9 +50,9 @@ namespace chunk {
 constexpr int kTile = 64;              // positions per tile: four blocks
 constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
-constexpr int kThreads = 512;          // softmax 2 × 128, repack 128, producer 32, MMA 2 × 32, one warp idle
-constexpr int kRepackWarp = 8, kProducerWarp = 12, kMmaWarp = 13;
-constexpr int kKStages = 2, kVStages = 3;   // operand stages, 16 KiB each
+constexpr int kThreads = 512;          // softmax 2 × 128, repack 128, producer 32, S 2 × 32, O 32
+constexpr int kRepackWarp = 8, kProducerWarp = 12, kScoreWarp = 13, kOutWarp = 15;
+constexpr int kKStages = 2, kVStages = 2;   // operand stages, 16 KiB each
 constexpr int kInfos = 4;              // tiles whose masks and factors are kept
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
@@ -62,13 +62,20 @@ constexpr int kColS = 0, kColP = 128, kColO = 256;   // tensor memory columns: S
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
-constexpr int raw_stages(int kind) { return kind == kKindBf16 ? 5 : kind == kKindMixed ? 4 : 8; }   // two records each
-constexpr int max_record(int kind) {
-    return kind == kKindBf16 || kind == kKindMixed ? kRecordBf16
-           : kind == kKindInt4                     ? lowbit_record_bytes(4, 4)
-           : kind == kKindInt2                     ? lowbit_record_bytes(2, 4)
-                                                   : kRecordFp8;
+// Bytes of a record's parts.  A raw slot holds four blocks' K: codes, then the 8-bit record's scales or the
+// low-bit record's K words; or their V: codes, then the low-bit record's V words.
+constexpr int code_bytes(int kind) {
+    return kind == kKindBf16 || kind == kKindMixed ? kTileBf16
+           : kind == kKindInt4                     ? lowbit_tile_bytes(4)
+           : kind == kKindInt2                     ? lowbit_tile_bytes(2)
+                                                   : kTileFp8;
 }
+constexpr int k_slot(int kind) {
+    return kind == kKindBf16 || kind == kKindMixed ? kTileBf16 : code_bytes(kind) + (is_lowbit(kind) ? lowbit_meta_bytes(4) : kScaleBytes);
+}
+constexpr int v_slot(int kind) { return code_bytes(kind) + (is_lowbit(kind) ? lowbit_meta_bytes(4) : 0); }
+constexpr int raw_k_tiles(int kind) { return kind == kKindBf16 || kind == kKindMixed ? 3 : 4; }
+constexpr int raw_v_tiles(int kind) { return kind == kKindBf16 ? 3 : kind == kKindMixed ? 2 : 4; }
 
 struct TileInfo {
     unsigned long long mask;        // bit 16·block + t: position may be attended
@@ -79,14 +86,14 @@ template <int KIND>
 struct Smem {
     uint8_t k[kKStages][kOpBytes], v[kVStages][kOpBytes];       // operands; 1,024-byte aligned
     uint8_t q[2][2 * kOpBytes];                                 // 128 rows each
-    uint8_t raw[raw_stages(KIND)][2][max_record(KIND)];
+    uint8_t raw_k[raw_k_tiles(KIND)][4][k_slot(KIND)], raw_v[raw_v_tiles(KIND)][4][v_slot(KIND)];
     float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
     TileInfo info[kInfos];
-    uint32_t meta[raw_stages(KIND)][2];                         // block words
-    uint64_t raw_full[raw_stages(KIND)], raw_empty[raw_stages(KIND)];
+    uint32_t word_k[raw_k_tiles(KIND)][4], word_v[raw_v_tiles(KIND)][4];   // block words
+    uint64_t rk_full[raw_k_tiles(KIND)], rk_empty[raw_k_tiles(KIND)], rv_full[raw_v_tiles(KIND)], rv_empty[raw_v_tiles(KIND)];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t s_full[2], s_taken[2], p_last[2], pv_done[2];
-    uint64_t q_ready[2], merge_full, merge_empty, drain[2];
+    uint64_t s_full[2], s_taken[2], p_full[2][2], pv_done[2][2];
+    uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
     int64_t remaining;
     int b, h, qt, off;
     uint32_t tmem;
@@ -281,86 +288,89 @@ __device__ __forceinline__ void put_k(uint8_t* op, int n, int j, int x, uint32_t
 __device__ __forceinline__ uint32_t pair_mask(uint32_t m, int t) {
     return ((m >> t & 1u) ? 0xffffu : 0u) | ((m >> (t + 1) & 1u) ? 0xffff0000u : 0u);
 }
+// Whether a pair of bf16 has an infinity or a NaN (in the top bits of its halves).
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
+// V words of a lane, one dim: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p and 2p+1; masked tokens are zeroed
+// and, where rows of the unit differ in which they attend, non-finite elements zeroed and noted.
 struct VPut {
     uint8_t* op;
+    uint32_t keep[4];          // the lane's valid bits, by word
     unsigned long long bad;    // columns with non-finite elements
+    bool whole;                // every position of the tile is valid
     bool look;                 // the tile holds positions some rows attend and others do not
-    // Tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p and 2p+1, dim d; valid bits of the two blocks.
-    __device__ __forceinline__ void put(int d, int p, int x, uint32_t a, uint32_t b, uint32_t c, uint32_t e, uint32_t m0,
-                                        uint32_t m1) {
-        if ((m0 & m1) != 0xffffu) {
-            a &= pair_mask(m0, 2 * x);
-            b &= pair_mask(m0, 2 * x + 8);
-            c &= pair_mask(m1, 2 * x);
-            e &= pair_mask(m1, 2 * x + 8);
-        }
+    __device__ __forceinline__ VPut(uint8_t* o, const uint32_t (&word)[4], bool l, int lane) : op(o), bad(0), look(l) {
+        whole = (word[0] & word[1] & word[2] & word[3] & 0xffffu) == 0xffffu;
+        const int x = lane & 3;
+        const uint32_t m0 = (lane & 4) ? word[2] : word[0], m1 = (lane & 4) ? word[3] : word[1];
+        keep[0] = pair_mask(m0, 2 * x);
+        keep[1] = pair_mask(m0, 2 * x + 8);
+        keep[2] = pair_mask(m1, 2 * x);
+        keep[3] = pair_mask(m1, 2 * x + 8);
+    }
+    // Dim d, columns 32p + 8x + 0 .. 7, element by element.
+    __device__ __forceinline__ void put(int d, int lane, uint32_t a, uint32_t b, uint32_t c, uint32_t e) {
+        const int x = lane & 3, p = (lane >> 2) & 1;
+        uint32_t w[4] = {a & keep[0], b & keep[1], c & keep[2], e & keep[3]};
         if (look) {
-            uint32_t w[4] = {a, b, c, e};
             #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if ((w[i] >> (16 * k) & 0x7f80u) == 0x7f80u) {
-                        bad |= 1ull << (32 * p + 8 * x + 2 * i + k);
-                        w[i] &= k ? 0x0000ffffu : 0xffff0000u;
-                    }
-                }
+                const uint32_t n = nonfinite(w[i]);
+                if (n & 0x8000u) bad |= 1ull << (32 * p + 8 * x + 2 * i);
+                if (n & 0x80000000u) bad |= 2ull << (32 * p + 8 * x + 2 * i);
+                w[i] &= ~((n & 0x8000u ? 0xffffu : 0u) | (n & 0x80000000u ? 0xffff0000u : 0u));
             }
-            a = w[0];
-            b = w[1];
-            c = w[2];
-            e = w[3];
         }
-        put16(op, d, 4 * p + x, a, b, c, e);
+        put16(op, d, 4 * p + x, w[0], w[1], w[2], w[3]);
     }
 };
 
-// Four 8-bit codes -> two packed bf16 pairs, exact.  An E4M3 (E5M2) code is moved into a bf16's sign,
-// exponent and mantissa bits and scaled by 2^120 (2^112), the difference of the exponent biases;
-// codes with the top exponent pattern that are not numbers go through the conversion instruction.
+// Four 8-bit codes -> two packed bf16 pairs, exact for numbers.  An E4M3 (E5M2) code is moved into a bf16's
+// sign, exponent and mantissa bits and scaled by 2^120 (2^112), the difference of the exponent biases.
+// `special` collects codes that are no numbers: those go through the conversion instruction (any_code_to_bf16).
 template <int FMT>
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi, uint32_t& special) {
     constexpr uint32_t kBits = FMT == kFmtE5m2 ? 0x0fe00fe0u : 0x07f007f0u;
     constexpr int kShift = FMT == kFmtE5m2 ? 3 : 4;
     constexpr uint32_t kUp = FMT == kFmtE5m2 ? 0x77807780u : 0x7b807b80u;
-    const uint32_t special = FMT == kFmtE5m2 ? ((w & 0x7c7c7c7cu) + 0x04040404u) & 0x80808080u
-                                             : ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    if (special) {
-        uint32_t a, b;
-        f8x4_to_f16x2x2<FMT>(w, a, b);
-        const float2 x = unpack_f16(a), y = unpack_f16(b);
-        lo = pack_bf16(x.x, x.y);
-        hi = pack_bf16(y.x, y.y);
-        return;
-    }
+    special |= FMT == kFmtE5m2 ? (w & 0x7c7c7c7cu) + 0x04040404u : (w & 0x7f7f7f7fu) + 0x01010101u;
     const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
     uint32_t pa = ((a >> kShift) & kBits) | (a & 0x80008000u), pb = ((b >> kShift) & kBits) | (b & 0x80008000u);
-    const __nv_bfloat162 up = *reinterpret_cast<const __nv_bfloat162*>(&kUp);
-    __nv_bfloat162 ra = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&pa), up);
-    __nv_bfloat162 rb = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&pb), up);
+    const uint32_t up = kUp;
+    const __nv_bfloat162 u = *reinterpret_cast<const __nv_bfloat162*>(&up);
+    __nv_bfloat162 ra = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&pa), u);
+    __nv_bfloat162 rb = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&pb), u);
     lo = *reinterpret_cast<uint32_t*>(&ra);
     hi = *reinterpret_cast<uint32_t*>(&rb);
 }
+template <int FMT>
+__device__ __forceinline__ void any_code_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    uint32_t a, b;
+    f8x4_to_f16x2x2<FMT>(w, a, b);
+    const float2 x = unpack_f16(a), y = unpack_f16(b);
+    lo = pack_bf16(x.x, x.y);
+    hi = pack_bf16(y.x, y.y);
+}
 
-// A lane's byte offsets, the same for every tile; [q] for the even and the odd pieces.  K: the warp's block;
-// lanes of an eight read one 64-byte half each and write all eight pieces of two rows' 128-byte lines.  V: the
-// warp's 32 dims of all four blocks, likewise.  Neither side has bank conflicts.
+// A lane's byte offsets, the same for every tile; [q] for the even and the odd pieces.  K: the warp's block; V: the
+// warp's 32 dims of all four blocks.  Lanes of an eight read one 64-byte half each and write all eight pieces of
+// two rows' 128-byte lines, so neither side has bank conflicts.
 struct Offsets {
-    int k_ld[2][2], k_st[2][2];   // [8-bit record][q], [q][token t, t + 8]
-    int v_ld[2][2], v_st[2];      // [8-bit record][q], [q]
+    int k_ld[2], k_st[2][2];   // [q] (16-bit records: twice the part before the + of the 8-bit ones), [q][token t, t + 8]
+    int v_ld[2], v_st[2];
+    int k_half, v_warp;        // the parts that differ between 16- and 8-bit records
     __device__ __forceinline__ Offsets(int warp, int lane) {
         const int x = lane & 3, h = (lane >> 2) & 1, l = lane >> 3;
+        k_half = h * 512;
+        v_warp = warp * 512;
         #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int t = 2 * l + (q ^ h);   // K: token (mod 8); V: dim (mod 8)
             const int n = column_of(warp, t);
-            k_ld[0][q] = h * 1024 + (4 * t + x) * 16;
-            k_ld[1][q] = h * 512 + (4 * t + x) * 16;
+            k_ld[q] = (4 * t + x) * 16;
             k_st[q][0] = n * 128 + (((4 * h + x) ^ (n & 7)) << 4);
             k_st[q][1] = (n + 2) * 128 + (((4 * h + x) ^ ((n + 2) & 7)) << 4);
-            v_ld[0][q] = kTileBf16 + warp * 1024 + (4 * t + x) * 16;
-            v_ld[1][q] = kTileFp8 + warp * 512 + (4 * t + x) * 16;
+            v_ld[q] = (4 * t + x) * 16;
             v_st[q] = warp * 4096 + t * 128 + (((4 * h + x) ^ t) << 4);
         }
     }
@@ -371,14 +381,15 @@ __device__ __forceinline__ void st16(uint8_t* p, uint32_t a, uint32_t b, uint32_
     *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
 }
 
+// K of one block (codes) by one warp, every load before the stores.
 template <int FMT>
-__device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, const Offsets& o) {
+__device__ __forceinline__ void repack_k(const uint8_t* code, uint8_t* op, const Offsets& o) {
     if constexpr (FMT == kFmtBf16) {
         uint4 a[4], b[4];
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            a[i] = ld16(rec + o.k_ld[0][i & 1] + (i >> 1) * 2048);
-            b[i] = ld16(rec + o.k_ld[0][i & 1] + (i >> 1) * 2048 + 512);
+            a[i] = ld16(code + 2 * o.k_half + o.k_ld[i & 1] + (i >> 1) * 2048);
+            b[i] = ld16(code + 2 * o.k_half + o.k_ld[i & 1] + (i >> 1) * 2048 + 512);
         }
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -387,17 +398,32 @@ __device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, const 
         }
     } else {
         uint4 a[4];
+        uint32_t special = 0;
         #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = ld16(rec + o.k_ld[1][i & 1] + (i >> 1) * 1024);
+        for (int i = 0; i < 4; ++i) a[i] = ld16(code + o.k_half + o.k_ld[i & 1] + (i >> 1) * 1024);
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t lo[4], hi[4];
-            codes_to_bf16<FMT>(a[i].x, lo[0], hi[0]);
-            codes_to_bf16<FMT>(a[i].y, lo[1], hi[1]);
-            codes_to_bf16<FMT>(a[i].z, lo[2], hi[2]);
-            codes_to_bf16<FMT>(a[i].w, lo[3], hi[3]);
+            codes_to_bf16<FMT>(a[i].x, lo[0], hi[0], special);
+            codes_to_bf16<FMT>(a[i].y, lo[1], hi[1], special);
+            codes_to_bf16<FMT>(a[i].z, lo[2], hi[2], special);
+            codes_to_bf16<FMT>(a[i].w, lo[3], hi[3], special);
             st16(op + o.k_st[i & 1][0] + (i >> 1) * 8192, lo[0], lo[1], lo[2], lo[3]);
             st16(op + o.k_st[i & 1][1] + (i >> 1) * 8192, hi[0], hi[1], hi[2], hi[3]);
+        }
+        if (special & 0x80808080u) {   // rare
+            #pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const uint4 c = ld16(code + o.k_half + o.k_ld[0] + (i & 1) * (o.k_ld[1] - o.k_ld[0]) + (i >> 1) * 1024);
+                const int s0 = i & 1 ? o.k_st[1][0] : o.k_st[0][0], s1 = i & 1 ? o.k_st[1][1] : o.k_st[0][1];
+                uint32_t lo[4], hi[4];
+                any_code_to_bf16<FMT>(c.x, lo[0], hi[0]);
+                any_code_to_bf16<FMT>(c.y, lo[1], hi[1]);
+                any_code_to_bf16<FMT>(c.z, lo[2], hi[2]);
+                any_code_to_bf16<FMT>(c.w, lo[3], hi[3]);
+                st16(op + s0 + (i >> 1) * 8192, lo[0], lo[1], lo[2], lo[3]);
+                st16(op + s1 + (i >> 1) * 8192, hi[0], hi[1], hi[2], hi[3]);
+            }
         }
     }
 }
@@ -405,82 +431,99 @@ __device__ __forceinline__ void repack_k(const uint8_t* rec, uint8_t* op, const 
 // A V piece of two dims as bf16: group i (dims 16i + r and 16i + r + 8), lane 4r + x: tokens
 // (2x, 2x+1) of dim r, of dim r + 8, tokens (2x+8, 2x+9) of dim r, of dim r + 8.
 template <int FMT>
-__device__ __forceinline__ uint4 v_piece(const uint8_t* rec, int i, int l) {
+__device__ __forceinline__ uint4 v_piece(const uint8_t* code, int i, int l) {
     if constexpr (FMT == kFmtBf16) {
-        return *reinterpret_cast<const uint4*>(rec + kTileBf16 + (i * 32 + l) * 16);
+        return ld16(code + (i * 32 + l) * 16);
     } else {
-        const uint2 a = *reinterpret_cast<const uint2*>(rec + kTileFp8 + ((i >> 1) * 32 + l) * 16 + (i & 1) * 8);
+        const uint2 a = *reinterpret_cast<const uint2*>(code + ((i >> 1) * 32 + l) * 16 + (i & 1) * 8);
         uint4 o;
-        codes_to_bf16<FMT>(a.x, o.x, o.y);
-        codes_to_bf16<FMT>(a.y, o.z, o.w);
+        any_code_to_bf16<FMT>(a.x, o.x, o.y);
+        any_code_to_bf16<FMT>(a.y, o.z, o.w);
         return o;
     }
 }
-
 template <int KIND>
-__device__ __forceinline__ uint4 v_piece_kind(const uint8_t* rec, uint32_t word, int i, int l) {
+__device__ __forceinline__ uint4 v_piece_kind(const uint8_t* code, uint32_t word, int i, int l) {
     if constexpr (KIND == kKindBf16) {
-        return v_piece<kFmtBf16>(rec, i, l);
+        return v_piece<kFmtBf16>(code, i, l);
     } else if constexpr (KIND == kKindMixed) {
         const int f = (word >> 17) & 3u;
-        return f == kFmtBf16 ? v_piece<kFmtBf16>(rec, i, l)
-               : f == kFmtE4m3 ? v_piece<kFmtE4m3>(rec, i, l) : v_piece<kFmtE5m2>(rec, i, l);
+        return f == kFmtBf16 ? v_piece<kFmtBf16>(code, i, l)
+               : f == kFmtE4m3 ? v_piece<kFmtE4m3>(code, i, l) : v_piece<kFmtE5m2>(code, i, l);
     } else {
-        return v_piece<kFmtE4m3>(rec, i, l);
+        return v_piece<kFmtE4m3>(code, i, l);
     }
 }
-// pair: the lane's two records.
-template <int KIND>
-__device__ __forceinline__ void repack_v(const uint8_t* r0, const uint32_t (&word)[4], VPut& out, const Offsets& o, int warp,
-                                         int lane) {
-    constexpr int kRec = max_record(KIND);
-    const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
-    if (KIND != kKindMixed && !out.look && (word[0] & word[1] & word[2] & word[3] & 0xffffu) == 0xffffu) {
-        // the usual tile: every position attended by every row
-        if constexpr (KIND == kKindBf16) {
-            uint4 a[4], b[4];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = ld16(r0 + o.v_ld[0][i & 1] + (i >> 1) * 512);
-                b[i] = ld16(r0 + o.v_ld[0][i & 1] + (i >> 1) * 512 + kRec);
-            }
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint8_t* to = out.op + o.v_st[i & 1] + (i >> 1) * 2048;
-                st16(to, a[i].x, a[i].z, b[i].x, b[i].z);
-                st16(to + 1024, a[i].y, a[i].w, b[i].y, b[i].w);
-            }
-        } else {
-            uint4 a[2], b[2];
-            #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                a[q] = ld16(r0 + o.v_ld[1][q]);
-                b[q] = ld16(r0 + o.v_ld[1][q] + kRec);
-            }
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int q = i & 1;
-                uint32_t lo[4], hi[4];
-                codes_to_bf16<kFmtE4m3>(i >> 1 ? a[q].z : a[q].x, lo[0], hi[0]);
-                codes_to_bf16<kFmtE4m3>(i >> 1 ? a[q].w : a[q].y, lo[1], hi[1]);
-                codes_to_bf16<kFmtE4m3>(i >> 1 ? b[q].z : b[q].x, lo[2], hi[2]);
-                codes_to_bf16<kFmtE4m3>(i >> 1 ? b[q].w : b[q].y, lo[3], hi[3]);
-                uint8_t* to = out.op + o.v_st[q] + (i >> 1) * 2048;
-                st16(to, lo[0], lo[1], lo[2], lo[3]);
-                st16(to + 1024, hi[0], hi[1], hi[2], hi[3]);
-            }
+
+// V of the tile, 32 dims by one warp; pair: the lane's two blocks' codes.  MASK: some position is not valid; LOOK:
+// non-finite elements matter.  Returns whether the lane met something that wants the element-wise path.
+template <int KIND, bool MASK, bool LOOK>
+__device__ __forceinline__ bool repack_v_fast(const uint8_t* pair, const VPut& out, const Offsets& o) {
+    constexpr int kNext = v_slot(KIND);
+    uint32_t odd = 0, special = 0;
+    auto put = [&](uint8_t* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        if constexpr (MASK) {
+            a &= out.keep[0];
+            b &= out.keep[1];
+            c &= out.keep[2];
+            d &= out.keep[3];
         }
-        return;
+        if constexpr (LOOK) odd |= nonfinite(a) | nonfinite(b) | nonfinite(c) | nonfinite(d);
+        st16(to, a, b, c, d);
+    };
+    if constexpr (KIND == kKindBf16) {
+        uint4 a[4], b[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = ld16(pair + 2 * o.v_warp + o.v_ld[i & 1] + (i >> 1) * 512);
+            b[i] = ld16(pair + 2 * o.v_warp + o.v_ld[i & 1] + (i >> 1) * 512 + kNext);
+        }
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint8_t* to = out.op + o.v_st[i & 1] + (i >> 1) * 2048;
+            put(to, a[i].x, a[i].z, b[i].x, b[i].z);
+            put(to + 1024, a[i].y, a[i].w, b[i].y, b[i].w);
+        }
+    } else {
+        uint4 a[2], b[2];
+        #pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            a[q] = ld16(pair + o.v_warp + o.v_ld[q]);
+            b[q] = ld16(pair + o.v_warp + o.v_ld[q] + kNext);
+        }
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int q = i & 1;
+            uint32_t lo[4], hi[4];
+            codes_to_bf16<kFmtE4m3>(i >> 1 ? a[q].z : a[q].x, lo[0], hi[0], special);
+            codes_to_bf16<kFmtE4m3>(i >> 1 ? a[q].w : a[q].y, lo[1], hi[1], special);
+            codes_to_bf16<kFmtE4m3>(i >> 1 ? b[q].z : b[q].x, lo[2], hi[2], special);
+            codes_to_bf16<kFmtE4m3>(i >> 1 ? b[q].w : b[q].y, lo[3], hi[3], special);
+            uint8_t* to = out.op + o.v_st[q] + (i >> 1) * 2048;
+            put(to, lo[0], lo[1], lo[2], lo[3]);
+            put(to + 1024, hi[0], hi[1], hi[2], hi[3]);
+        }
     }
-    const uint32_t w0 = word[2 * p], w1 = word[2 * p + 1];
-    const uint32_t m0 = w0 & 0xffffu, m1 = w1 & 0xffffu;
+    return odd != 0 || (special & 0x80808080u) != 0;
+}
+template <int KIND>
+__device__ __forceinline__ void repack_v(const uint8_t* pair, const uint32_t (&word)[4], VPut& out, const Offsets& o, int warp,
+                                         int lane) {
+    if constexpr (KIND != kKindMixed) {
+        bool slow;
+        if (out.look) slow = repack_v_fast<KIND, true, true>(pair, out, o);
+        else if (!out.whole) slow = repack_v_fast<KIND, true, false>(pair, out, o);
+        else slow = repack_v_fast<KIND, false, false>(pair, out, o);
+        if (!__any_sync(kFull, slow)) return;
+    }
+    const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
     #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
         const int group = 2 * warp + (i >> 1), r = 2 * rl + ((i & 1) ^ p);
-        const uint4 a = v_piece_kind<KIND>(r0, w0, group, 4 * r + x);
-        const uint4 b = v_piece_kind<KIND>(r0 + kRec, w1, group, 4 * r + x);
-        out.put(16 * group + r, p, x, a.x, a.z, b.x, b.z, m0, m1);
-        out.put(16 * group + r + 8, p, x, a.y, a.w, b.y, b.w, m0, m1);
+        const uint4 a = v_piece_kind<KIND>(pair, word[2 * p], group, 4 * r + x);
+        const uint4 b = v_piece_kind<KIND>(pair + v_slot(KIND), word[2 * p + 1], group, 4 * r + x);
+        out.put(16 * group + r, lane, a.x, a.z, b.x, b.z);
+        out.put(16 * group + r + 8, lane, a.y, a.w, b.y, b.w);
     }
 }
 
@@ -493,7 +536,7 @@ __device__ __forceinline__ uint32_t low_pair(uint32_t word, int h, int j, float2
 template <int BITS>
 __device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, int k, int ng, int lane) {
     constexpr int kPer = 8 / BITS, kTileB = lowbit_tile_bytes(BITS);
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + 2 * kTileB);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + kTileB);
     const int x = lane & 3, r = lane >> 2;
     const int n = column_of(k, r);
     #pragma unroll
@@ -512,8 +555,7 @@ __device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, in
     }
 }
 template <int KIND, int BITS>
-__device__ __forceinline__ void repack_v_low(const uint8_t* pair, const uint32_t (&word)[4], VPut& out,
-                                             int ng, int warp, int lane) {
+__device__ __forceinline__ void repack_v_low(const uint8_t* pair, VPut& out, int ng, int warp, int lane) {
     constexpr int kPer = 8 / BITS, kTileB = lowbit_tile_bytes(BITS);
     const int x = lane & 3, p = (lane >> 2) & 1, rl = lane >> 3;
     #pragma unroll 1
@@ -525,21 +567,20 @@ __device__ __forceinline__ void repack_v_low(const uint8_t* pair, const uint32_t
             uint32_t o[2][4];   // dims r, r + 8: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p, 2p+1
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint8_t* b = pair + u * max_record(KIND);
-                const uint32_t* meta = reinterpret_cast<const uint32_t*>(b + 2 * kTileB) + kBs * ng;
+                const uint8_t* b = pair + u * v_slot(KIND);
+                const uint32_t* meta = reinterpret_cast<const uint32_t*>(b + kTileB);
                 const int gi = group * ng / 8;
                 #pragma unroll
                 for (int th = 0; th < 2; ++th) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(b + kTileB + lowbit_word(kg, 4 * r + x, th) * 4);
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(b + lowbit_word(kg, 4 * r + x, th) * 4);
                     const int t = 2 * x + 8 * th;
                     const float2 s0 = unpack_f16(meta[t * ng + gi]), s1 = unpack_f16(meta[(t + 1) * ng + gi]);
                     o[0][2 * u + th] = low_pair<BITS>(w, h, 0, s0, s1);
                     o[1][2 * u + th] = low_pair<BITS>(w, h, 2, s0, s1);
                 }
             }
-            const uint32_t m0 = word[2 * p] & 0xffffu, m1 = word[2 * p + 1] & 0xffffu;
-            out.put(16 * group + r, p, x, o[0][0], o[0][1], o[0][2], o[0][3], m0, m1);
-            out.put(16 * group + r + 8, p, x, o[1][0], o[1][1], o[1][2], o[1][3], m0, m1);
+            out.put(16 * group + r, lane, o[0][0], o[0][1], o[0][2], o[0][3]);
+            out.put(16 * group + r + 8, lane, o[1][0], o[1][1], o[1][2], o[1][3]);
         }
     }
 }
@@ -623,12 +664,34 @@ __device__ __forceinline__ bool wait_three(Smem<KIND>& s, uint64_t* a, uint32_t 
     return false;
 }
 
+// One block's K (or V) part into its raw slot.  Returns the bytes that will be counted on the barrier.
+template <int KIND>
+__device__ __forceinline__ uint32_t part_bytes(const ChunkParams& p, uint32_t word, bool value) {
+    if (!word) return 0;
+    const bool wide = KIND == kKindBf16 || (KIND == kKindMixed && ((word >> 17) & 3u) == kFmtBf16);
+    if (is_lowbit(KIND)) return code_bytes(KIND) + kBs * p.ng * 4;
+    return wide ? kTileBf16 : value ? kTileFp8 : kTileFp8 + kScaleBytes;
+}
+// copy(destination, source, bytes) of the part's one or two pieces.
+template <int KIND, class F>
+__device__ __forceinline__ void part_pieces(const ChunkParams& p, uint32_t word, bool value, uint8_t* slot, const uint8_t* rec, F copy) {
+    constexpr int kCode = is_lowbit(KIND) ? code_bytes(KIND) : kTileFp8;
+    const bool wide = KIND == kKindBf16 || (KIND == kKindMixed && ((word >> 17) & 3u) == kFmtBf16);
+    if (wide) {
+        copy(slot, rec + (value ? kTileBf16 : 0), kTileBf16);
+        return;
+    }
+    copy(slot, rec + (value ? kCode : 0), kCode);
+    if (is_lowbit(KIND)) copy(slot + kCode, rec + 2 * kCode + (value ? kBs * p.ng * 4 : 0), kBs * p.ng * 4);
+    else if (!value) copy(slot + kCode, rec + 2 * kCode, kScaleBytes);
+}
+
 template <int KIND>
 __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, int lane) {
-    constexpr int kRaw = raw_stages(KIND);
+    constexpr int kRk = raw_k_tiles(KIND), kRv = raw_v_tiles(KIND);
     Walk walk(p, s);
     Segment g;
-    uint32_t k = 0;   // pairs of blocks so far: two a tile
+    uint32_t k = 0, issued[2] = {0, 0};   // tiles whose K and whose V are under way
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const int32_t* row = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks;
@@ -643,81 +706,120 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
                 if (word) rec = record_at(p, phys, g.h);
                 host = word && p.host_direct && phys >= p.num_blocks;
             }
-            uint32_t bytes = 0;
-            if (word && !host)
-                bytes = KIND == kKindMixed && ((word >> 17) & 3u) != kFmtBf16 ? kRecordFp8 : static_cast<uint32_t>(p.record_bytes);
-            const uint32_t both = bytes + __shfl_xor_sync(kFull, bytes, 1);
-            const int n = 2 * min(8, g.t1 - tb);
-            for (int i = 0; i < n; ++i, ++k) {
-                const int st = k % kRaw;
-                ok = wait_bar(s, &s.raw_empty[st], (k / kRaw) + 1);
-                if (!ok) break;
-                const bool mine = (lane >> 1) == i;
-                if (mine) s.meta[st][lane & 1] = word;
-                if (p.host_direct) {   // records in host memory: copied by the load path, the whole warp
-                    unsigned hosts = __ballot_sync(kFull, mine && host);
-                    fence_proxy_async_shared();
-                    while (hosts) {
-                        const int l = __ffs(hosts) - 1;
-                        hosts &= hosts - 1;
-                        const uint8_t* src = reinterpret_cast<const uint8_t*>(
-                            __shfl_sync(kFull, reinterpret_cast<unsigned long long>(rec), l));
-                        for (int c = lane; c < p.record_bytes / 16; c += 32)
-                            cp_async16_g2s(s.raw[st][l & 1] + 16 * c, src + 16 * c);
+            const int n = min(8, g.t1 - tb);
+            for (int i = 0; ok && i < n; ++i, ++k) {
+                const bool mine = (lane >> 2) == i;
+                #pragma unroll 1
+                for (int value = 0; value < 2; ++value) {
+                    const uint32_t st = value ? k % kRv : k % kRk, use = value ? k / kRv : k / kRk;
+                    uint64_t* full = value ? &s.rv_full[st] : &s.rk_full[st];
+                    ok = wait_bar(s, value ? &s.rv_empty[st] : &s.rk_empty[st], use + 1);
+                    if (!ok) break;
+                    uint8_t* slot = value ? s.raw_v[st][lane & 3] : s.raw_k[st][lane & 3];
+                    if (mine) (value ? s.word_v[st] : s.word_k[st])[lane & 3] = word;
+                    uint32_t bytes = mine && !host ? part_bytes<KIND>(p, word, value) : 0;
+                    bytes += __shfl_xor_sync(kFull, bytes, 1);
+                    bytes += __shfl_xor_sync(kFull, bytes, 2);
+                    if (p.host_direct) {   // blocks in host memory: copied by the load path, the whole warp
+                        unsigned hosts = __ballot_sync(kFull, mine && host);
+                        fence_proxy_async_shared();
+                        while (hosts) {
+                            const int l = __ffs(hosts) - 1;
+                            hosts &= hosts - 1;
+                            const uint8_t* src = reinterpret_cast<const uint8_t*>(
+                                __shfl_sync(kFull, reinterpret_cast<unsigned long long>(rec), l));
+                            part_pieces<KIND>(p, __shfl_sync(kFull, word, l), value, value ? s.raw_v[st][l & 3] : s.raw_k[st][l & 3],
+                                              src, [&](uint8_t* to, const uint8_t* from, int b) {
+                                                  for (int c = lane; c < b / 16; c += 32) cp_async16_g2s(to + 16 * c, from + 16 * c);
+                                              });
+                        }
+                        cp_async_mbar_arrive(full);
                     }
-                    cp_async_mbar_arrive(&s.raw_full[st]);
+                    __syncwarp();
+                    if (lane == 4 * i) {
+                        if (bytes) mbar_arrive_expect_tx(full, bytes);
+                        else mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    if (mine && word && !host)
+                        part_pieces<KIND>(p, word, value, slot, rec,
+                                          [&](uint8_t* to, const uint8_t* from, int b) { bulk_copy(to, from, b, full); });
+                    if (value) ++issued[1];
+                    else ++issued[0];
                 }
-                __syncwarp();
-                if (lane == 2 * i) {
-                    if (both) mbar_arrive_expect_tx(&s.raw_full[st], both);
-                    else mbar_arrive(&s.raw_full[st]);
-                }
-                __syncwarp();
-                if (mine && bytes) bulk_copy(s.raw[st][lane & 1], rec, bytes, &s.raw_full[st]);
             }
         }
     }
     if (!ok) {   // the copies in flight land before the block leaves
-        const uint32_t from = k > kRaw ? k - kRaw : 0;
-        for (uint32_t i = from; i < k; ++i) mbar_wait(&s.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr, kWaitNs);
+        for (uint32_t i = issued[0] > kRk ? issued[0] - kRk : 0; i < issued[0]; ++i)
+            mbar_wait(&s.rk_full[i % kRk], (i / kRk) & 1u, nullptr, kWaitNs);
+        for (uint32_t i = issued[1] > kRv ? issued[1] - kRv : 0; i < issued[1]; ++i)
+            mbar_wait(&s.rv_full[i % kRv], (i / kRv) & 1u, nullptr, kWaitNs);
     }
+}
+
+// K of tile k, then V of tile k − 1: V is wanted a step later than K, and its stage is free later.
+template <int KIND>
+__device__ __forceinline__ bool repack_tile_v(Smem<KIND>& s, const ChunkParams& p, const Offsets& off, uint32_t k, bool look, int warp,
+                                              int lane) {
+    constexpr int kRv = raw_v_tiles(KIND);
+    const uint32_t st = k % kRv, vs = k % kVStages;
+    if (!wait_three(s, &s.rv_full[st], k / kRv, &s.v_empty[vs], (k / kVStages) + 1, &s.v_empty[vs], 0, false)) return false;
+    const uint32_t word[4] = {s.word_v[st][0], s.word_v[st][1], s.word_v[st][2], s.word_v[st][3]};
+    VPut v(s.v[vs], word, look, lane);
+    const uint8_t* pair = s.raw_v[st][(lane & 4) >> 1];   // lanes take the pair of blocks of their columns
+    if constexpr (is_lowbit(KIND)) repack_v_low<KIND, KIND == kKindInt4 ? 4 : 2>(pair, v, p.ng, warp, lane);
+    else repack_v<KIND>(pair, word, v, off, warp, lane);
+    fence_proxy_async_shared();
+    if (look) {
+        const uint32_t lo = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad));
+        const uint32_t hi = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad >> 32));
+        v.bad = static_cast<unsigned long long>(hi) << 32 | lo;
+    }
+    __syncwarp();
+    if (lane == 0) {
+        s.info[k % kInfos].nonfin[warp] = v.bad;
+        mbar_arrive(&s.v_full[vs]);
+        mbar_arrive(&s.rv_empty[st]);
+    }
+    return true;
 }
 
 template <int KIND>
 __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
-    constexpr int kRaw = raw_stages(KIND);
+    constexpr int kRk = raw_k_tiles(KIND);
     const Offsets off(warp, lane);
     Walk walk(p, s);
     Segment g;
     uint32_t k = 0;
-    while (walk.next(p, g)) {
-        for (int t = g.t0; t < g.t1; ++t, ++k) {
-            const int r0 = (2 * k) % kRaw, r1 = (2 * k + 1) % kRaw;   // the tile's pairs of blocks
-            const int ks = k % kKStages, vs = k % kVStages, in = k % kInfos;
-            if (!wait_bar(s, &s.raw_full[r0], 2 * k / kRaw) || !wait_bar(s, &s.raw_full[r1], (2 * k + 1) / kRaw) ||
-                !wait_bar(s, &s.k_empty[ks], (k / kKStages) + 1))
-                return;
-            const uint32_t word[4] = {s.meta[r0][0], s.meta[r0][1], s.meta[r1][0], s.meta[r1][1]};
-            const uint32_t mine = warp < 2 ? (warp & 1 ? word[1] : word[0]) : (warp & 1 ? word[3] : word[2]);
-            const bool look = t * kTile + kTile - 1 > g.first;
+    bool before = false;   // the tile before: rows differ in what they attend of it
+    bool more = walk.next(p, g);
+    int t = more ? g.t0 : 0;
+    while (true) {
+        bool look = false;
+        if (more) {
+            const uint32_t st = k % kRk, ks = k % kKStages, in = k % kInfos;
+            if (!wait_three(s, &s.rk_full[st], k / kRk, &s.k_empty[ks], (k / kKStages) + 1, &s.k_empty[ks], 0, false)) return;
+            const uint32_t mine = s.word_k[st][warp];
+            look = t * kTile + kTile - 1 > g.first;
             if (warp == 0 && lane == 0)
-                s.info[in].mask = static_cast<unsigned long long>(word[0] & 0xffffu) |
-                                  static_cast<unsigned long long>(word[1] & 0xffffu) << 16 |
-                                  static_cast<unsigned long long>(word[2] & 0xffffu) << 32 |
-                                  static_cast<unsigned long long>(word[3] & 0xffffu) << 48;
-            const uint8_t* rec = s.raw[warp < 2 ? r0 : r1][warp & 1];   // this warp's block
+                s.info[in].mask = static_cast<unsigned long long>(s.word_k[st][0] & 0xffffu) |
+                                  static_cast<unsigned long long>(s.word_k[st][1] & 0xffffu) << 16 |
+                                  static_cast<unsigned long long>(s.word_k[st][2] & 0xffffu) << 32 |
+                                  static_cast<unsigned long long>(s.word_k[st][3] & 0xffffu) << 48;
+            const uint8_t* code = s.raw_k[st][warp];   // this warp's block
             if constexpr (KIND == kKindBf16) {
-                repack_k<kFmtBf16>(rec, s.k[ks], off);
+                repack_k<kFmtBf16>(code, s.k[ks], off);
             } else if constexpr (is_lowbit(KIND)) {
-                repack_k_low<KIND == kKindInt4 ? 4 : 2>(rec, s.k[ks], warp, p.ng, lane);
+                repack_k_low<KIND == kKindInt4 ? 4 : 2>(code, s.k[ks], warp, p.ng, lane);
             } else {
                 int f = kFmtE4m3;
                 if constexpr (KIND == kKindMixed) f = (mine >> 17) & 3u;
-                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(rec, s.k[ks], off);
-                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(rec, s.k[ks], off);
-                else repack_k<kFmtE4m3>(rec, s.k[ks], off);
+                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(code, s.k[ks], off);
+                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(code, s.k[ks], off);
+                else repack_k<kFmtE4m3>(code, s.k[ks], off);
                 if (lane < kBs) {
-                    const float* sc = reinterpret_cast<const float*>(rec + 2 * kTileFp8);
+                    const float* sc = reinterpret_cast<const float*>(code + kTileFp8);
                     const bool on = mine >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
                     const int n = column_of(warp, lane);
                     s.factor[in][0][n] = wide ? 1.f : sc[lane];
@@ -726,56 +828,55 @@ __device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, in
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.k_full[ks]);
-            if (!wait_bar(s, &s.v_empty[vs], (k / kVStages) + 1)) return;
-            VPut v{s.v[vs], 0ull, look};
-            const uint8_t* pair = s.raw[(lane & 4) ? r1 : r0][0];   // lanes take the pair of blocks of their columns
-            if constexpr (is_lowbit(KIND)) repack_v_low<KIND, KIND == kKindInt4 ? 4 : 2>(pair, word, v, p.ng, warp, lane);
-            else repack_v<KIND>(pair, word, v, off, warp, lane);
-            fence_proxy_async_shared();
-            if (look) {
-                const uint32_t lo = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad));
-                const uint32_t hi = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad >> 32));
-                v.bad = static_cast<unsigned long long>(hi) << 32 | lo;
-            }
-            __syncwarp();
             if (lane == 0) {
-                s.info[in].nonfin[warp] = v.bad;
-                mbar_arrive(&s.v_full[vs]);
-                mbar_arrive(&s.raw_empty[r0]);
-                mbar_arrive(&s.raw_empty[r1]);
+                mbar_arrive(&s.k_full[ks]);
+                mbar_arrive(&s.rk_empty[st]);
             }
+        }
+        if (k > 0 && !repack_tile_v<KIND>(s, p, off, k - 1, before, warp, lane)) return;
+        if (!more) return;
+        before = look;
+        ++k;
+        if (++t == g.t1) {
+            more = walk.next(p, g);
+            t = more ? g.t0 : 0;
         }
     }
 }
 
-// The MMAs of warpgroup W, by one warp.  One arrival a step, s_taken: S(i) is in the warpgroup's registers
-// and P(i−1) in tensor memory; then O += P(i−1)·V(i−1) and S(i+1) = Q·K(i+1) are issued together, and one
-// commit, s_full, says that both are done.  So a warpgroup waits once a step, P needs two buffers (P(i+1)
-// is written when PV(i−1) is done), and the two warpgroups' bundles, some 650 cycles each, stagger them.
-// (Before, S and PV had barriers of their own and the waits, 100 to 300 cycles each, were most of a step.)
+// S of warpgroup W, by one warp: S(i+1) = Q·K(i+1) once the warpgroup has S(i) in registers.
 template <int KIND>
-__device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
-    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
+__device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
+    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile);
     const uint32_t W = uniform(warpgroup);
-    const uint32_t tmem = uniform(s.tmem);
-    const uint32_t k_op = uniform(smem_u32(s.k)), v_op = uniform(smem_u32(s.v)), q_op = uniform(smem_u32(s.q));
-    const uint32_t col_s = uniform(tmem + kColS + W * 64), col_o = uniform(tmem + kColO + W * 128);
+    const uint32_t col_s = uniform(s.tmem + kColS + W * 64);
+    const uint32_t k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, segs[2] = {0, 0}, step = 0, ends = 0;   // tiles before the segment; phases of q_ready, s_taken, p_last
+    uint32_t base = 0, step = 0, own = 0, ones = 0;   // tiles before the segment; phases of s_taken, q_ready, q_one
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
         const uint32_t mine = two ? n : (n + 1 - W) / 2, stride = two ? 1 : 2;
-        // both barriers' phases are followed in order, whether this warp has tiles or not
-        ok = wait_bar(s, &s.q_ready[0], segs[0]) && (!two || W == 0 || wait_bar(s, &s.q_ready[1], segs[1]));
+        if (mine > 0) ok = two || W == 0 ? wait_bar(s, &s.q_ready[W], own++) : wait_bar(s, &s.q_one, ones++);
         const uint32_t k0 = base + (two ? 0 : W);
         const uint32_t a = uniform(q_op + (two ? W : 0) * 2 * kOpBytes);
-        auto score = [&](uint32_t k) {   // S = Q·K^T of tile k
+        #pragma unroll 1
+        for (uint32_t i = 0; ok && i <= mine && mine > 0; ++i) {
+            const uint32_t k = k0 + i * stride;
+            if (i > 0) {
+                ok = wait_bar(s, &s.s_taken[W], step++);
+                if (!ok) break;
+                if (elect_one()) {   // two arrivals a stage: from both warpgroups, or twice from the one with the tile
+                    mbar_arrive(&s.k_empty[(k - stride) % kKStages]);
+                    if (!two) mbar_arrive(&s.k_empty[(k - stride) % kKStages]);
+                }
+                __syncwarp();
+            }
+            if (i == mine) break;
             const uint32_t st = k % kKStages;
             ok = wait_bar(s, &s.k_full[st], k / kKStages);
-            if (!ok) return;
+            if (!ok) break;
             tcgen_fence_after();
             const uint32_t b = uniform(k_op + st * kOpBytes);
             if (elect_one()) {
@@ -786,54 +887,59 @@ __device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, 
                 mma_commit(&s.s_full[W]);
             }
             __syncwarp();
-        };
-        if (ok && mine > 0) score(k0);
-        #pragma unroll 1
-        for (uint32_t i = 0; ok && mine > 0 && i <= mine; ++i) {
-            // (the last P has a barrier of its own: a warp may be there before another has taken its S)
-            ok = i < mine ? wait_bar(s, &s.s_taken[W], step++) : wait_bar(s, &s.p_last[W], ends++);
-            if (!ok) break;
-            tcgen_fence_after();
-            const uint32_t k = k0 + i * stride;
-            if (elect_one()) {   // two arrivals a stage: from both warpgroups, or twice from the one that has the tile
-                if (i < mine) {
-                    mbar_arrive(&s.k_empty[k % kKStages]);
-                    if (!two) mbar_arrive(&s.k_empty[k % kKStages]);
-                }
-                if (two && i >= 2 && i < mine) mbar_arrive(&s.v_empty[(k - 2) % kVStages]);   // S(i) came after PV(i−2)
-            }
-            __syncwarp();
-            if (i > 0) {   // O += P·V of the tile before
-                const uint32_t kp = k - stride, st = kp % kVStages;
-                ok = wait_bar(s, &s.v_full[st], kp / kVStages);
-                if (!ok) break;
-                tcgen_fence_after();
-                const uint32_t b = uniform(v_op + st * kOpBytes), c = uniform(tmem + kColP + W * 64 + ((i - 1) & 1) * 32);
-                const uint32_t more = uniform(i > 1);
-                if (elect_one()) {
-                    #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ts(col_o, c + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
-                    mma_commit(&s.pv_done[W]);
-                    // The stage goes back with the MMAs where no later step says that they are done: the last two, and
-                    // with tiles taken in turn every one (two steps later is four tiles, more than there are stages).
-                    if (!two || i == mine) mma_commit(&s.v_empty[st]);
-                    if (!two) mbar_arrive(&s.v_empty[st]);
-                    if (two && i == mine && i >= 2) mma_commit(&s.v_empty[(kp - 1) % kVStages]);
-                }
-                __syncwarp();
-            }
-            if (i + 1 < mine) score(k + stride);
         }
         base += n;
-        ++segs[0];
-        if (two) ++segs[1];
     }
-    __syncwarp();
     if (!ok) {   // what was issued completes before tensor memory is freed
         if (elect_one()) mma_commit(&s.drain[W]);
         __syncwarp();
         mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
+    }
+}
+
+// O of both warpgroups, by one warp: O_W += P_W(i)·V(i) when P_W(i) is in tensor memory, W = 0, 1 in turn (the
+// shared K stages keep the warpgroups within a step of each other).
+template <int KIND>
+__device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) {
+    constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
+    const uint32_t tmem = uniform(s.tmem), v_op = uniform(smem_u32(s.v));
+    Walk walk(p, s);
+    Segment g;
+    uint32_t base = 0, uses[2][2] = {{0, 0}, {0, 0}};   // tiles before the segment; uses of P's buffers before it
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
+        const uint32_t mine0 = two ? n : (n + 1) / 2, mine1 = two ? n : n / 2;
+        #pragma unroll 1
+        for (uint32_t j = 0; ok && j < 2 * mine0; ++j) {
+            const uint32_t W = j & 1u, i = j >> 1, buf = i & 1u;
+            if (W && i >= mine1) continue;
+            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kVStages;
+            const uint32_t used = W ? (buf ? uses[1][1] : uses[1][0]) : (buf ? uses[0][1] : uses[0][0]);
+            ok = wait_bar(s, &s.p_full[W][buf], used + (i >> 1)) && wait_bar(s, &s.v_full[st], k / kVStages);
+            if (!ok) break;
+            tcgen_fence_after();
+            const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColP + W * 64 + buf * 32);
+            const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
+            if (elect_one()) {
+                #pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
+                mma_commit(&s.pv_done[W][buf]);
+                mma_commit(&s.v_empty[st]);
+                if (!two) mbar_arrive(&s.v_empty[st]);
+            }
+            __syncwarp();
+        }
+        base += n;
+        uses[0][0] += (mine0 + 1) / 2;
+        uses[0][1] += mine0 / 2;
+        uses[1][0] += (mine1 + 1) / 2;
+        uses[1][1] += mine1 / 2;
+    }
+    if (!ok) {
+        if (elect_one()) mma_commit(&s.drain[2]);
+        __syncwarp();
+        mbar_wait(&s.drain[2], 0, nullptr, kWaitNs);
     }
 }
 
@@ -893,7 +999,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, done = 0, merges = 0;   // tiles before the segment, of both and of this warpgroup; phases of the merge
+    uint32_t base = 0, done = 0, ones = 0;   // tiles before the segment, of both and of this warpgroup; segments of one row group
+    uint32_t used0 = 0, used1 = 0;           // uses of P's buffers before the segment
     bool merge_pending = false;
     int seg_index = 0;
     while (walk.next(p, g)) {
@@ -905,7 +1012,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         const int64_t out_row = (static_cast<int64_t>(g.s0) + token) * p.n_q + head;
         const int pos = g.len < 0 ? -1 : g.len - g.T + token;
         if (merge_pending) {   // WG 0 has read the last unit's O and sums of this warpgroup
-            if (!wait_bar(s, &s.merge_empty, merges - 1)) return;
+            if (!wait_bar(s, &s.merge_empty, ones - 1)) return;
             merge_pending = false;
         }
         float rs = load_query<KIND>(p, p.q + (live ? out_row : 0) * kDh,
@@ -913,7 +1020,10 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                                     tid) * scale;
         rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
         __syncwarp();
-        if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
+        if (lane == 0) {
+            if (g.two || w == 0) mbar_arrive(&s.q_ready[w]);
+            if (!g.two && w == 0 && n > 1) mbar_arrive(&s.q_one);
+        }
         float m = -INFINITY, l = 0.f;
         int flagged = 0;
         unsigned long long flag_mask[8];
@@ -922,9 +1032,11 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             const uint32_t k = base + (g.two ? i : 2 * i + w);
             const int in = k % kInfos;
             const int t = g.t0 + (g.two ? i : 2 * i + w);
+            const uint32_t turn = i >> 1;   // earlier uses of P's buffer i & 1 in the segment
             // S(i) is there; so are the tile's mask and factors (k_full), and PV(i−2) is done, which leaves P(i)'s
-            // buffer free (pv_done, of which every phase is seen in order)
-            if (!wait_three(s, &s.s_full[w], done + i, &s.k_full[k % kKStages], k / kKStages, &s.pv_done[w], done + i - 2, i >= 2))
+            // buffer free.  A barrier per buffer: no phase can pass unseen.
+            if (!wait_three(s, &s.s_full[w], done + i, &s.k_full[k % kKStages], k / kKStages, &s.pv_done[w][i & 1],
+                            (i & 1 ? used1 : used0) + turn - 1, i >= 2))
                 return;
             tcgen_fence_after();
             uint32_t raw[2][32];
@@ -969,7 +1081,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             top = fmaxf(max3(top, x[kTile - 2], x[kTile - 1]), top2) * rs;
             if (__any_sync(kFull, top > m + kLazy)) {
                 if (i > 0) {   // O of the tiles before is complete
-                    if (!wait_bar(s, &s.pv_done[w], done + i - 1)) return;
+                    if (!wait_bar(s, &s.pv_done[w][(i - 1) & 1], ((i - 1) & 1 ? used1 : used0) + ((i - 1) >> 1))) return;
                     tcgen_fence_after();
                 }
                 const float nm = fmaxf(m, top);
@@ -1013,25 +1125,27 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_st32(col_p + (i & 1) * 32, pw);
-            tmem_wait_st();   // also before the registers are written again
+            tmem_wait_st();
             if (t_end > g.first) {   // non-finite V that only some rows attend (v_full: the repack has looked)
                 if (!wait_bar(s, &s.v_full[k % kVStages], k / kVStages)) return;
-                const unsigned long long* n4 = s.info[in].nonfin;
-                const unsigned long long bad = n4[0] | n4[1] | n4[2] | n4[3];
+                const unsigned long long* nf = s.info[in].nonfin;
+                const unsigned long long bad = nf[0] | nf[1] | nf[2] | nf[3];
                 if (bad && flagged < 8) {
                     flag_mask[flagged] = bad;
                     flag_tile[flagged++] = t;
                 }
             }
-        }
-        if (mine > 0) {
-            if (mine >= 2 && !wait_bar(s, &s.pv_done[w], done + mine - 2)) return;
             tcgen_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_last[w]);
-            if (!wait_bar(s, &s.pv_done[w], done + mine - 1)) return;
+            if (lane == 0) mbar_arrive(&s.p_full[w][i & 1]);
+        }
+        if (mine > 0) {
+            if (mine >= 2 && !wait_bar(s, &s.pv_done[w][mine & 1], (mine & 1 ? used1 : used0) + ((mine - 2) >> 1))) return;
+            if (!wait_bar(s, &s.pv_done[w][(mine - 1) & 1], ((mine - 1) & 1 ? used1 : used0) + ((mine - 1) >> 1))) return;
             tcgen_fence_after();
             done += mine;
+            used0 += (mine + 1) >> 1;
+            used1 += mine >> 1;
         }
         base += n;
         const bool merging = !g.two && n > 1;   // both warpgroups hold a part of the rows
@@ -1066,15 +1180,22 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 tmem_wait_st();
                 tcgen_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.merge_full);
-                ++merges;
-                merge_pending = true;
-                ++seg_index;
-                continue;
             }
-            if (!wait_bar(s, &s.merge_full, merges)) return;
-            ++merges;
+        }
+        if (!g.two && w == 1) {   // (without tiles too: the warpgroups stay within a segment of each other)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.merge_full);
+            ++ones;
+            merge_pending = true;
+            ++seg_index;
+            continue;
+        }
+        if (!g.two) {
+            if (!wait_bar(s, &s.merge_full, ones)) return;
+            ++ones;
             tcgen_fence_after();
+        }
+        if (merging) {
             const float m1 = s.ml()[tid], l1 = s.ml()[kWgRows + tid];
             const float M = fmaxf(m, m1);
             f0 = m == -INFINITY ? 0.f : ex2(m - M);
@@ -1083,9 +1204,6 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (m1 == M) f1 = M == -INFINITY ? f1 : 1.f;
             l = (m == -INFINITY && l == 0.f ? 0.f : l * f0) + (m1 == -INFINITY && l1 == 0.f ? 0.f : l1 * f1);
             m = M;
-        } else if (!g.two && w == 1) {
-            ++seg_index;
-            continue;
         }
         const bool whole = g.t0 == 0 && g.t1 == g.tiles;
         const int slot = 2 * blockIdx.x + (seg_index > 0);
@@ -1142,7 +1260,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             }
         }
         if (tid == 0 && w == 0 && !whole) p.part_seg[slot] = make_int4(g.b, g.h | g.qt << 16, g.t0, g.t1);
-        if (merging) {
+        if (!g.two) {
             tcgen_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.merge_empty);
@@ -1155,13 +1273,16 @@ template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p) {
     extern __shared__ uint8_t smem_raw[];
     Smem<KIND>& s = *reinterpret_cast<Smem<KIND>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-    constexpr int kRaw = raw_stages(KIND);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == kMmaWarp) tmem_alloc_all(&s.tmem);
+    if (warp == kOutWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
-        for (int i = 0; i < kRaw; ++i) {
-            mbar_init(&s.raw_full[i], 1);
-            mbar_init(&s.raw_empty[i], 4);
+        for (int i = 0; i < raw_k_tiles(KIND); ++i) {
+            mbar_init(&s.rk_full[i], 1);
+            mbar_init(&s.rk_empty[i], 4);
+        }
+        for (int i = 0; i < raw_v_tiles(KIND); ++i) {
+            mbar_init(&s.rv_full[i], 1);
+            mbar_init(&s.rv_empty[i], 4);
         }
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&s.k_full[i], 4);
@@ -1173,12 +1294,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_ready[i], 4);
-            mbar_init(&s.drain[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.s_taken[i], 4);
-            mbar_init(&s.p_last[i], 4);
-            mbar_init(&s.pv_done[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&s.p_full[i][b], 4);
+                mbar_init(&s.pv_done[i][b], 1);
+            }
         }
+        for (int i = 0; i < 3; ++i) mbar_init(&s.drain[i], 1);
+        mbar_init(&s.q_one, 4);
         mbar_init(&s.merge_full, 4);
         mbar_init(&s.merge_empty, 4);
         mbar_fence_init();
@@ -1188,8 +1312,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     pdl_wait();
     pdl_trigger();
     if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
-    make_schedule(p, s, reinterpret_cast<int64_t*>(s.raw));
-    fence_proxy_async_shared();   // the schedule's scratch lies where the copies will land
+    make_schedule(p, s, reinterpret_cast<int64_t*>(s.q));
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
@@ -1203,14 +1326,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         give_registers<88>();
         if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
         else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-        else if (warp < kMmaWarp + 2) mma_issuer<KIND>(s, p, warp - kMmaWarp);
+        else if (warp < kOutWarp) score_issuer<KIND>(s, p, warp - kScoreWarp);
+        else out_issuer<KIND>(s, p);
     }
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
     if (tid == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
-    if (warp == kMmaWarp) tmem_free_all(s.tmem);
+    if (warp == kOutWarp) tmem_free_all(s.tmem);
 }
 
 template <int KIND>
