@@ -50,10 +50,8 @@ namespace chunk {
 constexpr int kTile = 64;              // positions per tile: four blocks
 constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
-constexpr int kThreads = 512;          // softmax 2 × 128, repack 128, producer 32, S 2 × 32, O 32
-constexpr int kRepackWarp = 8, kProducerWarp = 12, kScoreWarp = 13, kOutWarp = 15;
-constexpr int kKStages = 2, kVStages = 2;   // operand stages, 16 KiB each
-constexpr int kInfos = 4;              // tiles whose masks and factors are kept
+constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, S 2 × 32, O 32
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kScoreWarp = 17, kOutWarp = 19;
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -62,36 +60,38 @@ constexpr int kColS = 0, kColP = 128, kColO = 256;   // tensor memory columns: S
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
-// Bytes of a record's parts.  A raw slot holds four blocks' K: codes, then the 8-bit record's scales or the
-// low-bit record's K words; or their V: codes, then the low-bit record's V words.
-constexpr int code_bytes(int kind) {
-    return kind == kKindBf16 || kind == kKindMixed ? kTileBf16
-           : kind == kKindInt4                     ? lowbit_tile_bytes(4)
-           : kind == kKindInt2                     ? lowbit_tile_bytes(2)
-                                                   : kTileFp8;
+// A raw slot holds a tile's four records.
+constexpr int max_record(int kind) {
+    return kind == kKindBf16 || kind == kKindMixed ? kRecordBf16
+           : kind == kKindInt4                     ? lowbit_record_bytes(4, 4)
+           : kind == kKindInt2                     ? lowbit_record_bytes(2, 4)
+                                                   : kRecordFp8;
 }
-constexpr int k_slot(int kind) {
-    return kind == kKindBf16 || kind == kKindMixed ? kTileBf16 : code_bytes(kind) + (is_lowbit(kind) ? lowbit_meta_bytes(4) : kScaleBytes);
-}
-constexpr int v_slot(int kind) { return code_bytes(kind) + (is_lowbit(kind) ? lowbit_meta_bytes(4) : 0); }
-constexpr int raw_k_tiles(int kind) { return kind == kKindBf16 || kind == kKindMixed ? 3 : 4; }
-constexpr int raw_v_tiles(int kind) { return kind == kKindBf16 ? 3 : kind == kKindMixed ? 2 : 4; }
+constexpr bool is_wide(int kind) { return kind == kKindBf16 || kind == kKindMixed; }
+// What fits beside Q: raw tiles, and operand stages of 16 KiB for K and for V.  A tile's masks and factors are
+// read until its warpgroup's next S is taken, in the worst case two tiles later: stages + 2 sets at least.
+constexpr int raw_tiles(int kind) { return kind == kKindMixed ? 2 : 3; }
+constexpr int op_stages(int kind) { return is_wide(kind) ? 2 : 3; }
+constexpr int info_sets(int kind) { return is_wide(kind) ? 4 : 8; }
 
 struct TileInfo {
-    unsigned long long mask;        // bit 16·block + t: position may be attended
-    unsigned long long nonfin[4];   // by repack warp; column n: its V has non-finite elements, zeroed in the operand
+    alignas(16) float limit[kTile];   // column: −inf where the position may not be attended, else +inf
+    unsigned long long mask;          // bit 16·block + t: position may be attended
+    unsigned long long nonfin[4];     // by repack warp; column n: its V has non-finite elements, zeroed in the operand
 };
+constexpr int kFlags = 5;           // tiles that hold positions of a unit's own tokens: ⌈(63 + 256)/64⌉
 
 template <int KIND>
 struct Smem {
-    uint8_t k[kKStages][kOpBytes], v[kVStages][kOpBytes];       // operands; 1,024-byte aligned
+    static constexpr int kStages = op_stages(KIND), kRaw = raw_tiles(KIND), kInfos = info_sets(KIND);
+    uint8_t k[kStages][kOpBytes], v[kStages][kOpBytes];         // operands; 1,024-byte aligned
     uint8_t q[2][2 * kOpBytes];                                 // 128 rows each
-    uint8_t raw_k[raw_k_tiles(KIND)][4][k_slot(KIND)], raw_v[raw_v_tiles(KIND)][4][v_slot(KIND)];
-    float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
+    uint8_t raw[kRaw][4][max_record(KIND)];
+    alignas(16) float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
     TileInfo info[kInfos];
-    uint32_t word_k[raw_k_tiles(KIND)][4], word_v[raw_v_tiles(KIND)][4];   // block words
-    uint64_t rk_full[raw_k_tiles(KIND)], rk_empty[raw_k_tiles(KIND)], rv_full[raw_v_tiles(KIND)], rv_empty[raw_v_tiles(KIND)];
-    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint32_t word[kRaw][4];                                     // block words
+    unsigned long long flags[8][kFlags];                        // by softmax warp: nonfin of the unit's last tiles
+    uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2], s_taken[2], p_full[2][2], pv_done[2][2];
     uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
     int64_t remaining;
@@ -103,22 +103,16 @@ struct Smem {
 };
 
 // ------------------------------------------------------------------ schedule
-// Σ_{i<n} ⌊(a·i + c)/m⌋.
-__device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t c) {
-    int64_t ans = 0;
-    if (n <= 0) return 0;
-    while (true) {
-        ans += n * (n - 1) / 2 * (a / m) + n * (c / m);
-        a %= m;
-        c %= m;
-        const int64_t y = a * n + c;
-        if (y < m) return ans;
-        n = y / m;
-        c = y % m;
-        const int64_t t = m;
-        m = a;
-        a = t;
-    }
+// Σ_{i<n} ⌊(a·i + c)/64⌋: the sum without the floors less that of the remainders, which repeat every 64 terms
+// (64/d values d apart, d = gcd(a, 64), each d times).
+__device__ inline int64_t tile_sum(int64_t n, int a, int64_t c) {
+    static_assert(kTile == 64, "the period of the remainders");
+    const int low = a & 63, d = low ? low & -low : 64;
+    int64_t rest = (n >> 6) * (64 * (c & (d - 1)) + 32 * (64 - d));
+    uint32_t at = static_cast<uint32_t>(c);
+    if (low == 0) rest += (n & 63) * (at & 63u);
+    else for (int i = 0; i < static_cast<int>(n & 63); ++i, at += low) rest += at & 63u;
+    return (a * (n * (n - 1) / 2) + c * n - rest) >> 6;
 }
 
 struct Request {
@@ -128,7 +122,7 @@ struct Request {
 __device__ __forceinline__ Request load_request(const ChunkParams& p, int b, bool tell) {
     Request r;
     r.s0 = p.q_start[b];
-    const int s1 = p.q_start[b + 1];
+    const int s1 = p.q_start[b + 1], len = p.seq_lens[b];
     r.T = 0;
     r.len = -1;
     if (r.s0 < 0 || s1 < r.s0 || s1 > p.n_tokens) {
@@ -137,7 +131,7 @@ __device__ __forceinline__ Request load_request(const ChunkParams& p, int b, boo
     }
     r.T = s1 - r.s0;
     if (r.T == 0) return r;
-    r.len = p.seq_lens[b];
+    r.len = len;
     if (r.len < r.T || static_cast<int64_t>(r.len) > static_cast<int64_t>(p.max_blocks) * kBs) {
         if (tell) report(p.err, KVD_ERR_OOB);
         r.len = -1;
@@ -154,7 +148,7 @@ __device__ inline int64_t tiles_before(const Request& r, int k, int tq) {   // t
     if (r.len < 0) return k;
     const int n = (r.T + tq - 1) / tq;
     const int whole = min(k, n - 1);
-    int64_t s = floor_sum(whole, kTile, tq, static_cast<int64_t>(r.len) - r.T + tq + kTile - 1);
+    int64_t s = tile_sum(whole, tq, static_cast<int64_t>(r.len) - r.T + tq + kTile - 1);
     if (k == n) s += unit_tiles(r, n - 1, tq);
     return s;
 }
@@ -247,21 +241,27 @@ __device__ inline void make_schedule(const ChunkParams& p, S& s, int64_t* scratc
                 if (lane >= o) up += v;
             }
             up += before;
-            if (lo >= up - c && lo < up) {
-                const int b = b0 + lane;
+            const unsigned at = __ballot_sync(kFull, lo >= up - c && lo < up);
+            if (at) {
+                const int src = __ffs(at) - 1, b = b0 + src;
+                const int64_t cost = __shfl_sync(kFull, c, src), from = __shfl_sync(kFull, up, src) - cost;
                 const Request r = load_request(p, b, false);
-                const int64_t head = c / p.n_kv, rem = lo - (up - c);
-                const int64_t in = rem % head;
-                int a = 0, z = (r.T + tq - 1) / tq - 1;   // the last unit that starts at or before `in`
-                while (a < z) {
-                    const int mid = (a + z + 1) / 2;
-                    if (tiles_before(r, mid, tq) <= in) a = mid;
-                    else z = mid - 1;
+                const int64_t head = cost / p.n_kv, rem = lo - from;
+                const int h = static_cast<int>(rem / head);
+                const int64_t in = rem - h * head;
+                int a = 0, z = (r.T + tq - 1) / tq;   // the last unit of [a, z) that starts at or before `in`
+                while (z - a > 1) {
+                    const int step = (z - a + 31) / 32, mid = a + lane * step;
+                    const int n = __popc(__ballot_sync(kFull, mid < z && tiles_before(r, mid, tq) <= in));
+                    a += (n - 1) * step;
+                    z = min(z, a + step);
                 }
-                s.b = b;
-                s.h = static_cast<int>(rem / head);
-                s.qt = a;
-                s.off = static_cast<int>(in - tiles_before(r, a, tq));
+                if (lane == 0) {
+                    s.b = b;
+                    s.h = h;
+                    s.qt = a;
+                    s.off = static_cast<int>(in - tiles_before(r, a, tq));
+                }
             }
             before = __shfl_sync(kFull, up, 31);
             if (before > lo) break;
@@ -385,16 +385,19 @@ __device__ __forceinline__ void st16(uint8_t* p, uint32_t a, uint32_t b, uint32_
 template <int FMT>
 __device__ __forceinline__ void repack_k(const uint8_t* code, uint8_t* op, const Offsets& o) {
     if constexpr (FMT == kFmtBf16) {
-        uint4 a[4], b[4];
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = ld16(code + 2 * o.k_half + o.k_ld[i & 1] + (i >> 1) * 2048);
-            b[i] = ld16(code + 2 * o.k_half + o.k_ld[i & 1] + (i >> 1) * 2048 + 512);
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            st16(op + o.k_st[i & 1][0] + (i >> 1) * 8192, a[i].x, a[i].z, b[i].x, b[i].z);
-            st16(op + o.k_st[i & 1][1] + (i >> 1) * 8192, a[i].y, a[i].w, b[i].y, b[i].w);
+        for (int j = 0; j < 2; ++j) {
+            uint4 a[2], b[2];
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                a[q] = ld16(code + 2 * o.k_half + o.k_ld[q] + j * 2048);
+                b[q] = ld16(code + 2 * o.k_half + o.k_ld[q] + j * 2048 + 512);
+            }
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                st16(op + o.k_st[q][0] + j * 8192, a[q].x, a[q].z, b[q].x, b[q].z);
+                st16(op + o.k_st[q][1] + j * 8192, a[q].y, a[q].w, b[q].y, b[q].w);
+            }
         }
     } else {
         uint4 a[4];
@@ -443,15 +446,15 @@ __device__ __forceinline__ uint4 v_piece(const uint8_t* code, int i, int l) {
     }
 }
 template <int KIND>
-__device__ __forceinline__ uint4 v_piece_kind(const uint8_t* code, uint32_t word, int i, int l) {
+__device__ __forceinline__ uint4 v_piece_kind(const uint8_t* rec, uint32_t word, int i, int l) {
     if constexpr (KIND == kKindBf16) {
-        return v_piece<kFmtBf16>(code, i, l);
+        return v_piece<kFmtBf16>(rec + kTileBf16, i, l);
     } else if constexpr (KIND == kKindMixed) {
         const int f = (word >> 17) & 3u;
-        return f == kFmtBf16 ? v_piece<kFmtBf16>(code, i, l)
-               : f == kFmtE4m3 ? v_piece<kFmtE4m3>(code, i, l) : v_piece<kFmtE5m2>(code, i, l);
+        return f == kFmtBf16 ? v_piece<kFmtBf16>(rec + kTileBf16, i, l)
+               : f == kFmtE4m3 ? v_piece<kFmtE4m3>(rec + kTileFp8, i, l) : v_piece<kFmtE5m2>(rec + kTileFp8, i, l);
     } else {
-        return v_piece<kFmtE4m3>(code, i, l);
+        return v_piece<kFmtE4m3>(rec + kTileFp8, i, l);
     }
 }
 
@@ -459,7 +462,8 @@ __device__ __forceinline__ uint4 v_piece_kind(const uint8_t* code, uint32_t word
 // non-finite elements matter.  Returns whether the lane met something that wants the element-wise path.
 template <int KIND, bool MASK, bool LOOK>
 __device__ __forceinline__ bool repack_v_fast(const uint8_t* pair, const VPut& out, const Offsets& o) {
-    constexpr int kNext = v_slot(KIND);
+    constexpr int kNext = max_record(KIND);
+    const uint8_t* code = pair + (KIND == kKindBf16 ? kTileBf16 : kTileFp8);
     uint32_t odd = 0, special = 0;
     auto put = [&](uint8_t* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
         if constexpr (MASK) {
@@ -472,24 +476,27 @@ __device__ __forceinline__ bool repack_v_fast(const uint8_t* pair, const VPut& o
         st16(to, a, b, c, d);
     };
     if constexpr (KIND == kKindBf16) {
-        uint4 a[4], b[4];
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = ld16(pair + 2 * o.v_warp + o.v_ld[i & 1] + (i >> 1) * 512);
-            b[i] = ld16(pair + 2 * o.v_warp + o.v_ld[i & 1] + (i >> 1) * 512 + kNext);
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint8_t* to = out.op + o.v_st[i & 1] + (i >> 1) * 2048;
-            put(to, a[i].x, a[i].z, b[i].x, b[i].z);
-            put(to + 1024, a[i].y, a[i].w, b[i].y, b[i].w);
+        for (int j = 0; j < 2; ++j) {
+            uint4 a[2], b[2];
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                a[q] = ld16(code + 2 * o.v_warp + o.v_ld[q] + j * 512);
+                b[q] = ld16(code + 2 * o.v_warp + o.v_ld[q] + j * 512 + kNext);
+            }
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint8_t* to = out.op + o.v_st[q] + j * 2048;
+                put(to, a[q].x, a[q].z, b[q].x, b[q].z);
+                put(to + 1024, a[q].y, a[q].w, b[q].y, b[q].w);
+            }
         }
     } else {
         uint4 a[2], b[2];
         #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            a[q] = ld16(pair + o.v_warp + o.v_ld[q]);
-            b[q] = ld16(pair + o.v_warp + o.v_ld[q] + kNext);
+            a[q] = ld16(code + o.v_warp + o.v_ld[q]);
+            b[q] = ld16(code + o.v_warp + o.v_ld[q] + kNext);
         }
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -521,7 +528,7 @@ __device__ __forceinline__ void repack_v(const uint8_t* pair, const uint32_t (&w
     for (int i = 0; i < 4; ++i) {
         const int group = 2 * warp + (i >> 1), r = 2 * rl + ((i & 1) ^ p);
         const uint4 a = v_piece_kind<KIND>(pair, word[2 * p], group, 4 * r + x);
-        const uint4 b = v_piece_kind<KIND>(pair + v_slot(KIND), word[2 * p + 1], group, 4 * r + x);
+        const uint4 b = v_piece_kind<KIND>(pair + max_record(KIND), word[2 * p + 1], group, 4 * r + x);
         out.put(16 * group + r, lane, a.x, a.z, b.x, b.z);
         out.put(16 * group + r + 8, lane, a.y, a.w, b.y, b.w);
     }
@@ -536,7 +543,7 @@ __device__ __forceinline__ uint32_t low_pair(uint32_t word, int h, int j, float2
 template <int BITS>
 __device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, int k, int ng, int lane) {
     constexpr int kPer = 8 / BITS, kTileB = lowbit_tile_bytes(BITS);
-    const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + kTileB);
+    const uint32_t* meta = reinterpret_cast<const uint32_t*>(rec + 2 * kTileB);
     const int x = lane & 3, r = lane >> 2;
     const int n = column_of(k, r);
     #pragma unroll
@@ -567,12 +574,12 @@ __device__ __forceinline__ void repack_v_low(const uint8_t* pair, VPut& out, int
             uint32_t o[2][4];   // dims r, r + 8: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p, 2p+1
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint8_t* b = pair + u * v_slot(KIND);
-                const uint32_t* meta = reinterpret_cast<const uint32_t*>(b + kTileB);
+                const uint8_t* b = pair + u * max_record(KIND);
+                const uint32_t* meta = reinterpret_cast<const uint32_t*>(b + 2 * kTileB) + kBs * ng;
                 const int gi = group * ng / 8;
                 #pragma unroll
                 for (int th = 0; th < 2; ++th) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(b + lowbit_word(kg, 4 * r + x, th) * 4);
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(b + kTileB + lowbit_word(kg, 4 * r + x, th) * 4);
                     const int t = 2 * x + 8 * th;
                     const float2 s0 = unpack_f16(meta[t * ng + gi]), s1 = unpack_f16(meta[(t + 1) * ng + gi]);
                     o[0][2 * u + th] = low_pair<BITS>(w, h, 0, s0, s1);
@@ -652,208 +659,181 @@ __device__ __forceinline__ bool wait_bar(Smem<KIND>& s, uint64_t* bar, uint32_t 
 
 // Three waits with one vote; the third only if `third`.
 template <int KIND>
+__device__ __forceinline__ bool wait_two(Smem<KIND>& s, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, bool second = true) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        const bool x = mbar_try_wait(a, pa & 1u), y = !second || mbar_try_wait(b, pb & 1u);
+        if (__all_sync(kFull, x && y)) return true;
+    }
+    s.abort = 1;   // reported at the kernel's end
+    return false;
+}
+template <int KIND>
 __device__ __forceinline__ bool wait_three(Smem<KIND>& s, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c,
                                            uint32_t pc, bool third) {
     #pragma unroll 1
     for (int i = 0; i < kTries; ++i) {
-        const bool x = mbar_try_wait(a, pa & 1u), y = mbar_try_now(b, pb & 1u);
-        const bool z = !third || mbar_try_now(c, pc & 1u);
+        const bool x = mbar_try_wait(a, pa & 1u), y = mbar_try_wait(b, pb & 1u);
+        const bool z = !third || mbar_try_wait(c, pc & 1u);
         if (__all_sync(kFull, x && y && z)) return true;
     }
     s.abort = 1;
     return false;
 }
 
-// One block's K (or V) part into its raw slot.  Returns the bytes that will be counted on the barrier.
-template <int KIND>
-__device__ __forceinline__ uint32_t part_bytes(const ChunkParams& p, uint32_t word, bool value) {
-    if (!word) return 0;
-    const bool wide = KIND == kKindBf16 || (KIND == kKindMixed && ((word >> 17) & 3u) == kFmtBf16);
-    if (is_lowbit(KIND)) return code_bytes(KIND) + kBs * p.ng * 4;
-    return wide ? kTileBf16 : value ? kTileFp8 : kTileFp8 + kScaleBytes;
-}
-// copy(destination, source, bytes) of the part's one or two pieces.
-template <int KIND, class F>
-__device__ __forceinline__ void part_pieces(const ChunkParams& p, uint32_t word, bool value, uint8_t* slot, const uint8_t* rec, F copy) {
-    constexpr int kCode = is_lowbit(KIND) ? code_bytes(KIND) : kTileFp8;
-    const bool wide = KIND == kKindBf16 || (KIND == kKindMixed && ((word >> 17) & 3u) == kFmtBf16);
-    if (wide) {
-        copy(slot, rec + (value ? kTileBf16 : 0), kTileBf16);
-        return;
-    }
-    copy(slot, rec + (value ? kCode : 0), kCode);
-    if (is_lowbit(KIND)) copy(slot + kCode, rec + 2 * kCode + (value ? kBs * p.ng * 4 : 0), kBs * p.ng * 4);
-    else if (!value) copy(slot + kCode, rec + 2 * kCode, kScaleBytes);
-}
-
 template <int KIND>
 __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, int lane) {
-    constexpr int kRk = raw_k_tiles(KIND), kRv = raw_v_tiles(KIND);
+    constexpr int kRaw = Smem<KIND>::kRaw;
     Walk walk(p, s);
     Segment g;
-    uint32_t k = 0, issued[2] = {0, 0};   // tiles whose K and whose V are under way
+    uint32_t k = 0;
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const int32_t* row = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks;
+        auto block_at = [&](int j) { return j < 4 * g.t1 && j * kBs < g.end ? row[j] : -1; };
+        int phys = block_at(4 * g.t0 + lane);   // 32 blocks: eight tiles; the next eight's are fetched meanwhile
         for (int tb = g.t0; ok && tb < g.t1; tb += 8) {
-            const int j = 4 * tb + lane;   // 32 blocks: eight tiles
+            const int j = 4 * tb + lane;
             uint32_t word = 0;
             const uint8_t* rec = nullptr;
             bool host = false;
             if (j < 4 * g.t1 && j * kBs < g.end) {
-                const int phys = row[j];
                 word = block_word_of<KIND>(p, phys, j, g.end);
                 if (word) rec = record_at(p, phys, g.h);
                 host = word && p.host_direct && phys >= p.num_blocks;
             }
+            phys = block_at(j + 32);
+            uint32_t bytes = 0;
+            if (word && !host)
+                bytes = KIND == kKindMixed && ((word >> 17) & 3u) != kFmtBf16 ? kRecordFp8 : static_cast<uint32_t>(p.record_bytes);
+            uint32_t four = bytes + __shfl_xor_sync(kFull, bytes, 1);
+            four += __shfl_xor_sync(kFull, four, 2);
             const int n = min(8, g.t1 - tb);
-            for (int i = 0; ok && i < n; ++i, ++k) {
+            for (int i = 0; i < n; ++i, ++k) {
+                const uint32_t st = k % kRaw;
+                ok = wait_bar(s, &s.raw_empty[st], k / kRaw + 1);
+                if (!ok) break;
                 const bool mine = (lane >> 2) == i;
-                #pragma unroll 1
-                for (int value = 0; value < 2; ++value) {
-                    const uint32_t st = value ? k % kRv : k % kRk, use = value ? k / kRv : k / kRk;
-                    uint64_t* full = value ? &s.rv_full[st] : &s.rk_full[st];
-                    ok = wait_bar(s, value ? &s.rv_empty[st] : &s.rk_empty[st], use + 1);
-                    if (!ok) break;
-                    uint8_t* slot = value ? s.raw_v[st][lane & 3] : s.raw_k[st][lane & 3];
-                    if (mine) (value ? s.word_v[st] : s.word_k[st])[lane & 3] = word;
-                    uint32_t bytes = mine && !host ? part_bytes<KIND>(p, word, value) : 0;
-                    bytes += __shfl_xor_sync(kFull, bytes, 1);
-                    bytes += __shfl_xor_sync(kFull, bytes, 2);
-                    if (p.host_direct) {   // blocks in host memory: copied by the load path, the whole warp
-                        unsigned hosts = __ballot_sync(kFull, mine && host);
-                        fence_proxy_async_shared();
-                        while (hosts) {
-                            const int l = __ffs(hosts) - 1;
-                            hosts &= hosts - 1;
-                            const uint8_t* src = reinterpret_cast<const uint8_t*>(
-                                __shfl_sync(kFull, reinterpret_cast<unsigned long long>(rec), l));
-                            part_pieces<KIND>(p, __shfl_sync(kFull, word, l), value, value ? s.raw_v[st][l & 3] : s.raw_k[st][l & 3],
-                                              src, [&](uint8_t* to, const uint8_t* from, int b) {
-                                                  for (int c = lane; c < b / 16; c += 32) cp_async16_g2s(to + 16 * c, from + 16 * c);
-                                              });
-                        }
-                        cp_async_mbar_arrive(full);
+                if (mine) s.word[st][lane & 3] = word;
+                if (p.host_direct) {   // records in host memory: copied by the load path, the whole warp
+                    unsigned hosts = __ballot_sync(kFull, mine && host);
+                    fence_proxy_async_shared();
+                    while (hosts) {
+                        const int l = __ffs(hosts) - 1;
+                        hosts &= hosts - 1;
+                        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+                            __shfl_sync(kFull, reinterpret_cast<unsigned long long>(rec), l));
+                        for (int c = lane; c < p.record_bytes / 16; c += 32)
+                            cp_async16_g2s(s.raw[st][l & 3] + 16 * c, src + 16 * c);
                     }
-                    __syncwarp();
-                    if (lane == 4 * i) {
-                        if (bytes) mbar_arrive_expect_tx(full, bytes);
-                        else mbar_arrive(full);
-                    }
-                    __syncwarp();
-                    if (mine && word && !host)
-                        part_pieces<KIND>(p, word, value, slot, rec,
-                                          [&](uint8_t* to, const uint8_t* from, int b) { bulk_copy(to, from, b, full); });
-                    if (value) ++issued[1];
-                    else ++issued[0];
+                    cp_async_mbar_arrive(&s.raw_full[st]);
                 }
+                __syncwarp();
+                if (lane == 4 * i) {
+                    if (four) mbar_arrive_expect_tx(&s.raw_full[st], four);
+                    else mbar_arrive(&s.raw_full[st]);
+                }
+                __syncwarp();
+                if (mine && bytes) bulk_copy(s.raw[st][lane & 3], rec, bytes, &s.raw_full[st]);
             }
         }
     }
     if (!ok) {   // the copies in flight land before the block leaves
-        for (uint32_t i = issued[0] > kRk ? issued[0] - kRk : 0; i < issued[0]; ++i)
-            mbar_wait(&s.rk_full[i % kRk], (i / kRk) & 1u, nullptr, kWaitNs);
-        for (uint32_t i = issued[1] > kRv ? issued[1] - kRv : 0; i < issued[1]; ++i)
-            mbar_wait(&s.rv_full[i % kRv], (i / kRv) & 1u, nullptr, kWaitNs);
+        for (uint32_t i = k > kRaw ? k - kRaw : 0; i < k; ++i) mbar_wait(&s.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr, kWaitNs);
     }
 }
 
-// K of tile k, then V of tile k − 1: V is wanted a step later than K, and its stage is free later.
+// K of every tile, a block a warp; with the tile's mask and factors.
 template <int KIND>
-__device__ __forceinline__ bool repack_tile_v(Smem<KIND>& s, const ChunkParams& p, const Offsets& off, uint32_t k, bool look, int warp,
-                                              int lane) {
-    constexpr int kRv = raw_v_tiles(KIND);
-    const uint32_t st = k % kRv, vs = k % kVStages;
-    if (!wait_three(s, &s.rv_full[st], k / kRv, &s.v_empty[vs], (k / kVStages) + 1, &s.v_empty[vs], 0, false)) return false;
-    const uint32_t word[4] = {s.word_v[st][0], s.word_v[st][1], s.word_v[st][2], s.word_v[st][3]};
-    VPut v(s.v[vs], word, look, lane);
-    const uint8_t* pair = s.raw_v[st][(lane & 4) >> 1];   // lanes take the pair of blocks of their columns
-    if constexpr (is_lowbit(KIND)) repack_v_low<KIND, KIND == kKindInt4 ? 4 : 2>(pair, v, p.ng, warp, lane);
-    else repack_v<KIND>(pair, word, v, off, warp, lane);
-    fence_proxy_async_shared();
-    if (look) {
-        const uint32_t lo = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad));
-        const uint32_t hi = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad >> 32));
-        v.bad = static_cast<unsigned long long>(hi) << 32 | lo;
+__device__ __forceinline__ void key_repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
+    constexpr int kRaw = Smem<KIND>::kRaw, kStages = Smem<KIND>::kStages;
+    const Offsets off(warp, lane);
+    const uint32_t tiles = static_cast<uint32_t>(s.remaining);
+    #pragma unroll 1
+    for (uint32_t k = 0; k < tiles; ++k) {
+        const uint32_t st = k % kRaw, ks = k % kStages, in = k % Smem<KIND>::kInfos;
+        if (!wait_two(s, &s.raw_full[st], k / kRaw, &s.k_empty[ks], k / kStages + 1)) return;
+        const uint32_t mine = s.word[st][warp];
+        if (warp == 0 && lane == 0)
+            s.info[in].mask = static_cast<unsigned long long>(s.word[st][0] & 0xffffu) |
+                              static_cast<unsigned long long>(s.word[st][1] & 0xffffu) << 16 |
+                              static_cast<unsigned long long>(s.word[st][2] & 0xffffu) << 32 |
+                              static_cast<unsigned long long>(s.word[st][3] & 0xffffu) << 48;
+        if (lane < kBs) s.info[in].limit[column_of(warp, lane)] = mine >> lane & 1u ? INFINITY : -INFINITY;
+        const uint8_t* code = s.raw[st][warp];   // this warp's block
+        if constexpr (KIND == kKindBf16) {
+            repack_k<kFmtBf16>(code, s.k[ks], off);
+        } else if constexpr (is_lowbit(KIND)) {
+            repack_k_low<KIND == kKindInt4 ? 4 : 2>(code, s.k[ks], warp, p.ng, lane);
+        } else {
+            int f = kFmtE4m3;
+            if constexpr (KIND == kKindMixed) f = (mine >> 17) & 3u;
+            if (lane < kBs) {
+                const float* sc = reinterpret_cast<const float*>(code + 2 * kTileFp8);
+                const bool on = mine >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
+                const int n = column_of(warp, lane);
+                s.factor[in][0][n] = wide ? 1.f : sc[lane];
+                s.factor[in][1][n] = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
+            }
+            if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(code, s.k[ks], off);
+            else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(code, s.k[ks], off);
+            else repack_k<kFmtE4m3>(code, s.k[ks], off);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&s.k_full[ks]);
+            mbar_arrive(&s.raw_empty[st]);
+        }
     }
-    __syncwarp();
-    if (lane == 0) {
-        s.info[k % kInfos].nonfin[warp] = v.bad;
-        mbar_arrive(&s.v_full[vs]);
-        mbar_arrive(&s.rv_empty[st]);
-    }
-    return true;
 }
 
+// V of every tile, 32 dims a warp.
 template <int KIND>
-__device__ __forceinline__ void repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
-    constexpr int kRk = raw_k_tiles(KIND);
+__device__ __forceinline__ void value_repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
+    constexpr int kRaw = Smem<KIND>::kRaw, kStages = Smem<KIND>::kStages;
     const Offsets off(warp, lane);
     Walk walk(p, s);
     Segment g;
     uint32_t k = 0;
-    bool before = false;   // the tile before: rows differ in what they attend of it
-    bool more = walk.next(p, g);
-    int t = more ? g.t0 : 0;
-    while (true) {
-        bool look = false;
-        if (more) {
-            const uint32_t st = k % kRk, ks = k % kKStages, in = k % kInfos;
-            if (!wait_three(s, &s.rk_full[st], k / kRk, &s.k_empty[ks], (k / kKStages) + 1, &s.k_empty[ks], 0, false)) return;
-            const uint32_t mine = s.word_k[st][warp];
-            look = t * kTile + kTile - 1 > g.first;
-            if (warp == 0 && lane == 0)
-                s.info[in].mask = static_cast<unsigned long long>(s.word_k[st][0] & 0xffffu) |
-                                  static_cast<unsigned long long>(s.word_k[st][1] & 0xffffu) << 16 |
-                                  static_cast<unsigned long long>(s.word_k[st][2] & 0xffffu) << 32 |
-                                  static_cast<unsigned long long>(s.word_k[st][3] & 0xffffu) << 48;
-            const uint8_t* code = s.raw_k[st][warp];   // this warp's block
-            if constexpr (KIND == kKindBf16) {
-                repack_k<kFmtBf16>(code, s.k[ks], off);
-            } else if constexpr (is_lowbit(KIND)) {
-                repack_k_low<KIND == kKindInt4 ? 4 : 2>(code, s.k[ks], warp, p.ng, lane);
-            } else {
-                int f = kFmtE4m3;
-                if constexpr (KIND == kKindMixed) f = (mine >> 17) & 3u;
-                if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(code, s.k[ks], off);
-                else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(code, s.k[ks], off);
-                else repack_k<kFmtE4m3>(code, s.k[ks], off);
-                if (lane < kBs) {
-                    const float* sc = reinterpret_cast<const float*>(code + kTileFp8);
-                    const bool on = mine >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
-                    const int n = column_of(warp, lane);
-                    s.factor[in][0][n] = wide ? 1.f : sc[lane];
-                    s.factor[in][1][n] = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
-                }
-            }
+    while (walk.next(p, g)) {
+        #pragma unroll 1
+        for (int t = g.t0; t < g.t1; ++t, ++k) {
+            const uint32_t st = k % kRaw, vs = k % kStages;
+            if (!wait_two(s, &s.raw_full[st], k / kRaw, &s.v_empty[vs], k / kStages + 1)) return;
+            const bool look = t * kTile + kTile - 1 > g.first;
+            const uint32_t word[4] = {s.word[st][0], s.word[st][1], s.word[st][2], s.word[st][3]};
+            VPut v(s.v[vs], word, look, lane);
+            const uint8_t* pair = s.raw[st][(lane & 4) >> 1];   // lanes take the pair of blocks of their columns
+            if constexpr (is_lowbit(KIND)) repack_v_low<KIND, KIND == kKindInt4 ? 4 : 2>(pair, v, p.ng, warp, lane);
+            else repack_v<KIND>(pair, word, v, off, warp, lane);
             fence_proxy_async_shared();
+            if (look) {
+                const uint32_t lo = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad));
+                const uint32_t hi = __reduce_or_sync(kFull, static_cast<uint32_t>(v.bad >> 32));
+                v.bad = static_cast<unsigned long long>(hi) << 32 | lo;
+            }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&s.k_full[ks]);
-                mbar_arrive(&s.rk_empty[st]);
+                s.info[k % Smem<KIND>::kInfos].nonfin[warp] = v.bad;
+                mbar_arrive(&s.v_full[vs]);
+                mbar_arrive(&s.raw_empty[st]);
             }
-        }
-        if (k > 0 && !repack_tile_v<KIND>(s, p, off, k - 1, before, warp, lane)) return;
-        if (!more) return;
-        before = look;
-        ++k;
-        if (++t == g.t1) {
-            more = walk.next(p, g);
-            t = more ? g.t0 : 0;
         }
     }
 }
 
-// S of warpgroup W, by one warp: S(i+1) = Q·K(i+1) once the warpgroup has S(i) in registers.
+// S of warpgroup W, by one warp: S(i+1) = Q·K(i+1) once the warpgroup has S(i) in registers (which frees its K too).
 template <int KIND>
 __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
     constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile);
+    constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t W = uniform(warpgroup);
     const uint32_t col_s = uniform(s.tmem + kColS + W * 64);
     const uint32_t k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, step = 0, own = 0, ones = 0;   // tiles before the segment; phases of s_taken, q_ready, q_one
+    uint32_t base = 0, step = 0, own = 0, ones = 0;   // tiles before the segment, of this warpgroup; phases of q_ready, q_one
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
@@ -862,20 +842,9 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
         const uint32_t k0 = base + (two ? 0 : W);
         const uint32_t a = uniform(q_op + (two ? W : 0) * 2 * kOpBytes);
         #pragma unroll 1
-        for (uint32_t i = 0; ok && i <= mine && mine > 0; ++i) {
-            const uint32_t k = k0 + i * stride;
-            if (i > 0) {
-                ok = wait_bar(s, &s.s_taken[W], step++);
-                if (!ok) break;
-                if (elect_one()) {   // two arrivals a stage: from both warpgroups, or twice from the one with the tile
-                    mbar_arrive(&s.k_empty[(k - stride) % kKStages]);
-                    if (!two) mbar_arrive(&s.k_empty[(k - stride) % kKStages]);
-                }
-                __syncwarp();
-            }
-            if (i == mine) break;
-            const uint32_t st = k % kKStages;
-            ok = wait_bar(s, &s.k_full[st], k / kKStages);
+        for (uint32_t i = 0; ok && i < mine; ++i, ++step) {
+            const uint32_t k = k0 + i * stride, st = k % kStages;
+            ok = wait_two(s, &s.k_full[st], k / kStages, &s.s_taken[W], step - 1, step > 0);
             if (!ok) break;
             tcgen_fence_after();
             const uint32_t b = uniform(k_op + st * kOpBytes);
@@ -902,6 +871,7 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
 template <int KIND>
 __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) {
     constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
+    constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t tmem = uniform(s.tmem), v_op = uniform(smem_u32(s.v));
     Walk walk(p, s);
     Segment g;
@@ -914,9 +884,9 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
         for (uint32_t j = 0; ok && j < 2 * mine0; ++j) {
             const uint32_t W = j & 1u, i = j >> 1, buf = i & 1u;
             if (W && i >= mine1) continue;
-            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kVStages;
+            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages;
             const uint32_t used = W ? (buf ? uses[1][1] : uses[1][0]) : (buf ? uses[0][1] : uses[0][0]);
-            ok = wait_bar(s, &s.p_full[W][buf], used + (i >> 1)) && wait_bar(s, &s.v_full[st], k / kVStages);
+            ok = wait_two(s, &s.p_full[W][buf], used + (i >> 1), &s.v_full[st], k / kStages);
             if (!ok) break;
             tcgen_fence_after();
             const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColP + W * 64 + buf * 32);
@@ -943,55 +913,75 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
     }
 }
 
-// A row of q as the A operand, in the dim order of the K operand: word 16j + 4x + m is the pair of dims
-// 32j + 2x + 8m.  Returns the factor of the row's logits (angle-domain).
+// A warp's 32 rows of q into the A operand, in the dim order of the K operand; base: the unit's first token; rel: the
+// lane's row counted from there, −1 for none.  Half a warp reads a row, two a load: dims 8c .. 8c+7 are words c & 3 of
+// four pieces.  Returns what multiplies the row's logits (angle keys; 1 else).
 template <int KIND>
-__device__ __forceinline__ float load_query(const ChunkParams& p, const uint16_t* q, bool row, bool store, bool flip, uint8_t* op,
-                                            int r) {
+__device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool store, bool flip, uint8_t* op, int warp, int lane) {
+    const int c = lane & 15, half = c >> 3;
     float factor = 1.f;
-    uint32_t w[2][32];
-    #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row) v = *reinterpret_cast<const uint4*>(q + 8 * i);
-        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    if (!store && KIND != kKindAngle) return factor;
+    #pragma unroll 1
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 v[8];
         #pragma unroll
-        for (int x = 0; x < 4; ++x) w[i >> 3][16 * ((i >> 2) & 1) + 4 * x + (i & 3)] = flip ? e[x] ^ 0x80008000u : e[x];
-    }
-    if constexpr (KIND == kKindAngle) {   // the E4M3 code of the row at its absmax scale, ||q||/||d_q||
-        float top = 0.f;
-        #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            const float2 v = unpack_bf16(w[i >> 5][i & 31]);
-            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+        for (int i = 0; i < 8; ++i) {
+            const int at = __shfl_sync(kFull, rel, 2 * (i0 + i) + (lane >> 4));
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) v[i] = ld16(reinterpret_cast<const uint8_t*>(base + static_cast<int64_t>(at) * kDh + 8 * c));
         }
-        const float sc = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
-        float r2 = 0.f, d2 = 0.f;
         #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            const float2 v = unpack_bf16(w[i >> 5][i & 31]);
-            const float a = __fdiv_rn(v.x, sc), b = __fdiv_rn(v.y, sc);
-            const float c = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
-            const float d = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
-            r2 += a * a + b * b;
-            d2 += c * c + d * d;
-            w[i >> 5][i & 31] = pack_bf16(c, d);
+        for (int i = 0; i < 8; ++i) {
+            uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            #pragma unroll
+            for (int x = 0; x < 4; ++x) e[x] = flip ? e[x] ^ 0x80008000u : e[x];
+            if constexpr (KIND == kKindAngle) {   // the E4M3 code of the row at its absmax scale, ||q||/||d_q||
+                float top = 0.f;
+                #pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float2 f = unpack_bf16(e[x]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+                #pragma unroll
+                for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                const float sc = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+                float r2 = 0.f, d2 = 0.f;
+                #pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float2 f = unpack_bf16(e[x]);
+                    const float a = __fdiv_rn(f.x, sc), b = __fdiv_rn(f.y, sc);
+                    const float da = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+                    const float db = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+                    r2 += a * a + b * b;
+                    d2 += da * da + db * db;
+                    e[x] = pack_bf16(da, db);
+                }
+                #pragma unroll
+                for (int o = 1; o < 16; o <<= 1) {
+                    r2 += __shfl_xor_sync(kFull, r2, o);
+                    d2 += __shfl_xor_sync(kFull, d2, o);
+                }
+                const float f = __shfl_sync(kFull, d2 == 0.f ? 0.f : sc * sqrtf(r2 / d2), (lane & 1) << 4);
+                if ((lane >> 1) == i0 + i) factor = f;
+            }
+            if (!store) continue;
+            const int row = 32 * warp + 2 * (i0 + i) + (lane >> 4);
+            uint8_t* to = op + half * kOpBytes + row * 128 + (c & 3) * 4;
+            #pragma unroll
+            for (int x = 0; x < 4; ++x) {   // the halves take turns the other way round: no bank conflicts
+                const int piece = 4 * ((c >> 2) & 1) + (x ^ (2 * half));
+                *reinterpret_cast<uint32_t*>(to + ((piece ^ (row & 7)) << 4)) = half ? e[x ^ 2] : e[x];
+            }
         }
-        factor = d2 == 0.f ? 0.f : sc * sqrtf(r2 / d2);
     }
-    if (store) {
-        #pragma unroll
-        for (int c = 0; c < 16; ++c)
-            put16(op + (c >> 3) * kOpBytes, r, c & 7, w[c >> 3][4 * (c & 7)], w[c >> 3][4 * (c & 7) + 1], w[c >> 3][4 * (c & 7) + 2],
-                  w[c >> 3][4 * (c & 7) + 3]);
-        fence_proxy_async_shared();
-    }
+    fence_proxy_async_shared();
     return factor;
 }
 
 template <int KIND>
 __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& p, int w, int tid, int lane) {
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
+    constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t tmem = s.tmem + lanes;
     const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 64, col_o = tmem + kColO + w * 128;
     // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
@@ -1008,16 +998,15 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         const int mine = g.two ? n : (n + 1 - w) / 2;   // tiles of this warpgroup
         const int row = g.two ? w * kWgRows + tid : tid;
         const bool live = row < g.rows;
-        const int token = g.tok0 + row / p.g, head = g.h * p.g + row % p.g;
-        const int64_t out_row = (static_cast<int64_t>(g.s0) + token) * p.n_q + head;
+        const int token = g.tok0 + row / p.g;
+        const int64_t first_row = (static_cast<int64_t>(g.s0) + g.tok0) * p.n_q;   // row of q and out; rel: the thread's from there
+        const int rel = live ? row / p.g * p.n_q + g.h * p.g + row % p.g : -1;
         const int pos = g.len < 0 ? -1 : g.len - g.T + token;
         if (merge_pending) {   // WG 0 has read the last unit's O and sums of this warpgroup
             if (!wait_bar(s, &s.merge_empty, ones - 1)) return;
             merge_pending = false;
         }
-        float rs = load_query<KIND>(p, p.q + (live ? out_row : 0) * kDh,
-                                    live && (g.two || w == 0 || KIND == kKindAngle), g.two || w == 0, flip, s.q[g.two ? w : 0],
-                                    tid) * scale;
+        float rs = load_query<KIND>(p.q + first_row * kDh, rel, g.two || w == 0, flip, s.q[g.two ? w : 0], tid >> 5, lane) * scale;
         rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
         __syncwarp();
         if (lane == 0) {
@@ -1025,17 +1014,16 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (!g.two && w == 0 && n > 1) mbar_arrive(&s.q_one);
         }
         float m = -INFINITY, l = 0.f;
-        int flagged = 0;
-        unsigned long long flag_mask[8];
-        int flag_tile[8];
+        unsigned flagged = 0;                     // tiles with noted V, from the first token's
+        const int tile0 = max(g.first, 0) / kTile;
         for (int i = 0; i < mine; ++i) {
             const uint32_t k = base + (g.two ? i : 2 * i + w);
-            const int in = k % kInfos;
+            const int in = k % Smem<KIND>::kInfos;
             const int t = g.t0 + (g.two ? i : 2 * i + w);
             const uint32_t turn = i >> 1;   // earlier uses of P's buffer i & 1 in the segment
             // S(i) is there; so are the tile's mask and factors (k_full), and PV(i−2) is done, which leaves P(i)'s
             // buffer free.  A barrier per buffer: no phase can pass unseen.
-            if (!wait_three(s, &s.s_full[w], done + i, &s.k_full[k % kKStages], k / kKStages, &s.pv_done[w][i & 1],
+            if (!wait_three(s, &s.s_full[w], done + i, &s.k_full[k % kStages], k / kStages, &s.pv_done[w][i & 1],
                             (i & 1 ? used1 : used0) + turn - 1, i >= 2))
                 return;
             tcgen_fence_after();
@@ -1047,7 +1035,11 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             tmem_wait_ld(raw[1]);
             tcgen_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.s_taken[w]);
+            if (lane == 0) {   // the K stage has been read by all that read it after eight arrivals
+                mbar_arrive(&s.s_taken[w]);
+                mbar_arrive(&s.k_empty[k % kStages]);
+                if (!g.two) mbar_arrive(&s.k_empty[k % kStages]);
+            }
             float x[kTile];
             #pragma unroll
             for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
@@ -1062,7 +1054,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 }
             }
             const int t_end = t * kTile + kTile - 1;
-            if (may != ~0ull || t_end > g.first) {
+            if (t_end > g.first) {
                 const int left = pos - t * kTile;   // the row attends places 0 .. left
                 if (left < kTile - 1) may &= left < 0 ? 0ull : (2ull << left) - 1ull;
                 const uint32_t lo = static_cast<uint32_t>(may), hi = static_cast<uint32_t>(may >> 32);
@@ -1070,6 +1062,15 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 for (int c = 0; c < kTile; ++c) {
                     const int at = place_of(c);
                     if (!((at < 32 ? lo >> at : hi >> (at - 32)) & 1u)) x[c] = -INFINITY;
+                }
+            } else if (may != ~0ull) {   // whatever a masked slot holds, the minimum with −inf is −inf
+                #pragma unroll
+                for (int c = 0; c < kTile; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&s.info[in].limit[c]);
+                    x[c] = fminf(x[c], f.x);
+                    x[c + 1] = fminf(x[c + 1], f.y);
+                    x[c + 2] = fminf(x[c + 2], f.z);
+                    x[c + 3] = fminf(x[c + 3], f.w);
                 }
             }
             float top = max3(x[0], x[1], x[2]), top2 = max3(x[3], x[4], x[5]);
@@ -1090,20 +1091,20 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 l *= f;
                 if (i > 0) {
                     #pragma unroll 1
-                    for (int c = 0; c < kDh; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(col_o + c, o);
+                    for (int c = 0; c < kDh; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(col_o + c, o);
                         tmem_wait_ld(o);
                         #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(col_o + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(col_o + c, o);
                     }
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 rs2 = make_float2(rs, rs), ref2 = make_float2(-ref, -ref);
-            uint32_t pw[32];
+            uint32_t pw[16];   // in two halves: fewer registers
             #pragma unroll
             for (int c = 0; c < kTile; c += 4) {
                 #pragma unroll
@@ -1120,19 +1121,21 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     x[c + 2] *= f.z;
                     x[c + 3] *= f.w;
                 }
-                pw[c / 2] = pack_bf16(x[c], x[c + 1]);
-                pw[c / 2 + 1] = pack_bf16(x[c + 2], x[c + 3]);
+                pw[(c / 2) & 15] = pack_bf16(x[c], x[c + 1]);
+                pw[((c / 2) & 15) + 1] = pack_bf16(x[c + 2], x[c + 3]);
+                if ((c & 31) == 28) tmem_st16(col_p + (i & 1) * 32 + (c >> 5) * 16, pw);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_st32(col_p + (i & 1) * 32, pw);
             tmem_wait_st();
             if (t_end > g.first) {   // non-finite V that only some rows attend (v_full: the repack has looked)
-                if (!wait_bar(s, &s.v_full[k % kVStages], k / kVStages)) return;
+                // once the tile before it in its stage has been read (this warpgroup may be ahead of both by then)
+                if (i > 0 && !wait_bar(s, &s.pv_done[w][(i - 1) & 1], ((i - 1) & 1 ? used1 : used0) + ((i - 1) >> 1))) return;
+                if (!wait_bar(s, &s.v_full[k % kStages], k / kStages)) return;
                 const unsigned long long* nf = s.info[in].nonfin;
                 const unsigned long long bad = nf[0] | nf[1] | nf[2] | nf[3];
-                if (bad && flagged < 8) {
-                    flag_mask[flagged] = bad;
-                    flag_tile[flagged++] = t;
+                if (bad) {
+                    flagged |= 1u << (t - tile0);
+                    if (lane == 0) s.flags[threadIdx.x >> 5][t - tile0] = bad;
                 }
             }
             tcgen_fence_before();
@@ -1158,7 +1161,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         if (merging) {
             if (w == 1) {
                 // non-finite values noted by this warpgroup are added to its own O below
-                for (int e = 0; e < flagged; ++e) {
+                for (unsigned e = flagged; e; e &= e - 1) {
+                    const int tile = __ffs(e) - 1;
                     #pragma unroll 1
                     for (int c = 0; c < kDh; c += 32) {
                         uint32_t o[32];
@@ -1166,8 +1170,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                         tmem_wait_ld(o);
                         #pragma unroll
                         for (int d = 0; d < 32; ++d) {
-                            for (unsigned long long bits = flag_mask[e]; bits; bits &= bits - 1) {
-                                const int at = flag_tile[e] * kTile + place_of(__ffsll(bits) - 1);
+                            for (unsigned long long bits = s.flags[threadIdx.x >> 5][tile]; bits; bits &= bits - 1) {
+                                const int at = (tile0 + tile) * kTile + place_of(__ffsll(bits) - 1);
                                 if (!live || at > pos) continue;
                                 const float v = pool_value<KIND>(p, g.b, g.h, at, c + d);
                                 if (!isfinite(v)) o[d] = __float_as_uint(__uint_as_float(o[d]) + v);
@@ -1208,6 +1212,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         const bool whole = g.t0 == 0 && g.t1 == g.tiles;
         const int slot = 2 * blockIdx.x + (seg_index > 0);
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint8_t* stage = s.q[g.two ? w : 0];
         #pragma unroll 1
         for (int c = 0; c < kDh; c += 32) {
             uint32_t o[32];
@@ -1222,9 +1227,10 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 #pragma unroll
                 for (int d = 0; d < 32; ++d) y[d] = y[d] * f0 + __uint_as_float(o[d]) * f1;
             }
-            for (int e = 0; e < flagged; ++e) {
-                for (unsigned long long bits = flag_mask[e]; bits; bits &= bits - 1) {
-                    const int at = flag_tile[e] * kTile + place_of(__ffsll(bits) - 1);
+            for (unsigned e = flagged; e; e &= e - 1) {
+                const int tile = __ffs(e) - 1;
+                for (unsigned long long bits = s.flags[threadIdx.x >> 5][tile]; bits; bits &= bits - 1) {
+                    const int at = (tile0 + tile) * kTile + place_of(__ffsll(bits) - 1);
                     if (!live || at > pos) continue;
                     #pragma unroll
                     for (int d = 0; d < 32; ++d) {
@@ -1234,21 +1240,38 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 }
             }
             __syncwarp();
-            if (!live) continue;
             if (!whole) {
                 float* part = p.part + static_cast<int64_t>(slot) * kDh * kUnitRows + row;
                 #pragma unroll
-                for (int d = 0; d < 32; ++d) part[(c + d) * kUnitRows] = y[d];
-            } else if (p.out_f32) {
-                float4* o4 = reinterpret_cast<float4*>(static_cast<float*>(p.out) + out_row * kDh + c);
-                #pragma unroll
-                for (int d = 0; d < 32; d += 4) o4[d / 4] = make_float4(y[d] * inv, y[d + 1] * inv, y[d + 2] * inv, y[d + 3] * inv);
-            } else {
-                uint4* o8 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * kDh + c);
-                #pragma unroll
-                for (int d = 0; d < 32; d += 8)
-                    o8[d / 8] = make_uint4(pack_bf16(y[d] * inv, y[d + 1] * inv), pack_bf16(y[d + 2] * inv, y[d + 3] * inv),
-                                           pack_bf16(y[d + 4] * inv, y[d + 5] * inv), pack_bf16(y[d + 6] * inv, y[d + 7] * inv));
+                for (int d = 0; d < 32; ++d)
+                    if (live) part[(c + d) * kUnitRows] = y[d];
+                continue;
+            }
+            // rows through shared memory (Q's, which no MMA reads any more; the warp's own rows): whole lines out
+            #pragma unroll
+            for (int d = 0; d < 32; d += 8) {
+                if (p.out_f32) {
+                    put16(stage + ((c >> 5) & 1) * kOpBytes, tid, d / 4, __float_as_uint(y[d] * inv), __float_as_uint(y[d + 1] * inv),
+                          __float_as_uint(y[d + 2] * inv), __float_as_uint(y[d + 3] * inv));
+                    put16(stage + ((c >> 5) & 1) * kOpBytes, tid, d / 4 + 1, __float_as_uint(y[d + 4] * inv),
+                          __float_as_uint(y[d + 5] * inv), __float_as_uint(y[d + 6] * inv), __float_as_uint(y[d + 7] * inv));
+                } else {
+                    put16(stage + (c >> 6) * kOpBytes, tid, (c & 32) / 8 + d / 8, pack_bf16(y[d] * inv, y[d + 1] * inv),
+                          pack_bf16(y[d + 2] * inv, y[d + 3] * inv), pack_bf16(y[d + 4] * inv, y[d + 5] * inv),
+                          pack_bf16(y[d + 6] * inv, y[d + 7] * inv));
+                }
+            }
+            if (c == 96 || (p.out_f32 && c == 32)) {   // 256 bytes of each row are there
+                __syncwarp();
+                uint8_t* out = static_cast<uint8_t*>(p.out) + (first_row * kDh + (p.out_f32 && c == 96 ? 64 : 0)) * (p.out_f32 ? 4 : 2);
+                const int64_t pitch = kDh * (p.out_f32 ? 4 : 2);
+                #pragma unroll 4
+                for (int e = 0; e < 16; ++e) {
+                    const int src = 2 * e + (lane >> 4), at = __shfl_sync(kFull, rel, src), r = (tid & ~31) + src, piece = lane & 7;
+                    const uint4 v = ld16(stage + ((lane >> 3) & 1) * kOpBytes + r * 128 + ((piece ^ (r & 7)) << 4));
+                    if (at >= 0) *reinterpret_cast<uint4*>(out + at * pitch + (lane & 15) * 16) = v;
+                }
+                __syncwarp();
             }
         }
         if (live) {
@@ -1256,7 +1279,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 p.part_ml[static_cast<int64_t>(slot) * 2 * kUnitRows + row] = m;
                 p.part_ml[static_cast<int64_t>(slot) * 2 * kUnitRows + kUnitRows + row] = l;
             } else if (p.lse_out) {
-                p.lse_out[out_row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+                p.lse_out[first_row + rel] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             }
         }
         if (tid == 0 && w == 0 && !whole) p.part_seg[slot] = make_int4(g.b, g.h | g.qt << 16, g.t0, g.t1);
@@ -1276,19 +1299,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == kOutWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
-        for (int i = 0; i < raw_k_tiles(KIND); ++i) {
-            mbar_init(&s.rk_full[i], 1);
-            mbar_init(&s.rk_empty[i], 4);
+        for (int i = 0; i < Smem<KIND>::kRaw; ++i) {
+            mbar_init(&s.raw_full[i], 1);
+            mbar_init(&s.raw_empty[i], 8);
         }
-        for (int i = 0; i < raw_v_tiles(KIND); ++i) {
-            mbar_init(&s.rv_full[i], 1);
-            mbar_init(&s.rv_empty[i], 4);
-        }
-        for (int i = 0; i < kKStages; ++i) {
+        for (int i = 0; i < Smem<KIND>::kStages; ++i) {
             mbar_init(&s.k_full[i], 4);
-            mbar_init(&s.k_empty[i], 2);
-        }
-        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&s.k_empty[i], 8);
             mbar_init(&s.v_full[i], 4);
             mbar_init(&s.v_empty[i], 2);
         }
@@ -1318,14 +1335,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     tcgen_fence_after();
     // one copy of each role's code: with one per warpgroup the loops outgrow the instruction cache
     // (its misses took 90% of the next level's rate, and every role ran at half speed)
-    // Registers: 512 threads at 128 take the whole file; 2·128·168 + 2·128·88 = 512·128.
+    // Registers: the launch has 640·96 of them; 2·128·152 + 128·(48 + 72 + 56) = 61,440 (8-bit: 56 + 64 + 56).
     if (warp < 8) {
-        take_registers<168>();
+        take_registers<152>();
         softmax_group<KIND>(s, p, warp >> 2, tid & 127, lane);
+    } else if (warp < kValueWarp) {
+        give_registers<is_wide(KIND) || is_lowbit(KIND) ? 48 : 56>();
+        key_repacker<KIND>(s, p, warp - kKeyWarp, lane);
+    } else if (warp < kProducerWarp) {
+        give_registers<is_wide(KIND) || is_lowbit(KIND) ? 72 : 64>();
+        value_repacker<KIND>(s, p, warp - kValueWarp, lane);
     } else {
-        give_registers<88>();
-        if (warp < kProducerWarp) repacker<KIND>(s, p, warp - kRepackWarp, lane);
-        else if (warp == kProducerWarp) producer<KIND>(s, p, lane);
+        give_registers<56>();
+        if (warp == kProducerWarp) producer<KIND>(s, p, lane);
         else if (warp < kOutWarp) score_issuer<KIND>(s, p, warp - kScoreWarp);
         else out_issuer<KIND>(s, p);
     }
@@ -1341,6 +1363,7 @@ template <int KIND>
 cudaError_t launch_kind(const ChunkParams& p, int grid, cudaStream_t stream) {
     const size_t smem = sizeof(Smem<KIND>) + 1024;
     static_assert(sizeof(Smem<KIND>) + 1024 <= 232448, "shared memory of one SM");
+    static_assert(max_record(KIND) % 16 == 0 && sizeof(TileInfo) % 16 == 0, "16-byte accesses");
     const cudaError_t e =
         cudaFuncSetAttribute(chunk_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
