@@ -56,7 +56,7 @@ constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kTries = 200000;         // tries of a wait: a second or so
-constexpr int kColS = 0, kColP = 128, kColO = 256;   // tensor memory columns: S 2 × 64, P 2 × 2 × 32, O 2 × 128
+constexpr int kColS = 0, kColP = 128, kColQ = 192, kColO = 256;   // tensor memory columns: S 2 × 64, P 2 × 32, Q 2 × 32, O 2 × 128
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
@@ -70,7 +70,7 @@ constexpr int max_record(int kind) {
 constexpr bool is_wide(int kind) { return kind == kKindBf16 || kind == kKindMixed; }
 // What fits beside Q: raw tiles, and operand stages of 16 KiB for K and for V.  A tile's masks and factors are
 // read until its warpgroup's next S is taken, in the worst case two tiles later: stages + 2 sets at least.
-constexpr int raw_tiles(int kind) { return kind == kKindMixed ? 2 : 3; }
+constexpr int raw_tiles(int kind) { return kind == kKindMixed ? 3 : 4; }
 constexpr int op_stages(int kind) { return is_wide(kind) ? 2 : 3; }
 constexpr int info_sets(int kind) { return is_wide(kind) ? 4 : 8; }
 
@@ -85,14 +85,14 @@ template <int KIND>
 struct Smem {
     static constexpr int kStages = op_stages(KIND), kRaw = raw_tiles(KIND), kInfos = info_sets(KIND);
     uint8_t k[kStages][kOpBytes], v[kStages][kOpBytes];         // operands; 1,024-byte aligned
-    uint8_t q[2][2 * kOpBytes];                                 // 128 rows each
+    uint8_t q[2][kOpBytes];                                     // dims 64 .. 127 of 128 rows each (the others: tensor memory)
     uint8_t raw[kRaw][4][max_record(KIND)];
     alignas(16) float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
     TileInfo info[kInfos];
     uint32_t word[kRaw][4];                                     // block words
     unsigned long long flags[8][kFlags];                        // by softmax warp: nonfin of the unit's last tiles
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[2], s_taken[2], p_full[2][2], pv_done[2][2];
+    uint64_t s_full[2], s_taken[2], p_full[2], pv_done[2];
     uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
     int64_t remaining;
     int b, h, qt, off;
@@ -668,18 +668,6 @@ __device__ __forceinline__ bool wait_two(Smem<KIND>& s, uint64_t* a, uint32_t pa
     s.abort = 1;   // reported at the kernel's end
     return false;
 }
-template <int KIND>
-__device__ __forceinline__ bool wait_three(Smem<KIND>& s, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c,
-                                           uint32_t pc, bool third) {
-    #pragma unroll 1
-    for (int i = 0; i < kTries; ++i) {
-        const bool x = mbar_try_wait(a, pa & 1u), y = mbar_try_wait(b, pb & 1u);
-        const bool z = !third || mbar_try_wait(c, pc & 1u);
-        if (__all_sync(kFull, x && y && z)) return true;
-    }
-    s.abort = 1;
-    return false;
-}
 
 template <int KIND>
 __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, int lane) {
@@ -840,7 +828,7 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
         const uint32_t mine = two ? n : (n + 1 - W) / 2, stride = two ? 1 : 2;
         if (mine > 0) ok = two || W == 0 ? wait_bar(s, &s.q_ready[W], own++) : wait_bar(s, &s.q_one, ones++);
         const uint32_t k0 = base + (two ? 0 : W);
-        const uint32_t a = uniform(q_op + (two ? W : 0) * 2 * kOpBytes);
+        const uint32_t a = uniform(q_op + (two ? W : 0) * kOpBytes), a0 = uniform(s.tmem + kColQ + (two ? W : 0) * 32);
         #pragma unroll 1
         for (uint32_t i = 0; ok && i < mine; ++i, ++step) {
             const uint32_t k = k0 + i * stride, st = k % kStages;
@@ -850,9 +838,10 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
             const uint32_t b = uniform(k_op + st * kOpBytes);
             if (elect_one()) {
                 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_ss(col_s, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
-                           smem_desc_sw128(b + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
+                for (int ks = 0; ks < 4; ++ks) mma_ts(col_s, a0 + ks * 8, smem_desc_sw128(b + ks * 32), kDescS, ks > 0);
+                #pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ss(col_s, smem_desc_sw128(a + ks * 32), smem_desc_sw128(b + 8192 + ks * 32), kDescS, 1u);
                 mma_commit(&s.s_full[W]);
             }
             __syncwarp();
@@ -875,36 +864,33 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
     const uint32_t tmem = uniform(s.tmem), v_op = uniform(smem_u32(s.v));
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, uses[2][2] = {{0, 0}, {0, 0}};   // tiles before the segment; uses of P's buffers before it
+    uint32_t base = 0, done0 = 0, done1 = 0;   // tiles before the segment, of both and of each warpgroup
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
         const uint32_t mine0 = two ? n : (n + 1) / 2, mine1 = two ? n : n / 2;
         #pragma unroll 1
         for (uint32_t j = 0; ok && j < 2 * mine0; ++j) {
-            const uint32_t W = j & 1u, i = j >> 1, buf = i & 1u;
+            const uint32_t W = j & 1u, i = j >> 1;
             if (W && i >= mine1) continue;
             const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages;
-            const uint32_t used = W ? (buf ? uses[1][1] : uses[1][0]) : (buf ? uses[0][1] : uses[0][0]);
-            ok = wait_two(s, &s.p_full[W][buf], used + (i >> 1), &s.v_full[st], k / kStages);
+            ok = wait_two(s, &s.p_full[W], (W ? done1 : done0) + i, &s.v_full[st], k / kStages);
             if (!ok) break;
             tcgen_fence_after();
-            const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColP + W * 64 + buf * 32);
+            const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColP + W * 32);
             const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
             if (elect_one()) {
                 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
-                mma_commit(&s.pv_done[W][buf]);
+                mma_commit(&s.pv_done[W]);
                 mma_commit(&s.v_empty[st]);
                 if (!two) mbar_arrive(&s.v_empty[st]);
             }
             __syncwarp();
         }
         base += n;
-        uses[0][0] += (mine0 + 1) / 2;
-        uses[0][1] += mine0 / 2;
-        uses[1][0] += (mine1 + 1) / 2;
-        uses[1][1] += mine1 / 2;
+        done0 += mine0;
+        done1 += mine1;
     }
     if (!ok) {
         if (elect_one()) mma_commit(&s.drain[2]);
@@ -913,68 +899,90 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
     }
 }
 
-// A warp's 32 rows of q into the A operand, in the dim order of the K operand; base: the unit's first token; rel: the
-// lane's row counted from there, −1 for none.  Half a warp reads a row, two a load: dims 8c .. 8c+7 are words c & 3 of
-// four pieces.  Returns what multiplies the row's logits (angle keys; 1 else).
+// A warp's 32 rows of q as the A operand, in the dim order of the K operand: dims 0 .. 63 to tensor memory (column col),
+// 64 .. 127 to shared memory (op).  base: the unit's first token; rel: the lane's row counted from there, −1 for none.
+// Eight lanes read half a row: dims 8c .. 8c+7 are words c & 3 of four 16-byte pieces.  Returns what multiplies the row's
+// logits (angle keys; 1 else).
 template <int KIND>
-__device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool store, bool flip, uint8_t* op, int warp, int lane) {
-    const int c = lane & 15, half = c >> 3;
+__device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool store, bool flip, uint8_t* op, uint32_t col, int warp,
+                                            int lane) {
     float factor = 1.f;
     if (!store && KIND != kKindAngle) return factor;
-    #pragma unroll 1
-    for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint4 v[8];
+    const int c = lane & 7;
+    uint32_t e[2][8][4];
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = __shfl_sync(kFull, rel, 4 * i + (lane >> 3));
         #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = __shfl_sync(kFull, rel, 2 * (i0 + i) + (lane >> 4));
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (at >= 0) v[i] = ld16(reinterpret_cast<const uint8_t*>(base + static_cast<int64_t>(at) * kDh + 8 * c));
+        for (int half = 0; half < 2; ++half) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (at >= 0) v = ld16(reinterpret_cast<const uint8_t*>(base + static_cast<int64_t>(at) * kDh + 64 * half + 8 * c));
+            e[half][i][0] = flip ? v.x ^ 0x80008000u : v.x;
+            e[half][i][1] = flip ? v.y ^ 0x80008000u : v.y;
+            e[half][i][2] = flip ? v.z ^ 0x80008000u : v.z;
+            e[half][i][3] = flip ? v.w ^ 0x80008000u : v.w;
         }
+    }
+    if constexpr (KIND == kKindAngle) {   // the E4M3 code of the row at its absmax scale, ||q||/||d_q||
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float top = 0.f;
             #pragma unroll
-            for (int x = 0; x < 4; ++x) e[x] = flip ? e[x] ^ 0x80008000u : e[x];
-            if constexpr (KIND == kKindAngle) {   // the E4M3 code of the row at its absmax scale, ||q||/||d_q||
-                float top = 0.f;
-                #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 f = unpack_bf16(e[x]);
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-                #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-                const float sc = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
-                float r2 = 0.f, d2 = 0.f;
-                #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 f = unpack_bf16(e[x]);
-                    const float a = __fdiv_rn(f.x, sc), b = __fdiv_rn(f.y, sc);
-                    const float da = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
-                    const float db = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
-                    r2 += a * a + b * b;
-                    d2 += da * da + db * db;
-                    e[x] = pack_bf16(da, db);
-                }
-                #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) {
-                    r2 += __shfl_xor_sync(kFull, r2, o);
-                    d2 += __shfl_xor_sync(kFull, d2, o);
-                }
-                const float f = __shfl_sync(kFull, d2 == 0.f ? 0.f : sc * sqrtf(r2 / d2), (lane & 1) << 4);
-                if ((lane >> 1) == i0 + i) factor = f;
+            for (int x = 0; x < 8; ++x) {
+                const float2 f = unpack_bf16(e[x >> 2][i][x & 3]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-            if (!store) continue;
-            const int row = 32 * warp + 2 * (i0 + i) + (lane >> 4);
-            uint8_t* to = op + half * kOpBytes + row * 128 + (c & 3) * 4;
             #pragma unroll
-            for (int x = 0; x < 4; ++x) {   // the halves take turns the other way round: no bank conflicts
-                const int piece = 4 * ((c >> 2) & 1) + (x ^ (2 * half));
-                *reinterpret_cast<uint32_t*>(to + ((piece ^ (row & 7)) << 4)) = half ? e[x ^ 2] : e[x];
+            for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            const float sc = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+            float r2 = 0.f, d2 = 0.f;
+            #pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float2 f = unpack_bf16(e[x >> 2][i][x & 3]);
+                const float a = __fdiv_rn(f.x, sc), b = __fdiv_rn(f.y, sc);
+                const float da = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+                const float db = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+                r2 += a * a + b * b;
+                d2 += da * da + db * db;
+                e[x >> 2][i][x & 3] = pack_bf16(da, db);
             }
+            #pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                r2 += __shfl_xor_sync(kFull, r2, o);
+                d2 += __shfl_xor_sync(kFull, d2, o);
+            }
+            const float f = __shfl_sync(kFull, d2 == 0.f ? 0.f : sc * sqrtf(r2 / d2), (lane & 3) << 3);
+            if ((lane >> 2) == i) factor = f;
+        }
+        if (!store) return factor;
+    }
+    #pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = 32 * warp + 4 * i + (lane >> 3);
+            #pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint32_t*>(op + row * 128 + (((4 * (c >> 2) + x) ^ (row & 7)) << 4) + (c & 3) * 4) = e[half][i][x];
+        }
+        if (half == 0) {   // each thread its own row
+            __syncwarp();
+            uint32_t w[32];
+            #pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint4 v = ld16(op + (32 * warp + lane) * 128 + ((x ^ (lane & 7)) << 4));
+                w[4 * x] = v.x;
+                w[4 * x + 1] = v.y;
+                w[4 * x + 2] = v.z;
+                w[4 * x + 3] = v.w;
+            }
+            tmem_st32(col, w);
+            __syncwarp();
         }
     }
     fence_proxy_async_shared();
+    tmem_wait_st();
+    tcgen_fence_before();
     return factor;
 }
 
@@ -983,14 +991,13 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
     constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t tmem = s.tmem + lanes;
-    const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 64, col_o = tmem + kColO + w * 128;
+    const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 32, col_o = tmem + kColO + w * 128;
     // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
     const bool flip = p.scale_log2 < 0.f;
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     Walk walk(p, s);
     Segment g;
     uint32_t base = 0, done = 0, ones = 0;   // tiles before the segment, of both and of this warpgroup; segments of one row group
-    uint32_t used0 = 0, used1 = 0;           // uses of P's buffers before the segment
     bool merge_pending = false;
     int seg_index = 0;
     while (walk.next(p, g)) {
@@ -1006,7 +1013,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (!wait_bar(s, &s.merge_empty, ones - 1)) return;
             merge_pending = false;
         }
-        float rs = load_query<KIND>(p.q + first_row * kDh, rel, g.two || w == 0, flip, s.q[g.two ? w : 0], tid >> 5, lane) * scale;
+        float rs = load_query<KIND>(p.q + first_row * kDh, rel, g.two || w == 0, flip, s.q[g.two ? w : 0], tmem + kColQ + (g.two ? w : 0) * 32,
+                                    tid >> 5, lane) * scale;
         rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
         __syncwarp();
         if (lane == 0) {
@@ -1020,12 +1028,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             const uint32_t k = base + (g.two ? i : 2 * i + w);
             const int in = k % Smem<KIND>::kInfos;
             const int t = g.t0 + (g.two ? i : 2 * i + w);
-            const uint32_t turn = i >> 1;   // earlier uses of P's buffer i & 1 in the segment
-            // S(i) is there; so are the tile's mask and factors (k_full), and PV(i−2) is done, which leaves P(i)'s
-            // buffer free.  A barrier per buffer: no phase can pass unseen.
-            if (!wait_three(s, &s.s_full[w], done + i, &s.k_full[k % kStages], k / kStages, &s.pv_done[w][i & 1],
-                            (i & 1 ? used1 : used0) + turn - 1, i >= 2))
-                return;
+            if (!wait_bar(s, &s.s_full[w], done + i)) return;   // S(i), and with it the tile's mask and factors
             tcgen_fence_after();
             uint32_t raw[2][32];
             tmem_ld32(col_s, raw[0]);
@@ -1035,11 +1038,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             tmem_wait_ld(raw[1]);
             tcgen_fence_before();
             __syncwarp();
-            if (lane == 0) {   // the K stage has been read by all that read it after eight arrivals
-                mbar_arrive(&s.s_taken[w]);
-                mbar_arrive(&s.k_empty[k % kStages]);
-                if (!g.two) mbar_arrive(&s.k_empty[k % kStages]);
-            }
+            // the K stage has been read by all that read it after eight arrivals: one a warp, two where a tile has one warpgroup
+            if (lane < (g.two ? 2 : 3)) mbar_arrive(lane == 0 ? &s.s_taken[w] : &s.k_empty[k % kStages]);
             float x[kTile];
             #pragma unroll
             for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
@@ -1082,7 +1082,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             top = fmaxf(max3(top, x[kTile - 2], x[kTile - 1]), top2) * rs;
             if (__any_sync(kFull, top > m + kLazy)) {
                 if (i > 0) {   // O of the tiles before is complete
-                    if (!wait_bar(s, &s.pv_done[w][(i - 1) & 1], ((i - 1) & 1 ? used1 : used0) + ((i - 1) >> 1))) return;
+                    if (!wait_bar(s, &s.pv_done[w], done + i - 1)) return;
                     tcgen_fence_after();
                 }
                 const float nm = fmaxf(m, top);
@@ -1123,13 +1123,15 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 }
                 pw[(c / 2) & 15] = pack_bf16(x[c], x[c + 1]);
                 pw[((c / 2) & 15) + 1] = pack_bf16(x[c + 2], x[c + 3]);
-                if ((c & 31) == 28) tmem_st16(col_p + (i & 1) * 32 + (c >> 5) * 16, pw);
+                if ((c & 31) == 28) {
+                    if (c == 28 && i > 0 && !wait_bar(s, &s.pv_done[w], done + i - 1)) return;   // P(i−1) has been read
+                    tmem_st16(col_p + (c >> 5) * 16, pw);
+                }
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
             if (t_end > g.first) {   // non-finite V that only some rows attend (v_full: the repack has looked)
-                // once the tile before it in its stage has been read (this warpgroup may be ahead of both by then)
-                if (i > 0 && !wait_bar(s, &s.pv_done[w][(i - 1) & 1], ((i - 1) & 1 ? used1 : used0) + ((i - 1) >> 1))) return;
+                // (PV(i−1) is done, so the tile before it in its stage has been read: no phase can be mistaken)
                 if (!wait_bar(s, &s.v_full[k % kStages], k / kStages)) return;
                 const unsigned long long* nf = s.info[in].nonfin;
                 const unsigned long long bad = nf[0] | nf[1] | nf[2] | nf[3];
@@ -1140,15 +1142,12 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             }
             tcgen_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_full[w][i & 1]);
+            if (lane == 0) mbar_arrive(&s.p_full[w]);
         }
         if (mine > 0) {
-            if (mine >= 2 && !wait_bar(s, &s.pv_done[w][mine & 1], (mine & 1 ? used1 : used0) + ((mine - 2) >> 1))) return;
-            if (!wait_bar(s, &s.pv_done[w][(mine - 1) & 1], ((mine - 1) & 1 ? used1 : used0) + ((mine - 1) >> 1))) return;
+            if (!wait_bar(s, &s.pv_done[w], done + mine - 1)) return;
             tcgen_fence_after();
             done += mine;
-            used0 += (mine + 1) >> 1;
-            used1 += mine >> 1;
         }
         base += n;
         const bool merging = !g.two && n > 1;   // both warpgroups hold a part of the rows
@@ -1251,25 +1250,25 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             #pragma unroll
             for (int d = 0; d < 32; d += 8) {
                 if (p.out_f32) {
-                    put16(stage + ((c >> 5) & 1) * kOpBytes, tid, d / 4, __float_as_uint(y[d] * inv), __float_as_uint(y[d + 1] * inv),
+                    put16(stage, tid, d / 4, __float_as_uint(y[d] * inv), __float_as_uint(y[d + 1] * inv),
                           __float_as_uint(y[d + 2] * inv), __float_as_uint(y[d + 3] * inv));
-                    put16(stage + ((c >> 5) & 1) * kOpBytes, tid, d / 4 + 1, __float_as_uint(y[d + 4] * inv),
-                          __float_as_uint(y[d + 5] * inv), __float_as_uint(y[d + 6] * inv), __float_as_uint(y[d + 7] * inv));
+                    put16(stage, tid, d / 4 + 1, __float_as_uint(y[d + 4] * inv), __float_as_uint(y[d + 5] * inv),
+                          __float_as_uint(y[d + 6] * inv), __float_as_uint(y[d + 7] * inv));
                 } else {
-                    put16(stage + (c >> 6) * kOpBytes, tid, (c & 32) / 8 + d / 8, pack_bf16(y[d] * inv, y[d + 1] * inv),
+                    put16(stage, tid, (c & 32) / 8 + d / 8, pack_bf16(y[d] * inv, y[d + 1] * inv),
                           pack_bf16(y[d + 2] * inv, y[d + 3] * inv), pack_bf16(y[d + 4] * inv, y[d + 5] * inv),
                           pack_bf16(y[d + 6] * inv, y[d + 7] * inv));
                 }
             }
-            if (c == 96 || (p.out_f32 && c == 32)) {   // 256 bytes of each row are there
+            if (p.out_f32 || (c & 32)) {   // 128 bytes of each row are there
                 __syncwarp();
-                uint8_t* out = static_cast<uint8_t*>(p.out) + (first_row * kDh + (p.out_f32 && c == 96 ? 64 : 0)) * (p.out_f32 ? 4 : 2);
                 const int64_t pitch = kDh * (p.out_f32 ? 4 : 2);
-                #pragma unroll 4
-                for (int e = 0; e < 16; ++e) {
-                    const int src = 2 * e + (lane >> 4), at = __shfl_sync(kFull, rel, src), r = (tid & ~31) + src, piece = lane & 7;
-                    const uint4 v = ld16(stage + ((lane >> 3) & 1) * kOpBytes + r * 128 + ((piece ^ (r & 7)) << 4));
-                    if (at >= 0) *reinterpret_cast<uint4*>(out + at * pitch + (lane & 15) * 16) = v;
+                uint8_t* out = static_cast<uint8_t*>(p.out) + first_row * pitch + (p.out_f32 ? 4 * c : 2 * (c - 32)) + (lane & 7) * 16;
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int src = 4 * e + (lane >> 3), at = __shfl_sync(kFull, rel, src), row128 = (tid & ~31) + src;
+                    const uint4 v = ld16(stage + row128 * 128 + (((lane & 7) ^ (row128 & 7)) << 4));
+                    if (at >= 0) *reinterpret_cast<uint4*>(out + at * pitch) = v;
                 }
                 __syncwarp();
             }
@@ -1313,10 +1312,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
             mbar_init(&s.q_ready[i], 4);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.s_taken[i], 4);
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&s.p_full[i][b], 4);
-                mbar_init(&s.pv_done[i][b], 1);
-            }
+            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.pv_done[i], 1);
         }
         for (int i = 0; i < 3; ++i) mbar_init(&s.drain[i], 1);
         mbar_init(&s.q_one, 4);
