@@ -50,8 +50,8 @@ namespace chunk {
 constexpr int kTile = 64;              // positions per tile: four blocks
 constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
-constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, S 2 × 32, O 32
-constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kScoreWarp = 17, kOutWarp = 19;
+constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, S 32, O 2 × 32
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kScoreWarp = 17, kOutWarp = 18;
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -93,7 +93,7 @@ struct Smem {
     unsigned long long flags[8][kFlags];                        // by softmax warp: nonfin of the unit's last tiles
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2], s_taken[2], p_full[2], pv_done[2];
-    uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
+    uint64_t q_ready[2], merge_full, merge_empty, drain[3];
     int64_t remaining;
     int b, h, qt, off;
     uint32_t tmem;
@@ -811,80 +811,40 @@ __device__ __forceinline__ void value_repacker(Smem<KIND>& s, const ChunkParams&
     }
 }
 
-// S of warpgroup W, by one warp: S(i+1) = Q·K(i+1) once the warpgroup has S(i) in registers (which frees its K too).
+// S of both warpgroups, by one warp: S(i+1) = Q·K(i+1) once the warpgroup has S(i) in registers (which frees its K
+// too); W = 0, 1 in turn.
 template <int KIND>
-__device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
+__device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p) {
     constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile);
     constexpr int kStages = Smem<KIND>::kStages;
-    const uint32_t W = uniform(warpgroup);
-    const uint32_t col_s = uniform(s.tmem + kColS + W * 64);
-    const uint32_t k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
+    const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, step = 0, own = 0, ones = 0;   // tiles before the segment, of this warpgroup; phases of q_ready, q_one
-    bool ok = true;
-    while (ok && walk.next(p, g)) {
-        const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
-        const uint32_t mine = two ? n : (n + 1 - W) / 2, stride = two ? 1 : 2;
-        if (mine > 0) ok = two || W == 0 ? wait_bar(s, &s.q_ready[W], own++) : wait_bar(s, &s.q_one, ones++);
-        const uint32_t k0 = base + (two ? 0 : W);
-        const uint32_t a = uniform(q_op + (two ? W : 0) * kOpBytes), a0 = uniform(s.tmem + kColQ + (two ? W : 0) * 32);
-        #pragma unroll 1
-        for (uint32_t i = 0; ok && i < mine; ++i, ++step) {
-            const uint32_t k = k0 + i * stride, st = k % kStages;
-            ok = wait_two(s, &s.k_full[st], k / kStages, &s.s_taken[W], step - 1, step > 0);
-            if (!ok) break;
-            tcgen_fence_after();
-            const uint32_t b = uniform(k_op + st * kOpBytes);
-            if (elect_one()) {
-                #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ts(col_s, a0 + ks * 8, smem_desc_sw128(b + ks * 32), kDescS, ks > 0);
-                #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(col_s, smem_desc_sw128(a + ks * 32), smem_desc_sw128(b + 8192 + ks * 32), kDescS, 1u);
-                mma_commit(&s.s_full[W]);
-            }
-            __syncwarp();
-        }
-        base += n;
-    }
-    if (!ok) {   // what was issued completes before tensor memory is freed
-        if (elect_one()) mma_commit(&s.drain[W]);
-        __syncwarp();
-        mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
-    }
-}
-
-// O of both warpgroups, by one warp: O_W += P_W(i)·V(i) when P_W(i) is in tensor memory, W = 0, 1 in turn (the
-// shared K stages keep the warpgroups within a step of each other).
-template <int KIND>
-__device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) {
-    constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
-    constexpr int kStages = Smem<KIND>::kStages;
-    const uint32_t tmem = uniform(s.tmem), v_op = uniform(smem_u32(s.v));
-    Walk walk(p, s);
-    Segment g;
-    uint32_t base = 0, done0 = 0, done1 = 0;   // tiles before the segment, of both and of each warpgroup
+    uint32_t base = 0, done0 = 0, done1 = 0, own0 = 0, own1 = 0;   // tiles before the segment, of both and of each; phases of q_ready
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
         const uint32_t mine0 = two ? n : (n + 1) / 2, mine1 = two ? n : n / 2;
+        ok = wait_bar(s, &s.q_ready[0], own0++);
         #pragma unroll 1
         for (uint32_t j = 0; ok && j < 2 * mine0; ++j) {
             const uint32_t W = j & 1u, i = j >> 1;
             if (W && i >= mine1) continue;
-            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages;
-            ok = wait_two(s, &s.p_full[W], (W ? done1 : done0) + i, &s.v_full[st], k / kStages);
+            if (j == 1 && two) ok = wait_bar(s, &s.q_ready[1], own1++);
+            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages, step = (W ? done1 : done0) + i;
+            ok = ok && wait_two(s, &s.k_full[st], k / kStages, &s.s_taken[W], step - 1, step > 0);
             if (!ok) break;
             tcgen_fence_after();
-            const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColP + W * 32);
-            const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
+            const uint32_t x = two ? W : 0u;   // whose Q
+            const uint32_t d = uniform(tmem + kColS + W * 64), a0 = uniform(tmem + kColQ + x * 32);
+            const uint32_t a = uniform(q_op + x * kOpBytes), b = uniform(k_op + st * kOpBytes), bar = uniform(smem_u32(&s.s_full[W]));
             if (elect_one()) {
                 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
-                mma_commit(&s.pv_done[W]);
-                mma_commit(&s.v_empty[st]);
-                if (!two) mbar_arrive(&s.v_empty[st]);
+                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a0 + ks * 8, smem_desc_sw128(b + ks * 32), kDescS, ks > 0);
+                #pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ss(d, smem_desc_sw128(a + ks * 32), smem_desc_sw128(b + 8192 + ks * 32), kDescS, 1u);
+                mma_commit(bar);
             }
             __syncwarp();
         }
@@ -892,10 +852,51 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
         done0 += mine0;
         done1 += mine1;
     }
-    if (!ok) {
-        if (elect_one()) mma_commit(&s.drain[2]);
+    if (!ok) {   // what was issued completes before tensor memory is freed
+        if (elect_one()) mma_commit(smem_u32(&s.drain[0]));
         __syncwarp();
-        mbar_wait(&s.drain[2], 0, nullptr, kWaitNs);
+        mbar_wait(&s.drain[0], 0, nullptr, kWaitNs);
+    }
+}
+
+// O of a warpgroup, by one warp: O += P(i)·V(i) when P(i) is in tensor memory.
+template <int KIND>
+__device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
+    constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
+    constexpr int kStages = Smem<KIND>::kStages;
+    const uint32_t W = uniform(warpgroup);
+    const uint32_t d = uniform(s.tmem + kColO + W * 128), a = uniform(s.tmem + kColP + W * 32), v_op = uniform(smem_u32(s.v));
+    const uint32_t done_bar = uniform(smem_u32(&s.pv_done[W]));
+    Walk walk(p, s);
+    Segment g;
+    uint32_t base = 0, done = 0;   // tiles before the segment, of both and of this warpgroup
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
+        const uint32_t mine = two ? n : (n + 1 - W) / 2;
+        #pragma unroll 1
+        for (uint32_t i = 0; i < mine; ++i) {
+            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages;
+            ok = wait_two(s, &s.p_full[W], done + i, &s.v_full[st], k / kStages);
+            if (!ok) break;
+            tcgen_fence_after();
+            const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0), empty = uniform(smem_u32(&s.v_empty[st]));
+            if (elect_one()) {
+                #pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
+                mma_commit(done_bar);
+                mma_commit(empty);
+                if (!two) mbar_arrive(&s.v_empty[st]);
+            }
+            __syncwarp();
+        }
+        base += n;
+        done += mine;
+    }
+    if (!ok) {
+        if (elect_one()) mma_commit(smem_u32(&s.drain[1 + W]));
+        __syncwarp();
+        mbar_wait(&s.drain[1 + W], 0, nullptr, kWaitNs);
     }
 }
 
@@ -1017,10 +1018,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                                     tid >> 5, lane) * scale;
         rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
         __syncwarp();
-        if (lane == 0) {
-            if (g.two || w == 0) mbar_arrive(&s.q_ready[w]);
-            if (!g.two && w == 0 && n > 1) mbar_arrive(&s.q_one);
-        }
+        if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
         float m = -INFINITY, l = 0.f;
         unsigned flagged = 0;                     // tiles with noted V, from the first token's
         const int tile0 = max(g.first, 0) / kTile;
@@ -1047,10 +1045,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 #pragma unroll
                 for (int c = 0; c < kTile; c += 4) {
                     const float4 f = *reinterpret_cast<const float4*>(&s.factor[in][0][c]);
-                    x[c] *= f.x;
-                    x[c + 1] *= f.y;
-                    x[c + 2] *= f.z;
-                    x[c + 3] *= f.w;
+                    set2(&x[c], mul2(make_float2(x[c], x[c + 1]), make_float2(f.x, f.y)));
+                    set2(&x[c + 2], mul2(make_float2(x[c + 2], x[c + 3]), make_float2(f.z, f.w)));
                 }
             }
             const int t_end = t * kTile + kTile - 1;
@@ -1073,13 +1069,16 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     x[c + 3] = fminf(x[c + 3], f.w);
                 }
             }
-            float top = max3(x[0], x[1], x[2]), top2 = max3(x[3], x[4], x[5]);
+            float part[4];   // four chains
             #pragma unroll
-            for (int c = 6; c < kTile - 2; c += 4) {
-                top = max3(top, x[c], x[c + 1]);
-                top2 = max3(top2, x[c + 2], x[c + 3]);
-            }
-            top = fmaxf(max3(top, x[kTile - 2], x[kTile - 1]), top2) * rs;
+            for (int e = 0; e < 4; ++e) part[e] = max3(x[e], x[e + 4], x[e + 8]);
+            #pragma unroll
+            for (int c = 12; c < kTile - 4; c += 8)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) part[e] = max3(part[e], x[c + e], x[c + e + 4]);
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) part[e] = fmaxf(part[e], x[kTile - 4 + e]);
+            const float top = fmaxf(max3(part[0], part[1], part[2]), part[3]) * rs;
             if (__any_sync(kFull, top > m + kLazy)) {
                 if (i > 0) {   // O of the tiles before is complete
                     if (!wait_bar(s, &s.pv_done[w], done + i - 1)) return;
@@ -1116,10 +1115,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 }
                 if constexpr (has_factors(KIND)) {
                     const float4 f = *reinterpret_cast<const float4*>(&s.factor[in][1][c]);
-                    x[c] *= f.x;
-                    x[c + 1] *= f.y;
-                    x[c + 2] *= f.z;
-                    x[c + 3] *= f.w;
+                    set2(&x[c], mul2(make_float2(x[c], x[c + 1]), make_float2(f.x, f.y)));
+                    set2(&x[c + 2], mul2(make_float2(x[c + 2], x[c + 3]), make_float2(f.z, f.w)));
                 }
                 pw[(c / 2) & 15] = pack_bf16(x[c], x[c + 1]);
                 pw[((c / 2) & 15) + 1] = pack_bf16(x[c + 2], x[c + 3]);
@@ -1316,7 +1313,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
             mbar_init(&s.pv_done[i], 1);
         }
         for (int i = 0; i < 3; ++i) mbar_init(&s.drain[i], 1);
-        mbar_init(&s.q_one, 4);
         mbar_init(&s.merge_full, 4);
         mbar_init(&s.merge_empty, 4);
         mbar_fence_init();
@@ -1345,8 +1341,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     } else {
         give_registers<56>();
         if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-        else if (warp < kOutWarp) score_issuer<KIND>(s, p, warp - kScoreWarp);
-        else out_issuer<KIND>(s, p);
+        else if (warp == kScoreWarp) score_issuer<KIND>(s, p);
+        else out_issuer<KIND>(s, p, warp - kOutWarp);
     }
     __syncwarp();
     tcgen_fence_before();
