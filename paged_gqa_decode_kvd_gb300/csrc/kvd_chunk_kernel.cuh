@@ -50,13 +50,13 @@ namespace chunk {
 constexpr int kTile = 64;              // positions per tile: four blocks
 constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
-constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, S 32, O 2 × 32
-constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kScoreWarp = 17, kOutWarp = 18;
+constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, MMA 2 × 32, one warp idle
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kMmaWarp = 17;
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kTries = 200000;         // tries of a wait: a second or so
-constexpr int kColS = 0, kColP = 128, kColQ = 192, kColO = 256;   // tensor memory columns: S 2 × 64, P 2 × 32, Q 2 × 32, O 2 × 128
+constexpr int kColS = 0, kColO = 256;   // tensor memory columns: S and P 2 × 2 × 64, O 2 × 128
 constexpr int kMinTiles = 4;           // smallest share of a CTA
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
@@ -69,10 +69,11 @@ constexpr int max_record(int kind) {
 }
 constexpr bool is_wide(int kind) { return kind == kKindBf16 || kind == kKindMixed; }
 // What fits beside Q: raw tiles, and operand stages of 16 KiB for K and for V.  A tile's masks and factors are
-// read until its warpgroup's next S is taken, in the worst case two tiles later: stages + 2 sets at least.
-constexpr int raw_tiles(int kind) { return kind == kKindMixed ? 3 : 4; }
+// read until its P is there.  K may be as far ahead as the stages' tiles behind the other S that a warpgroup has
+// been given before: with a warpgroup on every second tile, four tiles and the stages.
+constexpr int raw_tiles(int kind) { return kind == kKindMixed ? 2 : 3; }
 constexpr int op_stages(int kind) { return is_wide(kind) ? 2 : 3; }
-constexpr int info_sets(int kind) { return is_wide(kind) ? 4 : 8; }
+constexpr int info_sets(int kind) { return is_wide(kind) ? 6 : 8; }
 
 struct TileInfo {
     alignas(16) float limit[kTile];   // column: −inf where the position may not be attended, else +inf
@@ -85,15 +86,15 @@ template <int KIND>
 struct Smem {
     static constexpr int kStages = op_stages(KIND), kRaw = raw_tiles(KIND), kInfos = info_sets(KIND);
     uint8_t k[kStages][kOpBytes], v[kStages][kOpBytes];         // operands; 1,024-byte aligned
-    uint8_t q[2][kOpBytes];                                     // dims 64 .. 127 of 128 rows each (the others: tensor memory)
+    uint8_t q[2][2 * kOpBytes];                                 // 128 rows each
     uint8_t raw[kRaw][4][max_record(KIND)];
     alignas(16) float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
     TileInfo info[kInfos];
     uint32_t word[kRaw][4];                                     // block words
     unsigned long long flags[8][kFlags];                        // by softmax warp: nonfin of the unit's last tiles
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[2], s_taken[2], p_full[2], pv_done[2];
-    uint64_t q_ready[2], merge_full, merge_empty, drain[3];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];         // [warpgroup][S and P buffer]
+    uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[2];
     int64_t remaining;
     int b, h, qt, off;
     uint32_t tmem;
@@ -811,102 +812,79 @@ __device__ __forceinline__ void value_repacker(Smem<KIND>& s, const ChunkParams&
     }
 }
 
-// S of both warpgroups, by one warp: S(i+1) = Q·K(i+1) once the warpgroup has S(i) in registers (which frees its K
-// too); W = 0, 1 in turn.
+// The MMAs of warpgroup W, by one warp: S(0), S(1), then O += P(i)·V(i) when P(i) is in tensor memory and S(i+2) = Q·K(i+2)
+// into the same columns: a warpgroup finds its next S ready when it is done with one.
 template <int KIND>
-__device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p) {
-    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile);
-    constexpr int kStages = Smem<KIND>::kStages;
-    const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
-    Walk walk(p, s);
-    Segment g;
-    uint32_t base = 0, done0 = 0, done1 = 0, own0 = 0, own1 = 0;   // tiles before the segment, of both and of each; phases of q_ready
-    bool ok = true;
-    while (ok && walk.next(p, g)) {
-        const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
-        const uint32_t mine0 = two ? n : (n + 1) / 2, mine1 = two ? n : n / 2;
-        ok = wait_bar(s, &s.q_ready[0], own0++);
-        #pragma unroll 1
-        for (uint32_t j = 0; ok && j < 2 * mine0; ++j) {
-            const uint32_t W = j & 1u, i = j >> 1;
-            if (W && i >= mine1) continue;
-            if (j == 1 && two) ok = wait_bar(s, &s.q_ready[1], own1++);
-            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages, step = (W ? done1 : done0) + i;
-            ok = ok && wait_two(s, &s.k_full[st], k / kStages, &s.s_taken[W], step - 1, step > 0);
-            if (!ok) break;
-            tcgen_fence_after();
-            const uint32_t x = two ? W : 0u;   // whose Q
-            const uint32_t d = uniform(tmem + kColS + W * 64), a0 = uniform(tmem + kColQ + x * 32);
-            const uint32_t a = uniform(q_op + x * kOpBytes), b = uniform(k_op + st * kOpBytes), bar = uniform(smem_u32(&s.s_full[W]));
-            if (elect_one()) {
-                #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a0 + ks * 8, smem_desc_sw128(b + ks * 32), kDescS, ks > 0);
-                #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(d, smem_desc_sw128(a + ks * 32), smem_desc_sw128(b + 8192 + ks * 32), kDescS, 1u);
-                mma_commit(bar);
-            }
-            __syncwarp();
-        }
-        base += n;
-        done0 += mine0;
-        done1 += mine1;
-    }
-    if (!ok) {   // what was issued completes before tensor memory is freed
-        if (elect_one()) mma_commit(smem_u32(&s.drain[0]));
-        __syncwarp();
-        mbar_wait(&s.drain[0], 0, nullptr, kWaitNs);
-    }
-}
-
-// O of a warpgroup, by one warp: O += P(i)·V(i) when P(i) is in tensor memory.
-template <int KIND>
-__device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
-    constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
+__device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
+    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
     constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t W = uniform(warpgroup);
-    const uint32_t d = uniform(s.tmem + kColO + W * 128), a = uniform(s.tmem + kColP + W * 32), v_op = uniform(smem_u32(s.v));
-    const uint32_t done_bar = uniform(smem_u32(&s.pv_done[W]));
+    const uint32_t col_s = uniform(s.tmem + kColS + W * 128), d = uniform(s.tmem + kColO + W * 128);
+    const uint32_t k_op = uniform(smem_u32(s.k)), v_op = uniform(smem_u32(s.v)), q_op = uniform(smem_u32(s.q));
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, done = 0;   // tiles before the segment, of both and of this warpgroup
+    uint32_t base = 0, done = 0, own = 0, ones = 0;   // tiles before the segment, of both and of this warpgroup; phases of q_ready, q_one
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
-        const uint32_t mine = two ? n : (n + 1 - W) / 2;
+        const int mine = two ? n : (n + 1 - W) / 2;
+        if (mine > 0) ok = two || W == 0 ? wait_bar(s, &s.q_ready[W], own++) : wait_bar(s, &s.q_one, ones++);
+        const uint32_t a = uniform(q_op + (two ? W : 0) * 2 * kOpBytes);
         #pragma unroll 1
-        for (uint32_t i = 0; i < mine; ++i) {
-            const uint32_t k = base + (two ? i : 2 * i + W), st = k % kStages;
-            ok = wait_two(s, &s.p_full[W], done + i, &s.v_full[st], k / kStages);
-            if (!ok) break;
-            tcgen_fence_after();
-            const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0), empty = uniform(smem_u32(&s.v_empty[st]));
-            if (elect_one()) {
-                #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
-                mma_commit(done_bar);
-                mma_commit(empty);
-                if (!two) mbar_arrive(&s.v_empty[st]);
+        for (int i = -2; ok && i < mine; ++i) {
+            const uint32_t x = done + i, buf = x & 1u, k = base + (two ? i : 2 * i + static_cast<int>(W));
+            const uint32_t cols = uniform(col_s + buf * 64);
+            if (i >= 0) {
+                const uint32_t st = k % kStages;
+                ok = wait_two(s, &s.p_full[W][buf], x >> 1, &s.v_full[st], k / kStages);
+                if (!ok) break;
+                tcgen_fence_after();
+                const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
+                const uint32_t full = uniform(smem_u32(&s.pv_done[W][buf])), empty = uniform(smem_u32(&s.v_empty[st]));
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) mma_ts(d, cols + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
+                    mma_commit(full);
+                    mma_commit(empty);
+                    if (!two) mbar_arrive(&s.v_empty[st]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (i + 2 < mine) {
+                const uint32_t k2 = k + (two ? 2 : 4), st = k2 % kStages;
+                ok = wait_bar(s, &s.k_full[st], k2 / kStages);
+                if (ok && i >= 0) ok = wait_bar(s, &s.pv_done[W][buf], x >> 1);   // P(i) has been read
+                if (!ok) break;
+                tcgen_fence_after();
+                const uint32_t b = uniform(k_op + st * kOpBytes);
+                const uint32_t full = uniform(smem_u32(&s.s_full[W][buf])), empty = uniform(smem_u32(&s.k_empty[st]));
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss(cols, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
+                               smem_desc_sw128(b + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
+                    mma_commit(full);
+                    mma_commit(empty);
+                    if (!two) mbar_arrive(&s.k_empty[st]);
+                }
+                __syncwarp();
+            }
         }
         base += n;
         done += mine;
     }
-    if (!ok) {
-        if (elect_one()) mma_commit(smem_u32(&s.drain[1 + W]));
+    if (!ok) {   // what was issued completes before tensor memory is freed
+        if (elect_one()) mma_commit(smem_u32(&s.drain[W]));
         __syncwarp();
-        mbar_wait(&s.drain[1 + W], 0, nullptr, kWaitNs);
+        mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
     }
 }
 
-// A warp's 32 rows of q as the A operand, in the dim order of the K operand: dims 0 .. 63 to tensor memory (column col),
-// 64 .. 127 to shared memory (op).  base: the unit's first token; rel: the lane's row counted from there, −1 for none.
-// Eight lanes read half a row: dims 8c .. 8c+7 are words c & 3 of four 16-byte pieces.  Returns what multiplies the row's
-// logits (angle keys; 1 else).
+// A warp's 32 rows of q as the A operand, in the dim order of the K operand.  base: the unit's first token; rel: the
+// lane's row counted from there, −1 for none.  Eight lanes read half a row: dims 8c .. 8c+7 are words c & 3 of four
+// 16-byte pieces.  Returns what multiplies the row's logits (angle keys; 1 else).
 template <int KIND>
-__device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool store, bool flip, uint8_t* op, uint32_t col, int warp,
-                                            int lane) {
+__device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool store, bool flip, uint8_t* op, int warp, int lane) {
     float factor = 1.f;
     if (!store && KIND != kKindAngle) return factor;
     const int c = lane & 7;
@@ -964,26 +942,10 @@ __device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool 
             const int row = 32 * warp + 4 * i + (lane >> 3);
             #pragma unroll
             for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint32_t*>(op + row * 128 + (((4 * (c >> 2) + x) ^ (row & 7)) << 4) + (c & 3) * 4) = e[half][i][x];
-        }
-        if (half == 0) {   // each thread its own row
-            __syncwarp();
-            uint32_t w[32];
-            #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const uint4 v = ld16(op + (32 * warp + lane) * 128 + ((x ^ (lane & 7)) << 4));
-                w[4 * x] = v.x;
-                w[4 * x + 1] = v.y;
-                w[4 * x + 2] = v.z;
-                w[4 * x + 3] = v.w;
-            }
-            tmem_st32(col, w);
-            __syncwarp();
+                *reinterpret_cast<uint32_t*>(op + half * kOpBytes + row * 128 + (((4 * (c >> 2) + x) ^ (row & 7)) << 4) + (c & 3) * 4) = e[half][i][x];
         }
     }
     fence_proxy_async_shared();
-    tmem_wait_st();
-    tcgen_fence_before();
     return factor;
 }
 
@@ -992,7 +954,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
     constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t tmem = s.tmem + lanes;
-    const uint32_t col_s = tmem + kColS + w * 64, col_p = tmem + kColP + w * 32, col_o = tmem + kColO + w * 128;
+    const uint32_t col_s = tmem + kColS + w * 128, col_o = tmem + kColO + w * 128;
     // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
     const bool flip = p.scale_log2 < 0.f;
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
@@ -1014,11 +976,13 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (!wait_bar(s, &s.merge_empty, ones - 1)) return;
             merge_pending = false;
         }
-        float rs = load_query<KIND>(p.q + first_row * kDh, rel, g.two || w == 0, flip, s.q[g.two ? w : 0], tmem + kColQ + (g.two ? w : 0) * 32,
-                                    tid >> 5, lane) * scale;
+        float rs = load_query<KIND>(p.q + first_row * kDh, rel, g.two || w == 0, flip, s.q[g.two ? w : 0], tid >> 5, lane) * scale;
         rs = fmaxf(rs, 1e-30f);   // a NaN or zero factor: the codes carry it
         __syncwarp();
-        if (lane == 0 && (g.two || w == 0)) mbar_arrive(&s.q_ready[w]);
+        if (lane == 0) {
+            if (g.two || w == 0) mbar_arrive(&s.q_ready[w]);
+            if (!g.two && w == 0 && n > 1) mbar_arrive(&s.q_one);
+        }
         float m = -INFINITY, l = 0.f;
         unsigned flagged = 0;                     // tiles with noted V, from the first token's
         const int tile0 = max(g.first, 0) / kTile;
@@ -1026,18 +990,15 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             const uint32_t k = base + (g.two ? i : 2 * i + w);
             const int in = k % Smem<KIND>::kInfos;
             const int t = g.t0 + (g.two ? i : 2 * i + w);
-            if (!wait_bar(s, &s.s_full[w], done + i)) return;   // S(i), and with it the tile's mask and factors
+            const uint32_t x_at = done + i, cols = col_s + (x_at & 1) * 64;   // S(i), later P(i)
+            if (!wait_bar(s, &s.s_full[w][x_at & 1], x_at >> 1)) return;      // and with S the tile's mask and factors
             tcgen_fence_after();
             uint32_t raw[2][32];
-            tmem_ld32(col_s, raw[0]);
-            tmem_ld32(col_s + 32, raw[1]);
+            tmem_ld32(cols, raw[0]);
+            tmem_ld32(cols + 32, raw[1]);
             unsigned long long may = s.info[in].mask;
             tmem_wait_ld(raw[0]);
             tmem_wait_ld(raw[1]);
-            tcgen_fence_before();
-            __syncwarp();
-            // the K stage has been read by all that read it after eight arrivals: one a warp, two where a tile has one warpgroup
-            if (lane < (g.two ? 2 : 3)) mbar_arrive(lane == 0 ? &s.s_taken[w] : &s.k_empty[k % kStages]);
             float x[kTile];
             #pragma unroll
             for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(raw[c >> 5][c & 31]);
@@ -1081,7 +1042,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             const float top = fmaxf(max3(part[0], part[1], part[2]), part[3]) * rs;
             if (__any_sync(kFull, top > m + kLazy)) {
                 if (i > 0) {   // O of the tiles before is complete
-                    if (!wait_bar(s, &s.pv_done[w], done + i - 1)) return;
+                    if (!wait_bar(s, &s.pv_done[w][(x_at - 1) & 1], (x_at - 1) >> 1)) return;
                     tcgen_fence_after();
                 }
                 const float nm = fmaxf(m, top);
@@ -1120,15 +1081,13 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 }
                 pw[(c / 2) & 15] = pack_bf16(x[c], x[c + 1]);
                 pw[((c / 2) & 15) + 1] = pack_bf16(x[c + 2], x[c + 3]);
-                if ((c & 31) == 28) {
-                    if (c == 28 && i > 0 && !wait_bar(s, &s.pv_done[w], done + i - 1)) return;   // P(i−1) has been read
-                    tmem_st16(col_p + (c >> 5) * 16, pw);
-                }
+                if ((c & 31) == 28) tmem_st16(cols + (c >> 5) * 16, pw);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
             if (t_end > g.first) {   // non-finite V that only some rows attend (v_full: the repack has looked)
-                // (PV(i−1) is done, so the tile before it in its stage has been read: no phase can be mistaken)
+                // once the tile before it in its stage has been read (this warpgroup may be ahead of both by then)
+                if (i > 0 && !wait_bar(s, &s.pv_done[w][(x_at - 1) & 1], (x_at - 1) >> 1)) return;
                 if (!wait_bar(s, &s.v_full[k % kStages], k / kStages)) return;
                 const unsigned long long* nf = s.info[in].nonfin;
                 const unsigned long long bad = nf[0] | nf[1] | nf[2] | nf[3];
@@ -1139,12 +1098,13 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             }
             tcgen_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_full[w]);
+            if (lane == 0) mbar_arrive(&s.p_full[w][x_at & 1]);
         }
         if (mine > 0) {
-            if (!wait_bar(s, &s.pv_done[w], done + mine - 1)) return;
-            tcgen_fence_after();
             done += mine;
+            if (mine > 1 && !wait_bar(s, &s.pv_done[w][done & 1], (done - 2) >> 1)) return;
+            if (!wait_bar(s, &s.pv_done[w][(done - 1) & 1], (done - 1) >> 1)) return;
+            tcgen_fence_after();
         }
         base += n;
         const bool merging = !g.two && n > 1;   // both warpgroups hold a part of the rows
@@ -1290,10 +1250,14 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    Smem<KIND>& s = *reinterpret_cast<Smem<KIND>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem<KIND>& s = *reinterpret_cast<Smem<KIND>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == kOutWarp) tmem_alloc_all(&s.tmem);
+    if (smem_u32(smem_raw) & 1023u) {   // the operands' swizzle wants it (and nothing else stands before it)
+        if (tid == 0) report(p.err, KVD_ERR_CUDA);
+        return;
+    }
+    if (warp == kMmaWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
         for (int i = 0; i < Smem<KIND>::kRaw; ++i) {
             mbar_init(&s.raw_full[i], 1);
@@ -1301,18 +1265,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         }
         for (int i = 0; i < Smem<KIND>::kStages; ++i) {
             mbar_init(&s.k_full[i], 4);
-            mbar_init(&s.k_empty[i], 8);
+            mbar_init(&s.k_empty[i], 2);
             mbar_init(&s.v_full[i], 4);
             mbar_init(&s.v_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_ready[i], 4);
-            mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.s_taken[i], 4);
-            mbar_init(&s.p_full[i], 4);
-            mbar_init(&s.pv_done[i], 1);
+            mbar_init(&s.drain[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&s.s_full[i][b], 1);
+                mbar_init(&s.p_full[i][b], 4);
+                mbar_init(&s.pv_done[i][b], 1);
+            }
         }
-        for (int i = 0; i < 3; ++i) mbar_init(&s.drain[i], 1);
+        mbar_init(&s.q_one, 4);
         mbar_init(&s.merge_full, 4);
         mbar_init(&s.merge_empty, 4);
         mbar_fence_init();
@@ -1341,21 +1307,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     } else {
         give_registers<56>();
         if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-        else if (warp == kScoreWarp) score_issuer<KIND>(s, p);
-        else out_issuer<KIND>(s, p, warp - kOutWarp);
+        else if (warp < kMmaWarp + 2) mma_issuer<KIND>(s, p, warp - kMmaWarp);
     }
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
     if (tid == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
-    if (warp == kOutWarp) tmem_free_all(s.tmem);
+    if (warp == kMmaWarp) tmem_free_all(s.tmem);
 }
 
 template <int KIND>
 cudaError_t launch_kind(const ChunkParams& p, int grid, cudaStream_t stream) {
-    const size_t smem = sizeof(Smem<KIND>) + 1024;
-    static_assert(sizeof(Smem<KIND>) + 1024 <= 232448, "shared memory of one SM");
+    const size_t smem = sizeof(Smem<KIND>);
+    static_assert(sizeof(Smem<KIND>) <= 232448, "shared memory of one SM");
     static_assert(max_record(KIND) % 16 == 0 && sizeof(TileInfo) % 16 == 0, "16-byte accesses");
     const cudaError_t e =
         cudaFuncSetAttribute(chunk_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
