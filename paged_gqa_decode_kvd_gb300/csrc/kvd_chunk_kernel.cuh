@@ -50,8 +50,8 @@ namespace chunk {
 constexpr int kTile = 64;              // positions per tile: four blocks
 constexpr int kWgRows = 128;           // rows of one MMA (tensor memory lanes)
 constexpr int kUnitRows = 2 * kWgRows;
-constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, MMA 2 × 32, one warp idle
-constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of V 128, producer 32, S 2 × 32, O 32
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kScoreWarp = 17, kOutWarp = 19;
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -94,7 +94,7 @@ struct Smem {
     unsigned long long flags[8][kFlags];                        // by softmax warp: nonfin of the unit's last tiles
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];         // [warpgroup][S and P buffer]
-    uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[2];
+    uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
     int64_t remaining;
     int b, h, qt, off;
     uint32_t tmem;
@@ -812,72 +812,95 @@ __device__ __forceinline__ void value_repacker(Smem<KIND>& s, const ChunkParams&
     }
 }
 
-// The MMAs of warpgroup W, by one warp: S(0), S(1), then O += P(i)·V(i) when P(i) is in tensor memory and S(i+2) = Q·K(i+2)
-// into the same columns: a warpgroup finds its next S ready when it is done with one.
+// What an issuing warp leaves behind when a wait ran out: nothing under way in tensor memory.
 template <int KIND>
-__device__ __forceinline__ void mma_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
-    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile), kDescO = mma_desc_bf16(kWgRows, kDh);
+__device__ __forceinline__ void drain_mma(Smem<KIND>& s, int i) {
+    if (elect_one()) mma_commit(smem_u32(&s.drain[i]));
+    __syncwarp();
+    mbar_wait(&s.drain[i], 0, nullptr, kWaitNs);
+}
+
+// S(i) = Q·K(i) of warpgroup W, by one warp: two tiles ahead, into the columns that held S(i−2) and P(i−2); a
+// warpgroup finds its next S ready when it is done with one.
+template <int KIND>
+__device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p, int warpgroup) {
+    constexpr uint32_t kDescS = mma_desc_bf16(kWgRows, kTile);
     constexpr int kStages = Smem<KIND>::kStages;
     const uint32_t W = uniform(warpgroup);
-    const uint32_t col_s = uniform(s.tmem + kColS + W * 128), d = uniform(s.tmem + kColO + W * 128);
-    const uint32_t k_op = uniform(smem_u32(s.k)), v_op = uniform(smem_u32(s.v)), q_op = uniform(smem_u32(s.q));
+    const uint32_t col_s = uniform(s.tmem + kColS + W * 128);
+    const uint32_t k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
     Walk walk(p, s);
     Segment g;
     uint32_t base = 0, done = 0, own = 0, ones = 0;   // tiles before the segment, of both and of this warpgroup; phases of q_ready, q_one
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
-        const int mine = two ? n : (n + 1 - W) / 2;
+        const uint32_t mine = two ? n : (n + 1 - W) / 2;
         if (mine > 0) ok = two || W == 0 ? wait_bar(s, &s.q_ready[W], own++) : wait_bar(s, &s.q_one, ones++);
         const uint32_t a = uniform(q_op + (two ? W : 0) * 2 * kOpBytes);
         #pragma unroll 1
-        for (int i = -2; ok && i < mine; ++i) {
-            const uint32_t x = done + i, buf = x & 1u, k = base + (two ? i : 2 * i + static_cast<int>(W));
-            const uint32_t cols = uniform(col_s + buf * 64);
-            if (i >= 0) {
-                const uint32_t st = k % kStages;
-                ok = wait_two(s, &s.p_full[W][buf], x >> 1, &s.v_full[st], k / kStages);
-                if (!ok) break;
-                tcgen_fence_after();
-                const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
-                const uint32_t full = uniform(smem_u32(&s.pv_done[W][buf])), empty = uniform(smem_u32(&s.v_empty[st]));
-                if (elect_one()) {
-                    #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) mma_ts(d, cols + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
-                    mma_commit(full);
-                    mma_commit(empty);
-                    if (!two) mbar_arrive(&s.v_empty[st]);
-                }
-                __syncwarp();
+        for (uint32_t i = 0; ok && i < mine; ++i) {
+            const uint32_t x = done + i, buf = x & 1u, k = base + (two ? i : 2 * i + W), st = k % kStages;
+            const uint32_t cols = uniform(col_s + buf * 64), b = uniform(k_op + st * kOpBytes);
+            const uint32_t full = uniform(smem_u32(&s.s_full[W][buf])), empty = uniform(smem_u32(&s.k_empty[st]));
+            ok = wait_two(s, &s.k_full[st], k / kStages, &s.pv_done[W][buf], (x >> 1) - 1, x >= 2);   // P(i−2) has been read
+            if (!ok) break;
+            tcgen_fence_after();
+            if (elect_one()) {
+                #pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    mma_ss(cols, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
+                           smem_desc_sw128(b + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
+                mma_commit(full);
+                mma_commit(empty);
+                if (!two) mbar_arrive(&s.k_empty[st]);
             }
-            if (i + 2 < mine) {
-                const uint32_t k2 = k + (two ? 2 : 4), st = k2 % kStages;
-                ok = wait_bar(s, &s.k_full[st], k2 / kStages);
-                if (ok && i >= 0) ok = wait_bar(s, &s.pv_done[W][buf], x >> 1);   // P(i) has been read
-                if (!ok) break;
-                tcgen_fence_after();
-                const uint32_t b = uniform(k_op + st * kOpBytes);
-                const uint32_t full = uniform(smem_u32(&s.s_full[W][buf])), empty = uniform(smem_u32(&s.k_empty[st]));
-                if (elect_one()) {
-                    #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ss(cols, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
-                               smem_desc_sw128(b + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
-                    mma_commit(full);
-                    mma_commit(empty);
-                    if (!two) mbar_arrive(&s.k_empty[st]);
-                }
-                __syncwarp();
-            }
+            __syncwarp();
         }
         base += n;
         done += mine;
     }
-    if (!ok) {   // what was issued completes before tensor memory is freed
-        if (elect_one()) mma_commit(smem_u32(&s.drain[W]));
-        __syncwarp();
-        mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
+    if (!ok) drain_mma(s, W);
+}
+
+// O += P(i)·V(i) of both warpgroups, by one warp, when P(i) is in tensor memory; W = 0, 1 in turn.
+template <int KIND>
+__device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) {
+    constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
+    constexpr int kStages = Smem<KIND>::kStages;
+    const uint32_t tmem = uniform(s.tmem), v_op = uniform(smem_u32(s.v));
+    Walk walk(p, s);
+    Segment g;
+    uint32_t base = 0, done0 = 0, done1 = 0;   // tiles before the segment, of both and of each warpgroup
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
+        const uint32_t mine0 = two ? n : (n + 1) / 2, mine1 = two ? n : n / 2;
+        #pragma unroll 1
+        for (uint32_t j = 0; j < 2 * mine0; ++j) {
+            const uint32_t W = j & 1u, i = j >> 1;
+            if (W && i >= mine1) continue;
+            const uint32_t x = (W ? done1 : done0) + i, buf = x & 1u, k = base + (two ? i : 2 * i + W), st = k % kStages;
+            const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColS + W * 128 + buf * 64);
+            const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
+            const uint32_t full = uniform(smem_u32(&s.pv_done[W][buf])), empty = uniform(smem_u32(&s.v_empty[st]));
+            ok = wait_two(s, &s.p_full[W][buf], x >> 1, &s.v_full[st], k / kStages);
+            if (!ok) break;
+            tcgen_fence_after();
+            if (elect_one()) {
+                #pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
+                mma_commit(full);
+                mma_commit(empty);
+                if (!two) mbar_arrive(&s.v_empty[st]);
+            }
+            __syncwarp();
+        }
+        base += n;
+        done0 += mine0;
+        done1 += mine1;
     }
+    if (!ok) drain_mma(s, 2);
 }
 
 // A warp's 32 rows of q as the A operand, in the dim order of the K operand.  base: the unit's first token; rel: the
@@ -1257,7 +1280,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         if (tid == 0) report(p.err, KVD_ERR_CUDA);
         return;
     }
-    if (warp == kMmaWarp) tmem_alloc_all(&s.tmem);
+    if (warp == kScoreWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
         for (int i = 0; i < Smem<KIND>::kRaw; ++i) {
             mbar_init(&s.raw_full[i], 1);
@@ -1278,6 +1301,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
                 mbar_init(&s.pv_done[i][b], 1);
             }
         }
+        mbar_init(&s.drain[2], 1);
         mbar_init(&s.q_one, 4);
         mbar_init(&s.merge_full, 4);
         mbar_init(&s.merge_empty, 4);
@@ -1294,27 +1318,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     tcgen_fence_after();
     // one copy of each role's code: with one per warpgroup the loops outgrow the instruction cache
     // (its misses took 90% of the next level's rate, and every role ran at half speed)
-    // Registers: the launch has 640·96 of them; 2·128·152 + 128·(48 + 72 + 56) = 61,440 (8-bit: 56 + 64 + 56).
+    // Registers: a scheduler has 512 a lane; five of the twenty warps are on each, at 96 at launch, then
+    // 2·152 + 48 + 72 + 56 = 480 = 5·96 (8-bit: 56 + 64 + 56).
+    constexpr int kLow = is_wide(KIND) || is_lowbit(KIND);   // 16-bit and low-bit records: the repack of V wants more than that of K
+    constexpr int kRegs = 96, kSoftmaxRegs = 152, kKeyRegs = kLow ? 48 : 56, kValueRegs = kLow ? 72 : 64, kIssueRegs = 56;
+    static_assert(kThreads % 128 == 0 && 2 * kSoftmaxRegs + kKeyRegs + kValueRegs + kIssueRegs <= kThreads / 128 * kRegs &&
+                      kThreads / 128 * kRegs <= 512,
+                  "a request beyond what the launch has would not return");
     if (warp < 8) {
-        take_registers<152>();
+        take_registers<kSoftmaxRegs>();
         softmax_group<KIND>(s, p, warp >> 2, tid & 127, lane);
     } else if (warp < kValueWarp) {
-        give_registers<is_wide(KIND) || is_lowbit(KIND) ? 48 : 56>();
+        give_registers<kKeyRegs>();
         key_repacker<KIND>(s, p, warp - kKeyWarp, lane);
     } else if (warp < kProducerWarp) {
-        give_registers<is_wide(KIND) || is_lowbit(KIND) ? 72 : 64>();
+        give_registers<kValueRegs>();
         value_repacker<KIND>(s, p, warp - kValueWarp, lane);
     } else {
-        give_registers<56>();
+        give_registers<kIssueRegs>();
         if (warp == kProducerWarp) producer<KIND>(s, p, lane);
-        else if (warp < kMmaWarp + 2) mma_issuer<KIND>(s, p, warp - kMmaWarp);
+        else if (warp < kOutWarp) score_issuer<KIND>(s, p, warp - kScoreWarp);
+        else out_issuer<KIND>(s, p);
     }
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
     if (tid == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
-    if (warp == kMmaWarp) tmem_free_all(s.tmem);
+    if (warp == kScoreWarp) tmem_free_all(s.tmem);
 }
 
 template <int KIND>
