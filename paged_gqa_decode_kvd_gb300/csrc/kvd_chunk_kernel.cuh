@@ -58,6 +58,8 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kTries = 200000;         // tries of a wait: a second or so
 constexpr int kColS = 0, kColO = 256;   // tensor memory columns: S and P 2 × 2 × 64, O 2 × 128
 constexpr int kMinTiles = 4;           // smallest share of a CTA
+constexpr int kUnitTiles = 6;          // what a unit costs beside its tiles (its Q, its first S, its rows out), in tiles
+constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
 // A raw slot holds a tile's four records.
@@ -82,6 +84,15 @@ struct TileInfo {
 };
 constexpr int kFlags = 5;           // tiles that hold positions of a unit's own tokens: ⌈(63 + 256)/64⌉
 
+struct Request {
+    int s0, T, len;   // first row, new tokens, context (−1: bad length, nothing is attended)
+};
+struct WalkState {
+    int64_t remaining;
+    int b, h, qt, off, extra;
+    Request r;
+};
+
 template <int KIND>
 struct Smem {
     static constexpr int kStages = op_stages(KIND), kRaw = raw_tiles(KIND), kInfos = info_sets(KIND);
@@ -91,12 +102,13 @@ struct Smem {
     alignas(16) float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
     TileInfo info[kInfos];
     uint32_t word[kRaw][4];                                     // block words
+    WalkState walks[8];                                         // by softmax warp: it has no registers to spare
     unsigned long long flags[8][kFlags];                        // by softmax warp: nonfin of the unit's last tiles
     uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];         // [warpgroup][S and P buffer]
     uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
-    int64_t remaining;
-    int b, h, qt, off;
+    int64_t remaining;   // the CTA's share of the schedule: length, first unit, and where in it, see Walk
+    int b, h, qt, off, extra;
     uint32_t tmem;
     int abort;
     // the merge of the two warpgroups: WG 1's maximum and sum, where no query of its own is
@@ -115,10 +127,6 @@ __device__ inline int64_t tile_sum(int64_t n, int a, int64_t c) {
     else for (int i = 0; i < static_cast<int>(n & 63); ++i, at += low) rest += at & 63u;
     return (a * (n * (n - 1) / 2) + c * n - rest) >> 6;
 }
-
-struct Request {
-    int s0, T, len;   // first row, new tokens, context (−1: bad length, nothing is attended)
-};
 
 __device__ __forceinline__ Request load_request(const ChunkParams& p, int b, bool tell) {
     Request r;
@@ -164,16 +172,15 @@ struct Segment {
     bool two;                // the warpgroups take 128 rows each
 };
 
-// The CTA's segments in order; every role walks them on its own.
-struct Walk {
-    int64_t remaining;
-    int b, h, qt, off;
-    Request r;
+// The CTA's segments in order; every role walks them on its own.  A unit takes `extra` + tiles of the schedule's
+// length, its tiles last: a share that ends before them has none of it.
+struct Walk : WalkState {
     template <class S>
     __device__ __forceinline__ Walk(const ChunkParams& p, const S& s)
-        : remaining(s.remaining), b(s.b), h(s.h), qt(s.qt), off(s.off) {
+        : WalkState{s.remaining, s.b, s.h, s.qt, s.off, s.extra, Request{0, 0, -1}} {
         if (remaining > 0) r = load_request(p, b, false);
     }
+    __device__ __forceinline__ explicit Walk(const WalkState& w) : WalkState(w) {}
     __device__ __forceinline__ bool next(const ChunkParams& p, Segment& g) {
         if (remaining <= 0) return false;
         const int tq = kUnitRows / p.g;
@@ -181,8 +188,9 @@ struct Walk {
         g.h = h;
         g.qt = qt;
         g.tiles = unit_tiles(r, qt, tq);
-        g.t0 = off;
-        g.t1 = static_cast<int>(min(static_cast<int64_t>(g.tiles), off + remaining));
+        const int take = static_cast<int>(min(static_cast<int64_t>(g.tiles) + extra - off, remaining));
+        g.t0 = max(off - extra, 0);
+        g.t1 = off + take - extra;
         g.s0 = r.s0;
         g.T = r.T;
         g.len = r.len;
@@ -191,7 +199,7 @@ struct Walk {
         g.first = r.len < 0 ? -1 : r.len - r.T + g.tok0;
         g.rows = min(tq, r.T - g.tok0) * p.g;
         g.two = g.rows > kWgRows;
-        remaining -= g.t1 - g.t0;
+        remaining -= take;
         off = 0;
         if (remaining > 0) {
             if (++qt * tq >= r.T) {
@@ -201,40 +209,54 @@ struct Walk {
                     do {
                         if (++b >= p.B) {
                             remaining = 0;
-                            return true;
+                            break;
                         }
                         r = load_request(p, b, false);
                     } while (r.T == 0);
                 }
             }
         }
-        return true;
+        return g.t1 > g.t0;
     }
 };
 
-// A CTA's share of the schedule, by every thread of the block; scratch holds p.B int64.
+// A CTA's share of the schedule, by every thread of the block; scratch holds 2·p.B int64.
 template <class S>
 __device__ inline void make_schedule(const ChunkParams& p, S& s, int64_t* scratch) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int tq = kUnitRows / p.g;
     for (int b = tid; b < p.B; b += kThreads) {
         const Request r = load_request(p, b, blockIdx.x == 0);
-        scratch[b] = r.T ? tiles_before(r, (r.T + tq - 1) / tq, tq) * p.n_kv : 0;
+        const int units = (r.T + tq - 1) / tq;
+        scratch[2 * b] = r.T ? tiles_before(r, units, tq) * p.n_kv : 0;
+        scratch[2 * b + 1] = static_cast<int64_t>(units) * p.n_kv;
     }
     __syncthreads();
     if (tid < 32) {
-        int64_t total = 0;
-        for (int b = lane; b < p.B; b += 32) total += scratch[b];
+        int64_t tiles = 0, units = 0;
+        for (int b = lane; b < p.B; b += 32) {
+            tiles += scratch[2 * b];
+            units += scratch[2 * b + 1];
+        }
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            tiles += __shfl_xor_sync(kFull, tiles, o);
+            units += __shfl_xor_sync(kFull, units, o);
+        }
+        // a small call is cut into its smallest shares; there the border must not fall beside the tiles
+        const int extra = static_cast<int>(min(static_cast<int64_t>(kUnitTiles), tiles / (8 * gridDim.x)));
+        const int64_t total = tiles + units * extra;
         const int64_t most = (total + kMinTiles - 1) / kMinTiles;
         const int64_t ctas = most < gridDim.x ? (most < 1 ? 1 : most) : gridDim.x;
         const int64_t lo = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
         const int64_t hi = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
-        if (lane == 0) s.remaining = hi - lo;
+        if (lane == 0) {
+            s.remaining = hi - lo;
+            s.extra = extra;
+        }
         int64_t before = 0;
         for (int b0 = 0; hi > lo && b0 < p.B; b0 += 32) {
-            const int64_t c = b0 + lane < p.B ? scratch[b0 + lane] : 0;
+            const int64_t c = b0 + lane < p.B ? scratch[2 * (b0 + lane)] + extra * scratch[2 * (b0 + lane) + 1] : 0;
             int64_t up = c;
             #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -253,7 +275,7 @@ __device__ inline void make_schedule(const ChunkParams& p, S& s, int64_t* scratc
                 int a = 0, z = (r.T + tq - 1) / tq;   // the last unit of [a, z) that starts at or before `in`
                 while (z - a > 1) {
                     const int step = (z - a + 31) / 32, mid = a + lane * step;
-                    const int n = __popc(__ballot_sync(kFull, mid < z && tiles_before(r, mid, tq) <= in));
+                    const int n = __popc(__ballot_sync(kFull, mid < z && tiles_before(r, mid, tq) + static_cast<int64_t>(mid) * extra <= in));
                     a += (n - 1) * step;
                     z = min(z, a + step);
                 }
@@ -261,7 +283,7 @@ __device__ inline void make_schedule(const ChunkParams& p, S& s, int64_t* scratc
                     s.b = b;
                     s.h = h;
                     s.qt = a;
-                    s.off = static_cast<int>(in - tiles_before(r, a, tq));
+                    s.off = static_cast<int>(in - tiles_before(r, a, tq) - static_cast<int64_t>(a) * extra);
                 }
             }
             before = __shfl_sync(kFull, up, 31);
@@ -727,21 +749,27 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
             }
         }
     }
+    if (ok && wait_bar(s, &s.raw_empty[k % kRaw], k / kRaw + 1)) {   // the end, for those that do not walk
+        if (lane == 0) {
+            s.word[k % kRaw][0] = kStop;
+            mbar_arrive(&s.raw_full[k % kRaw]);
+        }
+    }
     if (!ok) {   // the copies in flight land before the block leaves
         for (uint32_t i = k > kRaw ? k - kRaw : 0; i < k; ++i) mbar_wait(&s.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr, kWaitNs);
     }
 }
 
-// K of every tile, a block a warp; with the tile's mask and factors.
+// K of every tile, a block a warp; with the tile's mask, limits and factors.
 template <int KIND>
 __device__ __forceinline__ void key_repacker(Smem<KIND>& s, const ChunkParams& p, int warp, int lane) {
     constexpr int kRaw = Smem<KIND>::kRaw, kStages = Smem<KIND>::kStages;
     const Offsets off(warp, lane);
-    const uint32_t tiles = static_cast<uint32_t>(s.remaining);
     #pragma unroll 1
-    for (uint32_t k = 0; k < tiles; ++k) {
+    for (uint32_t k = 0;; ++k) {   // to the producer's mark
         const uint32_t st = k % kRaw, ks = k % kStages, in = k % Smem<KIND>::kInfos;
         if (!wait_two(s, &s.raw_full[st], k / kRaw, &s.k_empty[ks], k / kStages + 1)) return;
+        if (s.word[st][0] == kStop) return;
         const uint32_t mine = s.word[st][warp];
         if (warp == 0 && lane == 0)
             s.info[in].mask = static_cast<unsigned long long>(s.word[st][0] & 0xffffu) |
@@ -981,12 +1009,24 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
     // the scale's sign goes into q; a zero scale becomes one that leaves every finite logit at zero
     const bool flip = p.scale_log2 < 0.f;
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
-    Walk walk(p, s);
+    WalkState& state = s.walks[threadIdx.x >> 5];
+    {
+        const Walk walk(p, s);
+        if (lane == 0) state = walk;
+        __syncwarp();
+    }
     Segment g;
     uint32_t base = 0, done = 0, ones = 0;   // tiles before the segment, of both and of this warpgroup; segments of one row group
     bool merge_pending = false;
     int seg_index = 0;
-    while (walk.next(p, g)) {
+    while (true) {
+        {
+            Walk walk(state);
+            __syncwarp();
+            if (!walk.next(p, g)) return;
+            if (lane == 0) state = walk;
+            __syncwarp();
+        }
         const int n = g.t1 - g.t0;
         const int mine = g.two ? n : (n + 1 - w) / 2;   // tiles of this warpgroup
         const int row = g.two ? w * kWgRows + tid : tid;
@@ -1319,9 +1359,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     // one copy of each role's code: with one per warpgroup the loops outgrow the instruction cache
     // (its misses took 90% of the next level's rate, and every role ran at half speed)
     // Registers: a scheduler has 512 a lane; five of the twenty warps are on each, at 96 at launch, then
-    // 2·152 + 48 + 72 + 56 = 480 = 5·96 (8-bit: 56 + 64 + 56).
-    constexpr int kLow = is_wide(KIND) || is_lowbit(KIND);   // 16-bit and low-bit records: the repack of V wants more than that of K
-    constexpr int kRegs = 96, kSoftmaxRegs = 152, kKeyRegs = kLow ? 48 : 56, kValueRegs = kLow ? 72 : 64, kIssueRegs = 56;
+    // 2·152 + 48 + 72 + 56 = 480 = 5·96.
+    constexpr int kRegs = 96, kSoftmaxRegs = 152, kKeyRegs = 48, kValueRegs = 72, kIssueRegs = 56;
     static_assert(kThreads % 128 == 0 && 2 * kSoftmaxRegs + kKeyRegs + kValueRegs + kIssueRegs <= kThreads / 128 * kRegs &&
                       kThreads / 128 * kRegs <= 512,
                   "a request beyond what the launch has would not return");
