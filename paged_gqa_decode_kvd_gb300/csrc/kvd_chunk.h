@@ -29,7 +29,7 @@ struct RopeParams {
     int ng;
     int rot;
     int interleaved;
-    int heads_per_cta;           // set by the launcher
+    int heads_per_cta, kv_heads_per_cta;           // set by the launcher
     float mscale;
 };
 cudaError_t launch_rope_append(RopeParams p, int kind, int num_sms, cudaStream_t stream);

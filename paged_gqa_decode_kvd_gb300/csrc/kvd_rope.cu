@@ -20,32 +20,42 @@ namespace {
 constexpr int kTok = 16;               // tokens per CTA: the most that share a block
 constexpr int kRopeThreads = 256;
 constexpr int kRowPad = kDh + 8;       // bf16 elements per staged row (bank spread)
+constexpr int kRows = 8;               // rows a thread holds: query heads, or K and V of half as many KV heads
 
 struct RopeSmem {
     float2 cs[kTok][kDh / 2];                              // (cos, sin)·m per (token, pair)
     __align__(16) uint16_t krow[2][kTok][kRowPad];         // rotated K rows of one head, then its V rows
     int64_t slot[kTok];
+    uint8_t* record[kTok];                                 // of the token's K and V (the first head's), or null
+    int pos[kTok];
     int src[kBs];                                          // the token that goes to slot offset t, or -1
     int ok[kTok];                                          // the token takes part
     int shared_offset;                                     // two tokens want the same slot offset
 };
 
-// One row of 128 values by 16 lanes, 8 consecutive dims each (lane16 = lane % 16), rotated in fp32
-// and rounded to bf16.
+// (cos, sin)·m of a lane's 8 consecutive dims (lane16 = lane % 16): by pair if neighbours are paired, else by dim.
 template <bool INTERLEAVED>
-__device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2* cs, int rot, int lane16) {
+__device__ __forceinline__ void lane_factors(float2 (&f)[8], const float2* cs, int rot, int lane16) {
+    const int half = rot >> 1;
+    #pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int d = lane16 * 8 + e;
+        f[e] = make_float2(1.f, 0.f);
+        if (INTERLEAVED ? (e < 4 && lane16 * 4 + e < half) : d < rot) f[e] = cs[INTERLEAVED ? lane16 * 4 + e : d < half ? d : d - half];
+    }
+}
+
+// One row of 128 values by 16 lanes, 8 consecutive dims each, rotated in fp32 and rounded to bf16.
+template <bool INTERLEAVED>
+__device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2 (&f)[8], int rot, int lane16) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t out[4];
     if constexpr (INTERLEAVED) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int d = lane16 * 8 + 2 * i;
-            const float2 x = unpack_bf16(w[i]);
-            out[i] = w[i];
-            if (d < rot) {
-                const float2 c = cs[d >> 1];
-                out[i] = pack_bf16(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
-            }
+            const float2 x = unpack_bf16(w[i]), c = f[i];
+            const uint32_t v = pack_bf16(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+            out[i] = lane16 * 8 + 2 * i < rot ? v : w[i];
         }
         return make_uint4(out[0], out[1], out[2], out[3]);
     }
@@ -71,13 +81,9 @@ __device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2* cs, int rot
             const float2 pv = unpack_bf16(__shfl_sync(kFull, w[i], other));
             #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int e = 2 * i + k, d = lane16 * 8 + e;
+                const int e = 2 * i + k;
                 const float b = k ? pv.y : pv.x;
-                y[e] = x[e];
-                if (d < rot) {
-                    const float2 c = cs[low ? d : d - half];
-                    y[e] = low ? x[e] * c.x - b * c.y : b * c.y + x[e] * c.x;
-                }
+                y[e] = low ? x[e] * f[e].x - b * f[e].y : b * f[e].y + x[e] * f[e].x;
             }
         }
     } else {
@@ -95,11 +101,7 @@ __device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2* cs, int rot
             }
             const float2 pv = unpack_bf16(pw);
             const float b = (pd & 1) ? pv.y : pv.x;
-            y[e] = x[e];
-            if (d < rot) {
-                const float2 c = cs[low ? d : d - half];
-                y[e] = low ? x[e] * c.x - b * c.y : b * c.y + x[e] * c.x;
-            }
+            y[e] = low ? x[e] * f[e].x - b * f[e].y : b * f[e].y + x[e] * f[e].x;
         }
     }
     #pragma unroll
@@ -139,9 +141,9 @@ __device__ __forceinline__ void put_token(const RopeParams& p, uint8_t* record, 
     }
 }
 
-// CTA (tile of 16 tokens, group of heads).  Heads 0 .. n_q-1 of the list are query heads, the rest
-// KV heads.  Tiles start at a multiple of 16 slots behind the first token's block start, so a chunk
-// of one request fills whole blocks (a record's 16-byte pieces hold two or four of its tokens).
+// CTA (tile of 16 tokens, group of query heads or one KV head).  A thread has all its rows' loads under way
+// before the angles are there.  Tiles start at a multiple of 16 slots behind the first token's block start, so a
+// chunk of one request fills whole blocks (a record's 16-byte pieces hold two or four of its tokens).
 template <int KIND, int NG, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
     __shared__ RopeSmem s;
@@ -151,30 +153,56 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
     const int64_t first = p.slot_mapping[0];
     const int shift = first > 0 ? static_cast<int>(first % kBs) : 0;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTok - shift;
-    const int h0 = blockIdx.y * p.heads_per_cta;
-    const int h1 = min(h0 + p.heads_per_cta, p.n_q + p.n_kv);
+    const int groups = (p.n_q + p.heads_per_cta - 1) / p.heads_per_cta;
+    const bool query = static_cast<int>(blockIdx.y) < groups;
+    const int h0 = query ? blockIdx.y * p.heads_per_cta : (blockIdx.y - groups) * p.kv_heads_per_cta;
+    const int heads = query ? min(p.heads_per_cta, p.n_q - h0) : min(p.kv_heads_per_cta, p.n_kv - h0);
+    const int half_id = tid >> 4, lane16 = tid & 15;   // 16 half-warps, a token each
+    const int64_t row = n0 + half_id;
+    uint4 x[kRows];
+    #pragma unroll
+    for (int i = 0; i < kRows; ++i) x[i] = make_uint4(0, 0, 0, 0);
+    if (row >= 0 && row < p.n_tokens) {
+        if (query) {
+            #pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (i < heads) x[i] = *reinterpret_cast<const uint4*>(p.q + row * p.q_stride + (h0 + i) * kDh + lane16 * 8);
+        } else {
+            #pragma unroll
+            for (int i = 0; i < kRows; i += 2) {
+                if (i / 2 >= heads) continue;
+                x[i] = *reinterpret_cast<const uint4*>(p.k + row * p.k_stride + (h0 + i / 2) * kDh + lane16 * 8);
+                x[i + 1] = *reinterpret_cast<const uint4*>(p.v + row * p.v_stride + (h0 + i / 2) * kDh + lane16 * 8);
+            }
+        }
+    }
     if (tid < kTok) {
         const int64_t n = n0 + tid;
         int ok = n >= 0 && n < p.n_tokens;
         int64_t slot = -1;
+        int pos = 0;
         if (ok) {
-            const int pos = p.positions[n];
+            pos = p.positions[n];
+            slot = p.slot_mapping[n];
             if (pos < 0 || pos >= kMaxRopePos) {
                 if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
                 ok = 0;
-            } else {
-                slot = p.slot_mapping[n];
-                if (slot >= 0 && slot / kBs >= p.num_blocks + p.host_blocks) {
-                    if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
-                    slot = -1;
-                }
+                slot = -1;
+            } else if (slot >= 0 && slot / kBs >= p.num_blocks + p.host_blocks) {
+                if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
+                slot = -1;
             }
         }
+        const int64_t blk = slot / kBs;
         s.ok[tid] = ok;
+        s.pos[tid] = pos;
         s.slot[tid] = slot;
+        s.record[tid] = slot < 0 || query ? nullptr
+                        : blk < p.num_blocks ? p.kv + (blk * p.n_kv + h0) * record_size<KIND, NG>()
+                                             : p.host_kv + ((blk - p.num_blocks) * p.n_kv + h0) * record_size<KIND, NG>();
     }
     __syncthreads();
-    if (h1 > p.n_q && tid < kBs) {   // slot offset -> token
+    if (!query && tid < kBs) {   // slot offset -> token
         int found = -1, twice = 0;
         for (int i = 0; i < kTok; ++i) {
             if (s.slot[i] >= 0 && s.slot[i] % kBs == tid) {
@@ -187,62 +215,45 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
         if (tid == 0) s.shared_offset = any != 0;
     }
     const int pairs = p.rot >> 1;
-    for (int i = tid; i < kTok * pairs; i += kRopeThreads) {
-        const int tk = i / pairs, j = i % pairs;
-        float2 c = make_float2(0.f, 0.f);
-        if (s.ok[tk]) {
-            const float pos = static_cast<float>(p.positions[n0 + tk]);
-            const float2 f = p.turns[j];
-            const float a = __fmul_rn(pos, f.x);
-            const float rest = __fmaf_rn(pos, f.x, -a);
-            const float turn = __fadd_rn(__fsub_rn(a, rintf(a)), __fmaf_rn(pos, f.y, rest));
-            float sn, cn;
-            sincospif(2.f * turn, &sn, &cn);
-            c = make_float2(cn * p.mscale, sn * p.mscale);
-        }
-        s.cs[tk][j] = c;
+    const float pos = static_cast<float>(s.pos[half_id]);
+    for (int j = lane16; j < pairs; j += 16) {
+        const float2 f = p.turns[j];
+        const float a = __fmul_rn(pos, f.x);
+        const float rest = __fmaf_rn(pos, f.x, -a);
+        const float turn = __fadd_rn(__fsub_rn(a, rintf(a)), __fmaf_rn(pos, f.y, rest));
+        float sn, cn;
+        sincospif(2.f * turn, &sn, &cn);
+        s.cs[half_id][j] = make_float2(cn * p.mscale, sn * p.mscale);
     }
     __syncthreads();
-    const int half_id = tid >> 4, lane16 = tid & 15;   // 16 half-warps, a row each
-    for (int h = h0; h < h1; ++h) {
-        if (h < p.n_q) {
-            const int tk = half_id;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (s.ok[tk])
-                x = *reinterpret_cast<const uint4*>(p.q + (n0 + tk) * p.q_stride + h * kDh + lane16 * 8);
-            x = rotate_row<INTERLEAVED>(x, s.cs[tk], p.rot, lane16);
-            if (s.ok[tk])
-                *reinterpret_cast<uint4*>(p.q_out + (n0 + tk) * p.q_out_stride + h * kDh + lane16 * 8) = x;
-            continue;
+    float2 factor[8];
+    lane_factors<INTERLEAVED>(factor, s.cs[half_id], p.rot, lane16);
+    if (query) {
+        #pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (i >= heads) break;
+            const uint4 y = rotate_row<INTERLEAVED>(x[i], factor, p.rot, lane16);
+            if (s.ok[half_id]) *reinterpret_cast<uint4*>(p.q_out + row * p.q_out_stride + (h0 + i) * kDh + lane16 * 8) = y;
         }
-        const int kh = h - p.n_q;
-        {
-            const int tk = half_id;
-            uint4 k = make_uint4(0, 0, 0, 0), v = k;
-            if (s.slot[tk] >= 0) {
-                k = *reinterpret_cast<const uint4*>(p.k + (n0 + tk) * p.k_stride + kh * kDh + lane16 * 8);
-                v = *reinterpret_cast<const uint4*>(p.v + (n0 + tk) * p.v_stride + kh * kDh + lane16 * 8);
-            }
-            k = rotate_row<INTERLEAVED>(k, s.cs[tk], p.rot, lane16);
-            *reinterpret_cast<uint4*>(&s.krow[0][tk][lane16 * 8]) = k;
-            *reinterpret_cast<uint4*>(&s.krow[1][tk][lane16 * 8]) = v;
-        }
+        return;
+    }
+    #pragma unroll
+    for (int h = 0; h < kRows / 2; ++h) {
+        if (h >= heads) break;
+        if (h) __syncthreads();   // the head before has been written out
+        *reinterpret_cast<uint4*>(&s.krow[0][half_id][lane16 * 8]) = rotate_row<INTERLEAVED>(x[2 * h], factor, p.rot, lane16);
+        *reinterpret_cast<uint4*>(&s.krow[1][half_id][lane16 * 8]) = x[2 * h + 1];
         __syncthreads();
-        const int64_t kRec = record_size<KIND, NG>();
-        auto record = [&](int tk) -> uint8_t* {
-            const int64_t blk = s.slot[tk] / kBs;
-            return blk < p.num_blocks ? p.kv + (blk * p.n_kv + kh) * kRec
-                                      : p.host_kv + ((blk - p.num_blocks) * p.n_kv + kh) * kRec;
-        };
+        auto record = [&](int tk) -> uint8_t* { return s.record[tk] ? s.record[tk] + h * record_size<KIND, NG>() : nullptr; };
         if (KIND == kKindBf16 && !s.shared_offset) {
             // 16-byte pieces of the two tiles: a K piece holds dims (2x, 2x+1, 2x+8, 2x+9) of tokens
             // t and t + 8, a V piece tokens (2x, 2x+1, 2x+8, 2x+9) of dims r and r + 8.  Whole
             // pieces where their tokens go to the same record, smaller stores where they do not.
             for (int c = tid; c < 512; c += kRopeThreads) {
-                const int i = (c >> 5) & 7, l = c & 31, x = l & 3, r = l >> 2;
+                const int i = (c >> 5) & 7, l = c & 31, x4 = l & 3, r = l >> 2;
                 if (c < 256) {
                     const int ta = s.src[r], tb = s.src[r + 8];
-                    const int d = 16 * i + 2 * x;
+                    const int d = 16 * i + 2 * x4;
                     uint32_t a0 = 0, a1 = 0, b0 = 0, b1 = 0;
                     if (ta >= 0) {
                         a0 = *reinterpret_cast<const uint32_t*>(&s.krow[0][ta][d]);
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
                     uint8_t* rec[4];
                     #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int tk = s.src[2 * x + (k & 1) + 8 * (k >> 1)];
+                        const int tk = s.src[2 * x4 + (k & 1) + 8 * (k >> 1)];
                         rec[k] = tk >= 0 ? record(tk) : nullptr;
                         lo[k] = tk >= 0 ? s.krow[1][tk][d] : 0;
                         hi[k] = tk >= 0 ? s.krow[1][tk][d + 8] : 0;
@@ -301,7 +312,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopePar
                                     s.krow[1][tk], lane);
             }
         }
-        __syncthreads();
     }
 }
 
@@ -315,10 +325,13 @@ cudaError_t launch(const RopeParams& p, dim3 grid, cudaStream_t stream) {
 
 cudaError_t launch_rope_append(RopeParams p, int kind, int num_sms, cudaStream_t stream) {
     const int64_t tiles = (p.n_tokens + kTok - 1) / kTok + 1;   // one more: the first tile may start before token 0
-    const int heads = p.n_q + p.n_kv;
-    p.heads_per_cta = 8;
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + p.heads_per_cta - 1) / p.heads_per_cta));
-    (void)num_sms;
+    // Eight query heads (four KV heads) a CTA where that leaves four CTAs an SM: their angles are computed once.
+    // Fewer tiles take more CTAs instead.
+    const bool many = tiles * ((p.n_q + 7) / 8) >= 4 * num_sms;
+    p.heads_per_cta = many ? 8 : 2;
+    p.kv_heads_per_cta = many ? 4 : 1;
+    const int groups = (p.n_q + p.heads_per_cta - 1) / p.heads_per_cta;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(groups + (p.n_kv + p.kv_heads_per_cta - 1) / p.kv_heads_per_cta));
     switch (kind) {
         case kKindFp8: return launch<kKindFp8, 1>(p, grid, stream);
         case kKindMixed: return launch<kKindMixed, 1>(p, grid, stream);
