@@ -367,20 +367,20 @@ def kvd_rope_freqs(rot_dim, base, scaling="plain", factor=1.0, original_len=0.0,
     return turns, m.value
 
 
-def _heads(t, name):
+def _heads(t, name, dtype):
     """Token stride of a bf16 [n][heads][128] tensor (a slice of a projection's output counts)."""
-    import torch
-
-    if t.dim() != 3 or t.shape[2] != 128 or t.dtype != torch.bfloat16:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != 128 or t.dtype is not dtype:
         raise ValueError(f"{name} must be bfloat16 [tokens][heads][128]")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128)):
+    n, h, _ = shape
+    if (stride[2] != 1 or (h > 1 and stride[1] != 128)) and n and h:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1) * 128
+    return stride[0] if n > 1 else max(h, 1) * 128
 
 
 def _like(t, name, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}")
 
 
 def kvd_rope_append(handle, layer, q, k_new, v_new, positions, rope, slot_mapping, q_out=None, stream=None):
@@ -389,23 +389,27 @@ def kvd_rope_append(handle, layer, q, k_new, v_new, positions, rope, slot_mappin
     contiguous; q may be None (append only)."""
     import torch
 
-    n = int(k_new.shape[0])
-    ks, vs = _heads(k_new, "k_new"), _heads(v_new, "v_new")
-    dev = k_new.device
-    if v_new.shape != k_new.shape or v_new.device != dev or rope.turns.device != dev:
+    bf16 = torch.bfloat16
+    n = k_new.shape[0]
+    ks, vs = _heads(k_new, "k_new", bf16), _heads(v_new, "v_new", bf16)
+    dev = k_new.get_device()   # comparing torch.device objects takes three times as long, and a step is short
+    if v_new.shape != k_new.shape or v_new.get_device() != dev or rope.turns.get_device() != dev:
         raise ValueError("k_new, v_new and rope must agree in shape and device")
     _like(positions, "positions", torch.int32, (n,), dev)
     _like(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
     n_q, qs, os_ = 0, 0, 0
     if q is not None:
         q_out = q if q_out is None else q_out
-        if q.shape[0] != n or q_out.shape != q.shape or q.device != dev or q_out.device != dev:
+        if q.shape[0] != n or q_out.shape != q.shape or q.get_device() != dev or q_out.get_device() != dev:
             raise ValueError("q and q_out must have k_new's tokens and device")
-        n_q, qs, os_ = int(q.shape[1]), _heads(q, "q"), _heads(q_out, "q_out")
+        n_q, qs = q.shape[1], _heads(q, "q", bf16)
+        os_ = qs if q_out is q else _heads(q_out, "q_out", bf16)
     d = RopeDesc(rope.turns.data_ptr(), rope.rot_dim, 1 if rope.interleaved else 0, rope.mscale)
-    _check("kvd_rope_append", load().kvd_rope_append(
-        handle, int(layer), _ptr(q), qs, n_q, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(positions), ctypes.byref(d),
-        _ptr(slot_mapping), n, _ptr(q_out if q is not None else None), os_, _stream(stream)))
+    status = load().kvd_rope_append(
+        handle, int(layer), 0 if q is None else q.data_ptr(), qs, n_q, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+        positions.data_ptr(), d, slot_mapping.data_ptr(), n, 0 if q is None else q_out.data_ptr(), os_, _stream(stream))
+    if status != KVD_OK:
+        _check("kvd_rope_append", status)
 
 
 def kvd_chunk_workspace_bytes(handle, n_q, batch):
@@ -426,13 +430,14 @@ def kvd_chunk_attn(handle, layer, q, q_start, block_table, seq_lens, workspace, 
         raise ValueError("q must be contiguous bfloat16 [tokens][heads][128]")
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out must be bfloat16 or float32")
-    _like(out, "out", out.dtype, q.shape, q.device)
-    batch = int(seq_lens.shape[0])
-    _like(seq_lens, "seq_lens", torch.int32, (batch,), q.device)
-    _like(q_start, "q_start", torch.int32, (batch + 1,), q.device)
-    _like(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), q.device)
+    dev = q.get_device()
+    _like(out, "out", out.dtype, q.shape, dev)
+    batch = seq_lens.shape[0]
+    _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _like(q_start, "q_start", torch.int32, (batch + 1,), dev)
+    _like(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), dev)
     if lse_out is not None:
-        _like(lse_out, "lse_out", torch.float32, (n, n_q), q.device)
+        _like(lse_out, "lse_out", torch.float32, (n, n_q), dev)
     if softmax_scale is None:
         softmax_scale = d_h ** -0.5
     _check("kvd_chunk_attn", load().kvd_chunk_attn(
@@ -456,7 +461,7 @@ def kvd_compact(handle, block_table, seq_lens, new_table, new_lens, workspace, r
     import torch
 
     batch, mb = block_table.shape
-    dev = block_table.device
+    dev = block_table.get_device()
     _like(block_table, "block_table", torch.int32, (batch, mb), dev)
     _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
     _like(new_table, "new_table", torch.int32, (batch, new_table.shape[1]), dev)

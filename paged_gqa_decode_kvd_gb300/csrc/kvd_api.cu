@@ -823,7 +823,7 @@ kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int max_block
     p.B = batch;
     p.L = pool->desc.num_layers;
     p.n_kv = pool->desc.n_kv;
-    return cuda_status(kvd::launch_compact(p, pool_kind(pool), pool_ng(&pool->desc), static_cast<cudaStream_t>(stream)));
+    return cuda_status(kvd::launch_compact(p, pool_kind(pool), pool_ng(&pool->desc), pool->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 kvd_status kvd_combine_splits(const float* part_o, const float* part_lse, const int32_t* unit_first,

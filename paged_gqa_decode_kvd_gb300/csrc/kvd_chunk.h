@@ -89,6 +89,6 @@ struct CompactParams {
     int L;
     int n_kv;
 };
-cudaError_t launch_compact(const CompactParams& p, int kind, int ng, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, int kind, int ng, int num_sms, cudaStream_t stream);
 
 }  // namespace kvd

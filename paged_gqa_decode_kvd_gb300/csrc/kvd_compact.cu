@@ -35,11 +35,10 @@ __device__ __forceinline__ uint32_t kept_slots(const CompactParams& p, int len, 
 
 // One CTA per request: source of every new slot, the new length, the scores.  Clears the claims.
 __global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const CompactParams p) {
-    __shared__ int scan[kRankThreads];
-    __shared__ int base;
+    __shared__ int sums[kRankThreads / 32];
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     for (int64_t i = static_cast<int64_t>(b) * kRankThreads + tid; i < p.num_blocks + p.host_blocks;
          i += static_cast<int64_t>(gridDim.x) * kRankThreads)
         p.claim[i] = 0;
@@ -49,12 +48,11 @@ __global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const Compac
         if (tid == 0) report(p.err, KVD_ERR_OOB);
         nb = 0;
     }
-    if (tid == 0) base = 0;
     const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
     uint32_t* source = p.source + static_cast<int64_t>(b) * p.max_blocks * kBs;
     const float* from = p.scores ? p.scores + static_cast<int64_t>(b) * p.scores_stride : nullptr;
     float* to = p.scores ? p.new_scores + static_cast<int64_t>(b) * p.new_scores_stride : nullptr;
-    __syncthreads();
+    int base = 0;
     for (int j0 = 0; j0 < nb; j0 += kRankThreads) {
         const int j = j0 + tid;
         uint32_t kept = 0;
@@ -65,15 +63,22 @@ __global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const Compac
             if (phys < 0 || phys >= p.num_blocks + p.host_blocks) report(p.err, KVD_ERR_OOB);
         }
         const int n = __popc(kept);
-        scan[tid] = n;
-        __syncthreads();
-        for (int off = 1; off < kRankThreads; off <<= 1) {
-            const int v = tid >= off ? scan[tid - off] : 0;
-            __syncthreads();
-            scan[tid] += v;
-            __syncthreads();
+        int up = n;   // of this block and those before it in the warp
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, up, o);
+            if (lane >= o) up += v;
         }
-        int r = base + scan[tid] - n;
+        if (lane == 31) sums[tid >> 5] = up;
+        __syncthreads();
+        int before = 0, all = 0;
+        #pragma unroll
+        for (int w = 0; w < kRankThreads / 32; ++w) {
+            before += w < (tid >> 5) ? sums[w] : 0;
+            all += sums[w];
+        }
+        int r = base + before + up - n;
+        base += all;
         while (kept) {
             const int t = __ffs(kept) - 1;
             kept &= kept - 1;
@@ -84,8 +89,6 @@ __global__ void __launch_bounds__(kRankThreads) compact_rank_kernel(const Compac
             }
             ++r;
         }
-        __syncthreads();
-        if (tid == kRankThreads - 1) base += scan[tid];
         __syncthreads();
     }
     int total = base;
@@ -129,95 +132,64 @@ struct Rec {
     static constexpr int kPieces = kBytes / 16;
 };
 
-// K tile of a 16- or 8-bit record: 16-byte piece = fragment lane (r, x); token t = r + 8·((k >> 1) & 1)
-// for element e, elements in pairs (W = bytes of an element).
+// The source piece of new slot t's token: piece(u) gives its number in the tile for slot offset u.  All lanes load
+// whole 16-byte pieces and pick the token's part: a fourth of the loads that the parts alone would take.
+template <class F>
+__device__ __forceinline__ uint4 source_piece(const uint8_t* const* rec, const int* off, int t, F piece) {
+    const uint8_t* from = rec[t];
+    if (!from) return make_uint4(0, 0, 0, 0);
+    return __ldg(reinterpret_cast<const uint4*>(from) + piece(off[t]));
+}
+
+// K tile: 16-byte piece = fragment lane (r, x) of a group: tokens r and r + 8.  W = bytes of an element; 0: low-bit codes.
 template <int W>
 __device__ __forceinline__ uint4 gather_k(const uint8_t* const* rec, const int* off, int piece) {
     const int l = piece & 31, x = l & 3, r = l >> 2, group = piece >> 5;
-    uint4 out;
-    uint32_t* o = reinterpret_cast<uint32_t*>(&out);
-    auto at = [&](int t) -> const uint8_t* {   // the piece of token t's source that holds its pairs
-        const int u = off[t];
-        return rec[t] + (group * 32 + 4 * (u & 7) + x) * 16 + (u >> 3) * 2 * W;
-    };
-    const uint8_t* a = rec[r] ? at(r) : nullptr;
-    const uint8_t* b = rec[r + 8] ? at(r + 8) : nullptr;
-    if constexpr (W == 2) {
-        o[0] = a ? *reinterpret_cast<const uint32_t*>(a) : 0u;
-        o[1] = b ? *reinterpret_cast<const uint32_t*>(b) : 0u;
-        o[2] = a ? *reinterpret_cast<const uint32_t*>(a + 8) : 0u;
-        o[3] = b ? *reinterpret_cast<const uint32_t*>(b + 8) : 0u;
-    } else {
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) {   // group 2i (k < 2) and 2i + 1; dims + 0 and + 8
-            const uint32_t lo = a ? *reinterpret_cast<const uint16_t*>(a + 4 * k) : 0u;
-            const uint32_t hi = b ? *reinterpret_cast<const uint16_t*>(b + 4 * k) : 0u;
-            o[k] = lo | (hi << 16);
-        }
+    auto number = [&](int u) { return group * 32 + 4 * (u & 7) + x; };
+    const uint4 a = source_piece(rec, off, r, number), b = source_piece(rec, off, r + 8, number);
+    const bool ah = off[r] >> 3, bh = off[r + 8] >> 3;   // which of the piece's tokens
+    if constexpr (W == 1) {   // pairs of codes: the halves of each word
+        const uint32_t pick = (ah ? 0x32u : 0x10u) | (bh ? 0x7600u : 0x5400u);
+        return make_uint4(__byte_perm(a.x, b.x, pick), __byte_perm(a.y, b.y, pick), __byte_perm(a.z, b.z, pick),
+                          __byte_perm(a.w, b.w, pick));
+    } else {                  // words 0, 2: the first token; 1, 3: the second
+        return make_uint4(ah ? a.y : a.x, bh ? b.y : b.x, ah ? a.w : a.z, bh ? b.w : b.z);
     }
-    return out;
 }
 
-// V tile: 16-byte piece = fragment lane (r, x); elements of tokens 2x, 2x+1, 2x+8, 2x+9, dims r and r + 8.
+// V tile at `tile`: 16-byte piece = fragment lane (r, x): tokens 2x, 2x+1, 2x+8, 2x+9 of dims r and r + 8 (of two groups:
+// 8-bit and low-bit codes, alike here).
 template <int W>
-__device__ __forceinline__ uint4 gather_v(const uint8_t* const* rec, const int* off, int piece) {
+__device__ __forceinline__ uint4 gather_v(const uint8_t* const* rec, const int* off, int piece, int tile) {
     const int l = piece & 31, x = l & 3, r = l >> 2, group = piece >> 5;
-    uint32_t e[2][2][4] = {};   // [group half (8-bit)][dim half][token]
+    auto number = [&](int u) { return tile / 16 + group * 32 + 4 * r + ((u & 7) >> 1); };
+    uint32_t lo[4], hi[4], odd[4];   // the words that hold the token
     #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int t = 2 * x + (k & 1) + 8 * (k >> 1);
-        if (!rec[t]) continue;
-        const int u = off[t];
-        const uint8_t* base = rec[t] + Rec<W == 2 ? kKindBf16 : kKindFp8, 1>::kTile +
-                              (group * 32 + 4 * r + ((u & 7) >> 1)) * 16 + ((u & 1) + 4 * (u >> 3)) * W;
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (W == 2) {
-                e[0][h][k] = *reinterpret_cast<const uint16_t*>(base + h * 4);
-            } else {
-                e[0][h][k] = base[h * 2];
-                e[1][h][k] = base[8 + h * 2];
-            }
+        const uint4 v = source_piece(rec, off, t, number);
+        const bool second = off[t] >> 3;
+        if constexpr (W == 2) {   // words 0, 1 or 2, 3: dims r and r + 8, a half each
+            lo[k] = second ? v.z : v.x;
+            hi[k] = second ? v.w : v.y;
+        } else {                  // words 0, 2 or 1, 3: the two groups, bytes 0, 2 or 1, 3
+            lo[k] = second ? v.y : v.x;
+            hi[k] = second ? v.w : v.z;
         }
+        odd[k] = off[t] & 1;
     }
-    if constexpr (W == 2) {
-        return make_uint4(e[0][0][0] | e[0][0][1] << 16, e[0][1][0] | e[0][1][1] << 16, e[0][0][2] | e[0][0][3] << 16,
-                          e[0][1][2] | e[0][1][3] << 16);
-    } else {
-        auto word = [&](int g, int hi) {
-            const int k = 2 * hi;
-            return e[g][0][k] | e[g][0][k + 1] << 8 | e[g][1][k] << 16 | e[g][1][k + 1] << 24;
-        };
-        return make_uint4(word(0, 0), word(0, 1), word(1, 0), word(1, 1));
-    }
-}
-
-// A low-bit tile's piece: words (kg parity, th) of lane l.  K words hold one token's codes, V bytes
-// two tokens of one dim each.
-__device__ __forceinline__ uint4 gather_low(const uint8_t* const* rec, const int* off, int piece, int tile, bool value) {
-    const int l = piece & 31, x = l & 3, r = l >> 2, group = piece >> 5;
     uint32_t o[4];
     #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const int par = w >> 1, th = w & 1;
-        if (!value) {
-            const int t = r + 8 * th;
-            o[w] = 0;
-            if (rec[t])
-                o[w] = *reinterpret_cast<const uint32_t*>(
-                    rec[t] + ((group * 32 + 4 * (off[t] & 7) + x) * 4 + par * 2 + (off[t] >> 3)) * 4);
-        } else {
-            uint32_t v = 0;
-            #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int t = 2 * x + k + 8 * th;
-                if (!rec[t]) continue;
-                const int u = off[t];
-                const uint8_t* base =
-                    rec[t] + tile + ((group * 32 + 4 * r + ((u & 7) >> 1)) * 4 + par * 2 + (u >> 3)) * 4 + (u & 1);
-                v |= static_cast<uint32_t>(base[0]) << (8 * k) | static_cast<uint32_t>(base[2]) << (8 * k + 16);
-            }
-            o[w] = v;
+    for (int k = 0; k < 4; k += 2) {
+        const uint32_t pick = W == 2 ? (odd[k] ? 0x32u : 0x10u) | (odd[k + 1] ? 0x7600u : 0x5400u)
+                                     : 0x6240u + odd[k] * 0x0101u + odd[k + 1] * 0x1010u;
+        const uint32_t a = __byte_perm(lo[k], lo[k + 1], pick), b = __byte_perm(hi[k], hi[k + 1], pick);
+        if constexpr (W == 2) {   // words: (r, first), (r + 8, first), (r, second), (r + 8, second tokens)
+            o[k] = a;
+            o[k + 1] = b;
+        } else {                  // words: (group, first), (group, second), (group + 1, first), (group + 1, second)
+            o[k / 2] = a;
+            o[2 + k / 2] = b;
         }
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
@@ -240,16 +212,10 @@ template <int KIND, int NG>
 __device__ __forceinline__ uint4 gather_piece(const uint8_t* const* rec, const int* off, int c) {
     using R = Rec<KIND, NG>;
     constexpr int kT = R::kTile / 16;
-    if constexpr (R::kWide) {
-        return c < kT ? gather_k<2>(rec, off, c) : gather_v<2>(rec, off, c - kT);
-    } else if constexpr (R::kLow) {
-        if (c < 2 * kT) return gather_low(rec, off, c < kT ? c : c - kT, R::kTile, c >= kT);
-        return gather_words<NG>(rec, off, c - 2 * kT, 2 * R::kTile);
-    } else {
-        if (c < kT) return gather_k<1>(rec, off, c);
-        if (c < 2 * kT) return gather_v<1>(rec, off, c - kT);
-        return gather_words<1>(rec, off, c - 2 * kT, 2 * R::kTile);
-    }
+    if (c < kT) return gather_k<R::kWide ? 2 : R::kLow ? 0 : 1>(rec, off, c);
+    if (c < 2 * kT) return gather_v<R::kWide ? 2 : 1>(rec, off, c - kT, R::kTile);
+    if constexpr (R::kWide) return make_uint4(0, 0, 0, 0);
+    else return gather_words<R::kLow ? NG : 1>(rec, off, c - 2 * kT, 2 * R::kTile);
 }
 
 constexpr int kGatherThreads = 256;
@@ -264,17 +230,19 @@ __global__ void __launch_bounds__(kGatherThreads) compact_gather_kernel(const Co
     pdl_wait();
     const int tid = threadIdx.x;
     const int b = blockIdx.z, j = blockIdx.x;
-    const int n = p.new_lens[b];
-    if (static_cast<int64_t>(j) * kBs >= n) return;
+    if (j >= p.new_max_blocks) return;
+    const int n = p.new_lens[b];   // these three are under way at once
     const int to = p.new_table[static_cast<int64_t>(b) * p.new_max_blocks + j];
+    const uint32_t from = tid < kBs ? p.source[(static_cast<int64_t>(b) * p.max_blocks + j) * kBs + tid] : 0;
+    if (static_cast<int64_t>(j) * kBs >= n) return;
     if (to < 0 || to >= p.num_blocks + p.host_blocks || p.claim[to] != 2u) {   // no block, or not this one's alone
         if (tid == 0 && blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
         return;
     }
     if (tid == 0 && blockIdx.y == 0 && p.retain) p.retain[to] = 0xffffu;   // `to` is no source: nobody reads its mask
     if (tid < kBs) {
-        src[tid] = p.source[(static_cast<int64_t>(b) * p.max_blocks + j) * kBs + tid];
-        off[tid] = static_cast<int>(src[tid] % kBs);
+        src[tid] = from;
+        off[tid] = static_cast<int>(from % kBs);
     }
     __syncthreads();
     auto record = [&](int64_t id, int layer, int h) -> uint8_t* {
@@ -289,7 +257,9 @@ __global__ void __launch_bounds__(kGatherThreads) compact_gather_kernel(const Co
         if (tid < kBs) rec[k][tid] = src[tid] == kNoSource ? nullptr : record(src[tid] / kBs, layer, h);
         __syncthreads();
         uint4* out = reinterpret_cast<uint4*>(record(to, layer, h));
-        for (int c = tid; c < R::kPieces; c += kGatherThreads) out[c] = gather_piece<KIND, NG>(rec[k], off, c);
+        #pragma unroll
+        for (int c0 = 0; c0 < R::kPieces; c0 += kGatherThreads)
+            if (c0 + tid < R::kPieces) out[c0 + tid] = gather_piece<KIND, NG>(rec[k], off, c0 + tid);
     }
 }
 
@@ -300,7 +270,7 @@ cudaError_t launch_gather(const CompactParams& p, dim3 grid, cudaStream_t stream
 
 }  // namespace
 
-cudaError_t launch_compact(const CompactParams& p, int kind, int ng, cudaStream_t stream) {
+cudaError_t launch_compact(const CompactParams& p, int kind, int ng, int num_sms, cudaStream_t stream) {
     cudaError_t e = launch_dependent(compact_rank_kernel, dim3(static_cast<unsigned>(p.B)), dim3(kRankThreads), 0, -1,
                                      stream, p);
     if (e != cudaSuccess) return e;
@@ -308,8 +278,12 @@ cudaError_t launch_compact(const CompactParams& p, int kind, int ng, cudaStream_
     e = launch_dependent(compact_claim_kernel, claims, dim3(kRankThreads), 0, -1, stream, p);
     if (e != cudaSuccess) return e;
     const int pairs = p.L * p.n_kv;
-    const dim3 grid(static_cast<unsigned>(p.max_blocks), static_cast<unsigned>(pairs < 8 ? pairs : 8),
-                    static_cast<unsigned>(p.B));
+    // Eight shares of the (layer, KV head) pairs a block; more where the blocks alone leave SMs without their
+    // eight CTAs: a share is a chain of loads and stores.
+    const int64_t blocks = static_cast<int64_t>(p.max_blocks) * p.B;
+    const int64_t want = (8 * static_cast<int64_t>(num_sms) + blocks - 1) / blocks;
+    const int64_t shares = min(static_cast<int64_t>(pairs), max(want, static_cast<int64_t>(8)));
+    const dim3 grid(static_cast<unsigned>(p.max_blocks), static_cast<unsigned>(shares), static_cast<unsigned>(p.B));
     switch (kind) {
         case kKindFp8:
         case kKindAngle: return launch_gather<kKindFp8, 1>(p, grid, stream);

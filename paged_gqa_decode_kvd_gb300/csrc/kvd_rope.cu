@@ -145,7 +145,7 @@ __device__ __forceinline__ void put_token(const RopeParams& p, uint8_t* record, 
 // before the angles are there.  Tiles start at a multiple of 16 slots behind the first token's block start, so a
 // chunk of one request fills whole blocks (a record's 16-byte pieces hold two or four of its tokens).
 template <int KIND, int NG, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const RopeParams p) {
     __shared__ RopeSmem s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
