@@ -132,22 +132,34 @@ struct Rec {
     static constexpr int kPieces = kBytes / 16;
 };
 
+// The sources of a block's 16 slots in the record of one (layer, KV head): offset of the token in its record, and the
+// record's place in the first layer's first head's, to which a pair adds its own, by tier.
+struct Sources {
+    const uint8_t* const* rec;
+    const int* off;
+    const bool* host;
+    int64_t device_pair, host_pair;
+    __device__ __forceinline__ const uint8_t* operator[](int t) const {
+        return rec[t] ? rec[t] + (host[t] ? host_pair : device_pair) : nullptr;
+    }
+};
+
 // The source piece of new slot t's token: piece(u) gives its number in the tile for slot offset u.  All lanes load
 // whole 16-byte pieces and pick the token's part: a fourth of the loads that the parts alone would take.
 template <class F>
-__device__ __forceinline__ uint4 source_piece(const uint8_t* const* rec, const int* off, int t, F piece) {
-    const uint8_t* from = rec[t];
+__device__ __forceinline__ uint4 source_piece(const Sources& s, int t, F piece) {
+    const uint8_t* from = s[t];
     if (!from) return make_uint4(0, 0, 0, 0);
-    return __ldg(reinterpret_cast<const uint4*>(from) + piece(off[t]));
+    return __ldg(reinterpret_cast<const uint4*>(from) + piece(s.off[t]));
 }
 
 // K tile: 16-byte piece = fragment lane (r, x) of a group: tokens r and r + 8.  W = bytes of an element; 0: low-bit codes.
 template <int W>
-__device__ __forceinline__ uint4 gather_k(const uint8_t* const* rec, const int* off, int piece) {
+__device__ __forceinline__ uint4 gather_k(const Sources& s, int piece) {
     const int l = piece & 31, x = l & 3, r = l >> 2, group = piece >> 5;
     auto number = [&](int u) { return group * 32 + 4 * (u & 7) + x; };
-    const uint4 a = source_piece(rec, off, r, number), b = source_piece(rec, off, r + 8, number);
-    const bool ah = off[r] >> 3, bh = off[r + 8] >> 3;   // which of the piece's tokens
+    const uint4 a = source_piece(s, r, number), b = source_piece(s, r + 8, number);
+    const bool ah = s.off[r] >> 3, bh = s.off[r + 8] >> 3;   // which of the piece's tokens
     if constexpr (W == 1) {   // pairs of codes: the halves of each word
         const uint32_t pick = (ah ? 0x32u : 0x10u) | (bh ? 0x7600u : 0x5400u);
         return make_uint4(__byte_perm(a.x, b.x, pick), __byte_perm(a.y, b.y, pick), __byte_perm(a.z, b.z, pick),
@@ -160,15 +172,15 @@ __device__ __forceinline__ uint4 gather_k(const uint8_t* const* rec, const int* 
 // V tile at `tile`: 16-byte piece = fragment lane (r, x): tokens 2x, 2x+1, 2x+8, 2x+9 of dims r and r + 8 (of two groups:
 // 8-bit and low-bit codes, alike here).
 template <int W>
-__device__ __forceinline__ uint4 gather_v(const uint8_t* const* rec, const int* off, int piece, int tile) {
+__device__ __forceinline__ uint4 gather_v(const Sources& s, int piece, int tile) {
     const int l = piece & 31, x = l & 3, r = l >> 2, group = piece >> 5;
     auto number = [&](int u) { return tile / 16 + group * 32 + 4 * r + ((u & 7) >> 1); };
     uint32_t lo[4], hi[4], odd[4];   // the words that hold the token
     #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int t = 2 * x + (k & 1) + 8 * (k >> 1);
-        const uint4 v = source_piece(rec, off, t, number);
-        const bool second = off[t] >> 3;
+        const uint4 v = source_piece(s, t, number);
+        const bool second = s.off[t] >> 3;
         if constexpr (W == 2) {   // words 0, 1 or 2, 3: dims r and r + 8, a half each
             lo[k] = second ? v.z : v.x;
             hi[k] = second ? v.w : v.y;
@@ -176,7 +188,7 @@ __device__ __forceinline__ uint4 gather_v(const uint8_t* const* rec, const int* 
             lo[k] = second ? v.y : v.x;
             hi[k] = second ? v.w : v.z;
         }
-        odd[k] = off[t] & 1;
+        odd[k] = s.off[t] & 1;
     }
     uint32_t o[4];
     #pragma unroll
@@ -197,36 +209,40 @@ __device__ __forceinline__ uint4 gather_v(const uint8_t* const* rec, const int* 
 
 // Words after the tiles: [2][16 tokens][words per token]; four words a piece.
 template <int WORDS>
-__device__ __forceinline__ uint4 gather_words(const uint8_t* const* rec, const int* off, int piece, int tiles) {
+__device__ __forceinline__ uint4 gather_words(const Sources& s, int piece, int tiles) {
     uint32_t o[4];
     #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const int i = piece * 4 + w;
         const int side = i / (kBs * WORDS), t = i / WORDS % kBs, g = i % WORDS;
-        o[w] = rec[t] ? reinterpret_cast<const uint32_t*>(rec[t] + tiles)[(side * kBs + off[t]) * WORDS + g] : 0u;
+        const uint8_t* from = s[t];
+        o[w] = from ? __ldg(reinterpret_cast<const uint32_t*>(from + tiles) + (side * kBs + s.off[t]) * WORDS + g) : 0u;
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int KIND, int NG>
-__device__ __forceinline__ uint4 gather_piece(const uint8_t* const* rec, const int* off, int c) {
+__device__ __forceinline__ uint4 gather_piece(const Sources& s, int c) {
     using R = Rec<KIND, NG>;
     constexpr int kT = R::kTile / 16;
-    if (c < kT) return gather_k<R::kWide ? 2 : R::kLow ? 0 : 1>(rec, off, c);
-    if (c < 2 * kT) return gather_v<R::kWide ? 2 : 1>(rec, off, c - kT, R::kTile);
+    if (c < kT) return gather_k<R::kWide ? 2 : R::kLow ? 0 : 1>(s, c);
+    if (c < 2 * kT) return gather_v<R::kWide ? 2 : 1>(s, c - kT, R::kTile);
     if constexpr (R::kWide) return make_uint4(0, 0, 0, 0);
-    else return gather_words<R::kLow ? NG : 1>(rec, off, c - 2 * kT, 2 * R::kTile);
+    else return gather_words<R::kLow ? NG : 1>(s, c - 2 * kT, 2 * R::kTile);
 }
 
-constexpr int kGatherThreads = 256;
+// A thread holds a piece or two: an 8-bit record has 264, a 16-bit one 512.  Every thread slot of an SM is taken (32
+// registers): the gather waits for memory.
+template <int KIND>
+constexpr int gather_threads() { return KIND == kKindFp8 ? 288 : 256; }
 
 // CTA (new block j of request b, share of the (layer, KV head) pairs).
 template <int KIND, int NG>
-__global__ void __launch_bounds__(kGatherThreads) compact_gather_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(gather_threads<KIND>(), 2048 / gather_threads<KIND>()) compact_gather_kernel(const CompactParams p) {
     using R = Rec<KIND, NG>;
-    __shared__ const uint8_t* rec[2][kBs];
+    __shared__ const uint8_t* rec[kBs];
     __shared__ int off[kBs];
-    __shared__ uint32_t src[kBs];
+    __shared__ bool host[kBs];
     pdl_wait();
     const int tid = threadIdx.x;
     const int b = blockIdx.z, j = blockIdx.x;
@@ -240,32 +256,32 @@ __global__ void __launch_bounds__(kGatherThreads) compact_gather_kernel(const Co
         return;
     }
     if (tid == 0 && blockIdx.y == 0 && p.retain) p.retain[to] = 0xffffu;   // `to` is no source: nobody reads its mask
+    auto record = [&](int64_t id) -> uint8_t* {   // of the first layer and head
+        return id < p.num_blocks ? p.kv + id * p.n_kv * R::kBytes : p.host_kv + (id - p.num_blocks) * p.n_kv * R::kBytes;
+    };
     if (tid < kBs) {
-        src[tid] = from;
+        const int64_t id = from / kBs;
+        rec[tid] = from == kNoSource ? nullptr : record(id);
         off[tid] = static_cast<int>(from % kBs);
+        host[tid] = id >= p.num_blocks;
     }
     __syncthreads();
-    auto record = [&](int64_t id, int layer, int h) -> uint8_t* {
-        return id < p.num_blocks
-                   ? p.kv + ((static_cast<int64_t>(layer) * p.num_blocks + id) * p.n_kv + h) * R::kBytes
-                   : p.host_kv + ((static_cast<int64_t>(layer) * p.host_blocks + (id - p.num_blocks)) * p.n_kv + h) * R::kBytes;
-    };
+    uint8_t* const first = record(to);
     const int pairs = p.L * p.n_kv;
-    int k = 0;
-    for (int i = blockIdx.y; i < pairs; i += gridDim.y, k ^= 1) {
-        const int layer = i / p.n_kv, h = i % p.n_kv;
-        if (tid < kBs) rec[k][tid] = src[tid] == kNoSource ? nullptr : record(src[tid] / kBs, layer, h);
-        __syncthreads();
-        uint4* out = reinterpret_cast<uint4*>(record(to, layer, h));
+    #pragma unroll 1
+    for (int i = blockIdx.y; i < pairs; i += gridDim.y) {
+        const int64_t layer = i / p.n_kv, h = i % p.n_kv;
+        const Sources s{rec, off, host, (layer * p.num_blocks * p.n_kv + h) * R::kBytes, (layer * p.host_blocks * p.n_kv + h) * R::kBytes};
+        uint4* out = reinterpret_cast<uint4*>(first + (to < p.num_blocks ? s.device_pair : s.host_pair));
         #pragma unroll
-        for (int c0 = 0; c0 < R::kPieces; c0 += kGatherThreads)
-            if (c0 + tid < R::kPieces) out[c0 + tid] = gather_piece<KIND, NG>(rec[k], off, c0 + tid);
+        for (int c0 = 0; c0 < R::kPieces; c0 += gather_threads<KIND>())
+            if (c0 + tid < R::kPieces) out[c0 + tid] = gather_piece<KIND, NG>(s, c0 + tid);
     }
 }
 
 template <int KIND, int NG>
 cudaError_t launch_gather(const CompactParams& p, dim3 grid, cudaStream_t stream) {
-    return launch_dependent(compact_gather_kernel<KIND, NG>, grid, dim3(kGatherThreads), 0, -1, stream, p);
+    return launch_dependent(compact_gather_kernel<KIND, NG>, grid, dim3(gather_threads<KIND>()), 0, -1, stream, p);
 }
 
 }  // namespace
