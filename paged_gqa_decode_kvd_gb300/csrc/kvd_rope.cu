@@ -142,7 +142,7 @@ __device__ __forceinline__ void put_token(const RopeParams& p, uint8_t* record, 
 }
 
 // CTA (tile of 16 tokens, group of query heads or one KV head).  A thread has all its rows' loads under way
-// before the angles are there.  Tiles start at a multiple of 16 slots behind the first token's block start, so a
+// before the angles are there.  A KV head's tiles start at a multiple of 16 slots behind the first token's block start, so a
 // chunk of one request fills whole blocks (a record's 16-byte pieces hold two or four of its tokens).
 template <int KIND, int NG, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const RopeParams p) {
@@ -150,11 +150,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const Rope
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
-    const int64_t first = p.slot_mapping[0];
-    const int shift = first > 0 ? static_cast<int>(first % kBs) : 0;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTok - shift;
     const int groups = (p.n_q + p.heads_per_cta - 1) / p.heads_per_cta;
     const bool query = static_cast<int>(blockIdx.y) < groups;
+    int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTok;
+    if (!query) {
+        const int64_t first = p.slot_mapping[0];
+        n0 -= first > 0 ? first % kBs : 0;
+    }
     const int h0 = query ? blockIdx.y * p.heads_per_cta : (blockIdx.y - groups) * p.kv_heads_per_cta;
     const int heads = query ? min(p.heads_per_cta, p.n_q - h0) : min(p.kv_heads_per_cta, p.n_kv - h0);
     const int half_id = tid >> 4, lane16 = tid & 15;   // 16 half-warps, a token each
@@ -183,13 +185,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const Rope
         int pos = 0;
         if (ok) {
             pos = p.positions[n];
-            slot = p.slot_mapping[n];
+            if (!query) slot = p.slot_mapping[n];
             if (pos < 0 || pos >= kMaxRopePos) {
                 if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
                 ok = 0;
                 slot = -1;
             } else if (slot >= 0 && slot / kBs >= p.num_blocks + p.host_blocks) {
-                if (blockIdx.y == 0) report(p.err, KVD_ERR_OOB);
+                if (h0 == 0) report(p.err, KVD_ERR_OOB);
                 slot = -1;
             }
         }
