@@ -33,7 +33,8 @@ struct RopeSmem {
     int shared_offset;                                     // two tokens want the same slot offset
 };
 
-// (cos, sin)·m of a lane's 8 consecutive dims (lane16 = lane % 16): by pair if neighbours are paired, else by dim.
+// (cos, sin)·m of a lane's 8 consecutive dims (lane16 = lane % 16): by pair if neighbours are paired, else by dim, where
+// the sine has the sign with which it multiplies the partner.
 template <bool INTERLEAVED>
 __device__ __forceinline__ void lane_factors(float2 (&f)[8], const float2* cs, int rot, int lane16) {
     const int half = rot >> 1;
@@ -42,6 +43,7 @@ __device__ __forceinline__ void lane_factors(float2 (&f)[8], const float2* cs, i
         const int d = lane16 * 8 + e;
         f[e] = make_float2(1.f, 0.f);
         if (INTERLEAVED ? (e < 4 && lane16 * 4 + e < half) : d < rot) f[e] = cs[INTERLEAVED ? lane16 * 4 + e : d < half ? d : d - half];
+        if (!INTERLEAVED && d < half) f[e].y = -f[e].y;
     }
 }
 
@@ -83,7 +85,7 @@ __device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2 (&f)[8], int
             for (int k = 0; k < 2; ++k) {
                 const int e = 2 * i + k;
                 const float b = k ? pv.y : pv.x;
-                y[e] = low ? x[e] * f[e].x - b * f[e].y : b * f[e].y + x[e] * f[e].x;
+                y[e] = fmaf(b, f[e].y, x[e] * f[e].x);
             }
         }
     } else {
@@ -101,7 +103,7 @@ __device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2 (&f)[8], int
             }
             const float2 pv = unpack_bf16(pw);
             const float b = (pd & 1) ? pv.y : pv.x;
-            y[e] = low ? x[e] * f[e].x - b * f[e].y : b * f[e].y + x[e] * f[e].x;
+            y[e] = fmaf(b, f[e].y, x[e] * f[e].x);
         }
     }
     #pragma unroll
@@ -109,7 +111,7 @@ __device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2 (&f)[8], int
         // dims past rot keep their bits (a NaN's payload too)
         const int d = lane16 * 8 + 2 * i;
         const uint32_t v = pack_bf16(y[2 * i], y[2 * i + 1]);
-        out[i] = d + 1 < rot ? v : d >= rot ? w[i] : (v & 0xffffu) | (w[i] & 0xffff0000u);
+        out[i] = rot == kDh || d + 1 < rot ? v : d >= rot ? w[i] : (v & 0xffffu) | (w[i] & 0xffff0000u);
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
