@@ -7,29 +7,40 @@
 //   out = Σ_t softmax(l)_t · V_t,  lse = log Σ_t exp(l_t).
 //
 // Work.  A unit is (request, KV head, TQ = ⌊256/g⌋ new tokens): up to 256 rows (token, head of the
-// group) that share every K and V.  Its cost is its tiles of 64 positions up to its last row's.  The
-// units' tiles, laid end to end, are cut into equal ranges, one per CTA (one CTA per SM), so every
-// CTA does the same number of tiles whatever the batch holds; a unit cut by a range border leaves
+// group) that share every K and V.  Its cost is its tiles of 64 positions up to its last row's, and a few
+// tiles' time for its start and end.  The units' costs, laid end to end, are cut into equal shares, one per CTA
+// (one CTA per SM), so every CTA does the same work whatever the batch holds; a unit cut by a border leaves
 // fp32 partials (unnormalised sum, maximum, sum of weights) that chunk_combine_kernel joins.
 //
-// One CTA, four roles:
+// One CTA, 20 warps:
 //  * producer warp: follows the block table and bulk-copies (TMA engine) the four 16-token records
 //    of a tile into a raw ring;
-//  * repack warpgroup: turns the records' mma.m16n8k16 fragment order into the 128-byte-swizzled
-//    K-major operands the tensor cores read, by 16-byte shared loads and stores and register renaming
-//    only.  A K piece holds four dims of tokens t and t + 8: two pieces give eight dims of each, so
+//  * two repack warpgroups, one for K and one for V: turn the records' mma.m16n8k16 fragment order into the
+//    128-byte-swizzled K-major operands the tensor cores read, by 16-byte shared loads and stores and register
+//    renaming only.  A K piece holds four dims of tokens t and t + 8: two pieces give eight dims of each, so
 //    the operand's dims stand in the order 32j + {2x, 2x+1, 2x+8, 2x+9, 16 + the same} (q is laid
 //    out alike, the product does not care).  A V piece holds four tokens of dims r and r + 8: the pieces
 //    of two blocks give eight tokens of each, which fixes the order of a tile's 64 columns:
 //    column 32p + 8x + 4u + w = token 2x + (w & 1) + 8(w >> 1) of block 2p + u.  8-bit codes become
 //    bf16 exactly on the way; low-bit codes become bf16(code·scale + zero);
-//  * MMA warp: issues S = Q·K^T and O += P·V, Q and P from tensor memory (reading them
-//    from shared memory would take its whole bandwidth), accumulators in tensor memory;
+//  * two warps that issue S = Q·K^T, one for each softmax warpgroup, and one that issues O += P·V for both; Q, K and V
+//    from shared memory, P and the accumulators in tensor memory;
 //  * two softmax warpgroups, one thread a row: online softmax in fp32 (exp2 domain), P back to tensor
-//    memory as bf16.  The reference maximum moves only when a row's maximum passes it by 8 (weights up
-//    to 2^8), so O is rarely rescaled.
+//    memory as bf16, over the S it came from.  A warpgroup has two S: the next is ready when a step ends, so a step
+//    has one wait and one arrival.  The reference maximum moves only when a row's maximum passes it by 8
+//    (weights up to 2^8), so O is rarely rescaled.
 // With more than 128 rows the warpgroups take 128 rows each and share every tile; with fewer they
 // take the even and the odd tiles of the same rows and are merged at the unit's end.
+//
+// Waits.  Each barrier's waiter is at most one phase behind it: a tile's stages, its S and its P are handed on in
+// order, and where a warpgroup might be ahead or behind (tiles of one warpgroup only, a segment's end) it waits for
+// the phase before first.  Every wait gives up after a second or so; the kernel then reports it and ends.
+//
+// Bound, BF16, 32 + 8 heads: 2,048 tokens behind 8,192 take 266 us, 1.16 PFLOP/s (61% of the measured matrix rate).  A tile of
+// 256 rows takes about 1,900 cycles: the MMAs 1,300 (their A and B from shared memory: 128 of its 224 KB a tile; the copies
+// and the repack move the rest), a softmax step 1,500 behind the one before it.  Without its repack it would
+// take 250 us, without its exponentials 255: no one role stands out.  32 × 5 tokens behind 8,187 stream the cache at
+// 5.4 TB/s (82% of the measured bandwidth).
 //
 // 8-bit records: the K scale multiplies the fp32 logit, the V scale the fp32 weight before it is
 // rounded, so codes enter the MMAs exactly.  Angle-domain keys: q enters as its direction code, with
@@ -54,11 +65,15 @@ constexpr int kThreads = 640;          // softmax 2 × 128, repack of K 128, of 
 constexpr int kKeyWarp = 8, kValueWarp = 12, kProducerWarp = 16, kScoreWarp = 17, kOutWarp = 19;
 constexpr int kOpBytes = 16384;
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
-constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kTries = 200000;         // tries of a wait: a second or so
+constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
+constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so (a clock read a try costs more than the wait)
 constexpr int kColS = 0, kColO = 256;   // tensor memory columns: S and P 2 × 2 × 64, O 2 × 128
-constexpr int kMinTiles = 4;           // smallest share of a CTA
-constexpr int kUnitTiles = 6;          // what a unit costs beside its tiles (its Q, its first S, its rows out), in tiles
+// Smallest share of a CTA.  Four tokens behind 1,019 take 30.7, 21.1, 22.6, 16.1, 20.7, 17.6 us with 1, 2, 3, 4, 6, 8:
+// a smaller share leaves more parts to join, and a share that does not divide the units leaves two parts a CTA.
+constexpr int kMinTiles = 4;
+// What a unit costs beside its tiles (its Q, its first S, its rows out), in tiles.  A serving batch (units of 1 to 260
+// tiles) takes 668, 496, 405, 357, 360, 383 us with 0, 2, 4, 6, 8, 12; a whole prompt of 8,192 598, 556, 515, 476, 475, 486.
+constexpr int kUnitTiles = 6;
 constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
@@ -275,7 +290,8 @@ __device__ inline void make_schedule(const ChunkParams& p, S& s, int64_t* scratc
                 int a = 0, z = (r.T + tq - 1) / tq;   // the last unit of [a, z) that starts at or before `in`
                 while (z - a > 1) {
                     const int step = (z - a + 31) / 32, mid = a + lane * step;
-                    const int n = __popc(__ballot_sync(kFull, mid < z && tiles_before(r, mid, tq) + static_cast<int64_t>(mid) * extra <= in));
+                    const bool at_or_before = mid < z && tiles_before(r, mid, tq) + static_cast<int64_t>(mid) * extra <= in;
+                    const int n = __popc(__ballot_sync(kFull, at_or_before));
                     a += (n - 1) * step;
                     z = min(z, a + step);
                 }
@@ -859,7 +875,8 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
     const uint32_t k_op = uniform(smem_u32(s.k)), q_op = uniform(smem_u32(s.q));
     Walk walk(p, s);
     Segment g;
-    uint32_t base = 0, done = 0, own = 0, ones = 0;   // tiles before the segment, of both and of this warpgroup; phases of q_ready, q_one
+    uint32_t base = 0, done = 0;   // tiles before the segment, of both and of this warpgroup
+    uint32_t own = 0, ones = 0;    // phases of q_ready and q_one
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const uint32_t n = uniform(g.t1 - g.t0), two = uniform(g.two);
@@ -931,6 +948,11 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
     if (!ok) drain_mma(s, 2);
 }
 
+// The E4M3 value nearest to x.
+__device__ __forceinline__ float e4m3_value(float x) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+}
+
 // A warp's 32 rows of q as the A operand, in the dim order of the K operand.  base: the unit's first token; rel: the
 // lane's row counted from there, −1 for none.  Eight lanes read half a row: dims 8c .. 8c+7 are words c & 3 of four
 // 16-byte pieces.  Returns what multiplies the row's logits (angle keys; 1 else).
@@ -970,8 +992,7 @@ __device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool 
             for (int x = 0; x < 8; ++x) {
                 const float2 f = unpack_bf16(e[x >> 2][i][x & 3]);
                 const float a = __fdiv_rn(f.x, sc), b = __fdiv_rn(f.y, sc);
-                const float da = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
-                const float db = __half2float(__half(__nv_cvt_fp8_to_halfraw(__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3), __NV_E4M3)));
+                const float da = e4m3_value(a), db = e4m3_value(b);
                 r2 += a * a + b * b;
                 d2 += da * da + db * db;
                 e[x >> 2][i][x & 3] = pack_bf16(da, db);
@@ -991,9 +1012,10 @@ __device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool 
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int row = 32 * warp + 4 * i + (lane >> 3);
+            uint8_t* to = op + half * kOpBytes + row * 128 + (c & 3) * 4;
             #pragma unroll
             for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint32_t*>(op + half * kOpBytes + row * 128 + (((4 * (c >> 2) + x) ^ (row & 7)) << 4) + (c & 3) * 4) = e[half][i][x];
+                *reinterpret_cast<uint32_t*>(to + (((4 * (c >> 2) + x) ^ (row & 7)) << 4)) = e[half][i][x];
         }
     }
     fence_proxy_async_shared();
@@ -1316,10 +1338,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem<KIND>& s = *reinterpret_cast<Smem<KIND>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (smem_u32(smem_raw) & 1023u) {   // the operands' swizzle wants it (and nothing else stands before it)
-        if (tid == 0) report(p.err, KVD_ERR_CUDA);
-        return;
-    }
     if (warp == kScoreWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
         for (int i = 0; i < Smem<KIND>::kRaw; ++i) {
@@ -1353,6 +1371,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     pdl_trigger();
     if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
     make_schedule(p, s, reinterpret_cast<int64_t*>(s.q));
+    if (tid == 0 && (smem_u32(smem_raw) & 1023u)) {   // the operands' swizzle wants it (nothing else stands before them)
+        report(p.err, KVD_ERR_CUDA);
+        s.remaining = 0;
+    }
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
