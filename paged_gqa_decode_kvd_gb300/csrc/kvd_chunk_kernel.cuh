@@ -49,7 +49,8 @@
 // Masked positions: logits become −inf by selection and V is zeroed, so what a slot holds does not
 // matter.  Inside the chunk a token's V is attended by later rows and masked for earlier ones, and
 // 0·NaN would reach the earlier ones: non-finite V there is zeroed too, noted, and added at the end
-// to the rows that attend it.
+// to the rows that attend it.  An 8-bit V whose scale is not finite (its token held an infinity: every code is zero
+// or NaN, every product NaN) is left out everywhere and makes NaN of the rows that attend it.
 #pragma once
 
 #include "kvd_chunk.h"
@@ -96,6 +97,7 @@ struct TileInfo {
     alignas(16) float limit[kTile];   // column: −inf where the position may not be attended, else +inf
     unsigned long long mask;          // bit 16·block + t: position may be attended
     unsigned long long nonfin[4];     // by repack warp; column n: its V has non-finite elements, zeroed in the operand
+    unsigned long long wild;          // like mask: the V factor is not finite, and zero in the table
 };
 constexpr int kFlags = 5;           // tiles that hold positions of a unit's own tokens: ⌈(63 + 256)/64⌉
 
@@ -806,7 +808,10 @@ __device__ __forceinline__ void key_repacker(Smem<KIND>& s, const ChunkParams& p
                 const bool on = mine >> lane & 1u, wide = KIND == kKindMixed && f == kFmtBf16;
                 const int n = column_of(warp, lane);
                 s.factor[in][0][n] = wide ? 1.f : sc[lane];
-                s.factor[in][1][n] = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
+                const float v = !on ? 0.f : wide ? 1.f : sc[kBs + lane];
+                const unsigned wild = __ballot_sync(0xffffu, !isfinite(v));
+                s.factor[in][1][n] = isfinite(v) ? v : 0.f;
+                if (lane == 0) reinterpret_cast<uint16_t*>(&s.info[in].wild)[warp] = static_cast<uint16_t>(wild);
             }
             if (KIND == kKindMixed && f == kFmtBf16) repack_k<kFmtBf16>(code, s.k[ks], off);
             else if (KIND == kKindMixed && f == kFmtE5m2) repack_k<kFmtE5m2>(code, s.k[ks], off);
@@ -1070,6 +1075,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
         }
         float m = -INFINITY, l = 0.f;
         unsigned flagged = 0;                     // tiles with noted V, from the first token's
+        float poison = 0.f;                       // NaN where a position with a wild V factor is attended
         const int tile0 = max(g.first, 0) / kTile;
         for (int i = 0; i < mine; ++i) {
             const uint32_t k = base + (g.two ? i : 2 * i + w);
@@ -1114,6 +1120,9 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     x[c + 2] = fminf(x[c + 2], f.z);
                     x[c + 3] = fminf(x[c + 3], f.w);
                 }
+            }
+            if constexpr (has_factors(KIND)) {
+                if (s.info[in].wild & may) poison = NAN;
             }
             float part[4];   // four chains
             #pragma unroll
@@ -1190,6 +1199,20 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
             if (mine > 1 && !wait_bar(s, &s.pv_done[w][done & 1], (done - 2) >> 1)) return;
             if (!wait_bar(s, &s.pv_done[w][(done - 1) & 1], (done - 1) >> 1)) return;
             tcgen_fence_after();
+        }
+        if constexpr (has_factors(KIND)) {
+            if (__any_sync(kFull, poison != 0.f)) {
+                #pragma unroll 1
+                for (int c = 0; c < kDh; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(col_o + c, o);
+                    tmem_wait_ld(o);
+                    #pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + poison);
+                    tmem_st16(col_o + c, o);
+                }
+                tmem_wait_st();
+            }
         }
         base += n;
         const bool merging = !g.two && n > 1;   // both warpgroups hold a part of the rows

@@ -156,6 +156,58 @@ def test_a_bad_value_reaches_its_own_rows_only(cuda_device, value):
     assert_within(lse, rlse, ltol, "lse")
 
 
+@pytest.mark.parametrize("q_len,n_q", [(40, 4), (20, 1)])
+@pytest.mark.parametrize("kind", ["fp8", "angle", "mixed", "int4", "int2"])
+def test_masked_slots_of_any_format_may_hold_anything(cuda_device, kind, q_len, n_q):
+    """NaN and infinities in evicted slots and behind the last position, in tiles with and without new tokens."""
+    c = Case(cuda_device, kind, n_q, 1, [q_len], [300], seed=29, evict=0.2)
+    ref, rlse, tol, ltol = c.reference()
+    bad = torch.full((1, 1, 128), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    for p in range(304):
+        blk, t = int(c.bt[0, p // 16]), p % 16
+        if p >= 300 or not (int(c.retain[blk]) >> t) & 1:
+            x = bad if p % 2 else torch.full_like(bad, float("inf"))
+            kvd.kvd_append_kv(c.pool.handle, 0, x, x, torch.tensor([blk * 16 + t], device=cuda_device))
+    out, lse = c.run()
+    assert_within(out.double().cpu().numpy(), ref, tol, "out")
+    assert_within(lse.double().cpu().numpy(), rlse, ltol, "lse")
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n_q", [1, 4])
+@pytest.mark.parametrize("kind", ["fp8", "angle", "mixed", "int4"])
+def test_a_bad_value_of_any_format_spares_earlier_rows(cuda_device, kind, n_q, value):
+    """A non-finite V of new token 23 reaches rows 23 and later and no earlier row; the logits do not know of it."""
+    c = Case(cuda_device, kind, n_q, 1, [40], [100], seed=30)
+    ref, rlse, tol, ltol = c.reference()
+    pos = 60 + 23
+    blk, t = int(c.bt[0, pos // 16]), pos % 16
+    good = torch.from_numpy(np.random.default_rng(31).standard_normal((1, 1, 128))).bfloat16().to(cuda_device)
+    v = good.clone()
+    v[0, 0, 77] = value
+    slot = np.array([blk * 16 + t])
+    kvd.kvd_append_kv(c.pool.handle, 0, good, v, torch.from_numpy(slot).to(cuda_device))
+    assert c.opool.append(good.float().cpu().numpy(), good.float().cpu().numpy(), slot) == 0
+    ref, rlse, tol, ltol = c.reference()
+    out, lse = (x.double().cpu().numpy() for x in c.run())
+    assert_within(out[:23], ref[:23], tol[:23], "earlier rows")
+    assert_within(lse, rlse, ltol, "lse")
+    # (a low-bit record is finite whatever it is given: codes are clamped, and its scale and zero saturate in 16 bits)
+    assert kind == "int4" or not np.isfinite(out[23:, :, 77]).any()
+
+
+@pytest.mark.parametrize("kind,n_q", [("fp8", 4), ("fp8", 1), ("angle", 4)])
+def test_a_bad_cached_value_reaches_every_row(cuda_device, kind, n_q):
+    """An infinity in the cache ahead of the new tokens makes an 8-bit record's scale infinite: NaN in all rows."""
+    c = Case(cuda_device, kind, n_q, 1, [40], [300], seed=32)
+    blk, t = int(c.bt[0, 70 // 16]), 70 % 16
+    v = torch.ones((1, 1, 128), dtype=torch.bfloat16, device=cuda_device)
+    v[0, 0, 5] = float("inf")
+    kvd.kvd_append_kv(c.pool.handle, 0, torch.zeros_like(v), v, torch.tensor([blk * 16 + t], device=cuda_device))
+    out, lse = (x.double().cpu().numpy() for x in c.run())
+    assert np.isnan(out).all() and np.isfinite(lse).all()
+
+
 def test_a_nan_query_stays_in_its_row(cuda_device):
     c = Case(cuda_device, "bf16", 4, 1, [10], [100], seed=11)
     c.q[4, 2, 5] = float("nan")
