@@ -1393,6 +1393,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     pdl_wait();
     pdl_trigger();
     if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
+    static_assert(2 * kMaxBatch * sizeof(int64_t) <= sizeof(s.q), "the schedule's scratch");
     make_schedule(p, s, reinterpret_cast<int64_t*>(s.q));
     if (tid == 0 && (smem_u32(smem_raw) & 1023u)) {   // the operands' swizzle wants it (nothing else stands before them)
         report(p.err, KVD_ERR_CUDA);
