@@ -14,12 +14,12 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_combine_kernel(const Chunk
     pdl_trigger();
     int slot = 2 * blockIdx.x;
     int4 seg = p.part_seg[slot];
-    if (seg.x < 0 || seg.z != 0) {
+    if (seg.x < 0 || (seg.z & 1)) {   // not the first part of a unit
         seg = p.part_seg[++slot];
-        if (seg.x < 0 || seg.z != 0) return;
+        if (seg.x < 0 || (seg.z & 1)) return;
     }
     const int tq = kUnitRows / p.g;
-    const int b = seg.x, h = seg.y & 0xffff, qt = seg.y >> 16;
+    const int b = seg.x, h = seg.z >> 1, qt = seg.y;
     const Request r = load_request(p, b, false);
     const int tiles = unit_tiles(r, qt, tq);
     const int rows = min(tq, r.T - qt * tq) * p.g;

@@ -47,7 +47,7 @@ struct ChunkParams {
     float* lse_out;
     float* part;                 // workspace: [2·CTAs][128 dims][256 rows] unnormalised sums
     float* part_ml;              // workspace: [2·CTAs][2][256] maximum (log2 domain), sum of weights
-    int4* part_seg;              // workspace: [2·CTAs] (request or −1, head | unit << 16, first tile, end tile)
+    int4* part_seg;              // workspace: [2·CTAs] (request or −1, unit, head << 1 | not its first part, end tile)
     int32_t* err;
     int64_t num_blocks;
     int64_t host_blocks;

@@ -1346,7 +1346,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 p.lse_out[first_row + rel] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
             }
         }
-        if (tid == 0 && w == 0 && !whole) p.part_seg[slot] = make_int4(g.b, g.h | g.qt << 16, g.t0, g.t1);
+        if (tid == 0 && w == 0 && !whole) p.part_seg[slot] = make_int4(g.b, g.qt, g.h << 1 | (g.t0 > 0), g.t1);
         if (!g.two) {
             tcgen_fence_before();
             __syncwarp();
