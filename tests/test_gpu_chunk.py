@@ -208,6 +208,21 @@ def test_a_bad_cached_value_reaches_every_row(cuda_device, kind, n_q):
     assert np.isnan(out).all() and np.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "mixed"])
+@pytest.mark.parametrize("q_lens,lens,n_q", [([1], [3], 1), ([1, 4, 2], [7, 60, 700], 4), ([100], [130], 8), ([128], [900], 8)])
+def test_few_rows_keep_the_weights_precision(cuda_device, kind, q_lens, lens, n_q):
+    """Up to 1,024 rows a weight is the sum of two bf16: off by 2^-9 · 2^-9 of itself.  Its logit, an fp32 sum of 128
+    products and a multiplication, adds less than 2^-17 of it at |l| < 16, the fp32 sums over 900 positions less than
+    2^-16 together: 2^-15 of the weighted mean of |v| bounds them all (a weight of 8 bits alone would be off by 2^-9)."""
+    c = Case(cuda_device, kind, n_q, 1, q_lens, lens, seed=33)
+    assert sum(q_lens) * n_q <= 1024
+    out, _ = c.run()
+    ref = c.reference()[0]
+    k, v = c.opool.values()
+    size = chunk_ref(k, np.abs(v), c.q.double().numpy(), c.start, c.bt, c.lens, None, 128 ** -0.5)[0]
+    assert (np.abs(out.double().cpu().numpy() - ref) <= 2.0 ** -15 * size).all()
+
+
 def test_a_nan_query_stays_in_its_row(cuda_device):
     c = Case(cuda_device, "bf16", 4, 1, [10], [100], seed=11)
     c.q[4, 2, 5] = float("nan")
