@@ -388,3 +388,70 @@ def test_one_token_agrees_with_the_decode(cuda_device):
     _, _, tol, ltol = c.reference()
     assert_within(out.double().cpu().numpy(), o.double().cpu().numpy(), 2 * tol, "out")
     assert_within(lse.double().cpu().numpy(), z.double().cpu().numpy(), 2 * ltol, "lse")
+
+
+def run_many_rows(c):
+    """The call with rows behind the last request, more than 1,024 in all: those stay as they were."""
+    d, n = c.device(), c.q.shape[0]
+    d["q"] = torch.cat([d["q"], torch.full((1024 // c.n_q + 1, c.n_q, 128), float("nan"), dtype=torch.bfloat16, device=c.dev)])
+    out, lse = c.run(d=d)
+    assert (out[n:] == 9.0).all() and (lse[n:] == 9.0).all()
+    return out[:n].double().cpu().numpy(), lse[:n].double().cpu().numpy()
+
+
+def check_many_rows(c):
+    out, lse = run_many_rows(c)
+    ref, rlse, tol, ltol = c.reference()
+    assert kvd.kvd_get_device_error(c.pool.handle) == kvd.KVD_OK
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("g", [1, 3, 4, 7, 8])
+def test_many_rows_kinds_and_groups(cuda_device, kind, g):
+    check_many_rows(Case(cuda_device, kind, 2 * g, 2, [33, 1, 70], [97, 40, 133], seed=40 + g))
+
+
+@pytest.mark.parametrize("q_len,ctx", [(1, 0), (1, 63), (1, 64), (1, 1000), (16, 0), (64, 0), (65, 63), (200, 511)])
+@pytest.mark.parametrize("n_q", [4, 7])
+def test_many_rows_lengths(cuda_device, q_len, ctx, n_q):
+    check_many_rows(Case(cuda_device, "bf16", n_q, 1, [q_len], [q_len + ctx], seed=50 + q_len))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "mixed", "int4", "angle"])
+def test_many_rows_ragged_with_evictions(cuda_device, kind):
+    check_many_rows(Case(cuda_device, kind, 8, 2, [1, 0, 37, 4, 90, 1, 2, 300], [513, 100, 37, 260, 333, 1, 70, 301], seed=60,
+                         evict=0.3, factor=2.0))
+    check_many_rows(Case(cuda_device, kind, 4, 1, [3, 5], [9000, 4000], seed=61))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kind,n_q", [("bf16", 1), ("bf16", 4), ("fp8", 1), ("fp8", 4), ("angle", 4), ("mixed", 4)])
+def test_many_rows_a_bad_value_spares_earlier_rows(cuda_device, kind, n_q, value):
+    c = Case(cuda_device, kind, n_q, 1, [40], [100], seed=62)
+    pos = 60 + 23
+    blk, t = int(c.bt[0, pos // 16]), pos % 16
+    good = torch.from_numpy(np.random.default_rng(63).standard_normal((1, 1, 128))).bfloat16().to(cuda_device)
+    v = good.clone()
+    v[0, 0, 77] = value
+    slot = np.array([blk * 16 + t])
+    kvd.kvd_append_kv(c.pool.handle, 0, good, v, torch.from_numpy(slot).to(cuda_device))
+    assert c.opool.append(good.float().cpu().numpy(), good.float().cpu().numpy(), slot) == 0
+    ref, rlse, tol, ltol = c.reference()
+    out, lse = run_many_rows(c)
+    assert_within(out[:23], ref[:23], tol[:23], "earlier rows")
+    assert_within(lse, rlse, ltol, "lse")
+    assert not np.isfinite(out[23:, :, 77]).any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "mixed", "int4"])
+def test_many_rows_masked_slots_may_hold_anything(cuda_device, kind):
+    c = Case(cuda_device, kind, 4, 1, [40], [300], seed=64, evict=0.2)
+    bad = torch.full((1, 1, 128), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+    for p in range(304):
+        blk, t = int(c.bt[0, p // 16]), p % 16
+        if p >= 300 or not (int(c.retain[blk]) >> t) & 1:
+            x = bad if p % 2 else torch.full_like(bad, float("inf"))
+            kvd.kvd_append_kv(c.pool.handle, 0, x, x, torch.tensor([blk * 16 + t], device=cuda_device))
+    check_many_rows(c)
