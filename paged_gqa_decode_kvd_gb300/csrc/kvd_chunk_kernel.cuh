@@ -77,7 +77,8 @@ constexpr int kMinTiles = 4;
 constexpr int kUnitTiles = 6;
 // P's rounding to bf16 is off by about as much as the output's: 1.4 times the error together, on average over a call.
 // In a call of few rows it does not average out, and the tensor cores have time: there (FINE) P goes into the product as
-// the rounded value and the rounded remainder.  In every call that would cost 10 to 35% (the products, and registers).
+// the rounded value and the rounded remainder.  Four tokens behind 1,019 take 16.9 us so, 16.2 without; 2,048 behind
+// 8,192 would take 343 instead of 270, 32 × 5 behind 8,187 222 instead of 204, 512 behind 130,560 (FP8) 2,800 instead of 2,018.
 constexpr int64_t kFineRows = 1024;
 constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
 
