@@ -26,7 +26,9 @@
 //  * two warps that issue S = Q·K^T, one for each softmax warpgroup, and one that issues O += P·V for both; Q, K and V
 //    from shared memory, P and the accumulators in tensor memory;
 //  * two softmax warpgroups, one thread a row: online softmax in fp32 (exp2 domain), P back to tensor
-//    memory as bf16, over the S it came from.  A warpgroup has two S: the next is ready when a step ends, so a step
+//    memory, over the S it came from, as the value rounded to bf16 and the rounded remainder (two products: a weight is
+//    off by 2^-16; rounded once, by 2^-8, an output whose terms cancel would be off by more than the tolerance of the
+//    decode's outputs, 2e-3 + 1e-2 of the value).  A warpgroup has two S: the next is ready when a step ends, so a step
 //    has one wait and one arrival.  The reference maximum moves only when a row's maximum passes it by 8
 //    (weights up to 2^8), so O is rarely rescaled.
 // With more than 128 rows the warpgroups take 128 rows each and share every tile; with fewer they
@@ -75,11 +77,6 @@ constexpr int kMinTiles = 4;
 // What a unit costs beside its tiles (its Q, its first S, its rows out), in tiles.  A serving batch (units of 1 to 260
 // tiles) takes 668, 496, 405, 357, 360, 383 us with 0, 2, 4, 6, 8, 12; a whole prompt of 8,192 598, 556, 515, 476, 475, 486.
 constexpr int kUnitTiles = 6;
-// P's rounding to bf16 is off by about as much as the output's: 1.4 times the error together, on average over a call.
-// In a call of few rows it does not average out, and the tensor cores have time: there (FINE) P goes into the product as
-// the rounded value and the rounded remainder.  Four tokens behind 1,019 take 16.9 us so, 16.2 without; 2,048 behind
-// 8,192 would take 343 instead of 270, 32 × 5 behind 8,187 222 instead of 204, 512 behind 130,560 (FP8) 2,800 instead of 2,018.
-constexpr int64_t kFineRows = 1024;
 constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
@@ -919,7 +916,7 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
 }
 
 // O += P(i)·V(i) of both warpgroups, by one warp, when P(i) is in tensor memory; W = 0, 1 in turn.
-template <int KIND, bool FINE>
+template <int KIND>
 __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) {
     constexpr uint32_t kDescO = mma_desc_bf16(kWgRows, kDh);
     constexpr int kStages = Smem<KIND>::kStages;
@@ -945,10 +942,8 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
             if (elect_one()) {
                 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
-                if constexpr (FINE) {
-                    #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + 32 + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, 1u);
-                }
+                #pragma unroll   // the remainders
+                for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + 32 + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, 1u);
                 mma_commit(full);
                 mma_commit(empty);
                 if (!two) mbar_arrive(&s.v_empty[st]);
@@ -1036,7 +1031,7 @@ __device__ __forceinline__ float load_query(const uint16_t* base, int rel, bool 
     return factor;
 }
 
-template <int KIND, bool FINE>
+template <int KIND>
 __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& p, int w, int tid, int lane) {
     const uint32_t lanes = static_cast<uint32_t>((tid >> 5) & 3) << 21;   // this warp's 32 tensor memory lanes
     constexpr int kStages = Smem<KIND>::kStages;
@@ -1186,15 +1181,12 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                 pw[((c / 2) & 15) + 1] = pack_bf16(x[c + 2], x[c + 3]);
                 if ((c & 31) == 28) {
                     tmem_st16(cols + (c >> 5) * 16, pw);
-                    if constexpr (FINE) {   // the remainders, in the columns behind
-                        #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 v = unpack_bf16(pw[e]), of = make_float2(x[(c & 32) + 2 * e], x[(c & 32) + 2 * e + 1]);
-                            const float2 rest = add2(of, make_float2(-v.x, -v.y));
-                            pw[e] = isfinite(rest.x + rest.y) ? pack_bf16(rest.x, rest.y) : 0u;
-                        }
-                        tmem_st16(cols + 32 + (c >> 5) * 16, pw);
+                    #pragma unroll   // the remainders, in the columns behind (weight · V scale < 2^8 · 2^128/448 is finite)
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 v = unpack_bf16(pw[e]), of = make_float2(x[(c & 32) + 2 * e], x[(c & 32) + 2 * e + 1]);
+                        pw[e] = pack_bf16(of.x - v.x, of.y - v.y);
                     }
+                    tmem_st16(cols + 32 + (c >> 5) * 16, pw);
                 }
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -1376,7 +1368,7 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
     }
 }
 
-template <int KIND, bool FINE>
+template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem<KIND>& s = *reinterpret_cast<Smem<KIND>*>(smem_raw);
@@ -1432,7 +1424,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
                   "a request beyond what the launch has would not return");
     if (warp < 8) {
         take_registers<kSoftmaxRegs>();
-        softmax_group<KIND, FINE>(s, p, warp >> 2, tid & 127, lane);
+        softmax_group<KIND>(s, p, warp >> 2, tid & 127, lane);
     } else if (warp < kValueWarp) {
         give_registers<kKeyRegs>();
         key_repacker<KIND>(s, p, warp - kKeyWarp, lane);
@@ -1443,7 +1435,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         give_registers<kIssueRegs>();
         if (warp == kProducerWarp) producer<KIND>(s, p, lane);
         else if (warp < kOutWarp) score_issuer<KIND>(s, p, warp - kScoreWarp);
-        else out_issuer<KIND, FINE>(s, p);
+        else out_issuer<KIND>(s, p);
     }
     __syncwarp();
     tcgen_fence_before();
@@ -1453,21 +1445,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     if (warp == kScoreWarp) tmem_free_all(s.tmem);
 }
 
-template <int KIND, bool FINE>
-cudaError_t launch_variant(const ChunkParams& p, int grid, cudaStream_t stream) {
+template <int KIND>
+cudaError_t launch_kind(const ChunkParams& p, int grid, cudaStream_t stream) {
     const size_t smem = sizeof(Smem<KIND>);
     static_assert(sizeof(Smem<KIND>) <= 232448, "shared memory of one SM");
     static_assert(max_record(KIND) % 16 == 0 && sizeof(TileInfo) % 16 == 0, "16-byte accesses");
     const cudaError_t e =
-        cudaFuncSetAttribute(chunk_kernel<KIND, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaFuncSetAttribute(chunk_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_dependent(chunk_kernel<KIND, FINE>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, -1, stream, p);
-}
-
-template <int KIND>
-cudaError_t launch_kind(const ChunkParams& p, int grid, cudaStream_t stream) {
-    return static_cast<int64_t>(p.n_tokens) * p.n_q <= kFineRows ? launch_variant<KIND, true>(p, grid, stream)
-                                                                 : launch_variant<KIND, false>(p, grid, stream);
+    return launch_dependent(chunk_kernel<KIND>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, -1, stream, p);
 }
 
 }  // namespace chunk

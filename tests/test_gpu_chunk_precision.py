@@ -1,0 +1,88 @@
+"""Chunk attention keeps the output tolerance of the framework's attention whatever the number of rows in the call."""
+
+import numpy as np
+import pytest
+import torch
+
+from chunk_ref import KINDS
+from harness import assert_out_close
+from test_gpu_chunk import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(c, dev):
+    """(out, lse, Σ w·|v|, max_t scale·Σ|q||k|) in fp64, by request and KV head."""
+    k, v = (torch.from_numpy(x).to(dev) for x in c.opool.values())
+    q = c.q.double()
+    if c.kind == "angle":
+        import oracle
+        q = torch.from_numpy(oracle.angle_query(c.q.float().numpy())).double()
+    q = q.to(dev)
+    n, n_q, _ = q.shape
+    g = n_q // c.n_kv
+    out, mass, size = (torch.zeros_like(q) for _ in range(3))
+    lse = torch.full((n, n_q), -np.inf, dtype=torch.float64, device=dev)
+    for b, m in enumerate(c.lens):
+        s0, s1 = int(c.start[b]), int(c.start[b + 1])
+        if s1 == s0:
+            continue
+        ids = torch.from_numpy(c.bt[b, :-(-m // 16)].astype(np.int64)).to(dev)
+        seen = torch.arange(m, device=dev)[None, :] <= torch.arange(m - (s1 - s0), m, device=dev)[:, None]
+        if c.retain is not None:
+            bits = c.retain[c.bt[b, :-(-m // 16)]].astype(np.int64)
+            keep = ((bits[:, None] >> np.arange(16)) & 1).astype(bool).reshape(-1)[:m]
+            seen = seen & torch.from_numpy(keep).to(dev)[None, :]
+        for h in range(c.n_kv):
+            kk, vv = k[ids, h].reshape(-1, 128)[:m], v[ids, h].reshape(-1, 128)[:m]
+            x = q[s0:s1, h * g:h * g + g]
+            l = torch.einsum("tgd,nd->tgn", x, kk) * 128 ** -0.5
+            l = l.masked_fill(~seen[:, None, :], -np.inf)
+            z = torch.logsumexp(l, -1)
+            w = torch.exp(l - torch.where(torch.isneginf(z), 0.0, z)[..., None])
+            out[s0:s1, h * g:h * g + g] = torch.einsum("tgn,nd->tgd", w, vv)
+            mass[s0:s1, h * g:h * g + g] = torch.einsum("tgn,nd->tgd", w, vv.abs())
+            lse[s0:s1, h * g:h * g + g] = z
+            big = torch.einsum("tgd,nd->tgn", x.abs(), kk.abs()) * 128 ** -0.5
+            size[s0:s1, h * g:h * g + g] = big.masked_fill(~seen[:, None, :], 0.0).amax(-1, keepdim=True)
+    return out, lse, mass, size
+
+
+def short_contexts(dev, kind, requests=160, seed=70):
+    """Contexts of 1 to 48 positions, every position a row: few weights a row, so that their roundings do not average
+    out, and far more than 1,024 rows."""
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(1, 49, requests)
+    return Case(dev, kind, 16, 2, lens, lens, seed=seed)
+
+
+@pytest.mark.parametrize("kind", sorted(k for k in KINDS if not k.startswith("int")))
+def test_a_large_call_keeps_the_weights_precision(cuda_device, kind):
+    """A weight is the sum of two bf16.  bf16 is off by at most 2^-8 relative, so the sum by at most 2^-16.  The weight's
+    logit is off by δ = 2^-16·max_t scale·Σ|q||k| (fp32 sums of 128 products, as in chunk_ref), and so the weight by 2δ
+    relative with the normalisation; exp2, the scale of an 8-bit record and the sums add 2^-19."""
+    c = short_contexts(cuda_device, kind)
+    assert c.q.shape[0] * c.n_q > 1024
+    out, lse = c.run()
+    ref, rlse, mass, size = reference(c, cuda_device)
+    err = (out.double() - ref).abs()
+    tol = mass * (2 * 2.0 ** -16 * size + 2.0 ** -16 + 2.0 ** -19)
+    bad = err > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside the bound, worst ratio {(err / tol).max().item():.1f}"
+    assert bool(((lse.double() - rlse).abs() <= 2.0 ** -16 * size[..., 0] + 2.0 ** -20 * (1 + rlse.abs())).all())
+    assert_out_close(out.double().cpu().numpy(), ref.cpu().numpy())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_a_request_is_as_exact_in_a_batch_as_alone(cuda_device, kind):
+    """The same bound for a request of few rows, in a call of its own and beside rows of no request."""
+    c = Case(cuda_device, kind, 8, 2, [3], [30], seed=71)
+    ref, _, mass, size = reference(c, cuda_device)
+    tol = mass * (2 * 2.0 ** -16 * size + 2.0 ** -16 + 2.0 ** -19)
+    d = c.device()
+    alone = c.run(d=d)[0]
+    d["q"] = torch.cat([d["q"], torch.zeros(200, 8, 128, dtype=torch.bfloat16, device=cuda_device)])
+    beside = c.run(d=d)[0][:3]
+    for got in (alone, beside):
+        assert bool(((got.double() - ref).abs() <= tol).all())
+    assert torch.equal(alone, beside)
