@@ -26,8 +26,8 @@
 //  * two warps that issue S = Q·K^T, one for each softmax warpgroup, and one that issues O += P·V for both; Q, K and V
 //    from shared memory, P and the accumulators in tensor memory;
 //  * two softmax warpgroups, one thread a row: online softmax in fp32 (exp2 domain), P back to tensor
-//    memory, over the S it came from, as the value rounded to bf16 and the rounded remainder (two products: a weight is
-//    off by 2^-16; rounded once, by 2^-8, an output whose terms cancel would be off by more than the tolerance of the
+//    memory, over the S it came from, as two bf16, its leading bits and the remainder (two products: a weight is off
+//    by 2^-16; rounded once, by 2^-8, an output whose terms cancel would be off by more than the tolerance of the
 //    decode's outputs, 2e-3 + 1e-2 of the value).  A warpgroup has two S: the next is ready when a step ends, so a step
 //    has one wait and one arrival.  The reference maximum moves only when a row's maximum passes it by 8
 //    (weights up to 2^8), so O is rarely rescaled.
@@ -77,6 +77,11 @@ constexpr int kMinTiles = 4;
 // What a unit costs beside its tiles (its Q, its first S, its rows out), in tiles.  A serving batch (units of 1 to 260
 // tiles) takes 668, 496, 405, 357, 360, 383 us with 0, 2, 4, 6, 8, 12; a whole prompt of 8,192 598, 556, 515, 476, 475, 486.
 constexpr int kUnitTiles = 6;
+// P as two bf16: the weight times this, cut to 16 bits, is below the weight (by a step where 16 bits hold it, else by
+// less), and the remainder, rounded, is off by half a step of what has at most 8 bits less: 2^-16 of the weight.  Neither
+// term is zero or negative unless the weight is (nearly: below 2^-109) zero, so an infinity in V that every row attends stays one (a rounded
+// weight's remainder would have either sign, and make NaN of it).
+constexpr float kBelow = 1.f - 0x1p-22f;
 constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
 
 constexpr bool has_factors(int kind) { return kind == kKindFp8 || kind == kKindMixed || kind == kKindAngle; }
@@ -1177,15 +1182,19 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                     set2(&x[c], mul2(make_float2(x[c], x[c + 1]), make_float2(f.x, f.y)));
                     set2(&x[c + 2], mul2(make_float2(x[c + 2], x[c + 3]), make_float2(f.z, f.w)));
                 }
-                pw[(c / 2) & 15] = pack_bf16(x[c], x[c + 1]);
-                pw[((c / 2) & 15) + 1] = pack_bf16(x[c + 2], x[c + 3]);
+                #pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int at = ((c + e) / 2) & 15;
+                    const float2 v = make_float2(x[c + e], x[c + e + 1]);
+                    const float2 under = mul2(v, make_float2(kBelow, kBelow));
+                    const uint32_t a = __float_as_uint(under.x), b = __float_as_uint(under.y);
+                    pw[at] = __byte_perm(a, b, 0x7632);
+                    set2(&x[c + e], add2(v, make_float2(-__uint_as_float(a & 0xffff0000u), -__uint_as_float(b & 0xffff0000u))));
+                }
                 if ((c & 31) == 28) {
                     tmem_st16(cols + (c >> 5) * 16, pw);
-                    #pragma unroll   // the remainders, in the columns behind (weight · V scale < 2^8 · 2^128/448 is finite)
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 v = unpack_bf16(pw[e]), of = make_float2(x[(c & 32) + 2 * e], x[(c & 32) + 2 * e + 1]);
-                        pw[e] = pack_bf16(of.x - v.x, of.y - v.y);
-                    }
+                    #pragma unroll   // the remainders, in the columns behind
+                    for (int e = 0; e < 16; ++e) pw[e] = pack_bf16(x[(c & 32) + 2 * e], x[(c & 32) + 2 * e + 1]);
                     tmem_st16(cols + 32 + (c >> 5) * 16, pw);
                 }
             }

@@ -86,3 +86,44 @@ def test_a_request_is_as_exact_in_a_batch_as_alone(cuda_device, kind):
     for got in (alone, beside):
         assert bool(((got.double() - ref).abs() <= tol).all())
     assert torch.equal(alone, beside)
+
+
+def bad_value(c, pos, dim, value):
+    """Position pos of request 0 is written again with one bad element in V; its K stays what it was."""
+    blk, t = int(c.bt[0, pos // 16]), pos % 16
+    k, v = (torch.from_numpy(x[blk, :, t].copy()).bfloat16()[None].to(c.dev) for x in c.opool.values())
+    v[0, :, dim] = value
+    from paged_gqa_decode_kvd_gb300 import kvd_append_kv
+    kvd_append_kv(c.pool.handle, c.layer, k, v, torch.tensor([blk * 16 + t], device=c.dev))
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("q_len,n_q", [(40, 4), (20, 1), (300, 4)])
+@pytest.mark.parametrize("kind", ["bf16", "mixed"])
+def test_a_cached_infinity_stays_one(cuda_device, kind, q_len, n_q, value):
+    """An infinity in V ahead of the new tokens: every row attends it with a weight above zero, so the sum is that
+    infinity (no weight times infinity is NaN unless the weight is 0), in its dim only."""
+    c = Case(cuda_device, kind, n_q, 1, [q_len], [q_len + 260], seed=72)
+    wide = range(260) if kind == "bf16" else \
+        [p for p in range(260) if np.random.default_rng(72).integers(0, 3, c.nb)[c.bt[0, p // 16]] == 0]
+    for pos in (wide[0], wide[len(wide) // 2], wide[-1]):
+        bad_value(c, pos, 77, value)
+        out, lse = c.run()
+        ref, rlse, _, size = reference(c, cuda_device)
+        hit = out[..., 77]
+        assert bool(torch.isnan(hit).all() if np.isnan(value) else (hit == value).all())
+        rest = [d for d in range(128) if d != 77]
+        assert_out_close(out.double().cpu().numpy()[..., rest], ref.cpu().numpy()[..., rest])
+        assert bool(((lse.double() - rlse).abs() <= 2.0 ** -16 * size[..., 0] + 2.0 ** -20 * (1 + rlse.abs())).all())
+        bad_value(c, pos, 77, c.opool.values()[1][int(c.bt[0, pos // 16]), 0, pos % 16, 77])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mixed"])
+def test_infinities_that_cancel_are_nan(cuda_device, kind):
+    c = Case(cuda_device, kind, 4, 1, [40], [300], seed=73)
+    fmt = np.random.default_rng(73).integers(0, 3, c.nb)
+    wide = [p for p in range(260) if kind == "bf16" or fmt[c.bt[0, p // 16]] == 0]
+    bad_value(c, wide[0], 5, float("inf"))
+    bad_value(c, wide[-1], 5, float("-inf"))
+    out, _ = c.run()
+    assert bool(torch.isnan(out[..., 5]).all()) and bool(torch.isfinite(out[..., 6:]).all())
