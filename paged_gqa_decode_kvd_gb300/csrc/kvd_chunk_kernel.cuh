@@ -79,7 +79,7 @@ constexpr int kMinTiles = 4;
 constexpr int kUnitTiles = 6;
 // P as two bf16: the weight times this, cut to 16 bits, is below the weight (by a step where 16 bits hold it, else by
 // less), and the remainder, rounded, is off by half a step of what has at most 8 bits less: 2^-16 of the weight.  Neither
-// term is zero or negative unless the weight is (nearly: below 2^-109) zero, so an infinity in V that every row attends stays one (a rounded
+// term is zero or negative unless the weight is (nearly: below 2^-104) zero, so an infinity in V that every row attends stays one (a rounded
 // weight's remainder would have either sign, and make NaN of it).
 constexpr float kBelow = 1.f - 0x1p-22f;
 constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
@@ -1265,8 +1265,8 @@ __device__ __forceinline__ void softmax_group(Smem<KIND>& s, const ChunkParams& 
                         __syncwarp();
                         tmem_st32(col_o + c, o);
                     }
+                    tmem_wait_st();   // the next tile reads these columns again
                 }
-                tmem_wait_st();
                 tcgen_fence_before();
                 __syncwarp();
             }

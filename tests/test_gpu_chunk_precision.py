@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from chunk_ref import KINDS
+from chunk_ref import KINDS, tables
 from harness import assert_out_close
 from test_gpu_chunk import Case
 
@@ -127,3 +127,38 @@ def test_infinities_that_cancel_are_nan(cuda_device, kind):
     bad_value(c, wide[-1], 5, float("-inf"))
     out, _ = c.run()
     assert bool(torch.isnan(out[..., 5]).all()) and bool(torch.isfinite(out[..., 6:]).all())
+
+
+@pytest.mark.parametrize("seed", [74, 75, 76])
+@pytest.mark.parametrize("kind", ["bf16", "mixed"])
+def test_bad_values_in_several_new_tiles_of_a_warpgroup(cuda_device, kind, seed):
+    """128 rows behind 70 positions: four tiles, the last three with new tokens, two of them of the warpgroup that adds
+    its bad values to its sums in tensor memory before the two are joined.  Each bad V reaches its own row and the later
+    ones, in its own dim."""
+    def formats(x):   # of the request's blocks in a mixed pool
+        bt, nb = tables([198], 3, x)
+        return np.random.default_rng(x).integers(0, 3, nb)[bt[0]]
+
+    while kind == "mixed" and not (formats(seed)[12] == 0 and (formats(seed)[5:8] == 0).any()):
+        seed += 100   # 16-bit blocks in the second and the fourth tile
+    c = Case(cuda_device, kind, 1, 1, [128], [198], seed=seed)
+    fmt = np.random.default_rng(seed).integers(0, 3, c.nb)
+    wide = [p for p in range(70, 198) if kind == "bf16" or fmt[c.bt[0, p // 16]] == 0]
+    clean, rlse, _, size = reference(c, cuda_device)
+    values = [float("inf"), float("-inf"), float("nan")]
+    pick = [next((p for p in wide if a <= p < z), None) for a, z in ((70, 100), (100, 128), (128, 160), (160, 192), (192, 198))]
+    bad = {}
+    for i, pos in enumerate(p for p in pick if p is not None):
+        bad[pos] = (20 * i + 3, values[i % 3])
+        bad_value(c, pos, *bad[pos])
+    assert len(bad) >= (5 if kind == "bf16" else 2)
+    out, lse = c.run()
+    rest = [d for d in range(128) if d not in {x[0] for x in bad.values()}]
+    assert_out_close(out.double().cpu().numpy()[..., rest], clean.cpu().numpy()[..., rest])
+    for pos, (dim, value) in bad.items():
+        row = pos - 70
+        if row:
+            assert_out_close(out[:row, 0, dim].double().cpu().numpy(), clean[:row, 0, dim].cpu().numpy())
+        hit = out[row:, 0, dim]
+        assert bool(torch.isnan(hit).all() if np.isnan(value) else (hit == value).all())
+    assert bool(((lse.double() - rlse).abs() <= 2.0 ** -16 * size[..., 0] + 2.0 ** -20 * (1 + rlse.abs())).all())
