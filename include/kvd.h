@@ -179,6 +179,11 @@ KVD_API kvd_status kvd_pool_bytes(const kvd_pool_desc* desc, size_t* pool_bytes,
  * set on success. */
 KVD_API kvd_status kvd_pool_create(const kvd_pool_desc* desc, void* mem, size_t len, kvd_pool** out);
 
+/* What a caller checks its arrays against: the pool's description, its host-tier blocks (0 without a
+ * tier; block ids, and the retain mask, run over num_blocks + host_blocks) and the device it was
+ * created on.  Each of the three may be NULL.  Host only. */
+KVD_API kvd_status kvd_pool_info(const kvd_pool* pool, kvd_pool_desc* desc, int64_t* host_blocks, int32_t* device);
+
 /* Free the handle and its error word (not the caller's pool memory).  NULL is a no-op. */
 KVD_API void kvd_pool_destroy(kvd_pool* pool);
 

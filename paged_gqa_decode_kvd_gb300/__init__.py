@@ -38,6 +38,7 @@ from ._lib import (  # noqa: F401
     kvd_rope_append,
     kvd_rope_freqs,
     kvd_pool_attach_host_tier,
+    kvd_pool_info,
     kvd_tier_bytes,
     kvd_tier_prefetch,
     kvd_tier_plan,

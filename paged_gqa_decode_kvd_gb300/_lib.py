@@ -23,7 +23,7 @@ SYMBOLS = [
     "kvd_tier_bytes", "kvd_pool_attach_host_tier", "kvd_tier_prefetch", "kvd_tier_plan", "kvd_tier_move",
     "kvd_tier_reassign", "kvd_measure_read_stream", "kvd_pool_set_block_formats", "kvd_decode_plan",
     "kvd_rope_freqs", "kvd_rope_append", "kvd_chunk_workspace_bytes", "kvd_chunk_attn",
-    "kvd_compact_workspace_bytes", "kvd_compact",
+    "kvd_compact_workspace_bytes", "kvd_compact", "kvd_pool_info",
 ]
 ROPE_RULES = {"plain": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvd_rope_rule
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -119,6 +119,8 @@ def load(build_if_missing: bool = True):
     lib.kvd_decode_plan.argtypes = [P, i32, P, i32, P, i32, i32, i32, P, P, sz, P]
     lib.kvd_measure_read_stream.restype = i32
     lib.kvd_measure_read_stream.argtypes = [P, sz, P, sz, P]
+    lib.kvd_pool_info.restype = i32
+    lib.kvd_pool_info.argtypes = [P, ctypes.POINTER(PoolDesc), ctypes.POINTER(i64), ctypes.POINTER(ctypes.c_int32)]
     f64 = ctypes.c_double
     lib.kvd_rope_freqs.restype = i32
     lib.kvd_rope_freqs.argtypes = [i32, f64, ctypes.POINTER(RopeScaling), P, P]
@@ -243,6 +245,13 @@ def kvd_pool_create(num_layers, n_kv, num_blocks, kv_dtype, mem, d_h=128, block_
     n = mem.numel() * mem.element_size()
     _check("kvd_pool_create", load().kvd_pool_create(ctypes.byref(d), _ptr(mem), n, ctypes.byref(h)))
     return h
+
+
+def kvd_pool_info(handle):
+    """(description, host-tier blocks, device ordinal) of a pool; host only."""
+    d, host, dev = PoolDesc(), ctypes.c_int64(), ctypes.c_int32()
+    _check("kvd_pool_info", load().kvd_pool_info(handle, d, host, dev))
+    return d, host.value, dev.value
 
 
 def kvd_pool_set_block_formats(handle, block_fmt):
@@ -383,6 +392,28 @@ def _like(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}")
 
 
+def _mask(mask, ids, device):
+    """The retain mask of a pool of `ids` blocks: the kernels read (and compaction writes) it by block id."""
+    import torch
+
+    if mask is None:
+        return
+    if mask.dtype not in (torch.int16, torch.uint16) or not mask.is_contiguous() or mask.get_device() != device:
+        raise ValueError(f"retain_mask must be a contiguous 16-bit integer tensor on device {device}")
+    if mask.numel() < ids:
+        raise ValueError(f"retain_mask must have an element for each of the pool's {ids} blocks")
+
+
+def _scratch(workspace, device):
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {device}")
+
+
+def _on(device, pool_device):
+    if device != pool_device:
+        raise ValueError(f"the tensors must be on the pool's device, {pool_device}")
+
+
 def kvd_rope_append(handle, layer, q, k_new, v_new, positions, rope, slot_mapping, q_out=None, stream=None):
     """Rotate q (into q_out, or in place) and k_new at `positions` (int32) and append k_new, v_new at
     slot_mapping (int64).  rope: a Rope.  q, k_new, v_new: bf16 [n][heads][128], heads of a token
@@ -395,6 +426,7 @@ def kvd_rope_append(handle, layer, q, k_new, v_new, positions, rope, slot_mappin
     dev = k_new.get_device()   # comparing torch.device objects takes three times as long, and a step is short
     if v_new.shape != k_new.shape or v_new.get_device() != dev or rope.turns.get_device() != dev:
         raise ValueError("k_new, v_new and rope must agree in shape and device")
+    _on(dev, kvd_pool_info(handle)[2])
     _like(positions, "positions", torch.int32, (n,), dev)
     _like(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
     n_q, qs, os_ = 0, 0, 0
@@ -431,6 +463,10 @@ def kvd_chunk_attn(handle, layer, q, q_start, block_table, seq_lens, workspace, 
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out must be bfloat16 or float32")
     dev = q.get_device()
+    desc, host_blocks, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    _mask(retain_mask, desc.num_blocks + host_blocks, dev)
+    _scratch(workspace, dev)
     _like(out, "out", out.dtype, q.shape, dev)
     batch = seq_lens.shape[0]
     _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
@@ -462,6 +498,10 @@ def kvd_compact(handle, block_table, seq_lens, new_table, new_lens, workspace, r
 
     batch, mb = block_table.shape
     dev = block_table.get_device()
+    desc, host_blocks, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    _mask(retain_mask, desc.num_blocks + host_blocks, dev)
+    _scratch(workspace, dev)
     _like(block_table, "block_table", torch.int32, (batch, mb), dev)
     _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
     _like(new_table, "new_table", torch.int32, (batch, new_table.shape[1]), dev)

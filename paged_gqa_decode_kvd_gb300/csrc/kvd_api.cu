@@ -209,6 +209,14 @@ kvd_status kvd_pool_create(const kvd_pool_desc* desc, void* mem, size_t len, kvd
     return KVD_OK;
 }
 
+kvd_status kvd_pool_info(const kvd_pool* pool, kvd_pool_desc* desc, int64_t* host_blocks, int32_t* device) {
+    if (!pool) return KVD_ERR_INVALID;
+    if (desc) *desc = pool->desc;
+    if (host_blocks) *host_blocks = pool->host_blocks;
+    if (device) *device = pool->device;
+    return KVD_OK;
+}
+
 kvd_status kvd_tier_bytes(const kvd_pool_desc* desc, int64_t host_blocks, size_t* host_bytes, size_t* staging_bytes) {
     kvd_status st = check_desc(desc);
     if (st != KVD_OK) return st;

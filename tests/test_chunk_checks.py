@@ -1,0 +1,150 @@
+"""What the Python entry points of the chunk operators refuse before the library sees it: tensors of another device,
+type or size than the pool's.  Tensors are stand-ins with the attributes a check reads; nothing is launched."""
+
+import ctypes
+
+import pytest
+import torch
+
+import paged_gqa_decode_kvd_gb300 as kvd
+from test_chunk_host import fake
+
+BF16, I32, I64, F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+class Tensor:
+    """A contiguous device tensor, as far as a check can tell."""
+
+    def __init__(self, shape, dtype, device=0, contiguous=True, at=4096):
+        self.shape, self.dtype, self.device_index, self.contiguous, self.at = torch.Size(shape), dtype, device, contiguous, at
+
+    def stride(self, dim=None):
+        s = torch.empty(self.shape, device="meta").stride()
+        return s if dim is None else s[dim]
+
+    def get_device(self):
+        return self.device_index
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty((), dtype=self.dtype).element_size()
+
+    def data_ptr(self):
+        return self.at
+
+
+class Reached(Exception):
+    pass
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """The library with its launching entry points replaced: a call that passes the checks raises Reached."""
+    real = kvd.load()
+
+    class Library:
+        def __getattr__(self, name):
+            if name in ("kvd_chunk_attn", "kvd_compact", "kvd_rope_append"):
+                def reached(*_):
+                    raise Reached
+                return reached
+            return getattr(real, name)
+
+    monkeypatch.setattr(kvd._lib, "load", lambda *_: Library())
+
+
+def handle(device=0, host_blocks=0, **kw):
+    f = fake(**kw)
+    f.device, f.host_blocks = device, host_blocks
+    return f
+
+
+def chunk(pool, dev=0, **kw):
+    a = dict(q=Tensor((3, 4, 128), BF16, dev), q_start=Tensor((2,), I32, dev), block_table=Tensor((1, 4), I32, dev),
+             seq_lens=Tensor((1,), I32, dev), workspace=Tensor((1 << 20,), torch.uint8, dev),
+             out=Tensor((3, 4, 128), BF16, dev), retain_mask=Tensor((8,), torch.int16, dev),
+             lse_out=Tensor((3, 4), F32, dev))
+    a.update(kw)
+    kvd.kvd_chunk_attn(ctypes.byref(pool), 0, stream=0, **a)
+
+
+def compact(pool, dev=0, **kw):
+    a = dict(block_table=Tensor((2, 4), I32, dev), seq_lens=Tensor((2,), I32, dev), new_table=Tensor((2, 4), I32, dev),
+             new_lens=Tensor((2,), I32, dev, at=8192), workspace=Tensor((1 << 20,), torch.uint8, dev),
+             retain_mask=Tensor((8,), torch.int16, dev), scores=Tensor((2, 64), F32, dev),
+             new_scores=Tensor((2, 64), F32, dev, at=8192))
+    a.update(kw)
+    kvd.kvd_compact(ctypes.byref(pool), stream=0, **a)
+
+
+class Rope:
+    rot_dim, interleaved, mscale = 128, False, 1.0
+
+    def __init__(self, dev):
+        self.turns = Tensor((64, 2), F32, dev)
+
+
+def rope(pool, dev=0, **kw):
+    a = dict(q=Tensor((3, 4, 128), BF16, dev), k_new=Tensor((3, 2, 128), BF16, dev), v_new=Tensor((3, 2, 128), BF16, dev),
+             positions=Tensor((3,), I32, dev), rope=Rope(dev), slot_mapping=Tensor((3,), I64, dev),
+             q_out=Tensor((3, 4, 128), BF16, dev))
+    a.update(kw)
+    kvd.kvd_rope_append(ctypes.byref(pool), 0, stream=0, **a)
+
+
+@pytest.mark.parametrize("call", [chunk, compact, rope])
+def test_a_sound_call_passes(library, call):
+    with pytest.raises(Reached):
+        call(handle())
+
+
+@pytest.mark.parametrize("call", [chunk, compact, rope])
+@pytest.mark.parametrize("pool_device,dev", [(0, -1), (0, 1), (1, 0)])
+def test_every_tensor_is_on_the_pools_device(library, call, pool_device, dev):
+    """-1 is host memory: all tensors there agree with each other, and the kernels cannot read them."""
+    with pytest.raises(ValueError, match="device"):
+        call(handle(device=pool_device), dev=dev)
+
+
+@pytest.mark.parametrize("call", [chunk, compact])
+def test_the_mask_covers_the_pool(library, call):
+    """Block ids run over the pool's and the host tier's blocks; compaction writes the mask of a new block."""
+    for blocks, host in ((8, 0), (8, 5), (1000, 0)):
+        pool = handle(blocks=blocks, host_blocks=host)
+        with pytest.raises(Reached):
+            call(pool, retain_mask=Tensor((blocks + host,), torch.int16))
+        with pytest.raises(Reached):
+            call(pool, retain_mask=Tensor((blocks + host,), torch.uint16))
+        with pytest.raises(Reached):
+            call(pool, retain_mask=None)
+        with pytest.raises(ValueError, match="retain_mask"):
+            call(pool, retain_mask=Tensor((blocks + host - 1,), torch.int16))
+
+
+@pytest.mark.parametrize("call", [chunk, compact])
+@pytest.mark.parametrize("mask", [Tensor((8,), torch.int32), Tensor((8,), torch.uint8), Tensor((8,), torch.bool),
+                                  Tensor((8,), torch.int16, device=-1), Tensor((8,), torch.int16, device=1),
+                                  Tensor((8,), torch.int16, contiguous=False)])
+def test_masks_of_another_kind(library, call, mask):
+    with pytest.raises(ValueError, match="retain_mask"):
+        call(handle(), retain_mask=mask)
+
+
+@pytest.mark.parametrize("call", [chunk, compact])
+@pytest.mark.parametrize("workspace", [Tensor((1 << 20,), torch.uint8, device=-1), Tensor((1 << 20,), torch.uint8, device=1),
+                                       Tensor((1 << 20,), torch.uint8, contiguous=False)])
+def test_workspaces_elsewhere(library, call, workspace):
+    with pytest.raises(ValueError, match="workspace"):
+        call(handle(), workspace=workspace)
+
+
+def test_pool_info():
+    desc, host, device = kvd.kvd_pool_info(ctypes.byref(handle(device=3, host_blocks=7, n_kv=4, blocks=9)))
+    assert (desc.n_kv, desc.num_blocks, host, device) == (4, 9, 7, 3)
+    with pytest.raises(kvd.KvdError):
+        kvd.kvd_pool_info(None)
