@@ -426,7 +426,10 @@ def kvd_rope_append(handle, layer, q, k_new, v_new, positions, rope, slot_mappin
     dev = k_new.get_device()   # comparing torch.device objects takes three times as long, and a step is short
     if v_new.shape != k_new.shape or v_new.get_device() != dev or rope.turns.get_device() != dev:
         raise ValueError("k_new, v_new and rope must agree in shape and device")
-    _on(dev, kvd_pool_info(handle)[2])
+    desc, _, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    if k_new.shape[1] != desc.n_kv:
+        raise ValueError(f"k_new and v_new must have the pool's {desc.n_kv} heads")
     _like(positions, "positions", torch.int32, (n,), dev)
     _like(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
     n_q, qs, os_ = 0, 0, 0

@@ -143,6 +143,26 @@ def test_workspaces_elsewhere(library, call, workspace):
         call(handle(), workspace=workspace)
 
 
+class Wide(Tensor):
+    """A slice of a projection's output, 512 heads wide."""
+
+    def stride(self, dim=None):
+        s = (512 * 128, 128, 1)
+        return s if dim is None else s[dim]
+
+
+@pytest.mark.parametrize("kind", [Tensor, Wide])
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("heads", [1, 3, 8])
+def test_keys_have_the_pools_heads(library, kind, tokens, heads):
+    """The kernel reads the pool's two heads from every token's row: with fewer it would read past the slice, with more
+    the others would be lost."""
+    kv = dict(k_new=kind((tokens, heads, 128), BF16), v_new=kind((tokens, heads, 128), BF16), q=None, q_out=None,
+              positions=Tensor((tokens,), I32), slot_mapping=Tensor((tokens,), I64))
+    with pytest.raises(ValueError, match="heads"):
+        rope(handle(), **kv)
+
+
 def test_pool_info():
     desc, host, device = kvd.kvd_pool_info(ctypes.byref(handle(device=3, host_blocks=7, n_kv=4, blocks=9)))
     assert (desc.n_kv, desc.num_blocks, host, device) == (4, 9, 7, 3)
