@@ -462,6 +462,9 @@ KVD_API kvd_status kvd_accum_scores(const float* logits, int64_t logits_stride, 
                             const int32_t* seq_lens, int batch, int n_q, float inv_LH,
                             float* scores, int64_t scores_stride, void* stream);
 
+/* The entry points from here to kvd_compact run on the device the pool was created on, which has to
+ * be the current one (KVD_ERR_INVALID if it is not; kvd_pool_info tells which it is). */
+
 /* Rotary positions.  The pages cache keys that already carry their position and describe no
  * rotation; these two entry points have no counterpart in them.  Pair j < rot_dim/2 of a head's
  * first rot_dim dims, (j, j + rot_dim/2) or, interleaved, (2j, 2j+1), is turned by the angle

@@ -59,6 +59,16 @@ bool lowbit_dtype(int32_t t) { return t == KVD_INT4 || t == KVD_INT2; }
 // Groups per 128-value row of a low-bit pool (1 otherwise).
 int pool_ng(const kvd_pool_desc* d) { return lowbit_dtype(d->kv_dtype) ? kvd::kDh / d->group_size : 1; }
 
+// A kernel runs on the current device, where the pool's memory has to be.
+kvd_status check_device(int device) {
+    int now = 0;
+    if (cudaGetDevice(&now) != cudaSuccess) {
+        cudaGetLastError();
+        return KVD_ERR_CUDA;
+    }
+    return now == device ? KVD_OK : KVD_ERR_INVALID;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -663,6 +673,8 @@ kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_s
     if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(rope->turns) & 7u)) return KVD_ERR_INVALID;
     if (n_q > 0 && q_out == q && q_out_stride != q_stride) return KVD_ERR_INVALID;
     if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
+    const kvd_status st = check_device(pool->device);
+    if (st != KVD_OK) return st;
     kvd::RopeParams p;
     p.q = static_cast<const uint16_t*>(q);
     p.k = static_cast<const uint16_t*>(k_new);
@@ -737,6 +749,8 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
     if (st != KVD_OK) return st;
     if (workspace_bytes < need) return KVD_ERR_NOMEM;
     if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
+    st = check_device(pool->device);
+    if (st != KVD_OK) return st;
     kvd::ChunkParams p;
     p.kv = pool->mem + static_cast<size_t>(layer) * pool->layer_bytes;
     p.stage = !pool->host_blocks ? nullptr
@@ -809,6 +823,8 @@ kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int max_block
     if ((scores == nullptr) != (new_scores == nullptr)) return KVD_ERR_INVALID;
     if (scores && (scores == new_scores || scores_stride < 1 || new_scores_stride < 1)) return KVD_ERR_INVALID;
     if (workspace_bytes < total) return KVD_ERR_NOMEM;
+    st = check_device(pool->device);
+    if (st != KVD_OK) return st;
     kvd::CompactParams p;
     p.block_table = block_table;
     p.seq_lens = seq_lens;
