@@ -538,7 +538,8 @@ KVD_API kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int 
  *               skipped with KVD_ERR_OOB in the error word; T = 0 is a request with nothing to do
  *  seq_lens     int32 [batch], device: cached tokens, the new ones included; in
  *               [T, max_blocks_per_seq·16], else KVD_ERR_OOB and the rows get out = 0, lse = −inf
- *  block_table, max_blocks_per_seq, retain_mask, softmax_scale as in kvd_decode_attn; a block id
+ *  softmax_scale finite (also times log2 e), of either sign
+ *  block_table, max_blocks_per_seq, retain_mask as in kvd_decode_attn; a block id
  *               outside the pool (and its host tier) is reported and its 16 positions are not attended
  *  workspace    device scratch, 256-byte aligned, ≥ kvd_chunk_workspace_bytes; needs no
  *               initialisation and keeps nothing from call to call.  Calls that may run at the same

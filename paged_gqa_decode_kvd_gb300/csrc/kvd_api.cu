@@ -741,6 +741,7 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
     if (st != KVD_OK) return st;
     if (layer < 0 || layer >= pool->desc.num_layers || n_tokens < 0 || max_blocks_per_seq < 1) return KVD_ERR_INVALID;
     if (out_dtype != KVD_BF16 && out_dtype != KVD_F32) return KVD_ERR_INVALID;
+    if (!std::isfinite(softmax_scale * kvd::kLog2e)) return KVD_ERR_INVALID;
     if (batch == 0 || n_tokens == 0) return KVD_OK;
     if (!q || !q_start || !block_table || !seq_lens || !workspace || !out) return KVD_ERR_INVALID;
     if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return KVD_ERR_INVALID;

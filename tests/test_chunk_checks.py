@@ -163,6 +163,14 @@ def test_keys_have_the_pools_heads(library, kind, tokens, heads):
         rope(handle(), **kv)
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf"), 3e38])
+def test_a_scale_that_is_no_number_is_refused(scale):
+    """A NaN became the smallest scale, and every position weighed the same."""
+    p = ctypes.c_void_p
+    assert kvd.load().kvd_chunk_attn(ctypes.byref(fake()), 0, p(16), 4, p(4), 3, p(4), 4, p(4), 1, None, scale, p(256),
+                                     1 << 40, p(1 << 20), kvd.KVD_BF16, None, None) == kvd.KVD_ERR_INVALID
+
+
 def test_pool_info():
     desc, host, device = kvd.kvd_pool_info(ctypes.byref(handle(device=3, host_blocks=7, n_kv=4, blocks=9)))
     assert (desc.n_kv, desc.num_blocks, host, device) == (4, 9, 7, 3)
