@@ -545,6 +545,7 @@ KVD_API kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int 
  *               initialisation and keeps nothing from call to call.  Calls that may run at the same
  *               time need one each
  *  out          [n_tokens][n_q][128] in out_dtype (KVD_BF16 or KVD_F32), 16-byte aligned, apart from q
+ *               (KVD_ERR_INVALID if they overlap: rows are written while others' q is still read)
  *  lse_out      f32 [n_tokens][n_q] natural-log log-sum-exp, or NULL
  * A row with nothing to attend gets out = 0 and lse = −inf.  What a masked position's slot holds
  * (not yet written, a NaN) does not reach the result.  Every pool kind.  In an INT4 / INT2 pool

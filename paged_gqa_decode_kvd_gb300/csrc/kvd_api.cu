@@ -750,6 +750,9 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
     if (st != KVD_OK) return st;
     if (workspace_bytes < need) return KVD_ERR_NOMEM;
     if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t values = static_cast<uintptr_t>(n_tokens) * n_q * kvd::kDh;
+    if (o0 < q0 + 2 * values && q0 < o0 + (out_dtype == KVD_F32 ? 4 : 2) * values) return KVD_ERR_INVALID;
     st = check_device(pool->device);
     if (st != KVD_OK) return st;
     kvd::ChunkParams p;

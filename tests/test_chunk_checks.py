@@ -171,6 +171,22 @@ def test_a_scale_that_is_no_number_is_refused(scale):
                                      1 << 40, p(1 << 20), kvd.KVD_BF16, None, None) == kvd.KVD_ERR_INVALID
 
 
+@pytest.mark.parametrize("dtype,distance", [(kvd.KVD_BF16, 0), (kvd.KVD_BF16, 5104), (kvd.KVD_BF16, -5104),
+                                            (kvd.KVD_F32, 5104), (kvd.KVD_F32, -10224)])
+def test_out_over_q_is_refused(dtype, distance):
+    """Five tokens of four heads: 5,120 bytes of q, as many of out or twice that.  16 bytes further they are apart: such a
+    call gets as far as the device check, which a pool of a device that is not there does not pass."""
+    p, pool = ctypes.c_void_p, handle(device=99)
+
+    def call(at):
+        return kvd.load().kvd_chunk_attn(ctypes.byref(pool), 0, p(1 << 20), 4, p(4), 5, p(4), 4, p(4), 1, None, 0.1, p(256),
+                                         1 << 40, p((1 << 20) + at), dtype, None, None)
+
+    assert call(distance) == kvd.KVD_ERR_INVALID
+    if distance and not torch.cuda.is_available():
+        assert call(distance + (16 if distance > 0 else -16)) == kvd.KVD_ERR_CUDA
+
+
 def test_pool_info():
     desc, host, device = kvd.kvd_pool_info(ctypes.byref(handle(device=3, host_blocks=7, n_kv=4, blocks=9)))
     assert (desc.n_kv, desc.num_blocks, host, device) == (4, 9, 7, 3)
