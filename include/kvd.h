@@ -549,8 +549,8 @@ KVD_API kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int 
  *  lse_out      f32 [n_tokens][n_q] natural-log log-sum-exp, or NULL
  * A row with nothing to attend gets out = 0 and lse = −inf.  What a masked position's slot holds
  * (not yet written, a NaN) does not reach the result.  Every pool kind.  In an INT4 / INT2 pool
- * code·scale + zero is rounded to bf16 before the products; the other kinds' K and V enter them
- * exactly.  A weight enters the product with V as two bf16, its leading bits and the rounded
+ * code·scale + zero enters the products as two bf16 (off by 2^-16); the other kinds' K and V enter
+ * them exactly.  A weight enters the product with V as two bf16, its leading bits and the rounded
  * remainder (off by 2^-16); sums are fp32.
  * n_tokens = 0 or batch = 0 is a no-op. */
 KVD_API kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start,

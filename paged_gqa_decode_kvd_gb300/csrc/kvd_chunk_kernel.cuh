@@ -22,7 +22,8 @@
 //    out alike, the product does not care).  A V piece holds four tokens of dims r and r + 8: the pieces
 //    of two blocks give eight tokens of each, which fixes the order of a tile's 64 columns:
 //    column 32p + 8x + 4u + w = token 2x + (w & 1) + 8(w >> 1) of block 2p + u.  8-bit codes become
-//    bf16 exactly on the way; low-bit codes become bf16(code·scale + zero);
+//    bf16 exactly on the way; a low-bit code becomes the fp32 value code·scale + zero as two bf16, each in an operand
+//    of its own (rounded once, outputs whose terms cancel would be off by more than the decode's tolerance);
 //  * two warps that issue S = Q·K^T, one for each softmax warpgroup, and one that issues O += P·V for both; Q, K and V
 //    from shared memory, P and the accumulators in tensor memory;
 //  * two softmax warpgroups, one thread a row: online softmax in fp32 (exp2 domain), P back to tensor
@@ -93,12 +94,14 @@ constexpr int max_record(int kind) {
                                                    : kRecordFp8;
 }
 constexpr bool is_wide(int kind) { return kind == kKindBf16 || kind == kKindMixed; }
-// What fits beside Q: raw tiles, and operand stages of 16 KiB for K and for V.  A tile's masks and factors are
+// What fits beside Q: raw tiles, and operand stages of 16 KiB (32 KiB low-bit) for K and for V.  A tile's masks and factors are
 // read until its P is there.  K may be as far ahead as the stages' tiles behind the other S that a warpgroup has
 // been given before: with a warpgroup on every second tile, four tiles and the stages.
 constexpr int raw_tiles(int kind) { return kind == kKindMixed ? 2 : 3; }
-constexpr int op_stages(int kind) { return is_wide(kind) ? 2 : 3; }
-constexpr int info_sets(int kind) { return is_wide(kind) ? 6 : 8; }
+// Low-bit values have two operands, the rounded value and the rounded remainder.
+constexpr int op_parts(int kind) { return is_lowbit(kind) ? 2 : 1; }
+constexpr int op_stages(int kind) { return is_wide(kind) || is_lowbit(kind) ? 2 : 3; }
+constexpr int info_sets(int kind) { return op_stages(kind) == 2 ? 6 : 8; }
 
 struct TileInfo {
     alignas(16) float limit[kTile];   // column: −inf where the position may not be attended, else +inf
@@ -120,7 +123,7 @@ struct WalkState {
 template <int KIND>
 struct Smem {
     static constexpr int kStages = op_stages(KIND), kRaw = raw_tiles(KIND), kInfos = info_sets(KIND);
-    uint8_t k[kStages][kOpBytes], v[kStages][kOpBytes];         // operands; 1,024-byte aligned
+    uint8_t k[kStages][op_parts(KIND) * kOpBytes], v[kStages][op_parts(KIND) * kOpBytes];   // operands; 1,024-byte aligned
     uint8_t q[2][2 * kOpBytes];                                 // 128 rows each
     uint8_t raw[kRaw][4][max_record(KIND)];
     alignas(16) float factor[has_factors(KIND) ? kInfos : 1][2][has_factors(KIND) ? kTile : 1];   // column: K factor, V factor
@@ -582,11 +585,17 @@ __device__ __forceinline__ void repack_v(const uint8_t* pair, const uint32_t (&w
     }
 }
 
-// Low-bit codes: value = bf16(fp32(code·scale + zero)); one rounding, since the MMA takes bf16.
+// Low-bit codes: values fp32(code·scale + zero), as bf16 and the bf16 of what is left.
+struct LowPair {
+    uint32_t hi, lo;
+};
 template <int BITS>
-__device__ __forceinline__ uint32_t low_pair(uint32_t word, int h, int j, float2 sz0, float2 sz1) {
+__device__ __forceinline__ LowPair low_pair(uint32_t word, int h, int j, float2 sz0, float2 sz1) {
     const uint32_t c0 = word >> (8 * j + BITS * h) & ((1u << BITS) - 1), c1 = word >> (8 * (j + 1) + BITS * h) & ((1u << BITS) - 1);
-    return pack_bf16(fmaf(static_cast<float>(c0), sz0.x, sz0.y), fmaf(static_cast<float>(c1), sz1.x, sz1.y));
+    const float a = fmaf(static_cast<float>(c0), sz0.x, sz0.y), b = fmaf(static_cast<float>(c1), sz1.x, sz1.y);
+    const uint32_t hi = pack_bf16(a, b);
+    const float2 r = unpack_bf16(hi);
+    return {hi, pack_bf16(a - r.x, b - r.y)};
 }
 template <int BITS>
 __device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, int k, int ng, int lane) {
@@ -603,8 +612,10 @@ __device__ __forceinline__ void repack_k_low(const uint8_t* rec, uint8_t* op, in
             for (int q = 0; q < kPer / 2; ++q) {   // 32 dims each: one group of the row
                 const int j = kg * (kPer / 2) + q;
                 const float2 sz = unpack_f16(meta[(r + 8 * th) * ng + j * ng / 4]);
-                put_k(op, n + 2 * th, j, x, low_pair<BITS>(w, 2 * q, 0, sz, sz), low_pair<BITS>(w, 2 * q, 2, sz, sz),
-                      low_pair<BITS>(w, 2 * q + 1, 0, sz, sz), low_pair<BITS>(w, 2 * q + 1, 2, sz, sz));
+                const LowPair a = low_pair<BITS>(w, 2 * q, 0, sz, sz), b = low_pair<BITS>(w, 2 * q, 2, sz, sz);
+                const LowPair c = low_pair<BITS>(w, 2 * q + 1, 0, sz, sz), d = low_pair<BITS>(w, 2 * q + 1, 2, sz, sz);
+                put_k(op, n + 2 * th, j, x, a.hi, b.hi, c.hi, d.hi);
+                put_k(op + kOpBytes, n + 2 * th, j, x, a.lo, b.lo, c.lo, d.lo);
             }
         }
     }
@@ -619,7 +630,7 @@ __device__ __forceinline__ void repack_v_low(const uint8_t* pair, VPut& out, int
         #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int r = 2 * rl + (s ^ p);
-            uint32_t o[2][4];   // dims r, r + 8: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p, 2p+1
+            LowPair o[2][4];   // dims r, r + 8: tokens (2x, 2x+1), (2x+8, 2x+9) of blocks 2p, 2p+1
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint8_t* b = pair + u * max_record(KIND);
@@ -634,8 +645,13 @@ __device__ __forceinline__ void repack_v_low(const uint8_t* pair, VPut& out, int
                     o[1][2 * u + th] = low_pair<BITS>(w, h, 2, s0, s1);
                 }
             }
-            out.put(16 * group + r, lane, o[0][0], o[0][1], o[0][2], o[0][3]);
-            out.put(16 * group + r + 8, lane, o[1][0], o[1][1], o[1][2], o[1][3]);
+            #pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d = 16 * group + r + 8 * e;
+                out.put(d, lane, o[e][0].hi, o[e][1].hi, o[e][2].hi, o[e][3].hi);
+                put16(out.op + kOpBytes, d, 4 * p + x, o[e][0].lo & out.keep[0], o[e][1].lo & out.keep[1],
+                      o[e][2].lo & out.keep[2], o[e][3].lo & out.keep[3]);
+            }
         }
     }
 }
@@ -898,7 +914,7 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
         #pragma unroll 1
         for (uint32_t i = 0; ok && i < mine; ++i) {
             const uint32_t x = done + i, buf = x & 1u, k = base + (two ? i : 2 * i + W), st = k % kStages;
-            const uint32_t cols = uniform(col_s + buf * 64), b = uniform(k_op + st * kOpBytes);
+            const uint32_t cols = uniform(col_s + buf * 64), b = uniform(k_op + st * op_parts(KIND) * kOpBytes);
             const uint32_t full = uniform(smem_u32(&s.s_full[W][buf])), empty = uniform(smem_u32(&s.k_empty[st]));
             ok = wait_two(s, &s.k_full[st], k / kStages, &s.pv_done[W][buf], (x >> 1) - 1, x >= 2);   // P(i−2) has been read
             if (!ok) break;
@@ -908,6 +924,12 @@ __device__ __forceinline__ void score_issuer(Smem<KIND>& s, const ChunkParams& p
                 for (int ks = 0; ks < 8; ++ks)
                     mma_ss(cols, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
                            smem_desc_sw128(b + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, ks > 0);
+                if constexpr (op_parts(KIND) == 2) {
+                    #pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss(cols, smem_desc_sw128(a + (ks >> 2) * kOpBytes + (ks & 3) * 32),
+                               smem_desc_sw128(b + kOpBytes + (ks >> 2) * 8192 + (ks & 3) * 32), kDescS, 1u);
+                }
                 mma_commit(full);
                 mma_commit(empty);
                 if (!two) mbar_arrive(&s.k_empty[st]);
@@ -939,7 +961,7 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
             if (W && i >= mine1) continue;
             const uint32_t x = (W ? done1 : done0) + i, buf = x & 1u, k = base + (two ? i : 2 * i + W), st = k % kStages;
             const uint32_t d = uniform(tmem + kColO + W * 128), a = uniform(tmem + kColS + W * 128 + buf * 64);
-            const uint32_t b = uniform(v_op + st * kOpBytes), more = uniform(i > 0);
+            const uint32_t b = uniform(v_op + st * op_parts(KIND) * kOpBytes), more = uniform(i > 0);
             const uint32_t full = uniform(smem_u32(&s.pv_done[W][buf])), empty = uniform(smem_u32(&s.v_empty[st]));
             ok = wait_two(s, &s.p_full[W][buf], x >> 1, &s.v_full[st], k / kStages);
             if (!ok) break;
@@ -949,6 +971,10 @@ __device__ __forceinline__ void out_issuer(Smem<KIND>& s, const ChunkParams& p) 
                 for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, ks > 0 ? 1u : more);
                 #pragma unroll   // the remainders
                 for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + 32 + ks * 8, smem_desc_sw128(b + ks * 32), kDescO, 1u);
+                if constexpr (op_parts(KIND) == 2) {   // the remainders' own product, 2^-15 at most, is left out
+                    #pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) mma_ts(d, a + ks * 8, smem_desc_sw128(b + kOpBytes + ks * 32), kDescO, 1u);
+                }
                 mma_commit(full);
                 mma_commit(empty);
                 if (!two) mbar_arrive(&s.v_empty[st]);

@@ -73,6 +73,24 @@ def test_a_large_call_keeps_the_weights_precision(cuda_device, kind):
     assert_out_close(out.double().cpu().numpy(), ref.cpu().numpy())
 
 
+@pytest.mark.parametrize("kind", sorted(k for k in KINDS if k.startswith("int")))
+def test_low_bit_records_keep_their_precision(cuda_device, kind):
+    """code·scale + zero, an fp32 value, enters the products as the sum of two bf16: off by 2^-16 of itself, which moves a
+    logit by 2^-16·scale·Σ|q||k| more and an output by 2^-16·Σ w·|v| more than exact K and V do.  The product of a
+    weight's second part (2^-7 of it) and a value's (2^-8) is left out: 2^-15·Σ w·|v|."""
+    c = short_contexts(cuda_device, kind)
+    out, lse = c.run()
+    ref, rlse, mass, size = reference(c, cuda_device)
+    err = (out.double() - ref).abs()
+    tol = mass * (2 * 2.0 ** -15 * size + 2 * 2.0 ** -16 + 2.0 ** -15 + 2.0 ** -19)
+    bad = err > tol
+    outside = int((err > 2e-3 + 1e-2 * ref.abs()).sum())
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside the bound, worst ratio " \
+        f"{(err / tol).max().item():.1f}; {outside} outside the output tolerance"
+    assert bool(((lse.double() - rlse).abs() <= 2.0 ** -15 * size[..., 0] + 2.0 ** -20 * (1 + rlse.abs())).all())
+    assert_out_close(out.double().cpu().numpy(), ref.cpu().numpy())
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_a_request_is_as_exact_in_a_batch_as_alone(cuda_device, kind):
     """The same bound for a request of few rows, in a call of its own and beside rows of no request."""
