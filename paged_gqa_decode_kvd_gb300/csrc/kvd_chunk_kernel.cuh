@@ -136,7 +136,7 @@ struct Smem {
     uint64_t q_ready[2], q_one, merge_full, merge_empty, drain[3];
     int64_t remaining;   // the CTA's share of the schedule: length, first unit, and where in it, see Walk
     int b, h, qt, off, extra;
-    uint32_t tmem;
+    uint32_t tmem, tiles;   // tiles: of all segments, when the producer is through
     int abort;
     // the merge of the two warpgroups: WG 1's maximum and sum, where no query of its own is
     __device__ __forceinline__ float* ml() { return reinterpret_cast<float*>(q[1]); }
@@ -792,6 +792,7 @@ __device__ __forceinline__ void producer(Smem<KIND>& s, const ChunkParams& p, in
     }
     if (ok && wait_bar(s, &s.raw_empty[k % kRaw], k / kRaw + 1)) {   // the end, for those that do not walk
         if (lane == 0) {
+            s.tiles = k;
             s.word[k % kRaw][0] = kStop;
             mbar_arrive(&s.raw_full[k % kRaw]);
         }
@@ -1435,6 +1436,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
         mbar_init(&s.merge_empty, 4);
         mbar_fence_init();
         s.abort = 0;
+        s.tiles = 0;
         s.remaining = 0;
     }
     pdl_wait();
@@ -1476,8 +1478,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const ChunkParams p)
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
-    if (tid == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
-    if (warp == kScoreWarp) tmem_free_all(s.tmem);
+    if (warp == kScoreWarp) {
+        // The commits that gave back the last tiles' stages arrive in this block's shared memory: it must still be its
+        // own.  (The phases before them are over: those stages have been filled again.)
+        constexpr uint32_t kStages = Smem<KIND>::kStages;
+        for (uint32_t k = s.tiles > kStages ? s.tiles - kStages : 0; !s.abort && k < s.tiles; ++k)
+            if (!wait_two(s, &s.k_empty[k % kStages], k / kStages, &s.v_empty[k % kStages], k / kStages)) break;
+        __syncwarp();
+        if (lane == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
+        tmem_free_all(s.tmem);
+    }
 }
 
 template <int KIND>

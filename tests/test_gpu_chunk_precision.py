@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import paged_gqa_decode_kvd_gb300 as kvd
 from chunk_ref import KINDS, tables
 from harness import assert_out_close
 from test_gpu_chunk import Case
@@ -111,8 +112,7 @@ def bad_value(c, pos, dim, value):
     blk, t = int(c.bt[0, pos // 16]), pos % 16
     k, v = (torch.from_numpy(x[blk, :, t].copy()).bfloat16()[None].to(c.dev) for x in c.opool.values())
     v[0, :, dim] = value
-    from paged_gqa_decode_kvd_gb300 import kvd_append_kv
-    kvd_append_kv(c.pool.handle, c.layer, k, v, torch.tensor([blk * 16 + t], device=c.dev))
+    kvd.kvd_append_kv(c.pool.handle, c.layer, k, v, torch.tensor([blk * 16 + t], device=c.dev))
 
 
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
@@ -180,3 +180,23 @@ def test_bad_values_in_several_new_tiles_of_a_warpgroup(cuda_device, kind, seed)
         hit = out[row:, 0, dim]
         assert bool(torch.isnan(hit).all() if np.isnan(value) else (hit == value).all())
     assert bool(((lse.double() - rlse).abs() <= 2.0 ** -16 * size[..., 0] + 2.0 ** -20 * (1 + rlse.abs())).all())
+
+
+def test_calls_back_to_back(cuda_device):
+    """Calls of several kinds and sizes one behind the other, each block of one taking over an SM from the call before
+    as soon as that leaves it: the same bits as alone."""
+    cases = [Case(cuda_device, kind, n_q, n_kv, q, n, seed=77 + i) for i, (kind, n_q, n_kv, q, n) in enumerate([
+        ("bf16", 4, 1, [3], [70]), ("fp8", 8, 1, [100], [300]), ("int4", 4, 2, [40, 1], [90, 500]), ("bf16", 16, 2, [65], [65]),
+        ("mixed", 4, 1, [1], [5]), ("angle", 4, 1, [20], [400])])]
+    data = [c.device() for c in cases]
+    alone = []
+    for c, d in zip(cases, data):
+        alone.append(c.run(d=d))
+        torch.cuda.synchronize()
+    got = [[c.run(d=d) for c, d in zip(cases, data)] for _ in range(30)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for (a, x), (b, y) in zip(alone, turn):
+            assert torch.equal(a, b) and torch.equal(x, y)
+    for c in cases:
+        assert kvd.kvd_get_device_error(c.pool.handle) == kvd.KVD_OK
