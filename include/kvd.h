@@ -516,7 +516,11 @@ KVD_API kvd_status kvd_rope_freqs(int rot_dim, double base, const kvd_rope_scali
  *                q_out row is left as it was) with KVD_ERR_OOB in the error word
  *  slot_mapping  int64 [n_tokens], device, as in kvd_append_kv (s < 0: no append for that token; no
  *                slot twice in one call)
- * Every pool kind, host-tier blocks included.  n_tokens = 0 is a no-op. */
+ * Every pool kind, host-tier blocks included.  n_tokens = 0 is a no-op.
+ * A call with slots writes the pool, so a kvd_decode_attn right behind it must not pass
+ * KVD_EARLY_START.  To keep that flag and the decode's fused append, rotate without appending: every
+ * slot −1, q and then k (as q, n_kv heads) in two calls, and hand the rotated keys to the decode as
+ * k_new. */
 KVD_API kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_stride, int n_q,
                                    const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
                                    const int32_t* positions, const kvd_rope_desc* rope,
@@ -530,7 +534,7 @@ KVD_API kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int 
  * (a prompt's chunk, drafted tokens to verify, single tokens, mixed in one batch).  Page "LLM에서 KV
  * 캐시는 얼마나 생길까", section "KV 캐시란": the prompt's tokens are attended in parallel, each over
  * the keys up to its own.  The new tokens' K and V are in the cache already (kvd_rope_append or
- * kvd_append_kv).  Request b's new tokens are the rows q_start[b] .. q_start[b+1]-1 of q; with
+ * kvd_append_kv; of a staged host tier the layer is prefetched after that).  Request b's new tokens are the rows q_start[b] .. q_start[b+1]-1 of q; with
  * T of them, row i sits at position seq_lens[b] - T + i and attends the retained positions up to it.
  *  q            bf16 [n_tokens][n_q][128], device, 16-byte aligned
  *  q_start      int32 [batch + 1], device, 0 ≤ q_start[b] ≤ q_start[b+1] ≤ n_tokens.  Rows outside
@@ -570,6 +574,8 @@ KVD_API kvd_status kvd_compact_workspace_bytes(const kvd_pool* pool, int batch, 
  * new_table[b][j/16]; the slots behind the last one in its block are zeroed, and
  * retain_mask[new block] = 0xffff.  The old blocks are left as they are: when nothing else uses them
  * they are free once the stream has passed the call.  Without a mask it copies the requests (a fork).
+ * It writes the pool and the mask: a kvd_decode_attn right behind it must not pass KVD_EARLY_START,
+ * and with a staged host tier a layer is prefetched again before it is attended.
  *  block_table  int32 [batch][max_blocks_per_seq], device.  Requests may share old blocks
  *  seq_lens     int32 [batch], device, in [0, max_blocks_per_seq·16], else KVD_ERR_OOB on the device
  *               and the request is taken as empty
