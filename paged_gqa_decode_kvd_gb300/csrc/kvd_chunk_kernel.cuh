@@ -721,7 +721,7 @@ __device__ __forceinline__ bool wait_bar(Smem<KIND>& s, uint64_t* bar, uint32_t 
     return false;
 }
 
-// Three waits with one vote; the third only if `third`.
+// Two waits with one vote; the second only if `second`.
 template <int KIND>
 __device__ __forceinline__ bool wait_two(Smem<KIND>& s, uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, bool second = true) {
     #pragma unroll 1

@@ -8,7 +8,8 @@
 // Angles: θ_j is given in turns per position as an fp32 pair hi + lo (48 bits).  p = pos·hi has
 // its rounding error in one fma, so frac(p) + error + pos·lo is the position's place in the turn to
 // about 2^-25 for every pos < 2^24, where a single fp32 product is off by up to pos·θ·2^-24 radians
-// (0.008 at position 131,072).  cos and sin come once per (token, pair) and serve every head.
+// (0.008 at position 131,072).  cos and sin come once per (token, pair) of a CTA and serve its heads: two or eight query
+// heads, or K of one or four KV heads.
 //
 // Bound: HBM, 4·128 B per query row and 8·128 B per (token, KV head) against a few FMAs per element: 8,192 tokens
 // of 32 + 8 heads take 46 us (4.4 TB/s, 66% of the measured bandwidth: a CTA's loads, its angles and its stores follow
@@ -114,7 +115,7 @@ __device__ __forceinline__ uint4 rotate_row(uint4 raw, const float2 (&f)[8], int
         // dims past rot keep their bits (a NaN's payload too)
         const int d = lane16 * 8 + 2 * i;
         const uint32_t v = pack_bf16(y[2 * i], y[2 * i + 1]);
-        out[i] = rot == kDh || d + 1 < rot ? v : d >= rot ? w[i] : (v & 0xffffu) | (w[i] & 0xffff0000u);
+        out[i] = d < rot ? v : w[i];   // (rot is even)
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
