@@ -510,7 +510,8 @@ KVD_API kvd_status kvd_rope_freqs(int rot_dim, double base, const kvd_rope_scali
  *  q, k, v       bf16, device; token n's heads start at n·stride elements, heads of 128 contiguous
  *                (slices of one projection's output have one stride); 16-byte aligned, strides
  *                multiples of 8 and ≥ heads·128
- *  q_out         bf16, likewise; may be q itself with q's stride.  n_q = 0: only the append (q and
+ *  q_out         bf16, likewise; may be q itself with q's stride, else its rows are apart from q's, k's
+ *                and v's (KVD_ERR_INVALID if they overlap).  n_q = 0: only the append (q and
  *                q_out may be NULL)
  *  positions     int32 [n_tokens], device, in [0, 2^24): a token outside is skipped whole (its
  *                q_out row is left as it was) with KVD_ERR_OOB in the error word
@@ -583,12 +584,13 @@ KVD_API kvd_status kvd_compact_workspace_bytes(const kvd_pool* pool, int batch, 
  *  new_table    int32 [batch][new_max_blocks], device; of row b the first ⌈new_lens[b]/16⌉ ids are
  *               used.  A used id that is outside the pool (and host tier), is used twice or is also
  *               read by the call is reported (KVD_ERR_OOB) and not written
- *  new_lens     int32 [batch], device, out: retained positions (not seq_lens itself).  A request that
+ *  new_lens     int32 [batch], device, out: retained positions (apart from seq_lens).  A request that
  *               does not fit its new row is reported (KVD_ERR_OOB) and gets 0, nothing copied
  *  scores       f32 [batch][scores_stride] or NULL: importance scores by position; new_scores
  *               f32 [batch][new_scores_stride] gets those of the retained positions (0 for a
- *               position at or past scores_stride), then zeros
- *  workspace    device scratch, 256-byte aligned, ≥ kvd_compact_workspace_bytes
+ *               position at or past scores_stride), then zeros; apart from scores
+ *  workspace    device scratch, 256-byte aligned, ≥ kvd_compact_workspace_bytes.  Calls that may run
+ *               at the same time need one each
  * Needs num_blocks + host_blocks ≤ 2^27 and at most 65,535 requests.  A mixed pool is
  * KVD_ERR_UNSUPPORTED: a block's format cannot hold another's codes.  batch = 0 is a no-op. */
 KVD_API kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int max_blocks_per_seq,

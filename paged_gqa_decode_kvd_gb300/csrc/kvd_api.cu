@@ -71,6 +71,21 @@ kvd_status check_device(int device) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
+// Whether rows share memory: n rows of a_row and b_row bytes, a_pitch and b_pitch apart (slices of one tensor have one
+// pitch, and each its own part of it).
+bool rows_overlap(const void* a, size_t a_row, size_t a_pitch, const void* b, size_t b_row, size_t b_pitch, size_t n) {
+    if (!overlap(a, (n - 1) * a_pitch + a_row, b, (n - 1) * b_pitch + b_row)) return false;
+    if (a_pitch != b_pitch) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const size_t ahead = y >= x ? (y - x) % a_pitch : (a_pitch - (x - y) % a_pitch) % a_pitch;   // of b in a's rows
+    return ahead < a_row || a_pitch - ahead < b_row;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct WsLayout {
@@ -671,7 +686,15 @@ kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_s
                     !aligned16(q_out)))
         return KVD_ERR_INVALID;
     if (!aligned16(k_new) || !aligned16(v_new) || (reinterpret_cast<uintptr_t>(rope->turns) & 7u)) return KVD_ERR_INVALID;
-    if (n_q > 0 && q_out == q && q_out_stride != q_stride) return KVD_ERR_INVALID;
+    if (n_q > 0) {   // a CTA reads rows while another writes its own
+        const size_t n = static_cast<size_t>(n_tokens), row = 2 * static_cast<size_t>(q_row), kv = 2 * static_cast<size_t>(kv_row);
+        const size_t pitch = 2 * static_cast<size_t>(q_out_stride);
+        const bool in_place = q_out == q && q_out_stride == q_stride;
+        if ((!in_place && rows_overlap(q, row, 2 * static_cast<size_t>(q_stride), q_out, row, pitch, n)) ||
+            rows_overlap(k_new, kv, 2 * static_cast<size_t>(k_stride), q_out, row, pitch, n) ||
+            rows_overlap(v_new, kv, 2 * static_cast<size_t>(v_stride), q_out, row, pitch, n))
+            return KVD_ERR_INVALID;
+    }
     if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
     const kvd_status st = check_device(pool->device);
     if (st != KVD_OK) return st;
@@ -750,9 +773,8 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
     if (st != KVD_OK) return st;
     if (workspace_bytes < need) return KVD_ERR_NOMEM;
     if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
-    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t values = static_cast<uintptr_t>(n_tokens) * n_q * kvd::kDh;
-    if (o0 < q0 + 2 * values && q0 < o0 + (out_dtype == KVD_F32 ? 4 : 2) * values) return KVD_ERR_INVALID;
+    const size_t values = static_cast<size_t>(n_tokens) * n_q * kvd::kDh;
+    if (overlap(q, 2 * values, out, (out_dtype == KVD_F32 ? 4 : 2) * values)) return KVD_ERR_INVALID;
     st = check_device(pool->device);
     if (st != KVD_OK) return st;
     kvd::ChunkParams p;
@@ -821,11 +843,15 @@ kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int max_block
     if (st != KVD_OK) return st;
     if (new_max_blocks < 1) return KVD_ERR_INVALID;
     if (batch == 0) return KVD_OK;
-    if (!block_table || !seq_lens || !new_table || !new_lens || new_lens == seq_lens || !workspace ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    const size_t lens_bytes = static_cast<size_t>(batch) * sizeof(int32_t);
+    if (!block_table || !seq_lens || !new_table || !new_lens || overlap(new_lens, lens_bytes, seq_lens, lens_bytes) ||
+        !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return KVD_ERR_INVALID;
     if ((scores == nullptr) != (new_scores == nullptr)) return KVD_ERR_INVALID;
-    if (scores && (scores == new_scores || scores_stride < 1 || new_scores_stride < 1)) return KVD_ERR_INVALID;
+    if (scores && (scores_stride < 1 || new_scores_stride < 1 ||
+                   overlap(scores, static_cast<size_t>(batch) * scores_stride * sizeof(float), new_scores,
+                           static_cast<size_t>(batch) * new_scores_stride * sizeof(float))))
+        return KVD_ERR_INVALID;
     if (workspace_bytes < total) return KVD_ERR_NOMEM;
     st = check_device(pool->device);
     if (st != KVD_OK) return st;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import paged_gqa_decode_kvd_gb300 as kvd
-from test_chunk_host import fake
+from test_chunk_host import fake, rope_args
 
 BF16, I32, I64, F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
 
@@ -185,6 +185,52 @@ def test_out_over_q_is_refused(dtype, distance):
     assert call(distance) == kvd.KVD_ERR_INVALID
     if distance and not torch.cuda.is_available():
         assert call(distance + (16 if distance > 0 else -16)) == kvd.KVD_ERR_CUDA
+
+
+def status_of_rope(q_out, os=512, q=1 << 20, qs=1024, k=(1 << 20) + 1024, v=(1 << 20) + 1536, n=5):
+    """Five tokens of one projection, a row of 2,048 bytes: four query heads, two key heads, two value heads."""
+    p, pool = ctypes.c_void_p, handle(device=99)
+    return kvd.load().kvd_rope_append(*rope_args(pool, q=p(q), qs=qs, k=p(k), ks=1024, v=p(v), vs=1024, n=n, q_out=p(q_out),
+                                                 os=os))
+
+
+APART = kvd.KVD_ERR_INVALID if torch.cuda.is_available() else kvd.KVD_ERR_CUDA   # as far as the device check
+
+
+@pytest.mark.parametrize("q_out,stride", [(1 << 20, 512), ((1 << 20) + 16, 1024), ((1 << 20) - 16, 1024),
+                                          ((1 << 20) + 1008, 1024), ((1 << 20) + 1024, 1024), ((1 << 20) + 2048 - 16, 1024),
+                                          ((1 << 20) + 2048, 1024), ((1 << 20) + 1536, 512), ((1 << 20) - 5104, 512)])
+def test_rotated_queries_over_the_inputs_are_refused(q_out, stride):
+    assert status_of_rope(q_out, stride) == kvd.KVD_ERR_INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="tells a refusal from the device check by the lack of a device")
+def test_rotated_queries_apart_from_the_inputs_pass():
+    assert status_of_rope(1 << 20, 1024) == APART                    # q itself
+    assert status_of_rope(1 << 22, 512) == APART                     # a tensor of its own
+    assert status_of_rope((1 << 20) - 5120, 512) == APART            # right before the projection
+    # the unused part of a wider projection (a row of 4,096 bytes)
+    p, pool = ctypes.c_void_p, handle(device=99)
+    args = dict(q=p(1 << 20), qs=2048, k=p((1 << 20) + 1024), ks=2048, v=p((1 << 20) + 1536), vs=2048, n=5, os=2048)
+    for at, want in ((2048, APART), (2560, APART), (4096 - 1008, kvd.KVD_ERR_INVALID), (2032, kvd.KVD_ERR_INVALID)):
+        assert kvd.load().kvd_rope_append(*rope_args(pool, q_out=p((1 << 20) + at), **args)) == want
+
+
+@pytest.mark.parametrize("lens,new_lens,scores,new_scores", [
+    (4096, 4096 + 4, None, None), (4096 + 4, 4096, None, None), (4096, 8192, 16384, 16384 + 4),
+    (4096, 8192, 16384 + 508, 16384), (4096, 8192, 16384, 16384 + 508)])
+def test_compaction_writes_over_nothing_it_reads(lens, new_lens, scores, new_scores):
+    """Two requests, 64 scores each: 8 bytes of lengths, 512 of scores."""
+    p, pool = ctypes.c_void_p, handle(device=99)
+    assert kvd.load().kvd_compact(ctypes.byref(pool), p(64), 4, p(lens), 2, None, p(128), 4, p(new_lens),
+                                  p(scores), 64, p(new_scores), 64, p(256), 1 << 20, None) == kvd.KVD_ERR_INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="tells a refusal from the device check by the lack of a device")
+def test_compaction_apart_passes():
+    p, pool = ctypes.c_void_p, handle(device=99)
+    assert kvd.load().kvd_compact(ctypes.byref(pool), p(64), 4, p(4096), 2, None, p(128), 4, p(4096 + 8), p(16384), 64,
+                                  p(16384 + 512), 64, p(256), 1 << 20, None) == kvd.KVD_ERR_CUDA
 
 
 def test_pool_info():
