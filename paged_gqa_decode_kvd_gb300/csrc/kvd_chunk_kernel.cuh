@@ -39,11 +39,13 @@
 // order, and where a warpgroup might be ahead or behind (tiles of one warpgroup only, a segment's end) it waits for
 // the phase before first.  Every wait gives up after a second or so; the kernel then reports it and ends.
 //
-// Bound, BF16, 32 + 8 heads: 2,048 tokens behind 8,192 take 266 us, 1.16 PFLOP/s (61% of the measured matrix rate).  A tile of
-// 256 rows takes about 1,900 cycles: the MMAs 1,300 (their A and B from shared memory: 128 of its 224 KB a tile; the copies
-// and the repack move the rest), a softmax step 1,500 behind the one before it.  Without its repack it would
-// take 250 us, without its exponentials 255: no one role stands out.  32 × 5 tokens behind 8,187 stream the cache at
-// 5.4 TB/s (82% of the measured bandwidth).
+// Bound, BF16, 32 + 8 heads: 2,048 tokens behind 8,192 take 341 us, 906 TFLOP/s (48% of the measured matrix rate; with P's
+// second product the tensor pipe is 64% busy).  A tile of 256 rows takes about 2,400 cycles: the MMAs 1,800 (S 768, bound
+// by its operands in shared memory, and twice 512 for the two products with V).  In a graph, 331 us: without its repack it
+// would take 317, without its exponentials 328: no one role stands out.  32 × 5 tokens behind 8,187 stream the cache at
+// 5.1 TB/s (76% of the measured bandwidth).
+// The other pool kinds take, one call on a cold cache (BF16: 326 us): FP8 383, angle 434, mixed 542, INT4 832, INT2 839 (a
+// second operand for K and for V doubles their repack).
 //
 // 8-bit records: the K scale multiplies the fp32 logit, the V scale the fp32 weight before it is
 // rounded, so codes enter the MMAs exactly.  Angle-domain keys: q enters as its direction code, with
@@ -72,11 +74,11 @@ constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
 constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so (a clock read a try costs more than the wait)
 constexpr int kColS = 0, kColO = 256;   // tensor memory columns: S and P 2 × 2 × 64, O 2 × 128
-// Smallest share of a CTA.  Four tokens behind 1,019 take 30.7, 21.1, 22.6, 16.1, 20.7, 17.6 us with 1, 2, 3, 4, 6, 8:
+// Smallest share of a CTA.  Four tokens behind 1,019 take 31.4, 21.8, 24.8, 18.6, 23.7, 19.7 us in a graph with 1, 2, 3, 4, 6, 8:
 // a smaller share leaves more parts to join, and a share that does not divide the units leaves two parts a CTA.
 constexpr int kMinTiles = 4;
 // What a unit costs beside its tiles (its Q, its first S, its rows out), in tiles.  A serving batch (units of 1 to 260
-// tiles) takes 668, 496, 405, 357, 360, 383 us with 0, 2, 4, 6, 8, 12; a whole prompt of 8,192 598, 556, 515, 476, 475, 486.
+// tiles) takes 711, 530, 440, 404, 416, 441 us with 0, 2, 4, 6, 8, 12; a whole prompt of 8,192 711, 660, 617, 603, 608, 619.
 constexpr int kUnitTiles = 6;
 // P as two bf16: the weight times this, cut to 16 bits, is below the weight (by a step where 16 bits hold it, else by
 // less), and the remainder, rounded, is off by half a step of what has at most 8 bits less: 2^-16 of the weight.  Neither

@@ -9,8 +9,8 @@
 // Three launches: the ranks (one CTA per request, a prefix sum over its blocks' popcounts), the
 // blocks' claims (a new block named twice, or one that is also read, is skipped), and the gather.
 // Bound of the gather: HBM, each retained byte read and written once, and with them the evicted ones of the same
-// 16-byte pieces.  Eight traces of 7,000 to 8,192 positions in 28 layers, 3% evicted: 1,096 us, 6.4 TB/s (96% of the
-// measured bandwidth); one 8-bit request of 16,411 in 80 layers, a third evicted: 833 us (67%; 84% with the bytes that
+// 16-byte pieces.  Eight traces of 7,000 to 8,192 positions in 28 layers, 3% evicted: 1,092 us, 6.4 TB/s (96% of the
+// measured bandwidth); one 8-bit request of 16,411 in 80 layers, a third evicted: 828 us (67%; 84% with the bytes that
 // come along).  A short call is its three launches.
 #include "kvd_chunk.h"
 #include "kvd_common.cuh"

@@ -12,8 +12,9 @@
 // heads, or K of one or four KV heads.
 //
 // Bound: HBM, 4·128 B per query row and 8·128 B per (token, KV head) against a few FMAs per element: 8,192 tokens
-// of 32 + 8 heads take 46 us (4.4 TB/s, 66% of the measured bandwidth: a CTA's loads, its angles and its stores follow
-// one another, and three CTAs an SM do not cover all of it), 4,099 tokens of 64 + 8 heads, half rotated, 30 us (83%).
+// of 32 + 8 heads take 45 us (4.5 TB/s, 67% of the measured bandwidth: a CTA's loads, its angles and its stores follow
+// one another, and three CTAs an SM do not cover all of it; the angles of a token are made in six CTAs), 4,099 tokens of
+// 64 + 8 heads, half rotated, 30.5 us (83%).  At 80 registers some 28 bytes a thread are spilled.
 #include "kvd_chunk.h"
 #include "kvd_common.cuh"
 
@@ -334,7 +335,7 @@ cudaError_t launch(const RopeParams& p, dim3 grid, cudaStream_t stream) {
 cudaError_t launch_rope_append(RopeParams p, int kind, int num_sms, cudaStream_t stream) {
     const int64_t tiles = (p.n_tokens + kTok - 1) / kTok + 1;   // one more: the first tile may start before token 0
     // Eight query heads (four KV heads) a CTA where that leaves four CTAs an SM: the angles are computed once for
-    // them; else two (one).  8,192 tokens of 32 + 8 heads take 46 us so, 87 us the other way; a step of 32 tokens takes
+    // them; else two (one).  8,192 tokens of 32 + 8 heads take 45 us so, 87 us the other way; a step of 32 tokens takes
     // 4.7 us the other way, 11.1 us so.
     const bool many = tiles * ((p.n_q + 7) / 8) >= 4 * num_sms;
     p.heads_per_cta = many ? 8 : 2;
