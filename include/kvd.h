@@ -556,7 +556,8 @@ KVD_API kvd_status kvd_chunk_workspace_bytes(const kvd_pool* pool, int n_q, int 
  * (not yet written, a NaN) does not reach the result.  Every pool kind.  In an INT4 / INT2 pool
  * code·scale + zero enters the products as two bf16 (off by 2^-16); the other kinds' K and V enter
  * them exactly.  A weight enters the product with V as two bf16, its leading bits and the rounded
- * remainder (off by 2^-16); sums are fp32.
+ * remainder (off by 2^-16); sums are fp32.  The same call gives the same bits; where a long row's sum
+ * is cut and joined depends on all requests of the call, so another batch may round it otherwise.
  * n_tokens = 0 or batch = 0 is a no-op. */
 KVD_API kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start,
                                   int n_tokens, const int32_t* block_table, int max_blocks_per_seq,

@@ -74,16 +74,16 @@ constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
 constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so (a clock read a try costs more than the wait)
 constexpr int kColS = 0, kColO = 256;   // tensor memory columns: S and P 2 × 2 × 64, O 2 × 128
-// Smallest share of a CTA.  Four tokens behind 1,019 take 31.4, 21.8, 24.8, 18.6, 23.7, 19.7 us in a graph with 1, 2, 3, 4, 6, 8:
-// a smaller share leaves more parts to join, and a share that does not divide the units leaves two parts a CTA.
+// Smallest share of a CTA.  In a graph, four tokens behind 1,019 take 31.4, 21.8, 24.8, 18.6, 23.7, 19.7 us with 1, 2, 3,
+// 4, 6, 8: a smaller share leaves more parts to join, and a share that does not divide the units leaves two parts a CTA.
 constexpr int kMinTiles = 4;
 // What a unit costs beside its tiles (its Q, its first S, its rows out), in tiles.  A serving batch (units of 1 to 260
 // tiles) takes 711, 530, 440, 404, 416, 441 us with 0, 2, 4, 6, 8, 12; a whole prompt of 8,192 711, 660, 617, 603, 608, 619.
 constexpr int kUnitTiles = 6;
 // P as two bf16: the weight times this, cut to 16 bits, is below the weight (by a step where 16 bits hold it, else by
 // less), and the remainder, rounded, is off by half a step of what has at most 8 bits less: 2^-16 of the weight.  Neither
-// term is zero or negative unless the weight is (nearly: below 2^-104) zero, so an infinity in V that every row attends stays one (a rounded
-// weight's remainder would have either sign, and make NaN of it).
+// term is zero or negative unless the weight is zero (or nearly: below 2^-104), so an infinity in V that every row
+// attends stays one (a rounded weight's remainder would have either sign, and make NaN of it).
 constexpr float kBelow = 1.f - 0x1p-22f;
 constexpr uint32_t kStop = 0x80000000u;   // block word behind the last tile
 
