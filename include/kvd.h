@@ -521,7 +521,7 @@ KVD_API kvd_status kvd_rope_freqs(int rot_dim, double base, const kvd_rope_scali
  * A call with slots writes the pool, so a kvd_decode_attn right behind it must not pass
  * KVD_EARLY_START.  To keep that flag and the decode's fused append, rotate without appending: every
  * slot −1, q and then k (as q, n_kv heads) in two calls, and hand the rotated keys to the decode as
- * k_new. */
+ * k_new.  Both may be in place: k_new and v_new may be q itself if no token has a slot. */
 KVD_API kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_stride, int n_q,
                                    const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
                                    const int32_t* positions, const kvd_rope_desc* rope,

@@ -690,10 +690,11 @@ kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_s
         const size_t n = static_cast<size_t>(n_tokens), row = 2 * static_cast<size_t>(q_row), kv = 2 * static_cast<size_t>(kv_row);
         const size_t pitch = 2 * static_cast<size_t>(q_out_stride);
         const bool in_place = q_out == q && q_out_stride == q_stride;
-        if ((!in_place && rows_overlap(q, row, 2 * static_cast<size_t>(q_stride), q_out, row, pitch, n)) ||
-            rows_overlap(k_new, kv, 2 * static_cast<size_t>(k_stride), q_out, row, pitch, n) ||
-            rows_overlap(v_new, kv, 2 * static_cast<size_t>(v_stride), q_out, row, pitch, n))
-            return KVD_ERR_INVALID;
+        auto over = [&](const void* x, size_t x_row, int64_t stride) {   // (q itself is read by the thread that writes it)
+            return !(in_place && x == q && stride == q_stride) &&
+                   rows_overlap(x, x_row, 2 * static_cast<size_t>(stride), q_out, row, pitch, n);
+        };
+        if (over(q, row, q_stride) || over(k_new, kv, k_stride) || over(v_new, kv, v_stride)) return KVD_ERR_INVALID;
     }
     if (pool->desc.kv_dtype == KVD_MIXED && !pool->block_fmt) return KVD_ERR_INVALID;
     const kvd_status st = check_device(pool->device);

@@ -208,6 +208,8 @@ def test_rotated_queries_over_the_inputs_are_refused(q_out, stride):
 def test_rotated_queries_apart_from_the_inputs_pass():
     assert status_of_rope(1 << 20, 1024) == APART                    # q itself
     assert status_of_rope(1 << 22, 512) == APART                     # a tensor of its own
+    assert status_of_rope(1 << 20, 1024, k=1 << 20) == APART         # keys rotated in place, without slots
+    assert status_of_rope(1 << 20, 1024, k=1 << 20, v=1 << 20) == APART
     assert status_of_rope((1 << 20) - 5120, 512) == APART            # right before the projection
     # the unused part of a wider projection (a row of 4,096 bytes)
     p, pool = ctypes.c_void_p, handle(device=99)

@@ -58,3 +58,19 @@ def test_rotated_keys_through_the_fused_append(cuda_device, kind):
         assert torch.equal(pools[0].mem, pools[1].mem)
     for p in pools:
         assert kvd.kvd_get_device_error(p.handle) == kvd.KVD_OK
+
+
+def test_keys_rotated_in_place_without_an_append(cuda_device):
+    n, n_kv = 300, 3
+    g = torch.Generator("cpu").manual_seed(6)
+    x = torch.randn(n, 9, 128, generator=g).bfloat16().to(cuda_device)
+    k, v = x[:, 3:6], x[:, 6:]
+    pool, _ = make_pool("bf16", 1, n_kv, 4, cuda_device)
+    rope, pos = kvd.Rope(128, 10000.0, device=cuda_device), torch.arange(n, dtype=torch.int32, device=cuda_device)
+    nowhere = torch.full((n,), -1, dtype=torch.int64, device=cuda_device)
+    before, apart = x.clone(), torch.empty(n, n_kv, 128, dtype=torch.bfloat16, device=cuda_device)
+    kvd.kvd_rope_append(pool.handle, 0, k, k, v, pos, rope, nowhere, apart)
+    assert torch.equal(x, before)
+    kvd.kvd_rope_append(pool.handle, 0, k, k, v, pos, rope, nowhere)
+    assert torch.equal(k, apart) and torch.equal(x[:, :3], before[:, :3]) and torch.equal(v, before[:, 6:])
+    assert (pool.mem == 0xFF).all() and kvd.kvd_get_device_error(pool.handle) == kvd.KVD_OK
