@@ -64,6 +64,15 @@
  *    tile holds the E4M3 codes of each key row's direction, the V tile FP8 values; of the 32
  *    fp32 words after the tiles, index 0 holds per token the key's logit factor w (not a scale)
  *    and index 1 the V scale.
+ *  - A latent pool (KVD_LATENT_BF16, KVD_LATENT_FP8; n_kv = 1) has one record a block: dims 0 .. 511 of a token are
+ *    its latent, 512 .. 575 the rotated dims of its key.
+ *      BF16, 18,432 bytes: value (t, d) at byte (t/8)·9216 + (d/64)·1024 + (t%8)·128 + (((d%64)/8) ^ (t%8))·16 +
+ *        (d%8)·2, so that a record, copied as it is, is a tensor-core operand in shared memory (128-byte swizzle)
+ *      FP8, 10,304 bytes: code (t, d < 512) at byte (t/8)·4096 + (d/64)·512 + (t%8)·64 + d%64; the bf16 rotated dim
+ *        e = d − 512 at 8192 + (t/8)·1024 + (t%8)·128 + ((e/8) ^ (t%8))·16 + (e%8)·2; the fp32 scale of token t at
+ *        10,240 + 4t.  Value = code·scale
+ *    It is written only through kvd_latent_append and kvd_tier_move (copies of blocks), read by kvd_latent_gather and
+ *    kvd_latent_attn; the other entry points that take a pool's K and V refuse it (KVD_ERR_UNSUPPORTED).  No host tier.
  */
 #ifndef KVD_H
 #define KVD_H
@@ -99,8 +108,14 @@ typedef enum {
     KVD_MIXED = 4,            /* pool of mixed-precision blocks (kvd_pool_set_block_formats) */
     KVD_INT4 = 5,             /* w_kv = 1/2: 4-bit codes, half-precision scale and zero point per group */
     KVD_INT2 = 6,             /* w_kv = 1/4: 2-bit codes, likewise */
-    KVD_ANGLE = 7             /* angle-domain keys (E4M3 direction code + radius factor), FP8 values */
+    KVD_ANGLE = 7,            /* angle-domain keys (E4M3 direction code + radius factor), FP8 values */
+    KVD_LATENT_BF16 = 8,      /* a latent cache (kvd_latent_append): one vector a token for all heads */
+    KVD_LATENT_FP8 = 9        /* the same, the latent in E4M3 with an fp32 scale a token, the rotated dims bf16 */
 } kvd_dtype;
+
+/* Values of a token's latent vector, and rotated dims of its key: d_h of a latent pool is their sum. */
+#define KVD_LATENT_DIM 512
+#define KVD_LATENT_ROPE 64
 
 typedef struct {
     int32_t num_layers;       /* L */
@@ -108,7 +123,8 @@ typedef struct {
     int32_t d_h;              /* head dimension; 128 */
     int32_t block_size;       /* tokens per block; 16 */
     int64_t num_blocks;       /* physical blocks per layer */
-    int32_t kv_dtype;         /* KVD_BF16, KVD_FP8_E4M3, KVD_MIXED, KVD_INT4, KVD_INT2 or KVD_ANGLE */
+    int32_t kv_dtype;         /* KVD_BF16, KVD_FP8_E4M3, KVD_MIXED, KVD_INT4, KVD_INT2, KVD_ANGLE, or a latent pool's:
+                                 KVD_LATENT_BF16, KVD_LATENT_FP8 (n_kv 1, d_h 576) */
     int32_t group_size;       /* KVD_INT4 / KVD_INT2: values per scale group, 32, 64 or 128; ignored
                                  for the other types */
 } kvd_pool_desc;
@@ -462,7 +478,7 @@ KVD_API kvd_status kvd_accum_scores(const float* logits, int64_t logits_stride, 
                             const int32_t* seq_lens, int batch, int n_q, float inv_LH,
                             float* scores, int64_t scores_stride, void* stream);
 
-/* The entry points from here to kvd_compact run on the device the pool was created on, which has to
+/* The entry points from here to kvd_latent_prefill run on the device the pool was created on, which has to
  * be the current one (KVD_ERR_INVALID if it is not; kvd_pool_info tells which it is). */
 
 /* Rotary positions.  The pages cache keys that already carry their position and describe no
@@ -599,6 +615,100 @@ KVD_API kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int m
                                int new_max_blocks, int32_t* new_lens, const float* scores, int64_t scores_stride,
                                float* new_scores, int64_t new_scores_stride, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* Latent attention.  The page "The KV Cache Is the New Memory Wall", §2.1 and Tab. 1, lists a cache of one latent vector
+ * of 512 + 64 dims a token for all heads beside the grouped one; it has no layout and no kernel, these entry points
+ * are the library's own.  A layer projects a token's state to a latent c (512 values, normed) and to 64 key dims r, which
+ * are rotated; every head expands c to its own 128 dims of key and of value: k_h = (W_h·c, r), v_h = U_h·c, and
+ * attends with queries of 128 + 64 dims.  Two forms give the same result:
+ *  - absorbed (kvd_latent_attn, decode): <q_h, k_h> = <(W_hᵀ·q_h[:128], q_h[128:]), (c, r)> and Σ w·v_h = U_h·(Σ w·c), so
+ *    the cached rows serve all heads as they are, keys and values at once;
+ *  - expanded (kvd_latent_prefill, prompts): k_h and v_h of every token are made once (of a cached prefix from the
+ *    rows that kvd_latent_gather reads back), and a pair of rows costs 320 products a head instead of 1,088.
+ * The projections are the caller's. */
+
+/* Norm, rotate and append: one launch for one layer's new tokens.  For token n < n_tokens at position positions[n]:
+ *   y = latent[n]·w / sqrt(mean(latent[n]²) + eps) with w = norm_weight, or y = latent[n] without; r = R(pos)·k_rope[n];
+ *   q_rope_out[n][h] = R(pos)·q_rope[n][h] for the n_q query heads, R as in kvd_rope_append over 64 dims (rot_dim ≤ 64).
+ * y and r go to slot_mapping[n]: as bf16, or (FP8) r as bf16 and y as codes: scale = fp32(max|y|/448) (1 for a zero
+ * row), code = e4m3, nearest even, saturating, of the fp32 quotient y/scale (y itself is not rounded before).
+ *  latent        bf16 [n_tokens][512], device, rows latent_stride elements apart (slices of one projection's output have
+ *                one stride); likewise k_rope [n_tokens][64].  16-byte aligned, strides multiples of 8
+ *  norm_weight   bf16 [512], device, 16-byte aligned, or NULL: no norm.  norm_eps ≥ 0
+ *  q_rope        bf16, device: the 64 dims of head h of token n start at n·q_stride + h·q_head_stride elements (the last 64
+ *                of 192, say); 16-byte aligned, strides multiples of 8, heads and tokens apart.  n_q = 0: no queries
+ *  q_rope_out    bf16, likewise (the last 64 dims of the absorbed queries, say); may be q_rope itself with its strides,
+ *                else its rows are apart from q_rope's, latent's and k_rope's (KVD_ERR_INVALID if they overlap)
+ *  positions     int32 [n_tokens], device, in [0, 2^24): a token outside is skipped whole with KVD_ERR_OOB in the error
+ *                word.  rope NULL: nothing is rotated, positions is not read and n_q is 0
+ *  slot_mapping  int64 [n_tokens], device: physical_block·16 + offset; s < 0: no append for that token; beyond the pool:
+ *                KVD_ERR_OOB and no append.  No slot twice in one call
+ * n_q ≤ 256.  n_tokens = 0 is a no-op. */
+KVD_API kvd_status kvd_latent_append(kvd_pool* pool, int layer, const void* latent, int64_t latent_stride,
+                                     const void* k_rope, int64_t k_rope_stride, const void* norm_weight, float norm_eps,
+                                     const void* q_rope, int64_t q_stride, int64_t q_head_stride, int n_q,
+                                     const int32_t* positions, const kvd_rope_desc* rope, const int64_t* slot_mapping,
+                                     int n_tokens, void* q_rope_out, int64_t q_out_stride, int64_t q_out_head_stride,
+                                     void* stream);
+
+/* Read cached rows back, densely: out[row_start[b] + i] = the 576 values at position first[b] + i of request b, bf16
+ * (FP8: code·scale in fp32, rounded once), for i < row_start[b+1] − row_start[b].  out[:, :512] is what the expanding
+ * projection takes, out[:, 512:] is kvd_latent_prefill's k_rope.  Evicted slots are read like any other.
+ *  block_table   int32 [batch][max_blocks_per_seq], device
+ *  row_start     int32 [batch + 1], device, 0 ≤ row_start[b] ≤ row_start[b+1] ≤ n_rows.  Rows outside every request are
+ *                left as they were.  A request whose pair breaks this, or that reaches beyond max_blocks_per_seq·16, is
+ *                skipped with KVD_ERR_OOB in the error word
+ *  first         int32 [batch] ≥ 0, device, or NULL: all 0
+ *  out           bf16 [n_rows], rows out_stride ≥ 576 elements apart, a multiple of 8; 16-byte aligned, apart from the pool
+ * A block id outside the pool is reported and its rows are left as they were.  batch = 0 or n_rows = 0 is a no-op. */
+KVD_API kvd_status kvd_latent_gather(kvd_pool* pool, int layer, const int32_t* block_table, int max_blocks_per_seq,
+                                     const int32_t* row_start, const int32_t* first, int batch, int n_rows, void* out,
+                                     int64_t out_stride, void* stream);
+
+/* Bytes of kvd_latent_attn's workspace (does not depend on the lengths).  Host only. */
+KVD_API kvd_status kvd_latent_workspace_bytes(const kvd_pool* pool, int n_q, int batch, size_t* bytes_out);
+
+/* Absorbed latent attention over the paged cache, one layer: a decode step's single tokens, drafted tokens, chunks,
+ * mixed in one batch.  Request b's new tokens are the rows q_start[b] .. q_start[b+1]-1 of q, in the cache already; with
+ * T of them, row i sits at position seq_lens[b] − T + i and attends the retained positions t up to it:
+ *   l_t = softmax_scale·<q, (c_t, r_t)>, out = Σ softmax(l)_t·c_t, lse = log Σ exp(l_t).
+ *  q            bf16 [n_tokens][n_q][576], device, 16-byte aligned; n_q ≤ 256
+ *  out          [n_tokens][n_q][512] in out_dtype (KVD_BF16 or KVD_F32), 16-byte aligned, apart from q and the pool
+ *  softmax_scale finite (also times log2 e); 192^-1/2 for heads of 128 + 64 dims
+ *  q_start, seq_lens, block_table, retain_mask, lse_out, workspace (kvd_latent_workspace_bytes) and what is done about bad
+ *  lengths, bad block ids and rows with nothing to attend: as in kvd_chunk_attn
+ * What a masked position's slot holds (not yet written, a NaN) does not reach the result.  A weight enters the product
+ * with c rounded to bf16 (off by 2^-9 of itself), logits and sums are fp32.  The same call gives the same bits; where a
+ * long row's sum is cut and joined depends on all requests of the call, so another batch may round it otherwise.
+ * n_tokens = 0 or batch = 0 is a no-op. */
+KVD_API kvd_status kvd_latent_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start, int n_tokens,
+                                   const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens, int batch,
+                                   const uint16_t* retain_mask, float softmax_scale, void* workspace,
+                                   size_t workspace_bytes, void* out, int out_dtype, float* lse_out, void* stream);
+
+/* Expanded latent attention of ragged prompts.  Request b has the T rows q_start[b] .. q_start[b+1]-1 of q and the N keys
+ * kv_start[b] .. kv_start[b+1]-1; causal: row i attends its keys t ≤ N − T + i (the rows are the last T of the N
+ * tokens; with T > N the first T − N rows attend nothing), else all N (a piece of a prefix, whose result is merged with
+ * others by lse: kvd_combine_splits).
+ *   l_t = softmax_scale·(<q[:128], k_nope_t> + <q[128:], k_rope_t>), out = Σ softmax(l)_t·v_t, lse = log Σ exp(l_t)
+ *  pool         a latent pool: its device and error word (the cache itself is not read)
+ *  q            bf16 [n_tokens][n_q][192], device, 16-byte aligned; n_q ≤ 256
+ *  k_nope, v    bf16, device: the 128 dims of head h of key t start at t·stride + h·head_stride elements (slices of one
+ *               projection's [n_keys][n_q][256], say); k_rope: 64 dims at t·k_rope_stride, one for all heads.  16-byte
+ *               aligned, strides multiples of 8, rows apart
+ *  q_start      int32 [batch + 1], device, 0 ≤ q_start[b] ≤ q_start[b+1] ≤ n_tokens; kv_start likewise up to n_keys.  Rows
+ *               outside every request are left as they were.  A request whose pairs break this is skipped with KVD_ERR_OOB
+ *               in the error word
+ *  out          [n_tokens][n_q][128] in out_dtype (KVD_BF16 or KVD_F32), 16-byte aligned, apart from what is read
+ *  lse_out      f32 [n_tokens][n_q] natural-log log-sum-exp, or NULL
+ * A row with nothing to attend gets out = 0 and lse = −inf.  What a key that a row does not attend holds does not reach
+ * that row.  A weight enters the product with v rounded to bf16 (off by 2^-9 of itself), logits and sums are fp32.  The
+ * same call gives the same bits.  n_tokens = 0 or batch = 0 is a no-op. */
+KVD_API kvd_status kvd_latent_prefill(kvd_pool* pool, const void* q, int n_q, const int32_t* q_start, int n_tokens,
+                                      const void* k_nope, int64_t k_stride, int64_t k_head_stride, const void* v,
+                                      int64_t v_stride, int64_t v_head_stride, const void* k_rope, int64_t k_rope_stride,
+                                      const int32_t* kv_start, int n_keys, int batch, int causal, float softmax_scale,
+                                      void* out, int out_dtype, float* lse_out, void* stream);
 
 /* Synchronise `stream`, return the pool's device error word in *code (KVD_OK if none) and
  * clear it. */

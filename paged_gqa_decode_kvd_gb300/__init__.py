@@ -18,6 +18,10 @@ from ._lib import (  # noqa: F401
     KVD_FP8_E5M2,
     KVD_INT2,
     KVD_INT4,
+    KVD_LATENT_BF16,
+    KVD_LATENT_DIM,
+    KVD_LATENT_FP8,
+    KVD_LATENT_ROPE,
     KVD_MIXED,
     KVD_OK,
     KVD_ERR_CUDA,
@@ -37,6 +41,11 @@ from ._lib import (  # noqa: F401
     kvd_compact_workspace_bytes,
     kvd_rope_append,
     kvd_rope_freqs,
+    kvd_latent_append,
+    kvd_latent_attn,
+    kvd_latent_gather,
+    kvd_latent_prefill,
+    kvd_latent_workspace_bytes,
     kvd_pool_attach_host_tier,
     kvd_pool_info,
     kvd_tier_bytes,
@@ -116,6 +125,36 @@ class KVPool:
         self.staging = torch.empty(staging_bytes, dtype=torch.uint8, device=self.mem.device) if staged else None
         kvd_pool_attach_host_tier(self.handle, self.host_mem, self.staging, host_blocks)
         self.host_blocks = host_blocks
+
+    def close(self):
+        if self.handle is not None:
+            kvd_pool_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LatentPool:
+    """Device memory for a paged latent cache (torch allocations) plus its library handle: kv_dtype KVD_LATENT_BF16 or
+    KVD_LATENT_FP8."""
+
+    def __init__(self, num_layers: int, num_blocks: int, kv_dtype: int = KVD_LATENT_BF16, device="cuda"):
+        import torch
+
+        self.num_layers, self.num_blocks, self.kv_dtype = num_layers, num_blocks, kv_dtype
+        d_h = KVD_LATENT_DIM + KVD_LATENT_ROPE
+        pool_bytes, self.kv_bytes = kvd_pool_bytes(num_layers, 1, num_blocks, kv_dtype, d_h=d_h)
+        self.mem = torch.empty(pool_bytes, dtype=torch.uint8, device=device)
+        self.handle = kvd_pool_create(num_layers, 1, num_blocks, kv_dtype, self.mem, d_h=d_h)
+
+    @property
+    def record_bytes(self) -> int:
+        """Bytes of one (layer, block) record: 16 rows of 576 bf16 values, or 512 codes, 64 bf16 values and a scale."""
+        return 16 * (512 + 128 + 4) if self.kv_dtype == KVD_LATENT_FP8 else 16 * 1152
 
     def close(self):
         if self.handle is not None:

@@ -13,6 +13,8 @@ import os
 
 KVD_OK, KVD_ERR_INVALID, KVD_ERR_UNSUPPORTED, KVD_ERR_NOMEM, KVD_ERR_CUDA, KVD_ERR_OOB, KVD_ERR_TIMEOUT = range(7)
 KVD_BF16, KVD_FP8_E4M3, KVD_F32, KVD_FP8_E5M2, KVD_MIXED, KVD_INT4, KVD_INT2, KVD_ANGLE = 0, 1, 2, 3, 4, 5, 6, 7
+KVD_LATENT_BF16, KVD_LATENT_FP8 = 8, 9
+KVD_LATENT_DIM, KVD_LATENT_ROPE = 512, 64
 KVD_EARLY_START = 1   # kvd_decode_attn flags
 KVD_PLANNED = 2
 
@@ -24,6 +26,7 @@ SYMBOLS = [
     "kvd_tier_reassign", "kvd_measure_read_stream", "kvd_pool_set_block_formats", "kvd_decode_plan",
     "kvd_rope_freqs", "kvd_rope_append", "kvd_chunk_workspace_bytes", "kvd_chunk_attn",
     "kvd_compact_workspace_bytes", "kvd_compact", "kvd_pool_info",
+    "kvd_latent_append", "kvd_latent_gather", "kvd_latent_workspace_bytes", "kvd_latent_attn", "kvd_latent_prefill",
 ]
 ROPE_RULES = {"plain": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}   # kvd_rope_rule
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -134,6 +137,18 @@ def load(build_if_missing: bool = True):
     lib.kvd_compact_workspace_bytes.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
     lib.kvd_compact.restype = i32
     lib.kvd_compact.argtypes = [P, P, i32, P, i32, P, P, i32, P, P, i64, P, i64, P, sz, P]
+    rope = ctypes.POINTER(RopeDesc)
+    lib.kvd_latent_append.restype = i32
+    lib.kvd_latent_append.argtypes = [P, i32, P, i64, P, i64, P, f32, P, i64, i64, i32, P, rope, P, i32, P, i64, i64, P]
+    lib.kvd_latent_gather.restype = i32
+    lib.kvd_latent_gather.argtypes = [P, i32, P, i32, P, P, i32, i32, P, i64, P]
+    lib.kvd_latent_workspace_bytes.restype = i32
+    lib.kvd_latent_workspace_bytes.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
+    lib.kvd_latent_attn.restype = i32
+    lib.kvd_latent_attn.argtypes = [P, i32, P, i32, P, i32, P, i32, P, i32, P, f32, P, sz, P, i32, P, P]
+    lib.kvd_latent_prefill.restype = i32
+    lib.kvd_latent_prefill.argtypes = [P, P, i32, P, i32, P, i64, i64, P, i64, i64, P, i64, P, i32, i32, i32, f32, P, i32,
+                                       P, P]
     _lib = lib
     return lib
 
@@ -518,3 +533,157 @@ def kvd_compact(handle, block_table, seq_lens, new_table, new_lens, workspace, r
         handle, _ptr(block_table), mb, _ptr(seq_lens), batch, _ptr(retain_mask), _ptr(new_table), new_table.shape[1],
         _ptr(new_lens), _ptr(scores), ss, _ptr(new_scores), ns, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _rows(t, name, width, device):
+    """Row stride of a bfloat16 [n][width] tensor, rows contiguous (a slice of a projection's output counts)."""
+    import torch
+
+    if t.dim() != 2 or t.shape[1] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
+        raise ValueError(f"{name} must be bfloat16 [rows][{width}] on device {device}")
+    if t.stride(1) != 1 and t.numel():
+        raise ValueError(f"{name}: a row's values must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _head_rows(t, name, width, device):
+    """(token stride, head stride) of a bfloat16 [n][heads][width] tensor, a head's values contiguous."""
+    import torch
+
+    if t.dim() != 3 or t.shape[2] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
+        raise ValueError(f"{name} must be bfloat16 [rows][heads][{width}] on device {device}")
+    if t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name}: a head's values must be contiguous")
+    n, h, _ = t.shape
+    head = t.stride(1) if h > 1 else width
+    return t.stride(0) if n > 1 else max(h, 1) * head, head
+
+
+def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=None, rope=None, norm_weight=None,
+                      norm_eps=1e-6, q_rope=None, q_rope_out=None, stream=None):
+    """Norm latent (bf16 [n][512]; norm_weight bf16 [512] or None), rotate k_rope (bf16 [n][64]) at `positions` (int32,
+    with rope: a Rope) and write both at slot_mapping (int64); rotate q_rope (bf16 [n][heads][64]) into q_rope_out, or
+    in place."""
+    import torch
+
+    dev = latent.get_device()
+    _, _, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    n = latent.shape[0]
+    ls, ks = _rows(latent, "latent", KVD_LATENT_DIM, dev), _rows(k_rope, "k_rope", KVD_LATENT_ROPE, dev)
+    if k_rope.shape[0] != n:
+        raise ValueError("latent and k_rope must have the same rows")
+    _like(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
+    if (rope is None) != (positions is None):
+        raise ValueError("rope and positions go together")
+    d = None
+    if rope is not None:
+        _like(positions, "positions", torch.int32, (n,), dev)
+        if rope.turns.get_device() != dev:
+            raise ValueError(f"rope must be on device {dev}")
+        d = RopeDesc(rope.turns.data_ptr(), rope.rot_dim, 1 if rope.interleaved else 0, rope.mscale)
+    if norm_weight is not None:
+        _like(norm_weight, "norm_weight", torch.bfloat16, (KVD_LATENT_DIM,), dev)
+    n_q = qs = qh = os_ = oh = 0
+    if q_rope is not None:
+        q_rope_out = q_rope if q_rope_out is None else q_rope_out
+        if q_rope.shape[0] != n or q_rope_out.shape != q_rope.shape:
+            raise ValueError("q_rope and q_rope_out must have latent's rows")
+        n_q = q_rope.shape[1]
+        qs, qh = _head_rows(q_rope, "q_rope", KVD_LATENT_ROPE, dev)
+        os_, oh = _head_rows(q_rope_out, "q_rope_out", KVD_LATENT_ROPE, dev)
+    status = load().kvd_latent_append(
+        handle, int(layer), latent.data_ptr(), ls, k_rope.data_ptr(), ks, _ptr(norm_weight), float(norm_eps),
+        0 if q_rope is None else q_rope.data_ptr(), qs, qh, n_q, _ptr(positions), d, slot_mapping.data_ptr(), n,
+        0 if q_rope is None else q_rope_out.data_ptr(), os_, oh, _stream(stream))
+    if status != KVD_OK:
+        _check("kvd_latent_append", status)
+
+
+def kvd_latent_gather(handle, layer, block_table, row_start, out, first=None, stream=None):
+    """Rows row_start[b] .. row_start[b+1]-1 of out (bf16 [n][576]) = request b's cached rows from position first[b] (0)."""
+    import torch
+
+    dev = out.get_device()
+    _, _, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    stride = _rows(out, "out", KVD_LATENT_DIM + KVD_LATENT_ROPE, dev)
+    batch, mb = block_table.shape
+    _like(block_table, "block_table", torch.int32, (batch, mb), dev)
+    _like(row_start, "row_start", torch.int32, (batch + 1,), dev)
+    if first is not None:
+        _like(first, "first", torch.int32, (batch,), dev)
+    _check("kvd_latent_gather", load().kvd_latent_gather(
+        handle, int(layer), _ptr(block_table), mb, _ptr(row_start), _ptr(first), batch, out.shape[0], _ptr(out), stride,
+        _stream(stream)))
+
+
+def kvd_latent_workspace_bytes(handle, n_q, batch):
+    """Bytes of kvd_latent_attn's workspace; host only."""
+    b = ctypes.c_size_t()
+    _check("kvd_latent_workspace_bytes", load().kvd_latent_workspace_bytes(handle, int(n_q), int(batch), ctypes.byref(b)))
+    return b.value
+
+
+def kvd_latent_attn(handle, layer, q, q_start, block_table, seq_lens, workspace, out, retain_mask=None,
+                    softmax_scale=None, lse_out=None, stream=None):
+    """Absorbed latent attention of the rows q_start[b] .. q_start[b+1]-1 of q (bf16 [n][n_q][576]) over request b's cached
+    rows; out bf16 or float32 [n][n_q][512], lse_out f32 [n][n_q].  softmax_scale: 192^-1/2 unless given."""
+    import torch
+
+    n, n_q, _ = q.shape
+    dev = q.get_device()
+    desc, _, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    _like(q, "q", torch.bfloat16, (n, n_q, KVD_LATENT_DIM + KVD_LATENT_ROPE), dev)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be bfloat16 or float32")
+    _like(out, "out", out.dtype, (n, n_q, KVD_LATENT_DIM), dev)
+    _mask(retain_mask, desc.num_blocks, dev)
+    _scratch(workspace, dev)
+    batch = seq_lens.shape[0]
+    _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _like(q_start, "q_start", torch.int32, (batch + 1,), dev)
+    _like(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), dev)
+    if lse_out is not None:
+        _like(lse_out, "lse_out", torch.float32, (n, n_q), dev)
+    if softmax_scale is None:
+        softmax_scale = (128 + KVD_LATENT_ROPE) ** -0.5
+    _check("kvd_latent_attn", load().kvd_latent_attn(
+        handle, int(layer), _ptr(q), n_q, _ptr(q_start), n, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        batch, _ptr(retain_mask), float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(out), KVD_F32 if out.dtype == torch.float32 else KVD_BF16, _ptr(lse_out), _stream(stream)))
+
+
+def kvd_latent_prefill(handle, q, q_start, k_nope, v, k_rope, kv_start, out, causal=True, softmax_scale=None,
+                       lse_out=None, stream=None):
+    """Expanded latent attention of ragged prompts: rows q_start[b] .. of q (bf16 [n][n_q][192]) over keys kv_start[b] ..
+    of k_nope, v (bf16 [m][n_q][128]) and k_rope (bf16 [m][64]); out bf16 or float32 [n][n_q][128], lse_out f32 [n][n_q].
+    causal: the rows are their request's last tokens; else every row attends all its keys."""
+    import torch
+
+    n, n_q, _ = q.shape
+    dev = q.get_device()
+    _, _, pool_dev = kvd_pool_info(handle)
+    _on(dev, pool_dev)
+    _like(q, "q", torch.bfloat16, (n, n_q, 128 + KVD_LATENT_ROPE), dev)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be bfloat16 or float32")
+    _like(out, "out", out.dtype, (n, n_q, 128), dev)
+    m = k_rope.shape[0]
+    if k_nope.shape[:2] != (m, n_q) or v.shape[:2] != (m, n_q):
+        raise ValueError("k_nope and v must have k_rope's rows and q's heads")
+    ks, kh = _head_rows(k_nope, "k_nope", 128, dev)
+    vs, vh = _head_rows(v, "v", 128, dev)
+    rs = _rows(k_rope, "k_rope", KVD_LATENT_ROPE, dev)
+    batch = q_start.shape[0] - 1
+    _like(q_start, "q_start", torch.int32, (batch + 1,), dev)
+    _like(kv_start, "kv_start", torch.int32, (batch + 1,), dev)
+    if lse_out is not None:
+        _like(lse_out, "lse_out", torch.float32, (n, n_q), dev)
+    if softmax_scale is None:
+        softmax_scale = (128 + KVD_LATENT_ROPE) ** -0.5
+    _check("kvd_latent_prefill", load().kvd_latent_prefill(
+        handle, _ptr(q), n_q, _ptr(q_start), n, _ptr(k_nope), ks, kh, _ptr(v), vs, vh, _ptr(k_rope), rs, _ptr(kv_start), m,
+        batch, 1 if causal else 0, float(softmax_scale), _ptr(out), KVD_F32 if out.dtype == torch.float32 else KVD_BF16,
+        _ptr(lse_out), _stream(stream)))

@@ -10,40 +10,22 @@
 #include "kvd_chunk.h"
 #include "kvd_common.cuh"
 #include "kvd_internal.h"
+#include "kvd_latent.h"
+#include "kvd_pool.h"
 
-struct kvd_pool {
-    kvd_pool_desc desc;
-    uint8_t* mem;
-    int32_t* err;       // device error word
-    int device;
-    int num_sms;
-    size_t layer_bytes;
-    // host tier (T1): records in pinned host memory (device address) and two HBM staging slots
-    uint8_t* host_kv;      // device address of the host records
-    uint8_t* host_mem;     // the same records' host address (the prefetch's DMA source)
-    uint8_t* staging;
-    int64_t host_blocks;
-    size_t host_layer_bytes;
-    int host_direct;       // no staging: the decode kernel reads host records over the host link
-    // mixed pools: precision code of every physical block (device, caller-owned)
-    const uint8_t* block_fmt;
-    int64_t block_fmt_count;
-};
+using namespace kvd;
 
 namespace {
 
 constexpr int kMinBlocksPerSplit = 16;  // smallest per-CTA share the planner creates
 
-bool mul_ok(size_t a, size_t b, size_t* out) {
-    if (a != 0 && b > SIZE_MAX / a) return false;
-    *out = a * b;
-    return true;
-}
-
 kvd_status check_desc(const kvd_pool_desc* d) {
     if (!d) return KVD_ERR_INVALID;
     if (d->num_layers < 1 || d->n_kv < 1 || d->num_blocks < 1 || d->d_h < 1 || d->block_size < 1)
         return KVD_ERR_INVALID;
+    if (latent_dtype(d->kv_dtype))   // one vector a token for all heads
+        return d->n_kv == 1 && d->d_h == KVD_LATENT_DIM + KVD_LATENT_ROPE && d->block_size == kvd::kBs ? KVD_OK
+                                                                                                     : KVD_ERR_UNSUPPORTED;
     if (d->kv_dtype != KVD_BF16 && d->kv_dtype != KVD_FP8_E4M3 && d->kv_dtype != KVD_MIXED &&
         d->kv_dtype != KVD_INT4 && d->kv_dtype != KVD_INT2 && d->kv_dtype != KVD_ANGLE)
         return KVD_ERR_INVALID;
@@ -58,35 +40,6 @@ bool lowbit_dtype(int32_t t) { return t == KVD_INT4 || t == KVD_INT2; }
 
 // Groups per 128-value row of a low-bit pool (1 otherwise).
 int pool_ng(const kvd_pool_desc* d) { return lowbit_dtype(d->kv_dtype) ? kvd::kDh / d->group_size : 1; }
-
-// A kernel runs on the current device, where the pool's memory has to be.
-kvd_status check_device(int device) {
-    int now = 0;
-    if (cudaGetDevice(&now) != cudaSuccess) {
-        cudaGetLastError();
-        return KVD_ERR_CUDA;
-    }
-    return now == device ? KVD_OK : KVD_ERR_INVALID;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + b_bytes && y < x + a_bytes;
-}
-
-// Whether rows share memory: n rows of a_row and b_row bytes, a_pitch and b_pitch apart (slices of one tensor have one
-// pitch, and each its own part of it).
-bool rows_overlap(const void* a, size_t a_row, size_t a_pitch, const void* b, size_t b_row, size_t b_pitch, size_t n) {
-    if (!overlap(a, (n - 1) * a_pitch + a_row, b, (n - 1) * b_pitch + b_row)) return false;
-    if (a_pitch != b_pitch) return true;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    const size_t ahead = y >= x ? (y - x) % a_pitch : (a_pitch - (x - y) % a_pitch) % a_pitch;   // of b in a's rows
-    return ahead < a_row || a_pitch - ahead < b_row;
-}
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct WsLayout {
     size_t part_o, part_lse, unit_first, unit_count, plan, total;
@@ -127,8 +80,6 @@ int plan_splits(const kvd_pool* pool, int batch, int max_seq_len, int g) {
     return static_cast<int>(s < 1 ? 1 : s);
 }
 
-kvd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVD_OK : KVD_ERR_CUDA; }
-
 int pool_kind(const kvd_pool* pool) {
     switch (pool->desc.kv_dtype) {
         case KVD_FP8_E4M3: return kvd::kKindFp8;
@@ -142,6 +93,7 @@ int pool_kind(const kvd_pool* pool) {
 
 // Bytes of one (layer, block, KV head) record slot.
 size_t record_bytes(const kvd_pool_desc* d) {
+    if (latent_dtype(d->kv_dtype)) return kvd::latent_record_bytes(d->kv_dtype == KVD_LATENT_FP8);
     if (d->kv_dtype == KVD_INT4) return kvd::lowbit_record_bytes(4, pool_ng(d));
     if (d->kv_dtype == KVD_INT2) return kvd::lowbit_record_bytes(2, pool_ng(d));
     return d->kv_dtype == KVD_FP8_E4M3 || d->kv_dtype == KVD_ANGLE ? kvd::kRecordFp8 : kvd::kRecordBf16;
@@ -170,6 +122,15 @@ kvd_status kvd_pool_bytes(const kvd_pool_desc* desc, size_t* pool_bytes, size_t*
     kvd_status st = check_desc(desc);
     if (st != KVD_OK) return st;
     if (!kv_bytes || !pool_bytes) return KVD_ERR_INVALID;
+    if (latent_dtype(desc->kv_dtype)) {   // a record a block; 8 bits: 16 fp32 scales in it
+        size_t blocks = 0;
+        const bool fp8 = desc->kv_dtype == KVD_LATENT_FP8;
+        if (!mul_ok(static_cast<size_t>(desc->num_layers), static_cast<size_t>(desc->num_blocks), &blocks) ||
+            !mul_ok(blocks, record_bytes(desc), pool_bytes))
+            return KVD_ERR_INVALID;
+        *kv_bytes = *pool_bytes - (fp8 ? blocks * kvd::kBs * sizeof(float) : 0);
+        return KVD_OK;
+    }
     // a mixed pool sizes every record slot for BF16 (an 8-bit block uses the first part of it);
     // element bits: 16, 8, 4 or 2
     const bool fp8_records = desc->kv_dtype == KVD_FP8_E4M3 || desc->kv_dtype == KVD_ANGLE;
@@ -245,6 +206,7 @@ kvd_status kvd_pool_info(const kvd_pool* pool, kvd_pool_desc* desc, int64_t* hos
 kvd_status kvd_tier_bytes(const kvd_pool_desc* desc, int64_t host_blocks, size_t* host_bytes, size_t* staging_bytes) {
     kvd_status st = check_desc(desc);
     if (st != KVD_OK) return st;
+    if (latent_dtype(desc->kv_dtype)) return KVD_ERR_UNSUPPORTED;
     if (host_blocks < 0 || !host_bytes || !staging_bytes) return KVD_ERR_INVALID;
     const size_t rec = record_bytes(desc);
     size_t layer = 0, all = 0;
@@ -267,6 +229,7 @@ kvd_status kvd_pool_set_block_formats(kvd_pool* pool, const uint8_t* block_fmt, 
 kvd_status kvd_pool_attach_host_tier(kvd_pool* pool, void* host_mem, size_t host_len, void* staging_mem,
                                      size_t staging_len, int64_t host_blocks) {
     if (!pool || host_blocks < 0) return KVD_ERR_INVALID;
+    if (is_latent(pool) && host_blocks > 0) return KVD_ERR_UNSUPPORTED;
     if ((pool->desc.kv_dtype == KVD_MIXED || pool->desc.kv_dtype == KVD_ANGLE || lowbit_dtype(pool->desc.kv_dtype)) &&
         host_blocks > 0)
         return KVD_ERR_UNSUPPORTED;
@@ -429,6 +392,7 @@ void kvd_pool_destroy(kvd_pool* pool) {
 kvd_status kvd_append_kv(kvd_pool* pool, int layer, const void* k_new, const void* v_new,
                          const int64_t* slot_mapping, int n_tokens, void* stream) {
     if (!pool || layer < 0 || layer >= pool->desc.num_layers || n_tokens < 0) return KVD_ERR_INVALID;
+    if (is_latent(pool)) return KVD_ERR_UNSUPPORTED;
     if (n_tokens == 0) return KVD_OK;
     if (!k_new || !v_new || !slot_mapping) return KVD_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(k_new) & 7u) || (reinterpret_cast<uintptr_t>(v_new) & 7u)) return KVD_ERR_INVALID;
@@ -451,6 +415,7 @@ kvd_status kvd_append_kv(kvd_pool* pool, int layer, const void* k_new, const voi
 
 static kvd_status check_decode_shape(const kvd_pool* pool, int n_q, int batch, int max_seq_len) {
     if (!pool || n_q < 1 || batch < 0 || max_seq_len < 1) return KVD_ERR_INVALID;
+    if (is_latent(pool)) return KVD_ERR_UNSUPPORTED;
     if (n_q % pool->desc.n_kv != 0) return KVD_ERR_INVALID;
     const int g = n_q / pool->desc.n_kv;
     if (g > kvd::kMaxG || batch > kvd::kMaxBatch) return KVD_ERR_UNSUPPORTED;
@@ -675,6 +640,7 @@ kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_s
                            const kvd_rope_desc* rope, const int64_t* slot_mapping, int n_tokens, void* q_out,
                            int64_t q_out_stride, void* stream) {
     if (!pool || layer < 0 || layer >= pool->desc.num_layers || n_q < 0 || n_tokens < 0 || !rope) return KVD_ERR_INVALID;
+    if (is_latent(pool)) return KVD_ERR_UNSUPPORTED;
     if (rope->rot_dim < 2 || (rope->rot_dim & 1) || !rope->turns || (rope->interleaved != 0 && rope->interleaved != 1))
         return KVD_ERR_INVALID;
     if (rope->rot_dim > kvd::kDh || n_q > 65536) return KVD_ERR_UNSUPPORTED;
@@ -730,6 +696,7 @@ kvd_status kvd_rope_append(kvd_pool* pool, int layer, const void* q, int64_t q_s
 
 static kvd_status check_chunk_shape(const kvd_pool* pool, int n_q, int batch) {
     if (!pool || n_q < 1 || batch < 0 || n_q % pool->desc.n_kv != 0) return KVD_ERR_INVALID;
+    if (is_latent(pool)) return KVD_ERR_UNSUPPORTED;
     if (n_q / pool->desc.n_kv > kvd::kMaxG || batch > kvd::kMaxBatch) return KVD_ERR_UNSUPPORTED;
     return KVD_OK;
 }
@@ -815,7 +782,7 @@ kvd_status kvd_chunk_attn(kvd_pool* pool, int layer, const void* q, int n_q, con
 
 static kvd_status compact_layout(const kvd_pool* pool, int batch, int max_blocks_per_seq, size_t* claim_off, size_t* total) {
     if (!pool || batch < 0 || max_blocks_per_seq < 1) return KVD_ERR_INVALID;
-    if (pool->desc.kv_dtype == KVD_MIXED || batch > 65535) return KVD_ERR_UNSUPPORTED;
+    if (is_latent(pool) || pool->desc.kv_dtype == KVD_MIXED || batch > 65535) return KVD_ERR_UNSUPPORTED;
     if (pool->desc.num_blocks + pool->host_blocks > (1 << 27)) return KVD_ERR_UNSUPPORTED;
     size_t n = 0;
     if (!mul_ok(static_cast<size_t>(batch), static_cast<size_t>(max_blocks_per_seq), &n) ||

@@ -1,0 +1,250 @@
+// kvd_latent_cache.cu — the latent cache is written (norm, rotation, quantisation) and read back.
+//
+// Append, token n with latent x, key part k and position p:
+//   y = x·w / sqrt(mean(x²) + eps)      (w: the norm's weights; without them y = x)
+//   r = R(p)·k, and for every query head q' = R(p)·q, R the rotation of kvd_rope_append over 64 dims
+//   bf16 record: y and r rounded to bf16; 8-bit record: s = fp32(max|y|/448) (1 for a zero row), codes e4m3(y/s),
+//   rounded once from fp32, and r in bf16.
+// Read back: y (code·s, rounded to bf16) and r, side by side.
+#include "kvd_common.cuh"
+#include "kvd_latent.h"
+
+namespace kvd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPos = 1 << 24;       // positions a float holds exactly
+
+__device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void st16(void* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// cos and sin (times m) of a lane's 8 dims of a rotated vector of 64: by pair if neighbours are paired, else by dim,
+// where the sine has the sign with which it multiplies the partner.  Angles as in kvd_rope_append: turns per position as
+// hi + lo, the rounding error of pos·hi from one fma.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void lane_turns(float2 (&f)[8], const LatentAppendParams& p, float pos, int lane8) {
+    const int half = p.rot >> 1;
+    #pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = make_float2(1.f, 0.f);
+        const int d = lane8 * 8 + e;
+        const int pair = INTERLEAVED ? lane8 * 4 + e : d < half ? d : d - half;
+        if (INTERLEAVED ? e < 4 && pair < half : d < p.rot) {
+            const float2 t = p.turns[pair];
+            const float a = __fmul_rn(pos, t.x);
+            const float rest = __fmaf_rn(pos, t.x, -a);
+            const float turn = __fadd_rn(__fsub_rn(a, rintf(a)), __fmaf_rn(pos, t.y, rest));
+            float sn, cn;
+            sincospif(2.f * turn, &sn, &cn);
+            f[e] = make_float2(cn * p.mscale, sn * p.mscale);
+            if (!INTERLEAVED && d < half) f[e].y = -f[e].y;
+        }
+    }
+}
+
+// Eight dims of a vector of 64 by each of 8 lanes, rotated in fp32 and rounded to bf16; dims past rot keep their bits.
+// row: the vector in memory, for partners that do not stand in one lane's piece.
+template <bool INTERLEAVED>
+__device__ __forceinline__ uint4 rotate8(uint4 raw, const float2 (&f)[8], int rot, int lane8, const uint16_t* row, bool on) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o[4];
+    if constexpr (INTERLEAVED) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack_bf16(w[i]), c = f[i];
+            const uint32_t v = pack_bf16(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+            o[i] = lane8 * 8 + 2 * i < rot ? v : w[i];
+        }
+    } else {
+        const int half = rot >> 1, lanes = half >> 3, lane = threadIdx.x & 31;
+        const bool whole = (half & 7) == 0;   // partners stand half/8 lanes apart, at the same place
+        const int other = (lane & 24) | ((lane8 < lanes ? lane8 + lanes : lane8 - lanes) & 7);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack_bf16(w[i]);
+            float2 y = unpack_bf16(__shfl_sync(kFull, w[i], other));
+            if (!whole && on) {
+                const int d = lane8 * 8 + 2 * i;
+                const int a = d < half ? d + half : d - half, b = d + 1 < half ? d + 1 + half : d + 1 - half;
+                if (d < rot) {   // (rot is even)
+                    y.x = __uint_as_float(static_cast<uint32_t>(row[a]) << 16);
+                    y.y = __uint_as_float(static_cast<uint32_t>(row[b]) << 16);
+                }
+            }
+            const uint32_t v = pack_bf16(fmaf(y.x, f[2 * i].y, x.x * f[2 * i].x), fmaf(y.y, f[2 * i + 1].y, x.y * f[2 * i + 1].x));
+            o[i] = lane8 * 8 + 2 * i < rot ? v : w[i];
+        }
+        __syncwarp();   // every partner is read before any lane's result is written over it
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void unpack8(float* x, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = unpack_bf16(w[i]);
+        x[2 * i] = a.x;
+        x[2 * i + 1] = a.y;
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ uint32_t codes4(const float* x, float s) {
+    const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[0], s), __fdiv_rn(x[1], s)), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2], s), __fdiv_rn(x[3], s)), __NV_SATFINITE, __NV_E4M3);
+    return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+}
+
+// A warp takes one token's latent and key part, or p.heads of its query heads, four at a time.
+template <bool FP8, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, lane8 = lane & 7;
+    const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int groups = (p.n_q + p.heads - 1) / p.heads;
+    if (task >= p.n_tokens * (1 + groups)) return;
+    const bool query = task >= p.n_tokens;
+    const int64_t n = query ? (task - p.n_tokens) / groups : task;
+    int pos = 0;
+    if (p.turns) {
+        pos = p.positions[n];
+        if (pos < 0 || pos >= kMaxPos) {
+            if (lane == 0) report(p.err, KVD_ERR_OOB);
+            return;
+        }
+    }
+    float2 f[8];
+    if (query) {
+        const int h0 = static_cast<int>((task - p.n_tokens) % groups) * p.heads, h1 = min(h0 + p.heads, p.n_q);
+        lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane8);
+        for (int h = h0 + (lane >> 3); h - (lane >> 3) < h1; h += 4) {
+            const bool on = h < h1;
+            const uint16_t* row = p.q_rope + n * p.q_stride + h * p.q_head;
+            const uint4 x = on ? ld16(row + lane8 * 8) : make_uint4(0, 0, 0, 0);
+            const uint4 y = rotate8<INTERLEAVED>(x, f, p.rot, lane8, row, on);
+            if (on) st16(p.q_out + n * p.out_stride + h * p.out_head + lane8 * 8, y);
+        }
+        return;
+    }
+    const int64_t slot = p.slot_mapping[n];
+    if (slot < 0) return;
+    if (slot >= p.num_blocks * kBs) {
+        if (lane == 0) report(p.err, KVD_ERR_OOB);
+        return;
+    }
+    uint8_t* record = p.mem + (slot / kBs) * latent_record_bytes(FP8);
+    const int t = static_cast<int>(slot % kBs);
+    const uint16_t* row = p.latent + n * p.latent_stride;
+    const uint16_t* key = p.k_rope + n * p.k_stride;
+    uint4 raw[2] = {ld16(row + lane * 8), ld16(row + 256 + lane * 8)};
+    uint4 rot = lane < 8 ? ld16(key + lane8 * 8) : make_uint4(0, 0, 0, 0);
+    if (p.turns) {
+        lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane8);
+        rot = rotate8<INTERLEAVED>(rot, f, p.rot, lane8, key, lane < 8);
+    }
+    float x[16];
+    if (FP8 || p.norm) {
+        unpack8(x, raw[0]);
+        unpack8(x + 8, raw[1]);
+    }
+    if (p.norm) {
+        float w[16], sum = 0.f;
+        unpack8(w, ld16(p.norm + lane * 8));
+        unpack8(w + 8, ld16(p.norm + 256 + lane * 8));
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fmaf(x[i], x[i], sum);
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        const float r = __frcp_rn(__fsqrt_rn(fmaf(sum, 1.f / kLatDim, p.eps)));
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+        raw[0] = pack8(x);
+        raw[1] = pack8(x + 8);
+    }
+    if constexpr (FP8) {
+        float top = 0.f;
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const float s = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+        #pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint2*>(record + latent_code(t, lane + 32 * i)) = make_uint2(codes4(x + 8 * i, s), codes4(x + 8 * i + 4, s));
+        if (lane < 8) st16(record + latent_rope_piece(t, lane), rot);
+        if (lane == 0) *reinterpret_cast<float*>(record + kLatScales + 4 * t) = s;
+    } else {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) st16(record + latent_piece(t, lane + 32 * i), raw[i]);
+        if (lane < 8) st16(record + latent_piece(t, 64 + lane), rot);
+    }
+}
+
+// A warp a row; the rows of request b by the CTAs of column b.
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int64_t r0 = p.row_start[b], r1 = p.row_start[b + 1];
+    const int64_t first = p.first ? p.first[b] : 0;
+    if (r0 < 0 || r1 < r0 || r1 > p.n_rows || first < 0 || first + (r1 - r0) > static_cast<int64_t>(p.max_blocks) * kBs) {
+        if (threadIdx.x == 0) report(p.err, KVD_ERR_OOB);
+        return;
+    }
+    for (int64_t r = r0 + static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < r1;
+         r += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+        const int64_t pos = first + (r - r0);
+        const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+        const int t = static_cast<int>(pos % kBs);
+        if (block < 0 || block >= p.num_blocks) {
+            if (lane == 0) report(p.err, KVD_ERR_OOB);
+            continue;
+        }
+        const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
+        uint16_t* out = p.out + r * p.out_stride;
+        if constexpr (FP8) {
+            const float s = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
+                uint32_t h[4], o[4];
+                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 v = unpack_f16(h[k]);
+                    o[k] = pack_bf16(v.x * s, v.y * s);
+                }
+                st16(out + (lane + 32 * i) * 8, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+            if (lane < 8) st16(out + kLatDim + lane * 8, ld16(record + latent_rope_piece(t, lane)));
+        } else {
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) st16(out + (lane + 32 * i) * 8, ld16(record + latent_piece(t, lane + 32 * i)));
+            if (lane < 8) st16(out + kLatDim + lane * 8, ld16(record + latent_piece(t, 64 + lane)));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(LatentAppendParams p, bool fp8, int num_sms, cudaStream_t stream) {
+    p.heads = 4;
+    const int64_t tasks = p.n_tokens * (1 + (p.n_q + p.heads - 1) / p.heads);
+    const dim3 grid(static_cast<unsigned>((tasks + kThreads / 32 - 1) / (kThreads / 32)));
+    auto* kernel = fp8 ? (p.interleaved ? append_kernel<true, true> : append_kernel<true, false>)
+                       : (p.interleaved ? append_kernel<false, true> : append_kernel<false, false>);
+    return launch_dependent(kernel, grid, dim3(kThreads), 0, -1, stream, p);
+}
+
+cudaError_t launch_latent_gather(const LatentGatherParams& p, bool fp8, int num_sms, cudaStream_t stream) {
+    const int64_t most = (p.n_rows + kThreads / 32 - 1) / (kThreads / 32), share = (16 * num_sms + p.B - 1) / p.B;
+    const dim3 grid(static_cast<unsigned>(most < share ? most : share), static_cast<unsigned>(p.B));
+    return launch_dependent(fp8 ? gather_kernel<true> : gather_kernel<false>, grid, dim3(kThreads), 0, -1, stream, p);
+}
+
+}  // namespace kvd
