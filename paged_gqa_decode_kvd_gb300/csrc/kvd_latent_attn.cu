@@ -2,14 +2,26 @@
 //
 // Row (token i of the T new tokens of request b, head h), len = seq_lens[b], P = len − T + i:
 //   l_t = scale·<q, (c_t, r_t)> over 512 + 64 dims, t ≤ P and retained;  out = Σ_t softmax(l)_t·c_t,  lse = log Σ exp(l_t).
-// A warp a row: a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
-#include "kvd_common.cuh"
 #include "kvd_latent.h"
+#include "kvd_tcgen.cuh"
 
 namespace kvd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kTile = 64;              // positions per tile: four blocks
+constexpr int kRows = kLatUnitRows;
+constexpr int kStages = 3;
+constexpr int kTileBytes = kTile * kLatKey * 2;
+constexpr int kGroup = 9216;           // bytes of eight tokens of a tile
+constexpr int kProducerWarp = 4, kIssueWarp = 5, kFixWarp = 6, kConvertWarp = 8, kConvertWarps = 8;
+constexpr int threads_of(bool fp8) { return fp8 ? 32 * (kConvertWarp + kConvertWarps) : 256; }
+constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
+constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so
+constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
+// Tensor memory.  M = 64 leaves half of the lanes: 0 .. 15 of each 32 hold Q and S, 16 .. 31 hold O.
+constexpr uint32_t kColQ = 0, kColS = 288, kColR = 352, kHalf = 16u << 16;
+constexpr int kUnitTiles = 3;          // what a unit costs beside its tiles, in tiles
+constexpr int kMinShare = 2;
 
 __device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void unpack8(float* x, uint4 v) {
@@ -21,94 +33,866 @@ __device__ __forceinline__ void unpack8(float* x, uint4 v) {
         x[2 * i + 1] = a.y;
     }
 }
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const LatentAttnParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int s0 = p.q_start[b], s1 = p.q_start[b + 1], len = p.seq_lens[b];
-    if (s0 < 0 || s1 < s0 || s1 > p.n_tokens) {
-        if (threadIdx.x == 0) report(p.err, KVD_ERR_OOB);
-        return;
+struct Info {
+    alignas(16) float scale[kTile];    // 8-bit records: by column
+    unsigned long long mask;           // bit 16·block + t: position may be attended by the unit's last row
+    int base;                          // position of column 0
+    int id[4];                         // physical blocks, −1: none
+};
+constexpr int kBadRing = 8;
+
+struct Smem {
+    uint8_t k[kStages][kTileBytes];
+    uint8_t p[kRows * kTile * 2];
+    Info info[kStages];
+    uint64_t full[kStages], ready[kStages], empty[kStages], s_full, s_free, p_full, q_full, drain;
+    uint32_t tmem;
+    int bad[kBadRing];                 // segment + 1: a row of it that others may not attend has non-finite values
+    volatile int abort;
+    // the CTA's share of the schedule
+    int64_t at, remaining, share;
+    int b, tb, off, extra;
+};
+
+struct Request {
+    int s0, T, len;   // first row, new tokens, context (−1: bad length, nothing is attended)
+};
+struct Segment {
+    int b, tb, t0, t1, tiles;
+    int s0, T, len;
+    int tok0, first, end;    // first token, its position, positions that the last row attends
+    int parts;               // CTAs that share the unit
+    bool multi;              // rows of more than one token
+};
+
+__device__ __forceinline__ Request load_request(const LatentAttnParams& p, int b, bool tell) {
+    Request r;
+    r.s0 = p.q_start[b];
+    const int s1 = p.q_start[b + 1], len = p.seq_lens[b];
+    r.T = 0;
+    r.len = -1;
+    if (r.s0 < 0 || s1 < r.s0 || s1 > p.n_tokens) {
+        if (tell) report(p.err, KVD_ERR_OOB);
+        return r;
     }
-    const int T = s1 - s0;
-    if (T == 0) return;
-    const bool good = len >= T && static_cast<int64_t>(len) <= static_cast<int64_t>(p.max_blocks) * kBs;
-    if (!good && threadIdx.x == 0) report(p.err, KVD_ERR_OOB);
-    const int64_t rows = static_cast<int64_t>(T) * p.n_q, warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
-        const int64_t row = static_cast<int64_t>(s0) * p.n_q + r;
-        const uint16_t* qr = p.q + row * kLatKey;
-        float q[24], acc[16], m = -INFINITY, sum = 0.f;
-        unpack8(q, ld16(qr + lane * 8));
-        unpack8(q + 8, ld16(qr + 256 + lane * 8));
-        unpack8(q + 16, lane < 8 ? ld16(qr + kLatDim + lane * 8) : make_uint4(0, 0, 0, 0));
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-        const int end = good ? len - T + static_cast<int>(r / p.n_q) + 1 : 0;
-        for (int pos = 0; pos < end; ++pos) {
-            const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
-            const int t = pos % kBs;
-            if (block < 0 || block >= p.num_blocks) {
-                if (lane == 0 && t == 0) report(p.err, KVD_ERR_OOB);
-                continue;
+    r.T = s1 - r.s0;
+    if (r.T == 0) return r;
+    r.len = len;
+    if (r.len < r.T || static_cast<int64_t>(r.len) > static_cast<int64_t>(p.max_blocks) * kBs) {
+        if (tell) report(p.err, KVD_ERR_OOB);
+        r.len = -1;
+    }
+    return r;
+}
+__device__ __forceinline__ int unit_end(const Request& r, int tb, int tpb) {
+    return r.len < 0 ? 0 : r.len - r.T + min((tb + 1) * tpb, r.T);
+}
+__device__ __forceinline__ int unit_tiles(const Request& r, int tb, int tpb) {
+    return r.len < 0 ? 1 : (unit_end(r, tb, tpb) + kTile - 1) / kTile;
+}
+// Tiles of units 0 .. k-1: Σ ⌊(c + i·tpb)/64⌋, whose remainders repeat every 64 units.
+__device__ inline int64_t tiles_before(const Request& r, int k, int tpb) {
+    if (r.len < 0) return k;
+    const int n = (r.T + tpb - 1) / tpb;
+    const int64_t whole = min(k, n - 1), c = static_cast<int64_t>(r.len) - r.T + tpb + kTile - 1;
+    int64_t rest = 0;
+    if (whole >= 64) {
+        for (int i = 0; i < 64; ++i) rest += (c + static_cast<int64_t>(i) * tpb) & 63;
+        rest *= whole / 64;
+    }
+    for (int64_t i = whole & ~63ll; i < whole; ++i) rest += (c + i * tpb) & 63;
+    int64_t s = (tpb * (whole * (whole - 1) / 2) + c * whole - rest) >> 6;
+    if (k == n) s += unit_tiles(r, n - 1, tpb);
+    return s;
+}
+
+struct Heads {
+    int blocks, each, tpb, first, n;   // head blocks, heads of one, tokens of a unit; this CTA's heads
+    __device__ __forceinline__ Heads(const LatentAttnParams& p, int block) {
+        blocks = (p.n_q + kRows - 1) / kRows;
+        each = (p.n_q + blocks - 1) / blocks;
+        tpb = kRows / each;
+        first = block * each;
+        n = min(each, p.n_q - first);
+    }
+};
+
+// The CTA's segments in order; every role walks them on its own.
+struct Walk {
+    int64_t at, remaining, share;
+    int b, tb, off, extra, tpb;
+    Request r;
+    __device__ __forceinline__ Walk(const LatentAttnParams& p, const Smem& s, int tokens)
+        : at(s.at), remaining(s.remaining), share(s.share), b(s.b), tb(s.tb), off(s.off), extra(s.extra), tpb(tokens), r{0, 0, -1} {
+        if (remaining > 0) r = load_request(p, b, false);
+    }
+    __device__ __forceinline__ bool next(const LatentAttnParams& p, Segment& g) {
+        while (remaining > 0) {
+            g.b = b;
+            g.tb = tb;
+            g.tiles = unit_tiles(r, tb, tpb);
+            const int64_t start = at - off + extra;   // of the unit's tiles in the schedule
+            g.parts = static_cast<int>((start + g.tiles - 1) / share - start / share) + 1;
+            const int take = static_cast<int>(min(static_cast<int64_t>(g.tiles) + extra - off, remaining));
+            g.t0 = max(off - extra, 0);
+            g.t1 = off + take - extra;
+            g.s0 = r.s0;
+            g.T = r.T;
+            g.len = r.len;
+            g.end = unit_end(r, tb, tpb);
+            g.tok0 = tb * tpb;
+            g.first = r.len < 0 ? -1 : r.len - r.T + g.tok0;
+            g.multi = min(tpb, r.T - g.tok0) > 1;
+            at += take;
+            remaining -= take;
+            off = 0;
+            if (remaining > 0 && ++tb * tpb >= r.T) {
+                tb = 0;
+                do {
+                    if (++b >= p.B) {
+                        remaining = 0;
+                        break;
+                    }
+                    r = load_request(p, b, false);
+                } while (r.T == 0);
             }
-            if (p.retain && !((p.retain[block] >> t) & 1)) continue;
-            const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
-            float k[24];
-            if constexpr (FP8) {
-                const float s = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
+            if (g.t1 > g.t0) return true;
+        }
+        return false;
+    }
+};
+
+// The CTA's share, by every thread of the block; scratch holds 2·p.B int64.
+__device__ inline void make_schedule(const LatentAttnParams& p, Smem& s, int64_t* scratch, const Heads& hd, int threads) {
+    const int tid = threadIdx.x, lane = tid & 31, tpb = hd.tpb;
+    for (int b = tid; b < p.B; b += threads) {
+        const Request r = load_request(p, b, blockIdx.x == 0);
+        const int units = (r.T + tpb - 1) / tpb;
+        scratch[2 * b] = r.T ? tiles_before(r, units, tpb) : 0;
+        scratch[2 * b + 1] = units;
+    }
+    __syncthreads();
+    if (tid >= 32) return;
+    const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks;
+    int64_t tiles = 0, units = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        tiles += scratch[2 * b];
+        units += scratch[2 * b + 1];
+    }
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        tiles += __shfl_xor_sync(kFull, tiles, o);
+        units += __shfl_xor_sync(kFull, units, o);
+    }
+    // a small call is cut into its smallest shares; there the border must not fall beside the tiles
+    const int extra = static_cast<int>(min(static_cast<int64_t>(kUnitTiles), tiles / (8 * lanes)));
+    const int64_t total = tiles + units * extra;
+    const int64_t share = max((total + lanes - 1) / lanes, static_cast<int64_t>(kMinShare));
+    const int64_t lo = min(share * me, total), hi = me < lanes ? min(lo + share, total) : lo;
+    if (lane == 0) {
+        s.at = lo;
+        s.remaining = hi - lo;
+        s.share = share;
+        s.extra = extra;
+    }
+    int64_t before = 0;
+    for (int b0 = 0; hi > lo && b0 < p.B; b0 += 32) {
+        const int64_t c = b0 + lane < p.B ? scratch[2 * (b0 + lane)] + extra * scratch[2 * (b0 + lane) + 1] : 0;
+        int64_t up = c;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(kFull, up, o);
+            if (lane >= o) up += v;
+        }
+        up += before;
+        if (lo >= up - c && lo < up) {   // one lane
+            const int b = b0 + lane;
+            const Request r = load_request(p, b, false);
+            const int64_t in = lo - (up - c);
+            int a = 0, z = (r.T + tpb - 1) / tpb;   // the last unit of [a, z) that starts at or before `in`
+            while (z - a > 1) {
+                const int mid = a + (z - a) / 2;
+                if (tiles_before(r, mid, tpb) + static_cast<int64_t>(mid) * extra <= in) a = mid;
+                else z = mid;
+            }
+            s.b = b;
+            s.tb = a;
+            s.off = static_cast<int>(in - tiles_before(r, a, tpb) - static_cast<int64_t>(a) * extra);
+        }
+        before = __shfl_sync(kFull, up, 31);
+        if (before > lo) break;
+    }
+}
+
+__device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        if (__all_sync(kFull, mbar_try_wait(bar, phase & 1u))) return true;
+        if (s.abort) return false;
+    }
+    s.abort = 1;   // reported at the kernel's end
+    return false;
+}
+
+// ------------------------------------------------------------- one row, plainly
+// A warp a row: a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
+template <bool FP8>
+__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end) {
+    const int lane = threadIdx.x & 31;
+    const uint16_t* qr = p.q + row * kLatKey;
+    float q[24], acc[16], m = -INFINITY, sum = 0.f;
+    unpack8(q, ld16(qr + lane * 8));
+    unpack8(q + 8, ld16(qr + 256 + lane * 8));
+    unpack8(q + 16, lane < 8 ? ld16(qr + kLatDim + lane * 8) : make_uint4(0, 0, 0, 0));
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int pos = 0; pos < end; ++pos) {
+        const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+        const int t = pos % kBs;
+        if (block < 0 || block >= p.num_blocks || (p.retain && !((p.retain[block] >> t) & 1))) continue;
+        const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
+        float k[24];
+        if constexpr (FP8) {
+            const float s = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
+                uint32_t h[4];
+                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
                 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
-                    uint32_t h[4];
-                    e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
-                    e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = unpack_f16(h[j]);
-                        k[8 * i + 2 * j] = v.x * s;
-                        k[8 * i + 2 * j + 1] = v.y * s;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = unpack_f16(h[j]);
+                    k[8 * i + 2 * j] = v.x * s;
+                    k[8 * i + 2 * j + 1] = v.y * s;
+                }
+            }
+            unpack8(k + 16, lane < 8 ? ld16(record + latent_rope_piece(t, lane)) : make_uint4(0, 0, 0, 0));
+        } else {
+            unpack8(k, ld16(record + latent_piece(t, lane)));
+            unpack8(k + 8, ld16(record + latent_piece(t, 32 + lane)));
+            unpack8(k + 16, lane < 8 ? ld16(record + latent_piece(t, 64 + lane)) : make_uint4(0, 0, 0, 0));
+        }
+        float dot = 0.f;
+        #pragma unroll
+        for (int i = 0; i < 24; ++i) dot = fmaf(q[i], k[i], dot);
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        const float l = dot * p.scale_log2, top = fmaxf(m, l);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - ref), w = exp2f(l - ref);
+        m = top;
+        sum = sum * f + w;
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, k[i], acc[i] * f);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t at = row * kLatDim + (i >> 3) * 256 + lane * 8 + (i & 7);
+        if (p.out_f32) static_cast<float*>(p.out)[at] = acc[i] * inv;
+        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
+    }
+    if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------------ producer
+// Follows the block table, eight tiles of ids at a time; bf16 records are copied as they are.
+template <bool FP8>
+__device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, const Heads& hd, int lane) {
+    Walk walk(p, s, hd.tpb);
+    Segment g;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks;
+        #pragma unroll 1
+        for (int t = g.t0; ok && t < g.t1; t += 8) {
+            const int pos = t * kTile + lane * kBs;
+            int id = -1;
+            uint32_t bits = 0;
+            if (pos < g.end && t + (lane >> 2) < g.t1) {
+                id = table[pos / kBs];
+                if (id < 0 || id >= p.num_blocks) {
+                    report(p.err, KVD_ERR_OOB);
+                    id = -1;
+                } else {
+                    bits = p.retain ? p.retain[id] : 0xffffu;
+                    if (g.end - pos < kBs) bits &= (1u << (g.end - pos)) - 1u;
+                }
+            }
+            #pragma unroll 1
+            for (int u = 0; ok && u < 8 && t + u < g.t1; ++u, ++n) {
+                const uint32_t st = n % kStages;
+                if (n >= kStages) ok = wait_bar(s, &s.empty[st], n / kStages - 1);
+                if (!ok) break;
+                unsigned long long mask = 0;
+                int ids[4], copies = 0;
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    ids[k] = __shfl_sync(kFull, id, 4 * u + k);
+                    mask |= static_cast<unsigned long long>(__shfl_sync(kFull, bits, 4 * u + k)) << (16 * k);
+                    copies += ids[k] >= 0;
+                }
+                if (lane == 0) {
+                    Info& info = s.info[st];
+                    info.mask = mask;
+                    info.base = (t + u) * kTile;
+                    if constexpr (FP8) {
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k) info.id[k] = ids[k];
+                        mbar_arrive(&s.full[st]);
+                    } else {
+                        constexpr uint32_t kRecord = latent_record_bytes(false);
+                        if (copies) mbar_arrive_expect_tx(&s.full[st], copies * kRecord);
+                        else mbar_arrive(&s.full[st]);
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (ids[k] >= 0) bulk_copy(s.k[st] + k * kRecord, p.mem + static_cast<int64_t>(ids[k]) * kRecord, kRecord, &s.full[st]);
                     }
                 }
-                unpack8(k + 16, lane < 8 ? ld16(record + latent_rope_piece(t, lane)) : make_uint4(0, 0, 0, 0));
-            } else {
-                unpack8(k, ld16(record + latent_piece(t, lane)));
-                unpack8(k + 8, ld16(record + latent_piece(t, 32 + lane)));
-                unpack8(k + 16, lane < 8 ? ld16(record + latent_piece(t, 64 + lane)) : make_uint4(0, 0, 0, 0));
+                __syncwarp();
             }
-            float dot = 0.f;
+        }
+    }
+    if (!FP8 && s.abort) {   // copies under way must land in memory that is still this block's
+        for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) mbar_wait(&s.full[k % kStages], (k / kStages) & 1u, nullptr, kWaitNs);
+    }
+}
+
+// ----------------------------------------------------------------------- fix
+// Rows that nobody may attend are zeroed (their weight is 0, and 0·NaN would be NaN); a row that is attended by later
+// tokens of the unit only and is not finite is noted: the unit's rows are then computed one by one.
+__device__ __forceinline__ void fixer(Smem& s, const LatentAttnParams& p, const Heads& hd, int lane) {
+    Walk walk(p, s, hd.tpb);
+    Segment g;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int seg = 0; ok && walk.next(p, g); ++seg) {
+        #pragma unroll 1
+        for (int t = g.t0; t < g.t1; ++t, ++n) {
+            const uint32_t st = n % kStages;
+            ok = wait_bar(s, &s.full[st], n / kStages);
+            if (!ok) break;
+            unsigned long long zero = ~s.info[st].mask, look = 0;
+            if (g.multi && s.info[st].base + kTile > g.first + 1) {
+                const int from = max(g.first + 1 - s.info[st].base, 0);   // columns behind the first row's position
+                look = ~0ull << from & s.info[st].mask;
+            }
+            for (unsigned long long todo = zero | look; todo; todo &= todo - 1) {
+                const int c = __ffsll(todo) - 1;
+                uint8_t* row = s.k[st] + (c >> 3) * kGroup + (c & 7) * 128;
+                const bool clear = zero >> c & 1;
+                uint32_t odd = 0;
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint4* piece = reinterpret_cast<uint4*>(row + ((lane >> 3) + 4 * k) * 1024 + (lane & 7) * 16);
+                    if (clear) {
+                        *piece = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint4 v = *piece;
+                        odd |= nonfinite(v.x) | nonfinite(v.y) | nonfinite(v.z) | nonfinite(v.w);
+                    }
+                }
+                if (odd) s.bad[seg % kBadRing] = seg + 1;
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.ready[st]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- convert
+// 8-bit records become bf16 operands: codes exactly (every e4m3 value is a bf16 value), the scale stays outside.  A warp
+// takes eight tokens of a tile: 64 codes of each of them, 512 bytes, a load.
+__device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, const Heads& hd, int warp, int lane) {
+    Walk walk(p, s, hd.tpb);
+    Segment g;
+    uint32_t n = 0;
+    bool ok = true;
+    const int r = lane >> 2, j = lane & 3, tok = (warp & 1) * 8 + r;   // token of its block, pieces 2j and 2j + 1
+    for (int seg = 0; ok && walk.next(p, g); ++seg) {
+        #pragma unroll 1
+        for (int t = g.t0; t < g.t1; ++t, ++n) {
+            const uint32_t st = n % kStages;
+            ok = wait_bar(s, &s.full[st], n / kStages);
+            if (!ok) break;
+            const Info& info = s.info[st];
+            const int id = info.id[warp >> 1], c = warp * 8 + r;
+            const bool on = info.mask >> c & 1;
+            const uint8_t* record = p.mem + static_cast<int64_t>(max(id, 0)) * latent_record_bytes(true);
+            uint4 code[8], rot[2];
+            float scale = 0.f;
             #pragma unroll
-            for (int i = 0; i < 24; ++i) dot = fmaf(q[i], k[i], dot);
+            for (int i = 0; i < 8; ++i) code[i] = on ? ld16(record + (warp & 1) * 4096 + i * 512 + r * 64 + j * 16) : make_uint4(0, 0, 0, 0);
             #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-            const float l = dot * p.scale_log2, top = fmaxf(m, l);
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float f = exp2f(m - ref), w = exp2f(l - ref);
-            m = top;
-            sum = sum * f + w;
+            for (int i = 0; i < 2; ++i) rot[i] = on ? ld16(record + kLatCodes + (warp & 1) * 1024 + r * 128 + (2 * j + i) * 16) : make_uint4(0, 0, 0, 0);
+            if (on) scale = *reinterpret_cast<const float*>(record + kLatScales + 4 * tok);
+            uint8_t* group = s.k[st] + warp * kGroup + r * 128;
+            uint32_t odd = 0;
             #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, k[i], acc[i] * f);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+                uint32_t o[8];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16x2x2(w[k], lo, hi);
+                    const float2 a = unpack_f16(lo), b = unpack_f16(hi);
+                    o[2 * k] = pack_bf16(a.x, a.y);
+                    o[2 * k + 1] = pack_bf16(b.x, b.y);
+                    odd |= nonfinite(o[2 * k]) | nonfinite(o[2 * k + 1]);
+                }
+                *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j) ^ r) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j + 1) ^ r) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(group + 8192 + (2 * j + i) * 16) = rot[i];   // (in its order already)
+            if (j == 0) s.info[st].scale[c] = scale;
+            if (on && g.multi && info.base + c > g.first && (odd || !isfinite(scale))) s.bad[seg % kBadRing] = seg + 1;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.ready[st]);
+        }
+    }
+}
+
+// --------------------------------------------------------------------- issue
+// Operands with groups of eight rows `group` bytes apart: rows along M or N (K-major), or along K, where 64 columns of N
+// stand 1,024 bytes apart (N-major).
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr, uint32_t group) {
+    return static_cast<uint64_t>(addr >> 4) | (1ull << 16) | (static_cast<uint64_t>(group >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_n(uint32_t addr) {
+    return static_cast<uint64_t>(addr >> 4) | (64ull << 16) | (static_cast<uint64_t>(kGroup >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <bool FP8>
+__device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, const Heads& hd) {
+    constexpr uint32_t kDescS = mma_desc_bf16(64, kTile), kDescO = mma_desc_bf16(64, 256) | (1u << 16);
+    const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), p_op = uniform(smem_u32(s.p));
+    const uint32_t s_full = uniform(smem_u32(&s.s_full));
+    Walk walk(p, s, hd.tpb);
+    Segment g;
+    uint32_t n = 0, segs = 0;   // tiles before
+    bool ok = true;
+    auto scores = [&](uint32_t i) {   // S(i) = Q·K(i)ᵀ
+        const uint32_t st = i % kStages, op = uniform(k_op + st * kTileBytes);
+        ok = wait_bar(s, &s.ready[st], i / kStages) && (i == 0 || wait_bar(s, &s.s_free, i - 1));
+        if (!ok) return;
+        tcgen_fence_after();
+        if (elect_one()) {
+            #pragma unroll
+            for (int c = 0; c < 9; ++c)
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ts(tmem + (FP8 && c == 8 ? kColR : kColS), tmem + kColQ + c * 32 + k * 8, desc_k(op + c * 1024 + k * 32, kGroup),
+                           kDescS, (FP8 && c == 8 ? k : (c | k)) != 0);
+            mma_commit(s_full);
+        }
+        __syncwarp();
+    };
+    while (ok && walk.next(p, g)) {
+        const uint32_t tiles = uniform(g.t1 - g.t0);
+        ok = wait_bar(s, &s.q_full, segs++);
+        if (ok) scores(n);
+        #pragma unroll 1
+        for (uint32_t i = 0; ok && i < tiles; ++i) {
+            if (i + 1 < tiles) scores(n + i + 1);
+            if (!ok) break;
+            const uint32_t st = (n + i) % kStages, op = uniform(k_op + st * kTileBytes), empty = uniform(smem_u32(&s.empty[st]));
+            ok = wait_bar(s, &s.p_full, n + i);
+            if (!ok) break;
+            tcgen_fence_after();
+            if (elect_one()) {
+                #pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(tmem + kHalf + h * 256, desc_k(p_op + k * 32, 1024), desc_n(op + h * 4096 + k * 2 * kGroup), kDescO,
+                               i > 0 || k > 0);
+                mma_commit(empty);
+            }
+            __syncwarp();
+        }
+        n += tiles;
+    }
+    // the last commits arrive in this block's shared memory: it must still be its own
+    if (!s.abort)
+        for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
+            if (!wait_bar(s, &s.empty[k % kStages], k / kStages)) break;
+    if (s.abort) {   // nothing under way in tensor memory
+        if (elect_one()) mma_commit(smem_u32(&s.drain));
+        __syncwarp();
+        mbar_wait(&s.drain, 0, nullptr, kWaitNs);
+    }
+}
+
+// ------------------------------------------------------------------- softmax
+// 16 lanes × 64 columns: a thread has rows lane/4 and lane/4 + 8, of each column group of eight the two at 2·(lane%4):
+// v[4k], v[4k+1] of the first row, v[4k+2], v[4k+3] of the second.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st_16x64(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+template <bool FP8>
+__device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, const Heads& hd, int warp, int lane) {
+    const uint32_t mine = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int quad = lane & 3;
+    Walk walk(p, s, hd.tpb);
+    Segment g;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int seg = 0; ok && walk.next(p, g); ++seg) {
+        // row r is token r / each, head r % each of the unit
+        auto row_of = [&](int r) -> int64_t {
+            const int tok = r / hd.each, h = r - tok * hd.each;
+            return tok < hd.tpb && g.tok0 + tok < g.T && h < hd.n ? (static_cast<int64_t>(g.s0) + g.tok0 + tok) * p.n_q + hd.first + h : -1;
+        };
+        {   // Q: lanes 0 .. 15 a row each (lanes 16 .. 31 write where the next O will stand)
+            const int64_t row = row_of(warp * 16 + (lane & 15));
+            const uint16_t* src = p.q + max(row, static_cast<int64_t>(0)) * kLatKey;
+            #pragma unroll 1
+            for (int c = 0; c < 9; ++c) {
+                uint32_t v[32];
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 x = row >= 0 && lane < 16 ? ld16(src + c * 64 + i * 8) : make_uint4(0, 0, 0, 0);
+                    v[4 * i] = x.x;
+                    v[4 * i + 1] = x.y;
+                    v[4 * i + 2] = x.z;
+                    v[4 * i + 3] = x.w;
+                }
+                tmem_st32(mine + kColQ + c * 32, v);
+            }
+            tmem_wait_st();
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.q_full);
+        }
+        const int r0 = warp * 16 + (lane >> 2);
+        const int limit[2] = {g.first + r0 / hd.each, g.first + (r0 + 8) / hd.each};   // positions that the rows attend, at most
+        float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        #pragma unroll 1
+        for (int t = g.t0; t < g.t1; ++t, ++n) {
+            const uint32_t st = n % kStages;
+            uint32_t v[32];
+            float x[32];
+            ok = wait_bar(s, &s.ready[st], n / kStages) && wait_bar(s, &s.s_full, n);   // (what is known of the tile, and its S)
+            if (!ok) break;
+            tcgen_fence_after();
+            tmem_ld_16x64(mine + kColS, v);
+            const Info& info = s.info[st];
+            if constexpr (FP8) {
+                uint32_t r[32];
+                tmem_ld_16x64(mine + kColR, r);
+                tmem_wait_ld(v);
+                tmem_wait_ld(r);
+                #pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 f = *reinterpret_cast<const float2*>(&info.scale[8 * k + 2 * quad]);
+                    x[4 * k] = fmaf(__uint_as_float(v[4 * k]), f.x, __uint_as_float(r[4 * k])) * p.scale_log2;
+                    x[4 * k + 1] = fmaf(__uint_as_float(v[4 * k + 1]), f.y, __uint_as_float(r[4 * k + 1])) * p.scale_log2;
+                    x[4 * k + 2] = fmaf(__uint_as_float(v[4 * k + 2]), f.x, __uint_as_float(r[4 * k + 2])) * p.scale_log2;
+                    x[4 * k + 3] = fmaf(__uint_as_float(v[4 * k + 3]), f.y, __uint_as_float(r[4 * k + 3])) * p.scale_log2;
+                }
+            } else {
+                tmem_wait_ld(v);
+                #pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) * p.scale_log2;
+            }
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_free);
+            const unsigned long long mask = info.mask;
+            const int base = info.base;
+            if (mask != ~0ull || (g.multi && base + kTile > g.first + 1)) {
+                #pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    #pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = 8 * k + 2 * quad + e;
+                        const bool on = mask >> c & 1;
+                        if (!on || base + c > limit[0]) x[4 * k + e] = -INFINITY;
+                        if (!on || base + c > limit[1]) x[4 * k + 2 + e] = -INFINITY;
+                    }
+            }
+            float top[2] = {x[0], x[2]};
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                top[0] = fmaxf(top[0], fmaxf(x[4 * k], x[4 * k + 1]));
+                top[1] = fmaxf(top[1], fmaxf(x[4 * k + 2], x[4 * k + 3]));
+            }
+            float factor[2] = {1.f, 1.f};
+            bool moved = false;
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+                if (top[h] > ref[h] + kLazy) {
+                    factor[h] = ex2(ref[h] - top[h]);
+                    sum[h] *= factor[h];
+                    ref[h] = top[h];
+                    moved = true;
+                }
+            }
+            const float z0 = ref[0] == -INFINITY ? 0.f : ref[0], z1 = ref[1] == -INFINITY ? 0.f : ref[1];
+            uint32_t w[16];
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float a = ex2(x[4 * k] - z0), b = ex2(x[4 * k + 1] - z0), c = ex2(x[4 * k + 2] - z1), d = ex2(x[4 * k + 3] - z1);
+                sum[0] += a + b;
+                sum[1] += c + d;
+                if constexpr (FP8) {
+                    const float2 f = *reinterpret_cast<const float2*>(&info.scale[8 * k + 2 * quad]);
+                    a *= f.x;
+                    b *= f.y;
+                    c *= f.x;
+                    d *= f.y;
+                }
+                w[2 * k] = pack_bf16(a, b);
+                w[2 * k + 1] = pack_bf16(c, d);
+            }
+            if (n > 0) ok = wait_bar(s, &s.empty[(n - 1) % kStages], (n - 1) / kStages);   // P and O are free
+            if (!ok) break;
+            if (t > g.t0 && __any_sync(kFull, moved)) {
+                tcgen_fence_after();
+                #pragma unroll 1
+                for (int c = 0; c < 512; c += 64) {
+                    tmem_ld_16x64(mine + kHalf + c, v);
+                    tmem_wait_ld(v);
+                    #pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * factor[i >> 1 & 1]);
+                    tmem_st_16x64(mine + kHalf + c, v);
+                }
+                tmem_wait_st();
+                tcgen_fence_before();
+            }
+            uint8_t* pr = s.p + r0 * 128 + quad * 4;
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                *reinterpret_cast<uint32_t*>(pr + ((k ^ (r0 & 7)) << 4)) = w[2 * k];
+                *reinterpret_cast<uint32_t*>(pr + 1024 + ((k ^ (r0 & 7)) << 4)) = w[2 * k + 1];
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.p_full);
+        }
+        if (ok) ok = wait_bar(s, &s.empty[(n - 1) % kStages], (n - 1) / kStages);
+        if (!ok) break;
+        tcgen_fence_after();
+        const bool whole = g.t0 == 0 && g.t1 == g.tiles, bad = s.bad[seg % kBadRing] == seg + 1;
+        const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
+        const int64_t row[2] = {row_of(r0), row_of(r0 + 8)};
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
+            sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
+        }
+        if (!whole) {
+            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.tb, (g.t0 == 0 ? 1 : 0) | (bad ? 2 : 0), g.parts);
+            #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (quad == 0) {
+                    p.part_ml[(static_cast<int64_t>(slot) * 2) * kRows + r0 + 8 * h] = ref[h];
+                    p.part_ml[(static_cast<int64_t>(slot) * 2 + 1) * kRows + r0 + 8 * h] = sum[h];
+                }
+        } else if (quad == 0 && p.lse_out) {
+            #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (row[h] >= 0) p.lse_out[row[h]] = sum[h] == 0.f ? -INFINITY : (ref[h] + log2f(sum[h])) * kLn2;
+        }
+        const float inv[2] = {sum[0] == 0.f ? 0.f : 1.f / sum[0], sum[1] == 0.f ? 0.f : 1.f / sum[1]};
+        if (__any_sync(kFull, row[0] >= 0 || row[1] >= 0)) {
+            #pragma unroll 1
+            for (int c = 0; c < 512; c += 64) {
+                uint32_t v[32];
+                tmem_ld_16x64(mine + kHalf + c, v);
+                tmem_wait_ld(v);
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (row[h] < 0) continue;
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int d = c + 8 * k + 2 * quad;
+                        const float2 y = make_float2(__uint_as_float(v[4 * k + 2 * h]), __uint_as_float(v[4 * k + 2 * h + 1]));
+                        if (!whole)
+                            *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(slot) * kRows + r0 + 8 * h) * kLatDim + d) = y;
+                        else if (p.out_f32)
+                            *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row[h] * kLatDim + d) = make_float2(y.x * inv[h], y.y * inv[h]);
+                        else
+                            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row[h] * kLatDim + d) = pack_bf16(y.x * inv[h], y.y * inv[h]);
+                    }
+                }
+            }
+        }
+        tcgen_fence_before();
+        if (whole && bad) {
+            __syncwarp();
+            for (int r = warp * 16; r < warp * 16 + 16; ++r)
+                if (row_of(r) >= 0) plain_row<FP8>(p, g.b, row_of(r), g.len < 0 ? 0 : g.first + r / hd.each + 1);
+        }
+    }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAttnParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == kIssueWarp) tmem_alloc_all(&s.tmem);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.ready[i], FP8 ? kConvertWarps : 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        mbar_init(&s.s_full, 1);
+        mbar_init(&s.s_free, 4);
+        mbar_init(&s.p_full, 4);
+        mbar_init(&s.q_full, 4);
+        mbar_init(&s.drain, 1);
+        mbar_fence_init();
+        for (int i = 0; i < kBadRing; ++i) s.bad[i] = 0;
+        s.abort = 0;
+        s.remaining = 0;
+    }
+    pdl_wait();
+    pdl_trigger();
+    const Heads hd(p, blockIdx.x % ((p.n_q + kRows - 1) / kRows));
+    if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
+    static_assert(2 * kMaxBatch * sizeof(int64_t) <= sizeof(s.k), "the schedule's scratch");
+    make_schedule(p, s, reinterpret_cast<int64_t*>(s.k[0]), hd, threads_of(FP8));
+    if (tid == 0 && (smem_u32(smem_raw) & 1023u)) {   // the operands' swizzle wants it (nothing else stands before them)
+        report(p.err, KVD_ERR_CUDA);
+        s.remaining = 0;
+    }
+    fence_proxy_async_shared();   // the scratch is overwritten by bulk copies
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    if (warp < 4) softmax<FP8>(s, p, hd, warp, lane);
+    else if (warp == kProducerWarp) producer<FP8>(s, p, hd, lane);
+    else if (warp == kIssueWarp) issuer<FP8>(s, p, hd);
+    else if (!FP8 && warp == kFixWarp) fixer(s, p, hd, lane);
+    else if (FP8 && warp >= kConvertWarp) converter(s, p, hd, warp - kConvertWarp, lane);
+    __syncwarp();
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    if (warp == kIssueWarp) {
+        if (lane == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
+        tmem_free_all(s.tmem);
+    }
+}
+
+// Joins the parts of units that the schedule cut: a CTA a row at a time.
+constexpr int kJoinThreads = 128;
+template <bool FP8>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnParams p, int ctas) {
+    extern __shared__ int4 seg[];   // 2·ctas, then the starts
+    int* start = reinterpret_cast<int*>(seg + 2 * ctas);
+    __shared__ int count;
+    __shared__ float top_s[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_trigger();
+    if (tid == 0) count = 0;
+    for (int i = tid; i < 2 * ctas; i += kJoinThreads) seg[i] = p.part_seg[i];
+    __syncthreads();
+    if (warp == 0) {
+        int c = 0;
+        for (int i0 = 0; i0 < 2 * ctas; i0 += 32) {
+            const bool on = i0 + lane < 2 * ctas && seg[i0 + lane].x >= 0 && (seg[i0 + lane].z & 1);
+            const unsigned at = __ballot_sync(kFull, on);
+            if (on) start[c + __popc(at & ((1u << lane) - 1))] = i0 + lane;
+            c += __popc(at);
+        }
+        if (lane == 0) count = c;
+    }
+    __syncthreads();
+    const int blocks = (p.n_q + kRows - 1) / kRows;
+    for (int item = blockIdx.x; item < count * kRows; item += gridDim.x) {
+        const int slot0 = start[item / kRows], r = item % kRows;
+        const int4 g = seg[slot0];
+        const Heads hd(p, (slot0 >> 1) % blocks);
+        const Request q = load_request(p, g.x, false);
+        const int tok = r / hd.each, h = r - tok * hd.each, i = g.y * hd.tpb + tok;
+        if (tok >= hd.tpb || i >= q.T || h >= hd.n) continue;
+        const int64_t row = (static_cast<int64_t>(q.s0) + i) * p.n_q + hd.first + h;
+        auto slot_of = [&](int k) { return k == 0 ? slot0 : (((slot0 >> 1) + k * blocks) << 1); };   // a later part is its CTA's first
+        float m = -INFINITY;
+        bool bad = false;
+        for (int k = 0; k < g.w; ++k) bad |= (seg[slot_of(k)].z & 2) != 0;
+        if (bad) {
+            if (warp == 0) plain_row<FP8>(p, g.x, row, q.len < 0 ? 0 : q.len - q.T + i + 1);
+            continue;
+        }
+        for (int k = tid; k < g.w; k += kJoinThreads) m = fmaxf(m, p.part_ml[static_cast<int64_t>(slot_of(k)) * 2 * kRows + r]);
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        __syncthreads();
+        if (lane == 0) top_s[warp] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
+        const float z = m == -INFINITY ? 0.f : m;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        #pragma unroll 8
+        for (int k = 0; k < g.w; ++k) {
+            const int64_t sl = slot_of(k);
+            const float w = ex2(p.part_ml[sl * 2 * kRows + r] - z);
+            const float4 o = *reinterpret_cast<const float4*>(p.part + (sl * kRows + r) * kLatDim + 4 * tid);
+            sum = fmaf(w, p.part_ml[(sl * 2 + 1) * kRows + r], sum);
+            acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int64_t at = row * kLatDim + (i >> 3) * 256 + lane * 8 + (i & 7);
-            if (p.out_f32) static_cast<float*>(p.out)[at] = acc[i] * inv;
-            else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
-        }
-        if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        if (p.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatDim + 4 * tid) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kLatDim + 4 * tid) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (tid == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
+}
+
+template <bool FP8>
+cudaError_t launch(const LatentAttnParams& p, int ctas, cudaStream_t stream) {
+    static_assert(sizeof(Smem) <= 232448, "shared memory of one SM");
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(attn_kernel<FP8>, dim3(static_cast<unsigned>(ctas)), dim3(threads_of(FP8)), sizeof(Smem), -1, stream, p);
+    if (e != cudaSuccess) return e;
+    const size_t smem = static_cast<size_t>(2 * ctas) * (sizeof(int4) + sizeof(int));
+    return launch_dependent(join_kernel<FP8>, dim3(static_cast<unsigned>(8 * ctas)), dim3(kJoinThreads), smem, -1, stream, p, ctas);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, int num_sms, cudaStream_t stream) {
-    const int64_t most = (static_cast<int64_t>(p.n_tokens) * p.n_q + kThreads / 32 - 1) / (kThreads / 32);
-    const int64_t share = (16 * num_sms + p.B - 1) / p.B;
-    const dim3 grid(static_cast<unsigned>(most < share ? most : share), static_cast<unsigned>(p.B));
-    return launch_dependent(fp8 ? attn_kernel<true> : attn_kernel<false>, grid, dim3(kThreads), 0, -1, stream, p);
+    return fp8 ? launch<true>(p, num_sms, stream) : launch<false>(p, num_sms, stream);
 }
 
 }  // namespace kvd
