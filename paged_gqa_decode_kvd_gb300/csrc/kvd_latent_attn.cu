@@ -230,7 +230,7 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
     #pragma unroll 1
     for (int i = 0; i < kTries; ++i) {
         if (__all_sync(kFull, mbar_try_wait(bar, phase & 1u))) return true;
-        if (s.abort) return false;
+        if (__any_sync(kFull, s.abort)) return false;
     }
     s.abort = 1;   // reported at the kernel's end
     return false;

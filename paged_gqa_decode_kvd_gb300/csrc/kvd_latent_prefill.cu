@@ -3,15 +3,68 @@
 //
 // Row (token i of the T rows of request b, head h) over its N keys, causal: t ≤ N − T + i:
 //   l_t = scale·(<q[:128], k_t,h> + <q[128:], r_t>),  out = Σ_t softmax(l)_t·v_t,h,  lse = log Σ exp(l_t).
-// A warp a row: a lane has four dims of k and v and two rotated ones.
-#include "kvd_common.cuh"
+#include <cuda.h>
+
 #include "kvd_latent.h"
+#include "kvd_tcgen.cuh"
 
 namespace kvd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kTile = 128;             // keys per tile
+constexpr int kRows = 128;             // rows of a softmax warpgroup: one MMA
+constexpr int kPieces = 8, kPieceBytes = 16384, kTilePieces = 5;   // K: three times 64 dims of 128 keys; V: twice 64 keys
+constexpr int kChunk = kRows * 128;    // 64 dims of Q's rows
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kIssueWarp = 9, kFixWarp = 10;
+constexpr int kReaders = 10;           // warps that read a unit's description
+constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
+constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so
+constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
+constexpr uint32_t kColS = 0, kColO = 256;    // tensor memory columns: S (and P over it) 2 × 128, O 2 × 128
 
+struct Unit {
+    int b, h, s0, T, k0, N;
+    int tok0;                          // first token
+    int tiles[2];                      // of the warpgroups' rows (−1: no rows)
+    int end;                           // keys that the last row attends
+};
+
+struct Smem {
+    uint8_t q[2][3 * kChunk];
+    uint8_t piece[kPieces][kPieceBytes];
+    Unit unit[2];
+    uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], fixed, u_full[2], u_empty[2], drain;
+    uint32_t tmem;
+    volatile int abort;
+};
+
+struct Maps {
+    CUtensorMap q, k, v, r;
+};
+
+__device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        if (__all_sync(kFull, mbar_try_wait(bar, phase & 1u))) return true;
+        if (__any_sync(kFull, s.abort)) return false;
+    }
+    s.abort = 1;   // reported at the kernel's end
+    return false;
+}
+
+__device__ __forceinline__ void tma3(uint8_t* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tma2(uint8_t* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// ------------------------------------------------------------- one row, plainly
 __device__ __forceinline__ void unpack4(float* x, const uint16_t* p) {
     const uint2 v = *reinterpret_cast<const uint2*>(p);
     const float2 a = unpack_bf16(v.x), c = unpack_bf16(v.y);
@@ -20,63 +73,540 @@ __device__ __forceinline__ void unpack4(float* x, const uint16_t* p) {
     x[2] = c.x;
     x[3] = c.y;
 }
+// A warp a row: a lane has four dims of k and v and two rotated ones.
+__device__ __noinline__ void plain_row(const LatentPrefillParams& p, int64_t token, int h, int64_t k0, int end) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = token * p.n_q + h;
+    float q[6], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, sum = 0.f;
+    unpack4(q, p.q + row * kExpKey + lane * 4);
+    const float2 qr = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.q + row * kExpKey + kNope + lane * 2));
+    q[4] = qr.x;
+    q[5] = qr.y;
+    for (int64_t n = k0; n < k0 + end; ++n) {
+        float k[4], v[4];
+        unpack4(k, p.k_nope + n * p.k_stride + h * p.k_head + lane * 4);
+        unpack4(v, p.v + n * p.v_stride + h * p.v_head + lane * 4);
+        const float2 rot = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.k_rope + n * p.rope_stride + lane * 2));
+        float dot = fmaf(q[4], rot.x, q[5] * rot.y);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) dot = fmaf(q[j], k[j], dot);
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        const float l = dot * p.scale_log2, top = fmaxf(m, l);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - ref), w = exp2f(l - ref);
+        m = top;
+        sum = sum * f + w;
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, v[j], acc[j] * f);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    #pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t at = row * kExpVal + lane * 4 + j;
+        if (p.out_f32) static_cast<float*>(p.out)[at] = acc[j] * inv;
+        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[j] * inv);
+    }
+    if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
 
-__global__ void __launch_bounds__(kThreads) prefill_kernel(const LatentPrefillParams p) {
+// ------------------------------------------------------------------ producer
+// Units in order: requests, within one its tokens from the last 256 on, within these the heads.  CTA c of C takes the units
+// c, 2C − 1 − c, 2C + c, 4C − 1 − c, ..: neighbours cost about the same, and who has the dearer one of a turn has the cheaper
+// of the next.
+struct Units {
+    int64_t before;   // units of requests before lane 0's
+    int b0;
+    int64_t up;       // units up to this lane's request, itself included
+    int s0, T, k0, N;
+    __device__ __forceinline__ void load(const LatentPrefillParams& p, int lane, bool tell) {
+        const int b = b0 + lane;
+        int64_t c = 0;
+        s0 = T = k0 = N = 0;
+        if (b < p.B) {
+            s0 = p.q_start[b];
+            const int s1 = p.q_start[b + 1], k1 = p.kv_start[b + 1];
+            k0 = p.kv_start[b];
+            if (s0 < 0 || s1 < s0 || s1 > p.n_tokens || k0 < 0 || k1 < k0 || k1 > p.n_keys) {
+                if (tell) report(p.err, KVD_ERR_OOB);
+            } else {
+                T = s1 - s0;
+                N = k1 - k0;
+                c = static_cast<int64_t>((T + 2 * kRows - 1) / (2 * kRows)) * p.n_q;
+            }
+        }
+        up = c;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(kFull, up, o);
+            if (lane >= o) up += v;
+        }
+        up += before;
+    }
+    // Unit u (not before the last one asked for); false behind the last.
+    __device__ __forceinline__ bool find(const LatentPrefillParams& p, int64_t u, int lane, bool tell, Unit& x) {
+        while (true) {
+            const unsigned at = __ballot_sync(kFull, u < up);
+            if (at) {
+                const int src = __ffs(at) - 1;
+                const int64_t prev = __shfl_sync(kFull, up, src > 0 ? src - 1 : 0), first = src > 0 ? prev : before;
+                x.b = b0 + src;
+                x.s0 = __shfl_sync(kFull, s0, src);
+                x.T = __shfl_sync(kFull, T, src);
+                x.k0 = __shfl_sync(kFull, k0, src);
+                x.N = __shfl_sync(kFull, N, src);
+                const int64_t in = u - first;
+                x.h = static_cast<int>(in % p.n_q);
+                x.tok0 = ((x.T + 2 * kRows - 1) / (2 * kRows) - 1 - static_cast<int>(in / p.n_q)) * 2 * kRows;
+                x.end = 0;
+                #pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int last = min(x.tok0 + (w + 1) * kRows, x.T);   // behind the warpgroup's last token
+                    const int end = p.causal ? max(0, x.N - x.T + last) : x.N;
+                    x.tiles[w] = last > x.tok0 + w * kRows ? (end + kTile - 1) / kTile : -1;
+                    if (x.tiles[w] >= 0) x.end = end;
+                }
+                return true;
+            }
+            before = __shfl_sync(kFull, up, 31);
+            b0 += 32;
+            if (b0 >= p.B) return false;
+            load(p, lane, tell);
+        }
+    }
+};
+
+__device__ __forceinline__ void producer(Smem& s, const LatentPrefillParams& p, const Maps& m, int lane) {
+    Units units;
+    units.before = 0;
+    units.b0 = 0;
+    const bool tell = blockIdx.x == 0;
+    units.load(p, lane, tell);
+    uint32_t n = 0, pieces = 0, done[2] = {0, 0};   // tiles before; pieces asked for; units with rows of each warpgroup
+    bool ok = true;
+    #pragma unroll 1
+    for (uint32_t i = 0;; ++i) {
+        const int64_t turn = static_cast<int64_t>(i) * gridDim.x;
+        Unit x;
+        const bool more = units.find(p, turn + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, tell, x);
+        // (a turn that is cut off may lack this CTA's unit: so does every later one)
+        const uint32_t at = i & 1;
+        ok = i < 2 || wait_bar(s, &s.u_empty[at], i / 2 - 1);
+        if (!ok) break;
+        if (lane == 0) {
+            if (!more) x.b = -1;
+            s.unit[at] = x;
+            mbar_arrive(&s.u_full[at]);
+        }
+        __syncwarp();
+        if (!more) break;
+        const int tiles = max(x.tiles[0], x.tiles[1]);
+        #pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if (x.tiles[w] <= 0 || !ok) continue;
+            if (done[w]) ok = wait_bar(s, &s.q_empty[w], done[w] - 1);
+            if (!ok) continue;
+            ++done[w];
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&s.q_full[w], 3 * kChunk);
+                for (int c = 0; c < 3; ++c) tma3(s.q[w] + c * kChunk, &m.q, c * 64, x.h, x.s0 + x.tok0 + w * kRows, &s.q_full[w]);
+            }
+            __syncwarp();
+        }
+        #pragma unroll 1
+        for (int t = 0; ok && t < tiles; ++t, ++n) {
+            const int key = x.k0 + t * kTile;
+            #pragma unroll 1
+            for (int k = 0; k < kTilePieces; ++k) {
+                const uint32_t piece = n * kTilePieces + k, at = piece % kPieces;
+                if (piece >= kPieces) ok = wait_bar(s, &s.empty[at], piece / kPieces - 1);
+                if (!ok) break;
+                pieces = piece + 1;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s.full[at], kPieceBytes);
+                    if (k < 2) {
+                        tma3(s.piece[at], &m.k, k * 64, x.h, key, &s.full[at]);
+                    } else if (k == 2) {
+                        tma2(s.piece[at], &m.r, 0, key, &s.full[at]);
+                    } else {
+                        tma3(s.piece[at], &m.v, 0, x.h, key + (k - 3) * 64, &s.full[at]);
+                        tma3(s.piece[at] + kPieceBytes / 2, &m.v, 64, x.h, key + (k - 3) * 64, &s.full[at]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) break;
+    }
+    if (s.abort) {   // copies under way must land in memory that is still this block's
+        for (uint32_t k = pieces > kPieces ? pieces - kPieces : 0; k < pieces; ++k) mbar_wait(&s.full[k % kPieces], (k / kPieces) & 1u, nullptr, kWaitNs);
+        for (int w = 0; w < 2; ++w)
+            if (done[w]) mbar_wait(&s.q_full[w], (done[w] - 1) & 1u, nullptr, kWaitNs);
+    }
+}
+
+// The unit's description, by every role in turn; false behind the last.
+__device__ __forceinline__ bool next_unit(Smem& s, uint32_t i, Unit& x, int lane) {
+    if (!wait_bar(s, &s.u_full[i & 1], i / 2)) return false;
+    x = s.unit[i & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.u_empty[i & 1]);
+    return x.b >= 0;
+}
+
+// ----------------------------------------------------------------------- fix
+// V behind the last key that a row of the unit attends is zeroed: its weight is 0, and 0·NaN would be NaN.
+__device__ __forceinline__ void fixer(Smem& s, int lane) {
+    Unit x;
+    uint32_t n = 0;
+    for (uint32_t i = 0; next_unit(s, i, x, lane); ++i) {
+        const int tiles = max(x.tiles[0], x.tiles[1]);
+        if (tiles <= 0) continue;
+        n += tiles;
+        #pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t piece = (n - 1) * kTilePieces + 3 + half, at = piece % kPieces;
+            if (!wait_bar(s, &s.full[at], piece / kPieces)) return;
+            const int from = max(x.end - (tiles - 1) * kTile - half * 64, 0);
+            for (int r = from + (lane >> 4); r < 64; r += 2)
+                *reinterpret_cast<uint4*>(s.piece[at] + (lane >> 3 & 1) * (kPieceBytes / 2) + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.fixed);
+    }
+}
+
+// --------------------------------------------------------------------- issue
+// V as it is in memory: 64 dims a row of 128 bytes, groups of eight keys 1,024 bytes apart, the other 64 dims behind them.
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
+    return static_cast<uint64_t>(addr >> 4) | (static_cast<uint64_t>(kPieceBytes / 2 >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void issuer(Smem& s, int lane) {
+    constexpr uint32_t kDescS = mma_desc_bf16(kRows, kTile), kDescO = mma_desc_bf16(kRows, kExpVal) | (1u << 16);
+    const uint32_t tmem = uniform(s.tmem), q_op = uniform(smem_u32(s.q)), p_op = uniform(smem_u32(s.piece));
+    Unit x;
+    uint32_t n = 0, unit[2] = {0, 0}, step[2] = {0, 0}, fixes = 0;
+    bool ok = true;
+    auto scores = [&](uint32_t w, uint32_t t) {   // S of warpgroup w, the CTA's tile t
+        #pragma unroll 1
+        for (uint32_t c = 0; ok && c < 3; ++c) {
+            const uint32_t piece = t * kTilePieces + c, at = piece % kPieces;
+            const uint32_t a = uniform(q_op + (w * 3 + c) * kChunk), b = uniform(p_op + at * kPieceBytes), d = uniform(tmem + kColS + w * kTile);
+            ok = wait_bar(s, &s.full[at], piece / kPieces);
+            if (!ok) return;
+            tcgen_fence_after();
+            if (elect_one()) {
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss(d, smem_desc_sw128(a + k * 32), smem_desc_sw128(b + k * 32), kDescS, c > 0 || k > 0);
+            }
+            __syncwarp();
+        }
+    };
+    auto release = [&](uint32_t t, int k0, int k1) {   // pieces of a tile, once all that was issued so far is done
+        if (elect_one())
+            for (int k = k0; k < k1; ++k) mma_commit(smem_u32(&s.empty[(t * kTilePieces + k) % kPieces]));
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(smem_u32(bar));
+        __syncwarp();
+    };
+    for (uint32_t i = 0; ok && next_unit(s, i, x, lane); ++i) {
+        const int tiles = max(x.tiles[0], x.tiles[1]);
+        if (tiles <= 0) continue;
+        #pragma unroll 1
+        for (int t = -1; ok && t < tiles; ++t) {
+            // O(t) of a warpgroup, then its S(t + 1): the other one's softmax runs meanwhile
+            #pragma unroll 1
+            for (int w = 0; ok && w < 2; ++w) {
+                if (t >= 0 && t < x.tiles[w]) {
+                    if (t == tiles - 1 && !(w == 1 && x.tiles[0] == tiles)) ok = wait_bar(s, &s.fixed, fixes++);
+                    ok = ok && wait_bar(s, &s.p_full[w], step[w]++);
+                    const uint32_t d = uniform(tmem + kColO + w * kExpVal), a = uniform(tmem + kColS + w * kTile);
+                    #pragma unroll 1
+                    for (uint32_t half = 0; ok && half < 2; ++half) {
+                        const uint32_t piece = (n + t) * kTilePieces + 3 + half, at = piece % kPieces;
+                        const uint32_t b = uniform(p_op + at * kPieceBytes);
+                        ok = wait_bar(s, &s.full[at], piece / kPieces);
+                        if (!ok) break;
+                        tcgen_fence_after();
+                        if (elect_one()) {
+                            #pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_ts(d, a + (half * 4 + k) * 8, desc_v(b + k * 2048), kDescO, t > 0 || half > 0 || k > 0);
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && t == x.tiles[w] - 1) commit(&s.o_full[w]);
+                }
+                if (ok && t >= 0 && w == 1) release(n + t, 3, 5);
+                if (ok && t + 1 < x.tiles[w]) {
+                    if (t < 0) ok = wait_bar(s, &s.q_full[w], unit[w]++);
+                    if (ok) scores(w, n + t + 1);
+                    if (ok) commit(&s.s_full[w]);
+                    if (ok && t + 2 == x.tiles[w]) commit(&s.q_empty[w]);
+                }
+                if (ok && t + 1 < tiles && w == 1) release(n + t + 1, 0, 3);
+            }
+        }
+        n += tiles;
+    }
+    // the last commits arrive in this block's shared memory, and nothing is under way in tensor memory
+    commit(&s.drain);
+    mbar_wait(&s.drain, 0, nullptr, kWaitNs);
+    if (!s.abort) {
+        const uint32_t pieces = n * kTilePieces;
+        for (uint32_t k = pieces > kPieces ? pieces - kPieces : 0; k < pieces; ++k)
+            if (!wait_bar(s, &s.empty[k % kPieces], k / kPieces)) break;
+        for (int w = 0; w < 2; ++w)
+            if (unit[w]) wait_bar(s, &s.q_empty[w], unit[w] - 1);
+    }
+}
+
+// ------------------------------------------------------------------- softmax
+__device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, int w, int tid, int lane) {
+    const uint32_t mine = s.tmem + (static_cast<uint32_t>(tid & ~31) << 16);
+    const uint32_t col_s = mine + kColS + w * kTile, col_o = mine + kColO + w * kExpVal;
+    const bool negative = p.scale_log2 < 0.f;
+    const float scale = p.scale_log2 == 0.f ? 1e-38f : fabsf(p.scale_log2);   // (0·−inf of a masked key would be NaN)
+    Unit x;
+    uint32_t n = 0, units = 0;
+    for (uint32_t i = 0; next_unit(s, i, x, lane); ++i) {
+        if (x.tiles[w] < 0) continue;
+        const int r = x.tok0 + w * kRows + tid;               // token of the request
+        const int last = p.causal ? x.N - x.T + r : x.N - 1;   // the last key it attends
+        const int first = p.causal ? x.N - x.T + x.tok0 + w * kRows : x.N - 1;   // of the warpgroup's first row
+        float ref = -INFINITY;
+        float2 sum = make_float2(0.f, 0.f);
+        #pragma unroll 1
+        for (int t = 0; t < x.tiles[w]; ++t, ++n) {
+            if (!wait_bar(s, &s.s_full[w], n)) return;   // (the product with V before it is done as well)
+            tcgen_fence_after();
+            uint32_t v[4][32];
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(col_s + c * 32, v[c]);
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_ld(v[c]);
+            if (negative) {
+                #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e) v[c][e] ^= 0x80000000u;
+            }
+            const int base = t * kTile;
+            if (base + kTile - 1 > min(first, x.N - 1)) {
+                const int keep = min(last, x.N - 1) - base;   // columns up to this one
+                #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e > keep) v[c][e] = 0xff800000u;
+            }
+            float top[4];
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                top[c] = max3(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]), __uint_as_float(v[c][2]));
+                #pragma unroll
+                for (int e = 3; e < 31; e += 2) top[c] = max3(top[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                top[c] = fmaxf(top[c], __uint_as_float(v[c][31]));
+            }
+            const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            const bool moved = most > ref + kLazy;
+            if (__any_sync(kFull, moved)) {
+                const float f = moved ? ex2(ref - most) : 1.f;
+                if (moved) ref = most;
+                sum = mul2(sum, make_float2(f, f));
+                if (t > 0) {
+                    #pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(col_o + c * 32, o);
+                        tmem_wait_ld(o);
+                        #pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(col_o + c * 32, o);
+                    }
+                }
+            }
+            const float z = ref == -INFINITY ? 0.f : -ref;
+            #pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t pk[32];
+                #pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float2 a = make_float2(__uint_as_float(v[c + (e >> 4)][2 * (e & 15)]), __uint_as_float(v[c + (e >> 4)][2 * (e & 15) + 1]));
+                    a = fma2(a, make_float2(scale, scale), make_float2(z, z));
+                    a.x = ex2(a.x);
+                    a.y = ex2(a.y);
+                    sum = add2(sum, a);
+                    pk[e] = pack_bf16(a.x, a.y);
+                }
+                tmem_st32(col_s + c * 16, pk);
+            }
+            tmem_wait_st();
+            tcgen_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.p_full[w]);
+        }
+        const float total = sum.x + sum.y, inv = total == 0.f ? 0.f : 1.f / total;
+        const bool real = r < x.T;
+        const int64_t row = (static_cast<int64_t>(x.s0) + r) * p.n_q + x.h;
+        const bool any = x.tiles[w] > 0;
+        if (any) {
+            if (!wait_bar(s, &s.o_full[w], units++)) return;
+            tcgen_fence_after();
+        }
+        float odd = 0.f;
+        #pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            if (any) {
+                tmem_ld32(col_o + c * 32, o);
+                tmem_wait_ld(o);
+            } else {
+                #pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0;
+            }
+            float y[32];
+            #pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                y[e] = __uint_as_float(o[e]) * inv;
+                odd += y[e];
+            }
+            if (!real) continue;
+            if (p.out_f32) {
+                float* out = static_cast<float*>(p.out) + row * kExpVal + c * 32;
+                #pragma unroll
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(out + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            } else {
+                uint16_t* out = static_cast<uint16_t*>(p.out) + row * kExpVal + c * 32;
+                #pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4*>(out + e) = make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]), pack_bf16(y[e + 4], y[e + 5]), pack_bf16(y[e + 6], y[e + 7]));
+            }
+        }
+        if (real && p.lse_out) p.lse_out[row] = total == 0.f ? -INFINITY : (ref + log2f(total)) * kLn2;
+        tcgen_fence_before();
+        // A key that some rows of a tile attend and others do not may hold what is not finite: 0·NaN.  Such a row
+        // (or one that is NaN by right) is computed again, without the keys that it does not attend.
+        unsigned todo = __ballot_sync(kFull, p.causal && real && odd != odd);
+        for (; todo; todo &= todo - 1) {
+            const int rr = (r & ~31) + __ffs(todo) - 1;
+            __syncwarp();
+            plain_row(p, static_cast<int64_t>(x.s0) + rr, x.h, x.k0, max(0, x.N - x.T + rr + 1));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefillParams p, const __grid_constant__ Maps m) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == kIssueWarp) tmem_alloc_all(&s.tmem);
+    if (tid == 0) {
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.u_full[i], 1);
+            mbar_init(&s.u_empty[i], kReaders);
+        }
+        mbar_init(&s.fixed, 1);
+        mbar_init(&s.drain, 1);
+        mbar_fence_init();
+        s.abort = 0;
+    }
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int s0 = p.q_start[b], s1 = p.q_start[b + 1], k0 = p.kv_start[b], k1 = p.kv_start[b + 1];
-    if (s0 < 0 || s1 < s0 || s1 > p.n_tokens || k0 < 0 || k1 < k0 || k1 > p.n_keys) {
-        if (threadIdx.x == 0) report(p.err, KVD_ERR_OOB);
-        return;
-    }
-    const int T = s1 - s0, N = k1 - k0;
-    const int64_t rows = static_cast<int64_t>(T) * p.n_q, warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
-        const int64_t row = static_cast<int64_t>(s0) * p.n_q + r;
-        const int h = static_cast<int>(r % p.n_q), i = static_cast<int>(r / p.n_q);
-        float q[6], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, sum = 0.f;
-        unpack4(q, p.q + row * kExpKey + lane * 4);
-        const float2 qr = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.q + row * kExpKey + kNope + lane * 2));
-        q[4] = qr.x;
-        q[5] = qr.y;
-        const int end = p.causal ? max(0, N - T + i + 1) : N;
-        for (int64_t n = k0; n < k0 + end; ++n) {
-            float k[4], v[4];
-            unpack4(k, p.k_nope + n * p.k_stride + h * p.k_head + lane * 4);
-            unpack4(v, p.v + n * p.v_stride + h * p.v_head + lane * 4);
-            const float2 rot = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.k_rope + n * p.rope_stride + lane * 2));
-            float dot = fmaf(q[4], rot.x, q[5] * rot.y);
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) dot = fmaf(q[j], k[j], dot);
-            #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-            const float l = dot * p.scale_log2, top = fmaxf(m, l);
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float f = exp2f(m - ref), w = exp2f(l - ref);
-            m = top;
-            sum = sum * f + w;
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, v[j], acc[j] * f);
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    // the operands' swizzle wants 1,024-byte addresses (nothing else stands before them)
+    const bool aligned = (smem_u32(smem_raw) & 1023u) == 0;
+    if (!aligned && tid == 0) report(p.err, KVD_ERR_CUDA);
+    // a thread has 168 registers at launch: 2·208 + 80 = 496 ≤ 3·168
+    if (aligned) {
+        if (warp < 8) {
+            take_registers<208>();
+            softmax(s, p, warp >> 2, tid & 127, lane);
+        } else {
+            give_registers<80>();
+            if (warp == kProducerWarp) producer(s, p, m, lane);
+            else if (warp == kIssueWarp) issuer(s, lane);
+            else if (warp == kFixWarp) fixer(s, lane);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t at = row * kExpVal + lane * 4 + j;
-            if (p.out_f32) static_cast<float*>(p.out)[at] = acc[j] * inv;
-            else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[j] * inv);
-        }
-        if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
     }
+    __syncwarp();
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+    if (warp == kIssueWarp) {
+        if (lane == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
+        tmem_free_all(s.tmem);
+    }
+}
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+    static const Encode fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<Encode>(f);
+    }();
+    return fn;
+}
+
+// [rows][heads][dims] bf16 (heads 0: [rows][dims]), copied 64 dims of one head and `box` rows at a time; rows behind the
+// last are read as zeros.
+bool make_map(CUtensorMap* map, const void* base, int dims, int heads, int64_t rows, int64_t head_stride, int64_t stride, int box) {
+    cuuint64_t size[3] = {static_cast<cuuint64_t>(dims)}, pitch[2];
+    cuuint32_t tile[3] = {64}, step[3] = {1, 1, 1};
+    int rank = 1;
+    if (heads > 0) {
+        pitch[rank - 1] = static_cast<cuuint64_t>(2 * head_stride);
+        size[rank] = static_cast<cuuint64_t>(heads);
+        tile[rank++] = 1;
+    }
+    pitch[rank - 1] = static_cast<cuuint64_t>(2 * stride);
+    size[rank] = static_cast<cuuint64_t>(rows);
+    tile[rank++] = static_cast<cuuint32_t>(box);
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), size, pitch, tile, step,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, int num_sms, cudaStream_t stream) {
-    const int64_t most = (static_cast<int64_t>(p.n_tokens) * p.n_q + kThreads / 32 - 1) / (kThreads / 32);
-    const int64_t share = (16 * num_sms + p.B - 1) / p.B;
-    const dim3 grid(static_cast<unsigned>(most < share ? most : share), static_cast<unsigned>(p.B));
-    return launch_dependent(prefill_kernel, grid, dim3(kThreads), 0, -1, stream, p);
+    static_assert(sizeof(Smem) <= 232448, "shared memory of one SM");
+    Maps m;
+    if (!encoder()) return cudaErrorNotSupported;
+    // without keys no unit has a tile, and no map but a valid one is needed
+    const bool keys = p.n_keys > 0;
+    const void* any = p.q;
+    if (!make_map(&m.q, p.q, kExpKey, p.n_q, p.n_tokens, kExpKey, static_cast<int64_t>(p.n_q) * kExpKey, kRows) ||
+        !make_map(&m.k, keys ? p.k_nope : any, kNope, p.n_q, keys ? p.n_keys : 1, keys ? p.k_head : kNope, keys ? p.k_stride : kNope * p.n_q, kTile) ||
+        !make_map(&m.v, keys ? p.v : any, kExpVal, p.n_q, keys ? p.n_keys : 1, keys ? p.v_head : kExpVal, keys ? p.v_stride : kExpVal * p.n_q, 64) ||
+        !make_map(&m.r, keys ? p.k_rope : any, kLatRope, 0, keys ? p.n_keys : 1, 0, keys ? p.rope_stride : kLatRope, kTile))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(prefill_kernel, dim3(static_cast<unsigned>(num_sms)), dim3(kThreads), sizeof(Smem), -1, stream, p, m);
 }
 
 }  // namespace kvd
