@@ -16,8 +16,8 @@ constexpr int kRows = 128;             // rows of a softmax warpgroup: one MMA
 constexpr int kPieces = 8, kPieceBytes = 16384, kTilePieces = 5;   // K: three times 64 dims of 128 keys; V: twice 64 keys
 constexpr int kChunk = kRows * 128;    // 64 dims of Q's rows
 constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8, kIssueWarp = 9, kFixWarp = 10;
-constexpr int kReaders = 10;           // warps that read a unit's description
+constexpr int kProducerWarp = 8, kIssueWarp = 9;
+constexpr int kReaders = 9;            // warps that read a unit's description
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
@@ -34,7 +34,7 @@ struct Smem {
     uint8_t q[2][3 * kChunk];
     uint8_t piece[kPieces][kPieceBytes];
     Unit unit[2];
-    uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], fixed, u_full[2], u_empty[2], drain;
+    uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2], drain;
     uint32_t tmem;
     volatile int abort;
 };
@@ -254,29 +254,6 @@ __device__ __forceinline__ bool next_unit(Smem& s, uint32_t i, Unit& x, int lane
     return x.b >= 0;
 }
 
-// ----------------------------------------------------------------------- fix
-// V behind the last key that a row of the unit attends is zeroed: its weight is 0, and 0·NaN would be NaN.
-__device__ __forceinline__ void fixer(Smem& s, int lane) {
-    Unit x;
-    uint32_t n = 0;
-    for (uint32_t i = 0; next_unit(s, i, x, lane); ++i) {
-        const int tiles = max(x.tiles[0], x.tiles[1]);
-        if (tiles <= 0) continue;
-        n += tiles;
-        #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            const uint32_t piece = (n - 1) * kTilePieces + 3 + half, at = piece % kPieces;
-            if (!wait_bar(s, &s.full[at], piece / kPieces)) return;
-            const int from = max(x.end - (tiles - 1) * kTile - half * 64, 0);
-            for (int r = from + (lane >> 4); r < 64; r += 2)
-                *reinterpret_cast<uint4*>(s.piece[at] + (lane >> 3 & 1) * (kPieceBytes / 2) + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.fixed);
-    }
-}
-
 // --------------------------------------------------------------------- issue
 // V as it is in memory: 64 dims a row of 128 bytes, groups of eight keys 1,024 bytes apart, the other 64 dims behind them.
 __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
@@ -287,7 +264,7 @@ __device__ __forceinline__ void issuer(Smem& s, int lane) {
     constexpr uint32_t kDescS = mma_desc_bf16(kRows, kTile), kDescO = mma_desc_bf16(kRows, kExpVal) | (1u << 16);
     const uint32_t tmem = uniform(s.tmem), q_op = uniform(smem_u32(s.q)), p_op = uniform(smem_u32(s.piece));
     Unit x;
-    uint32_t n = 0, unit[2] = {0, 0}, step[2] = {0, 0}, fixes = 0;
+    uint32_t n = 0, unit[2] = {0, 0}, step[2] = {0, 0};
     bool ok = true;
     auto scores = [&](uint32_t w, uint32_t t) {   // S of warpgroup w, the CTA's tile t
         #pragma unroll 1
@@ -323,8 +300,7 @@ __device__ __forceinline__ void issuer(Smem& s, int lane) {
             #pragma unroll 1
             for (int w = 0; ok && w < 2; ++w) {
                 if (t >= 0 && t < x.tiles[w]) {
-                    if (t == tiles - 1 && !(w == 1 && x.tiles[0] == tiles)) ok = wait_bar(s, &s.fixed, fixes++);
-                    ok = ok && wait_bar(s, &s.p_full[w], step[w]++);
+                    ok = wait_bar(s, &s.p_full[w], step[w]++);
                     const uint32_t d = uniform(tmem + kColO + w * kExpVal), a = uniform(tmem + kColS + w * kTile);
                     #pragma unroll 1
                     for (uint32_t half = 0; ok && half < 2; ++half) {
@@ -373,8 +349,11 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
     const bool negative = p.scale_log2 < 0.f;
     const float scale = p.scale_log2 == 0.f ? 1e-38f : fabsf(p.scale_log2);   // (0·−inf of a masked key would be NaN)
     Unit x;
-    uint32_t n = 0, units = 0;
+    uint32_t n = 0, all = 0, units = 0;   // tiles before, of this warpgroup and of the CTA
     for (uint32_t i = 0; next_unit(s, i, x, lane); ++i) {
+        const int tiles = max(x.tiles[0], x.tiles[1]);
+        const uint32_t before = all;
+        all += max(tiles, 0);
         if (x.tiles[w] < 0) continue;
         const int r = x.tok0 + w * kRows + tid;               // token of the request
         const int last = p.causal ? x.N - x.T + r : x.N - 1;   // the last key it attends
@@ -445,6 +424,17 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
                     pk[e] = pack_bf16(a.x, a.y);
                 }
                 tmem_st32(col_s + c * 16, pk);
+            }
+            if (t == tiles - 1 && x.end < base + kTile && !(w == 1 && x.tiles[0] == tiles)) {
+                // V behind the last key that a row of the unit attends: its weight is 0, and 0·NaN would be NaN
+                #pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t piece = (before + t) * kTilePieces + 3 + half, at = piece % kPieces;
+                    if (!wait_bar(s, &s.full[at], piece / kPieces)) return;
+                    for (int c = max(x.end - base - half * 64, 0) + (tid >> 4); c < 64; c += 8)
+                        *reinterpret_cast<uint4*>(s.piece[at] + (tid >> 3 & 1) * (kPieceBytes / 2) + c * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_shared();
             }
             tmem_wait_st();
             tcgen_fence_before();
@@ -520,7 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
             mbar_init(&s.u_full[i], 1);
             mbar_init(&s.u_empty[i], kReaders);
         }
-        mbar_init(&s.fixed, 1);
         mbar_init(&s.drain, 1);
         mbar_fence_init();
         s.abort = 0;
@@ -542,7 +531,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
             give_registers<80>();
             if (warp == kProducerWarp) producer(s, p, m, lane);
             else if (warp == kIssueWarp) issuer(s, lane);
-            else if (warp == kFixWarp) fixer(s, lane);
         }
     }
     __syncwarp();
