@@ -678,7 +678,7 @@ KVD_API kvd_status kvd_latent_workspace_bytes(const kvd_pool* pool, int n_q, int
  *  q_start, seq_lens, block_table, retain_mask, lse_out, workspace (kvd_latent_workspace_bytes) and what is done about bad
  *  lengths, bad block ids and rows with nothing to attend: as in kvd_chunk_attn
  * What a masked position's slot holds (not yet written, a NaN) does not reach the result.  A weight enters the product
- * with c rounded to bf16 (off by 2^-9 of itself), logits and sums are fp32.  The same call gives the same bits; where a
+ * with c rounded to bf16 (off by at most 2^-8 of itself), logits and sums are fp32.  The same call gives the same bits; where a
  * long row's sum is cut and joined depends on all requests of the call, so another batch may round it otherwise.
  * n_tokens = 0 or batch = 0 is a no-op. */
 KVD_API kvd_status kvd_latent_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start, int n_tokens,
@@ -702,7 +702,7 @@ KVD_API kvd_status kvd_latent_attn(kvd_pool* pool, int layer, const void* q, int
  *  out          [n_tokens][n_q][128] in out_dtype (KVD_BF16 or KVD_F32), 16-byte aligned, apart from what is read
  *  lse_out      f32 [n_tokens][n_q] natural-log log-sum-exp, or NULL
  * A row with nothing to attend gets out = 0 and lse = −inf.  What a key that a row does not attend holds does not reach
- * that row.  A weight enters the product with v rounded to bf16 (off by 2^-9 of itself), logits and sums are fp32.  The
+ * that row.  A weight enters the product with v rounded to bf16 (off by at most 2^-8 of itself), logits and sums are fp32.  The
  * same call gives the same bits.  n_tokens = 0 or batch = 0 is a no-op. */
 KVD_API kvd_status kvd_latent_prefill(kvd_pool* pool, const void* q, int n_q, const int32_t* q_start, int n_tokens,
                                       const void* k_nope, int64_t k_stride, int64_t k_head_stride, const void* v,

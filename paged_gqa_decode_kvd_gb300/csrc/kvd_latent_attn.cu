@@ -33,7 +33,6 @@ __device__ __forceinline__ void unpack8(float* x, uint4 v) {
         x[2 * i + 1] = a.y;
     }
 }
-__device__ __forceinline__ uint32_t nonfinite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 struct Info {
     alignas(16) float scale[kTile];    // 8-bit records: by column
@@ -41,7 +40,6 @@ struct Info {
     int base;                          // position of column 0
     int id[4];                         // physical blocks, −1: none
 };
-constexpr int kBadRing = 8;
 
 struct Smem {
     uint8_t k[kStages][kTileBytes];
@@ -49,7 +47,6 @@ struct Smem {
     Info info[kStages];
     uint64_t full[kStages], ready[kStages], empty[kStages], s_full, s_free, p_full, q_full, drain;
     uint32_t tmem;
-    int bad[kBadRing];                 // segment + 1: a row of it that others may not attend has non-finite values
     volatile int abort;
     // the CTA's share of the schedule
     int64_t at, remaining, share;
@@ -363,40 +360,21 @@ __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, con
 }
 
 // ----------------------------------------------------------------------- fix
-// Rows that nobody may attend are zeroed (their weight is 0, and 0·NaN would be NaN); a row that is attended by later
-// tokens of the unit only and is not finite is noted: the unit's rows are then computed one by one.
+// Rows that nobody may attend are zeroed: their weight is 0, and 0·NaN would be NaN.
 __device__ __forceinline__ void fixer(Smem& s, const LatentAttnParams& p, const Heads& hd, int lane) {
     Walk walk(p, s, hd.tpb);
     Segment g;
     uint32_t n = 0;
-    bool ok = true;
-    for (int seg = 0; ok && walk.next(p, g); ++seg) {
+    while (walk.next(p, g)) {
         #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t, ++n) {
             const uint32_t st = n % kStages;
-            ok = wait_bar(s, &s.full[st], n / kStages);
-            if (!ok) break;
-            unsigned long long zero = ~s.info[st].mask, look = 0;
-            if (g.multi && s.info[st].base + kTile > g.first + 1) {
-                const int from = max(g.first + 1 - s.info[st].base, 0);   // columns behind the first row's position
-                look = ~0ull << from & s.info[st].mask;
-            }
-            for (unsigned long long todo = zero | look; todo; todo &= todo - 1) {
+            if (!wait_bar(s, &s.full[st], n / kStages)) return;
+            for (unsigned long long todo = ~s.info[st].mask; todo; todo &= todo - 1) {
                 const int c = __ffsll(todo) - 1;
-                uint8_t* row = s.k[st] + (c >> 3) * kGroup + (c & 7) * 128;
-                const bool clear = zero >> c & 1;
-                uint32_t odd = 0;
-                #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint4* piece = reinterpret_cast<uint4*>(row + ((lane >> 3) + 4 * k) * 1024 + (lane & 7) * 16);
-                    if (clear) {
-                        *piece = make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint4 v = *piece;
-                        odd |= nonfinite(v.x) | nonfinite(v.y) | nonfinite(v.z) | nonfinite(v.w);
-                    }
-                }
-                if (odd) s.bad[seg % kBadRing] = seg + 1;
+                uint8_t* row = s.k[st] + (c >> 3) * kGroup + (c & 7) * 128 + (lane >> 3) * 1024 + (lane & 7) * 16;
+                *reinterpret_cast<uint4*>(row) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(row + 4096) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_shared();
             __syncwarp();
@@ -412,14 +390,12 @@ __device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, co
     Walk walk(p, s, hd.tpb);
     Segment g;
     uint32_t n = 0;
-    bool ok = true;
     const int r = lane >> 2, j = lane & 3, tok = (warp & 1) * 8 + r;   // token of its block, pieces 2j and 2j + 1
-    for (int seg = 0; ok && walk.next(p, g); ++seg) {
+    while (walk.next(p, g)) {
         #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t, ++n) {
             const uint32_t st = n % kStages;
-            ok = wait_bar(s, &s.full[st], n / kStages);
-            if (!ok) break;
+            if (!wait_bar(s, &s.full[st], n / kStages)) return;
             const Info& info = s.info[st];
             const int id = info.id[warp >> 1], c = warp * 8 + r;
             const bool on = info.mask >> c & 1;
@@ -432,7 +408,6 @@ __device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, co
             for (int i = 0; i < 2; ++i) rot[i] = on ? ld16(record + kLatCodes + (warp & 1) * 1024 + r * 128 + (2 * j + i) * 16) : make_uint4(0, 0, 0, 0);
             if (on) scale = *reinterpret_cast<const float*>(record + kLatScales + 4 * tok);
             uint8_t* group = s.k[st] + warp * kGroup + r * 128;
-            uint32_t odd = 0;
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
@@ -444,7 +419,6 @@ __device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, co
                     const float2 a = unpack_f16(lo), b = unpack_f16(hi);
                     o[2 * k] = pack_bf16(a.x, a.y);
                     o[2 * k + 1] = pack_bf16(b.x, b.y);
-                    odd |= nonfinite(o[2 * k]) | nonfinite(o[2 * k + 1]);
                 }
                 *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j) ^ r) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j + 1) ^ r) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -452,7 +426,6 @@ __device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, co
             #pragma unroll
             for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(group + 8192 + (2 * j + i) * 16) = rot[i];   // (in its order already)
             if (j == 0) s.info[st].scale[c] = scale;
-            if (on && g.multi && info.base + c > g.first && (odd || !isfinite(scale))) s.bad[seg % kBadRing] = seg + 1;
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.ready[st]);
@@ -565,7 +538,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
     Segment g;
     uint32_t n = 0;
     bool ok = true;
-    for (int seg = 0; ok && walk.next(p, g); ++seg) {
+    while (ok && walk.next(p, g)) {
         // row r is token r / each, head r % each of the unit
         auto row_of = [&](int r) -> int64_t {
             const int tok = r / hd.each, h = r - tok * hd.each;
@@ -703,7 +676,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
         if (ok) ok = wait_bar(s, &s.empty[(n - 1) % kStages], (n - 1) / kStages);
         if (!ok) break;
         tcgen_fence_after();
-        const bool whole = g.t0 == 0 && g.t1 == g.tiles, bad = s.bad[seg % kBadRing] == seg + 1;
+        const bool whole = g.t0 == 0 && g.t1 == g.tiles;
         const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
         const int64_t row[2] = {row_of(r0), row_of(r0 + 8)};
         #pragma unroll
@@ -712,7 +685,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
         }
         if (!whole) {
-            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.tb, (g.t0 == 0 ? 1 : 0) | (bad ? 2 : 0), g.parts);
+            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.tb, g.t0 == 0 ? 1 : 0, g.parts);
             #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (quad == 0) {
@@ -725,6 +698,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                 if (row[h] >= 0) p.lse_out[row[h]] = sum[h] == 0.f ? -INFINITY : (ref[h] + log2f(sum[h])) * kLn2;
         }
         const float inv[2] = {sum[0] == 0.f ? 0.f : 1.f / sum[0], sum[1] == 0.f ? 0.f : 1.f / sum[1]};
+        float odd[2] = {0.f, 0.f};
         if (__any_sync(kFull, row[0] >= 0 || row[1] >= 0)) {
             #pragma unroll 1
             for (int c = 0; c < 512; c += 64) {
@@ -738,6 +712,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                     for (int k = 0; k < 8; ++k) {
                         const int d = c + 8 * k + 2 * quad;
                         const float2 y = make_float2(__uint_as_float(v[4 * k + 2 * h]), __uint_as_float(v[4 * k + 2 * h + 1]));
+                        odd[h] += y.x + y.y;
                         if (!whole)
                             *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(slot) * kRows + r0 + 8 * h) * kLatDim + d) = y;
                         else if (p.out_f32)
@@ -749,10 +724,17 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             }
         }
         tcgen_fence_before();
-        if (whole && bad) {
-            __syncwarp();
-            for (int r = warp * 16; r < warp * 16 + 16; ++r)
-                if (row_of(r) >= 0) plain_row<FP8>(p, g.b, row_of(r), g.len < 0 ? 0 : g.first + r / hd.each + 1);
+        // A token that some rows of the unit attend and others do not may hold what is not finite: 0·NaN.  Such a row (or
+        // one that is NaN by right) is computed again, without the tokens that it does not attend.
+        if (whole && g.multi) {
+            #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                for (unsigned todo = __ballot_sync(kFull, row[h] >= 0 && odd[h] != odd[h]); todo;) {
+                    const int i = (__ffs(todo) - 1) >> 2, r = warp * 16 + 8 * h + i;
+                    todo &= ~(15u << 4 * i);
+                    __syncwarp();
+                    plain_row<FP8>(p, g.b, row_of(r), g.len < 0 ? 0 : g.first + r / hd.each + 1);
+                }
         }
     }
 }
@@ -775,7 +757,6 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
         mbar_init(&s.q_full, 4);
         mbar_init(&s.drain, 1);
         mbar_fence_init();
-        for (int i = 0; i < kBadRing; ++i) s.bad[i] = 0;
         s.abort = 0;
         s.remaining = 0;
     }
@@ -844,12 +825,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnPara
         const int64_t row = (static_cast<int64_t>(q.s0) + i) * p.n_q + hd.first + h;
         auto slot_of = [&](int k) { return k == 0 ? slot0 : (((slot0 >> 1) + k * blocks) << 1); };   // a later part is its CTA's first
         float m = -INFINITY;
-        bool bad = false;
-        for (int k = 0; k < g.w; ++k) bad |= (seg[slot_of(k)].z & 2) != 0;
-        if (bad) {
-            if (warp == 0) plain_row<FP8>(p, g.x, row, q.len < 0 ? 0 : q.len - q.T + i + 1);
-            continue;
-        }
         for (int k = tid; k < g.w; k += kJoinThreads) m = fmaxf(m, p.part_ml[static_cast<int64_t>(slot_of(k)) * 2 * kRows + r]);
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
@@ -867,6 +842,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnPara
             const float4 o = *reinterpret_cast<const float4*>(p.part + (sl * kRows + r) * kLatDim + 4 * tid);
             sum = fmaf(w, p.part_ml[(sl * 2 + 1) * kRows + r], sum);
             acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+        }
+        // as in a whole unit: a row that is NaN is computed again without the tokens that it does not attend
+        const float odd = acc.x + acc.y + acc.z + acc.w;
+        if (__syncthreads_or(odd != odd) && min(hd.tpb, q.T - g.y * hd.tpb) > 1) {
+            if (warp == 0) plain_row<FP8>(p, g.x, row, q.len < 0 ? 0 : q.len - q.T + i + 1);
+            continue;
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         if (p.out_f32)

@@ -14,6 +14,7 @@
 
 #include "../../include/kvd.h"
 #include "kvd_internal.h"
+#include "kvd_pool.h"
 
 namespace {
 
@@ -57,6 +58,7 @@ extern "C" kvd_status kvd_decode_attn_noalloc(kvd_pool* pool, int layer, const v
                                               int64_t logits_stride, const kvd_scores_desc* scores_epilogue,
                                               unsigned flags, void* stream) {
     if (!pool) return KVD_ERR_INVALID;
+    if (kvd::is_latent(pool)) return KVD_ERR_UNSUPPORTED;
     if (!out && batch > 0) return KVD_ERR_INVALID;  // the partials would be unreachable
     if (flags & KVD_PLANNED) return KVD_ERR_INVALID;  // no step plan can be in the shared array
     int dev = 0;
