@@ -41,11 +41,14 @@ struct Info {
     int id[4];                         // physical blocks, −1: none
 };
 
+// What is known of a tile.  8-bit records are loaded by the converters, several tiles behind the producer.
+constexpr int infos_of(bool fp8) { return fp8 ? 8 : kStages; }
+
 struct Smem {
     uint8_t k[kStages][kTileBytes];
     uint8_t p[kRows * kTile * 2];
-    Info info[kStages];
-    uint64_t full[kStages], ready[kStages], empty[kStages], s_full, s_free, p_full, q_full, drain;
+    Info info[infos_of(true)];
+    uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages], s_full, s_free, p_full, q_full, drain;
     uint32_t tmem;
     volatile int abort;
     // the CTA's share of the schedule
@@ -296,62 +299,81 @@ __device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t
 }
 
 // ------------------------------------------------------------------ producer
-// Follows the block table, eight tiles of ids at a time; bf16 records are copied as they are.
+// Follows the block table, eight tiles of ids at a time and the next eight under way; bf16 records are copied as they are,
+// 8-bit ones fetched to L2.
+struct Ids {
+    int id;            // of the lane's block, −1: none
+    uint32_t bits;     // its slots that may be attended
+};
+__device__ __forceinline__ Ids load_ids(const LatentAttnParams& p, const int32_t* table, int t, const Segment& g, int lane) {
+    Ids x{-1, 0};
+    const int pos = t * kTile + lane * kBs;
+    if (pos < g.end && t + (lane >> 2) < g.t1) x.id = table[pos / kBs];
+    return x;
+}
+__device__ __forceinline__ void check_ids(const LatentAttnParams& p, Ids& x, int t, const Segment& g, int lane) {
+    const int pos = t * kTile + lane * kBs;
+    if (!(pos < g.end && t + (lane >> 2) < g.t1)) return;
+    if (x.id < 0 || x.id >= p.num_blocks) {
+        report(p.err, KVD_ERR_OOB);
+        x.id = -1;
+    } else {
+        x.bits = p.retain ? p.retain[x.id] : 0xffffu;
+        if (g.end - pos < kBs) x.bits &= (1u << (g.end - pos)) - 1u;
+    }
+}
+
 template <bool FP8>
 __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, const Heads& hd, int lane) {
+    constexpr int kInfos = infos_of(FP8);
+    constexpr uint32_t kRecord = latent_record_bytes(FP8);
     Walk walk(p, s, hd.tpb);
     Segment g;
     uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(p, g)) {
         const int32_t* table = p.block_table + static_cast<int64_t>(g.b) * p.max_blocks;
+        Ids ids = load_ids(p, table, g.t0, g, lane);
         #pragma unroll 1
         for (int t = g.t0; ok && t < g.t1; t += 8) {
-            const int pos = t * kTile + lane * kBs;
-            int id = -1;
-            uint32_t bits = 0;
-            if (pos < g.end && t + (lane >> 2) < g.t1) {
-                id = table[pos / kBs];
-                if (id < 0 || id >= p.num_blocks) {
-                    report(p.err, KVD_ERR_OOB);
-                    id = -1;
-                } else {
-                    bits = p.retain ? p.retain[id] : 0xffffu;
-                    if (g.end - pos < kBs) bits &= (1u << (g.end - pos)) - 1u;
-                }
-            }
+            check_ids(p, ids, t, g, lane);
+            const Ids next = load_ids(p, table, t + 8, g, lane);
             #pragma unroll 1
             for (int u = 0; ok && u < 8 && t + u < g.t1; ++u, ++n) {
-                const uint32_t st = n % kStages;
-                if (n >= kStages) ok = wait_bar(s, &s.empty[st], n / kStages - 1);
+                const uint32_t at = n % kInfos;
+                if (n >= kInfos) ok = wait_bar(s, FP8 ? &s.free[at] : &s.empty[at], n / kInfos - 1);
                 if (!ok) break;
                 unsigned long long mask = 0;
-                int ids[4], copies = 0;
+                int block[4], copies = 0;
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    ids[k] = __shfl_sync(kFull, id, 4 * u + k);
-                    mask |= static_cast<unsigned long long>(__shfl_sync(kFull, bits, 4 * u + k)) << (16 * k);
-                    copies += ids[k] >= 0;
+                    block[k] = __shfl_sync(kFull, ids.id, 4 * u + k);
+                    mask |= static_cast<unsigned long long>(__shfl_sync(kFull, ids.bits, 4 * u + k)) << (16 * k);
+                    copies += block[k] >= 0;
                 }
                 if (lane == 0) {
-                    Info& info = s.info[st];
+                    Info& info = s.info[at];
                     info.mask = mask;
                     info.base = (t + u) * kTile;
                     if constexpr (FP8) {
                         #pragma unroll
-                        for (int k = 0; k < 4; ++k) info.id[k] = ids[k];
-                        mbar_arrive(&s.full[st]);
+                        for (int k = 0; k < 4; ++k) {
+                            info.id[k] = block[k];
+                            if (block[k] >= 0)
+                                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.mem + static_cast<int64_t>(block[k]) * kRecord), "r"(kRecord) : "memory");
+                        }
+                        mbar_arrive(&s.full[at]);
                     } else {
-                        constexpr uint32_t kRecord = latent_record_bytes(false);
-                        if (copies) mbar_arrive_expect_tx(&s.full[st], copies * kRecord);
-                        else mbar_arrive(&s.full[st]);
+                        if (copies) mbar_arrive_expect_tx(&s.full[at], copies * kRecord);
+                        else mbar_arrive(&s.full[at]);
                         #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (ids[k] >= 0) bulk_copy(s.k[st] + k * kRecord, p.mem + static_cast<int64_t>(ids[k]) * kRecord, kRecord, &s.full[st]);
+                            if (block[k] >= 0) bulk_copy(s.k[at] + k * kRecord, p.mem + static_cast<int64_t>(block[k]) * kRecord, kRecord, &s.full[at]);
                     }
                 }
                 __syncwarp();
             }
+            ids = next;
         }
     }
     if (!FP8 && s.abort) {   // copies under way must land in memory that is still this block's
@@ -385,51 +407,69 @@ __device__ __forceinline__ void fixer(Smem& s, const LatentAttnParams& p, const 
 
 // ------------------------------------------------------------------- convert
 // 8-bit records become bf16 operands: codes exactly (every e4m3 value is a bf16 value), the scale stays outside.  A warp
-// takes eight tokens of a tile: 64 codes of each of them, 512 bytes, a load.
+// takes eight tokens of a tile: 64 codes of each of them, 512 bytes, a load.  A tile's loads are under way while the one
+// before it is converted.
+struct Raw {
+    uint4 code[8], rot[2];
+    float scale;
+};
+__device__ __forceinline__ bool load_raw(Smem& s, const LatentAttnParams& p, Raw& x, uint32_t n, int warp, int lane) {
+    const uint32_t at = n % infos_of(true);
+    if (!wait_bar(s, &s.full[at], n / infos_of(true))) return false;
+    const int r = lane >> 2, j = lane & 3;
+    const Info& info = s.info[at];
+    const bool on = info.mask >> (warp * 8 + r) & 1;
+    const uint8_t* record = p.mem + static_cast<int64_t>(max(info.id[warp >> 1], 0)) * latent_record_bytes(true);
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) x.code[i] = on ? ld16(record + (warp & 1) * 4096 + i * 512 + r * 64 + j * 16) : none;
+    #pragma unroll
+    for (int i = 0; i < 2; ++i) x.rot[i] = on ? ld16(record + kLatCodes + (warp & 1) * 1024 + r * 128 + (2 * j + i) * 16) : none;
+    x.scale = on ? *reinterpret_cast<const float*>(record + kLatScales + 4 * ((warp & 1) * 8 + r)) : 0.f;
+    return true;
+}
+__device__ __forceinline__ bool store_raw(Smem& s, const Raw& x, uint32_t n, int warp, int lane) {
+    const uint32_t st = n % kStages;
+    if (n >= kStages && !wait_bar(s, &s.empty[st], n / kStages - 1)) return false;
+    const int r = lane >> 2, j = lane & 3;
+    uint8_t* group = s.k[st] + warp * kGroup + r * 128;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
+        uint32_t o[8];
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16x2x2(w[k], lo, hi);
+            const float2 a = unpack_f16(lo), b = unpack_f16(hi);
+            o[2 * k] = pack_bf16(a.x, a.y);
+            o[2 * k + 1] = pack_bf16(b.x, b.y);
+        }
+        *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j) ^ r) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j + 1) ^ r) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    #pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(group + 8192 + (2 * j + i) * 16) = x.rot[i];   // (in its order already)
+    if (j == 0) s.info[n % infos_of(true)].scale[warp * 8 + r] = x.scale;
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.ready[st]);
+    return true;
+}
 __device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, const Heads& hd, int warp, int lane) {
     Walk walk(p, s, hd.tpb);
     Segment g;
-    uint32_t n = 0;
-    const int r = lane >> 2, j = lane & 3, tok = (warp & 1) * 8 + r;   // token of its block, pieces 2j and 2j + 1
-    while (walk.next(p, g)) {
-        #pragma unroll 1
-        for (int t = g.t0; t < g.t1; ++t, ++n) {
-            const uint32_t st = n % kStages;
-            if (!wait_bar(s, &s.full[st], n / kStages)) return;
-            const Info& info = s.info[st];
-            const int id = info.id[warp >> 1], c = warp * 8 + r;
-            const bool on = info.mask >> c & 1;
-            const uint8_t* record = p.mem + static_cast<int64_t>(max(id, 0)) * latent_record_bytes(true);
-            uint4 code[8], rot[2];
-            float scale = 0.f;
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) code[i] = on ? ld16(record + (warp & 1) * 4096 + i * 512 + r * 64 + j * 16) : make_uint4(0, 0, 0, 0);
-            #pragma unroll
-            for (int i = 0; i < 2; ++i) rot[i] = on ? ld16(record + kLatCodes + (warp & 1) * 1024 + r * 128 + (2 * j + i) * 16) : make_uint4(0, 0, 0, 0);
-            if (on) scale = *reinterpret_cast<const float*>(record + kLatScales + 4 * tok);
-            uint8_t* group = s.k[st] + warp * kGroup + r * 128;
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-                uint32_t o[8];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t lo, hi;
-                    e4m3x4_to_f16x2x2(w[k], lo, hi);
-                    const float2 a = unpack_f16(lo), b = unpack_f16(hi);
-                    o[2 * k] = pack_bf16(a.x, a.y);
-                    o[2 * k + 1] = pack_bf16(b.x, b.y);
-                }
-                *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j) ^ r) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(group + i * 1024 + (((2 * j + 1) ^ r) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-            #pragma unroll
-            for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(group + 8192 + (2 * j + i) * 16) = rot[i];   // (in its order already)
-            if (j == 0) s.info[st].scale[c] = scale;
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.ready[st]);
-        }
+    uint32_t tiles = 0;
+    while (walk.next(p, g)) tiles += g.t1 - g.t0;
+    Raw a, b;
+    if (tiles == 0 || !load_raw(s, p, a, 0, warp, lane)) return;
+    #pragma unroll 1
+    for (uint32_t n = 0; n < tiles; n += 2) {
+        if (n + 1 < tiles && !load_raw(s, p, b, n + 1, warp, lane)) return;
+        if (!store_raw(s, a, n, warp, lane)) return;
+        if (n + 1 >= tiles) return;
+        if (n + 2 < tiles && !load_raw(s, p, a, n + 2, warp, lane)) return;
+        if (!store_raw(s, b, n + 1, warp, lane)) return;
     }
 }
 
@@ -530,6 +570,58 @@ __device__ __forceinline__ void tmem_st_16x64(uint32_t addr, const uint32_t (&v)
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_16x32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// Row of q and out of row r of a unit (token r / each, head r % each), or −1.
+__device__ __forceinline__ int64_t row_of(const LatentAttnParams& p, const Heads& hd, const Segment& g, int r) {
+    const int tok = r / hd.each, h = r - tok * hd.each;
+    return tok < hd.tpb && g.tok0 + tok < g.T && h < hd.n ? (static_cast<int64_t>(g.s0) + g.tok0 + tok) * p.n_q + hd.first + h : -1;
+}
+
+// A unit's queries to tensor memory: column j holds dims 2j, 2j + 1 of a row.
+__device__ __forceinline__ void load_q(Smem& s, const LatentAttnParams& p, const Heads& hd, const Segment& g, uint32_t mine, int warp, int lane) {
+    const uint16_t* src[2];
+    bool on[2];
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t row = row_of(p, hd, g, warp * 16 + (lane >> 2) + 8 * h);
+        on[h] = row >= 0;
+        src[h] = p.q + max(row, static_cast<int64_t>(0)) * kLatKey + 4 * (lane & 3);
+    }
+    #pragma unroll 1
+    for (int c = 0; c < 5; c += 2) {   // 64 columns, 128 dims, twice; 32 columns at the end
+        uint32_t v[2][32];
+        #pragma unroll
+        for (int b = 0; b < 2; ++b)
+            #pragma unroll
+            for (int k = 0; k < 8; ++k)
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool use = on[h] && (c < 4 || (b == 0 && k < 4));
+                    const uint2 x = use ? *reinterpret_cast<const uint2*>(src[h] + (c + b) * 128 + k * 16) : make_uint2(0, 0);
+                    v[b][4 * k + 2 * h] = x.x;
+                    v[b][4 * k + 2 * h + 1] = x.y;
+                }
+        if (c < 4) {
+            tmem_st_16x64(mine + kColQ + c * 64, v[0]);
+            tmem_st_16x64(mine + kColQ + c * 64 + 64, v[1]);
+        } else {
+            tmem_st_16x32(mine + kColQ + c * 64, v[0]);
+        }
+    }
+    tmem_wait_st();
+    tcgen_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_full);
+}
+
 template <bool FP8>
 __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, const Heads& hd, int warp, int lane) {
     const uint32_t mine = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -538,33 +630,9 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
     Segment g;
     uint32_t n = 0;
     bool ok = true;
-    while (ok && walk.next(p, g)) {
-        // row r is token r / each, head r % each of the unit
-        auto row_of = [&](int r) -> int64_t {
-            const int tok = r / hd.each, h = r - tok * hd.each;
-            return tok < hd.tpb && g.tok0 + tok < g.T && h < hd.n ? (static_cast<int64_t>(g.s0) + g.tok0 + tok) * p.n_q + hd.first + h : -1;
-        };
-        {   // Q: lanes 0 .. 15 a row each (lanes 16 .. 31 write where the next O will stand)
-            const int64_t row = row_of(warp * 16 + (lane & 15));
-            const uint16_t* src = p.q + max(row, static_cast<int64_t>(0)) * kLatKey;
-            #pragma unroll 1
-            for (int c = 0; c < 9; ++c) {
-                uint32_t v[32];
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 x = row >= 0 && lane < 16 ? ld16(src + c * 64 + i * 8) : make_uint4(0, 0, 0, 0);
-                    v[4 * i] = x.x;
-                    v[4 * i + 1] = x.y;
-                    v[4 * i + 2] = x.z;
-                    v[4 * i + 3] = x.w;
-                }
-                tmem_st32(mine + kColQ + c * 32, v);
-            }
-            tmem_wait_st();
-            tcgen_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.q_full);
-        }
+    bool more = walk.next(p, g);
+    if (more) load_q(s, p, hd, g, mine, warp, lane);
+    while (ok && more) {
         const int r0 = warp * 16 + (lane >> 2);
         const int limit[2] = {g.first + r0 / hd.each, g.first + (r0 + 8) / hd.each};   // positions that the rows attend, at most
         float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
@@ -577,7 +645,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             if (!ok) break;
             tcgen_fence_after();
             tmem_ld_16x64(mine + kColS, v);
-            const Info& info = s.info[st];
+            const Info& info = s.info[n % infos_of(FP8)];
             if constexpr (FP8) {
                 uint32_t r[32];
                 tmem_ld_16x64(mine + kColR, r);
@@ -671,21 +739,28 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.p_full);
+            if (lane == 0) {
+                mbar_arrive(&s.p_full);
+                if (FP8) mbar_arrive(&s.free[n % infos_of(true)]);
+            }
         }
+        // the next unit's queries take the place of this one's, whose logits are all there: S goes on during what follows
+        Segment after;
+        more = ok && walk.next(p, after);
+        if (more) load_q(s, p, hd, after, mine, warp, lane);
         if (ok) ok = wait_bar(s, &s.empty[(n - 1) % kStages], (n - 1) / kStages);
         if (!ok) break;
         tcgen_fence_after();
         const bool whole = g.t0 == 0 && g.t1 == g.tiles;
         const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
-        const int64_t row[2] = {row_of(r0), row_of(r0 + 8)};
+        const int64_t row[2] = {row_of(p, hd, g, r0), row_of(p, hd, g, r0 + 8)};
         #pragma unroll
         for (int h = 0; h < 2; ++h) {
             sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
             sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
         }
         if (!whole) {
-            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.tb, g.t0 == 0 ? 1 : 0, g.parts);
+            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.tb, min(hd.tpb, g.T - g.tok0) * hd.each, g.parts);
             #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (quad == 0) {
@@ -733,9 +808,10 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                     const int i = (__ffs(todo) - 1) >> 2, r = warp * 16 + 8 * h + i;
                     todo &= ~(15u << 4 * i);
                     __syncwarp();
-                    plain_row<FP8>(p, g.b, row_of(r), g.len < 0 ? 0 : g.first + r / hd.each + 1);
+                    plain_row<FP8>(p, g.b, row_of(p, hd, g, r), g.len < 0 ? 0 : g.first + r / hd.each + 1);
                 }
         }
+        g = after;
     }
 }
 
@@ -746,8 +822,11 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == kIssueWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < infos_of(FP8); ++i) {
             mbar_init(&s.full[i], 1);
+            mbar_init(&s.free[i], 4);
+        }
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.ready[i], FP8 ? kConvertWarps : 1);
             mbar_init(&s.empty[i], 1);
         }
@@ -789,73 +868,165 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     }
 }
 
-// Joins the parts of units that the schedule cut: a CTA a row at a time.
-constexpr int kJoinThreads = 128;
+// Joins the parts of units that the schedule cut.  A CTA of the schedule starts at most one of them, as its last; the
+// others' parts are the following CTAs' first.  Rows of few parts are joined by a warp each, rows of many by a CTA.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kMaxCtas = 512;
+struct Join {
+    int4 start[kMaxCtas];            // (request, token block, rows, parts) of the unit that the CTA starts
+    uint32_t rows[kMaxCtas];         // running counts of rows: of few parts, of many << 16
+    float part[kJoinWarps][kLatDim];
+    float sum[kJoinWarps];
+};
+// The row of a unit: its place in out (−1: none), the end of what it attends, whether the unit has more tokens.
+struct JoinRow {
+    int64_t row;
+    int b, end, r;
+    bool multi;
+};
+__device__ __forceinline__ JoinRow join_row(const LatentAttnParams& p, const int4& g, int cta, int r) {
+    const Heads hd(p, cta % ((p.n_q + kRows - 1) / kRows));
+    const Request q = load_request(p, g.x, false);
+    const int tok = r / hd.each, h = r - tok * hd.each, i = g.y * hd.tpb + tok;
+    JoinRow x;
+    x.row = h < hd.n ? (static_cast<int64_t>(q.s0) + i) * p.n_q + hd.first + h : -1;
+    x.b = g.x;
+    x.end = q.len < 0 ? 0 : q.len - q.T + i + 1;
+    x.r = r;
+    x.multi = min(hd.tpb, q.T - g.y * hd.tpb) > 1;
+    return x;
+}
+__device__ __forceinline__ void put4(const LatentAttnParams& p, int64_t row, int d, float4 x, float inv) {
+    if (p.out_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatDim + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kLatDim + d) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnParams p, int ctas) {
-    extern __shared__ int4 seg[];   // 2·ctas, then the starts
-    int* start = reinterpret_cast<int*>(seg + 2 * ctas);
-    __shared__ int count;
-    __shared__ float top_s[4];
+    __shared__ Join s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) count = 0;
-    for (int i = tid; i < 2 * ctas; i += kJoinThreads) seg[i] = p.part_seg[i];
+    for (int i = tid; i < ctas; i += kJoinThreads) {
+        const int4 g = p.part_seg[2 * i + 1];
+        s.start[i] = g;
+        s.rows[i] = g.x < 0 ? 0u : g.w <= kJoinWarps ? static_cast<uint32_t>(g.z) : static_cast<uint32_t>(g.z) << 16;
+    }
     __syncthreads();
     if (warp == 0) {
-        int c = 0;
-        for (int i0 = 0; i0 < 2 * ctas; i0 += 32) {
-            const bool on = i0 + lane < 2 * ctas && seg[i0 + lane].x >= 0 && (seg[i0 + lane].z & 1);
-            const unsigned at = __ballot_sync(kFull, on);
-            if (on) start[c + __popc(at & ((1u << lane) - 1))] = i0 + lane;
-            c += __popc(at);
+        uint32_t before = 0;
+        for (int i = lane; i - lane < ctas; i += 32) {
+            uint32_t up = i < ctas ? s.rows[i] : 0;
+            #pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(kFull, up, o);
+                if (lane >= o) up += v;
+            }
+            up += before;
+            if (i < ctas) s.rows[i] = up;
+            before = __shfl_sync(kFull, up, 31);
         }
-        if (lane == 0) count = c;
     }
     __syncthreads();
     const int blocks = (p.n_q + kRows - 1) / kRows;
-    for (int item = blockIdx.x; item < count * kRows; item += gridDim.x) {
-        const int slot0 = start[item / kRows], r = item % kRows;
-        const int4 g = seg[slot0];
-        const Heads hd(p, (slot0 >> 1) % blocks);
-        const Request q = load_request(p, g.x, false);
-        const int tok = r / hd.each, h = r - tok * hd.each, i = g.y * hd.tpb + tok;
-        if (tok >= hd.tpb || i >= q.T || h >= hd.n) continue;
-        const int64_t row = (static_cast<int64_t>(q.s0) + i) * p.n_q + hd.first + h;
-        auto slot_of = [&](int k) { return k == 0 ? slot0 : (((slot0 >> 1) + k * blocks) << 1); };   // a later part is its CTA's first
-        float m = -INFINITY;
-        for (int k = tid; k < g.w; k += kJoinThreads) m = fmaxf(m, p.part_ml[static_cast<int64_t>(slot_of(k)) * 2 * kRows + r]);
+    const uint32_t total = s.rows[ctas - 1];
+    auto unit_of = [&](int item, int shift, int& r) {   // the CTA that starts the item's unit, and the row
+        int a = 0, z = ctas - 1;
+        while (a < z) {
+            const int mid = (a + z) >> 1;
+            if (static_cast<int>(s.rows[mid] >> shift & 0xffffu) > item) z = mid;
+            else a = mid + 1;
+        }
+        r = item - (a > 0 ? static_cast<int>(s.rows[a - 1] >> shift & 0xffffu) : 0);
+        return a;
+    };
+    auto slot_of = [&](int cta, int k) -> int64_t { return k == 0 ? 2 * cta + 1 : 2 * (cta + k * blocks); };
+    for (int item = blockIdx.x * kJoinWarps + warp; item < static_cast<int>(total & 0xffffu); item += gridDim.x * kJoinWarps) {
+        int r;
+        const int cta = unit_of(item, 0, r), parts = s.start[cta].w;
+        const JoinRow x = join_row(p, s.start[cta], cta, r);
+        if (x.row < 0) continue;
+        const int64_t mine = slot_of(cta, min(lane, parts - 1));
+        const float m = p.part_ml[mine * 2 * kRows + r], l = p.part_ml[(mine * 2 + 1) * kRows + r];
+        float4 acc[4];
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        __syncthreads();
-        if (lane == 0) top_s[warp] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
-        const float z = m == -INFINITY ? 0.f : m;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        #pragma unroll 8
-        for (int k = 0; k < g.w; ++k) {
-            const int64_t sl = slot_of(k);
-            const float w = ex2(p.part_ml[sl * 2 * kRows + r] - z);
-            const float4 o = *reinterpret_cast<const float4*>(p.part + (sl * kRows + r) * kLatDim + 4 * tid);
-            sum = fmaf(w, p.part_ml[(sl * 2 + 1) * kRows + r], sum);
-            acc = make_float4(fmaf(w, o.x, acc.x), fmaf(w, o.y, acc.y), fmaf(w, o.z, acc.z), fmaf(w, o.w, acc.w));
+        for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = m;
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const float w = ex2(m - (top == -INFINITY ? 0.f : top));
+        float sum = lane < parts ? w * l : 0.f;
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        #pragma unroll 2
+        for (int k = 0; k < parts; ++k) {
+            const float f = __shfl_sync(kFull, w, k);
+            const float* src = p.part + (slot_of(cta, k) * kRows + r) * kLatDim + 4 * lane;
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 o = *reinterpret_cast<const float4*>(src + 128 * j);
+                acc[j] = make_float4(fmaf(f, o.x, acc[j].x), fmaf(f, o.y, acc[j].y), fmaf(f, o.z, acc[j].z), fmaf(f, o.w, acc[j].w));
+            }
         }
-        // as in a whole unit: a row that is NaN is computed again without the tokens that it does not attend
-        const float odd = acc.x + acc.y + acc.z + acc.w;
-        if (__syncthreads_or(odd != odd) && min(hd.tpb, q.T - g.y * hd.tpb) > 1) {
-            if (warp == 0) plain_row<FP8>(p, g.x, row, q.len < 0 ? 0 : q.len - q.T + i + 1);
-            continue;
-        }
+        float odd = 0.f;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (p.out_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatDim + 4 * tid) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kLatDim + 4 * tid) =
-                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-        if (tid == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            odd += acc[j].x + acc[j].y + acc[j].z + acc[j].w;
+            put4(p, x.row, 4 * lane + 128 * j, acc[j], inv);
+        }
+        if (lane == 0 && p.lse_out) p.lse_out[x.row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        // as in a whole unit: a row that is NaN is computed again without the tokens that it does not attend
+        if (x.multi && __any_sync(kFull, odd != odd)) plain_row<FP8>(p, x.b, x.row, x.end);
+    }
+    for (int item = blockIdx.x; item < static_cast<int>(total >> 16); item += gridDim.x) {
+        int r;
+        const int cta = unit_of(item, 16, r), parts = s.start[cta].w;
+        const JoinRow x = join_row(p, s.start[cta], cta, r);
+        if (x.row < 0) continue;
+        float top = -INFINITY;
+        for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_ml[slot_of(cta, k) * 2 * kRows + r]);
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const float z = top == -INFINITY ? 0.f : top;
+        float4 acc[4];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        #pragma unroll 2
+        for (int k = warp; k < parts; k += kJoinWarps) {
+            const int64_t sl = slot_of(cta, k);
+            const float f = ex2(p.part_ml[sl * 2 * kRows + r] - z);
+            sum = fmaf(f, p.part_ml[(sl * 2 + 1) * kRows + r], sum);
+            const float* src = p.part + (sl * kRows + r) * kLatDim + 4 * lane;
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 o = *reinterpret_cast<const float4*>(src + 128 * j);
+                acc[j] = make_float4(fmaf(f, o.x, acc[j].x), fmaf(f, o.y, acc[j].y), fmaf(f, o.z, acc[j].z), fmaf(f, o.w, acc[j].w));
+            }
+        }
+        __syncthreads();   // the row before has been read
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(&s.part[warp][4 * lane + 128 * j]) = acc[j];
+        if (lane == 0) s.sum[warp] = sum;
+        __syncthreads();
+        float odd = 0.f;
+        sum = 0.f;
+        #pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) sum += s.sum[k];
+        if (warp < 4) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            #pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) {
+                const float4 o = *reinterpret_cast<const float4*>(&s.part[k][4 * tid]);
+                y = make_float4(y.x + o.x, y.y + o.y, y.z + o.z, y.w + o.w);
+            }
+            odd = y.x + y.y + y.z + y.w;
+            put4(p, x.row, 4 * tid, y, sum == 0.f ? 0.f : 1.f / sum);
+        }
+        if (tid == 0 && p.lse_out) p.lse_out[x.row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (__syncthreads_or(odd != odd) && x.multi && warp == 0) plain_row<FP8>(p, x.b, x.row, x.end);
     }
 }
 
@@ -866,14 +1037,14 @@ cudaError_t launch(const LatentAttnParams& p, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_dependent(attn_kernel<FP8>, dim3(static_cast<unsigned>(ctas)), dim3(threads_of(FP8)), sizeof(Smem), -1, stream, p);
     if (e != cudaSuccess) return e;
-    const size_t smem = static_cast<size_t>(2 * ctas) * (sizeof(int4) + sizeof(int));
-    return launch_dependent(join_kernel<FP8>, dim3(static_cast<unsigned>(8 * ctas)), dim3(kJoinThreads), smem, -1, stream, p, ctas);
+    return launch_dependent(join_kernel<FP8>, dim3(static_cast<unsigned>(2 * ctas)), dim3(kJoinThreads), 0, -1, stream, p, ctas);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, bool fp8, int num_sms, cudaStream_t stream) {
-    return fp8 ? launch<true>(p, num_sms, stream) : launch<false>(p, num_sms, stream);
+    const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+    return fp8 ? launch<true>(p, ctas, stream) : launch<false>(p, ctas, stream);
 }
 
 }  // namespace kvd
