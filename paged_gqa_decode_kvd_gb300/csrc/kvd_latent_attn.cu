@@ -51,9 +51,6 @@ struct Smem {
     uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages], s_full, s_free, p_full, q_full, drain;
     uint32_t tmem;
     volatile int abort;
-    // the CTA's share of the schedule
-    int64_t at, remaining, share;
-    int b, tb, off, extra;
 };
 
 struct Request {
@@ -63,7 +60,7 @@ struct Segment {
     int b, tb, t0, t1, tiles;
     int s0, T, len;
     int tok0, first, end;    // first token, its position, positions that the last row attends
-    int parts;               // CTAs that share the unit
+    int64_t start;           // of the unit's tiles in the schedule
     bool multi;              // rows of more than one token
 };
 
@@ -119,22 +116,22 @@ struct Heads {
     }
 };
 
+// Quotients are of 32 bits where they can be: the long division takes five times as long, and a call waits for it.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 // The CTA's segments in order; every role walks them on its own.
 struct Walk {
     int64_t at, remaining, share;
     int b, tb, off, extra, tpb;
     Request r;
-    __device__ __forceinline__ Walk(const LatentAttnParams& p, const Smem& s, int tokens)
-        : at(s.at), remaining(s.remaining), share(s.share), b(s.b), tb(s.tb), off(s.off), extra(s.extra), tpb(tokens), r{0, 0, -1} {
-        if (remaining > 0) r = load_request(p, b, false);
-    }
     __device__ __forceinline__ bool next(const LatentAttnParams& p, Segment& g) {
         while (remaining > 0) {
             g.b = b;
             g.tb = tb;
             g.tiles = unit_tiles(r, tb, tpb);
-            const int64_t start = at - off + extra;   // of the unit's tiles in the schedule
-            g.parts = static_cast<int>((start + g.tiles - 1) / share - start / share) + 1;
+            g.start = at - off + extra;
             const int take = static_cast<int>(min(static_cast<int64_t>(g.tiles) + extra - off, remaining));
             g.t0 = max(off - extra, 0);
             g.t1 = off + take - extra;
@@ -162,20 +159,23 @@ struct Walk {
         }
         return false;
     }
+    // CTAs that share the unit.
+    __device__ __forceinline__ int parts(const Segment& g) const {
+        return static_cast<int>(quotient(g.start + g.tiles - 1, share) - quotient(g.start, share)) + 1;
+    }
 };
 
-// The CTA's share, by every thread of the block; scratch holds 2·p.B int64.
-__device__ inline void make_schedule(const LatentAttnParams& p, Smem& s, int64_t* scratch, const Heads& hd, int threads) {
-    const int tid = threadIdx.x, lane = tid & 31, tpb = hd.tpb;
-    for (int b = tid; b < p.B; b += threads) {
+// The CTA's share, found by each warp; scratch holds 2·p.B int64 (what every request costs), filled before by all threads.
+__device__ inline void fill_scratch(const LatentAttnParams& p, int64_t* scratch, int tpb, int threads) {
+    for (int b = threadIdx.x; b < p.B; b += threads) {
         const Request r = load_request(p, b, blockIdx.x == 0);
         const int units = (r.T + tpb - 1) / tpb;
         scratch[2 * b] = r.T ? tiles_before(r, units, tpb) : 0;
         scratch[2 * b + 1] = units;
     }
-    __syncthreads();
-    if (tid >= 32) return;
-    const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks;
+}
+__device__ inline Walk find_share(const LatentAttnParams& p, const int64_t* scratch, const Heads& hd, int lane) {
+    const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks, tpb = hd.tpb;
     int64_t tiles = 0, units = 0;
     for (int b = lane; b < p.B; b += 32) {
         tiles += scratch[2 * b];
@@ -186,20 +186,19 @@ __device__ inline void make_schedule(const LatentAttnParams& p, Smem& s, int64_t
         tiles += __shfl_xor_sync(kFull, tiles, o);
         units += __shfl_xor_sync(kFull, units, o);
     }
+    Walk w{};
+    w.tpb = tpb;
     // a small call is cut into its smallest shares; there the border must not fall beside the tiles
-    const int extra = static_cast<int>(min(static_cast<int64_t>(kUnitTiles), tiles / (8 * lanes)));
-    const int64_t total = tiles + units * extra;
-    const int64_t share = max((total + lanes - 1) / lanes, static_cast<int64_t>(kMinShare));
-    const int64_t lo = min(share * me, total), hi = me < lanes ? min(lo + share, total) : lo;
-    if (lane == 0) {
-        s.at = lo;
-        s.remaining = hi - lo;
-        s.share = share;
-        s.extra = extra;
-    }
+    w.extra = static_cast<int>(min(static_cast<int64_t>(kUnitTiles), quotient(tiles, 8 * lanes)));
+    const int64_t total = tiles + units * w.extra;
+    w.share = max(quotient(total + lanes - 1, lanes), static_cast<int64_t>(kMinShare));
+    const int64_t lo = min(w.share * me, total), hi = me < lanes ? min(lo + w.share, total) : lo;
+    w.at = lo;
+    w.remaining = hi - lo;
+    if (hi <= lo) return w;
     int64_t before = 0;
-    for (int b0 = 0; hi > lo && b0 < p.B; b0 += 32) {
-        const int64_t c = b0 + lane < p.B ? scratch[2 * (b0 + lane)] + extra * scratch[2 * (b0 + lane) + 1] : 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int64_t c = b0 + lane < p.B ? scratch[2 * (b0 + lane)] + w.extra * scratch[2 * (b0 + lane) + 1] : 0;
         int64_t up = c;
         #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -207,23 +206,32 @@ __device__ inline void make_schedule(const LatentAttnParams& p, Smem& s, int64_t
             if (lane >= o) up += v;
         }
         up += before;
-        if (lo >= up - c && lo < up) {   // one lane
-            const int b = b0 + lane;
-            const Request r = load_request(p, b, false);
-            const int64_t in = lo - (up - c);
-            int a = 0, z = (r.T + tpb - 1) / tpb;   // the last unit of [a, z) that starts at or before `in`
+        const unsigned at = __ballot_sync(kFull, lo >= up - c && lo < up);
+        if (at) {
+            const int src = __ffs(at) - 1;
+            const int64_t in = lo - __shfl_sync(kFull, up - c, src);
+            w.b = b0 + src;
+            w.r = load_request(p, w.b, false);
+            int a = 0, z = (w.r.T + tpb - 1) / tpb;   // the last unit of [a, z) that starts at or before `in`
+            int64_t from = 0;
             while (z - a > 1) {
                 const int mid = a + (z - a) / 2;
-                if (tiles_before(r, mid, tpb) + static_cast<int64_t>(mid) * extra <= in) a = mid;
-                else z = mid;
+                const int64_t x = tiles_before(w.r, mid, tpb) + static_cast<int64_t>(mid) * w.extra;
+                if (x <= in) {
+                    a = mid;
+                    from = x;
+                } else {
+                    z = mid;
+                }
             }
-            s.b = b;
-            s.tb = a;
-            s.off = static_cast<int>(in - tiles_before(r, a, tpb) - static_cast<int64_t>(a) * extra);
+            w.tb = a;
+            w.off = static_cast<int>(in - from);
+            return w;
         }
         before = __shfl_sync(kFull, up, 31);
-        if (before > lo) break;
     }
+    w.remaining = 0;
+    return w;
 }
 
 __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase) {
@@ -237,9 +245,9 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
 }
 
 // ------------------------------------------------------------- one row, plainly
-// A warp a row: a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
+// A warp a row (quarter ≥ 0: 128 of its dims): a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
 template <bool FP8>
-__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end) {
+__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end, int quarter = -1) {
     const int lane = threadIdx.x & 31;
     const uint16_t* qr = p.q + row * kLatKey;
     float q[24], acc[16], m = -INFINITY, sum = 0.f;
@@ -291,11 +299,13 @@ __device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int64_t at = row * kLatDim + (i >> 3) * 256 + lane * 8 + (i & 7);
+        const int d = (i >> 3) * 256 + lane * 8 + (i & 7);
+        if (quarter >= 0 && d >> 7 != quarter) continue;
+        const int64_t at = row * kLatDim + d;
         if (p.out_f32) static_cast<float*>(p.out)[at] = acc[i] * inv;
         else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
     }
-    if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    if (lane == 0 && quarter <= 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ producer
@@ -324,10 +334,9 @@ __device__ __forceinline__ void check_ids(const LatentAttnParams& p, Ids& x, int
 }
 
 template <bool FP8>
-__device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, const Heads& hd, int lane) {
+__device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, Walk walk, int lane) {
     constexpr int kInfos = infos_of(FP8);
     constexpr uint32_t kRecord = latent_record_bytes(FP8);
-    Walk walk(p, s, hd.tpb);
     Segment g;
     uint32_t n = 0;
     bool ok = true;
@@ -383,8 +392,7 @@ __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, con
 
 // ----------------------------------------------------------------------- fix
 // Rows that nobody may attend are zeroed: their weight is 0, and 0·NaN would be NaN.
-__device__ __forceinline__ void fixer(Smem& s, const LatentAttnParams& p, const Heads& hd, int lane) {
-    Walk walk(p, s, hd.tpb);
+__device__ __forceinline__ void fixer(Smem& s, const LatentAttnParams& p, Walk walk, int lane) {
     Segment g;
     uint32_t n = 0;
     while (walk.next(p, g)) {
@@ -456,8 +464,7 @@ __device__ __forceinline__ bool store_raw(Smem& s, const Raw& x, uint32_t n, int
     if (lane == 0) mbar_arrive(&s.ready[st]);
     return true;
 }
-__device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, const Heads& hd, int warp, int lane) {
-    Walk walk(p, s, hd.tpb);
+__device__ __forceinline__ void converter(Smem& s, const LatentAttnParams& p, Walk walk, int warp, int lane) {
     Segment g;
     uint32_t tiles = 0;
     while (walk.next(p, g)) tiles += g.t1 - g.t0;
@@ -484,11 +491,10 @@ __device__ __forceinline__ uint64_t desc_n(uint32_t addr) {
 }
 
 template <bool FP8>
-__device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, const Heads& hd) {
+__device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, Walk walk) {
     constexpr uint32_t kDescS = mma_desc_bf16(64, kTile), kDescO = mma_desc_bf16(64, 256) | (1u << 16);
     const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), p_op = uniform(smem_u32(s.p));
     const uint32_t s_full = uniform(smem_u32(&s.s_full));
-    Walk walk(p, s, hd.tpb);
     Segment g;
     uint32_t n = 0, segs = 0;   // tiles before
     bool ok = true;
@@ -595,27 +601,21 @@ __device__ __forceinline__ void load_q(Smem& s, const LatentAttnParams& p, const
         on[h] = row >= 0;
         src[h] = p.q + max(row, static_cast<int64_t>(0)) * kLatKey + 4 * (lane & 3);
     }
-    #pragma unroll 1
-    for (int c = 0; c < 5; c += 2) {   // 64 columns, 128 dims, twice; 32 columns at the end
-        uint32_t v[2][32];
+    // all loads at once: behind the first tiles' copies each round of them would wait its turn (2.3 us)
+    uint32_t v[5][32];
+    #pragma unroll
+    for (int c = 0; c < 5; ++c)   // 64 columns, 128 dims; 32 columns at the end
         #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int k = 0; k < (c < 4 ? 8 : 4); ++k)
             #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bool use = on[h] && (c < 4 || (b == 0 && k < 4));
-                    const uint2 x = use ? *reinterpret_cast<const uint2*>(src[h] + (c + b) * 128 + k * 16) : make_uint2(0, 0);
-                    v[b][4 * k + 2 * h] = x.x;
-                    v[b][4 * k + 2 * h + 1] = x.y;
-                }
-        if (c < 4) {
-            tmem_st_16x64(mine + kColQ + c * 64, v[0]);
-            tmem_st_16x64(mine + kColQ + c * 64 + 64, v[1]);
-        } else {
-            tmem_st_16x32(mine + kColQ + c * 64, v[0]);
-        }
-    }
+            for (int h = 0; h < 2; ++h) {
+                const uint2 x = on[h] ? *reinterpret_cast<const uint2*>(src[h] + c * 128 + k * 16) : make_uint2(0, 0);
+                v[c][4 * k + 2 * h] = x.x;
+                v[c][4 * k + 2 * h + 1] = x.y;
+            }
+    #pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_st_16x64(mine + kColQ + c * 64, v[c]);
+    tmem_st_16x32(mine + kColQ + 256, v[4]);
     tmem_wait_st();
     tcgen_fence_before();
     __syncwarp();
@@ -623,10 +623,9 @@ __device__ __forceinline__ void load_q(Smem& s, const LatentAttnParams& p, const
 }
 
 template <bool FP8>
-__device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, const Heads& hd, int warp, int lane) {
+__device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, const Heads& hd, Walk walk, int warp, int lane) {
     const uint32_t mine = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int quad = lane & 3;
-    Walk walk(p, s, hd.tpb);
     Segment g;
     uint32_t n = 0;
     bool ok = true;
@@ -760,7 +759,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
         }
         if (!whole) {
-            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.tb, min(hd.tpb, g.T - g.tok0) * hd.each, g.parts);
+            if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.s0 + g.tok0, min(hd.tpb, g.T - g.tok0) * hd.each, walk.parts(g));
             #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (quad == 0) {
@@ -837,27 +836,37 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
         mbar_init(&s.drain, 1);
         mbar_fence_init();
         s.abort = 0;
-        s.remaining = 0;
     }
     pdl_wait();
     pdl_trigger();
     const Heads hd(p, blockIdx.x % ((p.n_q + kRows - 1) / kRows));
     if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
-    static_assert(2 * kMaxBatch * sizeof(int64_t) <= sizeof(s.k), "the schedule's scratch");
-    make_schedule(p, s, reinterpret_cast<int64_t*>(s.k[0]), hd, threads_of(FP8));
-    if (tid == 0 && (smem_u32(smem_raw) & 1023u)) {   // the operands' swizzle wants it (nothing else stands before them)
-        report(p.err, KVD_ERR_CUDA);
-        s.remaining = 0;
-    }
-    fence_proxy_async_shared();   // the scratch is overwritten by bulk copies
+    static_assert(2 * kMaxBatch * sizeof(int64_t) <= sizeof(s.k[kStages - 1]), "the schedule's scratch");
+    int64_t* scratch = reinterpret_cast<int64_t*>(s.k[kStages - 1]);
+    fill_scratch(p, scratch, hd.tpb, threads_of(FP8));
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
-    if (warp < 4) softmax<FP8>(s, p, hd, warp, lane);
-    else if (warp == kProducerWarp) producer<FP8>(s, p, hd, lane);
-    else if (warp == kIssueWarp) issuer<FP8>(s, p, hd);
-    else if (!FP8 && warp == kFixWarp) fixer(s, p, hd, lane);
-    else if (FP8 && warp >= kConvertWarp) converter(s, p, hd, warp - kConvertWarp, lane);
+    Walk walk = find_share(p, scratch, hd, lane);
+    if (smem_u32(smem_raw) & 1023u) {   // the operands' swizzle wants it (nothing else stands before them)
+        if (tid == 0) report(p.err, KVD_ERR_CUDA);
+        walk.remaining = 0;
+    }
+    fence_proxy_async_shared();
+    __syncthreads();   // the scratch has been read: copies may overwrite it
+    // 8 bits: a thread has 128 registers at launch: 200 + 72 + 2·120 = 4·128
+    if (warp < 4) {
+        if (FP8) take_registers<200>();
+        softmax<FP8>(s, p, hd, walk, warp, lane);
+    } else if (warp < kConvertWarp) {
+        if (FP8) give_registers<72>();
+        if (warp == kProducerWarp) producer<FP8>(s, p, walk, lane);
+        else if (warp == kIssueWarp) issuer<FP8>(s, p, walk);
+        else if (!FP8 && warp == kFixWarp) fixer(s, p, walk, lane);
+    } else if constexpr (FP8) {
+        give_registers<120>();
+        converter(s, p, walk, warp - kConvertWarp, lane);
+    }
     __syncwarp();
     tcgen_fence_before();
     __syncthreads();
@@ -869,41 +878,32 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
 }
 
 // Joins the parts of units that the schedule cut.  A CTA of the schedule starts at most one of them, as its last; the
-// others' parts are the following CTAs' first.  Rows of few parts are joined by a warp each, rows of many by a CTA.
+// others' parts are the following CTAs' first.  Rows of few parts are joined by a warp each, rows of many by four CTAs, 128 dims
+// each, whose warps share the parts.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kMaxCtas = 512;
 struct Join {
-    int4 start[kMaxCtas];            // (request, token block, rows, parts) of the unit that the CTA starts
+    int4 start[kMaxCtas];            // (request, first token, rows, parts) of the unit that the CTA starts
     uint32_t rows[kMaxCtas];         // running counts of rows: of few parts, of many << 16
-    float part[kJoinWarps][kLatDim];
-    float sum[kJoinWarps];
+    float part[kJoinWarps][128];
+    float weight[kMaxCtas], len[kMaxCtas];   // of a part: its factor, its sum
+    float top[kJoinWarps];
 };
-// The row of a unit: its place in out (−1: none), the end of what it attends, whether the unit has more tokens.
-struct JoinRow {
-    int64_t row;
-    int b, end, r;
-    bool multi;
-};
-__device__ __forceinline__ JoinRow join_row(const LatentAttnParams& p, const int4& g, int cta, int r) {
-    const Heads hd(p, cta % ((p.n_q + kRows - 1) / kRows));
-    const Request q = load_request(p, g.x, false);
-    const int tok = r / hd.each, h = r - tok * hd.each, i = g.y * hd.tpb + tok;
-    JoinRow x;
-    x.row = h < hd.n ? (static_cast<int64_t>(q.s0) + i) * p.n_q + hd.first + h : -1;
-    x.b = g.x;
-    x.end = q.len < 0 ? 0 : q.len - q.T + i + 1;
-    x.r = r;
-    x.multi = min(hd.tpb, q.T - g.y * hd.tpb) > 1;
-    return x;
-}
 __device__ __forceinline__ void put4(const LatentAttnParams& p, int64_t row, int d, float4 x, float inv) {
     if (p.out_f32)
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatDim + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     else
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kLatDim + d) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
 }
+// As in a whole unit: a row that is NaN is computed again without the tokens that it does not attend.
+template <bool FP8>
+__device__ __noinline__ void join_again(const LatentAttnParams& p, const int4& g, const Heads& hd, int r, int64_t row, int quarter) {
+    const Request q = load_request(p, g.x, false);
+    const int tok0 = g.y - q.s0;
+    if (min(hd.tpb, q.T - tok0) > 1) plain_row<FP8>(p, g.x, row, q.len < 0 ? 0 : q.len - q.T + tok0 + r / hd.each + 1, quarter);
+}
 
 template <bool FP8>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const LatentAttnParams p, int ctas) {
     __shared__ Join s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -942,25 +942,39 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnPara
         return a;
     };
     auto slot_of = [&](int cta, int k) -> int64_t { return k == 0 ? 2 * cta + 1 : 2 * (cta + k * blocks); };
+    auto place = [&](const int4& g, const Heads& hd, int r) -> int64_t {   // row of out, or −1
+        const int tok = r / hd.each, h = r - tok * hd.each;
+        return h < hd.n ? (static_cast<int64_t>(g.y) + tok) * p.n_q + hd.first + h : -1;
+    };
     for (int item = blockIdx.x * kJoinWarps + warp; item < static_cast<int>(total & 0xffffu); item += gridDim.x * kJoinWarps) {
         int r;
-        const int cta = unit_of(item, 0, r), parts = s.start[cta].w;
-        const JoinRow x = join_row(p, s.start[cta], cta, r);
-        if (x.row < 0) continue;
-        const int64_t mine = slot_of(cta, min(lane, parts - 1));
+        const int cta = unit_of(item, 0, r);
+        const int4 g = s.start[cta];
+        const Heads hd(p, cta % blocks);
+        const int64_t row = place(g, hd, r);
+        if (row < 0) continue;
+        const int64_t mine = slot_of(cta, min(lane, g.w - 1));
         const float m = p.part_ml[mine * 2 * kRows + r], l = p.part_ml[(mine * 2 + 1) * kRows + r];
-        float4 acc[4];
+        float4 acc[4], x[2][4];
         #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 2; ++k)   // (a cut unit has two parts at least)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[k][j] = *reinterpret_cast<const float4*>(p.part + (slot_of(cta, k) * kRows + r) * kLatDim + 4 * lane + 128 * j);
         float top = m;
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         const float w = ex2(m - (top == -INFINITY ? 0.f : top));
-        float sum = lane < parts ? w * l : 0.f;
+        float sum = lane < g.w ? w * l : 0.f;
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+        const float w0 = __shfl_sync(kFull, w, 0), w1 = __shfl_sync(kFull, w, 1);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = make_float4(fmaf(w1, x[1][j].x, w0 * x[0][j].x), fmaf(w1, x[1][j].y, w0 * x[0][j].y),
+                                 fmaf(w1, x[1][j].z, w0 * x[0][j].z), fmaf(w1, x[1][j].w, w0 * x[0][j].w));
         #pragma unroll 2
-        for (int k = 0; k < parts; ++k) {
+        for (int k = 2; k < g.w; ++k) {
             const float f = __shfl_sync(kFull, w, k);
             const float* src = p.part + (slot_of(cta, k) * kRows + r) * kLatDim + 4 * lane;
             #pragma unroll
@@ -974,59 +988,59 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LatentAttnPara
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
             odd += acc[j].x + acc[j].y + acc[j].z + acc[j].w;
-            put4(p, x.row, 4 * lane + 128 * j, acc[j], inv);
+            put4(p, row, 4 * lane + 128 * j, acc[j], inv);
         }
-        if (lane == 0 && p.lse_out) p.lse_out[x.row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        // as in a whole unit: a row that is NaN is computed again without the tokens that it does not attend
-        if (x.multi && __any_sync(kFull, odd != odd)) plain_row<FP8>(p, x.b, x.row, x.end);
+        if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (__any_sync(kFull, odd != odd)) join_again<FP8>(p, g, hd, r, row, -1);
     }
-    for (int item = blockIdx.x; item < static_cast<int>(total >> 16); item += gridDim.x) {
+    for (int item = blockIdx.x; item < 4 * static_cast<int>(total >> 16); item += gridDim.x) {
         int r;
-        const int cta = unit_of(item, 16, r), parts = s.start[cta].w;
-        const JoinRow x = join_row(p, s.start[cta], cta, r);
-        if (x.row < 0) continue;
+        const int cta = unit_of(item >> 2, 16, r), quarter = item & 3;
+        const int4 g = s.start[cta];
+        const Heads hd(p, cta % blocks);
+        const int64_t row = place(g, hd, r);
+        if (row < 0) continue;
+        __syncthreads();   // the row before has been read
         float top = -INFINITY;
-        for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_ml[slot_of(cta, k) * 2 * kRows + r]);
+        for (int k = tid; k < g.w; k += kJoinThreads) {
+            const int64_t sl = slot_of(cta, k);
+            const float m = p.part_ml[sl * 2 * kRows + r];
+            s.weight[k] = m;
+            s.len[k] = p.part_ml[(sl * 2 + 1) * kRows + r];
+            top = fmaxf(top, m);
+        }
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const float z = top == -INFINITY ? 0.f : top;
-        float4 acc[4];
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        #pragma unroll 2
-        for (int k = warp; k < parts; k += kJoinWarps) {
-            const int64_t sl = slot_of(cta, k);
-            const float f = ex2(p.part_ml[sl * 2 * kRows + r] - z);
-            sum = fmaf(f, p.part_ml[(sl * 2 + 1) * kRows + r], sum);
-            const float* src = p.part + (sl * kRows + r) * kLatDim + 4 * lane;
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 o = *reinterpret_cast<const float4*>(src + 128 * j);
-                acc[j] = make_float4(fmaf(f, o.x, acc[j].x), fmaf(f, o.y, acc[j].y), fmaf(f, o.z, acc[j].z), fmaf(f, o.w, acc[j].w));
-            }
-        }
-        __syncthreads();   // the row before has been read
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(&s.part[warp][4 * lane + 128 * j]) = acc[j];
-        if (lane == 0) s.sum[warp] = sum;
+        if (lane == 0) s.top[warp] = top;
         __syncthreads();
-        float odd = 0.f;
-        sum = 0.f;
         #pragma unroll
-        for (int k = 0; k < kJoinWarps; ++k) sum += s.sum[k];
-        if (warp < 4) {
+        for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s.top[k]);
+        const float z = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        #pragma unroll 8
+        for (int k = warp; k < g.w; k += kJoinWarps) {
+            const float f = ex2(s.weight[k] - z);
+            const float4 o = *reinterpret_cast<const float4*>(p.part + (slot_of(cta, k) * kRows + r) * kLatDim + quarter * 128 + 4 * lane);
+            acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
+        }
+        *reinterpret_cast<float4*>(&s.part[warp][4 * lane]) = acc;
+        __syncthreads();
+        if (warp == 0) {
+            float sum = 0.f;
+            for (int k = lane; k < g.w; k += 32) sum = fmaf(ex2(s.weight[k] - z), s.len[k], sum);
+            #pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
             #pragma unroll
             for (int k = 0; k < kJoinWarps; ++k) {
-                const float4 o = *reinterpret_cast<const float4*>(&s.part[k][4 * tid]);
+                const float4 o = *reinterpret_cast<const float4*>(&s.part[k][4 * lane]);
                 y = make_float4(y.x + o.x, y.y + o.y, y.z + o.z, y.w + o.w);
             }
-            odd = y.x + y.y + y.z + y.w;
-            put4(p, x.row, 4 * tid, y, sum == 0.f ? 0.f : 1.f / sum);
+            put4(p, row, quarter * 128 + 4 * lane, y, sum == 0.f ? 0.f : 1.f / sum);
+            if (lane == 0 && quarter == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            const float odd = y.x + y.y + y.z + y.w;
+            if (__any_sync(kFull, odd != odd)) join_again<FP8>(p, g, hd, r, row, quarter);
         }
-        if (tid == 0 && p.lse_out) p.lse_out[x.row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        if (__syncthreads_or(odd != odd) && x.multi && warp == 0) plain_row<FP8>(p, x.b, x.row, x.end);
     }
 }
 
