@@ -42,13 +42,13 @@ struct Info {
 };
 
 // What is known of a tile.  8-bit records are loaded by the converters, several tiles behind the producer.
-constexpr int infos_of(bool fp8) { return fp8 ? 8 : kStages; }
+constexpr int infos_of(bool fp8) { return fp8 ? 5 : kStages; }
 
 struct Smem {
     uint8_t k[kStages][kTileBytes];
     uint8_t p[kRows * kTile * 2];
     Info info[infos_of(true)];
-    uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages], s_full, s_free, p_full, q_full, drain;
+    uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages][4], s_full, s_free, p_full, q_full, drain;
     uint32_t tmem;
     volatile int abort;
 };
@@ -350,7 +350,7 @@ __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, Wal
             #pragma unroll 1
             for (int u = 0; ok && u < 8 && t + u < g.t1; ++u, ++n) {
                 const uint32_t at = n % kInfos;
-                if (n >= kInfos) ok = wait_bar(s, FP8 ? &s.free[at] : &s.empty[at], n / kInfos - 1);
+                if (n >= kInfos) ok = wait_bar(s, FP8 ? &s.free[at] : &s.empty[at][0], n / kInfos - 1);   // (a stage's blocks come free in order)
                 if (!ok) break;
                 unsigned long long mask = 0;
                 int block[4], copies = 0;
@@ -375,12 +375,18 @@ __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, Wal
                     } else {
                         if (copies) mbar_arrive_expect_tx(&s.full[at], copies * kRecord);
                         else mbar_arrive(&s.full[at]);
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (block[k] >= 0) bulk_copy(s.k[at] + k * kRecord, p.mem + static_cast<int64_t>(block[k]) * kRecord, kRecord, &s.full[at]);
                     }
                 }
                 __syncwarp();
+                if constexpr (!FP8) {
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k > 0 && n >= kInfos) ok = ok && wait_bar(s, &s.empty[at][k], n / kInfos - 1);
+                        // (a tile begun is copied whole: its barrier counts all its bytes)
+                        if (lane == 0 && block[k] >= 0) bulk_copy(s.k[at] + k * kRecord, p.mem + static_cast<int64_t>(block[k]) * kRecord, kRecord, &s.full[at]);
+                        __syncwarp();
+                    }
+                }
             }
             ids = next;
         }
@@ -438,7 +444,7 @@ __device__ __forceinline__ bool load_raw(Smem& s, const LatentAttnParams& p, Raw
 }
 __device__ __forceinline__ bool store_raw(Smem& s, const Raw& x, uint32_t n, int warp, int lane) {
     const uint32_t st = n % kStages;
-    if (n >= kStages && !wait_bar(s, &s.empty[st], n / kStages - 1)) return false;
+    if (n >= kStages && !wait_bar(s, &s.empty[st][warp >> 1], n / kStages - 1)) return false;
     const int r = lane >> 2, j = lane & 3;
     uint8_t* group = s.k[st] + warp * kGroup + r * 128;
     #pragma unroll
@@ -522,18 +528,19 @@ __device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, Walk 
         for (uint32_t i = 0; ok && i < tiles; ++i) {
             if (i + 1 < tiles) scores(n + i + 1);
             if (!ok) break;
-            const uint32_t st = (n + i) % kStages, op = uniform(k_op + st * kTileBytes), empty = uniform(smem_u32(&s.empty[st]));
+            const uint32_t st = (n + i) % kStages, op = uniform(k_op + st * kTileBytes), empty = uniform(smem_u32(&s.empty[st][0]));
             ok = wait_bar(s, &s.p_full, n + i);
             if (!ok) break;
             tcgen_fence_after();
             if (elect_one()) {
                 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int k = 0; k < 4; ++k) {   // a block at a time, which is free then
                     #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int h = 0; h < 2; ++h)
                         mma_ss(tmem + kHalf + h * 256, desc_k(p_op + k * 32, 1024), desc_n(op + h * 4096 + k * 2 * kGroup), kDescO,
                                i > 0 || k > 0);
-                mma_commit(empty);
+                    mma_commit(empty + 8 * k);
+                }
             }
             __syncwarp();
         }
@@ -542,7 +549,8 @@ __device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, Walk 
     // the last commits arrive in this block's shared memory: it must still be its own
     if (!s.abort)
         for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
-            if (!wait_bar(s, &s.empty[k % kStages], k / kStages)) break;
+            for (int i = 0; i < 4; ++i)
+                if (!wait_bar(s, &s.empty[k % kStages][i], k / kStages)) break;
     if (s.abort) {   // nothing under way in tensor memory
         if (elect_one()) mma_commit(smem_u32(&s.drain));
         __syncwarp();
@@ -715,7 +723,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                 w[2 * k] = pack_bf16(a, b);
                 w[2 * k + 1] = pack_bf16(c, d);
             }
-            if (n > 0) ok = wait_bar(s, &s.empty[(n - 1) % kStages], (n - 1) / kStages);   // P and O are free
+            if (n > 0) ok = wait_bar(s, &s.empty[(n - 1) % kStages][3], (n - 1) / kStages);   // P and O are free
             if (!ok) break;
             if (t > g.t0 && __any_sync(kFull, moved)) {
                 tcgen_fence_after();
@@ -747,7 +755,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
         Segment after;
         more = ok && walk.next(p, after);
         if (more) load_q(s, p, hd, after, mine, warp, lane);
-        if (ok) ok = wait_bar(s, &s.empty[(n - 1) % kStages], (n - 1) / kStages);
+        if (ok) ok = wait_bar(s, &s.empty[(n - 1) % kStages][3], (n - 1) / kStages);
         if (!ok) break;
         tcgen_fence_after();
         const bool whole = g.t0 == 0 && g.t1 == g.tiles;
@@ -827,7 +835,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.ready[i], FP8 ? kConvertWarps : 1);
-            mbar_init(&s.empty[i], 1);
+            for (int k = 0; k < 4; ++k) mbar_init(&s.empty[i][k], 1);
         }
         mbar_init(&s.s_full, 1);
         mbar_init(&s.s_free, 4);
