@@ -58,6 +58,13 @@ class RopeDesc(ctypes.Structure):
                 ("mscale", ctypes.c_float)]
 
 
+class PoolHandle(ctypes.c_void_p):
+    """A pool's handle.  latent: what the latent entry points check their tensors against, which never changes
+    (number of blocks, device); asking the library each time takes a sixth of a short call."""
+
+    latent = None
+
+
 _lib = None
 
 
@@ -256,9 +263,12 @@ def kvd_tier_reassign(num_blocks, host_blocks, tier, block_table, hbm_free, hbm_
 def kvd_pool_create(num_layers, n_kv, num_blocks, kv_dtype, mem, d_h=128, block_size=16, group_size=0):
     """Wrap a caller-owned device tensor (any dtype, pool_bytes long) as a pool; returns the handle (c_void_p)."""
     d = PoolDesc(num_layers, n_kv, d_h, block_size, num_blocks, kv_dtype, group_size)
-    h = ctypes.c_void_p()
+    h = PoolHandle()
     n = mem.numel() * mem.element_size()
     _check("kvd_pool_create", load().kvd_pool_create(ctypes.byref(d), _ptr(mem), n, ctypes.byref(h)))
+    if kv_dtype in (KVD_LATENT_BF16, KVD_LATENT_FP8):
+        desc, _, device = kvd_pool_info(h)
+        h.latent = (desc.num_blocks, device)
     return h
 
 
@@ -539,24 +549,46 @@ def _rows(t, name, width, device):
     """Row stride of a bfloat16 [n][width] tensor, rows contiguous (a slice of a projection's output counts)."""
     import torch
 
-    if t.dim() != 2 or t.shape[1] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be bfloat16 [rows][{width}] on device {device}")
-    if t.stride(1) != 1 and t.numel():
+    row, one = t.stride()
+    if one != 1 and shape[0]:
         raise ValueError(f"{name}: a row's values must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else width
+    return row if shape[0] > 1 else width
 
 
 def _head_rows(t, name, width, device):
     """(token stride, head stride) of a bfloat16 [n][heads][width] tensor, a head's values contiguous."""
     import torch
 
-    if t.dim() != 3 or t.shape[2] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be bfloat16 [rows][heads][{width}] on device {device}")
-    if t.stride(2) != 1 and t.numel():
+    n, h, _ = shape
+    row, head, one = t.stride()
+    if one != 1 and n and h:
         raise ValueError(f"{name}: a head's values must be contiguous")
-    n, h, _ = t.shape
-    head = t.stride(1) if h > 1 else width
-    return t.stride(0) if n > 1 else max(h, 1) * head, head
+    head = head if h > 1 else width
+    return row if n > 1 else max(h, 1) * head, head
+
+
+def _latent_pool(handle):
+    """(blocks, device) of a latent pool."""
+    known = getattr(handle, "latent", None)
+    if known is None:
+        desc, _, device = kvd_pool_info(handle)
+        known = (desc.num_blocks, device)
+    return known
+
+
+def _stream_of(stream, device):
+    """The stream to launch on as an integer: the given one, or the device's current one."""
+    if stream is None:
+        import torch
+
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=None, rope=None, norm_weight=None,
@@ -567,8 +599,7 @@ def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=Non
     import torch
 
     dev = latent.get_device()
-    _, _, pool_dev = kvd_pool_info(handle)
-    _on(dev, pool_dev)
+    _on(dev, _latent_pool(handle)[1])
     n = latent.shape[0]
     ls, ks = _rows(latent, "latent", KVD_LATENT_DIM, dev), _rows(k_rope, "k_rope", KVD_LATENT_ROPE, dev)
     if k_rope.shape[0] != n:
@@ -576,26 +607,29 @@ def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=Non
     _like(slot_mapping, "slot_mapping", torch.int64, (n,), dev)
     if (rope is None) != (positions is None):
         raise ValueError("rope and positions go together")
-    d = None
+    d = pos = norm = None
     if rope is not None:
         _like(positions, "positions", torch.int32, (n,), dev)
         if rope.turns.get_device() != dev:
             raise ValueError(f"rope must be on device {dev}")
+        pos = positions.data_ptr()
         d = RopeDesc(rope.turns.data_ptr(), rope.rot_dim, 1 if rope.interleaved else 0, rope.mscale)
     if norm_weight is not None:
         _like(norm_weight, "norm_weight", torch.bfloat16, (KVD_LATENT_DIM,), dev)
+        norm = norm_weight.data_ptr()
     n_q = qs = qh = os_ = oh = 0
+    src = dst = None
     if q_rope is not None:
         q_rope_out = q_rope if q_rope_out is None else q_rope_out
         if q_rope.shape[0] != n or q_rope_out.shape != q_rope.shape:
             raise ValueError("q_rope and q_rope_out must have latent's rows")
         n_q = q_rope.shape[1]
         qs, qh = _head_rows(q_rope, "q_rope", KVD_LATENT_ROPE, dev)
-        os_, oh = _head_rows(q_rope_out, "q_rope_out", KVD_LATENT_ROPE, dev)
+        os_, oh = (qs, qh) if q_rope_out is q_rope else _head_rows(q_rope_out, "q_rope_out", KVD_LATENT_ROPE, dev)
+        src, dst = q_rope.data_ptr(), q_rope_out.data_ptr()
     status = load().kvd_latent_append(
-        handle, int(layer), latent.data_ptr(), ls, k_rope.data_ptr(), ks, _ptr(norm_weight), float(norm_eps),
-        0 if q_rope is None else q_rope.data_ptr(), qs, qh, n_q, _ptr(positions), d, slot_mapping.data_ptr(), n,
-        0 if q_rope is None else q_rope_out.data_ptr(), os_, oh, _stream(stream))
+        handle, layer, latent.data_ptr(), ls, k_rope.data_ptr(), ks, norm, norm_eps, src, qs, qh, n_q, pos, d,
+        slot_mapping.data_ptr(), n, dst, os_, oh, _stream_of(stream, dev))
     if status != KVD_OK:
         _check("kvd_latent_append", status)
 
@@ -605,17 +639,18 @@ def kvd_latent_gather(handle, layer, block_table, row_start, out, first=None, st
     import torch
 
     dev = out.get_device()
-    _, _, pool_dev = kvd_pool_info(handle)
-    _on(dev, pool_dev)
+    _on(dev, _latent_pool(handle)[1])
     stride = _rows(out, "out", KVD_LATENT_DIM + KVD_LATENT_ROPE, dev)
     batch, mb = block_table.shape
     _like(block_table, "block_table", torch.int32, (batch, mb), dev)
     _like(row_start, "row_start", torch.int32, (batch + 1,), dev)
     if first is not None:
         _like(first, "first", torch.int32, (batch,), dev)
-    _check("kvd_latent_gather", load().kvd_latent_gather(
-        handle, int(layer), _ptr(block_table), mb, _ptr(row_start), _ptr(first), batch, out.shape[0], _ptr(out), stride,
-        _stream(stream)))
+    status = load().kvd_latent_gather(handle, layer, block_table.data_ptr(), mb, row_start.data_ptr(),
+                                      None if first is None else first.data_ptr(), batch, out.shape[0], out.data_ptr(),
+                                      stride, _stream_of(stream, dev))
+    if status != KVD_OK:
+        _check("kvd_latent_gather", status)
 
 
 def kvd_latent_workspace_bytes(handle, n_q, batch):
@@ -633,26 +668,29 @@ def kvd_latent_attn(handle, layer, q, q_start, block_table, seq_lens, workspace,
 
     n, n_q, _ = q.shape
     dev = q.get_device()
-    desc, _, pool_dev = kvd_pool_info(handle)
+    blocks, pool_dev = _latent_pool(handle)
     _on(dev, pool_dev)
     _like(q, "q", torch.bfloat16, (n, n_q, KVD_LATENT_DIM + KVD_LATENT_ROPE), dev)
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    dtype = out.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("out must be bfloat16 or float32")
-    _like(out, "out", out.dtype, (n, n_q, KVD_LATENT_DIM), dev)
-    _mask(retain_mask, desc.num_blocks, dev)
+    _like(out, "out", dtype, (n, n_q, KVD_LATENT_DIM), dev)
+    _mask(retain_mask, blocks, dev)
     _scratch(workspace, dev)
-    batch = seq_lens.shape[0]
+    batch, mb = block_table.shape
     _like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
     _like(q_start, "q_start", torch.int32, (batch + 1,), dev)
-    _like(block_table, "block_table", torch.int32, (batch, block_table.shape[1]), dev)
+    _like(block_table, "block_table", torch.int32, (batch, mb), dev)
     if lse_out is not None:
         _like(lse_out, "lse_out", torch.float32, (n, n_q), dev)
-    if softmax_scale is None:
-        softmax_scale = (128 + KVD_LATENT_ROPE) ** -0.5
-    _check("kvd_latent_attn", load().kvd_latent_attn(
-        handle, int(layer), _ptr(q), n_q, _ptr(q_start), n, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-        batch, _ptr(retain_mask), float(softmax_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _ptr(out), KVD_F32 if out.dtype == torch.float32 else KVD_BF16, _ptr(lse_out), _stream(stream)))
+    status = load().kvd_latent_attn(
+        handle, layer, q.data_ptr(), n_q, q_start.data_ptr(), n, block_table.data_ptr(), mb, seq_lens.data_ptr(), batch,
+        None if retain_mask is None else retain_mask.data_ptr(),
+        (128 + KVD_LATENT_ROPE) ** -0.5 if softmax_scale is None else softmax_scale, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), out.data_ptr(), KVD_F32 if dtype is torch.float32 else KVD_BF16,
+        None if lse_out is None else lse_out.data_ptr(), _stream_of(stream, dev))
+    if status != KVD_OK:
+        _check("kvd_latent_attn", status)
 
 
 def kvd_latent_prefill(handle, q, q_start, k_nope, v, k_rope, kv_start, out, causal=True, softmax_scale=None,
@@ -664,12 +702,12 @@ def kvd_latent_prefill(handle, q, q_start, k_nope, v, k_rope, kv_start, out, cau
 
     n, n_q, _ = q.shape
     dev = q.get_device()
-    _, _, pool_dev = kvd_pool_info(handle)
-    _on(dev, pool_dev)
+    _on(dev, _latent_pool(handle)[1])
     _like(q, "q", torch.bfloat16, (n, n_q, 128 + KVD_LATENT_ROPE), dev)
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    dtype = out.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("out must be bfloat16 or float32")
-    _like(out, "out", out.dtype, (n, n_q, 128), dev)
+    _like(out, "out", dtype, (n, n_q, 128), dev)
     m = k_rope.shape[0]
     if k_nope.shape[:2] != (m, n_q) or v.shape[:2] != (m, n_q):
         raise ValueError("k_nope and v must have k_rope's rows and q's heads")
@@ -681,9 +719,11 @@ def kvd_latent_prefill(handle, q, q_start, k_nope, v, k_rope, kv_start, out, cau
     _like(kv_start, "kv_start", torch.int32, (batch + 1,), dev)
     if lse_out is not None:
         _like(lse_out, "lse_out", torch.float32, (n, n_q), dev)
-    if softmax_scale is None:
-        softmax_scale = (128 + KVD_LATENT_ROPE) ** -0.5
-    _check("kvd_latent_prefill", load().kvd_latent_prefill(
-        handle, _ptr(q), n_q, _ptr(q_start), n, _ptr(k_nope), ks, kh, _ptr(v), vs, vh, _ptr(k_rope), rs, _ptr(kv_start), m,
-        batch, 1 if causal else 0, float(softmax_scale), _ptr(out), KVD_F32 if out.dtype == torch.float32 else KVD_BF16,
-        _ptr(lse_out), _stream(stream)))
+    status = load().kvd_latent_prefill(
+        handle, q.data_ptr(), n_q, q_start.data_ptr(), n, k_nope.data_ptr(), ks, kh, v.data_ptr(), vs, vh, k_rope.data_ptr(), rs,
+        kv_start.data_ptr(), m, batch, 1 if causal else 0,
+        (128 + KVD_LATENT_ROPE) ** -0.5 if softmax_scale is None else softmax_scale, out.data_ptr(),
+        KVD_F32 if dtype is torch.float32 else KVD_BF16, None if lse_out is None else lse_out.data_ptr(),
+        _stream_of(stream, dev))
+    if status != KVD_OK:
+        _check("kvd_latent_prefill", status)

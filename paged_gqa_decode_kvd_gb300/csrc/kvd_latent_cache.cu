@@ -120,12 +120,20 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendPara
     if (query) {
         const int h0 = static_cast<int>((task - p.n_tokens) % groups) * p.heads, h1 = min(h0 + p.heads, p.n_q);
         lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane8);
-        for (int h = h0 + (lane >> 3); h - (lane >> 3) < h1; h += 4) {
-            const bool on = h < h1;
-            const uint16_t* row = p.q_rope + n * p.q_stride + h * p.q_head;
-            const uint4 x = on ? ld16(row + lane8 * 8) : make_uint4(0, 0, 0, 0);
-            const uint4 y = rotate8<INTERLEAVED>(x, f, p.rot, lane8, row, on);
-            if (on) st16(p.q_out + n * p.out_stride + h * p.out_head + lane8 * 8, y);
+        const uint16_t* src = p.q_rope + n * p.q_stride;
+        uint16_t* dst = p.q_out + n * p.out_stride;
+        #pragma unroll 1
+        for (int h = h0 + (lane >> 3); h - (lane >> 3) < h1; h += 16) {
+            uint4 x[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = h + 4 * i < h1 ? ld16(src + (h + 4 * i) * p.q_head + lane8 * 8) : make_uint4(0, 0, 0, 0);
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (h + 4 * i - (lane >> 3) >= h1) break;
+                const bool on = h + 4 * i < h1;
+                const uint4 y = rotate8<INTERLEAVED>(x[i], f, p.rot, lane8, src + (h + 4 * i) * p.q_head, on);
+                if (on) st16(dst + (h + 4 * i) * p.out_head + lane8 * 8, y);
+            }
         }
         return;
     }
@@ -183,49 +191,112 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendPara
     }
 }
 
-// A warp a row; the rows of request b by the CTAs of column b.
+// Rows in chunks of 32, four a warp with all their loads under way; a CTA takes every gridDim-th chunk of all requests.
+constexpr int kChunkRows = 32, kWarpRows = 4;
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherParams p) {
+__global__ void __launch_bounds__(kThreads, 4) gather_kernel(const LatentGatherParams p) {
+    __shared__ int chunks[kMaxBatch];   // up to and with the request
+    __shared__ int warp_sum[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int64_t r0 = p.row_start[b], r1 = p.row_start[b + 1];
-    const int64_t first = p.first ? p.first[b] : 0;
-    if (r0 < 0 || r1 < r0 || r1 > p.n_rows || first < 0 || first + (r1 - r0) > static_cast<int64_t>(p.max_blocks) * kBs) {
-        if (threadIdx.x == 0) report(p.err, KVD_ERR_OOB);
-        return;
-    }
-    for (int64_t r = r0 + static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < r1;
-         r += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
-        const int64_t pos = first + (r - r0);
-        const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
-        const int t = static_cast<int>(pos % kBs);
-        if (block < 0 || block >= p.num_blocks) {
-            if (lane == 0) report(p.err, KVD_ERR_OOB);
-            continue;
-        }
-        const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
-        uint16_t* out = p.out + r * p.out_stride;
-        if constexpr (FP8) {
-            const float s = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
-            #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
-                uint32_t h[4], o[4];
-                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
-                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 v = unpack_f16(h[k]);
-                    o[k] = pack_bf16(v.x * s, v.y * s);
-                }
-                st16(out + (lane + 32 * i) * 8, make_uint4(o[0], o[1], o[2], o[3]));
+    int before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        int up = 0;
+        if (b < p.B) {
+            const int64_t r0 = p.row_start[b], r1 = p.row_start[b + 1], first = p.first ? p.first[b] : 0;
+            if (r0 < 0 || r1 < r0 || r1 > p.n_rows || first < 0 || first + (r1 - r0) > static_cast<int64_t>(p.max_blocks) * kBs) {
+                if (blockIdx.x == 0) report(p.err, KVD_ERR_OOB);
+            } else {
+                up = static_cast<int>((r1 - r0 + kChunkRows - 1) / kChunkRows);
             }
-            if (lane < 8) st16(out + kLatDim + lane * 8, ld16(record + latent_rope_piece(t, lane)));
-        } else {
+        }
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, up, o);
+            if (lane >= o) up += v;
+        }
+        if (lane == 31) warp_sum[warp] = up;
+        __syncthreads();
+        int all = before;
+        #pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) up += warp_sum[w];
+            all += warp_sum[w];
+        }
+        if (b < p.B) chunks[b] = before + up;
+        before = all;
+        __syncthreads();
+    }
+    for (int c = blockIdx.x; c < before; c += gridDim.x) {
+        int b = 0, z = p.B - 1;
+        while (b < z) {   // the first request with more than c chunks up to it
+            const int mid = (b + z) >> 1;
+            if (chunks[mid] > c) z = mid;
+            else b = mid + 1;
+        }
+        const int64_t r0 = p.row_start[b], r1 = p.row_start[b + 1], first = p.first ? p.first[b] : 0;
+        const int64_t row = r0 + static_cast<int64_t>(c - (b > 0 ? chunks[b - 1] : 0)) * kChunkRows + warp * kWarpRows;
+        const uint8_t* record[kWarpRows];
+        int t[kWarpRows];
+        #pragma unroll
+        for (int i = 0; i < kWarpRows; ++i) {
+            record[i] = nullptr;
+            const int64_t pos = first + (row + i - r0);
+            t[i] = static_cast<int>(pos % kBs);
+            if (row + i >= r1) continue;
+            const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+            if (block >= 0 && block < p.num_blocks) record[i] = p.mem + block * latent_record_bytes(FP8);
+            else if (lane == 0) report(p.err, KVD_ERR_OOB);
+        }
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        uint4 rope[kWarpRows];
+        if constexpr (FP8) {
+            uint2 code[kWarpRows][2];
+            float s[kWarpRows];
             #pragma unroll
-            for (int i = 0; i < 2; ++i) st16(out + (lane + 32 * i) * 8, ld16(record + latent_piece(t, lane + 32 * i)));
-            if (lane < 8) st16(out + kLatDim + lane * 8, ld16(record + latent_piece(t, 64 + lane)));
+            for (int i = 0; i < kWarpRows; ++i) {
+                #pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    code[i][k] = record[i] ? *reinterpret_cast<const uint2*>(record[i] + latent_code(t[i], lane + 32 * k)) : make_uint2(0, 0);
+                s[i] = record[i] ? *reinterpret_cast<const float*>(record[i] + kLatScales + 4 * t[i]) : 0.f;
+                rope[i] = record[i] && lane < 8 ? ld16(record[i] + latent_rope_piece(t[i], lane)) : none;
+            }
+            #pragma unroll
+            for (int i = 0; i < kWarpRows; ++i) {
+                if (!record[i]) continue;
+                uint16_t* out = p.out + (row + i) * p.out_stride;
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t h[4], o[4];
+                    e4m3x4_to_f16x2x2(code[i][k].x, h[0], h[1]);
+                    e4m3x4_to_f16x2x2(code[i][k].y, h[2], h[3]);
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = unpack_f16(h[j]);
+                        o[j] = pack_bf16(v.x * s[i], v.y * s[i]);
+                    }
+                    st16(out + (lane + 32 * k) * 8, make_uint4(o[0], o[1], o[2], o[3]));
+                }
+                if (lane < 8) st16(out + kLatDim + lane * 8, rope[i]);
+            }
+        } else {
+            uint4 x[kWarpRows][2];
+            #pragma unroll
+            for (int i = 0; i < kWarpRows; ++i) {
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) x[i][k] = record[i] ? ld16(record[i] + latent_piece(t[i], lane + 32 * k)) : none;
+                rope[i] = record[i] && lane < 8 ? ld16(record[i] + latent_piece(t[i], 64 + lane)) : none;
+            }
+            #pragma unroll
+            for (int i = 0; i < kWarpRows; ++i) {
+                if (!record[i]) continue;
+                uint16_t* out = p.out + (row + i) * p.out_stride;
+                #pragma unroll
+                for (int k = 0; k < 2; ++k) st16(out + (lane + 32 * k) * 8, x[i][k]);
+                if (lane < 8) st16(out + kLatDim + lane * 8, rope[i]);
+            }
         }
     }
 }
@@ -233,7 +304,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const LatentGatherPara
 }  // namespace
 
 cudaError_t launch_latent_append(LatentAppendParams p, bool fp8, int num_sms, cudaStream_t stream) {
-    p.heads = 4;
+    // A warp makes a token's cos and sin for its heads: 32 of them where that leaves four warps a scheduler.
+    p.heads = p.n_tokens * ((p.n_q + 31) / 32) >= 16 * num_sms ? 32 : 4;
     const int64_t tasks = p.n_tokens * (1 + (p.n_q + p.heads - 1) / p.heads);
     const dim3 grid(static_cast<unsigned>((tasks + kThreads / 32 - 1) / (kThreads / 32)));
     auto* kernel = fp8 ? (p.interleaved ? append_kernel<true, true> : append_kernel<true, false>)
@@ -242,8 +314,8 @@ cudaError_t launch_latent_append(LatentAppendParams p, bool fp8, int num_sms, cu
 }
 
 cudaError_t launch_latent_gather(const LatentGatherParams& p, bool fp8, int num_sms, cudaStream_t stream) {
-    const int64_t most = (p.n_rows + kThreads / 32 - 1) / (kThreads / 32), share = (16 * num_sms + p.B - 1) / p.B;
-    const dim3 grid(static_cast<unsigned>(most < share ? most : share), static_cast<unsigned>(p.B));
+    const int64_t most = p.n_rows / kChunkRows + p.B, full = 4 * num_sms;
+    const dim3 grid(static_cast<unsigned>(most < full ? most : full));
     return launch_dependent(fp8 ? gather_kernel<true> : gather_kernel<false>, grid, dim3(kThreads), 0, -1, stream, p);
 }
 
