@@ -13,7 +13,7 @@ constexpr int kRows = kLatUnitRows;
 constexpr int kStages = 3;
 constexpr int kTileBytes = kTile * kLatKey * 2;
 constexpr int kGroup = 9216;           // bytes of eight tokens of a tile
-constexpr int kProducerWarp = 4, kIssueWarp = 5, kFixWarp = 6, kConvertWarp = 8, kConvertWarps = 8;
+constexpr int kProducerWarp = 4, kScoreWarp = 5, kFixWarp = 6, kValueWarp = 7, kConvertWarp = 8, kConvertWarps = 8;
 constexpr int threads_of(bool fp8) { return fp8 ? 32 * (kConvertWarp + kConvertWarps) : 256; }
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so
@@ -48,7 +48,7 @@ struct Smem {
     uint8_t k[kStages][kTileBytes];
     uint8_t p[kRows * kTile * 2];
     Info info[infos_of(true)];
-    uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages][4], s_full, s_free, p_full, q_full, drain;
+    uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages][4], s_full, s_free, p_full, q_full, drain[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -496,40 +496,60 @@ __device__ __forceinline__ uint64_t desc_n(uint32_t addr) {
     return static_cast<uint64_t>(addr >> 4) | (64ull << 16) | (static_cast<uint64_t>(kGroup >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// Nothing under way in tensor memory when a warp that issued leaves.
+__device__ __forceinline__ void drain_mma(Smem& s, int i) {
+    const uint32_t bar = uniform(smem_u32(&s.drain[i]));
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+    mbar_wait(&s.drain[i], 0, nullptr, kWaitNs);
+}
+
+// A warp for each product: what stands between two runs of MMAs (waits, commits) would leave the tensor cores idle if one
+// warp had both.  S(t) = Q·K(t)ᵀ, when S(t − 1) has been read:
 template <bool FP8>
-__device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, Walk walk) {
-    constexpr uint32_t kDescS = mma_desc_bf16(64, kTile), kDescO = mma_desc_bf16(64, 256) | (1u << 16);
-    const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), p_op = uniform(smem_u32(s.p));
-    const uint32_t s_full = uniform(smem_u32(&s.s_full));
+__device__ __forceinline__ void score_issuer(Smem& s, const LatentAttnParams& p, Walk walk) {
+    constexpr uint32_t kDescS = mma_desc_bf16(64, kTile);
+    const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), s_full = uniform(smem_u32(&s.s_full));
     Segment g;
-    uint32_t n = 0, segs = 0;   // tiles before
+    uint32_t n = 0, segs = 0;
     bool ok = true;
-    auto scores = [&](uint32_t i) {   // S(i) = Q·K(i)ᵀ
-        const uint32_t st = i % kStages, op = uniform(k_op + st * kTileBytes);
-        ok = wait_bar(s, &s.ready[st], i / kStages) && (i == 0 || wait_bar(s, &s.s_free, i - 1));
-        if (!ok) return;
-        tcgen_fence_after();
-        if (elect_one()) {
-            #pragma unroll
-            for (int c = 0; c < 9; ++c)
-                #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ts(tmem + (FP8 && c == 8 ? kColR : kColS), tmem + kColQ + c * 32 + k * 8, desc_k(op + c * 1024 + k * 32, kGroup),
-                           kDescS, (FP8 && c == 8 ? k : (c | k)) != 0);
-            mma_commit(s_full);
-        }
-        __syncwarp();
-    };
     while (ok && walk.next(p, g)) {
-        const uint32_t tiles = uniform(g.t1 - g.t0);
+        const uint32_t end = uniform(n + g.t1 - g.t0);
         ok = wait_bar(s, &s.q_full, segs++);
-        if (ok) scores(n);
         #pragma unroll 1
-        for (uint32_t i = 0; ok && i < tiles; ++i) {
-            if (i + 1 < tiles) scores(n + i + 1);
+        for (; ok && n < end; ++n) {
+            const uint32_t st = n % kStages, op = uniform(k_op + st * kTileBytes);
+            ok = wait_bar(s, &s.ready[st], n / kStages) && (n == 0 || wait_bar(s, &s.s_free, n - 1));
             if (!ok) break;
-            const uint32_t st = (n + i) % kStages, op = uniform(k_op + st * kTileBytes), empty = uniform(smem_u32(&s.empty[st][0]));
-            ok = wait_bar(s, &s.p_full, n + i);
+            tcgen_fence_after();
+            if (elect_one()) {
+                #pragma unroll
+                for (int c = 0; c < 9; ++c)
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tmem + (FP8 && c == 8 ? kColR : kColS), tmem + kColQ + c * 32 + k * 8, desc_k(op + c * 1024 + k * 32, kGroup),
+                               kDescS, (FP8 && c == 8 ? k : (c | k)) != 0);
+                mma_commit(s_full);
+            }
+            __syncwarp();
+        }
+    }
+    drain_mma(s, 0);
+}
+// O += P(t)·C(t):
+__device__ __forceinline__ void value_issuer(Smem& s, const LatentAttnParams& p, Walk walk) {
+    constexpr uint32_t kDescO = mma_desc_bf16(64, 256) | (1u << 16);
+    const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), p_op = uniform(smem_u32(s.p));
+    Segment g;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(p, g)) {
+        const uint32_t first = uniform(n), end = uniform(n + g.t1 - g.t0);
+        #pragma unroll 1
+        for (; ok && n < end; ++n) {
+            const uint32_t st = n % kStages, op = uniform(k_op + st * kTileBytes), empty = uniform(smem_u32(&s.empty[st][0]));
+            const uint32_t add = uniform(n > first);
+            ok = wait_bar(s, &s.p_full, n);
             if (!ok) break;
             tcgen_fence_after();
             if (elect_one()) {
@@ -538,24 +558,19 @@ __device__ __forceinline__ void issuer(Smem& s, const LatentAttnParams& p, Walk 
                     #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         mma_ss(tmem + kHalf + h * 256, desc_k(p_op + k * 32, 1024), desc_n(op + h * 4096 + k * 2 * kGroup), kDescO,
-                               i > 0 || k > 0);
+                               k > 0 ? 1u : add);
                     mma_commit(empty + 8 * k);
                 }
             }
             __syncwarp();
         }
-        n += tiles;
     }
+    drain_mma(s, 1);
     // the last commits arrive in this block's shared memory: it must still be its own
     if (!s.abort)
         for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
             for (int i = 0; i < 4; ++i)
-                if (!wait_bar(s, &s.empty[k % kStages][i], k / kStages)) break;
-    if (s.abort) {   // nothing under way in tensor memory
-        if (elect_one()) mma_commit(smem_u32(&s.drain));
-        __syncwarp();
-        mbar_wait(&s.drain, 0, nullptr, kWaitNs);
-    }
+                if (!wait_bar(s, &s.empty[k % kStages][i], k / kStages)) return;
 }
 
 // ------------------------------------------------------------------- softmax
@@ -827,7 +842,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem& s = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == kIssueWarp) tmem_alloc_all(&s.tmem);
+    if (warp == kScoreWarp) tmem_alloc_all(&s.tmem);
     if (tid == 0) {
         for (int i = 0; i < infos_of(FP8); ++i) {
             mbar_init(&s.full[i], 1);
@@ -841,7 +856,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
         mbar_init(&s.s_free, 4);
         mbar_init(&s.p_full, 4);
         mbar_init(&s.q_full, 4);
-        mbar_init(&s.drain, 1);
+        mbar_init(&s.drain[0], 1);
+        mbar_init(&s.drain[1], 1);
         mbar_fence_init();
         s.abort = 0;
     }
@@ -869,7 +885,8 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     } else if (warp < kConvertWarp) {
         if (FP8) give_registers<72>();
         if (warp == kProducerWarp) producer<FP8>(s, p, walk, lane);
-        else if (warp == kIssueWarp) issuer<FP8>(s, p, walk);
+        else if (warp == kScoreWarp) score_issuer<FP8>(s, p, walk);
+        else if (warp == kValueWarp) value_issuer(s, p, walk);
         else if (!FP8 && warp == kFixWarp) fixer(s, p, walk, lane);
     } else if constexpr (FP8) {
         give_registers<120>();
@@ -879,7 +896,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
-    if (warp == kIssueWarp) {
+    if (warp == kScoreWarp) {
         if (lane == 0 && s.abort) report(p.err, KVD_ERR_TIMEOUT);
         tmem_free_all(s.tmem);
     }

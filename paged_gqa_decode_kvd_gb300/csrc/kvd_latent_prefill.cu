@@ -16,8 +16,8 @@ constexpr int kRows = 128;             // rows of a softmax warpgroup: one MMA
 constexpr int kPieces = 8, kPieceBytes = 16384, kTilePieces = 5;   // K: three times 64 dims of 128 keys; V: twice 64 keys
 constexpr int kChunk = kRows * 128;    // 64 dims of Q's rows
 constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8, kIssueWarp = 9;
-constexpr int kReaders = 9;            // warps that read a unit's description
+constexpr int kProducerWarp = 8, kIssueWarp = 9;   // the issuers are two
+constexpr int kReaders = 10;           // warps that read a unit's description
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
@@ -28,13 +28,14 @@ struct Unit {
     int tok0;                          // first token
     int tiles[2];                      // of the warpgroups' rows (−1: no rows)
     int end;                           // keys that the last row attends
+    uint32_t turn[2];                  // of Q of each warpgroup
 };
 
 struct Smem {
     uint8_t q[2][3 * kChunk];
     uint8_t piece[kPieces][kPieceBytes];
     Unit unit[2];
-    uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2], drain;
+    uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2], drain[2];
     uint32_t tmem;
     volatile int abort;
 };
@@ -195,6 +196,8 @@ __device__ __forceinline__ void producer(Smem& s, const LatentPrefillParams& p, 
         if (!ok) break;
         if (lane == 0) {
             if (!more) x.b = -1;
+            x.turn[0] = done[0];
+            x.turn[1] = done[1];
             s.unit[at] = x;
             mbar_arrive(&s.u_full[at]);
         }
@@ -260,86 +263,88 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
     return static_cast<uint64_t>(addr >> 4) | (static_cast<uint64_t>(kPieceBytes / 2 >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void issuer(Smem& s, int lane) {
+// A warp for each softmax warpgroup: O(t) += P(t)·V(t), then S(t + 1) = Q·K(t + 1)ᵀ over the P that has been read.  One warp for
+// both left the tensor cores idle for half of the time: what stands between two runs of MMAs (waits, descriptors, commits)
+// takes 500 to 700 cycles, a run 520 or 780, and few MMAs are taken ahead.
+// Every operand is a value that all lanes have, and known as one: an instruction then issues in its own time.
+__device__ __forceinline__ void issuer(Smem& s, int w, int lane) {
     constexpr uint32_t kDescS = mma_desc_bf16(kRows, kTile), kDescO = mma_desc_bf16(kRows, kExpVal) | (1u << 16);
-    const uint32_t tmem = uniform(s.tmem), q_op = uniform(smem_u32(s.q)), p_op = uniform(smem_u32(s.piece));
+    const uint32_t W = uniform(w), tmem = uniform(s.tmem), p_op = uniform(smem_u32(s.piece));
+    const uint32_t q_op = uniform(smem_u32(s.q) + W * 3 * kChunk), col_s = uniform(tmem + kColS + W * kTile), col_o = uniform(tmem + kColO + W * kExpVal);
     Unit x;
-    uint32_t n = 0, unit[2] = {0, 0}, step[2] = {0, 0};
+    uint32_t n = 0, units = 0, steps = 0;
     bool ok = true;
-    auto scores = [&](uint32_t w, uint32_t t) {   // S of warpgroup w, the CTA's tile t
-        #pragma unroll 1
-        for (uint32_t c = 0; ok && c < 3; ++c) {
-            const uint32_t piece = t * kTilePieces + c, at = piece % kPieces;
-            const uint32_t a = uniform(q_op + (w * 3 + c) * kChunk), b = uniform(p_op + at * kPieceBytes), d = uniform(tmem + kColS + w * kTile);
-            ok = wait_bar(s, &s.full[at], piece / kPieces);
+    auto place = [&](uint32_t piece) { return uniform(p_op + piece % kPieces * kPieceBytes); };
+    auto barrier = [&](uint32_t piece) { return uniform(smem_u32(&s.empty[piece % kPieces])); };
+    auto wait_piece = [&](uint32_t piece) { return wait_bar(s, &s.full[piece % kPieces], piece / kPieces); };
+    auto commit = [&](uint64_t* bar) {
+        const uint32_t b = uniform(smem_u32(bar));
+        if (elect_one()) mma_commit(b);
+        __syncwarp();
+    };
+    const uint32_t s_full = uniform(smem_u32(&s.s_full[W]));
+    auto scores = [&](uint32_t t, bool last) {   // the CTA's tile t; `last` of the unit's: Q has been read
+        const uint32_t piece = t * kTilePieces;
+        const uint32_t b[3] = {place(piece), place(piece + 1), place(piece + 2)};
+        const uint32_t e[3] = {barrier(piece), barrier(piece + 1), barrier(piece + 2)};
+        #pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            ok = wait_piece(piece + c);
             if (!ok) return;
             tcgen_fence_after();
             if (elect_one()) {
                 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ss(d, smem_desc_sw128(a + k * 32), smem_desc_sw128(b + k * 32), kDescS, c > 0 || k > 0);
+                    mma_ss(col_s, smem_desc_sw128(q_op + c * kChunk + k * 32), smem_desc_sw128(b[c] + k * 32), kDescS, (c | k) != 0);
+                if (c == 2) mma_commit(s_full);
+                mma_commit(e[c]);
             }
             __syncwarp();
         }
+        if (last) commit(&s.q_empty[W]);
     };
-    auto release = [&](uint32_t t, int k0, int k1) {   // pieces of a tile, once all that was issued so far is done
-        if (elect_one())
-            for (int k = k0; k < k1; ++k) mma_commit(smem_u32(&s.empty[(t * kTilePieces + k) % kPieces]));
-        __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-        if (elect_one()) mma_commit(smem_u32(bar));
-        __syncwarp();
-    };
-    for (uint32_t i = 0; ok && next_unit(s, i, x, lane); ++i) {
-        const int tiles = max(x.tiles[0], x.tiles[1]);
-        if (tiles <= 0) continue;
+    while (ok && next_unit(s, units, x, lane)) {
+        const uint32_t mine = uniform(max(x.tiles[W], 0)), tiles = uniform(max(max(x.tiles[0], x.tiles[1]), 0));
+        if (mine > 0) {
+            ok = wait_bar(s, &s.q_full[W], x.turn[W]);
+            if (ok) scores(n, mine == 1);
+        }
         #pragma unroll 1
-        for (int t = -1; ok && t < tiles; ++t) {
-            // O(t) of a warpgroup, then its S(t + 1): the other one's softmax runs meanwhile
-            #pragma unroll 1
-            for (int w = 0; ok && w < 2; ++w) {
-                if (t >= 0 && t < x.tiles[w]) {
-                    ok = wait_bar(s, &s.p_full[w], step[w]++);
-                    const uint32_t d = uniform(tmem + kColO + w * kExpVal), a = uniform(tmem + kColS + w * kTile);
-                    #pragma unroll 1
-                    for (uint32_t half = 0; ok && half < 2; ++half) {
-                        const uint32_t piece = (n + t) * kTilePieces + 3 + half, at = piece % kPieces;
-                        const uint32_t b = uniform(p_op + at * kPieceBytes);
-                        ok = wait_bar(s, &s.full[at], piece / kPieces);
-                        if (!ok) break;
-                        tcgen_fence_after();
-                        if (elect_one()) {
-                            #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_ts(d, a + (half * 4 + k) * 8, desc_v(b + k * 2048), kDescO, t > 0 || half > 0 || k > 0);
-                        }
-                        __syncwarp();
-                    }
-                    if (ok && t == x.tiles[w] - 1) commit(&s.o_full[w]);
+        for (uint32_t t = 0; ok && t < mine; ++t) {
+            const uint32_t piece = (n + t) * kTilePieces + 3;
+            const uint32_t b[2] = {place(piece), place(piece + 1)}, e[2] = {barrier(piece), barrier(piece + 1)}, add = uniform(t > 0);
+            ok = wait_bar(s, &s.p_full[W], steps++);
+            #pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                ok = ok && wait_piece(piece + half);
+                if (!ok) break;
+                tcgen_fence_after();
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(col_o, col_s + (half * 4 + k) * 8, desc_v(b[half] + k * 2048), kDescO, half > 0 || k > 0 ? 1u : add);
+                    mma_commit(e[half]);
                 }
-                if (ok && t >= 0 && w == 1) release(n + t, 3, 5);
-                if (ok && t + 1 < x.tiles[w]) {
-                    if (t < 0) ok = wait_bar(s, &s.q_full[w], unit[w]++);
-                    if (ok) scores(w, n + t + 1);
-                    if (ok) commit(&s.s_full[w]);
-                    if (ok && t + 2 == x.tiles[w]) commit(&s.q_empty[w]);
-                }
-                if (ok && t + 1 < tiles && w == 1) release(n + t + 1, 0, 3);
+                __syncwarp();
             }
+            if (!ok) break;
+            if (t + 1 < mine) scores(n + t + 1, t + 2 == mine);
+            else commit(&s.o_full[W]);
+        }
+        for (uint32_t k = (n + mine) * kTilePieces; ok && k < (n + tiles) * kTilePieces; ++k) {   // of the other warpgroup's rows alone
+            ok = wait_piece(k);
+            if (ok && lane == 0) mbar_arrive(&s.empty[k % kPieces]);
+            __syncwarp();
         }
         n += tiles;
+        ++units;
     }
     // the last commits arrive in this block's shared memory, and nothing is under way in tensor memory
-    commit(&s.drain);
-    mbar_wait(&s.drain, 0, nullptr, kWaitNs);
-    if (!s.abort) {
-        const uint32_t pieces = n * kTilePieces;
-        for (uint32_t k = pieces > kPieces ? pieces - kPieces : 0; k < pieces; ++k)
+    commit(&s.drain[W]);
+    mbar_wait(&s.drain[W], 0, nullptr, kWaitNs);
+    if (!s.abort)
+        for (uint32_t k = n * kTilePieces > kPieces ? n * kTilePieces - kPieces : 0; k < n * kTilePieces; ++k)
             if (!wait_bar(s, &s.empty[k % kPieces], k / kPieces)) break;
-        for (int w = 0; w < 2; ++w)
-            if (unit[w]) wait_bar(s, &s.q_empty[w], unit[w] - 1);
-    }
 }
 
 // ------------------------------------------------------------------- softmax
@@ -499,9 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
     if (tid == 0) {
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.drain[i], 1);
             mbar_init(&s.q_full[i], 1);
             mbar_init(&s.q_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
@@ -510,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
             mbar_init(&s.u_full[i], 1);
             mbar_init(&s.u_empty[i], kReaders);
         }
-        mbar_init(&s.drain, 1);
         mbar_fence_init();
         s.abort = 0;
     }
@@ -530,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
         } else {
             give_registers<80>();
             if (warp == kProducerWarp) producer(s, p, m, lane);
-            else if (warp == kIssueWarp) issuer(s, lane);
+            else if (warp == kIssueWarp || warp == kIssueWarp + 1) issuer(s, warp - kIssueWarp, lane);
         }
     }
     __syncwarp();
