@@ -37,6 +37,7 @@ struct Smem {
     Unit unit[2];
     uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2], drain[2];
     uint32_t tmem;
+    int turn;                          // the tensor cores are one issuer's
     volatile int abort;
 };
 
@@ -52,6 +53,45 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
     }
     s.abort = 1;   // reported at the kernel's end
     return false;
+}
+
+// A barrier a lane (null: none), all of them with one vote.
+__device__ __forceinline__ bool wait_lanes(Smem& s, uint64_t* bar, uint32_t phase) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        if (__all_sync(kFull, !bar || mbar_try_wait(bar, phase & 1u))) return true;
+        if (__any_sync(kFull, s.abort)) return false;
+    }
+    s.abort = 1;
+    return false;
+}
+
+// Whether all of them are there already.
+__device__ __forceinline__ bool test_lanes(uint64_t* bar, uint32_t phase) {
+    uint32_t ok = 1;
+    if (bar)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(phase & 1u)
+            : "memory");
+    return __all_sync(kFull, ok != 0);
+}
+// The tensor cores' queue is taken by one issuer at a time.
+__device__ __forceinline__ bool take_turn(Smem& s, int lane) {
+    #pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        if (__any_sync(kFull, lane == 0 && atomicCAS(&s.turn, 0, 1) == 0)) return true;
+        if (__any_sync(kFull, s.abort)) return false;
+    }
+    s.abort = 1;
+    return false;
+}
+__device__ __forceinline__ void give_turn(Smem& s, int lane) {
+    __syncwarp();
+    if (lane == 0) atomicExch(&s.turn, 0);
 }
 
 __device__ __forceinline__ void tma3(uint8_t* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -265,7 +305,8 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
 
 // A warp for each softmax warpgroup: O(t) += P(t)·V(t), then S(t + 1) = Q·K(t + 1)ᵀ over the P that has been read.  One warp for
 // both left the tensor cores idle for half of the time: what stands between two runs of MMAs (waits, descriptors, commits)
-// takes 500 to 700 cycles, a run 520 or 780, and few MMAs are taken ahead.
+// takes 500 to 700 cycles, a run 520 or 780, and few MMAs are taken ahead.  The two take turns: mixed, their MMAs end at the
+// same time, and both warpgroups' softmax runs while the tensor cores have nothing to do.
 // Every operand is a value that all lanes have, and known as one: an instruction then issues in its own time.
 __device__ __forceinline__ void issuer(Smem& s, int w, int lane) {
     constexpr uint32_t kDescS = mma_desc_bf16(kRows, kTile), kDescO = mma_desc_bf16(kRows, kExpVal) | (1u << 16);
@@ -283,53 +324,78 @@ __device__ __forceinline__ void issuer(Smem& s, int w, int lane) {
         __syncwarp();
     };
     const uint32_t s_full = uniform(smem_u32(&s.s_full[W]));
-    auto scores = [&](uint32_t t, bool last) {   // the CTA's tile t; `last` of the unit's: Q has been read
+    struct Keys {
+        uint32_t b[3], e[3];
+    };
+    auto keys_of = [&](uint32_t t) {   // of the CTA's tile t
         const uint32_t piece = t * kTilePieces;
-        const uint32_t b[3] = {place(piece), place(piece + 1), place(piece + 2)};
-        const uint32_t e[3] = {barrier(piece), barrier(piece + 1), barrier(piece + 2)};
-        #pragma unroll
-        for (int c = 0; c < 3; ++c) {
-            ok = wait_piece(piece + c);
+        return Keys{{place(piece), place(piece + 1), place(piece + 2)}, {barrier(piece), barrier(piece + 1), barrier(piece + 2)}};
+    };
+    // S of the CTA's tile t; `last` of the unit's: Q has been read.  With the turn, which goes while K is not there yet: K may
+    // want a place that the other warpgroup's product with V has to leave first.
+    auto scores = [&](uint32_t t, const Keys& k, bool last) {
+        const uint32_t piece = t * kTilePieces + min(lane, 2);
+        uint64_t* bar = lane < 3 ? &s.full[piece % kPieces] : nullptr;
+        if (!test_lanes(bar, piece / kPieces)) {
+            give_turn(s, lane);
+            ok = wait_lanes(s, bar, piece / kPieces) && take_turn(s, lane);
             if (!ok) return;
-            tcgen_fence_after();
-            if (elect_one()) {
-                #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss(col_s, smem_desc_sw128(q_op + c * kChunk + k * 32), smem_desc_sw128(b[c] + k * 32), kDescS, (c | k) != 0);
-                if (c == 2) mma_commit(s_full);
-                mma_commit(e[c]);
-            }
-            __syncwarp();
         }
+        tcgen_fence_after();
+        auto chunk = [&](int c) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_ss(col_s, smem_desc_sw128(q_op + c * kChunk + i * 32), smem_desc_sw128(k.b[c] + i * 32), kDescS, (c | i) != 0);
+        };
+        if (elect_one()) {
+            chunk(0);
+            mma_commit(k.e[0]);
+            chunk(1);
+            mma_commit(k.e[1]);
+        }
+        give_turn(s, lane);   // the other one comes while the rest runs
+        if (elect_one()) {
+            chunk(2);
+            mma_commit(s_full);
+            mma_commit(k.e[2]);
+        }
+        __syncwarp();
         if (last) commit(&s.q_empty[W]);
     };
     while (ok && next_unit(s, units, x, lane)) {
         const uint32_t mine = uniform(max(x.tiles[W], 0)), tiles = uniform(max(max(x.tiles[0], x.tiles[1]), 0));
         if (mine > 0) {
-            ok = wait_bar(s, &s.q_full[W], x.turn[W]);
-            if (ok) scores(n, mine == 1);
+            const Keys keys = keys_of(n);
+            ok = wait_bar(s, &s.q_full[W], x.turn[W]) && take_turn(s, lane);
+            if (ok) scores(n, keys, mine == 1);
         }
         #pragma unroll 1
         for (uint32_t t = 0; ok && t < mine; ++t) {
             const uint32_t piece = (n + t) * kTilePieces + 3;
             const uint32_t b[2] = {place(piece), place(piece + 1)}, e[2] = {barrier(piece), barrier(piece + 1)}, add = uniform(t > 0);
-            ok = wait_bar(s, &s.p_full[W], steps++);
-            #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                ok = ok && wait_piece(piece + half);
-                if (!ok) break;
-                tcgen_fence_after();
-                if (elect_one()) {
+            const Keys keys = keys_of(n + t + 1);
+            const uint32_t other = piece + (lane == 2);
+            ok = wait_lanes(s, lane == 0 ? &s.p_full[W] : lane < 3 ? &s.full[other % kPieces] : nullptr, lane == 0 ? steps : other / kPieces) &&
+                 take_turn(s, lane);
+            if (!ok) break;
+            ++steps;
+            tcgen_fence_after();
+            if (elect_one()) {
+                #pragma unroll
+                for (int half = 0; half < 2; ++half) {
                     #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_ts(col_o, col_s + (half * 4 + k) * 8, desc_v(b[half] + k * 2048), kDescO, half > 0 || k > 0 ? 1u : add);
                     mma_commit(e[half]);
                 }
-                __syncwarp();
             }
-            if (!ok) break;
-            if (t + 1 < mine) scores(n + t + 1, t + 2 == mine);
-            else commit(&s.o_full[W]);
+            __syncwarp();
+            if (t + 1 < mine) {
+                scores(n + t + 1, keys, t + 2 == mine);
+            } else {
+                give_turn(s, lane);
+                commit(&s.o_full[W]);
+            }
         }
         for (uint32_t k = (n + mine) * kTilePieces; ok && k < (n + tiles) * kTilePieces; ++k) {   // of the other warpgroup's rows alone
             ok = wait_piece(k);
@@ -415,6 +481,17 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
                     }
                 }
             }
+            if (t == tiles - 1 && x.end < base + kTile && !(w == 1 && x.tiles[0] == tiles)) {
+                // V behind the last key that a row of the unit attends: its weight is 0, and 0·NaN would be NaN
+                #pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t piece = (before + t) * kTilePieces + 3 + half, at = piece % kPieces;
+                    if (!wait_bar(s, &s.full[at], piece / kPieces)) return;
+                    for (int c = max(x.end - base - half * 64, 0) + (tid >> 4); c < 64; c += 8)
+                        *reinterpret_cast<uint4*>(s.piece[at] + (tid >> 3 & 1) * (kPieceBytes / 2) + c * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_shared();
+            }
             const float z = ref == -INFINITY ? 0.f : -ref;
             #pragma unroll
             for (int c = 0; c < 4; c += 2) {
@@ -429,17 +506,6 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
                     pk[e] = pack_bf16(a.x, a.y);
                 }
                 tmem_st32(col_s + c * 16, pk);
-            }
-            if (t == tiles - 1 && x.end < base + kTile && !(w == 1 && x.tiles[0] == tiles)) {
-                // V behind the last key that a row of the unit attends: its weight is 0, and 0·NaN would be NaN
-                #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t piece = (before + t) * kTilePieces + 3 + half, at = piece % kPieces;
-                    if (!wait_bar(s, &s.full[at], piece / kPieces)) return;
-                    for (int c = max(x.end - base - half * 64, 0) + (tid >> 4); c < 64; c += 8)
-                        *reinterpret_cast<uint4*>(s.piece[at] + (tid >> 3 & 1) * (kPieceBytes / 2) + c * 128 + (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_shared();
             }
             tmem_wait_st();
             tcgen_fence_before();
@@ -517,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
             mbar_init(&s.u_empty[i], kReaders);
         }
         mbar_fence_init();
+        s.turn = 0;
         s.abort = 0;
     }
     pdl_wait();
