@@ -23,6 +23,9 @@ constexpr int kTries = 200000;         // tries of a wait, which suspend: a seco
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
 constexpr uint32_t kColS = 0, kColO = 256;    // tensor memory columns: S (and P over it) 2 × 128, O 2 × 128
 
+constexpr int kSorted = 512;           // blocks of tokens that are put in order
+constexpr int kBlockBits = 20;
+
 struct Unit {
     int b, h, s0, T, k0, N;
     int tok0;                          // first token
@@ -38,6 +41,8 @@ struct Smem {
     uint64_t full[kPieces], empty[kPieces], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], u_full[2], u_empty[2], drain[2];
     uint32_t tmem;
     int turn;                          // the tensor cores are one issuer's
+    int sorted;                        // blocks of 256 tokens in `order`, or −1
+    uint32_t order[kSorted];           // request << 20 | block, dearest first
     volatile int abort;
 };
 
@@ -152,31 +157,77 @@ __device__ __noinline__ void plain_row(const LatentPrefillParams& p, int64_t tok
 }
 
 // ------------------------------------------------------------------ producer
-// Units in order: requests, within one its tokens from the last 256 on, within these the heads.  CTA c of C takes the units
-// c, 2C − 1 − c, 2C + c, 4C − 1 − c, ..: neighbours cost about the same, and who has the dearer one of a turn has the cheaper
-// of the next.
+// A unit is a block of 256 tokens of one head.  Blocks stand in order, the one with the most keys first (more than kSorted of
+// them as they come: requests, within one its tokens from the last 256 on), and the heads of a block side by side.  CTA c of C
+// takes the units c, 2C − 1 − c, 2C + c, 4C − 1 − c, ..: who has the dearer one of a turn has the cheaper of the next.
+struct Span {
+    int s0, T, k0, N;
+    __device__ __forceinline__ int blocks() const { return (T + 2 * kRows - 1) / (2 * kRows); }
+};
+__device__ __forceinline__ Span load_span(const LatentPrefillParams& p, int b, bool tell) {
+    Span x{p.q_start[b], 0, p.kv_start[b], 0};
+    const int s1 = p.q_start[b + 1], k1 = p.kv_start[b + 1];
+    if (x.s0 < 0 || s1 < x.s0 || s1 > p.n_tokens || x.k0 < 0 || k1 < x.k0 || k1 > p.n_keys) {
+        if (tell) report(p.err, KVD_ERR_OOB);
+        return x;
+    }
+    x.T = s1 - x.s0;
+    x.N = k1 - x.k0;
+    return x;
+}
+__device__ __forceinline__ int block_end(const LatentPrefillParams& p, const Span& x, int block) {   // keys its last row attends
+    return p.causal ? max(0, x.N - x.T + min((block + 1) * 2 * kRows, x.T)) : x.N;
+}
+__device__ __forceinline__ void make_unit(const LatentPrefillParams& p, const Span& x, int b, int h, int block, Unit& u) {
+    u.b = b;
+    u.h = h;
+    u.s0 = x.s0;
+    u.T = x.T;
+    u.k0 = x.k0;
+    u.N = x.N;
+    u.tok0 = block * 2 * kRows;
+    u.end = 0;
+    #pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int last = min(u.tok0 + (w + 1) * kRows, x.T);   // behind the warpgroup's last token
+        const int end = p.causal ? max(0, x.N - x.T + last) : x.N;
+        u.tiles[w] = last > u.tok0 + w * kRows ? (end + kTile - 1) / kTile : -1;
+        if (u.tiles[w] >= 0) u.end = end;
+    }
+}
+// By every thread; scratch: kSorted int2, and a word.
+__device__ inline void sort_blocks(const LatentPrefillParams& p, Smem& s, uint8_t* scratch) {
+    int2* found = reinterpret_cast<int2*>(scratch);
+    int* count = reinterpret_cast<int*>(scratch + kSorted * sizeof(int2));
+    if (threadIdx.x == 0) *count = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const Span x = load_span(p, b, blockIdx.x == 0);
+        const int n = x.blocks();
+        if (n == 0) continue;
+        const int at = atomicAdd(count, min(n, kSorted + 1));
+        for (int i = 0; i < n && at + i < kSorted; ++i) found[at + i] = make_int2(block_end(p, x, i), b << kBlockBits | i);
+    }
+    __syncthreads();
+    const int n = *count;
+    if (threadIdx.x == 0) s.sorted = n <= kSorted ? n : -1;
+    for (int i = threadIdx.x; n <= kSorted && i < n; i += kThreads) {   // (equal ones by request and block, however they came)
+        const int2 x = found[i];
+        int rank = 0;
+        for (int k = 0; k < n; ++k) rank += found[k].x > x.x || (found[k].x == x.x && found[k].y > x.y);
+        s.order[rank] = x.y;
+    }
+    __syncthreads();
+}
 struct Units {
     int64_t before;   // units of requests before lane 0's
     int b0;
     int64_t up;       // units up to this lane's request, itself included
-    int s0, T, k0, N;
-    __device__ __forceinline__ void load(const LatentPrefillParams& p, int lane, bool tell) {
+    Span x;
+    __device__ __forceinline__ void load(const LatentPrefillParams& p, int lane) {
         const int b = b0 + lane;
-        int64_t c = 0;
-        s0 = T = k0 = N = 0;
-        if (b < p.B) {
-            s0 = p.q_start[b];
-            const int s1 = p.q_start[b + 1], k1 = p.kv_start[b + 1];
-            k0 = p.kv_start[b];
-            if (s0 < 0 || s1 < s0 || s1 > p.n_tokens || k0 < 0 || k1 < k0 || k1 > p.n_keys) {
-                if (tell) report(p.err, KVD_ERR_OOB);
-            } else {
-                T = s1 - s0;
-                N = k1 - k0;
-                c = static_cast<int64_t>((T + 2 * kRows - 1) / (2 * kRows)) * p.n_q;
-            }
-        }
-        up = c;
+        x = b < p.B ? load_span(p, b, false) : Span{0, 0, 0, 0};
+        up = static_cast<int64_t>(x.blocks()) * p.n_q;
         #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(kFull, up, o);
@@ -185,34 +236,27 @@ struct Units {
         up += before;
     }
     // Unit u (not before the last one asked for); false behind the last.
-    __device__ __forceinline__ bool find(const LatentPrefillParams& p, int64_t u, int lane, bool tell, Unit& x) {
+    __device__ __forceinline__ bool find(const LatentPrefillParams& p, const Smem& s, int64_t u, int lane, Unit& out) {
+        if (s.sorted >= 0) {
+            if (u >= static_cast<int64_t>(s.sorted) * p.n_q) return false;
+            const uint32_t e = s.order[u / p.n_q];
+            const int b = static_cast<int>(e >> kBlockBits);
+            make_unit(p, load_span(p, b, false), b, static_cast<int>(u % p.n_q), static_cast<int>(e & ((1u << kBlockBits) - 1)), out);
+            return true;
+        }
         while (true) {
             const unsigned at = __ballot_sync(kFull, u < up);
             if (at) {
                 const int src = __ffs(at) - 1;
-                const int64_t prev = __shfl_sync(kFull, up, src > 0 ? src - 1 : 0), first = src > 0 ? prev : before;
-                x.b = b0 + src;
-                x.s0 = __shfl_sync(kFull, s0, src);
-                x.T = __shfl_sync(kFull, T, src);
-                x.k0 = __shfl_sync(kFull, k0, src);
-                x.N = __shfl_sync(kFull, N, src);
-                const int64_t in = u - first;
-                x.h = static_cast<int>(in % p.n_q);
-                x.tok0 = ((x.T + 2 * kRows - 1) / (2 * kRows) - 1 - static_cast<int>(in / p.n_q)) * 2 * kRows;
-                x.end = 0;
-                #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int last = min(x.tok0 + (w + 1) * kRows, x.T);   // behind the warpgroup's last token
-                    const int end = p.causal ? max(0, x.N - x.T + last) : x.N;
-                    x.tiles[w] = last > x.tok0 + w * kRows ? (end + kTile - 1) / kTile : -1;
-                    if (x.tiles[w] >= 0) x.end = end;
-                }
+                const int64_t prev = __shfl_sync(kFull, up, src > 0 ? src - 1 : 0), in = u - (src > 0 ? prev : before);
+                const Span y{__shfl_sync(kFull, x.s0, src), __shfl_sync(kFull, x.T, src), __shfl_sync(kFull, x.k0, src), __shfl_sync(kFull, x.N, src)};
+                make_unit(p, y, b0 + src, static_cast<int>(in % p.n_q), y.blocks() - 1 - static_cast<int>(in / p.n_q), out);
                 return true;
             }
             before = __shfl_sync(kFull, up, 31);
             b0 += 32;
             if (b0 >= p.B) return false;
-            load(p, lane, tell);
+            load(p, lane);
         }
     }
 };
@@ -221,15 +265,14 @@ __device__ __forceinline__ void producer(Smem& s, const LatentPrefillParams& p, 
     Units units;
     units.before = 0;
     units.b0 = 0;
-    const bool tell = blockIdx.x == 0;
-    units.load(p, lane, tell);
+    if (s.sorted < 0) units.load(p, lane);
     uint32_t n = 0, pieces = 0, done[2] = {0, 0};   // tiles before; pieces asked for; units with rows of each warpgroup
     bool ok = true;
     #pragma unroll 1
     for (uint32_t i = 0;; ++i) {
         const int64_t turn = static_cast<int64_t>(i) * gridDim.x;
         Unit x;
-        const bool more = units.find(p, turn + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, tell, x);
+        const bool more = units.find(p, s, turn + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, x);
         // (a turn that is cut off may lack this CTA's unit: so does every later one)
         const uint32_t at = i & 1;
         ok = i < 2 || wait_bar(s, &s.u_empty[at], i / 2 - 1);
@@ -413,12 +456,25 @@ __device__ __forceinline__ void issuer(Smem& s, int w, int lane) {
             if (!wait_bar(s, &s.empty[k % kPieces], k / kPieces)) break;
 }
 
+// 32 bytes, a whole sector of a row that no other thread writes to, if they stand on one.
+__device__ __forceinline__ void st32(void* p, const uint32_t* v, bool sector) {
+    if (sector) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                     "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 // ------------------------------------------------------------------- softmax
 __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, int w, int tid, int lane) {
     const uint32_t mine = s.tmem + (static_cast<uint32_t>(tid & ~31) << 16);
     const uint32_t col_s = mine + kColS + w * kTile, col_o = mine + kColO + w * kExpVal;
     const bool negative = p.scale_log2 < 0.f;
     const float scale = p.scale_log2 == 0.f ? 1e-38f : fabsf(p.scale_log2);   // (0·−inf of a masked key would be NaN)
+    const bool sector = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     Unit x;
     uint32_t n = 0, all = 0, units = 0;   // tiles before, of this warpgroup and of the CTA
     for (uint32_t i = 0; next_unit(s, i, x, lane); ++i) {
@@ -539,14 +595,17 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
             }
             if (!real) continue;
             if (p.out_f32) {
-                float* out = static_cast<float*>(p.out) + row * kExpVal + c * 32;
+                uint32_t z[32];
                 #pragma unroll
-                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(out + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(y[e]);
+                #pragma unroll
+                for (int e = 0; e < 32; e += 8) st32(static_cast<float*>(p.out) + row * kExpVal + c * 32 + e, z + e, sector);
             } else {
-                uint16_t* out = static_cast<uint16_t*>(p.out) + row * kExpVal + c * 32;
+                uint32_t z[16];
                 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4*>(out + e) = make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]), pack_bf16(y[e + 4], y[e + 5]), pack_bf16(y[e + 6], y[e + 7]));
+                for (int e = 0; e < 16; ++e) z[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                #pragma unroll
+                for (int e = 0; e < 16; e += 8) st32(static_cast<uint16_t*>(p.out) + row * kExpVal + c * 32 + 2 * e, z + e, sector);
             }
         }
         if (real && p.lse_out) p.lse_out[row] = total == 0.f ? -INFINITY : (ref + log2f(total)) * kLn2;
@@ -588,6 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
     }
     pdl_wait();
     pdl_trigger();
+    sort_blocks(p, s, s.piece[0]);
+    fence_proxy_async_shared();   // the scratch is copied over
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();

@@ -547,6 +547,26 @@ def test_prefill_of_many_units(cuda_device):
     Prefill(cuda_device, 40, [1, 300, 129, 17, 512, 0, 100], [500, 300, 130, 1000, 512, 3, 900], seed=3).check()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_prefill_out_on_any_16_bytes(cuda_device, dtype):
+    c = Prefill(cuda_device, 3, [140], [150], seed=12)
+    want, _ = c.run(dtype=dtype)
+    buf = torch.full((want.numel() + 16,), 9.0, dtype=dtype, device=cuda_device)
+    at = 16 // want.element_size()
+    out = buf[at:at + want.numel()].view(want.shape)
+    k, v, r = (to(cuda_device, x.contiguous()) for x in (c.k, c.v, c.r))
+    kvd.kvd_latent_prefill(c.pool.handle, to(cuda_device, c.q), to(cuda_device, c.start), k, v, r, to(cuda_device, c.kv_start), out)
+    assert out.data_ptr() % 32 == 16 and torch.equal(out, want)
+    assert bool((buf[:at] == 9.0).all()) and bool((buf[at + want.numel():] == 9.0).all())
+
+
+def test_prefill_of_more_blocks_than_are_sorted(cuda_device):
+    """More than 512 blocks of 256 tokens: they are taken as they come."""
+    rng = np.random.default_rng(13)
+    q = rng.integers(1, 300, 600)
+    Prefill(cuda_device, 1, q.tolist(), (q + rng.integers(0, 9, 600)).tolist(), seed=13).check()
+
+
 def test_prefill_many_requests(cuda_device):
     rng = np.random.default_rng(4)
     q = rng.integers(0, 4, 2048)
