@@ -42,7 +42,7 @@ struct Info {
 };
 
 // What is known of a tile.  8-bit records are loaded by the converters, several tiles behind the producer.
-constexpr int infos_of(bool fp8) { return fp8 ? 5 : kStages; }
+constexpr int infos_of(bool fp8) { return fp8 ? 4 : kStages; }
 
 struct Smem {
     uint8_t k[kStages][kTileBytes];
@@ -165,17 +165,80 @@ struct Walk {
     }
 };
 
-// The CTA's share, found by each warp; scratch holds 2·p.B int64 (what every request costs), filled before by all threads.
+// The CTA's share, found by each warp.  Requests cost tiles + units·extra; their units are searched by the same sums.
+struct Cost {
+    int64_t tiles;
+    int units;
+};
+__device__ __forceinline__ Cost cost_of(const Request& r, int tpb) {
+    const int units = (r.T + tpb - 1) / tpb;
+    return {units <= 1 ? (r.T ? unit_tiles(r, 0, tpb) : 0) : tiles_before(r, units, tpb), units};
+}
+template <class T>
+__device__ __forceinline__ T scan(T x, int lane) {
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T v = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += v;
+    }
+    return x;
+}
+// False: nothing for this CTA.
+__device__ __forceinline__ bool set_share(Walk& w, int64_t tiles, int64_t units, const Heads& hd) {
+    const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks;
+    // a small call is cut into its smallest shares; there the border must not fall beside the tiles
+    w.extra = tiles >= static_cast<int64_t>(8 * kUnitTiles) * lanes ? kUnitTiles : static_cast<int>(tiles) / (8 * lanes);
+    const int64_t total = tiles + units * w.extra;
+    w.share = max(quotient(total + lanes - 1, lanes), static_cast<int64_t>(kMinShare));
+    w.at = min(w.share * me, total);
+    w.remaining = me < lanes ? min(w.share, total - w.at) : 0;
+    return w.remaining > 0;
+}
+// The unit of request r that holds what is `in` from the request's start.
+__device__ __forceinline__ void find_unit(Walk& w, int64_t in) {
+    int a = 0, z = (w.r.T + w.tpb - 1) / w.tpb;   // the last unit of [a, z) that starts at or before `in`
+    int64_t from = 0;
+    while (z - a > 1) {
+        const int mid = a + (z - a) / 2;
+        const int64_t x = tiles_before(w.r, mid, w.tpb) + static_cast<int64_t>(mid) * w.extra;
+        if (x <= in) {
+            a = mid;
+            from = x;
+        } else {
+            z = mid;
+        }
+    }
+    w.tb = a;
+    w.off = static_cast<int>(in - from);
+}
+// Up to 32 requests, a lane each, their tiles' sum below 2^31 (true: found): no barrier, no long sums.
+__device__ inline bool find_share_small(const LatentAttnParams& p, const Heads& hd, int lane, Walk& w) {
+    w = Walk{};
+    w.tpb = hd.tpb;
+    const Request r = lane < p.B ? load_request(p, lane, blockIdx.x == 0 && threadIdx.x < 32) : Request{0, 0, -1};
+    const Cost c = cost_of(r, hd.tpb);
+    if (__any_sync(kFull, c.tiles >> 25 || c.units >> 23)) return false;
+    const int tiles = scan(static_cast<int>(c.tiles), lane), units = scan(c.units, lane);
+    if (!set_share(w, __shfl_sync(kFull, tiles, 31), __shfl_sync(kFull, units, 31), hd)) return true;
+    const int64_t up = tiles + static_cast<int64_t>(units) * w.extra;
+    const unsigned at = __ballot_sync(kFull, w.at < up);
+    const int src = __ffs(at) - 1;   // (the share starts in some request)
+    w.b = src;
+    w.r = {__shfl_sync(kFull, r.s0, src), __shfl_sync(kFull, r.T, src), __shfl_sync(kFull, r.len, src)};
+    find_unit(w, w.at - __shfl_sync(kFull, up - c.tiles - static_cast<int64_t>(c.units) * w.extra, src));
+    return true;
+}
+// Any number of them: scratch holds 2·p.B int64, filled before by all threads.
 __device__ inline void fill_scratch(const LatentAttnParams& p, int64_t* scratch, int tpb, int threads) {
     for (int b = threadIdx.x; b < p.B; b += threads) {
-        const Request r = load_request(p, b, blockIdx.x == 0);
-        const int units = (r.T + tpb - 1) / tpb;
-        scratch[2 * b] = r.T ? tiles_before(r, units, tpb) : 0;
-        scratch[2 * b + 1] = units;
+        const Cost c = cost_of(load_request(p, b, blockIdx.x == 0 && p.B > 32), tpb);
+        scratch[2 * b] = c.tiles;
+        scratch[2 * b + 1] = c.units;
     }
 }
 __device__ inline Walk find_share(const LatentAttnParams& p, const int64_t* scratch, const Heads& hd, int lane) {
-    const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks, tpb = hd.tpb;
+    Walk w{};
+    w.tpb = hd.tpb;
     int64_t tiles = 0, units = 0;
     for (int b = lane; b < p.B; b += 32) {
         tiles += scratch[2 * b];
@@ -186,46 +249,17 @@ __device__ inline Walk find_share(const LatentAttnParams& p, const int64_t* scra
         tiles += __shfl_xor_sync(kFull, tiles, o);
         units += __shfl_xor_sync(kFull, units, o);
     }
-    Walk w{};
-    w.tpb = tpb;
-    // a small call is cut into its smallest shares; there the border must not fall beside the tiles
-    w.extra = static_cast<int>(min(static_cast<int64_t>(kUnitTiles), quotient(tiles, 8 * lanes)));
-    const int64_t total = tiles + units * w.extra;
-    w.share = max(quotient(total + lanes - 1, lanes), static_cast<int64_t>(kMinShare));
-    const int64_t lo = min(w.share * me, total), hi = me < lanes ? min(lo + w.share, total) : lo;
-    w.at = lo;
-    w.remaining = hi - lo;
-    if (hi <= lo) return w;
+    if (!set_share(w, tiles, units, hd)) return w;
     int64_t before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int64_t c = b0 + lane < p.B ? scratch[2 * (b0 + lane)] + w.extra * scratch[2 * (b0 + lane) + 1] : 0;
-        int64_t up = c;
-        #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(kFull, up, o);
-            if (lane >= o) up += v;
-        }
-        up += before;
-        const unsigned at = __ballot_sync(kFull, lo >= up - c && lo < up);
+        const int64_t up = before + scan(c, lane);
+        const unsigned at = __ballot_sync(kFull, w.at < up);
         if (at) {
             const int src = __ffs(at) - 1;
-            const int64_t in = lo - __shfl_sync(kFull, up - c, src);
             w.b = b0 + src;
             w.r = load_request(p, w.b, false);
-            int a = 0, z = (w.r.T + tpb - 1) / tpb;   // the last unit of [a, z) that starts at or before `in`
-            int64_t from = 0;
-            while (z - a > 1) {
-                const int mid = a + (z - a) / 2;
-                const int64_t x = tiles_before(w.r, mid, tpb) + static_cast<int64_t>(mid) * w.extra;
-                if (x <= in) {
-                    a = mid;
-                    from = x;
-                } else {
-                    z = mid;
-                }
-            }
-            w.tb = a;
-            w.off = static_cast<int>(in - from);
+            find_unit(w, w.at - __shfl_sync(kFull, up - c, src));
             return w;
         }
         before = __shfl_sync(kFull, up, 31);
@@ -337,6 +371,8 @@ template <bool FP8>
 __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, Walk walk, int lane) {
     constexpr int kInfos = infos_of(FP8);
     constexpr uint32_t kRecord = latent_record_bytes(FP8);
+    // The cache passes through L2 once (or by neighbours at nearly the same time): what else is there stays, the kernels' code too.
+    const uint64_t policy = policy_evict_first();
     Segment g;
     uint32_t n = 0;
     bool ok = true;
@@ -368,8 +404,8 @@ __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, Wal
                         #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             info.id[k] = block[k];
-                            if (block[k] >= 0)
-                                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.mem + static_cast<int64_t>(block[k]) * kRecord), "r"(kRecord) : "memory");
+                            if (n >= 2 && block[k] >= 0)   // (the first two are loaded at once)
+                                asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(p.mem + static_cast<int64_t>(block[k]) * kRecord), "r"(kRecord), "l"(policy) : "memory");
                         }
                         mbar_arrive(&s.full[at]);
                     } else {
@@ -383,7 +419,7 @@ __device__ __forceinline__ void producer(Smem& s, const LatentAttnParams& p, Wal
                     for (int k = 0; k < 4; ++k) {
                         if (k > 0 && n >= kInfos) ok = ok && wait_bar(s, &s.empty[at][k], n / kInfos - 1);
                         // (a tile begun is copied whole: its barrier counts all its bytes)
-                        if (lane == 0 && block[k] >= 0) bulk_copy(s.k[at] + k * kRecord, p.mem + static_cast<int64_t>(block[k]) * kRecord, kRecord, &s.full[at]);
+                        if (lane == 0 && block[k] >= 0) bulk_g2s(s.k[at] + k * kRecord, p.mem + static_cast<int64_t>(block[k]) * kRecord, kRecord, &s.full[at], policy);
                         __syncwarp();
                     }
                 }
@@ -423,6 +459,13 @@ __device__ __forceinline__ void fixer(Smem& s, const LatentAttnParams& p, Walk w
 // 8-bit records become bf16 operands: codes exactly (every e4m3 value is a bf16 value), the scale stays outside.  A warp
 // takes eight tokens of a tile: 64 codes of each of them, 512 bytes, a load.  A tile's loads are under way while the one
 // before it is converted.
+__device__ __forceinline__ uint4 ld16_once(const void* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
+    return v;
+}
 struct Raw {
     uint4 code[8], rot[2];
     float scale;
@@ -435,10 +478,11 @@ __device__ __forceinline__ bool load_raw(Smem& s, const LatentAttnParams& p, Raw
     const bool on = info.mask >> (warp * 8 + r) & 1;
     const uint8_t* record = p.mem + static_cast<int64_t>(max(info.id[warp >> 1], 0)) * latent_record_bytes(true);
     const uint4 none = make_uint4(0, 0, 0, 0);
+    const uint64_t policy = policy_evict_first();
     #pragma unroll
-    for (int i = 0; i < 8; ++i) x.code[i] = on ? ld16(record + (warp & 1) * 4096 + i * 512 + r * 64 + j * 16) : none;
+    for (int i = 0; i < 8; ++i) x.code[i] = on ? ld16_once(record + (warp & 1) * 4096 + i * 512 + r * 64 + j * 16, policy) : none;
     #pragma unroll
-    for (int i = 0; i < 2; ++i) x.rot[i] = on ? ld16(record + kLatCodes + (warp & 1) * 1024 + r * 128 + (2 * j + i) * 16) : none;
+    for (int i = 0; i < 2; ++i) x.rot[i] = on ? ld16_once(record + kLatCodes + (warp & 1) * 1024 + r * 128 + (2 * j + i) * 16, policy) : none;
     x.scale = on ? *reinterpret_cast<const float*>(record + kLatScales + 4 * ((warp & 1) * 8 + r)) : 0.f;
     return true;
 }
@@ -865,19 +909,30 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     pdl_trigger();
     const Heads hd(p, blockIdx.x % ((p.n_q + kRows - 1) / kRows));
     if (tid < 2) p.part_seg[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
-    static_assert(2 * kMaxBatch * sizeof(int64_t) <= sizeof(s.k[kStages - 1]), "the schedule's scratch");
-    int64_t* scratch = reinterpret_cast<int64_t*>(s.k[kStages - 1]);
-    fill_scratch(p, scratch, hd.tpb, threads_of(FP8));
+    // q of up to 16 MB to L2, a part by each CTA: the queries are read behind the first tiles' copies
+    const int64_t q_bytes = static_cast<int64_t>(p.n_tokens) * p.n_q * kLatKey * 2, part = (q_bytes / gridDim.x + 16) & ~15ll;
+    if (tid == 0 && q_bytes <= (16 << 20) && part * blockIdx.x < q_bytes)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<const uint8_t*>(p.q) + part * blockIdx.x),
+                     "r"(static_cast<uint32_t>(min(part, q_bytes - part * blockIdx.x)))
+                     : "memory");
+    Walk walk;
+    const bool found = p.B <= 32 && find_share_small(p, hd, lane, walk);   // (every warp finds the same)
     tcgen_fence_before();
     __syncthreads();
     tcgen_fence_after();
-    Walk walk = find_share(p, scratch, hd, lane);
+    if (!found) {
+        static_assert(2 * kMaxBatch * sizeof(int64_t) <= sizeof(s.k[kStages - 1]), "the schedule's scratch");
+        int64_t* scratch = reinterpret_cast<int64_t*>(s.k[kStages - 1]);
+        fill_scratch(p, scratch, hd.tpb, threads_of(FP8));
+        __syncthreads();
+        walk = find_share(p, scratch, hd, lane);
+        fence_proxy_async_shared();
+        __syncthreads();   // the scratch has been read: copies may overwrite it
+    }
     if (smem_u32(smem_raw) & 1023u) {   // the operands' swizzle wants it (nothing else stands before them)
         if (tid == 0) report(p.err, KVD_ERR_CUDA);
         walk.remaining = 0;
     }
-    fence_proxy_async_shared();
-    __syncthreads();   // the scratch has been read: copies may overwrite it
     // 8 bits: a thread has 128 registers at launch: 200 + 72 + 2·120 = 4·128
     if (warp < 4) {
         if (FP8) take_registers<200>();
