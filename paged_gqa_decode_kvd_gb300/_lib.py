@@ -545,12 +545,19 @@ def kvd_compact(handle, block_table, seq_lens, new_table, new_lens, workspace, r
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+def _torch(known=[]):
+    """torch, looked up once: an import statement in a function takes a third of a microsecond each time."""
+    if not known:
+        import torch
+
+        known.append(torch)
+    return known[0]
+
+
 def _rows(t, name, width, device):
     """Row stride of a bfloat16 [n][width] tensor, rows contiguous (a slice of a projection's output counts)."""
-    import torch
-
     shape = t.shape
-    if len(shape) != 2 or shape[1] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
+    if len(shape) != 2 or shape[1] != width or t.dtype is not _torch().bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be bfloat16 [rows][{width}] on device {device}")
     row, one = t.stride()
     if one != 1 and shape[0]:
@@ -560,10 +567,8 @@ def _rows(t, name, width, device):
 
 def _head_rows(t, name, width, device):
     """(token stride, head stride) of a bfloat16 [n][heads][width] tensor, a head's values contiguous."""
-    import torch
-
     shape = t.shape
-    if len(shape) != 3 or shape[2] != width or t.dtype is not torch.bfloat16 or t.get_device() != device:
+    if len(shape) != 3 or shape[2] != width or t.dtype is not _torch().bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be bfloat16 [rows][heads][{width}] on device {device}")
     n, h, _ = shape
     row, head, one = t.stride()
@@ -585,9 +590,7 @@ def _latent_pool(handle):
 def _stream_of(stream, device):
     """The stream to launch on as an integer: the given one, or the device's current one."""
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream(device).cuda_stream
+        return _torch().cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -596,8 +599,7 @@ def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=Non
     """Norm latent (bf16 [n][512]; norm_weight bf16 [512] or None), rotate k_rope (bf16 [n][64]) at `positions` (int32,
     with rope: a Rope) and write both at slot_mapping (int64); rotate q_rope (bf16 [n][heads][64]) into q_rope_out, or
     in place."""
-    import torch
-
+    torch = _torch()
     dev = latent.get_device()
     _on(dev, _latent_pool(handle)[1])
     n = latent.shape[0]
@@ -636,8 +638,7 @@ def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=Non
 
 def kvd_latent_gather(handle, layer, block_table, row_start, out, first=None, stream=None):
     """Rows row_start[b] .. row_start[b+1]-1 of out (bf16 [n][576]) = request b's cached rows from position first[b] (0)."""
-    import torch
-
+    torch = _torch()
     dev = out.get_device()
     _on(dev, _latent_pool(handle)[1])
     stride = _rows(out, "out", KVD_LATENT_DIM + KVD_LATENT_ROPE, dev)
@@ -664,8 +665,7 @@ def kvd_latent_attn(handle, layer, q, q_start, block_table, seq_lens, workspace,
                     softmax_scale=None, lse_out=None, stream=None):
     """Absorbed latent attention of the rows q_start[b] .. q_start[b+1]-1 of q (bf16 [n][n_q][576]) over request b's cached
     rows; out bf16 or float32 [n][n_q][512], lse_out f32 [n][n_q].  softmax_scale: 192^-1/2 unless given."""
-    import torch
-
+    torch = _torch()
     n, n_q, _ = q.shape
     dev = q.get_device()
     blocks, pool_dev = _latent_pool(handle)
@@ -698,8 +698,7 @@ def kvd_latent_prefill(handle, q, q_start, k_nope, v, k_rope, kv_start, out, cau
     """Expanded latent attention of ragged prompts: rows q_start[b] .. of q (bf16 [n][n_q][192]) over keys kv_start[b] ..
     of k_nope, v (bf16 [m][n_q][128]) and k_rope (bf16 [m][64]); out bf16 or float32 [n][n_q][128], lse_out f32 [n][n_q].
     causal: the rows are their request's last tokens; else every row attends all its keys."""
-    import torch
-
+    torch = _torch()
     n, n_q, _ = q.shape
     dev = q.get_device()
     _on(dev, _latent_pool(handle)[1])
