@@ -2,6 +2,33 @@
 //
 // Row (token i of the T new tokens of request b, head h), len = seq_lens[b], P = len − T + i:
 //   l_t = scale·<q, (c_t, r_t)> over 512 + 64 dims, t ≤ P and retained;  out = Σ_t softmax(l)_t·c_t,  lse = log Σ exp(l_t).
+//
+// Work.  A unit is (request, 64 rows: some tokens of up to 64 heads), its cost its tiles of 64 positions and a few tiles' time for its
+// start and end.  With more than 64 heads a CTA has one block of heads, and neighbours have the same positions of the others at
+// nearly the same time, so the cache leaves DRAM once.  The units' costs, laid end to end, are cut into equal shares, one per CTA (one
+// CTA per SM); a unit cut by a border leaves fp32 partials that join_kernel joins.
+//
+// One CTA:
+//  * producer warp: follows the block table and bulk-copies (TMA engine) the four records of a tile.  A record is laid out as
+//    the 128-byte-swizzled operand that the tensor cores read, so it is used where it lands, and twice: K-major for the logits (groups of
+//    eight tokens 9,216 bytes apart), N-major for the product with c.  A block's place is free once its 16 positions' product is done;
+//  * fixer warp: zeroes the rows of positions that nobody may attend (evicted, behind the end, unknown blocks);
+//  * a warp that issues S = Q·Kᵀ (Q in tensor memory) and one that issues O += P·C (P in shared memory);
+//  * four softmax warps, online in fp32 (exp2 domain), the reference maximum moved only when a row's passes it by 8.
+// 64 rows, not 128, since 128 rows of 512 fp32 sums are all of tensor memory: M = 64 uses half its lanes, lanes 0 .. 15 of each 32 hold Q and
+// S, 16 .. 31 hold O.  An MMA with M = 64 takes as long as one with M = 128 (33 cycles for N = 64, 129 for N = 256), so the matrix rate ends at
+// half; that is enough up to 64 heads: a tile's MMAs take 2,240 cycles (1.15 us), its way through HBM 1.65 us.
+// Rounding.  K, C and Q enter the products exactly, logits, statistics and sums are fp32, a weight enters as one bf16 (off by at most 2^-8 of
+// itself; its sum is taken before).  Outputs are 1.05 to 1.3 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 a weight, as
+// the chunk kernel has, would make O's MMAs 2,060 cycles a tile instead of 1,030, more than the cache's own time.
+// 8 bits: converter warps load the codes (a tile under way while the one before it is converted) and store them as bf16, exactly, in the same
+// layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
+//
+// Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.0 TB/s (74% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 5 of
+// partials and join); 128 heads: 94 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 47 us, of it 13 until the
+// first tile is converted, 1.3 us a tile, 8 for 152 parts and their join.
+//
+// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so; the kernel then reports it and ends.
 #include "kvd_latent.h"
 #include "kvd_tcgen.cuh"
 
@@ -21,7 +48,7 @@ constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the bl
 // Tensor memory.  M = 64 leaves half of the lanes: 0 .. 15 of each 32 hold Q and S, 16 .. 31 hold O.
 constexpr uint32_t kColQ = 0, kColS = 288, kColR = 352, kHalf = 16u << 16;
 constexpr int kUnitTiles = 3;          // what a unit costs beside its tiles, in tiles
-constexpr int kMinShare = 2;
+constexpr int kMinShare = 2;           // tiles of the smallest share: another CTA costs its start and a part to join
 
 __device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void unpack8(float* x, uint4 v) {
@@ -279,56 +306,129 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
 }
 
 // ------------------------------------------------------------- one row, plainly
-// A warp a row (quarter ≥ 0: 128 of its dims): a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
+// A lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of a token's latent, lanes 0 .. 7 the rotated ones.
 template <bool FP8>
-__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end, int quarter = -1) {
-    const int lane = threadIdx.x & 31;
-    const uint16_t* qr = p.q + row * kLatKey;
-    float q[24], acc[16], m = -INFINITY, sum = 0.f;
-    unpack8(q, ld16(qr + lane * 8));
-    unpack8(q + 8, ld16(qr + 256 + lane * 8));
-    unpack8(q + 16, lane < 8 ? ld16(qr + kLatDim + lane * 8) : make_uint4(0, 0, 0, 0));
-    #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int pos = 0; pos < end; ++pos) {
-        const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
-        const int t = pos % kBs;
-        if (block < 0 || block >= p.num_blocks || (p.retain && !((p.retain[block] >> t) & 1))) continue;
-        const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
-        float k[24];
+struct Token {
+    uint4 lat[2], rope;
+    float scale;
+    __device__ __forceinline__ void load(const uint8_t* record, int t, int lane) {
         if constexpr (FP8) {
-            const float s = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
+            const uint2 a = *reinterpret_cast<const uint2*>(record + latent_code(t, lane));
+            const uint2 b = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32));
+            lat[0] = make_uint4(a.x, a.y, b.x, b.y);
+            scale = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
+        } else {
+            lat[0] = ld16(record + latent_piece(t, lane));
+            lat[1] = ld16(record + latent_piece(t, 32 + lane));
+        }
+        rope = lane < 8 ? ld16(record + (FP8 ? latent_rope_piece(t, lane) : latent_piece(t, 64 + lane))) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void values(float (&x)[16]) const {
+        if constexpr (FP8) {
+            const uint32_t w[4] = {lat[0].x, lat[0].y, lat[0].z, lat[0].w};
             #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
-                uint32_t h[4];
-                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
-                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[2];
+                e4m3x4_to_f16x2x2(w[i], h[0], h[1]);
                 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 v = unpack_f16(h[j]);
-                    k[8 * i + 2 * j] = v.x * s;
-                    k[8 * i + 2 * j + 1] = v.y * s;
+                for (int k = 0; k < 2; ++k) {
+                    const float2 v = unpack_f16(h[k]);
+                    x[4 * i + 2 * k] = v.x * scale;
+                    x[4 * i + 2 * k + 1] = v.y * scale;
                 }
             }
-            unpack8(k + 16, lane < 8 ? ld16(record + latent_rope_piece(t, lane)) : make_uint4(0, 0, 0, 0));
         } else {
-            unpack8(k, ld16(record + latent_piece(t, lane)));
-            unpack8(k + 8, ld16(record + latent_piece(t, 32 + lane)));
-            unpack8(k + 16, lane < 8 ? ld16(record + latent_piece(t, 64 + lane)) : make_uint4(0, 0, 0, 0));
+            unpack8(x, lat[0]);
+            unpack8(x + 8, lat[1]);
         }
-        float dot = 0.f;
+    }
+};
+// The record of a position, or null where it is not attended by anyone.
+template <bool FP8>
+__device__ __forceinline__ const uint8_t* record_of(const LatentAttnParams& p, int b, int pos) {
+    const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+    if (block < 0 || block >= p.num_blocks || (p.retain && !((p.retain[block] >> (pos % kBs)) & 1))) return nullptr;
+    return p.mem + block * latent_record_bytes(FP8);
+}
+// Whether a retained token of positions from .. to − 1 has a latent that is not finite; by a warp.
+template <bool FP8>
+__device__ __noinline__ bool odd_tokens(const LatentAttnParams& p, int b, int from, int to) {
+    const int lane = threadIdx.x & 31;
+    bool odd = false;
+    for (int pos = from; pos < to; ++pos) {
+        const uint8_t* record = record_of<FP8>(p, b, pos);
+        if (!record) continue;
+        Token<FP8> x;
+        float v[16], sum = 0.f;
+        x.load(record, pos % kBs, lane);
+        x.values(v);
         #pragma unroll
-        for (int i = 0; i < 24; ++i) dot = fmaf(q[i], k[i], dot);
+        for (int i = 0; i < 16; ++i) sum = fmaf(v[i], 0.f, sum);
+        odd |= sum != 0.f;   // (0·x is NaN unless x is finite)
+    }
+    return __any_sync(kFull, odd);
+}
+// A warp a row (quarter ≥ 0: 128 of its dims), four positions at a time.
+template <bool FP8>
+__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end, int quarter) {
+    const int lane = threadIdx.x & 31;
+    const uint16_t* qr = p.q + row * kLatKey;
+    float q[16], qrope[8], acc[16], m = -INFINITY, sum = 0.f;
+    unpack8(q, ld16(qr + lane * 8));
+    unpack8(q + 8, ld16(qr + 256 + lane * 8));
+    unpack8(qrope, lane < 8 ? ld16(qr + kLatDim + lane * 8) : make_uint4(0, 0, 0, 0));
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    #pragma unroll 1
+    for (int pos = 0; pos < end; pos += 4) {
+        Token<FP8> x[4];
+        float l[4];
+        bool on[4];
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-        const float l = dot * p.scale_log2, top = fmaxf(m, l);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float f = exp2f(m - ref), w = exp2f(l - ref);
+        for (int j = 0; j < 4; ++j) {
+            const uint8_t* record = pos + j < end ? record_of<FP8>(p, b, pos + j) : nullptr;
+            on[j] = record != nullptr;
+            if (on[j]) x[j].load(record, (pos + j) % kBs, lane);
+        }
+        float top = m;
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float dot = 0.f;
+            if (on[j]) {
+                float v[16], r[8];
+                x[j].values(v);
+                unpack8(r, x[j].rope);
+                #pragma unroll
+                for (int i = 0; i < 16; ++i) dot = fmaf(q[i], v[i], dot);
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) dot = fmaf(qrope[i], r[i], dot);
+            }
+            l[j] = dot;
+        }
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) l[j] += __shfl_xor_sync(kFull, l[j], o);
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            l[j] = on[j] ? l[j] * p.scale_log2 : -INFINITY;
+            top = fmaxf(top, l[j]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref);
         m = top;
-        sum = sum * f + w;
+        sum *= f;
         #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, k[i], acc[i] * f);
+        for (int i = 0; i < 16; ++i) acc[i] *= f;
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!on[j]) continue;
+            const float w = exp2f(l[j] - ref);
+            float v[16];
+            x[j].values(v);
+            sum += w;
+            #pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     #pragma unroll
@@ -340,6 +440,13 @@ __device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t
         else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
     }
     if (lane == 0 && quarter <= 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+// A token that some rows of a unit attend and others do not may hold what is not finite: its weight is 0 for those, and 0·NaN
+// is NaN.  A row that came out as NaN is computed again, plainly, if such a token stands behind what it attends
+// (else it is NaN by right).  end: positions that the row attends; unit_end: that the unit's last row does.
+template <bool FP8>
+__device__ __forceinline__ void again(const LatentAttnParams& p, int b, int64_t row, int end, int unit_end, int quarter) {
+    if (odd_tokens<FP8>(p, b, end, unit_end)) plain_row<FP8>(p, b, row, end, quarter);
 }
 
 // ------------------------------------------------------------------ producer
@@ -567,10 +674,10 @@ __device__ __forceinline__ void score_issuer(Smem& s, const LatentAttnParams& p,
             if (!ok) break;
             tcgen_fence_after();
             if (elect_one()) {
-                #pragma unroll
-                for (int c = 0; c < 9; ++c)
+                #pragma unroll 1   // (less code to fetch: the first tile waits for it)
+                for (uint32_t c = 0; c < 9; ++c)
                     #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (uint32_t k = 0; k < 4; ++k)
                         mma_ts(tmem + (FP8 && c == 8 ? kColR : kColS), tmem + kColQ + c * 32 + k * 8, desc_k(op + c * 1024 + k * 32, kGroup),
                                kDescS, (FP8 && c == 8 ? k : (c | k)) != 0);
                 mma_commit(s_full);
@@ -841,6 +948,15 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
         const float inv[2] = {sum[0] == 0.f ? 0.f : 1.f / sum[0], sum[1] == 0.f ? 0.f : 1.f / sum[1]};
         float odd[2] = {0.f, 0.f};
         if (__any_sync(kFull, row[0] >= 0 || row[1] >= 0)) {
+            // sums as they are to the partials, or rows to out: a thread has a pair of every eight dims of two rows
+            const bool f32 = !whole || p.out_f32;
+            const float by[2] = {whole ? inv[0] : 1.f, whole ? inv[1] : 1.f};
+            uint8_t* dst[2];
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = whole ? max(row[h], static_cast<int64_t>(0)) : static_cast<int64_t>(slot) * kRows + r0 + 8 * h;
+                dst[h] = (whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.part)) + (at * kLatDim + 2 * quad) * (f32 ? 4 : 2);
+            }
             #pragma unroll 1
             for (int c = 0; c < 512; c += 64) {
                 uint32_t v[32];
@@ -848,25 +964,24 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                 tmem_wait_ld(v);
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (row[h] < 0) continue;
+                    float2 y[8];
                     #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int d = c + 8 * k + 2 * quad;
-                        const float2 y = make_float2(__uint_as_float(v[4 * k + 2 * h]), __uint_as_float(v[4 * k + 2 * h + 1]));
-                        odd[h] += y.x + y.y;
-                        if (!whole)
-                            *reinterpret_cast<float2*>(p.part + (static_cast<int64_t>(slot) * kRows + r0 + 8 * h) * kLatDim + d) = y;
-                        else if (p.out_f32)
-                            *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row[h] * kLatDim + d) = make_float2(y.x * inv[h], y.y * inv[h]);
-                        else
-                            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row[h] * kLatDim + d) = pack_bf16(y.x * inv[h], y.y * inv[h]);
+                        y[k] = make_float2(__uint_as_float(v[4 * k + 2 * h]) * by[h], __uint_as_float(v[4 * k + 2 * h + 1]) * by[h]);
+                        odd[h] += y[k].x + y[k].y;
+                    }
+                    if (row[h] < 0) continue;
+                    if (f32) {
+                        #pragma unroll
+                        for (int k = 0; k < 8; ++k) *reinterpret_cast<float2*>(dst[h] + 4 * (c + 8 * k)) = y[k];
+                    } else {
+                        #pragma unroll
+                        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint32_t*>(dst[h] + 2 * (c + 8 * k)) = pack_bf16(y[k].x, y[k].y);
                     }
                 }
             }
         }
         tcgen_fence_before();
-        // A token that some rows of the unit attend and others do not may hold what is not finite: 0·NaN.  Such a row (or
-        // one that is NaN by right) is computed again, without the tokens that it does not attend.
         if (whole && g.multi) {
             #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -874,7 +989,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                     const int i = (__ffs(todo) - 1) >> 2, r = warp * 16 + 8 * h + i;
                     todo &= ~(15u << 4 * i);
                     __syncwarp();
-                    plain_row<FP8>(p, g.b, row_of(p, hd, g, r), g.len < 0 ? 0 : g.first + r / hd.each + 1);
+                    if (g.len >= 0) again<FP8>(p, g.b, row_of(p, hd, g, r), g.first + r / hd.each + 1, g.end, -1);
                 }
         }
         g = after;
@@ -974,12 +1089,11 @@ __device__ __forceinline__ void put4(const LatentAttnParams& p, int64_t row, int
     else
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kLatDim + d) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
 }
-// As in a whole unit: a row that is NaN is computed again without the tokens that it does not attend.
 template <bool FP8>
 __device__ __noinline__ void join_again(const LatentAttnParams& p, const int4& g, const Heads& hd, int r, int64_t row, int quarter) {
     const Request q = load_request(p, g.x, false);
-    const int tok0 = g.y - q.s0;
-    if (min(hd.tpb, q.T - tok0) > 1) plain_row<FP8>(p, g.x, row, q.len < 0 ? 0 : q.len - q.T + tok0 + r / hd.each + 1, quarter);
+    const int tok0 = g.y - q.s0, first = q.len - q.T;
+    if (q.len >= 0) again<FP8>(p, g.x, row, first + tok0 + r / hd.each + 1, first + min(tok0 + hd.tpb, q.T), quarter);
 }
 
 template <bool FP8>
