@@ -28,7 +28,8 @@
 // partials and join); 128 heads: 94 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 47 us, of it 13 until the
 // first tile is converted, 1.3 us a tile, 8 for 152 parts and their join.
 //
-// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so; the kernel then reports it and ends.
+// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (a try suspends 3.8 us; not while a
+// row is computed again, which ends by itself and takes 0.5 us a position); the kernel then reports it and ends.
 #include "kvd_latent.h"
 #include "kvd_tcgen.cuh"
 
@@ -78,6 +79,7 @@ struct Smem {
     uint64_t full[infos_of(true)], free[infos_of(true)], ready[kStages], empty[kStages][4], s_full, s_free, p_full, q_full, drain[2];
     uint32_t tmem;
     volatile int abort;
+    int again;   // warps that compute a row again: every other wait may be longer for it
 };
 
 struct Request {
@@ -300,135 +302,63 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
     for (int i = 0; i < kTries; ++i) {
         if (__all_sync(kFull, mbar_try_wait(bar, phase & 1u))) return true;
         if (__any_sync(kFull, s.abort)) return false;
+        if (i == kTries - 1 && __any_sync(kFull, *static_cast<volatile int*>(&s.again) > 0)) i = 0;
     }
     s.abort = 1;   // reported at the kernel's end
     return false;
 }
 
 // ------------------------------------------------------------- one row, plainly
-// A lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of a token's latent, lanes 0 .. 7 the rotated ones.
-template <bool FP8>
-struct Token {
-    uint4 lat[2], rope;
-    float scale;
-    __device__ __forceinline__ void load(const uint8_t* record, int t, int lane) {
-        if constexpr (FP8) {
-            const uint2 a = *reinterpret_cast<const uint2*>(record + latent_code(t, lane));
-            const uint2 b = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32));
-            lat[0] = make_uint4(a.x, a.y, b.x, b.y);
-            scale = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
-        } else {
-            lat[0] = ld16(record + latent_piece(t, lane));
-            lat[1] = ld16(record + latent_piece(t, 32 + lane));
-        }
-        rope = lane < 8 ? ld16(record + (FP8 ? latent_rope_piece(t, lane) : latent_piece(t, 64 + lane))) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void values(float (&x)[16]) const {
-        if constexpr (FP8) {
-            const uint32_t w[4] = {lat[0].x, lat[0].y, lat[0].z, lat[0].w};
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t h[2];
-                e4m3x4_to_f16x2x2(w[i], h[0], h[1]);
-                #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 v = unpack_f16(h[k]);
-                    x[4 * i + 2 * k] = v.x * scale;
-                    x[4 * i + 2 * k + 1] = v.y * scale;
-                }
-            }
-        } else {
-            unpack8(x, lat[0]);
-            unpack8(x + 8, lat[1]);
-        }
-    }
-};
-// The record of a position, or null where it is not attended by anyone.
-template <bool FP8>
-__device__ __forceinline__ const uint8_t* record_of(const LatentAttnParams& p, int b, int pos) {
-    const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
-    if (block < 0 || block >= p.num_blocks || (p.retain && !((p.retain[block] >> (pos % kBs)) & 1))) return nullptr;
-    return p.mem + block * latent_record_bytes(FP8);
-}
-// Whether a retained token of positions from .. to − 1 has a latent that is not finite; by a warp.
-template <bool FP8>
-__device__ __noinline__ bool odd_tokens(const LatentAttnParams& p, int b, int from, int to) {
-    const int lane = threadIdx.x & 31;
-    bool odd = false;
-    for (int pos = from; pos < to; ++pos) {
-        const uint8_t* record = record_of<FP8>(p, b, pos);
-        if (!record) continue;
-        Token<FP8> x;
-        float v[16], sum = 0.f;
-        x.load(record, pos % kBs, lane);
-        x.values(v);
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) sum = fmaf(v[i], 0.f, sum);
-        odd |= sum != 0.f;   // (0·x is NaN unless x is finite)
-    }
-    return __any_sync(kFull, odd);
-}
-// A warp a row (quarter ≥ 0: 128 of its dims), four positions at a time.
+// A warp a row (quarter ≥ 0: 128 of its dims): a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
 template <bool FP8>
 __device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end, int quarter) {
     const int lane = threadIdx.x & 31;
     const uint16_t* qr = p.q + row * kLatKey;
-    float q[16], qrope[8], acc[16], m = -INFINITY, sum = 0.f;
+    float q[24], acc[16], m = -INFINITY, sum = 0.f;
     unpack8(q, ld16(qr + lane * 8));
     unpack8(q + 8, ld16(qr + 256 + lane * 8));
-    unpack8(qrope, lane < 8 ? ld16(qr + kLatDim + lane * 8) : make_uint4(0, 0, 0, 0));
+    unpack8(q + 16, lane < 8 ? ld16(qr + kLatDim + lane * 8) : make_uint4(0, 0, 0, 0));
     #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    #pragma unroll 1
-    for (int pos = 0; pos < end; pos += 4) {
-        Token<FP8> x[4];
-        float l[4];
-        bool on[4];
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint8_t* record = pos + j < end ? record_of<FP8>(p, b, pos + j) : nullptr;
-            on[j] = record != nullptr;
-            if (on[j]) x[j].load(record, (pos + j) % kBs, lane);
-        }
-        float top = m;
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float dot = 0.f;
-            if (on[j]) {
-                float v[16], r[8];
-                x[j].values(v);
-                unpack8(r, x[j].rope);
+    for (int pos = 0; pos < end; ++pos) {
+        const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+        const int t = pos % kBs;
+        if (block < 0 || block >= p.num_blocks || (p.retain && !((p.retain[block] >> t) & 1))) continue;
+        const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
+        float k[24];
+        if constexpr (FP8) {
+            const float s = *reinterpret_cast<const float*>(record + kLatScales + 4 * t);
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
+                uint32_t h[4];
+                e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
                 #pragma unroll
-                for (int i = 0; i < 16; ++i) dot = fmaf(q[i], v[i], dot);
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) dot = fmaf(qrope[i], r[i], dot);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = unpack_f16(h[j]);
+                    k[8 * i + 2 * j] = v.x * s;
+                    k[8 * i + 2 * j + 1] = v.y * s;
+                }
             }
-            l[j] = dot;
+            unpack8(k + 16, lane < 8 ? ld16(record + latent_rope_piece(t, lane)) : make_uint4(0, 0, 0, 0));
+        } else {
+            unpack8(k, ld16(record + latent_piece(t, lane)));
+            unpack8(k + 8, ld16(record + latent_piece(t, 32 + lane)));
+            unpack8(k + 16, lane < 8 ? ld16(record + latent_piece(t, 64 + lane)) : make_uint4(0, 0, 0, 0));
         }
+        float dot = 0.f;
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) l[j] += __shfl_xor_sync(kFull, l[j], o);
+        for (int i = 0; i < 24; ++i) dot = fmaf(q[i], k[i], dot);
         #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            l[j] = on[j] ? l[j] * p.scale_log2 : -INFINITY;
-            top = fmaxf(top, l[j]);
-        }
-        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref);
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        const float l = dot * p.scale_log2, top = fmaxf(m, l);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - ref), w = exp2f(l - ref);
         m = top;
-        sum *= f;
+        sum = sum * f + w;
         #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] *= f;
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!on[j]) continue;
-            const float w = exp2f(l[j] - ref);
-            float v[16];
-            x[j].values(v);
-            sum += w;
-            #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, v[i], acc[i]);
-        }
+        for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, k[i], acc[i] * f);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     #pragma unroll
@@ -440,6 +370,33 @@ __device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t
         else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
     }
     if (lane == 0 && quarter <= 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+// Whether a retained token of positions from .. to − 1 has a latent that is not finite; by a warp.
+template <bool FP8>
+__device__ __noinline__ bool odd_tokens(const LatentAttnParams& p, int b, int from, int to) {
+    const int lane = threadIdx.x & 31;
+    bool odd = false;
+    #pragma unroll 1
+    for (int pos = from; pos < to; ++pos) {
+        const int64_t block = p.block_table[static_cast<int64_t>(b) * p.max_blocks + pos / kBs];
+        const int t = pos % kBs;
+        if (block < 0 || block >= p.num_blocks || (p.retain && !((p.retain[block] >> t) & 1))) continue;
+        const uint8_t* record = p.mem + block * latent_record_bytes(FP8);
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (FP8) {   // (a code that is NaN, or a scale that makes it one)
+                const uint2 c = *reinterpret_cast<const uint2*>(record + latent_code(t, lane + 32 * i));
+                const auto nan = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+                odd |= (nan(c.x) | nan(c.y)) != 0 || !isfinite(*reinterpret_cast<const float*>(record + kLatScales + 4 * t));
+            } else {
+                const uint4 c = ld16(record + latent_piece(t, lane + 32 * i));
+                const auto nan = [](uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+                odd |= (nan(c.x) | nan(c.y) | nan(c.z) | nan(c.w)) != 0;
+            }
+        }
+    }
+    return __any_sync(kFull, odd);
 }
 // A token that some rows of a unit attend and others do not may hold what is not finite: its weight is 0 for those, and 0·NaN
 // is NaN.  A row that came out as NaN is computed again, plainly, if such a token stands behind what it attends
@@ -989,7 +946,10 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                     const int i = (__ffs(todo) - 1) >> 2, r = warp * 16 + 8 * h + i;
                     todo &= ~(15u << 4 * i);
                     __syncwarp();
-                    if (g.len >= 0) again<FP8>(p, g.b, row_of(p, hd, g, r), g.first + r / hd.each + 1, g.end, -1);
+                    if (g.len < 0) continue;
+                    if (lane == 0) atomicAdd(&s.again, 1);
+                    again<FP8>(p, g.b, row_of(p, hd, g, r), g.first + r / hd.each + 1, g.end, -1);
+                    if (lane == 0) atomicSub(&s.again, 1);
                 }
         }
         g = after;
@@ -1019,6 +979,7 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
         mbar_init(&s.drain[1], 1);
         mbar_fence_init();
         s.abort = 0;
+        s.again = 0;
     }
     pdl_wait();
     pdl_trigger();

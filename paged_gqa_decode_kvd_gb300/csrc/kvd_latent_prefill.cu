@@ -17,7 +17,8 @@
 // turns leave between two runs.  Ragged prompts: 119 us against 53 of HBM: a unit's first tile waits 3 us for Q and K, its rows take 1 to 2 us,
 // and rows of at most 128 tokens leave a warpgroup idle.
 //
-// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so; the kernel then reports it and ends.
+// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (a try suspends 3.8 us; not while a
+// row is computed again, which ends by itself and takes 0.5 us a position); the kernel then reports it and ends.
 #include <cuda.h>
 
 #include "kvd_latent.h"
@@ -59,6 +60,7 @@ struct Smem {
     int sorted;                        // blocks of 256 tokens in `order`, or −1
     uint32_t order[kSorted];           // request << 20 | block, dearest first
     volatile int abort;
+    int again;                         // warps that compute a row again: every other wait may be longer for it
 };
 
 struct Maps {
@@ -70,6 +72,7 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
     for (int i = 0; i < kTries; ++i) {
         if (__all_sync(kFull, mbar_try_wait(bar, phase & 1u))) return true;
         if (__any_sync(kFull, s.abort)) return false;
+        if (i == kTries - 1 && __any_sync(kFull, *static_cast<volatile int*>(&s.again) > 0)) i = 0;
     }
     s.abort = 1;   // reported at the kernel's end
     return false;
@@ -81,6 +84,7 @@ __device__ __forceinline__ bool wait_lanes(Smem& s, uint64_t* bar, uint32_t phas
     for (int i = 0; i < kTries; ++i) {
         if (__all_sync(kFull, !bar || mbar_try_wait(bar, phase & 1u))) return true;
         if (__any_sync(kFull, s.abort)) return false;
+        if (i == kTries - 1 && __any_sync(kFull, *static_cast<volatile int*>(&s.again) > 0)) i = 0;
     }
     s.abort = 1;
     return false;
@@ -105,6 +109,7 @@ __device__ __forceinline__ bool take_turn(Smem& s, int lane) {
     for (int i = 0; i < kTries; ++i) {
         if (__any_sync(kFull, lane == 0 && atomicCAS(&s.turn, 0, 1) == 0)) return true;
         if (__any_sync(kFull, s.abort)) return false;
+        if (i == kTries - 1 && __any_sync(kFull, *static_cast<volatile int*>(&s.again) > 0)) i = 0;
     }
     s.abort = 1;
     return false;
@@ -138,7 +143,7 @@ __device__ __forceinline__ void unpack4(float* x, const uint16_t* p) {
 __device__ __noinline__ bool odd_values(const LatentPrefillParams& p, int h, int64_t k0, int from, int to) {
     const int lane = threadIdx.x & 31;
     bool odd = false;
-    #pragma unroll 4
+    #pragma unroll 1
     for (int64_t n = k0 + from; n < k0 + to; ++n) {
         float v[4];
         unpack4(v, p.v + n * p.v_stride + h * p.v_head + lane * 4);
@@ -146,7 +151,7 @@ __device__ __noinline__ bool odd_values(const LatentPrefillParams& p, int h, int
     }
     return __any_sync(kFull, odd);
 }
-// A warp a row, four keys at a time: a lane has four dims of k and v and two rotated ones.
+// A warp a row: a lane has four dims of k and v and two rotated ones.
 __device__ __noinline__ void plain_row(const LatentPrefillParams& p, int64_t token, int h, int64_t k0, int end) {
     const int lane = threadIdx.x & 31;
     const int64_t row = token * p.n_q + h;
@@ -155,45 +160,23 @@ __device__ __noinline__ void plain_row(const LatentPrefillParams& p, int64_t tok
     const float2 qr = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.q + row * kExpKey + kNope + lane * 2));
     q[4] = qr.x;
     q[5] = qr.y;
-    #pragma unroll 1
-    for (int t = 0; t < end; t += 4) {
-        float v[4][4], l[4];
+    for (int64_t n = k0; n < k0 + end; ++n) {
+        float k[4], v[4];
+        unpack4(k, p.k_nope + n * p.k_stride + h * p.k_head + lane * 4);
+        unpack4(v, p.v + n * p.v_stride + h * p.v_head + lane * 4);
+        const float2 rot = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.k_rope + n * p.rope_stride + lane * 2));
+        float dot = fmaf(q[4], rot.x, q[5] * rot.y);
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            l[i] = 0.f;
-            if (t + i >= end) continue;
-            const int64_t n = k0 + t + i;
-            float k[4];
-            unpack4(k, p.k_nope + n * p.k_stride + h * p.k_head + lane * 4);
-            unpack4(v[i], p.v + n * p.v_stride + h * p.v_head + lane * 4);
-            const float2 rot = unpack_bf16(*reinterpret_cast<const uint32_t*>(p.k_rope + n * p.rope_stride + lane * 2));
-            l[i] = fmaf(q[4], rot.x, q[5] * rot.y);
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) l[i] = fmaf(q[j], k[j], l[i]);
-        }
+        for (int j = 0; j < 4; ++j) dot = fmaf(q[j], k[j], dot);
         #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) l[i] += __shfl_xor_sync(kFull, l[i], o);
-        float top = m;
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            l[i] = t + i < end ? l[i] * p.scale_log2 : -INFINITY;
-            top = fmaxf(top, l[i]);
-        }
-        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref);
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+        const float l = dot * p.scale_log2, top = fmaxf(m, l);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(m - ref), w = exp2f(l - ref);
         m = top;
-        sum *= f;
+        sum = sum * f + w;
         #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] *= f;
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (t + i >= end) continue;
-            const float w = exp2f(l[i] - ref);
-            sum += w;
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, v[i][j], acc[j]);
-        }
+        for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, v[j], acc[j] * f);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     #pragma unroll
@@ -666,7 +649,10 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
         for (; todo; todo &= todo - 1) {
             const int rr = (r & ~31) + __ffs(todo) - 1, end = max(0, x.N - x.T + rr + 1);
             __syncwarp();
-            if (odd_values(p, x.h, x.k0, end, min(x.tiles[w] * kTile, x.end))) plain_row(p, static_cast<int64_t>(x.s0) + rr, x.h, x.k0, end);
+            if (!odd_values(p, x.h, x.k0, end, min(x.tiles[w] * kTile, x.end))) continue;
+            if (lane == 0) atomicAdd(&s.again, 1);
+            plain_row(p, static_cast<int64_t>(x.s0) + rr, x.h, x.k0, end);
+            if (lane == 0) atomicSub(&s.again, 1);
         }
     }
 }
@@ -694,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
         mbar_fence_init();
         s.turn = 0;
         s.abort = 0;
+        s.again = 0;
     }
     pdl_wait();
     pdl_trigger();
