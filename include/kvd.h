@@ -630,8 +630,8 @@ KVD_API kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int m
 /* Norm, rotate and append: one launch for one layer's new tokens.  For token n < n_tokens at position positions[n]:
  *   y = latent[n]·w / sqrt(mean(latent[n]²) + eps) with w = norm_weight, or y = latent[n] without; r = R(pos)·k_rope[n];
  *   q_rope_out[n][h] = R(pos)·q_rope[n][h] for the n_q query heads, R as in kvd_rope_append over 64 dims (rot_dim ≤ 64).
- * y and r go to slot_mapping[n]: as bf16, or (FP8) r as bf16 and y as codes: scale = fp32(max|y|/448) (1 for a zero
- * row), code = e4m3, nearest even, saturating, of the fp32 quotient y/scale (y itself is not rounded before).
+ * y and r go to slot_mapping[n]: as bf16, or (FP8) r as bf16 and y as codes: scale = fp32(max|y|/448) (1 where
+ * that is 0), code = e4m3, nearest even, saturating, of the fp32 quotient y/scale (y itself is not rounded before).
  *  latent        bf16 [n_tokens][512], device, rows latent_stride elements apart (slices of one projection's output have
  *                one stride); likewise k_rope [n_tokens][64].  16-byte aligned, strides multiples of 8
  *  norm_weight   bf16 [512], device, 16-byte aligned, or NULL: no norm.  norm_eps ≥ 0

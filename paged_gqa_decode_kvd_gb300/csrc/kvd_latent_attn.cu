@@ -116,7 +116,7 @@ __device__ __forceinline__ int unit_end(const Request& r, int tb, int tpb) {
     return r.len < 0 ? 0 : r.len - r.T + min((tb + 1) * tpb, r.T);
 }
 __device__ __forceinline__ int unit_tiles(const Request& r, int tb, int tpb) {
-    return r.len < 0 ? 1 : (unit_end(r, tb, tpb) + kTile - 1) / kTile;
+    return r.len < 0 ? 1 : static_cast<int>((static_cast<uint32_t>(unit_end(r, tb, tpb)) + kTile - 1) / kTile);   // (up to 2^31 − 1 positions)
 }
 // Tiles of units 0 .. k-1: Σ ⌊(c + i·tpb)/64⌋, whose remainders repeat every 64 units.
 __device__ inline int64_t tiles_before(const Request& r, int k, int tpb) {

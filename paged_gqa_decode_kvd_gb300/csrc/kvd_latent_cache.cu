@@ -3,7 +3,7 @@
 // Append, token n with latent x, key part k and position p:
 //   y = x·w / sqrt(mean(x²) + eps)      (w: the norm's weights; without them y = x)
 //   r = R(p)·k, and for every query head q' = R(p)·q, R the rotation of kvd_rope_append over 64 dims
-//   bf16 record: y and r rounded to bf16; 8-bit record: s = fp32(max|y|/448) (1 for a zero row), codes e4m3(y/s),
+//   bf16 record: y and r rounded to bf16; 8-bit record: s = fp32(max|y|/448) (1 where that is 0), codes e4m3(y/s),
 //   rounded once from fp32, and r in bf16.
 // Read back: y (code·s, rounded to bf16) and r, side by side.
 //
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendPara
         for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const float s = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+        float s = __fdiv_rn(top, 448.f);
+        if (s == 0.f) s = 1.f;   // (a row of zeros, or of a few times fp32's smallest value)
         #pragma unroll
         for (int i = 0; i < 2; ++i)
             *reinterpret_cast<uint2*>(record + latent_code(t, lane + 32 * i)) = make_uint2(codes4(x + 8 * i, s), codes4(x + 8 * i + 4, s));

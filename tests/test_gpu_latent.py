@@ -145,6 +145,20 @@ def test_append_without_rotation_or_norm_copies(cuda_device, kind):
         assert bool(got[6, 7].isnan()) and int(got[6, :LAT].isnan().sum()) == 1
 
 
+def test_append_of_rows_too_small_for_a_scale(cuda_device):
+    """A row whose largest value over 448 is below fp32's smallest: scale 1 and zeros, not 0/0."""
+    dev = cuda_device
+    pool = poisoned(1, 1, FP8, dev)
+    w = torch.zeros(LAT, dtype=torch.bfloat16)
+    w[::2] = 2.0 ** -133
+    ones = torch.ones(1, LAT, dtype=torch.bfloat16)   # y = w / sqrt(1 + 10^8): 2^-146 or 0
+    kvd.kvd_latent_append(pool.handle, 0, to(dev, ones), to(dev, ones[:, :ROT].contiguous()), to(dev, np.zeros(1, np.int64)),
+                          norm_weight=to(dev, w), norm_eps=1e8)
+    ok(pool)
+    values, _, scales = read_pool(pool)
+    assert float(scales[0].flatten()[0]) == 1.0 and bool((values[0][0, :LAT] == 0).all())
+
+
 @KINDS
 def test_append_in_place_and_bad_tokens(cuda_device, kind):
     dev, rng, n = cuda_device, np.random.default_rng(4), 6
@@ -469,6 +483,51 @@ def test_attn_same_bits_streams_and_graphs(cuda_device, kind):
     ok(c.pool)
 
 
+def test_attn_repairs_long_rows_in_peace(cuda_device):
+    """A NaN in the last token, 120,000 positions, whole units: the first token's rows are computed again for longer than
+    the other warps' waits last."""
+    dev, sms, blocks, n_q = cuda_device, torch.cuda.get_device_properties(0).multi_processor_count, 7500, 32
+    B, N = 2 * sms, 16 * blocks
+    pool = poisoned(1, 2, BF16, dev)
+    rng = np.random.default_rng(9)
+    lat, key = rand(rng, 32, LAT), rand(rng, 32, ROT)
+    lat[31, 5] = float("nan")
+    kvd.kvd_latent_append(pool.handle, 0, to(dev, lat), to(dev, key), to(dev, np.arange(32, dtype=np.int64)))
+    table = torch.zeros(B, blocks, dtype=torch.int32, device=dev)
+    table[:, -1] = 1
+    q = torch.zeros(2 * B, n_q, KEY, dtype=torch.bfloat16, device=dev)
+    out, lse = torch.zeros(2 * B, n_q, LAT, device=dev), torch.zeros(2 * B, n_q, device=dev)
+    ws = torch.empty(kvd.kvd_latent_workspace_bytes(pool.handle, n_q, B), dtype=torch.uint8, device=dev)
+    kvd.kvd_latent_attn(pool.handle, 0, q, torch.arange(0, 2 * B + 1, 2, dtype=torch.int32, device=dev), table,
+                        torch.full((B,), N, dtype=torch.int32, device=dev), ws, out, softmax_scale=SCALE, lse_out=lse)
+    ok(pool)
+    # every weight is 1; N additions in a row, each off by at most 2^-24 of a sum of absolute values
+    x = lat[:31].double()
+    mean, size = ((blocks - 1) * y[:16].sum(0) / (N - 1) + y[16:].sum(0) / (N - 1) for y in (x, x.abs()))
+    assert_within(out[::2].cpu(), mean.expand(B, n_q, LAT), (2 * N * 2.0 ** -24 * size).expand(B, n_q, LAT), "out")
+    assert float((lse[::2].double() - np.log(N - 1)).abs().max()) < 2 * N * 2.0 ** -24
+    assert bool(out[1::2, :, 5].isnan().all())
+
+
+def test_attn_of_the_longest_request(cuda_device):
+    """2^31 − 1 positions, all in one block: lengths and tiles stay within their types."""
+    dev, rng = cuda_device, np.random.default_rng(8)
+    pool = poisoned(1, 1, BF16, dev)
+    lat = torch.ones(16, LAT, dtype=torch.bfloat16)
+    kvd.kvd_latent_append(pool.handle, 0, to(dev, lat), to(dev, rand(rng, 16, ROT)), to(dev, np.arange(16, dtype=np.int64)))
+    table = torch.zeros(1, 1 << 27, dtype=torch.int32, device=dev)
+    q = torch.zeros(1, 1, KEY, dtype=torch.bfloat16, device=dev)
+    out, lse = torch.zeros(1, 1, LAT, device=dev), torch.zeros(1, 1, device=dev)
+    ws = torch.empty(kvd.kvd_latent_workspace_bytes(pool.handle, 1, 1), dtype=torch.uint8, device=dev)
+    kvd.kvd_latent_attn(pool.handle, 0, q, torch.tensor([0, 1], dtype=torch.int32, device=dev), table,
+                        torch.tensor([2 ** 31 - 1], dtype=torch.int32, device=dev), ws, out, softmax_scale=SCALE, lse_out=lse)
+    ok(pool)
+    # every weight is 1; a CTA's sum takes 2^25/152 tiles of 16 additions a lane, each off by at most 2^-24 of the sum
+    slack = (2 ** 25 // 152 + 1) * 16 * 2.0 ** -24
+    assert abs(float(lse) - 31 * np.log(2.0)) < -np.log1p(-slack)
+    assert bool(((out - 1).abs() < 2 * slack).all())
+
+
 def test_attn_many_requests(cuda_device):
     rng = np.random.default_rng(18)
     q_lens = rng.integers(0, 3, 2048).tolist()
@@ -605,6 +664,27 @@ def test_prefill_later_tokens_do_not_reach_earlier_rows(cuda_device, bad, T, N, 
         assert bool(out[j:, 1, 9].isnan().all()) and bool(out[j:, 2].isnan().all())
     else:
         assert bool((out[j:, 1, 9] == bad).all())
+
+
+def test_prefill_repairs_long_rows_in_peace(cuda_device):
+    """A NaN in the last of 131,072 keys, 65 rows: those before it are computed again, 32 a warp, for longer than the other
+    warps' waits last."""
+    dev, rng, T, N = cuda_device, np.random.default_rng(10), 65, 1 << 17
+    pool = kvd.LatentPool(1, 1, BF16, device=dev)
+    v = rand(rng, 64, 128).repeat(N // 64, 1).view(N, 1, 128)
+    v[-1, 0, 3] = float("nan")
+    zeros = torch.zeros(N, 1, 192, dtype=torch.bfloat16, device=dev)
+    out, lse = torch.zeros(T, 1, 128, device=dev), torch.zeros(T, 1, device=dev)
+    starts = [torch.tensor([0, n], dtype=torch.int32, device=dev) for n in (T, N)]
+    kvd.kvd_latent_prefill(pool.handle, zeros[:T], starts[0], zeros[..., :128], to(dev, v), zeros[:, 0, 128:], starts[1], out, lse_out=lse)
+    ok(pool)
+    # every weight is 1; N additions in a row, each off by at most 2^-24 of a sum of absolute values
+    ends = torch.arange(N - T + 1, N)[:, None]
+    x = v[:, 0].double().nan_to_num(0.0)
+    mean, size = (y.cumsum(0)[ends[:, 0] - 1] / ends for y in (x, x.abs()))
+    assert_within(out[:-1, 0].cpu(), mean, 2 * N * 2.0 ** -24 * size, "out")
+    assert float((lse[:-1, 0].cpu().double() - ends[:, 0].double().log()).abs().max()) < 2 * N * 2.0 ** -24
+    assert bool(out[-1, 0, 3].isnan())
 
 
 def test_prefill_what_no_row_attends_may_be_anything(cuda_device):
