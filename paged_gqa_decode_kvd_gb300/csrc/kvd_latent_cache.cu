@@ -7,8 +7,8 @@
 //   rounded once from fp32, and r in bf16.
 // Read back: y (code·s, rounded to bf16) and r, side by side.
 //
-// Bound: HBM.  4,099 tokens into 8 bits with 128 heads' queries: 28 us, 5.0 TB/s (74% of measured: 34 MB of queries are read and written in
-// pieces of 128 bytes); a decode step of 32 tokens: 2.9 us in a graph, 17 with the host call.  226,000 rows of 24 requests from 8 bits: 64 us,
+// Bound: HBM.  4,099 tokens into 8 bits with 128 heads' queries: 26 us, 5.4 TB/s (80% of measured: 67 MB of queries are read and written in
+// pieces of 128 bytes); a decode step of 32 tokens: 2.6 us in a graph, 11 with the host call.  226,000 rows of 24 requests from 8 bits: 64 us,
 // 6.3 TB/s (93%).
 #include "kvd_common.cuh"
 #include "kvd_latent.h"
@@ -24,25 +24,26 @@ __device__ __forceinline__ void st16(void* p, uint4 v) { *reinterpret_cast<uint4
 
 // cos and sin (times m) of a lane's 8 dims of a rotated vector of 64: by pair if neighbours are paired, else by dim,
 // where the sine has the sign with which it multiplies the partner.  Angles as in kvd_rope_append: turns per position as
-// hi + lo, the rounding error of pos·hi from one fma.
+// hi + lo, the rounding error of pos·hi from one fma.  A lane makes one pair's, and the warp hands them round.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void lane_turns(float2 (&f)[8], const LatentAppendParams& p, float pos, int lane8) {
-    const int half = p.rot >> 1;
+__device__ __forceinline__ void lane_turns(float2 (&f)[8], const LatentAppendParams& p, float pos, int lane) {
+    const int half = p.rot >> 1, lane8 = lane & 7;
+    float2 mine = make_float2(1.f, 0.f);
+    if (lane < half) {
+        const float2 t = p.turns[lane];
+        const float a = __fmul_rn(pos, t.x);
+        const float rest = __fmaf_rn(pos, t.x, -a);
+        const float turn = __fadd_rn(__fsub_rn(a, rintf(a)), __fmaf_rn(pos, t.y, rest));
+        float sn, cn;
+        sincospif(2.f * turn, &sn, &cn);
+        mine = make_float2(cn * p.mscale, sn * p.mscale);
+    }
     #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        f[e] = make_float2(1.f, 0.f);
+    for (int e = 0; e < (INTERLEAVED ? 4 : 8); ++e) {
         const int d = lane8 * 8 + e;
         const int pair = INTERLEAVED ? lane8 * 4 + e : d < half ? d : d - half;
-        if (INTERLEAVED ? e < 4 && pair < half : d < p.rot) {
-            const float2 t = p.turns[pair];
-            const float a = __fmul_rn(pos, t.x);
-            const float rest = __fmaf_rn(pos, t.x, -a);
-            const float turn = __fadd_rn(__fsub_rn(a, rintf(a)), __fmaf_rn(pos, t.y, rest));
-            float sn, cn;
-            sincospif(2.f * turn, &sn, &cn);
-            f[e] = make_float2(cn * p.mscale, sn * p.mscale);
-            if (!INTERLEAVED && d < half) f[e].y = -f[e].y;
-        }
+        f[e] = make_float2(__shfl_sync(kFull, mine.x, pair & 31), __shfl_sync(kFull, mine.y, pair & 31));
+        if (!INTERLEAVED && d < half) f[e].y = -f[e].y;
     }
 }
 
@@ -101,9 +102,10 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float s) {
     return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
 }
 
-// A warp takes one token's latent and key part, or p.heads of its query heads, four at a time.
+// A warp takes one token's latent and key part, or p.heads of its query heads, four at a time.  Five CTAs an SM (48 registers; what
+// is spilled is the latent's): 26.2 us for the prompt above, with four 27.5, with six 26.4.
 template <bool FP8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendParams p) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const LatentAppendParams p) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, lane8 = lane & 7;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendPara
     float2 f[8];
     if (query) {
         const int h0 = static_cast<int>((task - p.n_tokens) % groups) * p.heads, h1 = min(h0 + p.heads, p.n_q);
-        lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane8);
+        lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane);
         const uint16_t* src = p.q_rope + n * p.q_stride;
         uint16_t* dst = p.q_out + n * p.out_stride;
         #pragma unroll 1
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const LatentAppendPara
     uint4 raw[2] = {ld16(row + lane * 8), ld16(row + 256 + lane * 8)};
     uint4 rot = lane < 8 ? ld16(key + lane8 * 8) : make_uint4(0, 0, 0, 0);
     if (p.turns) {
-        lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane8);
+        lane_turns<INTERLEAVED>(f, p, static_cast<float>(pos), lane);
         rot = rotate8<INTERLEAVED>(rot, f, p.rot, lane8, key, lane < 8);
     }
     float x[16];
