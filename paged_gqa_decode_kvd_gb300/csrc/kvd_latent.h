@@ -73,7 +73,7 @@ struct LatentAttnParams {
     const uint16_t* retain;      // [num_blocks] or null
     void* out;                   // [n_tokens][n_q][512]
     float* lse_out;              // [n_tokens][n_q] or null
-    float* part;                 // workspace: [2·CTAs][64 rows][512] unnormalised sums
+    float* part;                 // workspace: [2·CTAs][64 rows · 512] unnormalised sums, in the order of part_at
     float* part_ml;              // workspace: [2·CTAs][2][64] maximum (log2 domain), sum of weights
     int4* part_seg;              // workspace: [2·CTAs]
     int32_t* err;

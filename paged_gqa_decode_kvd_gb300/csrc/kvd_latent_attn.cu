@@ -24,9 +24,9 @@
 // 8 bits: converter warps load the codes (a tile under way while the one before it is converted) and store them as bf16, exactly, in the same
 // layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
 //
-// Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.0 TB/s (74% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 5 of
-// partials and join); 128 heads: 94 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 47 us, of it 13 until the
-// first tile is converted, 1.3 us a tile, 8 for 152 parts and their join.
+// Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.1 TB/s (75% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 7 of
+// partials and join); 128 heads: 94 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 46 us, of it 10 until the
+// first tile is converted, 1.3 us a tile, 8 for 147 parts and their join.
 //
 // Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (a try suspends 3.8 us; not while a
 // row is computed again, which ends by itself and takes 0.5 us a position); the kernel then reports it and ends.
@@ -140,6 +140,9 @@ struct Heads {
         blocks = (p.n_q + kRows - 1) / kRows;
         each = (p.n_q + blocks - 1) / blocks;
         tpb = kRows / each;
+        set(p, block);
+    }
+    __device__ __forceinline__ void set(const LatentAttnParams& p, int block) {
         first = block * each;
         n = min(each, p.n_q - first);
     }
@@ -247,6 +250,28 @@ __device__ inline bool find_share_small(const LatentAttnParams& p, const Heads& 
     const Request r = lane < p.B ? load_request(p, lane, blockIdx.x == 0 && threadIdx.x < 32) : Request{0, 0, -1};
     const Cost c = cost_of(r, hd.tpb);
     if (__any_sync(kFull, c.tiles >> 25 || c.units >> 23)) return false;
+    if (!__any_sync(kFull, c.units > 1)) {
+        // Whole shares for every unit, if that makes them no longer than another unit's start and end would: 3 x 16,384 positions,
+        // 64 heads 31.6 us (36.3 with shares of the sum), 4 x 4,000, 16 heads 16.3 (19.1).
+        const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks, n = static_cast<int>(c.tiles);
+        const int least = max((static_cast<int>(__reduce_add_sync(kFull, n)) + lanes - 1) / lanes, kMinShare);
+        auto ctas_of = [&](int share) { return (n + share - 1) / share; };
+        if (static_cast<int>(__reduce_add_sync(kFull, ctas_of(least + kUnitTiles))) <= lanes) {
+            int share = least;
+            while (static_cast<int>(__reduce_add_sync(kFull, ctas_of(share))) > lanes) ++share;
+            const int up = scan(ctas_of(share), lane);
+            const unsigned at = __ballot_sync(kFull, me < up);
+            if (at == 0) return true;
+            const int src = __ffs(at) - 1;
+            w.share = share;
+            w.at = static_cast<int64_t>(share) * me;
+            w.b = src;
+            w.r = {__shfl_sync(kFull, r.s0, src), __shfl_sync(kFull, r.T, src), __shfl_sync(kFull, r.len, src)};
+            w.off = (me - __shfl_sync(kFull, up - ctas_of(share), src)) * share;
+            w.remaining = min(share, __shfl_sync(kFull, n, src) - w.off);
+            return true;
+        }
+    }
     const int tiles = scan(static_cast<int>(c.tiles), lane), units = scan(c.units, lane);
     if (!set_share(w, __shfl_sync(kFull, tiles, 31), __shfl_sync(kFull, units, 31), hd)) return true;
     const int64_t up = tiles + static_cast<int64_t>(units) * w.extra;
@@ -309,9 +334,9 @@ __device__ __forceinline__ bool wait_bar(Smem& s, uint64_t* bar, uint32_t phase)
 }
 
 // ------------------------------------------------------------- one row, plainly
-// A warp a row (quarter ≥ 0: 128 of its dims): a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
+// A warp a row, of which it writes dims from .. to − 1 (and lse with the first): a lane has dims 8·lane .. +7 and 256 + 8·lane .. +7 of the latent, lanes 0 .. 7 the rotated ones.
 template <bool FP8>
-__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end, int quarter) {
+__device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t row, int end, int from, int to) {
     const int lane = threadIdx.x & 31;
     const uint16_t* qr = p.q + row * kLatKey;
     float q[24], acc[16], m = -INFINITY, sum = 0.f;
@@ -364,12 +389,12 @@ __device__ __noinline__ void plain_row(const LatentAttnParams& p, int b, int64_t
     #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int d = (i >> 3) * 256 + lane * 8 + (i & 7);
-        if (quarter >= 0 && d >> 7 != quarter) continue;
+        if (d < from || d >= to) continue;
         const int64_t at = row * kLatDim + d;
         if (p.out_f32) static_cast<float*>(p.out)[at] = acc[i] * inv;
         else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i] * inv);
     }
-    if (lane == 0 && quarter <= 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    if (lane == 0 && from == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // Whether a retained token of positions from .. to − 1 has a latent that is not finite; by a warp.
@@ -402,8 +427,8 @@ __device__ __noinline__ bool odd_tokens(const LatentAttnParams& p, int b, int fr
 // is NaN.  A row that came out as NaN is computed again, plainly, if such a token stands behind what it attends
 // (else it is NaN by right).  end: positions that the row attends; unit_end: that the unit's last row does.
 template <bool FP8>
-__device__ __forceinline__ void again(const LatentAttnParams& p, int b, int64_t row, int end, int unit_end, int quarter) {
-    if (odd_tokens<FP8>(p, b, end, unit_end)) plain_row<FP8>(p, b, row, end, quarter);
+__device__ __forceinline__ void again(const LatentAttnParams& p, int b, int64_t row, int end, int unit_end, int from, int to) {
+    if (odd_tokens<FP8>(p, b, end, unit_end)) plain_row<FP8>(p, b, row, end, from, to);
 }
 
 // ------------------------------------------------------------------ producer
@@ -681,6 +706,20 @@ __device__ __forceinline__ void value_issuer(Smem& s, const LatentAttnParams& p,
                 if (!wait_bar(s, &s.empty[k % kStages][i], k / kStages)) return;
 }
 
+// Four lanes side by side have a pair of dims each of four groups of eight: lane i gets group i whole.
+__device__ __forceinline__ uint4 whole_group(const uint32_t* t, int lane) {
+    const bool odd = lane & 1, high = lane & 2;
+    const uint32_t a = __shfl_xor_sync(kFull, odd ? t[0] : t[1], 1), b = __shfl_xor_sync(kFull, odd ? t[2] : t[3], 1);
+    const uint32_t x[4] = {odd ? a : t[0], odd ? t[1] : a, odd ? b : t[2], odd ? t[3] : b};
+    const uint32_t c = __shfl_xor_sync(kFull, high ? x[0] : x[2], 2), d = __shfl_xor_sync(kFull, high ? x[1] : x[3], 2);
+    return high ? make_uint4(c, d, x[2], x[3]) : make_uint4(x[0], x[1], c, d);
+}
+
+// Partials: four values a lane (of rows lane/4 and lane/4 + 8 of a group of 16 two dims each), 32 lanes for eight dims.
+__device__ __forceinline__ int64_t part_at(int64_t slot, int group, int eight, int lane) {
+    return ((slot * (kRows / 16) + group) * (kLatDim / 8) + eight) * 32 + lane;
+}
+
 // ------------------------------------------------------------------- softmax
 // 16 lanes × 64 columns: a thread has rows lane/4 and lane/4 + 8, of each column group of eight the two at 2·(lane%4):
 // v[4k], v[4k+1] of the first row, v[4k+2], v[4k+3] of the second.
@@ -905,35 +944,55 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
         const float inv[2] = {sum[0] == 0.f ? 0.f : 1.f / sum[0], sum[1] == 0.f ? 0.f : 1.f / sum[1]};
         float odd[2] = {0.f, 0.f};
         if (__any_sync(kFull, row[0] >= 0 || row[1] >= 0)) {
-            // sums as they are to the partials, or rows to out: a thread has a pair of every eight dims of two rows
-            const bool f32 = !whole || p.out_f32;
-            const float by[2] = {whole ? inv[0] : 1.f, whole ? inv[1] : 1.f};
-            uint8_t* dst[2];
-            #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = whole ? max(row[h], static_cast<int64_t>(0)) : static_cast<int64_t>(slot) * kRows + r0 + 8 * h;
-                dst[h] = (whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.part)) + (at * kLatDim + 2 * quad) * (f32 ? 4 : 2);
-            }
-            #pragma unroll 1
-            for (int c = 0; c < 512; c += 64) {
-                uint32_t v[32];
-                tmem_ld_16x64(mine + kHalf + c, v);
-                tmem_wait_ld(v);
+            if (!whole) {
+                // sums as they are to the partials, in this order: each store is 512 bytes in a row (as rows, in pieces of 32 bytes,
+                // 64 of them took 3.0 us)
+                float4* dst = reinterpret_cast<float4*>(p.part) + part_at(slot, warp, 0, lane);
+                #pragma unroll 1
+                for (int c = 0; c < 512; c += 64) {
+                    uint32_t v[32];
+                    tmem_ld_16x64(mine + kHalf + c, v);
+                    tmem_wait_ld(v);
+                    #pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[(c / 8 + k) * 32] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
+                                                            __uint_as_float(v[4 * k + 3]));
+                }
+            } else {
+                // rows to out: a thread has a pair of every eight dims of two rows
+                uint8_t* dst[2];
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float2 y[8];
+                    const int64_t at = max(row[h], static_cast<int64_t>(0)) * kLatDim;
+                    dst[h] = static_cast<uint8_t*>(p.out) + (p.out_f32 ? (at + 2 * quad) * 4 : (at + 8 * quad) * 2);
+                }
+                #pragma unroll 1
+                for (int c = 0; c < 512; c += 64) {
+                    uint32_t v[32];
+                    tmem_ld_16x64(mine + kHalf + c, v);
+                    tmem_wait_ld(v);
                     #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        y[k] = make_float2(__uint_as_float(v[4 * k + 2 * h]) * by[h], __uint_as_float(v[4 * k + 2 * h + 1]) * by[h]);
-                        odd[h] += y[k].x + y[k].y;
-                    }
-                    if (row[h] < 0) continue;
-                    if (f32) {
+                    for (int h = 0; h < 2; ++h) {
+                        float2 y[8];
                         #pragma unroll
-                        for (int k = 0; k < 8; ++k) *reinterpret_cast<float2*>(dst[h] + 4 * (c + 8 * k)) = y[k];
-                    } else {
-                        #pragma unroll
-                        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint32_t*>(dst[h] + 2 * (c + 8 * k)) = pack_bf16(y[k].x, y[k].y);
+                        for (int k = 0; k < 8; ++k) {
+                            y[k] = make_float2(__uint_as_float(v[4 * k + 2 * h]) * inv[h], __uint_as_float(v[4 * k + 2 * h + 1]) * inv[h]);
+                            odd[h] += y[k].x + y[k].y;
+                        }
+                        if (p.out_f32) {
+                            #pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (row[h] >= 0) *reinterpret_cast<float2*>(dst[h] + 4 * (c + 8 * k)) = y[k];
+                        } else {
+                            #pragma unroll
+                            for (int k = 0; k < 8; k += 4) {
+                                uint32_t t[4];
+                                #pragma unroll
+                                for (int i = 0; i < 4; ++i) t[i] = pack_bf16(y[k + i].x, y[k + i].y);
+                                const uint4 g8 = whole_group(t, lane);
+                                if (row[h] >= 0) *reinterpret_cast<uint4*>(dst[h] + 2 * (c + 8 * k)) = g8;
+                            }
+                        }
                     }
                 }
             }
@@ -948,7 +1007,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                     __syncwarp();
                     if (g.len < 0) continue;
                     if (lane == 0) atomicAdd(&s.again, 1);
-                    again<FP8>(p, g.b, row_of(p, hd, g, r), g.first + r / hd.each + 1, g.end, -1);
+                    again<FP8>(p, g.b, row_of(p, hd, g, r), g.first + r / hd.each + 1, g.end, 0, kLatDim);
                     if (lane == 0) atomicSub(&s.again, 1);
                 }
         }
@@ -1034,168 +1093,215 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
 }
 
 // Joins the parts of units that the schedule cut.  A CTA of the schedule starts at most one of them, as its last; the
-// others' parts are the following CTAs' first.  Rows of few parts are joined by a warp each, rows of many by four CTAs, 128 dims
-// each, whose warps share the parts.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kMaxCtas = 512;
+// others' parts are the following CTAs' first.  Units of few parts are joined 16 rows and 32 dims a warp, those of many 16 rows and
+// eight dims a CTA, whose warps share the parts.  Many are more than eight; where the rows are enough for the warps, more than an
+// eighth of the rows, up to 32: 768 rows of 13 parts by warps 61 us (the call), by CTAs 78; 64 of 32 parts 32 and 22.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kMaxCtas = 512, kJoinDims = 32;
 struct Join {
     int4 start[kMaxCtas];            // (request, first token, rows, parts) of the unit that the CTA starts
-    uint32_t rows[kMaxCtas];         // running counts of rows: of few parts, of many << 16
-    float part[kJoinWarps][128];
-    float weight[kMaxCtas], len[kMaxCtas];   // of a part: its factor, its sum
-    float top[kJoinWarps];
+    uint32_t groups[kMaxCtas];       // running counts of groups of 16 rows: of few parts, of many << 16
+    float4 part[kJoinWarps][32];
+    float top[kJoinWarps][16], sum[kJoinWarps][16];
 };
-__device__ __forceinline__ void put4(const LatentAttnParams& p, int64_t row, int d, float4 x, float inv) {
-    if (p.out_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kLatDim + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kLatDim + d) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+__device__ __forceinline__ void put2(const LatentAttnParams& p, int64_t row, int d, float x, float y, float inv) {
+    if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * kLatDim + d) = make_float2(x * inv, y * inv);
+    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * kLatDim + d) = pack_bf16(x * inv, y * inv);
+}
+// A CTA's k-th part of the unit that it starts: in its own second place, or in the first of the k-th CTA behind it.
+__device__ __forceinline__ int64_t slot_of(int cta, int k, int blocks) { return k == 0 ? 2 * cta + 1 : 2 * (cta + k * blocks); }
+// Parts from, from + step, .. of a group's dims 8·eight .. + 8·N − 1: sums, maximum and sum of weights of a lane's two rows, BATCH parts'
+// loads under way at a time.
+template <int N, int BATCH>
+__device__ __forceinline__ void join_parts(const LatentAttnParams& p, int cta, int blocks, int parts, int from, int step, int group, int eight,
+                                           int lane, float4 (&acc)[N], float (&top)[2], float (&sum)[2]) {
+    #pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    top[0] = top[1] = -INFINITY;
+    sum[0] = sum[1] = 0.f;
+    #pragma unroll 1
+    for (int k = from; k < parts; k += BATCH * step) {
+        float4 x[BATCH][N];
+        float m[BATCH][2], l[BATCH][2];
+        #pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const bool on = k + b * step < parts;
+            const int64_t slot = slot_of(cta, on ? k + b * step : k, blocks);
+            const float* ml = p.part_ml + slot * 2 * kRows + group * 16 + (lane >> 2);
+            const float4* src = reinterpret_cast<const float4*>(p.part) + part_at(slot, group, eight, lane);
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m[b][h] = on ? ml[8 * h] : -INFINITY;
+                l[b][h] = on ? ml[kRows + 8 * h] : 0.f;
+            }
+            #pragma unroll
+            for (int j = 0; j < N; ++j) x[b][j] = on ? src[32 * j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float z[2];
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float was = top[h];
+            #pragma unroll
+            for (int b = 0; b < BATCH; ++b) top[h] = fmaxf(top[h], m[b][h]);
+            z[h] = top[h] == -INFINITY ? 0.f : top[h];
+            const float f = ex2(was - z[h]);
+            sum[h] *= f;
+            #pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (h == 0) acc[j].x *= f, acc[j].y *= f;
+                else acc[j].z *= f, acc[j].w *= f;
+        }
+        #pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const float f0 = ex2(m[b][0] - z[0]), f1 = ex2(m[b][1] - z[1]);
+            sum[0] = fmaf(f0, l[b][0], sum[0]);
+            sum[1] = fmaf(f1, l[b][1], sum[1]);
+            #pragma unroll
+            for (int j = 0; j < N; ++j)
+                acc[j] = make_float4(fmaf(f0, x[b][j].x, acc[j].x), fmaf(f0, x[b][j].y, acc[j].y), fmaf(f1, x[b][j].z, acc[j].z), fmaf(f1, x[b][j].w, acc[j].w));
+        }
+    }
 }
 template <bool FP8>
-__device__ __noinline__ void join_again(const LatentAttnParams& p, const int4& g, const Heads& hd, int r, int64_t row, int quarter) {
+__device__ __noinline__ void join_again(const LatentAttnParams& p, const int4& g, const Heads& hd, int r, int64_t row, int from, int to) {
     const Request q = load_request(p, g.x, false);
     const int tok0 = g.y - q.s0, first = q.len - q.T;
-    if (q.len >= 0) again<FP8>(p, g.x, row, first + tok0 + r / hd.each + 1, first + min(tok0 + hd.tpb, q.T), quarter);
+    if (q.len >= 0) again<FP8>(p, g.x, row, first + tok0 + r / hd.each + 1, first + min(tok0 + hd.tpb, q.T), from, to);
+}
+
+// Row of out of row r of the unit, or −1.  by_each: ⌈2^16/heads of a token⌉, whose product with r < 64 has r/heads above bit 16.
+__device__ __forceinline__ int64_t join_row(const LatentAttnParams& p, const int4& g, const Heads& hd, int by_each, int r) {
+    const int tok = r * by_each >> 16, h = r - tok * hd.each;
+    return r < g.z && h < hd.n ? (static_cast<int64_t>(g.y) + tok) * p.n_q + hd.first + h : -1;
+}
+// 16 rows and 32 dims, by a warp.
+template <bool FP8>
+__device__ __forceinline__ void join_few(const LatentAttnParams& p, const int4& g, const Heads& hd, int by_each, int cta, int group, int chunk) {
+    constexpr int kN = kJoinDims / 8;
+    static_assert(kN == 4, "whole_group's");
+    const int lane = threadIdx.x & 31, quad = lane & 3, r0 = group * 16 + (lane >> 2);
+    float4 acc[kN];
+    float top[2], sum[2];
+    join_parts<kN, 2>(p, cta, hd.blocks, g.w, 0, 1, group, kN * chunk, lane, acc, top, sum);
+    const int64_t row[2] = {join_row(p, g, hd, by_each, r0), join_row(p, g, hd, by_each, r0 + 8)};
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];
+        float odd = 0.f;
+        uint32_t t[kN];
+        #pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const float a = h ? acc[j].z : acc[j].x, b = h ? acc[j].w : acc[j].y;
+            odd += a + b;
+            t[j] = pack_bf16(a * inv, b * inv);
+            if (p.out_f32 && row[h] >= 0) put2(p, row[h], kJoinDims * chunk + 8 * j + 2 * quad, a, b, inv);
+        }
+        if (!p.out_f32) {
+            const uint4 g8 = whole_group(t, lane);
+            if (row[h] >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row[h] * kLatDim + kJoinDims * chunk + 8 * quad) = g8;
+        }
+        if (row[h] >= 0 && chunk == 0 && quad == 0 && p.lse_out) p.lse_out[row[h]] = sum[h] == 0.f ? -INFINITY : (top[h] + log2f(sum[h])) * kLn2;
+        for (unsigned todo = __ballot_sync(kFull, row[h] >= 0 && odd != odd); todo;) {
+            const int i = (__ffs(todo) - 1) >> 2, r = group * 16 + 8 * h + i;
+            todo &= ~(15u << 4 * i);
+            __syncwarp();
+            join_again<FP8>(p, g, hd, r, join_row(p, g, hd, by_each, r), kJoinDims * chunk, kJoinDims * (chunk + 1));
+        }
+    }
+}
+// 16 rows and eight dims, by a CTA.
+template <bool FP8>
+__device__ __forceinline__ void join_many(Join& s, const LatentAttnParams& p, const int4& g, const Heads& hd, int by_each, int cta, int group, int eight) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = lane & 3, i0 = lane >> 2;
+    float4 acc[1];
+    float top[2], sum[2];
+    join_parts<1, 8>(p, cta, hd.blocks, g.w, warp, kJoinWarps, group, eight, lane, acc, top, sum);
+    __syncthreads();   // what the one before left has been read
+    s.part[warp][lane] = acc[0];
+    if (quad == 0) {
+        s.top[warp][i0] = top[0];
+        s.top[warp][i0 + 8] = top[1];
+        s.sum[warp][i0] = sum[0];
+        s.sum[warp][i0 + 8] = sum[1];
+    }
+    __syncthreads();
+    // a warp (of the first eight) writes rows `warp` and `warp` + 8 of the group, eight lanes the eight dims of both
+    float odd = 0.f;
+    if (lane < 8 && warp < 8) {
+        const int h = lane >> 2, i = warp + 8 * h;
+        float a = 0.f, b = 0.f, l = 0.f, m = s.top[0][i];
+        #pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) m = fmaxf(m, s.top[k][i]);
+        #pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) {
+            const float4 x = s.part[k][4 * warp + quad];
+            const float f = ex2(s.top[k][i] - (m == -INFINITY ? 0.f : m));
+            a = fmaf(f, h ? x.z : x.x, a);
+            b = fmaf(f, h ? x.w : x.y, b);
+            l = fmaf(f, s.sum[k][i], l);
+        }
+        const int64_t row = join_row(p, g, hd, by_each, group * 16 + i);
+        if (row >= 0) {
+            put2(p, row, 8 * eight + 2 * quad, a, b, l == 0.f ? 0.f : 1.f / l);
+            if (eight == 0 && quad == 0 && p.lse_out) p.lse_out[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            odd = a + b;
+        }
+    }
+    for (unsigned todo = __ballot_sync(kFull, odd != odd); todo;) {
+        const int h = (__ffs(todo) - 1) >> 2, r = group * 16 + warp + 8 * h;
+        todo &= ~(15u << 4 * h);
+        __syncwarp();
+        join_again<FP8>(p, g, hd, r, join_row(p, g, hd, by_each, r), 8 * eight, 8 * eight + 8);
+    }
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const LatentAttnParams p, int ctas) {
     __shared__ Join s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Heads hd(p, 0);
+    const int by_each = ((1 << 16) + hd.each - 1) / hd.each;
     pdl_wait();
     pdl_trigger();
+    const int few = static_cast<int>(min(max(static_cast<int64_t>(p.n_tokens) * p.n_q / 8, static_cast<int64_t>(8)), static_cast<int64_t>(32)));
     for (int i = tid; i < ctas; i += kJoinThreads) {
         const int4 g = p.part_seg[2 * i + 1];
+        const uint32_t n = static_cast<uint32_t>(g.z + 15) / 16;
         s.start[i] = g;
-        s.rows[i] = g.x < 0 ? 0u : g.w <= kJoinWarps ? static_cast<uint32_t>(g.z) : static_cast<uint32_t>(g.z) << 16;
+        s.groups[i] = g.x < 0 ? 0u : g.w <= few ? n : n << 16;
     }
     __syncthreads();
     if (warp == 0) {
         uint32_t before = 0;
         for (int i = lane; i - lane < ctas; i += 32) {
-            uint32_t up = i < ctas ? s.rows[i] : 0;
-            #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(kFull, up, o);
-                if (lane >= o) up += v;
-            }
-            up += before;
-            if (i < ctas) s.rows[i] = up;
+            const uint32_t up = before + scan(i < ctas ? s.groups[i] : 0u, lane);
+            if (i < ctas) s.groups[i] = up;
             before = __shfl_sync(kFull, up, 31);
         }
     }
     __syncthreads();
-    const int blocks = (p.n_q + kRows - 1) / kRows;
-    const uint32_t total = s.rows[ctas - 1];
-    auto unit_of = [&](int item, int shift, int& r) {   // the CTA that starts the item's unit, and the row
+    const uint32_t total = s.groups[ctas - 1];
+    auto unit_of = [&](int n, int shift, int& group) {   // the CTA that starts group n's unit, and the group in it
         int a = 0, z = ctas - 1;
         while (a < z) {
             const int mid = (a + z) >> 1;
-            if (static_cast<int>(s.rows[mid] >> shift & 0xffffu) > item) z = mid;
+            if (static_cast<int>(s.groups[mid] >> shift & 0xffffu) > n) z = mid;
             else a = mid + 1;
         }
-        r = item - (a > 0 ? static_cast<int>(s.rows[a - 1] >> shift & 0xffffu) : 0);
+        group = n - (a > 0 ? static_cast<int>(s.groups[a - 1] >> shift & 0xffffu) : 0);
         return a;
     };
-    auto slot_of = [&](int cta, int k) -> int64_t { return k == 0 ? 2 * cta + 1 : 2 * (cta + k * blocks); };
-    auto place = [&](const int4& g, const Heads& hd, int r) -> int64_t {   // row of out, or −1
-        const int tok = r / hd.each, h = r - tok * hd.each;
-        return h < hd.n ? (static_cast<int64_t>(g.y) + tok) * p.n_q + hd.first + h : -1;
-    };
-    for (int item = blockIdx.x * kJoinWarps + warp; item < static_cast<int>(total & 0xffffu); item += gridDim.x * kJoinWarps) {
-        int r;
-        const int cta = unit_of(item, 0, r);
-        const int4 g = s.start[cta];
-        const Heads hd(p, cta % blocks);
-        const int64_t row = place(g, hd, r);
-        if (row < 0) continue;
-        const int64_t mine = slot_of(cta, min(lane, g.w - 1));
-        const float m = p.part_ml[mine * 2 * kRows + r], l = p.part_ml[(mine * 2 + 1) * kRows + r];
-        float4 acc[4], x[2][4];
-        #pragma unroll
-        for (int k = 0; k < 2; ++k)   // (a cut unit has two parts at least)
-            #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[k][j] = *reinterpret_cast<const float4*>(p.part + (slot_of(cta, k) * kRows + r) * kLatDim + 4 * lane + 128 * j);
-        float top = m;
-        #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const float w = ex2(m - (top == -INFINITY ? 0.f : top));
-        float sum = lane < g.w ? w * l : 0.f;
-        #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        const float w0 = __shfl_sync(kFull, w, 0), w1 = __shfl_sync(kFull, w, 1);
-        #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[j] = make_float4(fmaf(w1, x[1][j].x, w0 * x[0][j].x), fmaf(w1, x[1][j].y, w0 * x[0][j].y),
-                                 fmaf(w1, x[1][j].z, w0 * x[0][j].z), fmaf(w1, x[1][j].w, w0 * x[0][j].w));
-        #pragma unroll 2
-        for (int k = 2; k < g.w; ++k) {
-            const float f = __shfl_sync(kFull, w, k);
-            const float* src = p.part + (slot_of(cta, k) * kRows + r) * kLatDim + 4 * lane;
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 o = *reinterpret_cast<const float4*>(src + 128 * j);
-                acc[j] = make_float4(fmaf(f, o.x, acc[j].x), fmaf(f, o.y, acc[j].y), fmaf(f, o.z, acc[j].z), fmaf(f, o.w, acc[j].w));
-            }
-        }
-        float odd = 0.f;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            odd += acc[j].x + acc[j].y + acc[j].z + acc[j].w;
-            put4(p, row, 4 * lane + 128 * j, acc[j], inv);
-        }
-        if (lane == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        if (__any_sync(kFull, odd != odd)) join_again<FP8>(p, g, hd, r, row, -1);
+    constexpr int kChunks = kLatDim / kJoinDims, kEights = kLatDim / 8;
+    for (int item = blockIdx.x * kJoinWarps + warp; item < kChunks * static_cast<int>(total & 0xffffu); item += gridDim.x * kJoinWarps) {
+        int group;
+        const int cta = unit_of(item / kChunks, 0, group);
+        if (hd.blocks > 1) hd.set(p, cta % hd.blocks);
+        join_few<FP8>(p, s.start[cta], hd, by_each, cta, group, item % kChunks);
     }
-    for (int item = blockIdx.x; item < 4 * static_cast<int>(total >> 16); item += gridDim.x) {
-        int r;
-        const int cta = unit_of(item >> 2, 16, r), quarter = item & 3;
-        const int4 g = s.start[cta];
-        const Heads hd(p, cta % blocks);
-        const int64_t row = place(g, hd, r);
-        if (row < 0) continue;
-        __syncthreads();   // the row before has been read
-        float top = -INFINITY;
-        for (int k = tid; k < g.w; k += kJoinThreads) {
-            const int64_t sl = slot_of(cta, k);
-            const float m = p.part_ml[sl * 2 * kRows + r];
-            s.weight[k] = m;
-            s.len[k] = p.part_ml[(sl * 2 + 1) * kRows + r];
-            top = fmaxf(top, m);
-        }
-        #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        if (lane == 0) s.top[warp] = top;
-        __syncthreads();
-        #pragma unroll
-        for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, s.top[k]);
-        const float z = top == -INFINITY ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        #pragma unroll 8
-        for (int k = warp; k < g.w; k += kJoinWarps) {
-            const float f = ex2(s.weight[k] - z);
-            const float4 o = *reinterpret_cast<const float4*>(p.part + (slot_of(cta, k) * kRows + r) * kLatDim + quarter * 128 + 4 * lane);
-            acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
-        }
-        *reinterpret_cast<float4*>(&s.part[warp][4 * lane]) = acc;
-        __syncthreads();
-        if (warp == 0) {
-            float sum = 0.f;
-            for (int k = lane; k < g.w; k += 32) sum = fmaf(ex2(s.weight[k] - z), s.len[k], sum);
-            #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) {
-                const float4 o = *reinterpret_cast<const float4*>(&s.part[k][4 * lane]);
-                y = make_float4(y.x + o.x, y.y + o.y, y.z + o.z, y.w + o.w);
-            }
-            put4(p, row, quarter * 128 + 4 * lane, y, sum == 0.f ? 0.f : 1.f / sum);
-            if (lane == 0 && quarter == 0 && p.lse_out) p.lse_out[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-            const float odd = y.x + y.y + y.z + y.w;
-            if (__any_sync(kFull, odd != odd)) join_again<FP8>(p, g, hd, r, row, quarter);
-        }
+    for (int item = blockIdx.x; item < kEights * static_cast<int>(total >> 16); item += gridDim.x) {
+        int group;
+        const int cta = unit_of(item / kEights, 16, group);
+        if (hd.blocks > 1) hd.set(p, cta % hd.blocks);
+        join_many<FP8>(s, p, s.start[cta], hd, by_each, cta, group, item % kEights);
     }
 }
 

@@ -322,6 +322,19 @@ def test_attn_long_rows_are_cut_and_joined(cuda_device, kind):
 
 
 @KINDS
+@pytest.mark.parametrize("n_q,q_lens,lens", [
+    (64, [1] * 12, [4096] * 12), (40, [1] * 9, [5000, 37, 2300, 1, 0, 4100, 3000, 5001, 64]), (128, [1] * 3, [2500, 40, 3000]),
+    (16, [1] * 4, [4000] * 4), (5, [2, 2, 0, 1], [3000, 2, 0, 2999]), (70, [3] * 4, [2100] * 4), (1, [1] * 32, [1500] * 32)])
+def test_attn_cut_units(cuda_device, kind, n_q, q_lens, lens):
+    """Few requests, whose units get whole shares, and cut ones: joins of few and of many parts, of few and of many rows."""
+    q_lens = [q if n else 0 for q, n in zip(q_lens, lens)]
+    c = Attn(cuda_device, kind, n_q, q_lens, lens, seed=n_q + len(lens), evict=0.05)
+    c.check(torch.bfloat16, device=cuda_device)
+    c.check(device=cuda_device)
+    ok(c.pool)
+
+
+@KINDS
 def test_attn_growing_logits_move_the_reference(cuda_device, kind):
     """Each tile's maximum passes the last one's by more than the lazy border, so O is rescaled many times."""
     dev, n = cuda_device, 900
