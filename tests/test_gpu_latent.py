@@ -661,6 +661,23 @@ def test_prefill_growing_logits_move_the_reference(cuda_device):
     c.check(scale=-0.5, causal=False)
 
 
+@pytest.mark.parametrize("n_q,q_lens,kv_lens", [
+    (3, [100, 300, 1], [900, 1000, 5000]), (40, [33] * 6, [2000] * 6), (40, [128, 129, 384, 20], [640, 640, 900, 3000]),
+    (1, [128], [513]), (2, [60], [511]), (1, [1], [385]), (32, [1, 2] * 10, [600, 1300] * 10), (9, [390, 64, 700, 5] * 5, [390, 777, 5000, 640] * 5)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_few_rows_behind_many_keys(cuda_device, n_q, q_lens, kv_lens, causal):
+    """Rows of one warpgroup alone, over several tiles of keys."""
+    c = Prefill(cuda_device, n_q, q_lens, kv_lens, seed=n_q + 1)
+    c.check(causal)
+    c.check(causal, torch.bfloat16)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("T,N,j", [(100, 700, 60), (60, 513, 1), (128, 1000, 127)])
+def test_prefill_later_tokens_behind_many_keys(cuda_device, bad, T, N, j):
+    test_prefill_later_tokens_do_not_reach_earlier_rows(cuda_device, bad, T, N, j)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("T,N,j", [(100, 100, 50), (300, 400, 150), (300, 300, 299), (2, 130, 1)])
 def test_prefill_later_tokens_do_not_reach_earlier_rows(cuda_device, bad, T, N, j):
