@@ -19,12 +19,12 @@
 // S, 16 .. 31 hold O.  An MMA with M = 64 takes as long as one with M = 128 (33 cycles for N = 64, 129 for N = 256), so the matrix rate ends at
 // half; that is enough up to 64 heads: a tile's MMAs take 2,240 cycles (1.15 us), its way through HBM 1.65 us.
 // Rounding.  K, C and Q enter the products exactly, logits, statistics and sums are fp32, a weight enters as one bf16 (off by at most 2^-8 of
-// itself; its sum is taken before).  Outputs are 1.05 to 1.3 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 a weight, as
+// itself; its sum is taken before).  Outputs are 1.05 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 a weight, as
 // the chunk kernel has, would make O's MMAs 2,060 cycles a tile instead of 1,030, more than the cache's own time.
 // 8 bits: converter warps load the codes (a tile under way while the one before it is converted) and store them as bf16, exactly, in the same
 // layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
 //
-// Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.1 TB/s (75% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 7 of
+// Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.0 TB/s (74% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 7 of
 // partials and join); 128 heads: 94 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 46 us, of it 10 until the
 // first tile is converted, 1.3 us a tile, 8 for 147 parts and their join.
 //

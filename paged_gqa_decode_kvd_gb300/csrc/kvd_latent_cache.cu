@@ -7,7 +7,7 @@
 //   rounded once from fp32, and r in bf16.
 // Read back: y (code·s, rounded to bf16) and r, side by side.
 //
-// Bound: HBM.  4,099 tokens into 8 bits with 128 heads' queries: 26 us, 5.4 TB/s (80% of measured: 67 MB of queries are read and written in
+// Bound: HBM.  4,099 tokens into 8 bits with 128 heads' queries: 26.6 us, 5.3 TB/s (78% of measured: 67 MB of queries are read and written in
 // pieces of 128 bytes); a decode step of 32 tokens: 2.6 us in a graph, 11 with the host call.  226,000 rows of 24 requests from 8 bits: 64 us,
 // 6.3 TB/s (93%).
 #include "kvd_common.cuh"
