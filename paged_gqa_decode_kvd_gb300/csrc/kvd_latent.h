@@ -74,7 +74,7 @@ struct LatentAttnParams {
     void* out;                   // [n_tokens][n_q][512]
     float* lse_out;              // [n_tokens][n_q] or null
     float* part;                 // workspace: [2·CTAs][64 rows · 512] unnormalised sums, in the order of part_at
-    float* part_ml;              // workspace: [2·CTAs][2][64] maximum (log2 domain), sum of weights
+    float* part_ml;              // workspace: [2·CTAs][3][64] maximum (log2 domain), sum of weights, of rounded ones
     int4* part_seg;              // workspace: [2·CTAs]
     int32_t* err;
     int64_t num_blocks;

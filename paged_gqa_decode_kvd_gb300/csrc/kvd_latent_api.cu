@@ -40,7 +40,7 @@ LatentLayout latent_layout(const kvd_pool* pool) {
     LatentLayout w;
     w.part = 0;
     w.ml = align256(w.part + slots * kLatUnitRows * kLatDim * sizeof(float));
-    w.seg = align256(w.ml + slots * kLatUnitRows * 2 * sizeof(float));
+    w.seg = align256(w.ml + slots * kLatUnitRows * 3 * sizeof(float));
     w.total = align256(w.seg + slots * sizeof(int4));
     return w;
 }

@@ -19,7 +19,9 @@
 // S, 16 .. 31 hold O.  An MMA with M = 64 takes as long as one with M = 128 (33 cycles for N = 64, 129 for N = 256), so the matrix rate ends at
 // half; that is enough up to 64 heads: a tile's MMAs take 2,240 cycles (1.15 us), its way through HBM 1.65 us.
 // Rounding.  K, C and Q enter the products exactly, logits, statistics and sums are fp32, a weight enters as one bf16 (off by at most 2^-8 of
-// itself; its sum is taken before).  Outputs are 1.05 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 a weight, as
+// itself; in 8 bits with its token's scale).  out is divided by the sum of the weights as they were rounded, so that what all of a row's
+// weight is on comes out exactly; lse is that of the weights before.  Outputs are 1.1 to 1.35 times as far from 64 bits as an fp32 form's
+// rounded to bf16 (divided by the sum before: up to 1.8 in 8 bits; 1 to 2 us less a call).  Two bf16 a weight, as
 // the chunk kernel has, would make O's MMAs 2,060 cycles a tile instead of 1,030, more than the cache's own time.
 // 8 bits: converter warps load the codes (a tile under way while the one before it is converted) and store them as bf16, exactly, in the same
 // layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
@@ -64,6 +66,7 @@ __device__ __forceinline__ void unpack8(float* x, uint4 v) {
 
 struct Info {
     alignas(16) float scale[kTile];    // 8-bit records: by column
+    float by[kTile];                   // 1/scale, or 0 where that is no number
     unsigned long long mask;           // bit 16·block + t: position may be attended by the unit's last row
     int base;                          // position of column 0
     int id[4];                         // physical blocks, −1: none
@@ -597,7 +600,12 @@ __device__ __forceinline__ bool store_raw(Smem& s, const Raw& x, uint32_t n, int
     }
     #pragma unroll
     for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(group + 8192 + (2 * j + i) * 16) = x.rot[i];   // (in its order already)
-    if (j == 0) s.info[n % infos_of(true)].scale[warp * 8 + r] = x.scale;
+    if (j == 0) {
+        Info& info = s.info[n % infos_of(true)];
+        const float by = 1.f / x.scale;
+        info.scale[warp * 8 + r] = x.scale;
+        info.by[warp * 8 + r] = isfinite(by) ? by : 0.f;
+    }
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.ready[st]);
@@ -804,7 +812,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
     while (ok && more) {
         const int r0 = warp * 16 + (lane >> 2);
         const int limit[2] = {g.first + r0 / hd.each, g.first + (r0 + 8) / hd.each};   // positions that the rows attend, at most
-        float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, cut[2] = {0.f, 0.f};   // sums of weights, of rounded weights
         #pragma unroll 1
         for (int t = g.t0; t < g.t1; ++t, ++n) {
             const uint32_t st = n % kStages;
@@ -864,6 +872,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                 if (top[h] > ref[h] + kLazy) {
                     factor[h] = ex2(ref[h] - top[h]);
                     sum[h] *= factor[h];
+                    cut[h] *= factor[h];
                     ref[h] = top[h];
                     moved = true;
                 }
@@ -872,18 +881,21 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             uint32_t w[16];
             #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                float a = ex2(x[4 * k] - z0), b = ex2(x[4 * k + 1] - z0), c = ex2(x[4 * k + 2] - z1), d = ex2(x[4 * k + 3] - z1);
+                const float a = ex2(x[4 * k] - z0), b = ex2(x[4 * k + 1] - z0), c = ex2(x[4 * k + 2] - z1), d = ex2(x[4 * k + 3] - z1);
                 sum[0] += a + b;
                 sum[1] += c + d;
-                if constexpr (FP8) {
-                    const float2 f = *reinterpret_cast<const float2*>(&info.scale[8 * k + 2 * quad]);
-                    a *= f.x;
-                    b *= f.y;
-                    c *= f.x;
-                    d *= f.y;
+                const float2 f = FP8 ? *reinterpret_cast<const float2*>(&info.scale[8 * k + 2 * quad]) : make_float2(1.f, 1.f);
+                w[2 * k] = FP8 ? pack_bf16(a * f.x, b * f.y) : pack_bf16(a, b);
+                w[2 * k + 1] = FP8 ? pack_bf16(c * f.x, d * f.y) : pack_bf16(c, d);
+                const float2 p0 = unpack_bf16(w[2 * k]), p1 = unpack_bf16(w[2 * k + 1]);
+                if constexpr (FP8) {   // (without a factor of a normal size the weight itself)
+                    const float2 by = *reinterpret_cast<const float2*>(&info.by[8 * k + 2 * quad]);
+                    cut[0] += (by.x != 0.f ? p0.x * by.x : a) + (by.y != 0.f ? p0.y * by.y : b);
+                    cut[1] += (by.x != 0.f ? p1.x * by.x : c) + (by.y != 0.f ? p1.y * by.y : d);
+                } else {
+                    cut[0] += p0.x + p0.y;
+                    cut[1] += p1.x + p1.y;
                 }
-                w[2 * k] = pack_bf16(a, b);
-                w[2 * k + 1] = pack_bf16(c, d);
             }
             if (n > 0) ok = wait_bar(s, &s.empty[(n - 1) % kStages][3], (n - 1) / kStages);   // P and O are free
             if (!ok) break;
@@ -927,21 +939,25 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
         for (int h = 0; h < 2; ++h) {
             sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
             sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
+            cut[h] += __shfl_xor_sync(kFull, cut[h], 1);
+            cut[h] += __shfl_xor_sync(kFull, cut[h], 2);
         }
         if (!whole) {
             if (warp == 0 && lane == 0) p.part_seg[slot] = make_int4(g.b, g.s0 + g.tok0, min(hd.tpb, g.T - g.tok0) * hd.each, walk.parts(g));
             #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (quad == 0) {
-                    p.part_ml[(static_cast<int64_t>(slot) * 2) * kRows + r0 + 8 * h] = ref[h];
-                    p.part_ml[(static_cast<int64_t>(slot) * 2 + 1) * kRows + r0 + 8 * h] = sum[h];
+                    float* ml = p.part_ml + static_cast<int64_t>(slot) * 3 * kRows + r0 + 8 * h;
+                    ml[0] = ref[h];
+                    ml[kRows] = sum[h];
+                    ml[2 * kRows] = cut[h];
                 }
         } else if (quad == 0 && p.lse_out) {
             #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (row[h] >= 0) p.lse_out[row[h]] = sum[h] == 0.f ? -INFINITY : (ref[h] + log2f(sum[h])) * kLn2;
         }
-        const float inv[2] = {sum[0] == 0.f ? 0.f : 1.f / sum[0], sum[1] == 0.f ? 0.f : 1.f / sum[1]};
+        const float inv[2] = {cut[0] == 0.f ? 0.f : 1.f / cut[0], cut[1] == 0.f ? 0.f : 1.f / cut[1]};
         float odd[2] = {0.f, 0.f};
         if (__any_sync(kFull, row[0] >= 0 || row[1] >= 0)) {
             if (!whole) {
@@ -1101,7 +1117,7 @@ struct Join {
     int4 start[kMaxCtas];            // (request, first token, rows, parts) of the unit that the CTA starts
     uint32_t groups[kMaxCtas];       // running counts of groups of 16 rows: of few parts, of many << 16
     float4 part[kJoinWarps][32];
-    float top[kJoinWarps][16], sum[kJoinWarps][16];
+    float top[kJoinWarps][16], sum[kJoinWarps][16], cut[kJoinWarps][16];
 };
 __device__ __forceinline__ void put2(const LatentAttnParams& p, int64_t row, int d, float x, float y, float inv) {
     if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * kLatDim + d) = make_float2(x * inv, y * inv);
@@ -1109,29 +1125,30 @@ __device__ __forceinline__ void put2(const LatentAttnParams& p, int64_t row, int
 }
 // A CTA's k-th part of the unit that it starts: in its own second place, or in the first of the k-th CTA behind it.
 __device__ __forceinline__ int64_t slot_of(int cta, int k, int blocks) { return k == 0 ? 2 * cta + 1 : 2 * (cta + k * blocks); }
-// Parts from, from + step, .. of a group's dims 8·eight .. + 8·N − 1: sums, maximum and sum of weights of a lane's two rows, BATCH parts'
+// Parts from, from + step, .. of a group's dims 8·eight .. + 8·N − 1: sums, maximum and sums of weights of a lane's two rows, BATCH parts'
 // loads under way at a time.
 template <int N, int BATCH>
 __device__ __forceinline__ void join_parts(const LatentAttnParams& p, int cta, int blocks, int parts, int from, int step, int group, int eight,
-                                           int lane, float4 (&acc)[N], float (&top)[2], float (&sum)[2]) {
+                                           int lane, float4 (&acc)[N], float (&top)[2], float (&sum)[2], float (&cut)[2]) {
     #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     top[0] = top[1] = -INFINITY;
-    sum[0] = sum[1] = 0.f;
+    sum[0] = sum[1] = cut[0] = cut[1] = 0.f;
     #pragma unroll 1
     for (int k = from; k < parts; k += BATCH * step) {
         float4 x[BATCH][N];
-        float m[BATCH][2], l[BATCH][2];
+        float m[BATCH][2], l[BATCH][2], c[BATCH][2];
         #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const bool on = k + b * step < parts;
             const int64_t slot = slot_of(cta, on ? k + b * step : k, blocks);
-            const float* ml = p.part_ml + slot * 2 * kRows + group * 16 + (lane >> 2);
+            const float* ml = p.part_ml + slot * 3 * kRows + group * 16 + (lane >> 2);
             const float4* src = reinterpret_cast<const float4*>(p.part) + part_at(slot, group, eight, lane);
             #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 m[b][h] = on ? ml[8 * h] : -INFINITY;
                 l[b][h] = on ? ml[kRows + 8 * h] : 0.f;
+                c[b][h] = on ? ml[2 * kRows + 8 * h] : 0.f;
             }
             #pragma unroll
             for (int j = 0; j < N; ++j) x[b][j] = on ? src[32 * j] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1145,6 +1162,7 @@ __device__ __forceinline__ void join_parts(const LatentAttnParams& p, int cta, i
             z[h] = top[h] == -INFINITY ? 0.f : top[h];
             const float f = ex2(was - z[h]);
             sum[h] *= f;
+            cut[h] *= f;
             #pragma unroll
             for (int j = 0; j < N; ++j)
                 if (h == 0) acc[j].x *= f, acc[j].y *= f;
@@ -1155,6 +1173,8 @@ __device__ __forceinline__ void join_parts(const LatentAttnParams& p, int cta, i
             const float f0 = ex2(m[b][0] - z[0]), f1 = ex2(m[b][1] - z[1]);
             sum[0] = fmaf(f0, l[b][0], sum[0]);
             sum[1] = fmaf(f1, l[b][1], sum[1]);
+            cut[0] = fmaf(f0, c[b][0], cut[0]);
+            cut[1] = fmaf(f1, c[b][1], cut[1]);
             #pragma unroll
             for (int j = 0; j < N; ++j)
                 acc[j] = make_float4(fmaf(f0, x[b][j].x, acc[j].x), fmaf(f0, x[b][j].y, acc[j].y), fmaf(f1, x[b][j].z, acc[j].z), fmaf(f1, x[b][j].w, acc[j].w));
@@ -1180,12 +1200,12 @@ __device__ __forceinline__ void join_few(const LatentAttnParams& p, const int4& 
     static_assert(kN == 4, "whole_group's");
     const int lane = threadIdx.x & 31, quad = lane & 3, r0 = group * 16 + (lane >> 2);
     float4 acc[kN];
-    float top[2], sum[2];
-    join_parts<kN, 2>(p, cta, hd.blocks, g.w, 0, 1, group, kN * chunk, lane, acc, top, sum);
+    float top[2], sum[2], cut[2];
+    join_parts<kN, 2>(p, cta, hd.blocks, g.w, 0, 1, group, kN * chunk, lane, acc, top, sum, cut);
     const int64_t row[2] = {join_row(p, g, hd, by_each, r0), join_row(p, g, hd, by_each, r0 + 8)};
     #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];
+        const float inv = cut[h] == 0.f ? 0.f : 1.f / cut[h];
         float odd = 0.f;
         uint32_t t[kN];
         #pragma unroll
@@ -1213,8 +1233,8 @@ template <bool FP8>
 __device__ __forceinline__ void join_many(Join& s, const LatentAttnParams& p, const int4& g, const Heads& hd, int by_each, int cta, int group, int eight) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = lane & 3, i0 = lane >> 2;
     float4 acc[1];
-    float top[2], sum[2];
-    join_parts<1, 8>(p, cta, hd.blocks, g.w, warp, kJoinWarps, group, eight, lane, acc, top, sum);
+    float top[2], sum[2], cut[2];
+    join_parts<1, 8>(p, cta, hd.blocks, g.w, warp, kJoinWarps, group, eight, lane, acc, top, sum, cut);
     __syncthreads();   // what the one before left has been read
     s.part[warp][lane] = acc[0];
     if (quad == 0) {
@@ -1222,13 +1242,15 @@ __device__ __forceinline__ void join_many(Join& s, const LatentAttnParams& p, co
         s.top[warp][i0 + 8] = top[1];
         s.sum[warp][i0] = sum[0];
         s.sum[warp][i0 + 8] = sum[1];
+        s.cut[warp][i0] = cut[0];
+        s.cut[warp][i0 + 8] = cut[1];
     }
     __syncthreads();
     // a warp (of the first eight) writes rows `warp` and `warp` + 8 of the group, eight lanes the eight dims of both
     float odd = 0.f;
     if (lane < 8 && warp < 8) {
         const int h = lane >> 2, i = warp + 8 * h;
-        float a = 0.f, b = 0.f, l = 0.f, m = s.top[0][i];
+        float a = 0.f, b = 0.f, l = 0.f, c = 0.f, m = s.top[0][i];
         #pragma unroll
         for (int k = 1; k < kJoinWarps; ++k) m = fmaxf(m, s.top[k][i]);
         #pragma unroll
@@ -1238,10 +1260,11 @@ __device__ __forceinline__ void join_many(Join& s, const LatentAttnParams& p, co
             a = fmaf(f, h ? x.z : x.x, a);
             b = fmaf(f, h ? x.w : x.y, b);
             l = fmaf(f, s.sum[k][i], l);
+            c = fmaf(f, s.cut[k][i], c);
         }
         const int64_t row = join_row(p, g, hd, by_each, group * 16 + i);
         if (row >= 0) {
-            put2(p, row, 8 * eight + 2 * quad, a, b, l == 0.f ? 0.f : 1.f / l);
+            put2(p, row, 8 * eight + 2 * quad, a, b, c == 0.f ? 0.f : 1.f / c);
             if (eight == 0 && quad == 0 && p.lse_out) p.lse_out[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             odd = a + b;
         }
