@@ -27,8 +27,8 @@
 // layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
 //
 // Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.0 TB/s (74% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 7 of
-// partials and join); 128 heads: 94 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 46 us, of it 10 until the
-// first tile is converted, 1.3 us a tile, 8 for 147 parts and their join.
+// partials and join); 128 heads: 95 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 47 us, of it 10 until the
+// first tile is converted, 1.4 us a tile, 8 for 147 parts and their join.
 //
 // Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (a try suspends 3.8 us; not while a
 // row is computed again, which ends by itself and takes 0.5 us a position); the kernel then reports it and ends.
@@ -255,7 +255,7 @@ __device__ inline bool find_share_small(const LatentAttnParams& p, const Heads& 
     if (__any_sync(kFull, c.tiles >> 25 || c.units >> 23)) return false;
     if (!__any_sync(kFull, c.units > 1)) {
         // Whole shares for every unit, if that makes them no longer than another unit's start and end would: 3 x 16,384 positions,
-        // 64 heads 31.6 us (36.3 with shares of the sum), 4 x 4,000, 16 heads 16.3 (19.1).
+        // 64 heads 32 us (36 with shares of the sum), 4 x 4,000, 16 heads 16.3 (19.1).
         const int lanes = gridDim.x / hd.blocks, me = blockIdx.x / hd.blocks, n = static_cast<int>(c.tiles);
         const int least = max((static_cast<int>(__reduce_add_sync(kFull, n)) + lanes - 1) / lanes, kMinShare);
         auto ctas_of = [&](int share) { return (n + share - 1) / share; };

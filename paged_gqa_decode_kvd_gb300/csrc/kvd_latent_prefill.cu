@@ -10,9 +10,10 @@
 // shared memory, P over S in tensor memory, O += P·V.  A piece is free when both have used it.  The reference maximum moves only when a row's
 // passes it by 8.
 // Rounding: q, k, v enter exactly, logits, statistics and sums are fp32, a weight enters as one bf16 (off by at most 2^-8 of itself; its sum
-// is taken before): outputs are 1.2 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 would cost 40% more MMAs.
+// is taken before): outputs are 1.2 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 would cost 40% more MMAs;
+// divided by the sum of the weights as they were rounded (as in the absorbed kernel) they are no nearer, and the call takes 11% longer.
 //
-// Bound: a whole prompt of 8,192, 32 heads: 448 us, 1,534 TFLOP/s (79% of measured).  A tile takes both warpgroups 3,600 cycles, its MMAs 2,750
+// Bound: a whole prompt of 8,192, 32 heads: 450 us, 1,527 TFLOP/s (78% of measured).  A tile takes both warpgroups 3,600 cycles, its MMAs 2,750
 // (S 12 x 71, at the limit of shared memory's 128 bytes a cycle, O 8 x 65 each), a softmax 1,300 beside the other's MMAs; the rest is what the
 // turns leave between two runs.  Ragged prompts: 119 us against 53 of HBM: a unit's first tile waits 3 us for Q and K, its rows take 1 to 2 us,
 // and rows of at most 128 tokens leave a warpgroup idle.
