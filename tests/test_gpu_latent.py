@@ -335,6 +335,31 @@ def test_attn_cut_units(cuda_device, kind, n_q, q_lens, lens):
 
 
 @KINDS
+@pytest.mark.parametrize("n", [1, 70, 5000])
+def test_attn_of_one_token_is_its_value(cuda_device, kind, n):
+    """Where a row's whole weight is on one token, that weight's rounding (in 8 bits with the token's scale) cancels."""
+    dev, rng = cuda_device, np.random.default_rng(n)
+    c = Cache(dev, kind, [n], seed=n)
+    at = rng.integers(0, n, 16)
+    key = torch.zeros(n, ROT, dtype=torch.bfloat16)
+    q = torch.zeros(1, 16, KEY, dtype=torch.bfloat16)
+    for h, j in enumerate(at):   # two of the rotated dims tell a head's token: a logit of 2^16·scale, others at most half of it
+        key[j, h] = key[j, 16 + h] = 256.0
+        q[0, h, LAT + h] = q[0, h, LAT + 16 + h] = 128.0
+    lat = rand(rng, n, LAT)
+    c.put(0, 0, n, lat, key)
+    out, lse = torch.zeros(1, 16, LAT, device=dev), torch.zeros(1, 16, device=dev)
+    ws = torch.empty(kvd.kvd_latent_workspace_bytes(c.pool.handle, 16, 1), dtype=torch.uint8, device=dev)
+    kvd.kvd_latent_attn(c.pool.handle, 0, to(dev, q), to(dev, np.array([0, 1], np.int32)), to(dev, c.bt), to(dev, np.array([n], np.int32)),
+                        ws, out, softmax_scale=SCALE, lse_out=lse)
+    ok(c.pool)
+    want = c.rows()[slots_of(c.bt, 0, 0, n)][at, :LAT]
+    # a quotient, two products and at most 147 parts' sums of which one is not 0
+    assert_within(out[0], want, want.abs() * 2.0 ** -21, "out")
+    assert_within(lse[0], torch.full((16,), 2.0 ** 16 * SCALE, dtype=torch.float64), torch.full((16,), 2.0 ** 16 * SCALE * 2.0 ** -21, dtype=torch.float64), "lse")
+
+
+@KINDS
 def test_attn_growing_logits_move_the_reference(cuda_device, kind):
     """Each tile's maximum passes the last one's by more than the lazy border, so O is rescaled many times."""
     dev, n = cuda_device, 900
