@@ -570,8 +570,10 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
                     }
                 }
             }
-            if (t == tiles - 1 && x.end < base + kTile && !(w == 1 && x.tiles[0] == tiles)) {
-                // V behind the last key that a row of the unit attends: its weight is 0, and 0·NaN would be NaN
+            if (t == tiles - 1 && x.end < base + kTile) {
+                // V behind the last key that a row of the unit attends: its weight is 0, and 0·NaN would be NaN.  Each warpgroup with
+                // rows there does it before its own p_full: nothing else orders the other's stores before its product.  (Zeros over
+                // zeros the second time, in a piece that stays until this warpgroup's issuer has released it too.)
                 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const uint32_t piece = (before + t) * kTilePieces + 3 + half, at = piece % kPieces;

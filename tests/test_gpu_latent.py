@@ -758,6 +758,43 @@ def test_prefill_what_no_row_attends_may_be_anything(cuda_device):
     assert d.n_q == 3
 
 
+@pytest.mark.parametrize("n_q,T,N,causal", [
+    (5, 200, 250, True), (5, 254, 383, True), (40, 130, 380, True), (2, 129, 1000, True), (3, 456, 600, True),
+    (5, 200, 300, False), (3, 256, 10, False), (40, 255, 129, False), (2, 600, 383, False), (1, 129, 1, False)])
+def test_prefill_keys_of_others_beside_the_last_tile_of_two_warpgroups(cuda_device, n_q, T, N, causal):
+    """Both warpgroups of a block of tokens end in one tile of keys, which holds the first keys of the next request: nothing of
+    what those are reaches either's rows.  Requests of one warpgroup's rows stand between, so that the warpgroups of a
+    multiprocessor are apart when they come to the tile."""
+    B = 24
+    q_lens, kv_lens = [T, 100] * B, [N, 120] * B
+    c = Prefill(cuda_device, n_q, q_lens, kv_lens, seed=T, behind=140)
+    mine = np.concatenate([np.arange(c.start[2 * b], c.start[2 * b + 1]) for b in range(B)])
+    want = [x[mine] for x in c.run(causal)]
+    ok(c.pool)
+    ref, rl, tol, lt = prefill_ref(c.q, c.k, c.v, c.r, c.start[:2], c.kv_start[:2], causal, SCALE, cuda_device)
+    assert_within(want[0][:T], ref[:T], tol[:T], "out")
+    assert_within(want[1][:T], rl[:T], lt[:T], "lse")
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for b in range(B):   # the requests between, and (behind the last of them) rows of nobody
+            c.v[c.kv_start[2 * b + 1]:c.kv_start[2 * b + 2]] = bad
+        c.v[c.kv_start[-1]:] = bad
+        for _ in range(3):
+            got = c.run(causal)
+            assert torch.equal(got[0][mine], want[0]) and torch.equal(got[1][mine], want[1])
+
+
+def test_prefill_rows_of_nobody_behind_the_last_tile_of_two_warpgroups(cuda_device):
+    """Room to spare behind the only request's keys, never written: with and without a mask."""
+    for T, N, causal in ((200, 250, True), (254, 383, True), (200, 300, False), (256, 1, False)):
+        c = Prefill(cuda_device, 64, [T], [N], seed=N, behind=300)
+        want = c.run(causal)
+        for x in (c.k, c.v, c.r):
+            x[N:] = float("nan")
+        for _ in range(5):
+            got = c.run(causal)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_prefill_bad_pairs(cuda_device):
     dev = cuda_device
     for start, kv, skipped in (([0, 30, 20, 60], [0, 30, 60, 90], [1]), ([0, 20, 40, 61], [0, 30, 60, 90], [2]),
