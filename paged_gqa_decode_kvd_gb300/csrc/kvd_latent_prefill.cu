@@ -18,8 +18,9 @@
 // turns leave between two runs.  Ragged prompts: 119 us against 53 of HBM: a unit's first tile waits 3 us for Q and K, its rows take 1 to 2 us,
 // and rows of at most 128 tokens leave a warpgroup idle.
 //
-// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (a try suspends 3.8 us; not while a
-// row is computed again, which ends by itself and takes 0.5 us a position); the kernel then reports it and ends.
+// Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (200,000 tries; a barrier's suspends
+// 3.8 us, a turn's sleeps as long once the first thousand have failed; not while a row is computed again, which ends by itself and takes
+// 0.5 us a position); the kernel then reports it and ends.
 #include <cuda.h>
 
 #include "kvd_latent.h"
@@ -37,6 +38,8 @@ constexpr int kProducerWarp = 8, kIssueWarp = 9;   // the issuers are two
 constexpr int kReaders = 10;           // warps that read a unit's description
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
 constexpr int kTries = 200000;         // tries of a wait, which suspend: a second or so
+constexpr int kQuickTries = 1000;      // of a turn, which do not, before they sleep
+constexpr uint32_t kTryNs = 3800;      // a barrier's try
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
 constexpr uint32_t kColS = 0, kColO = 256;    // tensor memory columns: S (and P over it) 2 × 128, O 2 × 128
 
@@ -104,12 +107,15 @@ __device__ __forceinline__ bool test_lanes(uint64_t* bar, uint32_t phase) {
             : "memory");
     return __all_sync(kFull, ok != 0);
 }
-// The tensor cores' queue is taken by one issuer at a time.
+// The tensor cores' queue is taken by one issuer at a time, for as long as it takes to issue a product's MMAs.  A try here does
+// not suspend by itself: after the first ones, tens of microseconds of them, each is followed by a sleep, so that this wait's
+// limit is the others' and its tries leave the softmax warps their issue slots.
 __device__ __forceinline__ bool take_turn(Smem& s, int lane) {
     #pragma unroll 1
     for (int i = 0; i < kTries; ++i) {
         if (__any_sync(kFull, lane == 0 && atomicCAS(&s.turn, 0, 1) == 0)) return true;
         if (__any_sync(kFull, s.abort)) return false;
+        if (i >= kQuickTries) __nanosleep(kTryNs);
         if (i == kTries - 1 && __any_sync(kFull, *static_cast<volatile int*>(&s.again) > 0)) i = 0;
     }
     s.abort = 1;
