@@ -657,7 +657,8 @@ KVD_API kvd_status kvd_latent_append(kvd_pool* pool, int layer, const void* late
  *  block_table   int32 [batch][max_blocks_per_seq], device
  *  row_start     int32 [batch + 1], device, 0 ≤ row_start[b] ≤ row_start[b+1] ≤ n_rows.  Rows outside every request are
  *                left as they were.  A request whose pair breaks this, or that reaches beyond max_blocks_per_seq·16, is
- *                skipped with KVD_ERR_OOB in the error word
+ *                skipped with KVD_ERR_OOB in the error word.  Where a broken pair leaves others overlapping, a row is one of
+ *                theirs, and what is behind the first 2^33 rows of all of them is skipped
  *  first         int32 [batch] ≥ 0, device, or NULL: all 0
  *  out           bf16 [n_rows], rows out_stride ≥ 576 elements apart, a multiple of 8; 16-byte aligned, apart from the pool
  * A block id outside the pool is reported and its rows are left as they were.  batch = 0 or n_rows = 0 is a no-op. */

@@ -201,6 +201,10 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const LatentAppendP
 // Rows in chunks of eight, one a warp; a CTA takes every gridDim-th chunk of all requests.  226,000 rows of 24 requests from
 // 8 bits take 64.5 us so, at eight CTAs an SM; with four rows a warp, all loads under way, and four CTAs 76 us, with two 75 us.
 constexpr int kChunkRows = kThreads / 32, kGatherCtas = 8;
+// Pairs that are sound by themselves may overlap where others are not, and add up to more than 32 bits.  Counts stop here, far above
+// what rows that are apart can be, and the requests behind are skipped (64 bits: the prefix of 8,192 4.6 us instead of 4.3, the
+// 226,000 rows 65.6 instead of 64.4).
+constexpr int kMostChunks = (1 << 30) - 1;
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const LatentGatherParams p) {
     __shared__ int chunks[kMaxBatch];   // up to and with the request
@@ -223,17 +227,17 @@ __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const Lat
         #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(kFull, up, o);
-            if (lane >= o) up += v;
+            if (lane >= o) up = min(up + v, kMostChunks);
         }
         if (lane == 31) warp_sum[warp] = up;
         __syncthreads();
         int all = before;
         #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) up += warp_sum[w];
-            all += warp_sum[w];
+            if (w < warp) up = min(up + warp_sum[w], kMostChunks);
+            all = min(all + warp_sum[w], kMostChunks);
         }
-        if (b < p.B) chunks[b] = before + up;
+        if (b < p.B) chunks[b] = min(before + up, kMostChunks);
         before = all;
         __syncthreads();
     }

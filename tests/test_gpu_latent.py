@@ -253,6 +253,21 @@ def test_gather_skips_what_is_wrong(cuda_device, kind):
             assert torch.equal(got[keep], rows[at][keep].float().bfloat16())
 
 
+def test_gather_of_pairs_that_overlap(cuda_device):
+    """Every second pair is the whole of out, the others are backwards: 2^31 chunks of eight rows, more than 32 bits count."""
+    dev, rng, batch, n = cuda_device, np.random.default_rng(7), 2048, 1 << 24
+    pool = poisoned(1, 1, BF16, dev)
+    rows = rand(rng, 16, KEY)
+    kvd.kvd_latent_append(pool.handle, 0, to(dev, rows[:, :LAT]), to(dev, rows[:, LAT:]), to(dev, np.arange(16, dtype=np.int64)))
+    table = torch.zeros(batch, n // 16, dtype=torch.int32, device=dev)
+    start = torch.tensor([0, n] * (batch // 2) + [0], dtype=torch.int32, device=dev)
+    out = torch.full((n, KEY), 9.0, dtype=torch.bfloat16, device=dev)
+    kvd.kvd_latent_gather(pool.handle, 0, table, start, out)
+    oob(pool)
+    want = to(dev, rows).repeat(1 << 12, 1)
+    assert all(torch.equal(x, want) for x in out.split(1 << 16))
+
+
 # ------------------------------------------------------------- absorbed attention
 class Attn(Cache):
     def __init__(self, dev, kind, n_q, q_lens, lens, seed=0, evict=0.0, **kw):
