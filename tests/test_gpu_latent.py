@@ -499,6 +499,61 @@ def test_attn_wrong_lengths_and_blocks(cuda_device, kind):
 
 
 @KINDS
+def test_attn_starts_that_break(cuda_device, kind):
+    """A pair of q_start that runs backwards, or out of q: that request's rows are left, the others' are as they should be."""
+    dev = cuda_device
+    c = Attn(dev, kind, 6, [3, 2, 4], [40, 30, 100], seed=15)
+    rows = c.rows()
+    for start, good in (([0, 3, 2, 9], [0, 2]), ([0, 3, 5, 10], [0, 1]), ([-1, 3, 5, 9], [1, 2]), ([0, 10, 5, 9], [2]), ([3, 3, 3, 9], [2])):
+        a = c.args()
+        a["q_start"] = to(dev, np.array(start, np.int32))
+        out, lse = c.run(a=a)
+        if start[0] != 3:
+            oob(c.pool)
+        owners = np.zeros(9, int)
+        for b in good:
+            owners[start[b]:start[b + 1]] += 1
+        for b in good:
+            lens = [n if i == b else 0 for i, n in enumerate(c.lens)]
+            ref, rl, tol, lt = attn_ref(rows, c.q, start, c.bt, lens, None, SCALE)
+            mine = [r for r in range(start[b], start[b + 1]) if owners[r] == 1]   # (where two overlap it is either's)
+            assert_within(out[mine], ref[mine], tol[mine], "out")
+            assert_within(lse[mine], rl[mine], lt[mine], "lse")
+        assert bool((out[owners == 0] == 9.0).all()) and bool((lse[owners == 0] == 9.0).all())
+
+
+@KINDS
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("n_q,T,N", [(8, 8, 100), (8, 8, 3000), (20, 70, 70), (128, 2, 400)])
+def test_attn_of_an_infinite_token(cuda_device, kind, bad, n_q, T, N):
+    """One value of a new token's latent is infinite.  A head that gives it the logit +inf has no finite value; one that gives it
+    -inf has the others' softmax, and in that dim 0·inf.  In 8 bits the token's scale is infinite and its codes times it NaN."""
+    dev, j = cuda_device, T // 2
+    c = Attn(dev, kind, n_q, [T], [N], seed=22)
+    pos = N - T + j
+    lat, key = rand(c.rng, 1, LAT), rand(c.rng, 1, ROT)
+    lat[0, 100] = bad
+    c.retain = np.full(c.nb, 0xFFFF, np.uint16)
+    c.put(0, pos, pos + 1, lat, key)
+    out, lse = c.run()
+    rows = c.rows()
+    c.retain[c.bt[0, pos // 16]] ^= 1 << (pos % 16)   # the others' softmax
+    ref, rl, tol, lt = attn_ref(rows, c.q, c.start, c.bt, c.lens, c.retain, SCALE, dev)
+    assert_within(out[:j], ref[:j], tol[:j], "rows before it")
+    assert_within(lse[:j], rl[:j], lt[:j], "lse before it")
+    out, lse, ref, rl, tol, lt = (x[j:].cpu() for x in (out, lse, ref, rl, tol, lt))
+    if kind == FP8:
+        assert bool(out.isnan().all()) and bool(lse.isnan().all())
+        return
+    most = c.q[j:, :, 100].float() * bad > 0
+    assert bool(out[most].isnan().all()) and not bool(lse[most].isfinite().any())
+    assert bool(out[~most][:, 100].isnan().all())
+    rest = np.arange(LAT) != 100
+    assert_within(out[~most][:, rest], ref[~most][:, rest], tol[~most][:, rest], "the others")
+    assert_within(lse[~most], rl[~most], lt[~most], "lse")
+
+
+@KINDS
 def test_attn_same_bits_streams_and_graphs(cuda_device, kind):
     dev = cuda_device
     c = Attn(dev, kind, 16, [1, 3, 1], [3000, 500, 77], seed=16, evict=0.1)
