@@ -8,7 +8,7 @@
 // Read back: y (code·s, rounded to bf16) and r, side by side.
 //
 // Bound: HBM.  4,099 tokens into 8 bits with 128 heads' queries: 26.6 us, 5.3 TB/s (78% of measured: 67 MB of queries are read and written in
-// pieces of 128 bytes); a decode step of 32 tokens: 2.6 us in a graph, 11 with the host call.  226,000 rows of 24 requests from 8 bits: 64 us,
+// pieces of 128 bytes); with halves paired 32.4 us (every dim's partner and angle come from other lanes); a decode step of 32 tokens: 2.6 us in a graph, 11 with the host call.  226,000 rows of 24 requests from 8 bits: 64 us,
 // 6.3 TB/s (93%).
 #include "kvd_common.cuh"
 #include "kvd_latent.h"
@@ -102,10 +102,12 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float s) {
     return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
 }
 
-// A warp takes one token's latent and key part, or p.heads of its query heads, four at a time.  Five CTAs an SM (48 registers; what
-// is spilled is the latent's): 26.2 us for the prompt above, with four 27.5, with six 26.4.
+// A warp takes one token's latent and key part, or p.heads of its query heads, four at a time.  Neighbours paired: five CTAs an SM (48
+// registers, 4 to 8 bytes spilled) take 26.2 us for the prompt above, four 27.5, six 26.4.  Halves paired, a lane has eight dims' cos and sin
+// in place of four pairs': at five 100 bytes are spilled and more loaded again, in the queries' path too: 34.9 us, with four 32.4, with three
+// 38.9; 7,700 tokens of 32 heads in BF16 23.4, 21.3 and 25.8.
 template <bool FP8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 5) append_kernel(const LatentAppendParams p) {
+__global__ void __launch_bounds__(kThreads, INTERLEAVED ? 5 : 4) append_kernel(const LatentAppendParams p) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, lane8 = lane & 7;
