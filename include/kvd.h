@@ -704,8 +704,8 @@ KVD_API kvd_status kvd_latent_attn(kvd_pool* pool, int layer, const void* q, int
  *  out          [n_tokens][n_q][128] in out_dtype (KVD_BF16 or KVD_F32), 16-byte aligned, apart from what is read
  *  lse_out      f32 [n_tokens][n_q] natural-log log-sum-exp, or NULL
  * A row with nothing to attend gets out = 0 and lse = −inf.  What a key that a row does not attend holds does not reach
- * that row.  A weight enters the product with v rounded to bf16 (off by at most 2^-8 of itself), logits and sums are fp32.  The
- * same call gives the same bits.  n_tokens = 0 or batch = 0 is a no-op. */
+ * that row.  A weight enters the product with v rounded to bf16 (off by at most 2^-8 of itself) where out is KVD_BF16, as two
+ * bf16 (2^-15) where it is KVD_F32; logits and sums are fp32.  The same call gives the same bits.  n_tokens = 0 or batch = 0 is a no-op. */
 KVD_API kvd_status kvd_latent_prefill(kvd_pool* pool, const void* q, int n_q, const int32_t* q_start, int n_tokens,
                                       const void* k_nope, int64_t k_stride, int64_t k_head_stride, const void* v,
                                       int64_t v_stride, int64_t v_head_stride, const void* k_rope, int64_t k_rope_stride,

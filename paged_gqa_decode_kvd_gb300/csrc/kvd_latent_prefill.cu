@@ -9,9 +9,11 @@
 // which all heads share) and V (twice 64 keys) by TMA; V is read N-major, as it lands.  An issuing warp for each warpgroup: S = Q·Kᵀ from
 // shared memory, P over S in tensor memory, O += P·V.  A piece is free when both have used it.  The reference maximum moves only when a row's
 // passes it by 8.
-// Rounding: q, k, v enter exactly, logits, statistics and sums are fp32, a weight enters as one bf16 (off by at most 2^-8 of itself; its sum
-// is taken before): outputs are 1.2 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16.  Two bf16 would cost 40% more MMAs;
-// divided by the sum of the weights as they were rounded (as in the absorbed kernel) they are no nearer, and the call takes 11% longer.
+// Rounding: q, k, v enter exactly, logits, statistics and sums are fp32.  Where out is bf16 a weight enters as one bf16 (off by at most 2^-8
+// of itself; its sum is taken before): outputs are 1.2 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16; divided by the sum of
+// the weights as they were rounded (as in the absorbed kernel) they are no nearer, and the call takes 11% longer.  Where out is fp32 (TWO) nothing
+// behind it hides that, so a weight enters as two bf16, cut off and its rest (off by at most 2^-15 of itself), for 40% more MMAs: 628 us in place of 454 for the
+// prompt below.
 //
 // Bound: a whole prompt of 8,192, 32 heads: 450 us, 1,527 TFLOP/s (78% of measured).  A tile takes both warpgroups 3,600 cycles, its MMAs 2,750
 // (S 12 x 71, at the limit of shared memory's 128 bytes a cycle, O 8 x 65 each), a softmax 1,300 beside the other's MMAs; the rest is what the
@@ -42,6 +44,7 @@ constexpr int kQuickTries = 1000;      // of a turn, which do not, before they s
 constexpr uint32_t kTryNs = 3800;      // a barrier's try
 constexpr uint64_t kWaitNs = 1000000000ull;   // of what must land before the block leaves
 constexpr uint32_t kColS = 0, kColO = 256;    // tensor memory columns: S (and P over it) 2 × 128, O 2 × 128
+constexpr uint32_t kColRest = 64;             // what P's rounding left, from S on
 
 constexpr int kSorted = 512;           // blocks of tokens that are put in order
 constexpr int kBlockBits = 20;
@@ -390,6 +393,7 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
 // takes 500 to 700 cycles, a run 520 or 780, and few MMAs are taken ahead.  The two take turns: mixed, their MMAs end at the
 // same time, and both warpgroups' softmax runs while the tensor cores have nothing to do.
 // Every operand is a value that all lanes have, and known as one: an instruction then issues in its own time.
+template <bool TWO>
 __device__ __forceinline__ void issuer(Smem& s, int w, int lane) {
     constexpr uint32_t kDescS = mma_desc_bf16(kRows, kTile), kDescO = mma_desc_bf16(kRows, kExpVal) | (1u << 16);
     const uint32_t W = uniform(w), tmem = uniform(s.tmem), p_op = uniform(smem_u32(s.piece));
@@ -466,8 +470,10 @@ __device__ __forceinline__ void issuer(Smem& s, int w, int lane) {
                 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
                         mma_ts(col_o, col_s + (half * 4 + k) * 8, desc_v(b[half] + k * 2048), kDescO, half > 0 || k > 0 ? 1u : add);
+                        if (TWO) mma_ts(col_o, col_s + kColRest + (half * 4 + k) * 8, desc_v(b[half] + k * 2048), kDescO, 1u);
+                    }
                     mma_commit(e[half]);
                 }
             }
@@ -508,6 +514,15 @@ __device__ __forceinline__ void st32(void* p, const uint32_t* v, bool sector) {
 }
 
 // ------------------------------------------------------------------- softmax
+// What two weights' upper 16 bits leave of them, as two bf16, and 2^-23 of them more: above 0 wherever a weight is (one of 2^-102 or
+// more), so that an infinite value times either part has the value's sign.  (By a minimum and a maximum, which have no such border, a prompt of
+// 8,192 takes 699 us, by packed ones 665.)
+__device__ __forceinline__ uint32_t rests_of(float2 a, uint32_t x, uint32_t y) {
+    const float c = 1.f + 0x1p-23f;
+    const float2 d = fma2(a, make_float2(c, c), make_float2(__uint_as_float((x & 0xffff0000u) ^ 0x80000000u), __uint_as_float((y & 0xffff0000u) ^ 0x80000000u)));
+    return pack_bf16(d.x, d.y);
+}
+template <bool TWO>
 __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, int w, int tid, int lane) {
     const uint32_t mine = s.tmem + (static_cast<uint32_t>(tid & ~31) << 16);
     const uint32_t col_s = mine + kColS + w * kTile, col_o = mine + kColO + w * kExpVal;
@@ -590,19 +605,31 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
                 fence_proxy_async_shared();
             }
             const float z = ref == -INFINITY ? 0.f : -ref;
+            constexpr int kStep = TWO ? 1 : 2;   // (16 registers of each at a time: 32 spill)
             #pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-                uint32_t pk[32];
+            for (int c = 0; c < 4; c += kStep) {
+                uint32_t pk[16 * kStep], rest[16];
                 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
+                for (int e = 0; e < 16 * kStep; ++e) {
                     float2 a = make_float2(__uint_as_float(v[c + (e >> 4)][2 * (e & 15)]), __uint_as_float(v[c + (e >> 4)][2 * (e & 15) + 1]));
                     a = fma2(a, make_float2(scale, scale), make_float2(z, z));
                     a.x = ex2(a.x);
                     a.y = ex2(a.y);
                     sum = add2(sum, a);
-                    pk[e] = pack_bf16(a.x, a.y);
+                    if constexpr (TWO) {
+                        const uint32_t x = __float_as_uint(a.x), y = __float_as_uint(a.y);
+                        pk[e] = __byte_perm(x, y, 0x7632);
+                        rest[e] = rests_of(a, x, y);
+                    } else {
+                        pk[e] = pack_bf16(a.x, a.y);
+                    }
                 }
-                tmem_st32(col_s + c * 16, pk);
+                if constexpr (TWO) {
+                    tmem_st16(col_s + c * 16, pk);
+                    tmem_st16(col_s + kColRest + c * 16, rest);
+                } else {
+                    tmem_st32(col_s + c * 16, pk);
+                }
             }
             tmem_wait_st();
             tcgen_fence_before();
@@ -635,7 +662,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
                 odd += y[e];
             }
             if (!real) continue;
-            if (p.out_f32) {
+            if constexpr (TWO) {
                 uint32_t z[32];
                 #pragma unroll
                 for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(y[e]);
@@ -666,6 +693,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentPrefillParams& p, i
     }
 }
 
+template <bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefillParams p, const __grid_constant__ Maps m) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem& s = *reinterpret_cast<Smem*>(smem_raw);
@@ -705,11 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const LatentPrefil
     if (aligned) {
         if (warp < 8) {
             take_registers<208>();
-            softmax(s, p, warp >> 2, tid & 127, lane);
+            softmax<TWO>(s, p, warp >> 2, tid & 127, lane);
         } else {
             give_registers<80>();
             if (warp == kProducerWarp) producer(s, p, m, lane);
-            else if (warp == kIssueWarp || warp == kIssueWarp + 1) issuer(s, warp - kIssueWarp, lane);
+            else if (warp == kIssueWarp || warp == kIssueWarp + 1) issuer<TWO>(s, warp - kIssueWarp, lane);
         }
     }
     __syncwarp();
@@ -771,9 +799,10 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, int num_sms, cud
         !make_map(&m.v, keys ? p.v : any, kExpVal, p.n_q, keys ? p.n_keys : 1, keys ? p.v_head : kExpVal, keys ? p.v_stride : kExpVal * p.n_q, 64) ||
         !make_map(&m.r, keys ? p.k_rope : any, kLatRope, 0, keys ? p.n_keys : 1, 0, keys ? p.rope_stride : kLatRope, kTile))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+    auto* kernel = p.out_f32 ? prefill_kernel<true> : prefill_kernel<false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
     if (e != cudaSuccess) return e;
-    return launch_dependent(prefill_kernel, dim3(static_cast<unsigned>(num_sms)), dim3(kThreads), sizeof(Smem), -1, stream, p, m);
+    return launch_dependent(kernel, dim3(static_cast<unsigned>(num_sms)), dim3(kThreads), sizeof(Smem), -1, stream, p, m);
 }
 
 }  // namespace kvd
