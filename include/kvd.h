@@ -679,8 +679,8 @@ KVD_API kvd_status kvd_latent_workspace_bytes(const kvd_pool* pool, int n_q, int
  *  q_start, seq_lens, block_table, retain_mask, lse_out, workspace (kvd_latent_workspace_bytes) and what is done about bad
  *  lengths, bad block ids and rows with nothing to attend: as in kvd_chunk_attn
  * What a masked position's slot holds (not yet written, a NaN) does not reach the result.  A weight enters the product
- * with c rounded to bf16 (off by at most 2^-8 of itself) and the sum that divides it as it was rounded; lse is that of the weights
- * themselves, logits and sums are fp32.  The same call gives the same bits; where a
+ * with c rounded to bf16 (off by at most 2^-8 of itself) where out is KVD_BF16, as two bf16 (2^-16) where it is KVD_F32, and the sum
+ * that divides it as it was rounded; lse is that of the weights themselves, logits and sums are fp32.  The same call gives the same bits; where a
  * long row's sum is cut and joined depends on all requests of the call, so another batch may round it otherwise.
  * n_tokens = 0 or batch = 0 is a no-op. */
 KVD_API kvd_status kvd_latent_attn(kvd_pool* pool, int layer, const void* q, int n_q, const int32_t* q_start, int n_tokens,

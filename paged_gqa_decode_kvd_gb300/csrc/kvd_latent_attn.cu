@@ -18,11 +18,13 @@
 // 64 rows, not 128, since 128 rows of 512 fp32 sums are all of tensor memory: M = 64 uses half its lanes, lanes 0 .. 15 of each 32 hold Q and
 // S, 16 .. 31 hold O.  An MMA with M = 64 takes as long as one with M = 128 (33 cycles for N = 64, 129 for N = 256), so the matrix rate ends at
 // half; that is enough up to 64 heads: a tile's MMAs take 2,240 cycles (1.15 us), its way through HBM 1.65 us.
-// Rounding.  K, C and Q enter the products exactly, logits, statistics and sums are fp32, a weight enters as one bf16 (off by at most 2^-8 of
-// itself; in 8 bits with its token's scale).  out is divided by the sum of the weights as they were rounded, so that what all of a row's
-// weight is on comes out exactly; lse is that of the weights before.  Outputs are 1.1 to 1.35 times as far from 64 bits as an fp32 form's
-// rounded to bf16 (divided by the sum before: up to 1.8 in 8 bits; 1 to 2 us less a call).  Two bf16 a weight, as
-// the chunk kernel has, would make O's MMAs 2,060 cycles a tile instead of 1,030, more than the cache's own time.
+// Rounding.  K, C and Q enter the products exactly, logits, statistics and sums are fp32.  Where out is bf16 a weight enters as one bf16 (off
+// by at most 2^-8 of itself; in 8 bits with its token's scale).  out is divided by the sum of the weights as they were rounded, so that what all
+// of a row's weight is on comes out exactly; lse is that of the weights before.  Outputs are 1.1 to 1.35 times as far from 64 bits as an fp32
+// form's rounded to bf16 (divided by the sum before: up to 1.8 in 8 bits; 1 to 2 us less a call).  Where out is fp32 (TWO) nothing behind it hides
+// that: a weight enters as two bf16, as in the chunk kernel (off by at most 2^-16 of itself); what the first leaves of it lies where the tile's
+// rotated dims were, which only S reads.  That makes O's MMAs 2,060 cycles a tile instead of 1,030: 32 x 8,192 positions with 16 heads 69 us
+// (bf16 61), with 128 heads 116 (96), 131,072 in 8 bits 52 (47).
 // 8 bits: converter warps load the codes (a tile under way while the one before it is converted) and store them as bf16, exactly, in the same
 // layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
 //
@@ -43,6 +45,7 @@ constexpr int kRows = kLatUnitRows;
 constexpr int kStages = 3;
 constexpr int kTileBytes = kTile * kLatKey * 2;
 constexpr int kGroup = 9216;           // bytes of eight tokens of a tile
+constexpr int kRotated = 8192;         // from where on those of their rotated dims stand
 constexpr int kProducerWarp = 4, kScoreWarp = 5, kFixWarp = 6, kValueWarp = 7, kConvertWarp = 8, kConvertWarps = 8;
 constexpr int threads_of(bool fp8) { return fp8 ? 32 * (kConvertWarp + kConvertWarps) : 256; }
 constexpr float kLazy = 8.f;           // log2: how far a row's maximum may pass its reference
@@ -678,6 +681,7 @@ __device__ __forceinline__ void score_issuer(Smem& s, const LatentAttnParams& p,
     drain_mma(s, 0);
 }
 // O += P(t)·C(t):
+template <bool TWO>
 __device__ __forceinline__ void value_issuer(Smem& s, const LatentAttnParams& p, Walk walk) {
     constexpr uint32_t kDescO = mma_desc_bf16(64, 256) | (1u << 16);
     const uint32_t tmem = uniform(s.tmem), k_op = uniform(smem_u32(s.k)), p_op = uniform(smem_u32(s.p));
@@ -694,12 +698,20 @@ __device__ __forceinline__ void value_issuer(Smem& s, const LatentAttnParams& p,
             if (!ok) break;
             tcgen_fence_after();
             if (elect_one()) {
+                if constexpr (TWO) {   // the weights' rests first: they lie in all of the tile's blocks
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        #pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            mma_ss(tmem + kHalf + h * 256, desc_k(op + kRotated + k * 32, kGroup), desc_n(op + h * 4096 + k * 2 * kGroup), kDescO,
+                                   k > 0 ? 1u : add);
+                }
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) {   // a block at a time, which is free then
                     #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         mma_ss(tmem + kHalf + h * 256, desc_k(p_op + k * 32, 1024), desc_n(op + h * 4096 + k * 2 * kGroup), kDescO,
-                               k > 0 ? 1u : add);
+                               TWO || k > 0 ? 1u : add);
                     mma_commit(empty + 8 * k);
                 }
             }
@@ -800,7 +812,7 @@ __device__ __forceinline__ void load_q(Smem& s, const LatentAttnParams& p, const
     if (lane == 0) mbar_arrive(&s.q_full);
 }
 
-template <bool FP8>
+template <bool FP8, bool TWO>
 __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, const Heads& hd, Walk walk, int warp, int lane) {
     const uint32_t mine = s.tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int quad = lane & 3;
@@ -879,6 +891,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
             }
             const float z0 = ref[0] == -INFINITY ? 0.f : ref[0], z1 = ref[1] == -INFINITY ? 0.f : ref[1];
             uint32_t w[16];
+            uint8_t* rest = s.k[st] + 2 * warp * kGroup + kRotated + (lane >> 2) * 128 + quad * 4;   // (of row r0; S has been read)
             #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float a = ex2(x[4 * k] - z0), b = ex2(x[4 * k + 1] - z0), c = ex2(x[4 * k + 2] - z1), d = ex2(x[4 * k + 3] - z1);
@@ -887,7 +900,15 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
                 const float2 f = FP8 ? *reinterpret_cast<const float2*>(&info.scale[8 * k + 2 * quad]) : make_float2(1.f, 1.f);
                 w[2 * k] = FP8 ? pack_bf16(a * f.x, b * f.y) : pack_bf16(a, b);
                 w[2 * k + 1] = FP8 ? pack_bf16(c * f.x, d * f.y) : pack_bf16(c, d);
-                const float2 p0 = unpack_bf16(w[2 * k]), p1 = unpack_bf16(w[2 * k + 1]);
+                float2 p0 = unpack_bf16(w[2 * k]), p1 = unpack_bf16(w[2 * k + 1]);
+                if constexpr (TWO) {
+                    const uint32_t l0 = FP8 ? pack_bf16(a * f.x - p0.x, b * f.y - p0.y) : pack_bf16(a - p0.x, b - p0.y);
+                    const uint32_t l1 = FP8 ? pack_bf16(c * f.x - p1.x, d * f.y - p1.y) : pack_bf16(c - p1.x, d - p1.y);
+                    *reinterpret_cast<uint32_t*>(rest + ((k ^ (r0 & 7)) << 4)) = l0;
+                    *reinterpret_cast<uint32_t*>(rest + kGroup + ((k ^ (r0 & 7)) << 4)) = l1;
+                    p0 = add2(p0, unpack_bf16(l0));
+                    p1 = add2(p1, unpack_bf16(l1));
+                }
                 if constexpr (FP8) {   // (without a factor of a normal size the weight itself)
                     const float2 by = *reinterpret_cast<const float2*>(&info.by[8 * k + 2 * quad]);
                     cut[0] += (by.x != 0.f ? p0.x * by.x : a) + (by.y != 0.f ? p0.y * by.y : b);
@@ -1031,7 +1052,7 @@ __device__ __forceinline__ void softmax(Smem& s, const LatentAttnParams& p, cons
     }
 }
 
-template <bool FP8>
+template <bool FP8, bool TWO>
 __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem& s = *reinterpret_cast<Smem*>(smem_raw);
@@ -1087,12 +1108,12 @@ __global__ void __launch_bounds__(threads_of(FP8), 1) attn_kernel(const LatentAt
     // 8 bits: a thread has 128 registers at launch: 200 + 72 + 2·120 = 4·128
     if (warp < 4) {
         if (FP8) take_registers<200>();
-        softmax<FP8>(s, p, hd, walk, warp, lane);
+        softmax<FP8, TWO>(s, p, hd, walk, warp, lane);
     } else if (warp < kConvertWarp) {
         if (FP8) give_registers<72>();
         if (warp == kProducerWarp) producer<FP8>(s, p, walk, lane);
         else if (warp == kScoreWarp) score_issuer<FP8>(s, p, walk);
-        else if (warp == kValueWarp) value_issuer(s, p, walk);
+        else if (warp == kValueWarp) value_issuer<TWO>(s, p, walk);
         else if (!FP8 && warp == kFixWarp) fixer(s, p, walk, lane);
     } else if constexpr (FP8) {
         give_registers<120>();
@@ -1331,9 +1352,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const LatentAttnP
 template <bool FP8>
 cudaError_t launch(const LatentAttnParams& p, int ctas, cudaStream_t stream) {
     static_assert(sizeof(Smem) <= 232448, "shared memory of one SM");
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+    auto* kernel = p.out_f32 ? attn_kernel<FP8, true> : attn_kernel<FP8, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
     if (e != cudaSuccess) return e;
-    e = launch_dependent(attn_kernel<FP8>, dim3(static_cast<unsigned>(ctas)), dim3(threads_of(FP8)), sizeof(Smem), -1, stream, p);
+    e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(threads_of(FP8)), sizeof(Smem), -1, stream, p);
     if (e != cudaSuccess) return e;
     return launch_dependent(join_kernel<FP8>, dim3(static_cast<unsigned>(2 * ctas)), dim3(kJoinThreads), 0, -1, stream, p, ctas);
 }
