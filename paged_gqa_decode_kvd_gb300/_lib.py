@@ -621,6 +621,8 @@ def kvd_latent_append(handle, layer, latent, k_rope, slot_mapping, positions=Non
         norm = norm_weight.data_ptr()
     n_q = qs = qh = os_ = oh = 0
     src = dst = None
+    if q_rope is None and q_rope_out is not None:
+        raise ValueError("q_rope_out without q_rope")
     if q_rope is not None:
         q_rope_out = q_rope if q_rope_out is None else q_rope_out
         if q_rope.shape[0] != n or q_rope_out.shape != q_rope.shape:

@@ -294,6 +294,11 @@ def test_tensors_of_another_kind(library, fn, bad):
         fn(latent(), **bad)
 
 
+def test_an_output_without_its_input(library):
+    with pytest.raises(ValueError, match="q_rope"):
+        append(latent(), q_rope=None)
+
+
 def test_slices_of_projections_pass(library):
     for a in (dict(latent=view((3, 512), BF16, strides=(576, 1)), k_rope=view((3, 64), BF16, strides=(576, 1)),
                    q_rope=view((3, 4, 64), BF16, strides=(768, 192, 1)), q_rope_out=view((3, 4, 64), BF16, strides=(2304, 576, 1))),
