@@ -636,7 +636,8 @@ KVD_API kvd_status kvd_compact(kvd_pool* pool, const int32_t* block_table, int m
  *                one stride); likewise k_rope [n_tokens][64].  16-byte aligned, strides multiples of 8
  *  norm_weight   bf16 [512], device, 16-byte aligned, or NULL: no norm.  norm_eps ≥ 0
  *  q_rope        bf16, device: the 64 dims of head h of token n start at n·q_stride + h·q_head_stride elements (the last 64
- *                of 192, say); 16-byte aligned, strides multiples of 8, heads and tokens apart.  n_q = 0: no queries
+ *                of 192, say), heads apart, all of a token's within its stride; 16-byte aligned, strides multiples of 8.
+ *                n_q = 0: no queries
  *  q_rope_out    bf16, likewise (the last 64 dims of the absorbed queries, say); may be q_rope itself with its strides,
  *                else its rows are apart from q_rope's, latent's and k_rope's (KVD_ERR_INVALID if they overlap)
  *  positions     int32 [n_tokens], device, in [0, 2^24): a token outside is skipped whole with KVD_ERR_OOB in the error
@@ -696,8 +697,8 @@ KVD_API kvd_status kvd_latent_attn(kvd_pool* pool, int layer, const void* q, int
  *  pool         a latent pool: its device and error word (the cache itself is not read)
  *  q            bf16 [n_tokens][n_q][192], device, 16-byte aligned; n_q ≤ 256
  *  k_nope, v    bf16, device: the 128 dims of head h of key t start at t·stride + h·head_stride elements (slices of one
- *               projection's [n_keys][n_q][256], say); k_rope: 64 dims at t·k_rope_stride, one for all heads.  16-byte
- *               aligned, strides multiples of 8, rows apart
+ *               projection's [n_keys][n_q][256], say), all heads of a key within its stride; k_rope: 64 dims at
+ *               t·k_rope_stride, one for all heads.  16-byte aligned, strides multiples of 8, rows apart
  *  q_start      int32 [batch + 1], device, 0 ≤ q_start[b] ≤ q_start[b+1] ≤ n_tokens; kv_start likewise up to n_keys.  Rows
  *               outside every request are left as they were.  A request whose pairs break this is skipped with KVD_ERR_OOB
  *               in the error word

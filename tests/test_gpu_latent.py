@@ -865,6 +865,29 @@ def test_prefill_rows_of_nobody_behind_the_last_tile_of_two_warpgroups(cuda_devi
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("n_q,gap,behind", [(3, 8, 8), (5, 24, 16), (1, 8, 40), (2, 0, 8)])
+def test_prefill_strides_that_are_no_multiples(cuda_device, n_q, gap, behind):
+    """Heads `gap` values apart and `behind` more behind a token's last: a token's stride is no multiple of a head's."""
+    dev = cuda_device
+    c = Prefill(dev, n_q, [140, 9], [200, 77], seed=n_q)
+    want = c.run()
+
+    def spread(x):
+        n, h, d = x.shape
+        wide = torch.full((n, h * (d + gap) + behind), float("nan"), dtype=torch.bfloat16, device=dev)
+        y = wide.as_strided((n, h, d), (wide.shape[1], d + gap, 1))
+        y.copy_(to(dev, x))
+        return y
+
+    r = torch.full((c.r.shape[0], ROT + behind), float("nan"), dtype=torch.bfloat16, device=dev)
+    r[:, :ROT] = to(dev, c.r)
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    kvd.kvd_latent_prefill(c.pool.handle, to(dev, c.q), to(dev, c.start), spread(c.k), spread(c.v), r[:, :ROT], to(dev, c.kv_start), out,
+                           lse_out=lse)
+    ok(c.pool)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_prefill_bad_pairs(cuda_device):
     dev = cuda_device
     for start, kv, skipped in (([0, 30, 20, 60], [0, 30, 60, 90], [1]), ([0, 20, 40, 61], [0, 30, 60, 90], [2]),
