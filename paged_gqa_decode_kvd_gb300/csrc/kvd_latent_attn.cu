@@ -26,10 +26,11 @@
 // rotated dims were, which only S reads.  That makes O's MMAs 2,060 cycles a tile instead of 1,030: 32 x 8,192 positions with 16 heads 69 us
 // (bf16 61), with 128 heads 116 (96), 131,072 in 8 bits 52 (47).
 // 8 bits: converter warps load the codes (a tile under way while the one before it is converted) and store them as bf16, exactly, in the same
-// layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.
+// layout; the token's scale multiplies the logit's first 512 dims (they and the rotated ones are summed apart) and the weight.  The roles share
+// 128 registers a thread at launch, and the kernel spills for it (1,012 bytes of stores, 592 of loads); with bf16 records nothing is spilled.
 //
 // Bound: 32 x 8,192 positions, 16 heads: 60 us, 5.0 TB/s (74% of measured; the tiles alone at 6.9 TB/s, then 8 us of start, 7 of
-// partials and join); 128 heads: 95 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 47 us, of it 10 until the
+// partials and join); 128 heads: 96 us, the tensor cores (85% busy in a tile); 131,072 positions in 8 bits, 64 heads: 47 us, of it 10 until the
 // first tile is converted, 1.4 us a tile, 8 for 147 parts and their join.
 //
 // Waits.  Each barrier's waiter is at most one phase behind it.  Every wait gives up after a second or so (a try suspends 3.8 us; not while a

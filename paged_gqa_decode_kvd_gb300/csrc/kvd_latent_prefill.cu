@@ -12,11 +12,11 @@
 // Rounding: q, k, v enter exactly, logits, statistics and sums are fp32.  Where out is bf16 a weight enters as one bf16 (off by at most 2^-8
 // of itself; its sum is taken before): outputs are 1.2 to 1.4 times as far from 64 bits as an fp32 form's rounded to bf16; divided by the sum of
 // the weights as they were rounded (as in the absorbed kernel) they are no nearer, and the call takes 11% longer.  Where out is fp32 (TWO) nothing
-// behind it hides that, so a weight enters as two bf16, cut off and its rest (off by at most 2^-15 of itself), for 40% more MMAs: 628 us in place of 454 for the
-// prompt below.
+// behind it hides that, so a weight enters as two bf16, cut off and its rest (off by at most 2^-15 of itself), for 40% more MMAs: 628 us
+// in place of 454 for the prompt below.
 //
-// Bound: a whole prompt of 8,192, 32 heads: 450 us, 1,527 TFLOP/s (78% of measured).  A tile takes both warpgroups 3,600 cycles, its MMAs 2,750
-// (S 12 x 71, at the limit of shared memory's 128 bytes a cycle, O 8 x 65 each), a softmax 1,300 beside the other's MMAs; the rest is what the
+// Bound: a whole prompt of 8,192, 32 heads: 453 us, 1,515 TFLOP/s (79% of measured; in a row of seconds, at the power cap and 1,920 MHz,
+// 485 us, 83% of the rate measured so).  A tile takes both warpgroups 3,600 cycles, its MMAs 2,750 (S 12 x 71, at the limit of shared memory's 128 bytes a cycle, O 8 x 65 each), a softmax 1,300 beside the other's MMAs; the rest is what the
 // turns leave between two runs.  Ragged prompts: 119 us against 53 of HBM: a unit's first tile waits 3 us for Q and K, its rows take 1 to 2 us,
 // and rows of at most 128 tokens leave a warpgroup idle.
 //
