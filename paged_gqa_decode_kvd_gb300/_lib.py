@@ -261,7 +261,10 @@ def kvd_tier_reassign(num_blocks, host_blocks, tier, block_table, hbm_free, hbm_
 
 
 def kvd_pool_create(num_layers, n_kv, num_blocks, kv_dtype, mem, d_h=128, block_size=16, group_size=0):
-    """Wrap a caller-owned device tensor (any dtype, pool_bytes long) as a pool; returns the handle (c_void_p)."""
+    """Wrap a caller-owned tensor on the current device (any dtype, pool_bytes long) as a pool; returns the handle
+    (c_void_p)."""
+    if mem.get_device() != _torch().cuda.current_device():
+        raise ValueError("mem must be on the current device: the pool's kernels run there")
     d = PoolDesc(num_layers, n_kv, d_h, block_size, num_blocks, kv_dtype, group_size)
     h = PoolHandle()
     n = mem.numel() * mem.element_size()

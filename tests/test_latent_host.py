@@ -182,6 +182,14 @@ def test_a_prefill_of_nothing():
 
 
 # ------------------------------------------------------------- the Python entry points
+@pytest.mark.parametrize("current,dev", [(0, 1), (1, 0), (0, -1)])
+@pytest.mark.parametrize("kind", FORMATS + [kvd.KVD_BF16])
+def test_a_pools_memory_is_on_the_current_device(monkeypatch, current, dev, kind):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    with pytest.raises(ValueError, match="current device"):
+        kvd.kvd_pool_create(1, 1, 4, kind, Tensor((1 << 20,), torch.uint8, dev), d_h=576 if kind in FORMATS else 128)
+
+
 @pytest.fixture
 def library(monkeypatch):
     real = kvd.load()
